@@ -37,7 +37,9 @@ EXPORTED = ("vtmu_attention_params_init", "vtmu_attention_workspace_size", "vtmu
             "vtmu_device_error", "vtmu_decode_step", "vtmu_decode_step_host_workspace_size",
             "vtmu_decode_step_host", "vtmu_rope_params_init", "vtmu_rope", "vtmu_decode_step_rope",
             "vtmu_mla_params_init", "vtmu_mla_workspace_size", "vtmu_mla_attention", "vtmu_mla_decode_step",
-            "vtmu_mla_decode_step_host_workspace_size", "vtmu_mla_decode_step_host")
+            "vtmu_mla_decode_step_host_workspace_size", "vtmu_mla_decode_step_host",
+            "vtmu_page_map", "vtmu_tree_plan", "vtmu_rope_at", "vtmu_paged_write", "vtmu_paged_params_init",
+            "vtmu_paged_workspace_size", "vtmu_paged_attention")
 NOALLOC_SCRATCH_BYTES = 8 << 20  # VTMU_NOALLOC_SCRATCH_BYTES
 
 
@@ -109,6 +111,31 @@ class vtmu_mla_params(ctypes.Structure):
     ]
 
 
+class vtmu_paged_params(ctypes.Structure):
+    """Mirror of ``vtmu_paged_params`` (include/vtmu_attention.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("pages", ctypes.c_int64),
+        ("requests", ctypes.c_int32),
+        ("max_rows", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("tree", ctypes.c_int32),
+        ("has_scale", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("softcap", ctypes.c_float),
+        ("kernel", ctypes.c_int32),
+        ("window", ctypes.c_int64),
+        ("sinks", ctypes.c_int64),
+    ]
+
+
+VTMU_PAGED_AUTO, VTMU_PAGED_CUDA_CORES, VTMU_PAGED_TENSOR_CORES = 0, 1, 2
+TREE_MAX_ROWS = 64  # VTMU_TREE_MAX_ROWS
+
 MLA_KERNEL_AUTO, MLA_KERNEL_CUDA_CORES, MLA_KERNEL_TENSOR_CORES = 0, 1, 2
 
 _lib = None
@@ -174,6 +201,22 @@ def load_library():
         lib.vtmu_mla_decode_step_host.argtypes = [vp, ctypes.c_int64, vp, ctypes.c_int64, ctypes.c_int64, vp, vp,
                                                   vp, vp, M, vp, ctypes.c_size_t, vp]
         lib.vtmu_mla_decode_step_host.restype = ctypes.c_int
+        i32, i64 = ctypes.c_int32, ctypes.c_int64
+        lib.vtmu_page_map.argtypes = [vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, i32, i64, i32, i32, vp]
+        lib.vtmu_page_map.restype = ctypes.c_int
+        lib.vtmu_tree_plan.argtypes = [vp, vp, vp, vp, vp, i32, i64, vp]
+        lib.vtmu_tree_plan.restype = ctypes.c_int
+        lib.vtmu_rope_at.argtypes = [vp, vp, i64, i32, vp, R, vp]
+        lib.vtmu_rope_at.restype = ctypes.c_int
+        lib.vtmu_paged_write.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, i64, vp]
+        lib.vtmu_paged_write.restype = ctypes.c_int
+        G = ctypes.POINTER(vtmu_paged_params)
+        lib.vtmu_paged_params_init.argtypes = [G]
+        lib.vtmu_paged_params_init.restype = None
+        lib.vtmu_paged_workspace_size.argtypes = [G, ctypes.POINTER(ctypes.c_size_t)]
+        lib.vtmu_paged_workspace_size.restype = ctypes.c_int
+        lib.vtmu_paged_attention.argtypes = [vp] * 11 + [G, vp, ctypes.c_size_t, vp]
+        lib.vtmu_paged_attention.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -327,6 +370,52 @@ def vtmu_mla_decode_step_host(state, max_rows: int, state_new_host, new_rows: in
                                                     int(new_rows), int(offset), _haddr(q_host), _addr(k_b),
                                                     _addr(v_b), _haddr(out_host), ctypes.byref(p), _addr(workspace),
                                                     int(workspace_bytes), stream or None))
+
+
+def vtmu_page_map(lens, cu_rows, accept, block_table, free_pages, free_capacity: int, n_free, slots, positions,
+                  new_lens, n_free_out, requests: int, rows: int, page_size: int, max_pages: int,
+                  stream: int = 0) -> None:
+    _check(load_library().vtmu_page_map(_addr(lens), _addr(cu_rows), _addr(accept), _addr(block_table),
+                                        _addr(free_pages), int(free_capacity), _addr(n_free), _addr(slots),
+                                        _addr(positions), _addr(new_lens), _addr(n_free_out), int(requests),
+                                        int(rows), int(page_size), int(max_pages), stream or None))
+
+
+def vtmu_tree_plan(parents, cu_rows, lens, masks, positions, requests: int, rows: int, stream: int = 0) -> None:
+    _check(load_library().vtmu_tree_plan(_addr(parents), _addr(cu_rows), _addr(lens), _addr(masks),
+                                         _addr(positions), int(requests), int(rows), stream or None))
+
+
+def vtmu_rope_at(x, out, T: int, heads: int, positions, r: vtmu_rope_params, stream: int = 0) -> None:
+    _check(load_library().vtmu_rope_at(_addr(x), _addr(out), int(T), int(heads), _addr(positions), ctypes.byref(r),
+                                       stream or None))
+
+
+def vtmu_paged_write(k_pool, v_pool, pool_rows: int, k_width: int, v_width: int, k_new, v_new, slots, rows: int,
+                     stream: int = 0) -> None:
+    _check(load_library().vtmu_paged_write(_addr(k_pool), _addr(v_pool), int(pool_rows), int(k_width),
+                                           int(v_width), _addr(k_new), _addr(v_new), _addr(slots), int(rows),
+                                           stream or None))
+
+
+def vtmu_paged_params_init() -> vtmu_paged_params:
+    p = vtmu_paged_params()
+    load_library().vtmu_paged_params_init(ctypes.byref(p))
+    return p
+
+
+def vtmu_paged_workspace_size(p: vtmu_paged_params) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().vtmu_paged_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+    return int(n.value)
+
+
+def vtmu_paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, k_new, v_new, masks, positions, out,
+                         p: vtmu_paged_params, workspace, workspace_bytes: int, stream: int = 0) -> None:
+    _check(load_library().vtmu_paged_attention(_addr(q), _addr(k_pool), _addr(v_pool), _addr(block_table),
+                                               _addr(lens), _addr(cu_rows), _addr(k_new), _addr(v_new),
+                                               _addr(masks), _addr(positions), _addr(out), ctypes.byref(p),
+                                               _addr(workspace), int(workspace_bytes), stream or None))
 
 
 def vtmu_device_error() -> int:
@@ -587,4 +676,153 @@ def mla_decode_step(state, state_new, offset: int, q, k_b, v_b, *, heads, qk_nop
     buf, cap = ws.get(nbytes)
     st = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
     vtmu_mla_decode_step(state, state.shape[0], state_new, R, offset, q, k_b, v_b, out, p, buf, cap, st)
+    return out
+
+
+# ------------------------------------------------------------- paged caches
+def _need(name, t, dtype, device=None):
+    """A contiguous CUDA tensor of the type, on the call's device."""
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or (device is not None and t.device != device):
+        where = "" if device is None else f" on {device}"
+        raise ValueError(f"{name} must be a contiguous {str(dtype).removeprefix('torch.')} CUDA tensor{where}")
+
+
+def page_map(lens, cu_rows, block_table, free_pages, n_free, *, rows: int, pageSize: int, accept=None, stream=None):
+    """Block tables, slot maps and positions of a step's new rows on CUDA
+    tensors (vtmu_page_map): lens [requests] and cu_rows [requests + 1] int32,
+    block_table [requests, maxPages] int32 (completed in place), the stack
+    free_pages [n] with n_free [1] pages on it, accept [requests] int64 bit
+    masks of the rows to add (None: all).  Returns (slots [rows],
+    positions [rows], new_lens [requests], n_free [1]), all int32."""
+    import torch
+    dev, n = lens.device, lens.shape[0]
+    i32 = torch.int32
+    for name, t in (("lens", lens), ("cu_rows", cu_rows), ("block_table", block_table), ("free_pages", free_pages),
+                    ("n_free", n_free)):
+        _need(name, t, i32, dev)
+    if accept is not None:
+        _need("accept", accept, torch.int64, dev)
+    if (cu_rows.shape != (n + 1,) or block_table.dim() != 2 or block_table.shape[0] != n or n_free.numel() != 1 or
+            (accept is not None and accept.shape != (n,))):
+        raise ValueError("page_map: cu_rows [requests + 1], block_table [requests, maxPages], n_free [1], "
+                         "accept [requests]")
+    slots = torch.empty(rows, dtype=i32, device=dev)
+    positions = torch.empty(rows, dtype=i32, device=dev)
+    new_lens = torch.empty(n, dtype=i32, device=dev)
+    left = torch.empty(1, dtype=i32, device=dev)
+    with torch.cuda.device(dev):
+        st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+        vtmu_page_map(lens, cu_rows, accept, block_table, free_pages, free_pages.numel(), n_free, slots, positions,
+                      new_lens, left, n, rows, pageSize, block_table.shape[1], st)
+    return slots, positions, new_lens, left
+
+
+def tree_plan(parents, cu_rows, lens, *, stream=None):
+    """Ancestor masks and positions of drafted trees on CUDA tensors
+    (vtmu_tree_plan): parents [rows], cu_rows [requests + 1] and lens
+    [requests] int32.  Returns (masks [rows] int64, positions [rows] int32)."""
+    import torch
+    dev = parents.device
+    for name, t in (("parents", parents), ("cu_rows", cu_rows), ("lens", lens)):
+        _need(name, t, torch.int32, dev)
+    if cu_rows.shape != (lens.shape[0] + 1,):
+        raise ValueError("tree_plan: cu_rows [requests + 1], lens [requests]")
+    masks = torch.empty(parents.shape[0], dtype=torch.int64, device=dev)
+    positions = torch.empty(parents.shape[0], dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+        vtmu_tree_plan(parents, cu_rows, lens, masks, positions, lens.shape[0], parents.shape[0], st)
+    return masks, positions
+
+
+def rope_at(x, positions, *, headDim, out=None, stream=None, **params):
+    """op "rope" on a CUDA tensor x [T, heads*headDim] whose row t sits at
+    positions[t] (int32; a row at a negative position is left as it was in
+    out); ``out=x`` turns it in place.  Params as make_rope_params."""
+    import torch
+    dev = x.device
+    _need("x", x, torch.float32)
+    _need("positions", positions, torch.int32, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    _need("out", out, torch.float32, dev)
+    if x.dim() != 2 or x.shape[1] % headDim or positions.shape != (x.shape[0],) or out.shape != x.shape:
+        raise ValueError("rope_at: x and out [T, heads*headDim], positions [T]")
+    r = make_rope_params(headDim=headDim, **params)
+    with torch.cuda.device(dev):
+        st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+        vtmu_rope_at(x, out, x.shape[0], x.shape[1] // headDim, positions, r, st)
+    return out
+
+
+def paged_write(k_pool, v_pool, k_new, v_new, slots, *, stream=None):
+    """op "cache_write" through a slot map on CUDA tensors: rows of k_new and
+    v_new into the pools at the rows that slots (int32) names; rows whose slot
+    is outside the pool are skipped.  Returns (k_pool, v_pool)."""
+    import torch
+    dev = k_pool.device
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool), ("k_new", k_new), ("v_new", v_new)):
+        _need(name, t, torch.float32, dev)
+    _need("slots", slots, torch.int32, dev)
+    n = slots.shape[0]
+    if (k_pool.dim() != 2 or v_pool.dim() != 2 or k_pool.shape[0] != v_pool.shape[0] or
+            k_new.shape != (n, k_pool.shape[1]) or v_new.shape != (n, v_pool.shape[1])):
+        raise ValueError("paged_write: pools [poolRows, width], k_new and v_new [rows, width], slots [rows]")
+    with torch.cuda.device(dev):
+        st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+        vtmu_paged_write(k_pool, v_pool, k_pool.shape[0], k_pool.shape[1], v_pool.shape[1], k_new, v_new, slots, n, st)
+    return k_pool, v_pool
+
+
+def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, headDim, pageSize, maxRows, kvHeads=None,
+                    tree=None, scale=None, softcap=None, window=None, sinks=None, kernel=VTMU_PAGED_AUTO, out=None,
+                    workspace=None, stream=None):
+    """op "attention" of a ragged batch over a paged cache on CUDA tensors
+    (vtmu_paged_attention): q [rows, heads*headDim], pools [pages*pageSize,
+    kvHeads*headDim], block_table [requests, maxPages], lens [requests] and
+    cu_rows [requests + 1] int32; maxRows bounds the rows of one request.
+    ``tree=(k_new, v_new, masks, positions)`` attends to drafted rows beside
+    the cache (positions may be None without a window).  Returns out [rows,
+    heads*headDim]; rows of no request are not written."""
+    import torch
+    dev = q.device
+    f32, i32 = torch.float32, torch.int32
+    for name, t in (("q", q), ("k_pool", k_pool), ("v_pool", v_pool)):
+        _need(name, t, f32, dev)
+    for name, t in (("block_table", block_table), ("lens", lens), ("cu_rows", cu_rows)):
+        _need(name, t, i32, dev)
+    hk = heads if kvHeads is None else kvHeads
+    rows, n = q.shape[0], lens.shape[0]
+    if (q.shape != (rows, heads * headDim) or k_pool.dim() != 2 or k_pool.shape[1] != hk * headDim or
+            k_pool.shape != v_pool.shape or k_pool.shape[0] % pageSize or block_table.dim() != 2 or
+            block_table.shape[0] != n or cu_rows.shape != (n + 1,)):
+        raise ValueError("paged_attention: q [rows, heads*headDim], pools [pages*pageSize, kvHeads*headDim], "
+                         "block_table [requests, maxPages], lens [requests], cu_rows [requests + 1]")
+    k_new = v_new = masks = positions = None
+    if tree is not None:
+        k_new, v_new, masks, positions = tree
+        for name, t in (("k_new", k_new), ("v_new", v_new)):
+            _need(name, t, f32, dev)
+        _need("masks", masks, torch.int64, dev)
+        if positions is not None:
+            _need("positions", positions, i32, dev)
+        if (k_new.shape != (rows, hk * headDim) or v_new.shape != k_new.shape or masks.shape != (rows,) or
+                (positions is not None and positions.shape != (rows,))):
+            raise ValueError("paged_attention: k_new and v_new [rows, kvHeads*headDim], masks and positions [rows]")
+    if out is None:
+        out = torch.empty_like(q)
+    _need("out", out, f32, dev)
+    if out.shape != q.shape:
+        raise ValueError("paged_attention: out [rows, heads*headDim]")
+    p = vtmu_paged_params(rows=rows, pages=k_pool.shape[0] // pageSize, requests=n, max_rows=maxRows,
+                          page_size=pageSize, max_pages=block_table.shape[1], heads=heads, kv_heads=hk,
+                          head_dim=headDim, tree=0 if tree is None else 1, has_scale=0 if scale is None else 1,
+                          scale=0.0 if scale is None else scale, softcap=softcap or 0.0, kernel=kernel,
+                          window=window or 0, sinks=sinks or 0)
+    with torch.cuda.device(dev):
+        nbytes = vtmu_paged_workspace_size(p)
+        buf, cap = (workspace if workspace is not None else _default_workspace(dev)).get(nbytes)
+        st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+        vtmu_paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, k_new, v_new, masks, positions, out, p,
+                             buf, cap, st)
     return out

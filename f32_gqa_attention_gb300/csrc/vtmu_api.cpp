@@ -10,6 +10,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -359,6 +360,79 @@ size_t mla_workspace(const vtmu::MlaDesc& m) {
     vtmu::MlaPlan plan;
     vtmu::mla_plan(m, 1 << 20, &plan);
     return plan.workspace_bytes;
+}
+
+// Checks of paged attention's parameters that need no pointer; fills the
+// kernels' description (pointers excepted).
+vtmu_status resolve_paged(const vtmu_paged_params* p, vtmu::PagedDesc* a) {
+    if (!p) return fail(VTMU_ERR_INVALID, "paged params is NULL");
+    std::memset(a, 0, sizeof(*a));
+    if (p->rows < 0 || p->pages < 0)
+        return fail(VTMU_ERR_INVALID, "paged: rows %lld and pages %lld must be >= 0", (long long)p->rows,
+                    (long long)p->pages);
+    if (p->requests < 1 || p->max_rows < 0)
+        return fail(VTMU_ERR_INVALID, "paged: requests %d must be > 0 and max_rows %d >= 0", p->requests, p->max_rows);
+    if (p->page_size < 1 || p->max_pages < 1)
+        return fail(VTMU_ERR_INVALID, "paged: page_size %d and max_pages %d must be > 0", p->page_size, p->max_pages);
+    if (p->heads <= 0) return fail(VTMU_ERR_INVALID, "paged: heads must be > 0 (got %d)", p->heads);
+    const int Hk = p->kv_heads == 0 ? p->heads : p->kv_heads;
+    if (Hk <= 0 || p->heads % Hk != 0)
+        return fail(VTMU_ERR_INVALID, "paged: heads (%d) must be a multiple of kvHeads (%d)", p->heads, Hk);
+    if (p->head_dim <= 0) return fail(VTMU_ERR_INVALID, "paged: headDim must be > 0 (got %d)", p->head_dim);
+    if (p->tree != 0 && p->tree != 1) return fail(VTMU_ERR_INVALID, "paged: tree %d is not 0 or 1", p->tree);
+    if (p->has_scale && !std::isfinite(p->scale)) return fail(VTMU_ERR_INVALID, "paged: scale must be finite");
+    if (!(p->softcap >= 0.f) || !std::isfinite(p->softcap))
+        return fail(VTMU_ERR_INVALID, "paged: softcap must be finite and >= 0");
+    if (p->window < 0 || p->sinks < 0) return fail(VTMU_ERR_INVALID, "paged: window and sinks must be >= 0");
+    if (p->kernel < VTMU_PAGED_AUTO || p->kernel > VTMU_PAGED_TENSOR_CORES)
+        return fail(VTMU_ERR_INVALID, "paged: kernel %d is not a vtmu_paged_kernel", p->kernel);
+    if (p->head_dim > 256) return fail(VTMU_ERR_UNSUPPORTED, "paged: headDim %d > 256 is not supported", p->head_dim);
+    if (p->heads > 65535) return fail(VTMU_ERR_UNSUPPORTED, "paged: more than 65535 heads");
+    if (p->requests > vtmu::kPagedMaxRequests)
+        return fail(VTMU_ERR_UNSUPPORTED, "paged: %d requests, %d at most", p->requests, vtmu::kPagedMaxRequests);
+    if (p->tree && p->max_rows > vtmu::kTreeMaxRows)
+        return fail(VTMU_ERR_UNSUPPORTED, "paged: a tree of %d rows, %d at most", p->max_rows, vtmu::kTreeMaxRows);
+    if (p->rows >= ((int64_t)1 << 31) || p->pages >= ((int64_t)1 << 31) ||
+        p->pages * p->page_size >= ((int64_t)1 << 31) || (int64_t)p->max_pages * p->page_size >= ((int64_t)1 << 31))
+        return fail(VTMU_ERR_UNSUPPORTED, "paged: rows, pool rows and a request's rows must be below 2^31");
+    if ((int64_t)p->max_rows * (p->heads / Hk) >= ((int64_t)1 << 31))
+        return fail(VTMU_ERR_UNSUPPORTED, "paged: max_rows x group size must be below 2^31");
+    a->rows = p->rows;
+    a->pages = p->pages;
+    a->window = p->window;
+    a->sinks = p->window > 0 ? p->sinks : 0;  // without a window no key is dropped
+    a->B = p->requests;
+    a->H = p->heads;
+    a->Hk = Hk;
+    a->G = p->heads / Hk;
+    a->D = p->head_dim;
+    a->page_size = p->page_size;
+    a->max_pages = p->max_pages;
+    a->max_rows = p->max_rows;
+    a->tree = p->tree;
+    const double scale = p->has_scale ? (double)p->scale : 1.0 / std::sqrt((double)p->head_dim);
+    a->softcap_on = p->softcap > 0.f ? 1 : 0;
+    a->qk_mul = (float)(a->softcap_on ? scale / (double)p->softcap : scale * 1.4426950408889634);
+    a->cap_log2 = a->softcap_on ? (float)((double)p->softcap * 1.4426950408889634) : 0.f;
+    return VTMU_OK;
+}
+
+// True when one of the n outputs (the first `n_out` entries) overlaps any other entry.
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+bool outputs_overlap(const Span* s, int n_out, int n) {
+    for (int i = 0; i < n_out; ++i)
+        for (int j = 0; j < n; ++j)
+            if (i != j && overlaps(s[i].p, s[i].bytes, s[j].p, s[j].bytes)) return true;
+    return false;
+}
+
+bool misaligned(std::initializer_list<const void*> ptrs, uintptr_t mask) {
+    uintptr_t m = 0;
+    for (const void* p : ptrs) m |= reinterpret_cast<uintptr_t>(p);
+    return (m & mask) != 0;
 }
 
 }  // namespace
@@ -974,6 +1048,147 @@ vtmu_status vtmu_mla_decode_step_host(float* state, int64_t max_rows, const floa
     }
     e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_fail(e, "mla_decode_step_host: stream synchronisation");
+    return ok();
+}
+
+vtmu_status vtmu_page_map(const int32_t* lens, const int32_t* cu_rows, const uint64_t* accept, int32_t* block_table,
+                          const int32_t* free_pages, int64_t free_capacity, const int32_t* n_free, int32_t* slots,
+                          int32_t* positions, int32_t* new_lens, int32_t* n_free_out, int32_t requests, int64_t rows,
+                          int32_t page_size, int32_t max_pages, cudaStream_t stream) {
+    if (requests < 0 || rows < 0 || free_capacity < 0)
+        return fail(VTMU_ERR_INVALID, "page_map: negative size (requests %d, rows %lld, free_capacity %lld)", requests,
+                    (long long)rows, (long long)free_capacity);
+    if (page_size < 1 || max_pages < 1)
+        return fail(VTMU_ERR_INVALID, "page_map: page_size %d and max_pages %d must be > 0", page_size, max_pages);
+    if (requests == ((int32_t)1 << 31) - 1) return fail(VTMU_ERR_INVALID, "page_map: too many requests");
+    if (!cu_rows || !n_free || !n_free_out || (requests > 0 && (!lens || !block_table || !new_lens)) ||
+        (rows > 0 && !slots) || (free_capacity > 0 && !free_pages))
+        return fail(VTMU_ERR_INVALID, "page_map: a pointer is NULL");
+    if (misaligned({lens, cu_rows, block_table, free_pages, n_free, slots, positions, new_lens, n_free_out}, 3u) ||
+        misaligned({accept}, 7u))
+        return fail(VTMU_ERR_INVALID, "page_map: a pointer is misaligned");
+    const size_t b4 = (size_t)requests * 4;
+    const Span spans[] = {{block_table, b4 * (size_t)max_pages}, {slots, (size_t)rows * 4},
+                          {positions, (size_t)rows * 4}, {new_lens, b4}, {n_free_out, 4}, {lens, b4},
+                          {cu_rows, b4 + 4}, {accept, 2 * b4}, {free_pages, (size_t)free_capacity * 4}, {n_free, 4}};
+    if (outputs_overlap(spans, 5, 10)) return fail(VTMU_ERR_INVALID, "page_map: an output overlaps another buffer");
+    const vtmu::PageMapArgs a{lens,      cu_rows,    accept,        block_table, free_pages, n_free,    slots,    positions,
+                              new_lens, n_free_out, free_capacity, rows,        requests,   page_size, max_pages};
+    const cudaError_t e = vtmu::launch_page_map(a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "page_map launch");
+    return ok();
+}
+
+vtmu_status vtmu_tree_plan(const int32_t* parents, const int32_t* cu_rows, const int32_t* lens, uint64_t* masks,
+                           int32_t* positions, int32_t requests, int64_t rows, cudaStream_t stream) {
+    if (requests < 0 || rows < 0)
+        return fail(VTMU_ERR_INVALID, "tree_plan: negative size (requests %d, rows %lld)", requests, (long long)rows);
+    if (!cu_rows || (requests > 0 && !lens) || (rows > 0 && (!parents || !masks || !positions)))
+        return fail(VTMU_ERR_INVALID, "tree_plan: a pointer is NULL");
+    if (misaligned({parents, cu_rows, lens, positions}, 3u) || misaligned({masks}, 7u))
+        return fail(VTMU_ERR_INVALID, "tree_plan: a pointer is misaligned");
+    const size_t r4 = (size_t)rows * 4, b4 = (size_t)requests * 4;
+    const Span spans[] = {{masks, 2 * r4}, {positions, r4}, {parents, r4}, {cu_rows, b4 + 4}, {lens, b4}};
+    if (outputs_overlap(spans, 2, 5)) return fail(VTMU_ERR_INVALID, "tree_plan: an output overlaps another buffer");
+    if (rows == 0) return ok();
+    const cudaError_t e = vtmu::launch_tree_plan(parents, cu_rows, lens, masks, positions, requests, rows, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "tree_plan launch");
+    return ok();
+}
+
+vtmu_status vtmu_rope_at(const float* x, float* out, int64_t T, int32_t heads, const int32_t* positions,
+                         const vtmu_rope_params* rp, cudaStream_t stream) {
+    vtmu::RopeDev rd;
+    vtmu_status st = resolve_rope(rp, &rd);
+    if (st != VTMU_OK) return st;
+    if (T < 0 || heads <= 0)
+        return fail(VTMU_ERR_INVALID, "rope_at: T %lld and heads %d must be >= 0 and > 0", (long long)T, heads);
+    if (T == 0) return ok();
+    if (!x || !out || !positions) return fail(VTMU_ERR_INVALID, "rope_at: x, out or positions is NULL");
+    if (misaligned({x, out, positions}, 3u)) return fail(VTMU_ERR_INVALID, "rope_at: pointers must be 4-byte aligned");
+    const size_t nb = (size_t)T * heads * rp->head_dim * 4;
+    if ((x != out && overlaps(x, nb, out, nb)) || overlaps(out, nb, positions, (size_t)T * 4))
+        return fail(VTMU_ERR_INVALID, "rope_at: out overlaps x without being x, or positions");
+    const cudaError_t e = vtmu::launch_rope_at(x, out, T, heads, rp->head_dim, positions, rd, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "rope_at launch");
+    return ok();
+}
+
+vtmu_status vtmu_paged_write(float* k_pool, float* v_pool, int64_t pool_rows, int64_t k_width, int64_t v_width,
+                             const float* k_new, const float* v_new, const int32_t* slots, int64_t rows,
+                             cudaStream_t stream) {
+    if (pool_rows < 0 || k_width < 0 || v_width < 0 || rows < 0)
+        return fail(VTMU_ERR_INVALID, "paged_write: negative size (pool_rows %lld, widths %lld and %lld, rows %lld)",
+                    (long long)pool_rows, (long long)k_width, (long long)v_width, (long long)rows);
+    if (rows == 0 || pool_rows == 0) return ok();
+    if (!slots || (k_width > 0 && (!k_pool || !k_new)) || (v_width > 0 && (!v_pool || !v_new)))
+        return fail(VTMU_ERR_INVALID, "paged_write: a pointer is NULL");
+    if (misaligned({k_pool, v_pool, k_new, v_new, slots}, 3u))
+        return fail(VTMU_ERR_INVALID, "paged_write: pointers must be 4-byte aligned");
+    const Span spans[] = {{k_pool, (size_t)(pool_rows * k_width) * 4}, {v_pool, (size_t)(pool_rows * v_width) * 4},
+                          {k_new, (size_t)(rows * k_width) * 4}, {v_new, (size_t)(rows * v_width) * 4},
+                          {slots, (size_t)rows * 4}};
+    if (outputs_overlap(spans, 2, 5)) return fail(VTMU_ERR_INVALID, "paged_write: a pool overlaps another buffer");
+    const cudaError_t e = vtmu::launch_paged_write(k_pool, v_pool, pool_rows, k_width, v_width, k_new, v_new, slots,
+                                                   rows, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "paged_write launch");
+    return ok();
+}
+
+void vtmu_paged_params_init(vtmu_paged_params* p) {
+    if (p) std::memset(p, 0, sizeof(*p));
+}
+
+vtmu_status vtmu_paged_workspace_size(const vtmu_paged_params* p, size_t* bytes) {
+    if (!bytes) return fail(VTMU_ERR_INVALID, "bytes is NULL");
+    vtmu::PagedDesc a;
+    vtmu_status st = resolve_paged(p, &a);
+    if (st != VTMU_OK) return st;
+    *bytes = 0;
+    return ok();
+}
+
+vtmu_status vtmu_paged_attention(const float* q, const float* k_pool, const float* v_pool, const int32_t* block_table,
+                                 const int32_t* lens, const int32_t* cu_rows, const float* k_new, const float* v_new,
+                                 const uint64_t* masks, const int32_t* positions, float* out,
+                                 const vtmu_paged_params* p, void* workspace, size_t workspace_bytes,
+                                 cudaStream_t stream) {
+    vtmu::PagedDesc a;
+    vtmu_status st = resolve_paged(p, &a);
+    if (st != VTMU_OK) return st;
+    if (a.rows == 0 || a.max_rows == 0) return ok();
+    if (!q || !out || !lens || !cu_rows || !block_table || (a.pages > 0 && (!k_pool || !v_pool)))
+        return fail(VTMU_ERR_INVALID, "paged: q, out, lens, cu_rows, block_table or a pool is NULL");
+    if (a.tree ? (!k_new || !v_new || !masks || (a.window > 0 && !positions))
+               : (k_new || v_new || masks || positions))
+        return fail(VTMU_ERR_INVALID, "paged: tree arguments (k_new, v_new, masks, positions with a window) and "
+                                      "params.tree disagree");
+    if (misaligned({q, k_pool, v_pool, block_table, lens, cu_rows, k_new, v_new, positions, out}, 3u) ||
+        misaligned({masks}, 7u))
+        return fail(VTMU_ERR_INVALID, "paged: a pointer is misaligned");
+    const size_t qb = (size_t)a.rows * a.H * a.D * 4, nb = (size_t)a.rows * a.Hk * a.D * 4,
+                 pb = (size_t)a.pages * a.page_size * a.Hk * a.D * 4, b4 = (size_t)a.B * 4;
+    const Span spans[] = {{out, qb}, {q, qb}, {k_pool, pb}, {v_pool, pb}, {block_table, b4 * (size_t)a.max_pages},
+                          {lens, b4}, {cu_rows, b4 + 4}, {k_new, nb}, {v_new, nb}, {masks, (size_t)a.rows * 8},
+                          {positions, (size_t)a.rows * 4}};
+    if (outputs_overlap(spans, 1, 11)) return fail(VTMU_ERR_INVALID, "paged: out overlaps an input");
+    a.q = q;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.block_table = block_table;
+    a.lens = lens;
+    a.cu_rows = cu_rows;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.masks = masks;
+    a.positions = positions;
+    a.out = out;
+    if (p->kernel == VTMU_PAGED_TENSOR_CORES)
+        return fail(VTMU_ERR_UNSUPPORTED, "paged: kernel TENSOR_CORES does not cover this call");
+    (void)workspace;
+    (void)workspace_bytes;
+    const cudaError_t e = vtmu::launch_paged_ffma(a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
     return ok();
 }
 

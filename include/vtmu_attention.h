@@ -478,6 +478,189 @@ VTMU_API vtmu_status vtmu_mla_decode_step_host(float* state, int64_t max_rows, c
                                                size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * ---- Paged caches: batches of requests and trees of drafted tokens ----------
+ *
+ * The entry points below serve several requests at once.  Their K and V rows
+ * live in pages of one shared pool, k_pool / v_pool [pages * page_size,
+ * kvHeads * headDim] (rows laid out as in every cache of this library): row s
+ * of request b is pool row block_table[b, s / page_size] * page_size + s %
+ * page_size.  The rows that a step adds are packed request after request:
+ * request b owns rows cu_rows[b] .. cu_rows[b + 1] - 1 of q, out, the new K/V
+ * rows and every per-row array; rows behind cu_rows[requests] belong to no
+ * request.  Lengths and tables are DEVICE memory and read by the kernels
+ * alone, so a captured graph serves every later step whose rows and pages fit
+ * the sizes it was captured with.  Values outside their range on the device
+ * (a negative length, a page id outside the pool, a decreasing cu_rows) are
+ * clamped or skipped as each entry point says; none leads out of a buffer.
+ *
+ * A step of tokens that are already decided: vtmu_page_map, vtmu_rope_at on q
+ * and the new keys, vtmu_paged_write, vtmu_paged_attention without a tree.
+ * A step that verifies drafted trees: vtmu_tree_plan, vtmu_rope_at,
+ * vtmu_paged_attention with the drafted rows beside the cache; once the
+ * accepted rows are known, vtmu_page_map with `accept` and vtmu_paged_write
+ * bring these rows, and no others, into the cache.
+ */
+
+/* Most drafted rows of one request in a tree (one bit each in a mask). */
+#define VTMU_TREE_MAX_ROWS 64
+
+/*
+ * Block tables, slot maps and positions from request lengths, in one launch.
+ * Request b holds lens[b] rows and adds a_b: its packed rows, or, with
+ * `accept`, those of its first 64 packed rows whose bit is set in accept[b].
+ * The i-th row it adds becomes row lens[b] + i of the request.  Pages are
+ * taken from the top of the stack free_pages[0 .. *n_free) in the order of
+ * (request, page): the k-th new page of the call is free_pages[*n_free-1-k].
+ *   lens [requests], cu_rows [requests + 1]: int32, DEVICE.  A negative length
+ *     counts as 0; cu_rows entries are clamped to 0 .. rows and a decreasing
+ *     pair holds no rows.
+ *   accept [requests]: uint64, DEVICE, or NULL (every packed row is added).
+ *   block_table [requests, max_pages]: int32, DEVICE; entries of pages that
+ *     the call adds are written, the others left.  A request's rows past
+ *     max_pages * page_size get slot -1 and take no page.
+ *   free_pages [free_capacity], n_free [1]: int32, DEVICE; not changed.
+ *     *n_free is clamped to 0 .. free_capacity.
+ *   slots [rows]: int32 out: the pool row of each packed row; -1 for a row
+ *     that is not added, behind the last request, or without a page.
+ *   positions [rows]: int32 out or NULL: the row's place in its request (its
+ *     token position), -1 where it is not added.
+ *   new_lens [requests]: int32 out: lens + a_b.
+ *   n_free_out [1]: int32 out: pages left; negative when that many pages were
+ *     missing: entries and slots of missing pages are -1.
+ * The outputs may not overlap an input or each other.  A page goes back by
+ * writing its id at free_pages[*n_free_out] and counting one more (a finished
+ * request's ids are the first ceil(lens[b] / page_size) of its table row).
+ * Errors: VTMU_ERR_INVALID (null pointer, negative size, page_size or
+ * max_pages < 1, a misaligned pointer, overlapping buffers), VTMU_ERR_CUDA.
+ */
+VTMU_API vtmu_status vtmu_page_map(const int32_t* lens, const int32_t* cu_rows, const uint64_t* accept,
+                                   int32_t* block_table, const int32_t* free_pages, int64_t free_capacity,
+                                   const int32_t* n_free, int32_t* slots, int32_t* positions,
+                                   int32_t* new_lens, int32_t* n_free_out, int32_t requests, int64_t rows,
+                                   int32_t page_size, int32_t max_pages, cudaStream_t stream);
+
+/*
+ * Masks and positions of drafted trees, in one launch.  Packed row j of a
+ * request hangs below its row parents[j] when 0 <= parents[j] < j, and below
+ * the request's context otherwise.  masks[j] has the bits of j's ancestors
+ * and of j itself; positions[j] = lens[b] + the number of its ancestors.
+ *   parents [rows], cu_rows [requests + 1], lens [requests] (rows of context,
+ *     a negative one counts as 0): int32, DEVICE.
+ *   masks [rows]: uint64 out; positions [rows]: int32 out.  Rows past a
+ *     request's 64th and rows behind the last request get mask 0, position -1.
+ * Errors: VTMU_ERR_INVALID (null or misaligned pointer, negative size,
+ * overlapping buffers), VTMU_ERR_CUDA.
+ */
+VTMU_API vtmu_status vtmu_tree_plan(const int32_t* parents, const int32_t* cu_rows, const int32_t* lens,
+                                    uint64_t* masks, int32_t* positions, int32_t requests, int64_t rows,
+                                    cudaStream_t stream);
+
+/*
+ * op "rope" with a position for each row: vtmu_rope where row t sits at
+ * positions[t] (int32, DEVICE, [T]) instead of offset + t.  A row whose
+ * position is negative is left as it was in `out`.  Errors: those of
+ * vtmu_rope (positions NULL, misaligned or overlapping out included).
+ */
+VTMU_API vtmu_status vtmu_rope_at(const float* x, float* out, int64_t T, int32_t heads, const int32_t* positions,
+                                  const vtmu_rope_params* r, cudaStream_t stream);
+
+/*
+ * op "cache_write" through a slot map, for K and V in one launch: k_pool[
+ * slots[r], :] = k_new[r, :] and v_pool[slots[r], :] = v_new[r, :] for r <
+ * rows, bit-exact; a row whose slot is outside 0 .. pool_rows - 1 is skipped,
+ * pool rows without a slot are untouched.  The slots of one call are distinct
+ * (those of vtmu_page_map are); where two rows name one slot, each element
+ * there comes from one of the two.
+ *   k_pool [pool_rows, k_width], v_pool [pool_rows, v_width], k_new [rows,
+ *     k_width], v_new [rows, v_width]: row-major f32, DEVICE; slots [rows]:
+ *     int32, DEVICE.  None may overlap another.
+ * Errors: VTMU_ERR_INVALID (null pointer with rows > 0, negative size,
+ * misaligned or overlapping buffers), VTMU_ERR_CUDA.
+ */
+VTMU_API vtmu_status vtmu_paged_write(float* k_pool, float* v_pool, int64_t pool_rows, int64_t k_width,
+                                      int64_t v_width, const float* k_new, const float* v_new,
+                                      const int32_t* slots, int64_t rows, cudaStream_t stream);
+
+/* Kernel choice of vtmu_paged_attention.  AUTO takes the tensor cores where
+ * they cover the call (headDim 64 or 128, page_size a multiple of 64 or one of
+ * 8, 16, 32; 16-byte aligned pools and, in a tree, k_new and v_new), else the
+ * CUDA cores (any headDim to 256, any page_size). */
+typedef enum vtmu_paged_kernel {
+    VTMU_PAGED_AUTO = 0,
+    VTMU_PAGED_CUDA_CORES = 1,
+    VTMU_PAGED_TENSOR_CORES = 2
+} vtmu_paged_kernel;
+
+/* Parameters of one paged attention call; fill with
+ * vtmu_paged_params_init(), then set fields. */
+typedef struct vtmu_paged_params {
+    int64_t rows;        /* packed query rows that the buffers hold (0 is a no-op) */
+    int64_t pages;       /* pages of the pools */
+    int32_t requests;    /* 1..1024 */
+    int32_t max_rows;    /* most rows of one request; with a tree at most 64 */
+    int32_t page_size;   /* cache rows per page, > 0 */
+    int32_t max_pages;   /* columns of the block table, > 0 */
+    int32_t heads;       /* query heads, > 0 */
+    int32_t kv_heads;    /* 0 means "= heads"; heads % kv_heads == 0 */
+    int32_t head_dim;    /* 1..256, of queries, keys and values */
+    int32_t tree;        /* 1: drafted rows beside the cache, with masks */
+    int32_t has_scale;   /* 0: scale = 1/sqrt(head_dim) */
+    float scale;         /* used when has_scale != 0; must be finite */
+    float softcap;       /* 0 = off; > 0: x = softcap * tanh(x / softcap) */
+    int32_t kernel;      /* vtmu_paged_kernel */
+    int64_t window;      /* 0 = off; a key at position s needs s > p - window */
+    int64_t sinks;       /* with a window: cache rows s < sinks stay visible */
+} vtmu_paged_params;
+
+/* Writes the defaults: everything 0 / off / AUTO. */
+VTMU_API void vtmu_paged_params_init(vtmu_paged_params* p);
+
+/* Scratch bytes that vtmu_paged_attention needs for `p` (partial results of
+ * requests whose keys are split over the GPU).  Errors: those of
+ * vtmu_paged_attention's parameter checks. */
+VTMU_API vtmu_status vtmu_paged_workspace_size(const vtmu_paged_params* p, size_t* bytes);
+
+/*
+ * op "attention" of a ragged batch over the paged cache.  Row t of request b
+ * attends with every head:
+ *   tree == 0: lens[b] rows are in the cache, the request's own rows T_b
+ *     among them as the last ones: row t sits at position p = lens[b] - T_b +
+ *     t and sees the cache rows s <= p;
+ *   tree == 1: the cache holds the context, lens[b] rows, and the drafted rows
+ *     are k_new / v_new [rows, kvHeads*headDim], not in the cache.  Row t sees
+ *     every row of the context and the drafted rows of its request whose bit
+ *     is set in masks[t]; its position is positions[t] (both as
+ *     vtmu_tree_plan writes them; positions is read with a window only and
+ *     may be NULL without one).
+ * With a window a key must also lie at s > p - window (drafted rows at their
+ * own positions), or among the first `sinks` cache rows.  Scores are scale *
+ * q.k, then softcap; the output is the max-subtracted softmax applied to the
+ * values.  A row that sees no key is written as zeros; keys and values that a
+ * row does not see do not enter it, whatever they hold.
+ *   q, out [rows, heads*headDim]; lens, cu_rows, block_table as for
+ *   vtmu_page_map.  Rows behind the last request, and a request's rows past
+ *   max_rows, are left as they were in out.  Lengths are clamped to 0 ..
+ *   max_pages * page_size; a page id outside 0 .. pages - 1 stands for rows of
+ *   zeros.  out must not overlap an input; k_new, v_new, masks and positions
+ *   are NULL without a tree.
+ *   workspace: DEVICE, at least vtmu_paged_workspace_size() bytes, 256-byte
+ *   aligned, no initial contents needed (the first 64 KiB, other calls'
+ *   arrival counters, are left alone); calls that share one must not overlap on
+ *   the GPU, replays of captured graphs included.
+ * Errors: VTMU_ERR_INVALID (null or misaligned pointer, bad size or
+ * parameter, tree arguments that disagree with p->tree, out overlapping an
+ * input), VTMU_ERR_UNSUPPORTED (head_dim above 256, more than 1024 requests,
+ * more than 64 rows in a tree, pools of 2^31 rows or more, a forced kernel
+ * that does not cover the call), VTMU_ERR_WORKSPACE, VTMU_ERR_CUDA.
+ */
+VTMU_API vtmu_status vtmu_paged_attention(const float* q, const float* k_pool, const float* v_pool,
+                                          const int32_t* block_table, const int32_t* lens,
+                                          const int32_t* cu_rows, const float* k_new, const float* v_new,
+                                          const uint64_t* masks, const int32_t* positions, float* out,
+                                          const vtmu_paged_params* p, void* workspace,
+                                          size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Kernel-side failures.  Every wait inside a kernel (TMA stage arrival,
  * stage release) gives up after one second instead of hanging the GPU; the
  * kernel then sets a bit in a device flag, abandons its output and returns.
