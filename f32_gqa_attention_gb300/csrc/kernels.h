@@ -202,5 +202,12 @@ struct PagedDesc {
     float qk_mul, cap_log2;
 };
 cudaError_t launch_paged_ffma(const PagedDesc& a, cudaStream_t stream);
+// The tensor-core kernel: headDim 64 or 128, pages of a multiple of 64 or of 8,
+// 16 or 32 rows; 16-byte aligned pools and new rows are checked at launch.
+constexpr int kPagedMaxCtas = 160;  // the workspace holds two partials for each
+bool paged_tc_supported(const PagedDesc& a);
+size_t paged_tc_workspace(const PagedDesc& a);
+cudaError_t launch_paged_tc(const PagedDesc& a, int num_sms, void* workspace, cudaStream_t stream);
+unsigned int paged_take_device_error();
 
 }  // namespace vtmu

@@ -1144,7 +1144,15 @@ vtmu_status vtmu_paged_workspace_size(const vtmu_paged_params* p, size_t* bytes)
     vtmu::PagedDesc a;
     vtmu_status st = resolve_paged(p, &a);
     if (st != VTMU_OK) return st;
-    *bytes = 0;
+    // AUTO may fall back to the CUDA cores by the pointers' alignment; it asks
+    // for the tensor cores' scratch all the same.
+    const bool tc = p->kernel != VTMU_PAGED_CUDA_CORES && vtmu::paged_tc_supported(a);
+    if (!tc && p->kernel == VTMU_PAGED_TENSOR_CORES)
+        return fail(VTMU_ERR_UNSUPPORTED,
+                    "paged: kernel TENSOR_CORES covers headDim 64 and 128 with page_size 8, 16, 32 or a multiple of 64 "
+                    "(got headDim %d, page_size %d)",
+                    a.D, a.page_size);
+    *bytes = tc ? vtmu::paged_tc_workspace(a) : 0;
     return ok();
 }
 
@@ -1183,11 +1191,23 @@ vtmu_status vtmu_paged_attention(const float* q, const float* k_pool, const floa
     a.masks = masks;
     a.positions = positions;
     a.out = out;
-    if (p->kernel == VTMU_PAGED_TENSOR_CORES)
-        return fail(VTMU_ERR_UNSUPPORTED, "paged: kernel TENSOR_CORES does not cover this call");
-    (void)workspace;
-    (void)workspace_bytes;
-    const cudaError_t e = vtmu::launch_paged_ffma(a, stream);
+    bool tc = p->kernel != VTMU_PAGED_CUDA_CORES && vtmu::paged_tc_supported(a);
+    if (tc && misaligned({k_pool, v_pool, k_new, v_new}, 15u)) tc = false;
+    if (!tc && p->kernel == VTMU_PAGED_TENSOR_CORES)
+        return fail(VTMU_ERR_UNSUPPORTED,
+                    "paged: kernel TENSOR_CORES covers headDim 64 and 128 with page_size 8, 16, 32 or a multiple of 64 "
+                    "and 16-byte aligned pools, k_new and v_new (got headDim %d, page_size %d)",
+                    a.D, a.page_size);
+    if (tc) {
+        const size_t need = vtmu::paged_tc_workspace(a);
+        if (!workspace || workspace_bytes < need)
+            return fail(VTMU_ERR_WORKSPACE, "paged attention needs a workspace of %zu bytes (got %zu)", need,
+                        workspace ? workspace_bytes : (size_t)0);
+        if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+            return fail(VTMU_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    }
+    const cudaError_t e =
+        tc ? vtmu::launch_paged_tc(a, device_sm_count(), workspace, stream) : vtmu::launch_paged_ffma(a, stream);
     if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
     return ok();
 }
@@ -1206,7 +1226,7 @@ vtmu_status vtmu_device_error(unsigned int* flags) {
     if (e != cudaSuccess) return cuda_fail(e, "device_error: synchronize");
     *flags = vtmu::decode_take_device_error() | vtmu::decode_tc_take_device_error() | vtmu::tc_take_device_error() |
              vtmu::mla_take_device_error() |
-             vtmu::mla_tc_take_device_error();
+             vtmu::mla_tc_take_device_error() | vtmu::paged_take_device_error();
     return ok();
 }
 

@@ -629,8 +629,8 @@ VTMU_API vtmu_status vtmu_paged_workspace_size(const vtmu_paged_params* p, size_
  *   tree == 1: the cache holds the context, lens[b] rows, and the drafted rows
  *     are k_new / v_new [rows, kvHeads*headDim], not in the cache.  Row t sees
  *     every row of the context and the drafted rows of its request whose bit
- *     is set in masks[t]; its position is positions[t] (both as
- *     vtmu_tree_plan writes them; positions is read with a window only and
+ *     is set in masks[t]; its position is positions[t], lens[b] or more (both
+ *     as vtmu_tree_plan writes them; positions is read with a window only and
  *     may be NULL without one).
  * With a window a key must also lie at s > p - window (drafted rows at their
  * own positions), or among the first `sinks` cache rows.  Scores are scale *
@@ -676,7 +676,8 @@ VTMU_API vtmu_status vtmu_paged_attention(const float* q, const float* k_pool, c
  * free score buffer, 0x2000000 drain (tensor-core kernel); tensor-core
  * decode bits: 0x4000000 ring item or query tiles, 0x8000000 free slot,
  * 0x10000000 split item, 0x20000000 score tile, 0x40000000 free score
- * buffer, 0x80000000 drain.  Errors: VTMU_ERR_INVALID (NULL flags), VTMU_ERR_CUDA.
+ * buffer, 0x80000000 drain; paged attention bits: 8 tile load, 16 free stage or
+ * drain, 32 score tile, probabilities or P.V product.  Errors: VTMU_ERR_INVALID (NULL flags), VTMU_ERR_CUDA.
  */
 VTMU_API vtmu_status vtmu_device_error(unsigned int* flags);
 

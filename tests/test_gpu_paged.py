@@ -227,3 +227,8 @@ def test_attention_cuda_core_shapes(case):
 @pytest.mark.parametrize("case", range(len(SHAPES)))
 def test_attention_cuda_cores(case):
     run_case(SHAPES[case], CUDA)
+
+
+@pytest.mark.parametrize("case", range(len(SHAPES)))
+def test_attention_tensor_cores(case):
+    run_case(SHAPES[case], TENSOR)
