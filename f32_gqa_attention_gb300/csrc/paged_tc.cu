@@ -53,6 +53,7 @@
 #include "launch_cache.h"
 #include "paged.cuh"
 #include "pdl.cuh"
+#include "softcap.cuh"
 #include "tcgen05_ops.cuh"
 #include "tma_sync.cuh"
 
@@ -67,6 +68,7 @@ constexpr int kKT = 64;        // keys per tile
 constexpr int kM = 128;        // virtual rows per row block
 constexpr int kThreads = 512;
 constexpr int kSplitWarps = 8;
+constexpr int kLast = 1 << 16;
 constexpr int kPShift = 14;    // probabilities are scaled to at most 2^14 in f16
 
 enum : unsigned int {
@@ -82,6 +84,7 @@ struct PgArgs {
     float* part_m;       // [2 CTAs][128]
     float* part_l;
     float* part_o;       // [2 CTAs][128][D]
+    float* odd;          // [CTAs][128][D]: values that are not finite
     int4* head;          // [CTAs]: the unit that a CTA starts and others go on with
 };
 
@@ -134,79 +137,99 @@ __device__ __forceinline__ Tiles tiles_of(const PagedDesc& a, const Req& r) {
     return t;
 }
 
+// A piece of a unit: what one CTA walks through, role by role.  Each warp keeps
+// its place in the list in shared memory (the roles' registers are full).
 struct Seg {
-    Req r;
-    Tiles t;
+    long long pos, end;  // tiles left to this CTA
+    int next_b;          // request of tile pos, or one before it
+    int row0, T, len, n; // Req
+    int lo_tile, n_sink, n_ctx, nt;  // Tiles; n_ctx: tiles of the cache, the drafted rows' tile follows
     int b, hk, rb;
-    int u0, u1;       // tiles of the unit, this CTA's
-    int slot;         // partial slot: 0 continues a unit, 1 starts one; -1: the whole unit
-    int last_team;    // slot 1: the team that ends the unit
+    int u0, u1;          // tiles of the unit, this CTA's
+    int slot;            // partial slot: 0 continues a unit, 1 starts one; -1: the whole unit
+    int last_team;       // slot 1: the team that ends the unit
 };
 
-struct Walk {
-    const PagedDesc& a;
-    const long long* prefix;
-    long long pos, end, total;
-    int b, team, member, teams;
-    __device__ __forceinline__ Walk(const PgArgs& g, const long long* prefix_) : a(g.a), prefix(prefix_) {
-        team = g.team;
-        member = blockIdx.x % team;
-        const int c = blockIdx.x / team;
-        total = prefix[a.B];
-        teams = (int)min((long long)(gridDim.x / team), total);
-        if (teams < 1) teams = 1;
-        pos = c < teams ? total * c / teams : 0;
-        end = c < teams ? total * (c + 1) / teams : 0;
-        b = 0;
-        int hi = a.B;  // the request of tile pos: the last one with prefix <= pos
-        while (hi - b > 1) {
-            const int mid = (b + hi) >> 1;
-            if (prefix[mid] <= pos) b = mid; else hi = mid;
-        }
+// This CTA's share of the list.  One lane.
+__device__ __noinline__ void walk_start(const PgArgs& g, const long long* prefix, Seg& s) {
+    const int c = blockIdx.x / g.team;
+    const long long total = prefix[g.a.B];
+    const long long teams = max(min((long long)(gridDim.x / g.team), total), 1ll);
+    s.pos = c < teams ? total * c / teams : 0;
+    s.end = c < teams ? total * (c + 1) / teams : 0;
+    int b = 0, hi = g.a.B;  // the last request whose prefix is at most pos
+    while (hi - b > 1) {
+        const int mid = (b + hi) >> 1;
+        if (prefix[mid] <= s.pos) b = mid; else hi = mid;
     }
-    // The next piece of a unit that this CTA has rows of; false at the end.  A
-    // piece may be empty (u1 <= u0) where causality leaves its tiles unseen.
-    __device__ __forceinline__ bool next(Seg& s) {
-        while (pos < end) {
-            while (prefix[b + 1] <= pos) ++b;
-            s.r = load_req(a, b);
-            s.t = tiles_of(a, s.r);
-            const int blocks = (s.r.T * a.G + kM - 1) / kM, groups = (blocks + team - 1) / team;
-            const long long rel = pos - prefix[b];
-            const long long unit = rel / s.t.nt;
-            s.u0 = (int)(rel - unit * s.t.nt);
-            s.u1 = (int)min((long long)s.t.nt, s.u0 + (end - pos));
-            const long long first = pos - s.u0;
-            pos += s.u1 - s.u0;
-            s.b = b;
-            s.hk = (int)(unit / groups);
-            s.rb = (int)(unit % groups) * team + member;
-            if (s.rb >= blocks) continue;
-            s.slot = s.u0 > 0 ? 0 : s.u1 < s.t.nt ? 1 : -1;
-            s.last_team = (int)(((first + s.t.nt) * teams - 1) / total);
-            if (!a.tree) {  // tiles past the block's last row's position
-                const int t_last = (min((s.rb + 1) * kM, s.r.T * a.G) - 1) / a.G;
-                const int p_last = s.r.len - s.r.n + t_last;
-                const int seen = p_last < 0 ? 0 : p_last / kKT + 1 - s.t.lo_tile;
-                int cap = s.t.n_sink + max(seen, 0);
-                if (cap < 1) cap = 1;  // a unit always has a first tile, so that its rows are written
-                s.u1 = min(s.u1, cap);
-            }
-            return true;
+    s.next_b = b;
+}
+
+// The next piece of a unit that this CTA has rows of; false at the end.  A
+// piece may be empty (u1 <= u0) where causality leaves its tiles unseen.  One lane.
+__device__ __noinline__ bool walk_next(const PgArgs& g, const long long* prefix, Seg& s) {
+    const PagedDesc& a = g.a;
+    const int team = g.team, member = blockIdx.x % team;
+    const long long total = prefix[a.B];
+    const long long teams = max(min((long long)(gridDim.x / team), total), 1ll);
+    while (s.pos < s.end) {
+        int b = s.next_b;
+        while (prefix[b + 1] <= s.pos) ++b;
+        s.next_b = b;
+        const Req r = load_req(a, b);
+        const Tiles t = tiles_of(a, r);
+        const int blocks = (r.T * a.G + kM - 1) / kM, groups = (blocks + team - 1) / team;
+        const long long rel = s.pos - prefix[b], unit = rel / t.nt;
+        const int u0 = (int)(rel - unit * t.nt);
+        int u1 = (int)min((long long)t.nt, u0 + (s.end - s.pos));
+        const long long first = s.pos - u0;
+        s.pos += u1 - u0;
+        const int rb = (int)(unit % groups) * team + member;
+        if (rb >= blocks) continue;
+        s.slot = u0 > 0 ? 0 : u1 < t.nt ? 1 : -1;
+        s.last_team = (int)(((first + t.nt) * teams - 1) / total);
+        if (!a.tree) {  // tiles past the block's last row's position
+            const int t_last = (min((rb + 1) * kM, r.T * a.G) - 1) / a.G;
+            const int p_last = r.len - r.n + t_last;
+            const int seen = p_last < 0 ? 0 : p_last / kKT + 1 - t.lo_tile;
+            int cap = t.n_sink + max(seen, 0);
+            if (cap < 1) cap = 1;  // a unit always has a first tile, so that its rows are written
+            u1 = min(u1, cap);
         }
-        return false;
+        s.row0 = r.row0;
+        s.T = r.T;
+        s.len = r.len;
+        s.n = r.n;
+        s.lo_tile = t.lo_tile;
+        s.n_sink = t.n_sink;
+        s.n_ctx = t.n_sink + t.n_main;
+        s.nt = t.nt;
+        s.b = b;
+        s.hk = (int)(unit / groups);
+        s.rb = rb;
+        s.u0 = u0;
+        s.u1 = u1;
+        return true;
     }
-};
+    return false;
+}
+// The same for a whole warp.
+__device__ __forceinline__ bool warp_next(const PgArgs& g, const long long* prefix, Seg& s) {
+    __syncwarp();  // every lane is done with the last piece
+    int more = 0;
+    if ((threadIdx.x & 31) == 0) more = walk_next(g, prefix, s);
+    return __shfl_sync(FULL, more, 0) != 0;  // orders lane 0's writes before the other lanes' reads
+}
 
 // First key of tile u, or -1 for the drafted rows' tile.
-__device__ __forceinline__ int tile_key(const Tiles& t, int tree, int u) {
-    if (u < t.n_sink) return u * kKT;
-    if (u < t.n_sink + t.n_main) return (t.lo_tile + u - t.n_sink) * kKT;
+__device__ __forceinline__ int tile_key(const Seg& s, int tree, int u) {
+    if (u < s.n_sink) return u * kKT;
+    if (u < s.n_ctx) return (s.lo_tile + u - s.n_sink) * kKT;
     return tree ? -1 : 0;  // 0: a unit without keys
 }
 // Rows of the tile that hold keys.
-__device__ __forceinline__ int tile_rows(const Req& r, int key) {
-    return key < 0 ? min(r.T, kKT) : max(min(r.len - key, kKT), 0);
+__device__ __forceinline__ int tile_rows(const Seg& s, int key) {
+    return key < 0 ? min(s.T, kKT) : max(min(s.len - key, kKT), 0);
 }
 
 // ---- f16 operands ---------------------------------------------------------------------
@@ -235,6 +258,24 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
+// Barrier over the four softmax warps; the AND of `v` over them.
+__device__ __forceinline__ bool rows_sync_and(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.and.pred p, 1, 128, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
+// True for one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
 // The power of two of a row whose largest |element| has the bits `top`: its
 // exponent, kept where both the scale and its inverse are normal and sums of
 // scaled probabilities stay finite.
@@ -244,8 +285,10 @@ __device__ __forceinline__ uint32_t row_exponent(uint32_t top) {
 }
 __device__ __forceinline__ float pow2_of(uint32_t biased) { return __uint_as_float(biased << 23); }
 
-// x0, x1 as f16 hi and lo pairs.
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+// A pair of f32 as f16 pairs hi and lo.
+__device__ __forceinline__ void split2(uint64_t x, uint32_t& hi, uint32_t& lo) {
+    float x0, x1;
+    f2_unpack(x, x0, x1);
     const __half2 h = __floats2half2_rn(x0, x1);
     const float2 f = __half22float2(h);
     const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
@@ -253,83 +296,255 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_
     lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
+// max(|x|, |y|), NaN if one of them is.
+__device__ __forceinline__ float abs_max(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(x)), "f"(fabsf(y)));
+    return r;
+}
+
 __device__ __forceinline__ float finite_or_zero(float x) {
     return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? 0.f : x;
 }
 
-// One raw tile (rows of D floats) to hi and lo tiles by the eight split warps,
+// One raw tile (rows of D floats) to its hi tile and, right behind it, its lo tile by the eight split warps,
 // eight rows each; the rows' inverse scales to `scale`.  Rows past `rows` are
 // zeros.  In value tiles elements that are not finite become zeros here, and
 // `bad` gets a bit for each row that had one (they are added in the fold, to
 // the rows that see them only); in key tiles they make their own scores
 // not finite, which the mask discards.
+__device__ __forceinline__ float4 lds4(uint32_t at) {
+    float4 x;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at));
+    return x;
+}
+__device__ __forceinline__ void sts2(uint32_t at, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+}
+
 template <int D, bool VALUES>
-__device__ __forceinline__ void split_tile(const unsigned char* raw, unsigned char* hi, unsigned char* lo,
-                                           float* scale, uint8_t* bad, int rows, int w, int lane) {
+__device__ __forceinline__ void split_tile(uint32_t raw, uint32_t hi, float* scale, uint8_t* bad, int rows, int w,
+                                           int lane) {
     constexpr int kLanes = D / 4;        // lanes per row
     constexpr int kRows = 32 / kLanes;   // rows per step
+    constexpr int kBatch = 4;            // steps whose chains overlap
+    asm volatile("" : "+r"(w), "+r"(lane));  // addresses are worked out here, not kept over the tile loop
     const int l = lane % kLanes, sub = lane / kLanes;
+    const uint32_t off0 = (l >> 4) * (kKT * 128) + (l & 1) * 8;
     uint32_t bad_bits = 0;
+    auto top_of = [](const float4& y) {  // bits of the row's largest |element|; NaN above all
+        uint32_t t = __float_as_uint(abs_max(abs_max(y.x, y.y), abs_max(y.z, y.w)));
+        if constexpr (kLanes == 32) {
+            return __reduce_max_sync(FULL, t);
+        } else {
 #pragma unroll
-    for (int i0 = 0; i0 < 8; i0 += 4) {
-        float4 x[4 / kRows];
+            for (int off = kLanes / 2; off > 0; off >>= 1) t = max(t, __shfl_xor_sync(FULL, t, off));
+            return t;
+        }
+    };
+#pragma unroll 1
+    for (int i0 = 0; i0 < 8; i0 += kBatch * kRows) {
+        const int r0 = 8 * w + i0 + sub;
+        float4 x[kBatch];
+        uint32_t top[kBatch], most = 0;
 #pragma unroll
-        for (int i = 0; i < 4 / kRows; ++i)
-            x[i] = *reinterpret_cast<const float4*>(raw + (size_t)(8 * w + i0 + i * kRows + sub) * D * 4 + l * 16);
+        for (int i = 0; i < kBatch; ++i)
+            x[i] = lds4(raw + (r0 + i * kRows) * D * 4 + l * 16);
+        if (8 * w + i0 + kBatch * kRows > rows) {  // the last tile of a cache, or drafted rows
 #pragma unroll
-        for (int i = 0; i < 4 / kRows; ++i) {
-            const int r = 8 * w + i0 + i * kRows + sub;
-            float4 v = x[i];
-            if (r >= rows) v = make_float4(0.f, 0.f, 0.f, 0.f);
-            auto top_of = [](const float4& y) {
-                return max(max(__float_as_uint(y.x) & 0x7fffffffu, __float_as_uint(y.y) & 0x7fffffffu),
-                           max(__float_as_uint(y.z) & 0x7fffffffu, __float_as_uint(y.w) & 0x7fffffffu));
-            };
-            auto row_max = [&](uint32_t t) {
-                if constexpr (kLanes == 32) {
-                    return __reduce_max_sync(FULL, t);
-                } else {
+            for (int i = 0; i < kBatch; ++i)
+                if (r0 + i * kRows >= rows) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
 #pragma unroll
-                    for (int off = kLanes / 2; off > 0; off >>= 1) t = max(t, __shfl_xor_sync(FULL, t, off));
-                    return t;
-                }
-            };
-            uint32_t top = row_max(top_of(v));
-            if (__any_sync(FULL, top >= 0x7f800000u)) {  // rare
+        for (int i = 0; i < kBatch; ++i) {
+            top[i] = top_of(x[i]);
+            most = max(most, top[i]);
+        }
+        if (__any_sync(FULL, most >= 0x7f800000u)) {  // rare
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const bool odd = top[i] >= 0x7f800000u;
                 if (VALUES) {
-                    const bool b = top >= 0x7f800000u;
-                    v = make_float4(finite_or_zero(v.x), finite_or_zero(v.y), finite_or_zero(v.z), finite_or_zero(v.w));
-                    top = row_max(top_of(v));
-                    const unsigned votes = __ballot_sync(FULL, b);
+                    x[i] = make_float4(finite_or_zero(x[i].x), finite_or_zero(x[i].y), finite_or_zero(x[i].z),
+                                       finite_or_zero(x[i].w));
+                    top[i] = top_of(x[i]);
+                    const unsigned votes = __ballot_sync(FULL, odd);
 #pragma unroll
                     for (int k = 0; k < kRows; ++k)
                         if ((votes >> (k * kLanes)) & 1u) bad_bits |= 1u << (i0 + i * kRows + k);
-                } else if (top >= 0x7f800000u) {
-                    top = 0x3f800000u;
+                } else if (odd) {
+                    top[i] = 0x3f800000u;
                 }
             }
-            const uint32_t e = row_exponent(top);
-            const float s = pow2_of(254u - e);
+        }
+        // Element 4 l of row r: block l / 16, 16-byte chunk (l % 16) / 2 of the
+        // row's 128 bytes, swizzled by r % 8.
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const uint32_t e = row_exponent(top[i]);
+            const float s1 = pow2_of(254u - e);
+            const uint64_t s2 = f2_pack(s1, s1);
             uint32_t h0, h1, l0, l1;
-            split2(v.x * s, v.y * s, h0, l0);
-            split2(v.z * s, v.w * s, h1, l1);
-            // Element 4 l of row r: block l / 16, 16-byte chunk (l % 16) / 2 of the
-            // row's 128 bytes, swizzled by r % 8.
-            const uint32_t off = (l >> 4) * (kKT * 128) + r * 128 + ((((l & 15) >> 1) ^ (r & 7)) << 4) + (l & 1) * 8;
-            *reinterpret_cast<uint2*>(hi + off) = make_uint2(h0, h1);
-            *reinterpret_cast<uint2*>(lo + off) = make_uint2(l0, l1);
+            split2(f2_mul(f2_pack(x[i].x, x[i].y), s2), h0, l0);
+            split2(f2_mul(f2_pack(x[i].z, x[i].w), s2), h1, l1);
+            const int r = r0 + i * kRows;
+            const uint32_t off = off0 + r * 128 + ((((l & 15) >> 1) ^ (r & 7)) << 4);
+            sts2(hi + off, h0, h1);
+            sts2(hi + Cfg<D>::kHalf + off, l0, l1);
             if (l == 0) scale[r] = pow2_of(e);
         }
     }
     if (VALUES && lane == 0) bad[w] = (uint8_t)bad_bits;
 }
 
+// mbar_wait, bounded in the same way, that looks at the clock after every 64 tries only:
+// half of the warps wait at any time here, and what they execute takes issue slots
+// from the rest (a look at the clock per try was half of all instructions).
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = global_ns();
+    do {
+#pragma unroll 4
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+    } while (global_ns() - t0 <= kWaitLimitNs);
+    return false;
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity);
+}
+
+// Values that are not finite would reach every row of a tile through 0 x inf =
+// NaN, so the tile has zeros in their place and they are added here, to the rows
+// that see them.  `rows_bad`: such keys of the tile; columns col .. col + n of each
+// go to `odd` (thread-private; `more`: it holds earlier ones already).
+__device__ __noinline__ bool add_odd_values(const PagedDesc& a, int4 tile, uint64_t rows_bad, float* odd, int col, int n,
+                                            bool more) {
+    const int D = a.D;
+    while (rows_bad) {
+        const int k = __ffsll((long long)rows_bad) - 1;
+        rows_bad &= rows_bad - 1;
+        const float* src;
+        if (tile.z < 0) {
+            src = a.v_new + (packed_rows(a.cu_rows, tile.y, a.rows).row0 + k) * a.Hk * D;
+        } else {
+            const int key = tile.z + k;
+            const int64_t page = __ldg(a.block_table + (int64_t)tile.y * a.max_pages + key / a.page_size);
+            if (page < 0 || page >= a.pages) continue;
+            src = a.v_pool + (page * a.page_size + key % a.page_size) * a.Hk * D;
+        }
+        src += (int64_t)tile.w * D + col;
+        for (int d = 0; d < n; ++d) {
+            const float x = src[d];
+            const float y = (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? x : 0.f;
+            odd[d] = more ? odd[d] + y : y;
+        }
+        more = true;
+    }
+    return more;
+}
+// ... and from there to the row's output once it is written.
+__device__ __noinline__ bool join_odd_values(float* to, const float* odd, int n) {
+    for (int d = 0; d < n; ++d) to[d] += odd[d];
+    return false;
+}
+
+// ---- softmax of one row of a tile -----------------------------------------------------
+// What a thread needs of the tile: its scores (TMEM columns `at`), the keys' and
+// values' scales, the mask.
+struct RowTile {
+    uint32_t at;
+    const float* ks;      // [64] key scales
+    const float* vs;      // [64] value scales; WHOLE: already times 2^kPShift / the largest
+    uint64_t see;         // keys that the row sees (not read when WHOLE)
+    float qs;             // the query's scale
+    float cap;            // softcap in base-2 units
+    float v_mul;          // not WHOLE: 2^kPShift / the largest value scale seen
+};
+
+// 32 scores from key 32 c on, masked.  With a cap they come in base-2 units,
+// else q.k times the key's scale alone: the query's is left to the exponent's FMA.
+template <bool CAP, bool WHOLE>
+__device__ __forceinline__ void row_scores(const RowTile& r, int c, float (&x)[32]) {
+    tmem_ld32(r.at + 32 * c, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+        const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(r.ks + 32 * c + k);
+        f2_unpack(f2_mul(f2_pack(x[k], x[k + 1]), ks.x), x[k], x[k + 1]);
+        f2_unpack(f2_mul(f2_pack(x[k + 2], x[k + 3]), ks.y), x[k + 2], x[k + 3]);
+    }
+    if constexpr (CAP) softcap_tile<32>(x, r.qs, r.cap);
+    if constexpr (!WHOLE) {
+        const uint32_t bits = (uint32_t)(r.see >> (32 * c));
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = (bits >> k) & 1u ? x[k] : -INFINITY;
+    }
+}
+
+// The online softmax's step: m and l move on, P goes over the scores (keys 32 c
+// .. as f16 hi in 16 columns, lo in 16).  Returns alpha.  The scores are read
+// twice, for the maximum and for the probabilities: 64 of them do not fit the
+// registers at once.
+template <bool CAP, bool WHOLE>
+__device__ __forceinline__ float row_softmax(const RowTile& r, float& m, float& l) {
+    float mt = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+        float x[32];
+        row_scores<CAP, WHOLE>(r, c, x);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) mt = fmaxf(fmaxf(mt, x[k]), x[k + 1]);
+    }
+    const float mul = CAP ? 1.f : r.qs;
+    const float mn = fmaxf(m, mt * mul), mu = mn == -INFINITY ? 0.f : mn;
+    const float alpha = fast_exp2(m - mu);
+    m = mn;
+    const uint64_t mul2 = f2_pack(mul, mul), mu2 = f2_pack(-mu, -mu), v2 = f2_pack(r.v_mul, r.v_mul);
+    uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+        float x[32];
+        row_scores<CAP, WHOLE>(r, c, x);
+        float phi[16], plo[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+            const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(r.vs + 32 * c + k);
+            float e0, e1, e2, e3;
+            f2_unpack(f2_fma(f2_pack(x[k], x[k + 1]), mul2, mu2), e0, e1);
+            f2_unpack(f2_fma(f2_pack(x[k + 2], x[k + 3]), mul2, mu2), e2, e3);
+            uint64_t p0 = f2_pack(fast_exp2(e0), fast_exp2(e1)), p1 = f2_pack(fast_exp2(e2), fast_exp2(e3));
+            sum0 = f2_add(sum0, p0);
+            sum1 = f2_add(sum1, p1);
+            p0 = f2_mul(p0, w.x);
+            p1 = f2_mul(p1, w.y);
+            if constexpr (!WHOLE) {
+                p0 = f2_mul(p0, v2);
+                p1 = f2_mul(p1, v2);
+            }
+            uint32_t h0, l0, h1, l1;
+            split2(p0, h0, l0);
+            split2(p1, h1, l1);
+            phi[k / 2] = __uint_as_float(h0);
+            phi[k / 2 + 1] = __uint_as_float(h1);
+            plo[k / 2] = __uint_as_float(l0);
+            plo[k / 2 + 1] = __uint_as_float(l1);
+        }
+        tmem_st16(r.at + 32 * c, phi);
+        tmem_st16(r.at + 32 * c + 16, plo);
+    }
+    float a0, a1, b0, b1;
+    f2_unpack(sum0, a0, a1);
+    f2_unpack(sum1, b0, b1);
+    l = fmaf(l, alpha, (a0 + a1) + (b0 + b1));
+    return alpha;
+}
+
 // ---- the kernel -------------------------------------------------------------------------
-template <int D>
+template <int D, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
-                    const PgArgs g) {
+                    const __grid_constant__ PgArgs g) {
     using C = Cfg<D>;
     constexpr int ST = C::kStages;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -343,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         o_full[2], o_free[2];
     __shared__ uint32_t tmem_base_s;
     __shared__ long long scan_s[kThreads / 32];
+    __shared__ Seg seg_s[kThreads / 32];
     // What tile n leaves for the roles that come later, at n % 4 (each is read
     // before the splitters can reach tile n + 4).
     __shared__ __align__(16) float k_scale[4][kKT], v_scale[4][kKT];
@@ -350,13 +566,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ float q_scale[4][kM];             // by piece % 4
     __shared__ float2 fold_f[4][kM];             // alpha, output scale
     __shared__ uint64_t row_bad[4][kM];          // values to add that are not finite
-    __shared__ int4 tile_at[4];                  // last tile of its piece, request, first key, KV head
+    __shared__ int4 tile_at[4];                  // rows of the block (kLast: last tile of its piece), request, first key, KV head
     __shared__ float* row_out[4][kM];            // last tile of a piece: where the row goes
     __shared__ float row_inv[4][kM];
     __shared__ __align__(16) float v_norm[4][kKT];  // per softmax warp: value scales of a tile all rows see
 
     const PagedDesc& a = g.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform, to the compiler too
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
@@ -411,8 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
 
-    Walk walk(g, prefix);
-    Seg s;
+    Seg& s = seg_s[warp];
+    if (lane == 0) walk_start(g, prefix, s);
 
     if (warp == 0) {
         // ---- producer: raw K and V tiles --------------------------------------------
@@ -424,11 +640,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nowhere = (int)(a.pages * a.page_size);  // a row out of bounds: zeros
         int it = 0;
         bool ok = true;
-        while (ok && walk.next(s)) {
+        while (ok && warp_next(g, prefix, s)) {
             int batch = -1, y_cur = nowhere;
-            const int subs = (s.r.len + g.sub - 1) / g.sub;
+            const int subs = (s.len + g.sub - 1) / g.sub;
             for (int u = s.u0; ok && u < s.u1; ++u) {
-                const int key = tile_key(s.t, a.tree, u);
+                const int key = tile_key(s, a.tree, u);
                 int y = nowhere;
                 if (key >= 0) {
                     const int q0 = key / g.sub;
@@ -447,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++it) {
                     const int st = it % ST;
-                    if (it >= ST && !__all_sync(FULL, mbar_wait(&raw_empty[st], (uint32_t)((it / ST - 1) & 1)))) {
+                    if (it >= ST && !__all_sync(FULL, wait_for(&raw_empty[st], (uint32_t)((it / ST - 1) & 1)))) {
                         raise_device_error(&g_paged_device_error, kErrPgFree);
                         ok = false;
                         break;
@@ -456,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     unsigned char* dst = raw + (size_t)st * C::kRaw;
                     if (key < 0) {
-                        if (lane == 0) tma_load_2d(dst, kv ? &tm_vn : &tm_kn, s.hk * D, s.r.row0, &raw_full[st]);
+                        if (lane == 0) tma_load_2d(dst, kv ? &tm_vn : &tm_kn, s.hk * D, s.row0, &raw_full[st]);
                     } else if (lane < nsub) {
                         tma_load_2d(dst + (size_t)lane * g.sub * D * 4, kv ? &tm_v : &tm_k, s.hk * D, y, &raw_full[st]);
                     }
@@ -465,70 +681,80 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // No copy may be in flight when the CTA exits.
         for (int j = it < ST ? 0 : it - ST; j < it; ++j)
-            if (!mbar_wait(&raw_full[j % ST], (uint32_t)((j / ST) & 1)))
+            if (!wait_for(&raw_full[j % ST], (uint32_t)((j / ST) & 1)))
                 raise_device_error(&g_paged_device_error, kErrPgFree);
     } else if (warp == 1) {
-        // ---- MMAs ------------------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_f16(kM, kKT, false), id_o = idesc_f16(kM, D, true);
-            int n = 0;
-            bool ok = true;
-            auto pv = [&](int j) -> bool {  // O(j) = P(j).V(j)
-                const int bf = j & 1;
-                const uint32_t ph = (uint32_t)((j >> 1) & 1);
-                if (!mbar_wait(&p_full[bf], ph) || !mbar_wait(&v_ready[bf], ph) ||
-                    (j >= 2 && !mbar_wait(&o_free[bf], ph ^ 1u))) {
-                    raise_device_error(&g_paged_device_error, kErrPgMma);
-                    return false;
-                }
-                tc_fence_after();
-                const uint32_t d = tmem + C::kColO + bf * D;
-                const uint32_t phi = tmem + C::kColS + bf * kKT, plo = phi + kKT / 2;
-                const uint64_t vhi = smem_desc_mn(vt + bf * 2 * C::kHalf, C::kBlock);
-                const uint64_t vlo = smem_desc_mn(vt + bf * 2 * C::kHalf + C::kHalf, C::kBlock);
+        // ---- MMAs: the warp stays together and one elected lane issues (behind a
+        // lane == 0 test an MMA took 45 cycles to issue, behind elect 10) ----
+        constexpr uint32_t id_s = idesc_f16(kM, kKT, false), id_o = idesc_f16(kM, D, true);
+        const uint32_t tm = __shfl_sync(FULL, tmem, 0);
+        const uint64_t khi = smem_desc_sw128(kt), klo = smem_desc_sw128(kt + C::kHalf);
+        int n = 0;
+        bool ok = true;
+        auto pv = [&](int j) -> bool {  // O(j) = P(j).V(j)
+            const int bf = j & 1;
+            const uint32_t ph = (uint32_t)((j >> 1) & 1);
+            if (!__all_sync(FULL, wait_for(&p_full[bf], ph) && wait_for(&v_ready[bf], ph) &&
+                                      (j < 2 || wait_for(&o_free[bf], ph ^ 1u)))) {
+                raise_device_error(&g_paged_device_error, kErrPgMma);
+                return false;
+            }
+            tc_fence_after();
+            const uint32_t d = tm + C::kColO + bf * D;
+            const uint32_t p = tm + C::kColS + bf * kKT;  // 32 keys: hi in 16 columns, lo in 16
+            const uint64_t vhi = smem_desc_mn(vt, C::kBlock) + bf * (2 * C::kHalf >> 4);
+            const uint64_t vlo = vhi + (C::kHalf >> 4);
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kKT / 16; ++k) {  // 16 keys: 8 columns of P, 16 rows (2048 bytes) of V
-                    mma_f16_ts(d, phi + 8 * k, vhi + 128 * k, id_o, k > 0 ? 1u : 0u);
-                    mma_f16_ts(d, plo + 8 * k, vhi + 128 * k, id_o, 1u);
-                    mma_f16_ts(d, phi + 8 * k, vlo + 128 * k, id_o, 1u);
+                    const uint32_t phi = p + 32 * (k >> 1) + 8 * (k & 1), plo = phi + 16;
+                    mma_f16_ts(d, phi, vhi + 128 * k, id_o, k > 0 ? 1u : 0u);
+                    mma_f16_ts(d, plo, vhi + 128 * k, id_o, 1u);
+                    mma_f16_ts(d, phi, vlo + 128 * k, id_o, 1u);
                 }
                 mma_commit(&o_full[bf]);
-                return true;
-            };
-            while (ok && walk.next(s)) {
-                for (int u = s.u0; ok && u < s.u1; ++u, ++n) {
-                    if (!mbar_wait(&k_ready, (uint32_t)(n & 1))) {
-                        raise_device_error(&g_paged_device_error, kErrPgMma);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d = tmem + C::kColS + (n & 1) * kKT;
-                    const uint64_t khi = smem_desc_sw128(kt), klo = smem_desc_sw128(kt + C::kHalf);
+            }
+            __syncwarp();
+            return true;
+        };
+        while (ok && warp_next(g, prefix, s)) {
+            const int u1 = s.u1;
+            for (int u = s.u0; u < u1; ++u, ++n) {
+                if (!__all_sync(FULL, wait_for(&k_ready, (uint32_t)(n & 1)))) {
+                    raise_device_error(&g_paged_device_error, kErrPgMma);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tm + C::kColS + (n & 1) * kKT;
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {  // 16 dims: 8 columns of Q, 32 bytes of a K row
                         const uint64_t off = (uint64_t)(k >> 2) * (C::kBlock >> 4) + 2 * (k & 3);
-                        mma_f16_ts(d, tmem + C::kColQhi + 8 * k, khi + off, id_s, k > 0 ? 1u : 0u);
-                        mma_f16_ts(d, tmem + C::kColQlo + 8 * k, khi + off, id_s, 1u);
-                        mma_f16_ts(d, tmem + C::kColQhi + 8 * k, klo + off, id_s, 1u);
+                        mma_f16_ts(d, tm + C::kColQhi + 8 * k, khi + off, id_s, k > 0 ? 1u : 0u);
+                        mma_f16_ts(d, tm + C::kColQlo + 8 * k, khi + off, id_s, 1u);
+                        mma_f16_ts(d, tm + C::kColQhi + 8 * k, klo + off, id_s, 1u);
                     }
                     mma_commit(&k_free);
                     mma_commit(&s_full[n & 1]);
-                    if (n > 0 && !pv(n - 1)) ok = false;
+                }
+                __syncwarp();
+                if (n > 0 && !pv(n - 1)) {
+                    ok = false;
+                    break;
                 }
             }
-            if (ok && n > 0) pv(n - 1);
         }
+        if (ok && n > 0) pv(n - 1);
     } else if (warp >= 4 && warp < 8) {
         // ---- softmax: thread = virtual row -------------------------------------------
         const int i = threadIdx.x - 128;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         int n = 0, piece = 0;
         bool ok = true;
-        while (ok && walk.next(s)) {
+        while (ok && warp_next(g, prefix, s)) {
             const int v = s.rb * kM + i, t = v / a.G;
-            const bool alive = v < s.r.T * a.G;
-            const int64_t row = (int64_t)s.r.row0 + (alive ? t : 0);
+            const bool alive = v < s.T * a.G;
             const int64_t prow = (int64_t)(2 * blockIdx.x + (s.slot > 0 ? 1 : 0)) * kM + i;  // of the partials
             if (s.slot > 0 && i == 0)
                 g.head[blockIdx.x] = make_int4(s.last_team, s.hk, s.rb, s.b);
@@ -540,137 +766,91 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             // Keys of the cache that the row sees: [lo, hi], and those before `sinks`.
-            int64_t p = a.tree ? (int64_t)s.r.len : (int64_t)s.r.len - s.r.n + t;
-            if (a.tree && a.window > 0 && alive) p = __ldg(a.positions + row);
-            const int64_t hi = a.tree ? s.r.len - 1 : min(p, (int64_t)s.r.len - 1);
-            const int64_t lo = a.window > 0 ? max(p - a.window + 1, (int64_t)0) : 0;
+            int p = a.tree ? s.len : s.len - s.n + t;
+            if (a.tree && a.window > 0 && alive) p = __ldg(a.positions + s.row0 + t);
+            const int hi = a.tree ? s.len - 1 : min(p, s.len - 1);
+            const int lo = a.window > 0 ? (int)max((int64_t)p - a.window + 1, (int64_t)0) : 0;
+            const int sinks = (int)min(a.sinks, (int64_t)s.len);
             float m = -INFINITY, l = 0.f;
-            const bool idle = !__any_sync(FULL, alive);  // a warp without rows only keeps step
-            for (int u = s.u0; u < s.u1; ++u, ++n) {
-                const int key = tile_key(s.t, a.tree, u), nb = n & 3, bf = n & 1;
-                if (!__all_sync(FULL, mbar_wait(&s_full[bf], (uint32_t)((n >> 1) & 1)) &&
-                                          mbar_wait(&v_ready[bf], (uint32_t)((n >> 1) & 1)))) {
+            const int rows = min(s.T * a.G - s.rb * kM, kM), tiles = s.u1 - s.u0;
+            // A warp without rows waits at the barrier that ends the piece; the first
+            // warp, which always has one, arrives for it.
+            const int arrivals = warp == 4 ? 4 - (rows + 31) / 32 + 1 : 1;
+            for (int u = s.u0; u < s.u1 && __any_sync(FULL, alive); ++u, ++n) {
+                const int key = tile_key(s, a.tree, u), nb = n & 3, bf = n & 1;
+                if (!__all_sync(FULL, wait_for(&s_full[bf], (uint32_t)((n >> 1) & 1)) &&
+                                          wait_for(&v_ready[bf], (uint32_t)((n >> 1) & 1)))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
                     break;
                 }
-                if (idle) {
-                    row_out[nb][i] = nullptr;
-                    row_bad[nb][i] = 0;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[bf]);
-                    continue;
-                }
                 uint64_t see = ~0ull;  // rows of no request: anything
                 if (alive) {
-                    auto below = [](int64_t c) -> uint64_t { return c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1; };
+                    auto below = [](int c) -> uint64_t { return c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1; };
                     if (key >= 0) {
-                        see = below(hi - key + 1) & (~below(lo - key) | below(a.sinks - key));
+                        see = below(hi - key + 1) & (~below(lo - key) | below(sinks - key));
                     } else {
-                        see = __ldg(reinterpret_cast<const unsigned long long*>(a.masks) + row) & below(s.r.T);
+                        see = __ldg(reinterpret_cast<const unsigned long long*>(a.masks) + s.row0 + t) & below(s.T);
                         if (a.window > 0)
-                            for (int j = 0; j < s.r.T; ++j)
-                                if (__ldg(a.positions + s.r.row0 + j) <= p - a.window) see &= ~(1ull << j);
+                            for (int j = 0; j < s.T; ++j)
+                                if (__ldg(a.positions + s.row0 + j) <= p - a.window) see &= ~(1ull << j);
                     }
                 }
                 tc_fence_after();
-                float x[kKT];
-                tmem_ld32(tmem + lanes + C::kColS + bf * kKT, x);
-                tmem_ld32(tmem + lanes + C::kColS + bf * kKT + 32, x + 32);
-                tmem_wait_ld();
-                const float qs = q_scale[piece & 3][i];
-                const bool whole = __all_sync(FULL, see == ~0ull);
-#pragma unroll
-                for (int k = 0; k < kKT; k += 4) {
-                    const float4 ks = *reinterpret_cast<const float4*>(&k_scale[nb][k]);
-                    x[k] *= ks.x;
-                    x[k + 1] *= ks.y;
-                    x[k + 2] *= ks.z;
-                    x[k + 3] *= ks.w;
-                }
-                float mul = qs;  // x * mul is the score in base-2 units
-                if (a.softcap_on) {
-#pragma unroll
-                    for (int k = 0; k < kKT; ++k) x[k] = softcap_tanh(x[k] * qs);
-                    mul = a.cap_log2;
-                }
-                // The largest value scale among the keys seen.
+                RowTile rt;
+                rt.at = tmem + lanes + C::kColS + bf * kKT;
+                rt.ks = k_scale[nb];
+                rt.see = see;
+                rt.qs = q_scale[piece & 3][i];
+                rt.cap = a.cap_log2;
+                // The largest value scale among the keys seen sets the probabilities'.
                 uint32_t vtop;
-                if (whole) {
-                    const float2 v2 = make_float2(v_scale[nb][lane], v_scale[nb][lane + 32]);
-                    vtop = __reduce_max_sync(FULL, max(__float_as_uint(v2.x), __float_as_uint(v2.y)));
-                } else {
-                    float vm = pow2_of(27u);
-#pragma unroll
-                    for (int k = 0; k < kKT; ++k) {
-                        const bool vis = (see >> k) & 1;
-                        x[k] = vis ? x[k] : -INFINITY;
-                        vm = fmaxf(vm, vis ? v_scale[nb][k] : 0.f);
-                    }
-                    vtop = __float_as_uint(vm);
-                }
-                const float c = pow2_of(254u + kPShift - (vtop >> 23));  // 2^kPShift / the largest scale
-                if (whole) {
-                    v_norm[warp & 3][lane] = v_scale[nb][lane] * c;
-                    v_norm[warp & 3][lane + 32] = v_scale[nb][lane + 32] * c;
+                float alpha;
+                if (__all_sync(FULL, see == ~0ull)) {
+                    const float v0 = v_scale[nb][lane], v1 = v_scale[nb][lane + 32];
+                    vtop = __reduce_max_sync(FULL, max(__float_as_uint(v0), __float_as_uint(v1)));
+                    const float c = pow2_of(254u + kPShift - (vtop >> 23));
+                    v_norm[warp & 3][lane] = v0 * c;
+                    v_norm[warp & 3][lane + 32] = v1 * c;
                     __syncwarp();
+                    rt.vs = v_norm[warp & 3];
+                    rt.v_mul = 1.f;
+                    alpha = row_softmax<CAP, true>(rt, m, l);
+                } else {
+                    vtop = 27u << 23;
+#pragma unroll 4
+                    for (int k = 0; k < kKT; ++k)
+                        if ((see >> k) & 1) vtop = max(vtop, __float_as_uint(v_scale[nb][k]));
+                    rt.vs = v_scale[nb];
+                    rt.v_mul = pow2_of(254u + kPShift - (vtop >> 23));
+                    alpha = row_softmax<CAP, false>(rt, m, l);
                 }
-                float mt = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < kKT; ++k) mt = fmaxf(mt, x[k]);
-                const float mn = fmaxf(m, mt * mul), mu = mn == -INFINITY ? 0.f : mn;
-                const float alpha = fast_exp2(m - mu);
-                m = mn;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                const float* vs = whole ? v_norm[warp & 3] : v_scale[nb];
-                const float cc = whole ? 1.f : c;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float phi[16], plo[16];
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 w = *reinterpret_cast<const float4*>(&vs[32 * h + k]);
-                        const float e0 = fast_exp2(fmaf(x[32 * h + k], mul, -mu)), e1 = fast_exp2(fmaf(x[32 * h + k + 1], mul, -mu)),
-                                    e2 = fast_exp2(fmaf(x[32 * h + k + 2], mul, -mu)), e3 = fast_exp2(fmaf(x[32 * h + k + 3], mul, -mu));
-                        sum[0] += e0;
-                        sum[1] += e1;
-                        sum[2] += e2;
-                        sum[3] += e3;
-                        uint32_t h0, l0, h1, l1;
-                        split2(e0 * w.x * cc, e1 * w.y * cc, h0, l0);
-                        split2(e2 * w.z * cc, e3 * w.w * cc, h1, l1);
-                        phi[k / 2] = __uint_as_float(h0);
-                        phi[k / 2 + 1] = __uint_as_float(h1);
-                        plo[k / 2] = __uint_as_float(l0);
-                        plo[k / 2 + 1] = __uint_as_float(l1);
-                    }
-                    tmem_st16(tmem + lanes + C::kColS + bf * kKT + 16 * h, phi);
-                    tmem_st16(tmem + lanes + C::kColS + bf * kKT + kKT / 2 + 16 * h, plo);
-                }
-                l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
                 fold_f[nb][i] = make_float2(alpha, pow2_of((vtop >> 23) - kPShift));
                 const uint64_t bad = *reinterpret_cast<const uint64_t*>(v_bad[nb]);
-                if (bad) row_bad[nb][i] = alive ? bad & see : 0ull;
+                if (bad) row_bad[nb][i] = bad & see;
                 if (u == s.u1 - 1) {
-                    float* to = nullptr;
+                    float* to = g.part_o + prow * D;
                     float inv = 1.f;
                     if (s.slot < 0) {
-                        if (alive) to = a.out + (row * a.H + (int64_t)s.hk * a.G + (v - t * a.G)) * D;
+                        to = a.out + (((int64_t)s.row0 + t) * a.H + (int64_t)s.hk * a.G + (v - t * a.G)) * D;
                         inv = l != 0.f ? 1.f / l : 0.f;
                     } else {
-                        if (alive) to = g.part_o + prow * D;
                         g.part_m[prow] = m;
                         g.part_l[prow] = l;
                     }
                     row_out[nb][i] = to;
                     row_inv[nb][i] = inv;
                 }
-                if (i == 0) tile_at[nb] = make_int4(u == s.u1 - 1, s.b, key, s.hk);
+                if (i == 0) tile_at[nb] = make_int4(rows + (u == s.u1 - 1 ? kLast : 0), s.b, key, s.hk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[bf]);
+                if (lane == 0) mbar_arrive_n(&p_full[bf], arrivals);
             }
+            if (!__any_sync(FULL, alive)) n += tiles;
+            // One barrier a piece keeps the four warps' tile counts together; a failed
+            // wait ends the role for all of them.
+            ok = rows_sync_and(ok);
             ++piece;
         }
     } else if (warp >= 8) {
@@ -680,104 +860,100 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = 32 * quarter + lane;
         float o[D / 2];
 #pragma unroll
-        for (int d = 0; d < D / 2; ++d) o[d] = 0.f;
+        for (int d = 0; d < D / 2; ++d) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(o[d]));
         int n = 0, piece = 0, it = 0;
-        bool ok = true;
+        bool ok = true, odd = false;
         auto fold = [&](int j) -> bool {
             const int nb = j & 3, bf = j & 1;
-            if (!__all_sync(FULL, mbar_wait(&o_full[bf], (uint32_t)((j >> 1) & 1)))) {
+            if (!__all_sync(FULL, wait_for(&o_full[bf], (uint32_t)((j >> 1) & 1)))) {
                 raise_device_error(&g_paged_device_error, kErrPgMma);
                 return false;
             }
             tc_fence_after();
-            const float2 f = fold_f[nb][i];
-            const uint32_t at = tmem + lanes + C::kColO + bf * D + side * (D / 2);
+            const int4 ta = tile_at[nb];
+            const int rows = ta.x & (kLast - 1);
+            if (32 * quarter < rows) {
+                const float2 f = fold_f[nb][i];
+                const uint64_t fx = f2_pack(f.x, f.x), fy = f2_pack(f.y, f.y);
+                const uint32_t at = tmem + lanes + C::kColO + bf * D + side * (D / 2);
 #pragma unroll
-            for (int c0 = 0; c0 < D / 2; c0 += 16) {
-                float acc[16];
-                tmem_ld16(at + c0, acc);
-                tmem_wait_ld();
+                for (int c0 = 0; c0 < D / 2; c0 += 16) {
+                    float acc[16];
+                    tmem_ld16(at + c0, acc);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int d = 0; d < 16; ++d) o[c0 + d] = fmaf(acc[d], f.y, o[c0 + d] * f.x);
+                    for (int d = 0; d < 16; d += 2)
+                        f2_unpack(f2_fma(f2_pack(acc[d], acc[d + 1]), fy, f2_mul(f2_pack(o[c0 + d], o[c0 + d + 1]), fx)),
+                                  o[c0 + d], o[c0 + d + 1]);
+                }
+                tc_fence_before();
             }
-            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_free[bf]);
-            const int4 ta = tile_at[nb];
-            if (*reinterpret_cast<const uint64_t*>(v_bad[nb])) {
-                // Values that are not finite, for the rows that see them.
-                uint64_t rest = row_bad[nb][i];
-                while (rest) {
-                    const int k = __ffsll((long long)rest) - 1;
-                    rest &= rest - 1;
-                    const float* src = nullptr;
-                    if (ta.z < 0) {
-                        src = a.v_new + (packed_rows(a.cu_rows, ta.y, a.rows).row0 + k) * a.Hk * D;
-                    } else {
-                        const int key = ta.z + k;
-                        const int64_t page = __ldg(a.block_table + (int64_t)ta.y * a.max_pages + key / a.page_size);
-                        if (page >= 0 && page < a.pages)
-                            src = a.v_pool + (page * a.page_size + key % a.page_size) * a.Hk * D;
-                    }
-                    if (!src) continue;
-                    src += (int64_t)ta.w * D + side * (D / 2);
+            if (*reinterpret_cast<const uint64_t*>(v_bad[nb]) && i < rows && row_bad[nb][i])  // rare
+                odd = add_odd_values(a, ta, row_bad[nb][i], g.odd + ((int64_t)blockIdx.x * kM + i) * D + side * (D / 2),
+                                     side * (D / 2), D / 2, odd);
+            if (ta.x & kLast) {
+                if (i < rows) {
+                    float* to = row_out[nb][i] + side * (D / 2);
+                    const float inv = row_inv[nb][i];
 #pragma unroll
-                    for (int d = 0; d < D / 2; ++d) {
-                        const float x = __ldg(src + d);
-                        if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) o[d] += x;
-                    }
+                    for (int d = 0; d < D / 2; d += 4)
+                        *reinterpret_cast<float4*>(to + d) =
+                            make_float4(o[d] * inv, o[d + 1] * inv, o[d + 2] * inv, o[d + 3] * inv);
+                    if (odd) odd = join_odd_values(to, g.odd + ((int64_t)blockIdx.x * kM + i) * D + side * (D / 2), D / 2);
                 }
-            }
-            if (ta.x) {
-                float* to = row_out[nb][i];
-                const float inv = row_inv[nb][i];
-                if (to) {
-                    to += side * (D / 2);
-                    if (reinterpret_cast<uintptr_t>(to) & 15u) {
+                // Opaque zeros: as constants they make the compiler keep a second copy of
+                // the loop's registers, and spill.
 #pragma unroll
-                        for (int d = 0; d < D / 2; ++d) to[d] = o[d] * inv;
-                    } else {
-#pragma unroll
-                        for (int d = 0; d < D / 2; d += 4)
-                            *reinterpret_cast<float4*>(to + d) =
-                                make_float4(o[d] * inv, o[d + 1] * inv, o[d + 2] * inv, o[d + 3] * inv);
-                    }
-                }
-#pragma unroll
-                for (int d = 0; d < D / 2; ++d) o[d] = 0.f;
+                for (int d = 0; d < D / 2; ++d) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(o[d]));
             }
             return true;
         };
-        auto raw_tile = [&]() -> const unsigned char* {  // the next raw tile, once loaded
+        auto raw_tile = [&]() -> uint32_t {  // the next raw tile (0: it did not come)
             const int st = it % ST;
-            if (!__all_sync(FULL, mbar_wait(&raw_full[st], (uint32_t)((it / ST) & 1)))) {
+            if (!__all_sync(FULL, wait_for(&raw_full[st], (uint32_t)((it / ST) & 1)))) {
                 raise_device_error(&g_paged_device_error, kErrPgLoad);
-                return nullptr;
+                return 0;
             }
-            return raw + (size_t)st * C::kRaw;
+            return smem_u32(raw) + st * C::kRaw;
         };
-        while (ok && walk.next(s)) {
-            if (s.u1 <= s.u0) continue;
-            for (int u = s.u0; u < s.u1; ++u, ++n) {
-                const int key = tile_key(s.t, a.tree, u), nb = n & 3, bf = n & 1;
-                const int rows = tile_rows(s.r, key);
-                // K(n) once S(n - 1) is done; before the first one, the unit's queries.
-                if (n > 0 && !__all_sync(FULL, mbar_wait(&k_free, (uint32_t)((n - 1) & 1)))) {
+        // Tile n is split in step n and folded in step n + 2; the two steps after
+        // the last tile only fold.
+        int u = 0, u1 = 0, count = -1;
+        while (ok && (count < 0 || n < count + 2)) {
+            const int nb = n & 3, bf = n & 1;
+            bool first = false;
+            if (count < 0 && u >= u1) {
+                bool more;
+                do more = warp_next(g, prefix, s);
+                while (more && s.u1 <= s.u0);
+                if (more) {
+                    u = s.u0;
+                    u1 = s.u1;
+                    first = true;
+                } else {
+                    count = n;
+                    if (count == 0) break;
+                }
+            }
+            if (count < 0) {
+                const int rows = tile_rows(s, tile_key(s, a.tree, u));
+                // K(n) once S(n - 1) is done; before a piece's first one, its queries.
+                if (n > 0 && !__all_sync(FULL, wait_for(&k_free, (uint32_t)((n - 1) & 1)))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
                     break;
                 }
-                if (u == s.u0) {
+                if (first) {
                     // Row i of the block: q scaled by qk_mul, then as any row; columns
                     // side * D / 4 .. + D / 4 of Q hi and Q lo (two elements each).
                     const int v = s.rb * kM + i, t = v / a.G;
-                    const bool alive = v < s.r.T * a.G;
-                    const float* q = a.q + (((int64_t)s.r.row0 + t) * a.H + (int64_t)s.hk * a.G + (v - t * a.G)) * D;
-                    const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0;
+                    const bool alive = v < s.T * a.G;
+                    const float* q = a.q + (((int64_t)s.row0 + t) * a.H + (int64_t)s.hk * a.G + (v - t * a.G)) * D;
                     auto load4 = [&](int d) -> float4 {
                         if (!alive) return make_float4(0.f, 0.f, 0.f, 0.f);
-                        float4 y = vec ? __ldg(reinterpret_cast<const float4*>(q + d))
-                                       : make_float4(__ldg(q + d), __ldg(q + d + 1), __ldg(q + d + 2), __ldg(q + d + 3));
+                        const float4 y = __ldg(reinterpret_cast<const float4*>(q + d));
                         return make_float4(y.x * a.qk_mul, y.y * a.qk_mul, y.z * a.qk_mul, y.w * a.qk_mul);
                     };
                     float top = 0.f;
@@ -796,8 +972,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < 16; c += 2) {
                             const float4 y = load4(side * (D / 2) + 2 * (c0 + c));
                             uint32_t h0, l0, h1, l1;
-                            split2(y.x * sc, y.y * sc, h0, l0);
-                            split2(y.z * sc, y.w * sc, h1, l1);
+                            split2(f2_pack(y.x * sc, y.y * sc), h0, l0);
+                            split2(f2_pack(y.z * sc, y.w * sc), h1, l1);
                             qh[c] = __uint_as_float(h0);
                             qh[c + 1] = __uint_as_float(h1);
                             ql[c] = __uint_as_float(l0);
@@ -808,13 +984,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tmem_wait_st();
                     tc_fence_before();
+                    ++piece;
                 }
-                const unsigned char* rt = raw_tile();
+                uint32_t rt = raw_tile();
                 if (!rt) {
                     ok = false;
                     break;
                 }
-                split_tile<D, false>(rt, kt, kt + C::kHalf, k_scale[nb], nullptr, rows, w, lane);
+                split_tile<D, false>(rt, smem_u32(kt), k_scale[nb], nullptr, rows, w, lane);
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA, TMA
                 __syncwarp();
                 if (lane == 0) {
@@ -823,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++it;
                 // V(n) once O(n - 2) is done.
-                if (n >= 2 && !__all_sync(FULL, mbar_wait(&o_full[bf], (uint32_t)(((n - 2) >> 1) & 1)))) {
+                if (n >= 2 && !__all_sync(FULL, wait_for(&o_full[bf], (uint32_t)(((n - 2) >> 1) & 1)))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
                     break;
@@ -833,8 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                unsigned char* vb = vt + bf * 2 * C::kHalf;
-                split_tile<D, true>(rt, vb, vb + C::kHalf, v_scale[nb], v_bad[nb], rows, w, lane);
+                split_tile<D, true>(rt, smem_u32(vt) + bf * 2 * C::kHalf, v_scale[nb], v_bad[nb], rows, w, lane);
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
@@ -842,16 +1018,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&raw_empty[it % ST]);
                 }
                 ++it;
-                if (n >= 2 && !fold(n - 2)) {
-                    ok = false;
-                    break;
-                }
+                ++u;
             }
-            if (!ok) break;
-            ++piece;
+            if (n >= 2 && !fold(n - 2)) {
+                ok = false;
+                break;
+            }
+            ++n;
         }
-        if (ok && n >= 2) ok = fold(n - 2);
-        if (ok && n >= 1) fold(n - 1);
     }
 
     tc_fence_before();
@@ -947,7 +1121,7 @@ bool encode_rows(CUtensorMap* map, const float* p, int64_t rows, int64_t cols, i
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 struct PgScratch {
-    size_t m, l, o, head, total;
+    size_t m, l, o, odd, head, total;
 };
 PgScratch scratch_of(int ctas, int D) {
     PgScratch s;
@@ -955,7 +1129,8 @@ PgScratch scratch_of(int ctas, int D) {
     s.m = kWorkspaceHeader;
     s.l = s.m + up256(rows * 4);
     s.o = s.l + up256(rows * 4);
-    s.head = s.o + up256(rows * D * 4);
+    s.odd = s.o + up256(rows * D * 4);
+    s.head = s.odd + up256(rows / 2 * D * 4);
     s.total = s.head + up256((size_t)ctas * sizeof(int4));
     return s;
 }
@@ -981,6 +1156,7 @@ cudaError_t launch_d(const PagedDesc& a, int num_sms, void* workspace, cudaStrea
     g.part_m = reinterpret_cast<float*>(ws + sc.m);
     g.part_l = reinterpret_cast<float*>(ws + sc.l);
     g.part_o = reinterpret_cast<float*>(ws + sc.o);
+    g.odd = reinterpret_cast<float*>(ws + sc.odd);
     g.head = reinterpret_cast<int4*>(ws + sc.head);
     const int64_t cols = (int64_t)a.Hk * D, pool = a.pages * a.page_size;
     CUtensorMap tk, tv, tkn, tvn;
@@ -990,9 +1166,10 @@ cudaError_t launch_d(const PagedDesc& a, int num_sms, void* workspace, cudaStrea
     tvn = tv;
     if (a.tree && (!encode_rows(&tkn, a.k_new, a.rows, cols, D, kKT) || !encode_rows(&tvn, a.v_new, a.rows, cols, D, kKT)))
         return cudaErrorInvalidValue;
-    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(paged_tc_kernel<D>), (int)Cfg<D>::kSmem);
+    auto kern = a.softcap_on ? paged_tc_kernel<D, true> : paged_tc_kernel<D, false>;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), (int)Cfg<D>::kSmem);
     if (e != cudaSuccess) return e;
-    paged_tc_kernel<D><<<ctas, kThreads, Cfg<D>::kSmem, stream>>>(tk, tv, tkn, tvn, g);
+    kern<<<ctas, kThreads, Cfg<D>::kSmem, stream>>>(tk, tv, tkn, tvn, g);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t most = (int64_t)a.max_rows * a.G;

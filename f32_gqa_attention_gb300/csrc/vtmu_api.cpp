@@ -1192,11 +1192,11 @@ vtmu_status vtmu_paged_attention(const float* q, const float* k_pool, const floa
     a.positions = positions;
     a.out = out;
     bool tc = p->kernel != VTMU_PAGED_CUDA_CORES && vtmu::paged_tc_supported(a);
-    if (tc && misaligned({k_pool, v_pool, k_new, v_new}, 15u)) tc = false;
+    if (tc && misaligned({q, k_pool, v_pool, k_new, v_new, out}, 15u)) tc = false;
     if (!tc && p->kernel == VTMU_PAGED_TENSOR_CORES)
         return fail(VTMU_ERR_UNSUPPORTED,
                     "paged: kernel TENSOR_CORES covers headDim 64 and 128 with page_size 8, 16, 32 or a multiple of 64 "
-                    "and 16-byte aligned pools, k_new and v_new (got headDim %d, page_size %d)",
+                    "and 16-byte aligned q, pools, k_new, v_new and out (got headDim %d, page_size %d)",
                     a.D, a.page_size);
     if (tc) {
         const size_t need = vtmu::paged_tc_workspace(a);

@@ -583,8 +583,8 @@ VTMU_API vtmu_status vtmu_paged_write(float* k_pool, float* v_pool, int64_t pool
 
 /* Kernel choice of vtmu_paged_attention.  AUTO takes the tensor cores where
  * they cover the call (headDim 64 or 128, page_size a multiple of 64 or one of
- * 8, 16, 32; 16-byte aligned pools and, in a tree, k_new and v_new), else the
- * CUDA cores (any headDim to 256, any page_size). */
+ * 8, 16, 32; 16-byte aligned q, out, pools and, in a tree, k_new and v_new),
+ * else the CUDA cores (any headDim to 256, any page_size). */
 typedef enum vtmu_paged_kernel {
     VTMU_PAGED_AUTO = 0,
     VTMU_PAGED_CUDA_CORES = 1,
