@@ -36,8 +36,8 @@
 //   4 - 7   softmax, thread = virtual row: no exchange between threads; P goes
 //           back to TMEM over S as the A operand of P.V;
 //   8 - 15  split: raw f32 rows to hi and lo in the 128-byte swizzled layout
-//           (K K-major, V MN-major: the same bytes), the unit's Q to TMEM, and
-//           the fold o = o alpha + O of the tile before last, 64 columns a thread
+//           (K K-major, V MN-major: the same bytes; four warps each), the unit's
+//           Q to TMEM, and the fold o = o alpha + O of the tile before last, 64 columns a thread
 //           (a fresh accumulator per tile: no sum runs long inside the pipe).
 // TMEM: Q hi, lo (D columns), S / P two buffers (128), O two buffers (2 D).
 // Every wait is bounded; a wait that gives up sets a bit of the device flag.
@@ -67,7 +67,7 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int kKT = 64;        // keys per tile
 constexpr int kM = 128;        // virtual rows per row block
 constexpr int kThreads = 512;
-constexpr int kSplitWarps = 8;
+constexpr int kSplitWarps = 4;  // for keys, and as many for values; all of them fold
 constexpr int kLast = 1 << 16;
 constexpr int kPShift = 14;    // probabilities are scaled to at most 2^14 in f16
 
@@ -296,10 +296,13 @@ __device__ __forceinline__ void split2(uint64_t x, uint32_t& hi, uint32_t& lo) {
     lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// max(|x|, |y|), NaN if one of them is.
-__device__ __forceinline__ float abs_max(float x, float y) {
+// The largest of |x.x| .. |x.w| and 2^-100 (NaN if one of them is): the least
+// exponent that a row's scale takes.
+__device__ __forceinline__ float abs_top(const float4& x) {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(x)), "f"(fabsf(y)));
+    asm("{\n .reg .f32 t;\n max.NaN.f32 t, %1, %2, %5;\n max.NaN.f32 %0, t, %3, %4;\n}\n"
+        : "=f"(r)
+        : "f"(fabsf(x.x)), "f"(fabsf(x.y)), "f"(fabsf(x.z)), "f"(fabsf(x.w)), "f"(7.888609052210118e-31f));
     return r;
 }
 
@@ -307,12 +310,12 @@ __device__ __forceinline__ float finite_or_zero(float x) {
     return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? 0.f : x;
 }
 
-// One raw tile (rows of D floats) to its hi tile and, right behind it, its lo tile by the eight split warps,
-// eight rows each; the rows' inverse scales to `scale`.  Rows past `rows` are
-// zeros.  In value tiles elements that are not finite become zeros here, and
-// `bad` gets a bit for each row that had one (they are added in the fold, to
-// the rows that see them only); in key tiles they make their own scores
-// not finite, which the mask discards.
+// One raw tile (rows of D floats) to its hi tile and, right behind it, its lo tile by
+// four warps, 16 rows each; the rows' inverse scales to `scale`.  Rows past
+// `rows` are zeros.  In value tiles elements that are not finite become zeros
+// here, and `bad` gets a bit for each row that had one (they are added in the
+// fold, to the rows that see them only); in key tiles they make their own
+// scores not finite, which the mask discards.
 __device__ __forceinline__ float4 lds4(uint32_t at) {
     float4 x;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at));
@@ -322,18 +325,20 @@ __device__ __forceinline__ void sts2(uint32_t at, uint32_t x, uint32_t y) {
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
 }
 
-template <int D, bool VALUES>
-__device__ __forceinline__ void split_tile(uint32_t raw, uint32_t hi, float* scale, uint8_t* bad, int rows, int w,
-                                           int lane) {
+template <int D>
+__device__ __forceinline__ void split_tile(bool values, uint32_t raw, uint32_t hi, float* scale, uint16_t* bad, int rows,
+                                           int w, int lane) {
     constexpr int kLanes = D / 4;        // lanes per row
     constexpr int kRows = 32 / kLanes;   // rows per step
     constexpr int kBatch = 4;            // steps whose chains overlap
     asm volatile("" : "+r"(w), "+r"(lane));  // addresses are worked out here, not kept over the tile loop
     const int l = lane % kLanes, sub = lane / kLanes;
-    const uint32_t off0 = (l >> 4) * (kKT * 128) + (l & 1) * 8;
+    // Element 4 l of row r: block l / 16, 16-byte chunk (l % 16) / 2 of the row's
+    // 128 bytes, swizzled by r % 8.
+    const uint32_t off0 = hi + (l >> 4) * (kKT * 128) + (l & 1) * 8, chunk = (l & 15) >> 1;
     uint32_t bad_bits = 0;
     auto top_of = [](const float4& y) {  // bits of the row's largest |element|; NaN above all
-        uint32_t t = __float_as_uint(abs_max(abs_max(y.x, y.y), abs_max(y.z, y.w)));
+        uint32_t t = __float_as_uint(abs_top(y));
         if constexpr (kLanes == 32) {
             return __reduce_max_sync(FULL, t);
         } else {
@@ -342,15 +347,15 @@ __device__ __forceinline__ void split_tile(uint32_t raw, uint32_t hi, float* sca
             return t;
         }
     };
+    const uint32_t src = raw + (16 * w + sub) * D * 4 + l * 16;
 #pragma unroll 1
-    for (int i0 = 0; i0 < 8; i0 += kBatch * kRows) {
-        const int r0 = 8 * w + i0 + sub;
+    for (int i0 = 0; i0 < 16; i0 += kBatch * kRows) {
+        const int r0 = 16 * w + i0 + sub;
         float4 x[kBatch];
         uint32_t top[kBatch], most = 0;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            x[i] = lds4(raw + (r0 + i * kRows) * D * 4 + l * 16);
-        if (8 * w + i0 + kBatch * kRows > rows) {  // the last tile of a cache, or drafted rows
+        for (int i = 0; i < kBatch; ++i) x[i] = lds4(src + (i0 + i * kRows) * D * 4);
+        if (16 * w + i0 + kBatch * kRows > rows) {  // the last tile of a cache, or drafted rows
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
                 if (r0 + i * kRows >= rows) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -360,11 +365,11 @@ __device__ __forceinline__ void split_tile(uint32_t raw, uint32_t hi, float* sca
             top[i] = top_of(x[i]);
             most = max(most, top[i]);
         }
-        if (__any_sync(FULL, most >= 0x7f800000u)) {  // rare
+        if (__any_sync(FULL, most >= 0x7e800000u)) {  // rare: 2^126 or more, or not finite
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const bool odd = top[i] >= 0x7f800000u;
-                if (VALUES) {
+                if (values) {
                     x[i] = make_float4(finite_or_zero(x[i].x), finite_or_zero(x[i].y), finite_or_zero(x[i].z),
                                        finite_or_zero(x[i].w));
                     top[i] = top_of(x[i]);
@@ -375,26 +380,25 @@ __device__ __forceinline__ void split_tile(uint32_t raw, uint32_t hi, float* sca
                 } else if (odd) {
                     top[i] = 0x3f800000u;
                 }
+                top[i] = min(top[i], 0x7e800000u);
             }
         }
-        // Element 4 l of row r: block l / 16, 16-byte chunk (l % 16) / 2 of the
-        // row's 128 bytes, swizzled by r % 8.
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const uint32_t e = row_exponent(top[i]);
-            const float s1 = pow2_of(254u - e);
+            const uint32_t e = top[i] & 0x7f800000u;                // 2^E in f32
+            const float s1 = __uint_as_float(0x7f000000u - e);      // 2^-E
             const uint64_t s2 = f2_pack(s1, s1);
             uint32_t h0, h1, l0, l1;
             split2(f2_mul(f2_pack(x[i].x, x[i].y), s2), h0, l0);
             split2(f2_mul(f2_pack(x[i].z, x[i].w), s2), h1, l1);
             const int r = r0 + i * kRows;
-            const uint32_t off = off0 + r * 128 + ((((l & 15) >> 1) ^ (r & 7)) << 4);
-            sts2(hi + off, h0, h1);
-            sts2(hi + Cfg<D>::kHalf + off, l0, l1);
-            if (l == 0) scale[r] = pow2_of(e);
+            const uint32_t off = off0 + r * 128 + ((chunk ^ (r & 7)) << 4);
+            sts2(off, h0, h1);
+            sts2(off + Cfg<D>::kHalf, l0, l1);
+            if (l == 0) scale[r] = __uint_as_float(e);
         }
     }
-    if (VALUES && lane == 0) bad[w] = (uint8_t)bad_bits;
+    if (values && lane == 0) bad[w] = (uint16_t)bad_bits;
 }
 
 // mbar_wait, bounded in the same way, that looks at the clock after every 64 tries only:
@@ -562,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // What tile n leaves for the roles that come later, at n % 4 (each is read
     // before the splitters can reach tile n + 4).
     __shared__ __align__(16) float k_scale[4][kKT], v_scale[4][kKT];
-    __shared__ __align__(8) uint8_t v_bad[4][8];
+    __shared__ __align__(8) uint16_t v_bad[4][4];
     __shared__ float q_scale[4][kM];             // by piece % 4
     __shared__ float2 fold_f[4][kM];             // alpha, output scale
     __shared__ uint64_t row_bad[4][kM];          // values to add that are not finite
@@ -587,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
-            mbar_init(&o_free[i], kSplitWarps);
+            mbar_init(&o_free[i], 2 * kSplitWarps);
         }
         fence_barrier_init();
     }
@@ -854,14 +858,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++piece;
         }
     } else if (warp >= 8) {
-        // ---- split, queries and fold --------------------------------------------------
-        const int w = warp - 8, quarter = warp & 3, side = w >> 2;  // columns side * D / 2 ..
-        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-        const int i = 32 * quarter + lane;
+        // ---- split, queries and fold: warps 8 - 11 the keys and the queries, 12 - 15
+        // the values; both fold, each its half of the columns ----
+        const int w = warp & 3, side = (warp - 8) >> 2;
+        const uint32_t lanes = (uint32_t)(32 * w) << 16;
+        const int i = 32 * w + lane;
         float o[D / 2];
 #pragma unroll
         for (int d = 0; d < D / 2; ++d) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(o[d]));
-        int n = 0, piece = 0, it = 0;
+        int n = 0, piece = 0;
         bool ok = true, odd = false;
         auto fold = [&](int j) -> bool {
             const int nb = j & 3, bf = j & 1;
@@ -872,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const int4 ta = tile_at[nb];
             const int rows = ta.x & (kLast - 1);
-            if (32 * quarter < rows) {
+            if (32 * w < rows) {
                 const float2 f = fold_f[nb][i];
                 const uint64_t fx = f2_pack(f.x, f.x), fy = f2_pack(f.y, f.y);
                 const uint32_t at = tmem + lanes + C::kColO + bf * D + side * (D / 2);
@@ -888,8 +893,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&o_free[bf]);
             if (*reinterpret_cast<const uint64_t*>(v_bad[nb]) && i < rows && row_bad[nb][i])  // rare
                 odd = add_odd_values(a, ta, row_bad[nb][i], g.odd + ((int64_t)blockIdx.x * kM + i) * D + side * (D / 2),
                                      side * (D / 2), D / 2, odd);
@@ -908,15 +911,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int d = 0; d < D / 2; ++d) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(o[d]));
             }
+            __syncwarp();  // after everything that tile j left in shared memory has been read
+            if (lane == 0) mbar_arrive(&o_free[bf]);
             return true;
-        };
-        auto raw_tile = [&]() -> uint32_t {  // the next raw tile (0: it did not come)
-            const int st = it % ST;
-            if (!__all_sync(FULL, wait_for(&raw_full[st], (uint32_t)((it / ST) & 1)))) {
-                raise_device_error(&g_paged_device_error, kErrPgLoad);
-                return 0;
-            }
-            return smem_u32(raw) + st * C::kRaw;
         };
         // Tile n is split in step n and folded in step n + 2; the two steps after
         // the last tile only fold.
@@ -939,15 +936,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (count < 0) {
                 const int rows = tile_rows(s, tile_key(s, a.tree, u));
-                // K(n) once S(n - 1) is done; before a piece's first one, its queries.
-                if (n > 0 && !__all_sync(FULL, wait_for(&k_free, (uint32_t)((n - 1) & 1)))) {
+                // K(n) once S(n - 1) is done, V(n) once O(n - 2) is; before a piece's first
+                // keys its queries.
+                const bool free = side == 0 ? n == 0 || wait_for(&k_free, (uint32_t)((n - 1) & 1))
+                                            : n < 2 || wait_for(&o_full[bf], (uint32_t)(((n - 2) >> 1) & 1));
+                if (!__all_sync(FULL, free)) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
                     break;
                 }
-                if (first) {
-                    // Row i of the block: q scaled by qk_mul, then as any row; columns
-                    // side * D / 4 .. + D / 4 of Q hi and Q lo (two elements each).
+                if (first && side == 0) {
+                    // Row i of the block: q scaled by qk_mul, then as any row; two
+                    // elements to a column of Q hi and Q lo.
                     const int v = s.rb * kM + i, t = v / a.G;
                     const bool alive = v < s.T * a.G;
                     const float* q = a.q + (((int64_t)s.row0 + t) * a.H + (int64_t)s.hk * a.G + (v - t * a.G)) * D;
@@ -964,13 +964,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const uint32_t e = row_exponent(__float_as_uint(top));
                     const float sc = pow2_of(254u - e);
-                    if (side == 0) q_scale[piece & 3][i] = pow2_of(e);
+                    q_scale[piece & 3][i] = pow2_of(e);
 #pragma unroll 1
-                    for (int c0 = 0; c0 < D / 4; c0 += 16) {
+                    for (int c0 = 0; c0 < D / 2; c0 += 16) {
                         float qh[16], ql[16];
 #pragma unroll
                         for (int c = 0; c < 16; c += 2) {
-                            const float4 y = load4(side * (D / 2) + 2 * (c0 + c));
+                            const float4 y = load4(2 * (c0 + c));
                             uint32_t h0, l0, h1, l1;
                             split2(f2_pack(y.x * sc, y.y * sc), h0, l0);
                             split2(f2_pack(y.z * sc, y.w * sc), h1, l1);
@@ -979,45 +979,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ql[c] = __uint_as_float(l0);
                             ql[c + 1] = __uint_as_float(l1);
                         }
-                        tmem_st16(tmem + lanes + C::kColQhi + side * (D / 4) + c0, qh);
-                        tmem_st16(tmem + lanes + C::kColQlo + side * (D / 4) + c0, ql);
+                        tmem_st16(tmem + lanes + C::kColQhi + c0, qh);
+                        tmem_st16(tmem + lanes + C::kColQlo + c0, ql);
                     }
                     tmem_wait_st();
                     tc_fence_before();
                     ++piece;
                 }
-                uint32_t rt = raw_tile();
-                if (!rt) {
+                const int it = 2 * n + side, st = it % ST;
+                if (!__all_sync(FULL, wait_for(&raw_full[st], (uint32_t)((it / ST) & 1)))) {
+                    raise_device_error(&g_paged_device_error, kErrPgLoad);
                     ok = false;
                     break;
                 }
-                split_tile<D, false>(rt, smem_u32(kt), k_scale[nb], nullptr, rows, w, lane);
+                split_tile<D>(side != 0, smem_u32(raw) + st * C::kRaw,
+                              side ? smem_u32(vt) + bf * 2 * C::kHalf : smem_u32(kt), side ? v_scale[nb] : k_scale[nb],
+                              v_bad[nb], rows, w, lane);
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA, TMA
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&k_ready);
-                    mbar_arrive(&raw_empty[it % ST]);
+                    mbar_arrive(side ? &v_ready[bf] : &k_ready);
+                    mbar_arrive(&raw_empty[st]);
                 }
-                ++it;
-                // V(n) once O(n - 2) is done.
-                if (n >= 2 && !__all_sync(FULL, wait_for(&o_full[bf], (uint32_t)(((n - 2) >> 1) & 1)))) {
-                    raise_device_error(&g_paged_device_error, kErrPgMma);
-                    ok = false;
-                    break;
-                }
-                rt = raw_tile();
-                if (!rt) {
-                    ok = false;
-                    break;
-                }
-                split_tile<D, true>(rt, smem_u32(vt) + bf * 2 * C::kHalf, v_scale[nb], v_bad[nb], rows, w, lane);
-                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&v_ready[bf]);
-                    mbar_arrive(&raw_empty[it % ST]);
-                }
-                ++it;
                 ++u;
             }
             if (n >= 2 && !fold(n - 2)) {
