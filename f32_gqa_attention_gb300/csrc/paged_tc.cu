@@ -90,16 +90,16 @@ struct PgArgs {
 
 template <int D>
 struct Cfg {
-    static constexpr int kStages = D == 128 ? 3 : 6;             // raw tiles in flight
-    static constexpr uint32_t kRaw = kKT * D * 4;
-    static constexpr uint32_t kHalf = kKT * D * 2;               // hi (or lo) of a tile
-    static constexpr uint32_t kBlock = kKT * 128;                // [64 rows x 64 elements]
+    static constexpr int kSlots = D == 128 ? 6 : 12;              // tiles: K(n), V(n), K(n + 1), ..
+    static constexpr uint32_t kTile = kKT * D * 4;
+    static constexpr uint32_t kHalf = kTile / 2;                  // hi, then lo
+    static constexpr uint32_t kBlock = kKT * 128;                 // [64 rows x 128 bytes]
     static constexpr uint32_t kColQhi = 0, kColQlo = D / 2, kColS = D, kColO = D + 2 * kKT;
     static constexpr uint32_t kTmemCols = 512;
-    static constexpr size_t kSmemTiles = (size_t)kStages * kRaw + 2 * kHalf + 4 * kHalf;
-    static constexpr size_t kSmem = 1024 + kSmemTiles + (kPagedMaxRequests + 1) * 8;
+    static constexpr size_t kSmem = 1024 + (size_t)kSlots * kTile + (kPagedMaxRequests + 1) * 8;
     static_assert(kColO + 2 * D <= kTmemCols, "TMEM budget");
-    static_assert(kSmem + 20 * 1024 <= 232448, "shared memory budget");
+    static_assert(kSmem + 25 * 1024 <= 232448, "shared memory budget");
+    static_assert(kSlots % 2 == 0, "K in the even slots, V in the odd ones");
 };
 
 // ---- the list of tiles --------------------------------------------------------------
@@ -310,8 +310,11 @@ __device__ __forceinline__ float finite_or_zero(float x) {
     return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? 0.f : x;
 }
 
-// One raw tile (rows of D floats) to its hi tile and, right behind it, its lo tile by
-// four warps, 16 rows each; the rows' inverse scales to `scale`.  Rows past
+// One tile of f32 rows to its f16 hi and lo halves, in place, by four warps, 16 rows
+// each; the rows' inverse scales to `scale`.  TMA leaves 32 elements (128
+// bytes) of row r in row r of each block, 128-byte swizzled; hi takes the first
+// half of the blocks with 64 elements a row, lo the second: a row's bytes stay the
+// same, so a warp that has read a row may write it.  Rows past
 // `rows` are zeros.  In value tiles elements that are not finite become zeros
 // here, and `bad` gets a bit for each row that had one (they are added in the
 // fold, to the rows that see them only); in key tiles they make their own
@@ -326,16 +329,17 @@ __device__ __forceinline__ void sts2(uint32_t at, uint32_t x, uint32_t y) {
 }
 
 template <int D>
-__device__ __forceinline__ void split_tile(bool values, uint32_t raw, uint32_t hi, float* scale, uint16_t* bad, int rows,
-                                           int w, int lane) {
+__device__ __forceinline__ void split_tile(bool values, uint32_t tile, float* scale, uint16_t* bad, int rows, int w,
+                                           int lane) {
     constexpr int kLanes = D / 4;        // lanes per row
     constexpr int kRows = 32 / kLanes;   // rows per step
     constexpr int kBatch = 4;            // steps whose chains overlap
     asm volatile("" : "+r"(w), "+r"(lane));  // addresses are worked out here, not kept over the tile loop
     const int l = lane % kLanes, sub = lane / kLanes;
-    // Element 4 l of row r: block l / 16, 16-byte chunk (l % 16) / 2 of the row's
-    // 128 bytes, swizzled by r % 8.
-    const uint32_t off0 = hi + (l >> 4) * (kKT * 128) + (l & 1) * 8, chunk = (l & 15) >> 1;
+    // Elements 4 l .. of row r: f32 in block l / 8, chunk l % 8 of 16 bytes; f16 in
+    // block l / 16, chunk (l % 16) / 2; chunks are swizzled by r % 8.
+    const uint32_t src = tile + (l >> 3) * (kKT * 128), dst = tile + (l >> 4) * (kKT * 128) + (l & 1) * 8;
+    const uint32_t src_chunk = l & 7, dst_chunk = (l & 15) >> 1;
     uint32_t bad_bits = 0;
     auto top_of = [](const float4& y) {  // bits of the row's largest |element|; NaN above all
         uint32_t t = __float_as_uint(abs_top(y));
@@ -347,14 +351,16 @@ __device__ __forceinline__ void split_tile(bool values, uint32_t raw, uint32_t h
             return t;
         }
     };
-    const uint32_t src = raw + (16 * w + sub) * D * 4 + l * 16;
 #pragma unroll 1
     for (int i0 = 0; i0 < 16; i0 += kBatch * kRows) {
         const int r0 = 16 * w + i0 + sub;
         float4 x[kBatch];
         uint32_t top[kBatch], most = 0;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) x[i] = lds4(src + (i0 + i * kRows) * D * 4);
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * kRows;
+            x[i] = lds4(src + r * 128 + ((src_chunk ^ (r & 7)) << 4));
+        }
         if (16 * w + i0 + kBatch * kRows > rows) {  // the last tile of a cache, or drafted rows
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
@@ -392,7 +398,7 @@ __device__ __forceinline__ void split_tile(bool values, uint32_t raw, uint32_t h
             split2(f2_mul(f2_pack(x[i].x, x[i].y), s2), h0, l0);
             split2(f2_mul(f2_pack(x[i].z, x[i].w), s2), h1, l1);
             const int r = r0 + i * kRows;
-            const uint32_t off = off0 + r * 128 + ((chunk ^ (r & 7)) << 4);
+            const uint32_t off = dst + r * 128 + ((dst_chunk ^ (r & 7)) << 4);
             sts2(off, h0, h1);
             sts2(off + Cfg<D>::kHalf, l0, l1);
             if (l == 0) scale[r] = __uint_as_float(e);
@@ -550,23 +556,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
                     const __grid_constant__ PgArgs g) {
     using C = Cfg<D>;
-    constexpr int ST = C::kStages;
+    constexpr int ST = C::kSlots;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                           ~uintptr_t(1023));
-    unsigned char* raw = base;                                   // ST raw tiles
-    unsigned char* kt = raw + (size_t)ST * C::kRaw;              // K hi, lo
-    unsigned char* vt = kt + 2 * C::kHalf;                       // V hi, lo, two buffers
-    long long* prefix = reinterpret_cast<long long*>(vt + 4 * C::kHalf);
-    __shared__ __align__(8) uint64_t raw_full[ST], raw_empty[ST], k_ready, k_free, v_ready[2], s_full[2], p_full[2],
-        o_full[2], o_free[2];
+    unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                            ~uintptr_t(1023));  // tile 2 n: K(n), 2 n + 1: V(n)
+    long long* prefix = reinterpret_cast<long long*>(tiles + (size_t)ST * C::kTile);
+    // A slot is loaded by TMA (full), split in place (ready), read by the MMAs (free).
+    __shared__ __align__(8) uint64_t full[ST], ready[ST], freed[ST], s_full[2], p_full[2], o_full[2], o_free[2];
     __shared__ uint32_t tmem_base_s;
     __shared__ long long scan_s[kThreads / 32];
     __shared__ Seg seg_s[kThreads / 32];
-    // What tile n leaves for the roles that come later, at n % 4 (each is read
-    // before the splitters can reach tile n + 4).
-    __shared__ __align__(16) float k_scale[4][kKT], v_scale[4][kKT];
-    __shared__ __align__(8) uint16_t v_bad[4][4];
+    // What tile n leaves for the roles that come later.  From the splitters, at n % 8:
+    // they are at most three tiles ahead of the MMAs, and P.V of tile n + 4 means that
+    // tile n + 2 has been folded.  From the softmax, at n % 4: S(n + 4) follows
+    // P.V of tile n + 2, which follows the fold of tile n.
+    __shared__ __align__(16) float k_scale[8][kKT], v_scale[8][kKT];
+    __shared__ __align__(8) uint16_t v_bad[8][4];
     __shared__ float q_scale[4][kM];             // by piece % 4
     __shared__ float2 fold_f[4][kM];             // alpha, output scale
     __shared__ uint64_t row_bad[4][kM];          // values to add that are not finite
@@ -581,13 +586,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
-            mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], kSplitWarps);
+            mbar_init(&full[i], 1);
+            mbar_init(&ready[i], kSplitWarps);
+            mbar_init(&freed[i], 1);
         }
-        mbar_init(&k_ready, kSplitWarps);
-        mbar_init(&k_free, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&v_ready[i], kSplitWarps);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
@@ -640,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tensormap(&tm_k);
             prefetch_tensormap(&tm_v);
         }
-        const int nsub = kKT / g.sub;
+        const int nsub = kKT / g.sub, blk = lane / nsub, k_sub = lane % nsub;
         const int nowhere = (int)(a.pages * a.page_size);  // a row out of bounds: zeros
         int it = 0;
         bool ok = true;
@@ -662,43 +665,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (page >= 0 && page < a.pages) y_cur = page * a.page_size + row % a.page_size;
                         }
                     }
-                    y = __shfl_sync(FULL, y_cur, (q0 & 31) + (lane < nsub ? lane : 0));
+                    y = __shfl_sync(FULL, y_cur, (q0 & 31) + k_sub);
                 }
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++it) {
                     const int st = it % ST;
-                    if (it >= ST && !__all_sync(FULL, wait_for(&raw_empty[st], (uint32_t)((it / ST - 1) & 1)))) {
+                    if (it >= ST && !__all_sync(FULL, wait_for(&freed[st], (uint32_t)((it / ST - 1) & 1)))) {
                         raise_device_error(&g_paged_device_error, kErrPgFree);
                         ok = false;
                         break;
                     }
-                    if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], C::kRaw);
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kTile);
                     __syncwarp();
-                    unsigned char* dst = raw + (size_t)st * C::kRaw;
+                    // A lane for each box of 32 elements x the rows of a page (or of the tile).
+                    unsigned char* dst = tiles + (size_t)st * C::kTile;
                     if (key < 0) {
-                        if (lane == 0) tma_load_2d(dst, kv ? &tm_vn : &tm_kn, s.hk * D, s.row0, &raw_full[st]);
-                    } else if (lane < nsub) {
-                        tma_load_2d(dst + (size_t)lane * g.sub * D * 4, kv ? &tm_v : &tm_k, s.hk * D, y, &raw_full[st]);
+                        if (lane < D / 32)
+                            tma_load_2d(dst + lane * C::kBlock, kv ? &tm_vn : &tm_kn, s.hk * D + 32 * lane, s.row0, &full[st]);
+                    } else if (blk < D / 32) {
+                        tma_load_2d(dst + blk * C::kBlock + k_sub * g.sub * 128, kv ? &tm_v : &tm_k, s.hk * D + 32 * blk, y,
+                                    &full[st]);
                     }
                 }
             }
         }
         // No copy may be in flight when the CTA exits.
         for (int j = it < ST ? 0 : it - ST; j < it; ++j)
-            if (!wait_for(&raw_full[j % ST], (uint32_t)((j / ST) & 1)))
+            if (!wait_for(&full[j % ST], (uint32_t)((j / ST) & 1)))
                 raise_device_error(&g_paged_device_error, kErrPgFree);
     } else if (warp == 1) {
         // ---- MMAs: the warp stays together and one elected lane issues (behind a
         // lane == 0 test an MMA took 45 cycles to issue, behind elect 10) ----
         constexpr uint32_t id_s = idesc_f16(kM, kKT, false), id_o = idesc_f16(kM, D, true);
         const uint32_t tm = __shfl_sync(FULL, tmem, 0);
-        const uint64_t khi = smem_desc_sw128(kt), klo = smem_desc_sw128(kt + C::kHalf);
+        const uint64_t k0 = smem_desc_sw128(tiles), v0 = smem_desc_mn(tiles, C::kBlock);
         int n = 0;
         bool ok = true;
         auto pv = [&](int j) -> bool {  // O(j) = P(j).V(j)
-            const int bf = j & 1;
+            const int bf = j & 1, it = 2 * j + 1, st = it % ST;
             const uint32_t ph = (uint32_t)((j >> 1) & 1);
-            if (!__all_sync(FULL, wait_for(&p_full[bf], ph) && wait_for(&v_ready[bf], ph) &&
+            if (!__all_sync(FULL, wait_for(&p_full[bf], ph) && wait_for(&ready[st], (uint32_t)((it / ST) & 1)) &&
                                       (j < 2 || wait_for(&o_free[bf], ph ^ 1u)))) {
                 raise_device_error(&g_paged_device_error, kErrPgMma);
                 return false;
@@ -706,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t d = tm + C::kColO + bf * D;
             const uint32_t p = tm + C::kColS + bf * kKT;  // 32 keys: hi in 16 columns, lo in 16
-            const uint64_t vhi = smem_desc_mn(vt, C::kBlock) + bf * (2 * C::kHalf >> 4);
+            const uint64_t vhi = v0 + st * (C::kTile >> 4);
             const uint64_t vlo = vhi + (C::kHalf >> 4);
             if (elect_one()) {
 #pragma unroll
@@ -716,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_f16_ts(d, plo, vhi + 128 * k, id_o, 1u);
                     mma_f16_ts(d, phi, vlo + 128 * k, id_o, 1u);
                 }
+                mma_commit(&freed[st]);
                 mma_commit(&o_full[bf]);
             }
             __syncwarp();
@@ -724,13 +731,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && warp_next(g, prefix, s)) {
             const int u1 = s.u1;
             for (int u = s.u0; u < u1; ++u, ++n) {
-                if (!__all_sync(FULL, wait_for(&k_ready, (uint32_t)(n & 1)))) {
+                const int it = 2 * n, st = it % ST;
+                if (!__all_sync(FULL, wait_for(&ready[st], (uint32_t)((it / ST) & 1)))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d = tm + C::kColS + (n & 1) * kKT;
+                const uint64_t khi = k0 + st * (C::kTile >> 4), klo = khi + (C::kHalf >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {  // 16 dims: 8 columns of Q, 32 bytes of a K row
@@ -739,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_f16_ts(d, tm + C::kColQlo + 8 * k, khi + off, id_s, 1u);
                         mma_f16_ts(d, tm + C::kColQhi + 8 * k, klo + off, id_s, 1u);
                     }
-                    mma_commit(&k_free);
+                    mma_commit(&freed[st]);
                     mma_commit(&s_full[n & 1]);
                 }
                 __syncwarp();
@@ -781,9 +790,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // warp, which always has one, arrives for it.
             const int arrivals = warp == 4 ? 4 - (rows + 31) / 32 + 1 : 1;
             for (int u = s.u0; u < s.u1 && __any_sync(FULL, alive); ++u, ++n) {
-                const int key = tile_key(s, a.tree, u), nb = n & 3, bf = n & 1;
+                const int key = tile_key(s, a.tree, u), nb = n & 3, n8 = n & 7, bf = n & 1, it = 2 * n + 1;
                 if (!__all_sync(FULL, wait_for(&s_full[bf], (uint32_t)((n >> 1) & 1)) &&
-                                          wait_for(&v_ready[bf], (uint32_t)((n >> 1) & 1)))) {
+                                          wait_for(&ready[it % ST], (uint32_t)((it / ST) & 1)))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
                     break;
@@ -803,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 RowTile rt;
                 rt.at = tmem + lanes + C::kColS + bf * kKT;
-                rt.ks = k_scale[nb];
+                rt.ks = k_scale[n8];
                 rt.see = see;
                 rt.qs = q_scale[piece & 3][i];
                 rt.cap = a.cap_log2;
@@ -811,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t vtop;
                 float alpha;
                 if (__all_sync(FULL, see == ~0ull)) {
-                    const float v0 = v_scale[nb][lane], v1 = v_scale[nb][lane + 32];
+                    const float v0 = v_scale[n8][lane], v1 = v_scale[n8][lane + 32];
                     vtop = __reduce_max_sync(FULL, max(__float_as_uint(v0), __float_as_uint(v1)));
                     const float c = pow2_of(254u + kPShift - (vtop >> 23));
                     v_norm[warp & 3][lane] = v0 * c;
@@ -824,13 +833,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     vtop = 27u << 23;
 #pragma unroll 4
                     for (int k = 0; k < kKT; ++k)
-                        if ((see >> k) & 1) vtop = max(vtop, __float_as_uint(v_scale[nb][k]));
-                    rt.vs = v_scale[nb];
+                        if ((see >> k) & 1) vtop = max(vtop, __float_as_uint(v_scale[n8][k]));
+                    rt.vs = v_scale[n8];
                     rt.v_mul = pow2_of(254u + kPShift - (vtop >> 23));
                     alpha = row_softmax<CAP, false>(rt, m, l);
                 }
                 fold_f[nb][i] = make_float2(alpha, pow2_of((vtop >> 23) - kPShift));
-                const uint64_t bad = *reinterpret_cast<const uint64_t*>(v_bad[nb]);
+                const uint64_t bad = *reinterpret_cast<const uint64_t*>(v_bad[n8]);
                 if (bad) row_bad[nb][i] = bad & see;
                 if (u == s.u1 - 1) {
                     float* to = g.part_o + prow * D;
@@ -869,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n = 0, piece = 0;
         bool ok = true, odd = false;
         auto fold = [&](int j) -> bool {
-            const int nb = j & 3, bf = j & 1;
+            const int nb = j & 3, n8 = j & 7, bf = j & 1;
             if (!__all_sync(FULL, wait_for(&o_full[bf], (uint32_t)((j >> 1) & 1)))) {
                 raise_device_error(&g_paged_device_error, kErrPgMma);
                 return false;
@@ -893,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
             }
-            if (*reinterpret_cast<const uint64_t*>(v_bad[nb]) && i < rows && row_bad[nb][i])  // rare
+            if (*reinterpret_cast<const uint64_t*>(v_bad[n8]) && i < rows && row_bad[nb][i])  // rare
                 odd = add_odd_values(a, ta, row_bad[nb][i], g.odd + ((int64_t)blockIdx.x * kM + i) * D + side * (D / 2),
                                      side * (D / 2), D / 2, odd);
             if (ta.x & kLast) {
@@ -919,7 +928,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the last tile only fold.
         int u = 0, u1 = 0, count = -1;
         while (ok && (count < 0 || n < count + 2)) {
-            const int nb = n & 3, bf = n & 1;
             bool first = false;
             if (count < 0 && u >= u1) {
                 bool more;
@@ -936,11 +944,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (count < 0) {
                 const int rows = tile_rows(s, tile_key(s, a.tree, u));
-                // K(n) once S(n - 1) is done, V(n) once O(n - 2) is; before a piece's first
-                // keys its queries.
-                const bool free = side == 0 ? n == 0 || wait_for(&k_free, (uint32_t)((n - 1) & 1))
-                                            : n < 2 || wait_for(&o_full[bf], (uint32_t)(((n - 2) >> 1) & 1));
-                if (!__all_sync(FULL, free)) {
+                // A piece's queries once S(n - 1) is done with the last ones.
+                if (first && side == 0 && n > 0 &&
+                    !__all_sync(FULL, wait_for(&freed[(2 * n - 2) % ST], (uint32_t)(((2 * n - 2) / ST) & 1)))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
                     break;
@@ -987,20 +993,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++piece;
                 }
                 const int it = 2 * n + side, st = it % ST;
-                if (!__all_sync(FULL, wait_for(&raw_full[st], (uint32_t)((it / ST) & 1)))) {
+                if (!__all_sync(FULL, wait_for(&full[st], (uint32_t)((it / ST) & 1)))) {
                     raise_device_error(&g_paged_device_error, kErrPgLoad);
                     ok = false;
                     break;
                 }
-                split_tile<D>(side != 0, smem_u32(raw) + st * C::kRaw,
-                              side ? smem_u32(vt) + bf * 2 * C::kHalf : smem_u32(kt), side ? v_scale[nb] : k_scale[nb],
-                              v_bad[nb], rows, w, lane);
-                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA, TMA
+                split_tile<D>(side != 0, smem_u32(tiles) + st * C::kTile, side ? v_scale[n & 7] : k_scale[n & 7], v_bad[n & 7],
+                              rows, w, lane);
+                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(side ? &v_ready[bf] : &k_ready);
-                    mbar_arrive(&raw_empty[st]);
-                }
+                if (lane == 0) mbar_arrive(&ready[st]);
                 ++u;
             }
             if (n >= 2 && !fold(n - 2)) {
@@ -1086,17 +1088,17 @@ PFN_cuTensorMapEncodeTiled_v12000 pg_encoder() {
     return fn;
 }
 
-// Row-major [rows, cols] f32, boxes of box_rows rows x D columns, no swizzle.
-bool encode_rows(CUtensorMap* map, const float* p, int64_t rows, int64_t cols, int box_cols, int box_rows) {
-    return cached_tensor_map(map, p, rows, cols, box_cols, box_rows, 0, [&](CUtensorMap* m) {
+// Row-major [rows, cols] f32, boxes of box_rows rows x 32 columns, 128-byte swizzle.
+bool encode_rows(CUtensorMap* map, const float* p, int64_t rows, int64_t cols, int box_rows) {
+    return cached_tensor_map(map, p, rows, cols, 32, box_rows, 3, [&](CUtensorMap* m) {
         auto fn = pg_encoder();
         if (!fn) return false;
         const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
         const cuuint64_t strides[1] = {(cuuint64_t)cols * sizeof(float)};
-        const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+        const cuuint32_t box[2] = {32u, (cuuint32_t)box_rows};
         const cuuint32_t estr[2] = {1, 1};
         return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(p), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     });
 }
@@ -1143,11 +1145,11 @@ cudaError_t launch_d(const PagedDesc& a, int num_sms, void* workspace, cudaStrea
     g.head = reinterpret_cast<int4*>(ws + sc.head);
     const int64_t cols = (int64_t)a.Hk * D, pool = a.pages * a.page_size;
     CUtensorMap tk, tv, tkn, tvn;
-    if (!encode_rows(&tk, a.k_pool, pool, cols, D, g.sub) || !encode_rows(&tv, a.v_pool, pool, cols, D, g.sub))
+    if (!encode_rows(&tk, a.k_pool, pool, cols, g.sub) || !encode_rows(&tv, a.v_pool, pool, cols, g.sub))
         return cudaErrorInvalidValue;
     tkn = tk;
     tvn = tv;
-    if (a.tree && (!encode_rows(&tkn, a.k_new, a.rows, cols, D, kKT) || !encode_rows(&tvn, a.v_new, a.rows, cols, D, kKT)))
+    if (a.tree && (!encode_rows(&tkn, a.k_new, a.rows, cols, kKT) || !encode_rows(&tvn, a.v_new, a.rows, cols, kKT)))
         return cudaErrorInvalidValue;
     auto kern = a.softcap_on ? paged_tc_kernel<D, true> : paged_tc_kernel<D, false>;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), (int)Cfg<D>::kSmem);
