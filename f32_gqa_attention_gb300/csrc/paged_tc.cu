@@ -67,7 +67,7 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int kKT = 64;        // keys per tile
 constexpr int kM = 128;        // virtual rows per row block
 constexpr int kThreads = 512;
-constexpr int kSplitWarps = 4;  // for keys, and as many for values; all of them fold
+constexpr int kFoldWarps = 8;
 constexpr int kLast = 1 << 16;
 constexpr int kPShift = 14;    // probabilities are scaled to at most 2^14 in f16
 
@@ -92,8 +92,8 @@ template <int D>
 struct Cfg {
     static constexpr int kSlots = D == 128 ? 6 : 12;              // tiles: K(n), V(n), K(n + 1), ..
     static constexpr uint32_t kTile = kKT * D * 4;
-    static constexpr uint32_t kHalf = kTile / 2;                  // hi, then lo
-    static constexpr uint32_t kBlock = kKT * 128;                 // [64 rows x 128 bytes]
+    static constexpr uint32_t kBlock = kKT * 128;                 // [64 rows x 128 bytes]: 32 f32, or 64 f16 hi or lo
+    static constexpr int kSplitWarps = D == 128 ? 4 : 2;          // warps that split a tile
     static constexpr uint32_t kColQhi = 0, kColQlo = D / 2, kColS = D, kColO = D + 2 * kKT;
     static constexpr uint32_t kTmemCols = 512;
     static constexpr size_t kSmem = 1024 + (size_t)kSlots * kTile + (kPagedMaxRequests + 1) * 8;
@@ -306,105 +306,130 @@ __device__ __forceinline__ float abs_top(const float4& x) {
     return r;
 }
 
+__device__ __forceinline__ float nan_max(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
 __device__ __forceinline__ float finite_or_zero(float x) {
     return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? 0.f : x;
 }
 
-// One tile of f32 rows to its f16 hi and lo halves, in place, by four warps, 16 rows
-// each; the rows' inverse scales to `scale`.  TMA leaves 32 elements (128
-// bytes) of row r in row r of each block, 128-byte swizzled; hi takes the first
-// half of the blocks with 64 elements a row, lo the second: a row's bytes stay the
-// same, so a warp that has read a row may write it.  Rows past
-// `rows` are zeros.  In value tiles elements that are not finite become zeros
-// here, and `bad` gets a bit for each row that had one (they are added in the
-// fold, to the rows that see them only); in key tiles they make their own
-// scores not finite, which the mask discards.
 __device__ __forceinline__ float4 lds4(uint32_t at) {
     float4 x;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at));
     return x;
 }
-__device__ __forceinline__ void sts2(uint32_t at, uint32_t x, uint32_t y) {
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+__device__ __forceinline__ void sts4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// Barrier ID over the two warps that share 32 rows.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+
+// 64 elements of a row of a tile (two blocks from `at` on, swizzled by sw = (row % 8)
+// 16): the largest |element|, at least 2^-100; NaN if one is.
+__device__ __forceinline__ float row_top(uint32_t at, uint32_t sw) {
+    float t[4];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        const float4 x = lds4(at + (c >> 3) * (kKT * 128) + (((c & 7) << 4) ^ sw));
+        t[c & 3] = c < 4 ? abs_top(x) : nan_max(t[c & 3], abs_top(x));
+    }
+    return nan_max(nan_max(t[0], t[1]), nan_max(t[2], t[3]));
 }
 
-template <int D>
-__device__ __forceinline__ void split_tile(bool values, uint32_t tile, float* scale, uint16_t* bad, int rows, int w,
-                                           int lane) {
-    constexpr int kLanes = D / 4;        // lanes per row
-    constexpr int kRows = 32 / kLanes;   // rows per step
-    constexpr int kBatch = 4;            // steps whose chains overlap
-    asm volatile("" : "+r"(w), "+r"(lane));  // addresses are worked out here, not kept over the tile loop
-    const int l = lane % kLanes, sub = lane / kLanes;
-    // Elements 4 l .. of row r: f32 in block l / 8, chunk l % 8 of 16 bytes; f16 in
-    // block l / 16, chunk (l % 16) / 2; chunks are swizzled by r % 8.
-    const uint32_t src = tile + (l >> 3) * (kKT * 128), dst = tile + (l >> 4) * (kKT * 128) + (l & 1) * 8;
-    const uint32_t src_chunk = l & 7, dst_chunk = (l & 15) >> 1;
-    uint32_t bad_bits = 0;
-    auto top_of = [](const float4& y) {  // bits of the row's largest |element|; NaN above all
-        uint32_t t = __float_as_uint(abs_top(y));
-        if constexpr (kLanes == 32) {
-            return __reduce_max_sync(FULL, t);
-        } else {
-#pragma unroll
-            for (int off = kLanes / 2; off > 0; off >>= 1) t = max(t, __shfl_xor_sync(FULL, t, off));
-            return t;
-        }
+// The same 64 elements times `s` as f16: hi over the first block, lo over the
+// second, in place.  hi chunk c (8 elements, 16 bytes) lands on f32 chunk c, whose
+// elements went into hi chunk c / 2 (+ 4 in the second block); the first block is
+// taken upwards with its lo chunks kept, the second downwards, so that nothing is
+// written before it has been read.
+__device__ __forceinline__ void row_split(uint32_t at, uint32_t sw, float s) {
+    const uint64_t s2 = f2_pack(s, s);
+    constexpr uint32_t kB = kKT * 128;
+    uint32_t held[16];
+    // f32 chunks 2 c, 2 c + 1 of step i (c = 0 .. 3 of the first block, 3 .. 0 of the
+    // second); a step's loads are on their way while the last one is converted.
+    float4 x[2][2];
+    auto load = [&](int i) {
+        const int c = i < 4 ? i : 7 - i;
+        const uint32_t from = at + (i < 4 ? 0 : kB);
+        x[i & 1][0] = lds4(from + (((2 * c) << 4) ^ sw));
+        x[i & 1][1] = lds4(from + (((2 * c + 1) << 4) ^ sw));
     };
-#pragma unroll 1
-    for (int i0 = 0; i0 < 16; i0 += kBatch * kRows) {
-        const int r0 = 16 * w + i0 + sub;
-        float4 x[kBatch];
-        uint32_t top[kBatch], most = 0;
+    auto convert = [&](int i, uint32_t (&h)[4], uint32_t* l) {
+        const float4 u = x[i & 1][0], v = x[i & 1][1];
+        split2(f2_mul(f2_pack(u.x, u.y), s2), h[0], l[0]);
+        split2(f2_mul(f2_pack(u.z, u.w), s2), h[1], l[1]);
+        split2(f2_mul(f2_pack(v.x, v.y), s2), h[2], l[2]);
+        split2(f2_mul(f2_pack(v.z, v.w), s2), h[3], l[3]);
+    };
+    load(0);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + i * kRows;
-            x[i] = lds4(src + r * 128 + ((src_chunk ^ (r & 7)) << 4));
-        }
-        if (16 * w + i0 + kBatch * kRows > rows) {  // the last tile of a cache, or drafted rows
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (r0 + i * kRows >= rows) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            top[i] = top_of(x[i]);
-            most = max(most, top[i]);
-        }
-        if (__any_sync(FULL, most >= 0x7e800000u)) {  // rare: 2^126 or more, or not finite
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const bool odd = top[i] >= 0x7f800000u;
-                if (values) {
-                    x[i] = make_float4(finite_or_zero(x[i].x), finite_or_zero(x[i].y), finite_or_zero(x[i].z),
-                                       finite_or_zero(x[i].w));
-                    top[i] = top_of(x[i]);
-                    const unsigned votes = __ballot_sync(FULL, odd);
-#pragma unroll
-                    for (int k = 0; k < kRows; ++k)
-                        if ((votes >> (k * kLanes)) & 1u) bad_bits |= 1u << (i0 + i * kRows + k);
-                } else if (odd) {
-                    top[i] = 0x3f800000u;
-                }
-                top[i] = min(top[i], 0x7e800000u);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const uint32_t e = top[i] & 0x7f800000u;                // 2^E in f32
-            const float s1 = __uint_as_float(0x7f000000u - e);      // 2^-E
-            const uint64_t s2 = f2_pack(s1, s1);
-            uint32_t h0, h1, l0, l1;
-            split2(f2_mul(f2_pack(x[i].x, x[i].y), s2), h0, l0);
-            split2(f2_mul(f2_pack(x[i].z, x[i].w), s2), h1, l1);
-            const int r = r0 + i * kRows;
-            const uint32_t off = dst + r * 128 + ((dst_chunk ^ (r & 7)) << 4);
-            sts2(off, h0, h1);
-            sts2(off + Cfg<D>::kHalf, l0, l1);
-            if (l == 0) scale[r] = __uint_as_float(e);
+    for (int i = 0; i < 8; ++i) {
+        if (i < 7) load(i + 1);
+        uint32_t h[4], l[4];
+        if (i < 4) {
+            convert(i, h, held + 4 * i);
+            sts4(at + ((i << 4) ^ sw), h[0], h[1], h[2], h[3]);
+        } else {
+            const int c = 11 - i;  // hi and lo chunk
+            convert(i, h, l);
+            sts4(at + ((c << 4) ^ sw), h[0], h[1], h[2], h[3]);
+            sts4(at + kB + ((c << 4) ^ sw), l[0], l[1], l[2], l[3]);
         }
     }
-    if (values && lane == 0) bad[w] = (uint16_t)bad_bits;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        sts4(at + kB + ((c << 4) ^ sw), held[4 * c], held[4 * c + 1], held[4 * c + 2], held[4 * c + 3]);
+}
+
+// One tile of f32 rows to f16 hi and lo, in place; the rows' inverse scales to
+// `scale`.  TMA leaves 32 elements (128 bytes) of row r in row r of each block,
+// 128-byte swizzled; a thread takes 64 elements of one row (two blocks, which become
+// their hi and lo): with lane = row the swizzle makes its 16-byte accesses free of
+// bank conflicts, and nothing but the row's maximum crosses threads (D = 128: the
+// two halves of a row through `top`).  Rows past `rows` are zeros.  In value tiles
+// elements that are not finite become zeros here and `bad` gets the rows that had
+// one (they are added in the fold, to the rows that see them only); in key
+// tiles they make their own scores not finite, which the mask discards.
+template <int D>
+__device__ __forceinline__ void split_tile(bool values, uint32_t tile, float* scale, uint32_t* bad, float (*top)[kKT],
+                                           int rows, int w, int lane) {
+    const int half = D == 128 ? w & 1 : 0, row = 32 * (D == 128 ? w >> 1 : w & 1) + lane;
+    uint32_t at = tile + 2 * half * (kKT * 128) + row * 128;
+    asm volatile("" : "+r"(at));  // addresses are worked out here, not kept over the tile loop
+    const uint32_t sw = (row & 7) << 4;
+    if (rows < kKT && row >= rows) {  // the last tile of a cache, or drafted rows
+        for (int c = 0; c < 16; ++c) sts4(at + (c >> 3) * (kKT * 128) + (c & 7) * 16, 0, 0, 0, 0);
+    }
+    float t = row_top(at, sw);
+    uint32_t odd = 0;
+    if (__any_sync(FULL, !(t < 8.507059173023462e37f))) {  // rare: 2^126 or more, or not finite
+        const bool o = !(t < __int_as_float(0x7f800000));
+        odd = __ballot_sync(FULL, o);
+        if (o && values) {
+            for (int c = 0; c < 16; ++c) {
+                const uint32_t to = at + (c >> 3) * (kKT * 128) + (c & 7) * 16;
+                const float4 x = lds4(to);
+                sts4(to, __float_as_uint(finite_or_zero(x.x)), __float_as_uint(finite_or_zero(x.y)),
+                     __float_as_uint(finite_or_zero(x.z)), __float_as_uint(finite_or_zero(x.w)));
+            }
+            t = row_top(at, sw);
+        } else if (o) {
+            t = 1.f;
+        }
+        t = fminf(t, 8.507059173023462e37f);
+    }
+    if (values && lane == 0) bad[w] = odd;
+    if constexpr (D == 128) {
+        top[half][row] = t;
+        pair_sync(2 + 2 * (values ? 1 : 0) + (w >> 1));
+        t = fmaxf(t, top[half ^ 1][row]);
+    }
+    const uint32_t e = __float_as_uint(t) & 0x7f800000u;  // 2^E in f32; 2^-E is 0x7f000000 - e
+    if (half == 0) scale[row] = __uint_as_float(e);
+    row_split(at, sw, __uint_as_float(0x7f000000u - e));
 }
 
 // mbar_wait, bounded in the same way, that looks at the clock after every 64 tries only:
@@ -421,6 +446,13 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) {
 }
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
     return mbar_try_wait(bar, parity) || wait_long(bar, parity);
+}
+
+// Rows of a value tile with elements that are not finite, from what its warps found.
+template <int D>
+__device__ __forceinline__ uint64_t bad_rows(const uint32_t* b) {
+    const uint4 v = *reinterpret_cast<const uint4*>(b);
+    return D == 128 ? (v.x | v.y) | (uint64_t)(v.z | v.w) << 32 : (v.x | v.z) | (uint64_t)(v.y | v.w) << 32;
 }
 
 // Values that are not finite would reach every row of a tile through 0 x inf =
@@ -571,7 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tile n + 2 has been folded.  From the softmax, at n % 4: S(n + 4) follows
     // P.V of tile n + 2, which follows the fold of tile n.
     __shared__ __align__(16) float k_scale[8][kKT], v_scale[8][kKT];
-    __shared__ __align__(8) uint16_t v_bad[8][4];
+    __shared__ __align__(16) uint32_t v_bad[8][4];
+    __shared__ float row_max[2][2][2][kKT];      // by n % 2: keys and values, halves of the rows
     __shared__ float q_scale[4][kM];             // by piece % 4
     __shared__ float2 fold_f[4][kM];             // alpha, output scale
     __shared__ uint64_t row_bad[4][kM];          // values to add that are not finite
@@ -587,19 +620,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&ready[i], kSplitWarps);
+            mbar_init(&ready[i], C::kSplitWarps);
             mbar_init(&freed[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
-            mbar_init(&o_free[i], 2 * kSplitWarps);
+            mbar_init(&o_free[i], kFoldWarps);
         }
         fence_barrier_init();
     }
     if (warp == 1) tmem_alloc(&tmem_base_s, C::kTmemCols);
     if (threadIdx.x == 32) g.head[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (threadIdx.x < 32) (&v_bad[0][0])[threadIdx.x] = 0;
 
     // The requests' tiles and their running sum.
     long long carry = 0;
@@ -698,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // lane == 0 test an MMA took 45 cycles to issue, behind elect 10) ----
         constexpr uint32_t id_s = idesc_f16(kM, kKT, false), id_o = idesc_f16(kM, D, true);
         const uint32_t tm = __shfl_sync(FULL, tmem, 0);
-        const uint64_t k0 = smem_desc_sw128(tiles), v0 = smem_desc_mn(tiles, C::kBlock);
+        const uint64_t k0 = smem_desc_sw128(tiles), v0 = smem_desc_mn(tiles, 2 * C::kBlock);
         int n = 0;
         bool ok = true;
         auto pv = [&](int j) -> bool {  // O(j) = P(j).V(j)
@@ -713,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t d = tm + C::kColO + bf * D;
             const uint32_t p = tm + C::kColS + bf * kKT;  // 32 keys: hi in 16 columns, lo in 16
             const uint64_t vhi = v0 + st * (C::kTile >> 4);
-            const uint64_t vlo = vhi + (C::kHalf >> 4);
+            const uint64_t vlo = vhi + (C::kBlock >> 4);
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kKT / 16; ++k) {  // 16 keys: 8 columns of P, 16 rows (2048 bytes) of V
@@ -739,11 +773,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tm + C::kColS + (n & 1) * kKT;
-                const uint64_t khi = k0 + st * (C::kTile >> 4), klo = khi + (C::kHalf >> 4);
+                const uint64_t khi = k0 + st * (C::kTile >> 4), klo = khi + (C::kBlock >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {  // 16 dims: 8 columns of Q, 32 bytes of a K row
-                        const uint64_t off = (uint64_t)(k >> 2) * (C::kBlock >> 4) + 2 * (k & 3);
+                        const uint64_t off = (uint64_t)(k >> 2) * (2 * C::kBlock >> 4) + 2 * (k & 3);
                         mma_f16_ts(d, tm + C::kColQhi + 8 * k, khi + off, id_s, k > 0 ? 1u : 0u);
                         mma_f16_ts(d, tm + C::kColQlo + 8 * k, khi + off, id_s, 1u);
                         mma_f16_ts(d, tm + C::kColQhi + 8 * k, klo + off, id_s, 1u);
@@ -839,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     alpha = row_softmax<CAP, false>(rt, m, l);
                 }
                 fold_f[nb][i] = make_float2(alpha, pow2_of((vtop >> 23) - kPShift));
-                const uint64_t bad = *reinterpret_cast<const uint64_t*>(v_bad[n8]);
+                const uint64_t bad = bad_rows<D>(v_bad[n8]);
                 if (bad) row_bad[nb][i] = bad & see;
                 if (u == s.u1 - 1) {
                     float* to = g.part_o + prow * D;
@@ -890,19 +924,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 f = fold_f[nb][i];
                 const uint64_t fx = f2_pack(f.x, f.x), fy = f2_pack(f.y, f.y);
                 const uint32_t at = tmem + lanes + C::kColO + bf * D + side * (D / 2);
+                float acc[2][16];
+                tmem_ld16(at, acc[0]);
 #pragma unroll
                 for (int c0 = 0; c0 < D / 2; c0 += 16) {
-                    float acc[16];
-                    tmem_ld16(at + c0, acc);
+                    float(&now)[16] = acc[(c0 >> 4) & 1];
                     tmem_wait_ld();
+                    if (c0 + 16 < D / 2) tmem_ld16(at + c0 + 16, acc[((c0 >> 4) & 1) ^ 1]);
 #pragma unroll
                     for (int d = 0; d < 16; d += 2)
-                        f2_unpack(f2_fma(f2_pack(acc[d], acc[d + 1]), fy, f2_mul(f2_pack(o[c0 + d], o[c0 + d + 1]), fx)),
+                        f2_unpack(f2_fma(f2_pack(now[d], now[d + 1]), fy, f2_mul(f2_pack(o[c0 + d], o[c0 + d + 1]), fx)),
                                   o[c0 + d], o[c0 + d + 1]);
                 }
                 tc_fence_before();
             }
-            if (*reinterpret_cast<const uint64_t*>(v_bad[n8]) && i < rows && row_bad[nb][i])  // rare
+            if (bad_rows<D>(v_bad[n8]) && i < rows && row_bad[nb][i])  // rare
                 odd = add_odd_values(a, ta, row_bad[nb][i], g.odd + ((int64_t)blockIdx.x * kM + i) * D + side * (D / 2),
                                      side * (D / 2), D / 2, odd);
             if (ta.x & kLast) {
@@ -991,18 +1027,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                     tc_fence_before();
                     ++piece;
+                    // headDim 64: two of the four warps vouch for the tile, and with it for
+                    // the queries of all four.
+                    if (D == 64) asm volatile("bar.sync 6, 128;" ::: "memory");
                 }
-                const int it = 2 * n + side, st = it % ST;
-                if (!__all_sync(FULL, wait_for(&full[st], (uint32_t)((it / ST) & 1)))) {
-                    raise_device_error(&g_paged_device_error, kErrPgLoad);
-                    ok = false;
-                    break;
+                // headDim 64: the tile's two warps of the four.
+                if (D == 128 || (n & 1) == (w >> 1)) {
+                    const int it = 2 * n + side, st = it % ST;
+                    if (!__all_sync(FULL, wait_for(&full[st], (uint32_t)((it / ST) & 1)))) {
+                        raise_device_error(&g_paged_device_error, kErrPgLoad);
+                        ok = false;
+                        break;
+                    }
+                    split_tile<D>(side != 0, smem_u32(tiles) + st * C::kTile, side ? v_scale[n & 7] : k_scale[n & 7],
+                                  v_bad[n & 7], row_max[n & 1][side], rows, w, lane);
+                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ready[st]);
                 }
-                split_tile<D>(side != 0, smem_u32(tiles) + st * C::kTile, side ? v_scale[n & 7] : k_scale[n & 7], v_bad[n & 7],
-                              rows, w, lane);
-                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ready[st]);
                 ++u;
             }
             if (n >= 2 && !fold(n - 2)) {
