@@ -296,16 +296,14 @@ __device__ __forceinline__ void split2(uint64_t x, uint32_t& hi, uint32_t& lo) {
     lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// The largest of |x.x| .. |x.w| and 2^-100 (NaN if one of them is): the least
-// exponent that a row's scale takes.
-__device__ __forceinline__ float abs_top(const float4& x) {
+// The largest of t and |x.x| .. |x.w|; NaN if one of them is.
+__device__ __forceinline__ float abs_top(float t, const float4& x) {
     float r;
-    asm("{\n .reg .f32 t;\n max.NaN.f32 t, %1, %2, %5;\n max.NaN.f32 %0, t, %3, %4;\n}\n"
+    asm("{\n .reg .f32 u;\n max.NaN.f32 u, %1, %2, %3;\n max.NaN.f32 %0, u, %4, %5;\n}\n"
         : "=f"(r)
-        : "f"(fabsf(x.x)), "f"(fabsf(x.y)), "f"(fabsf(x.z)), "f"(fabsf(x.w)), "f"(7.888609052210118e-31f));
+        : "f"(t), "f"(fabsf(x.x)), "f"(fabsf(x.y)), "f"(fabsf(x.z)), "f"(fabsf(x.w)));
     return r;
 }
-
 __device__ __forceinline__ float nan_max(float x, float y) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
@@ -324,30 +322,24 @@ __device__ __forceinline__ float4 lds4(uint32_t at) {
 __device__ __forceinline__ void sts4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-// Barrier ID over the two warps that share 32 rows.
-__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+// Rows whose largest |element| lies in [2^-9, 2^9) (or is zero) are taken times kScale:
+// f16 then holds hi and lo to 2^-22 of that element, as it does with a power of
+// two of the row's own, which the other rows take (a second look at them, in
+// global memory: rare). One pass over the tile instead of two: its shared-memory
+// traffic is what bounds the kernel.
+constexpr float kScale = 64.f, kUnscale = 1.f / 64.f, kTopMost = 512.f, kTopLeast = 1.f / 512.f;
 
 // 64 elements of a row of a tile (two blocks from `at` on, swizzled by sw = (row % 8)
-// 16): the largest |element|, at least 2^-100; NaN if one is.
-__device__ __forceinline__ float row_top(uint32_t at, uint32_t sw) {
-    float t[4];
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        const float4 x = lds4(at + (c >> 3) * (kKT * 128) + (((c & 7) << 4) ^ sw));
-        t[c & 3] = c < 4 ? abs_top(x) : nan_max(t[c & 3], abs_top(x));
-    }
-    return nan_max(nan_max(t[0], t[1]), nan_max(t[2], t[3]));
-}
-
-// The same 64 elements times `s` as f16: hi over the first block, lo over the
-// second, in place.  hi chunk c (8 elements, 16 bytes) lands on f32 chunk c, whose
-// elements went into hi chunk c / 2 (+ 4 in the second block); the first block is
-// taken upwards with its lo chunks kept, the second downwards, so that nothing is
-// written before it has been read.
-__device__ __forceinline__ void row_split(uint32_t at, uint32_t sw, float s) {
-    const uint64_t s2 = f2_pack(s, s);
+// 16) times kScale as f16: hi over the first block, lo over the second, in place.
+// hi chunk c (8 elements, 16 bytes) lands on f32 chunk c, whose elements went into
+// hi chunk c / 2 (+ 4 in the second block); the first block is taken upwards with its
+// lo chunks kept, the second downwards, so that nothing is written before it has
+// been read.  Returns the largest |element| (NaN if one is).
+__device__ __forceinline__ float row_split(uint32_t at, uint32_t sw) {
+    const uint64_t s2 = f2_pack(kScale, kScale);
     constexpr uint32_t kB = kKT * 128;
     uint32_t held[16];
+    float t = 0.f;
     // f32 chunks 2 c, 2 c + 1 of step i (c = 0 .. 3 of the first block, 3 .. 0 of the
     // second); a step's loads are on their way while the last one is converted.
     float4 x[2][2];
@@ -359,6 +351,7 @@ __device__ __forceinline__ void row_split(uint32_t at, uint32_t sw, float s) {
     };
     auto convert = [&](int i, uint32_t (&h)[4], uint32_t* l) {
         const float4 u = x[i & 1][0], v = x[i & 1][1];
+        t = abs_top(abs_top(t, u), v);
         split2(f2_mul(f2_pack(u.x, u.y), s2), h[0], l[0]);
         split2(f2_mul(f2_pack(u.z, u.w), s2), h[1], l[1]);
         split2(f2_mul(f2_pack(v.x, v.y), s2), h[2], l[2]);
@@ -382,54 +375,89 @@ __device__ __forceinline__ void row_split(uint32_t at, uint32_t sw, float s) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
         sts4(at + kB + ((c << 4) ^ sw), held[4 * c], held[4 * c + 1], held[4 * c + 2], held[4 * c + 3]);
+    return t;
+}
+
+// Row k of a tile (first key `key` of request b, or its drafted rows) in global memory,
+// KV head hk; null for a page id outside the pool.
+__device__ __forceinline__ const float* global_row(const PagedDesc& a, const float* pool, const float* fresh, int b, int key,
+                                                   int k, int hk) {
+    if (key < 0) return fresh + ((packed_rows(a.cu_rows, b, a.rows).row0 + k) * a.Hk + hk) * a.D;
+    const int64_t page = __ldg(a.block_table + (int64_t)b * a.max_pages + (key + k) / a.page_size);
+    if (page < 0 || page >= a.pages) return nullptr;
+    return pool + ((page * a.page_size + (key + k) % a.page_size) * a.Hk + hk) * a.D;
+}
+
+// A row outside row_split's range once more, elements 64 half .. of it: with its own
+// power of two, which is returned.  Values that are not finite become zeros
+// (`odd`), keys that are not finite stay so.
+__device__ __noinline__ float row_rescue(const float* row, int D, int half, bool values, uint32_t at, uint32_t sw, bool* odd) {
+    float t = 0.f, all = 0.f;  // of the finite elements; of all
+    for (int d = 0; d < D; d += 4) {
+        float4 x = *reinterpret_cast<const float4*>(row + d);
+        all = abs_top(all, x);
+        x = make_float4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
+        t = abs_top(t, x);
+    }
+    *odd = !(all < __int_as_float(0x7f800000));
+    if (*odd && !values) t = 1.f;
+    t = fminf(fmaxf(t, 7.888609052210118e-31f), 8.507059173023462e37f);  // 2^-100 .. 2^126
+    const uint32_t e = __float_as_uint(t) & 0x7f800000u;  // 2^E in f32; 2^-E is 0x7f000000 - e
+    const float s = __uint_as_float(0x7f000000u - e);
+    for (int c = 0; c < 8; ++c) {
+        float x[8];
+        for (int i = 0; i < 8; ++i) {
+            x[i] = row[64 * half + 8 * c + i];
+            if (values) x[i] = finite_or_zero(x[i]);
+        }
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split2(f2_pack(x[2 * i] * s, x[2 * i + 1] * s), h[i], l[i]);
+        sts4(at + ((c << 4) ^ sw), h[0], h[1], h[2], h[3]);
+        sts4(at + kKT * 128 + ((c << 4) ^ sw), l[0], l[1], l[2], l[3]);
+    }
+    return __uint_as_float(e);
 }
 
 // One tile of f32 rows to f16 hi and lo, in place; the rows' inverse scales to
 // `scale`.  TMA leaves 32 elements (128 bytes) of row r in row r of each block,
 // 128-byte swizzled; a thread takes 64 elements of one row (two blocks, which become
-// their hi and lo): with lane = row the swizzle makes its 16-byte accesses free of
-// bank conflicts, and nothing but the row's maximum crosses threads (D = 128: the
-// two halves of a row through `top`).  Rows past `rows` are zeros.  In value tiles
-// elements that are not finite become zeros here and `bad` gets the rows that had
-// one (they are added in the fold, to the rows that see them only); in key
-// tiles they make their own scores not finite, which the mask discards.
+// their hi and lo), neighbouring lanes neighbouring rows, so that the swizzle makes
+// its 16-byte accesses free of bank conflicts.  headDim 128: lanes 0 - 15 the first
+// halves of 16 rows, lanes 16 - 31 the second ones.  Rows past `rows` are
+// zeros.  In value tiles elements that are not finite become zeros and `bad` gets the
+// rows that had one (they are added in the fold, to the rows that see them
+// only); in key tiles they make their own scores not finite, which the mask
+// discards.  `scaled` tells whether a row has a scale of its own.
 template <int D>
-__device__ __forceinline__ void split_tile(bool values, uint32_t tile, float* scale, uint32_t* bad, float (*top)[kKT],
-                                           int rows, int w, int lane) {
-    const int half = D == 128 ? w & 1 : 0, row = 32 * (D == 128 ? w >> 1 : w & 1) + lane;
+__device__ __forceinline__ void split_tile(const PagedDesc& a, bool values, uint32_t tile, float* scale, uint32_t* bad,
+                                           uint32_t* scaled, const Seg& s, int key, int w, int lane) {
+    const int half = D == 128 ? lane >> 4 : 0, row = D == 128 ? 16 * w + (lane & 15) : 32 * (w & 1) + lane;
     uint32_t at = tile + 2 * half * (kKT * 128) + row * 128;
     asm volatile("" : "+r"(at));  // addresses are worked out here, not kept over the tile loop
     const uint32_t sw = (row & 7) << 4;
+    const int rows = tile_rows(s, key);
     if (rows < kKT && row >= rows) {  // the last tile of a cache, or drafted rows
         for (int c = 0; c < 16; ++c) sts4(at + (c >> 3) * (kKT * 128) + (c & 7) * 16, 0, 0, 0, 0);
     }
-    float t = row_top(at, sw);
-    uint32_t odd = 0;
-    if (__any_sync(FULL, !(t < 8.507059173023462e37f))) {  // rare: 2^126 or more, or not finite
-        const bool o = !(t < __int_as_float(0x7f800000));
-        odd = __ballot_sync(FULL, o);
-        if (o && values) {
-            for (int c = 0; c < 16; ++c) {
-                const uint32_t to = at + (c >> 3) * (kKT * 128) + (c & 7) * 16;
-                const float4 x = lds4(to);
-                sts4(to, __float_as_uint(finite_or_zero(x.x)), __float_as_uint(finite_or_zero(x.y)),
-                     __float_as_uint(finite_or_zero(x.z)), __float_as_uint(finite_or_zero(x.w)));
-            }
-            t = row_top(at, sw);
-        } else if (o) {
-            t = 1.f;
+    float t = row_split(at, sw), unscale = kUnscale;
+    if constexpr (D == 128) t = nan_max(t, __shfl_xor_sync(FULL, t, 16));
+    uint32_t odd_rows = 0;
+    const bool rescue = !(t < kTopMost) || (t < kTopLeast && t > 0.f);
+    const uint32_t rescued = __ballot_sync(FULL, rescue);
+    if (rescued) {
+        bool odd = false;
+        if (rescue) {
+            const float* src = global_row(a, values ? a.v_pool : a.k_pool, values ? a.v_new : a.k_new, s.b, key, row, s.hk);
+            if (src) unscale = row_rescue(src, D, half, values, at, sw, &odd);
         }
-        t = fminf(t, 8.507059173023462e37f);
+        odd_rows = __ballot_sync(FULL, odd);
     }
-    if (values && lane == 0) bad[w] = odd;
-    if constexpr (D == 128) {
-        top[half][row] = t;
-        pair_sync(2 + 2 * (values ? 1 : 0) + (w >> 1));
-        t = fmaxf(t, top[half ^ 1][row]);
+    if (half == 0) scale[row] = unscale;
+    if (lane == 0) {
+        scaled[w] = rescued;
+        if (values) bad[w] = D == 128 ? odd_rows & 0xffffu : odd_rows;
     }
-    const uint32_t e = __float_as_uint(t) & 0x7f800000u;  // 2^E in f32; 2^-E is 0x7f000000 - e
-    if (half == 0) scale[row] = __uint_as_float(e);
-    row_split(at, sw, __uint_as_float(0x7f000000u - e));
 }
 
 // mbar_wait, bounded in the same way, that looks at the clock after every 64 tries only:
@@ -452,7 +480,11 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
 template <int D>
 __device__ __forceinline__ uint64_t bad_rows(const uint32_t* b) {
     const uint4 v = *reinterpret_cast<const uint4*>(b);
-    return D == 128 ? (v.x | v.y) | (uint64_t)(v.z | v.w) << 32 : (v.x | v.z) | (uint64_t)(v.y | v.w) << 32;
+    return D == 128 ? (v.x | v.y << 16) | (uint64_t)(v.z | v.w << 16) << 32 : (v.x | v.z) | (uint64_t)(v.y | v.w) << 32;
+}
+__device__ __forceinline__ bool any_of(const uint32_t* b) {
+    const uint4 v = *reinterpret_cast<const uint4*>(b);
+    return (v.x | v.y | v.z | v.w) != 0;
 }
 
 // Values that are not finite would reach every row of a tile through 0 x inf =
@@ -461,20 +493,12 @@ __device__ __forceinline__ uint64_t bad_rows(const uint32_t* b) {
 // go to `odd` (thread-private; `more`: it holds earlier ones already).
 __device__ __noinline__ bool add_odd_values(const PagedDesc& a, int4 tile, uint64_t rows_bad, float* odd, int col, int n,
                                             bool more) {
-    const int D = a.D;
     while (rows_bad) {
         const int k = __ffsll((long long)rows_bad) - 1;
         rows_bad &= rows_bad - 1;
-        const float* src;
-        if (tile.z < 0) {
-            src = a.v_new + (packed_rows(a.cu_rows, tile.y, a.rows).row0 + k) * a.Hk * D;
-        } else {
-            const int key = tile.z + k;
-            const int64_t page = __ldg(a.block_table + (int64_t)tile.y * a.max_pages + key / a.page_size);
-            if (page < 0 || page >= a.pages) continue;
-            src = a.v_pool + (page * a.page_size + key % a.page_size) * a.Hk * D;
-        }
-        src += (int64_t)tile.w * D + col;
+        const float* src = global_row(a, a.v_pool, a.v_new, tile.y, tile.z, k, tile.w);
+        if (!src) continue;
+        src += col;
         for (int d = 0; d < n; ++d) {
             const float x = src[d];
             const float y = (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? x : 0.f;
@@ -495,27 +519,25 @@ __device__ __noinline__ bool join_odd_values(float* to, const float* odd, int n)
 // values' scales, the mask.
 struct RowTile {
     uint32_t at;
-    const float* ks;      // [64] key scales
-    const float* vs;      // [64] value scales; WHOLE: already times 2^kPShift / the largest
     uint64_t see;         // keys that the row sees (not read when WHOLE)
-    float qs;             // the query's scale
+    float mul;            // a score of the MMA times this is one in base-2 units (the argument of tanh with a cap)
     float cap;            // softcap in base-2 units
-    float v_mul;          // not WHOLE: 2^kPShift / the largest value scale seen
+    const float* ks;      // SCALED: [64] key scales
+    const float* vs;      // SCALED: [64] value scales
+    float v_mul;          // SCALED: 1 / the largest value scale seen
 };
 
-// 32 scores from key 32 c on, masked.  With a cap they come in base-2 units,
-// else q.k times the key's scale alone: the query's is left to the exponent's FMA.
-template <bool CAP, bool WHOLE>
+// 32 scores from key 32 c on, masked, in base-2 units with a cap, else still to be
+// multiplied by r.mul (in the exponent's FMA).
+template <bool CAP, bool WHOLE, bool SCALED>
 __device__ __forceinline__ void row_scores(const RowTile& r, int c, float (&x)[32]) {
     tmem_ld32(r.at + 32 * c, x);
     tmem_wait_ld();
+    if constexpr (SCALED) {
 #pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-        const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(r.ks + 32 * c + k);
-        f2_unpack(f2_mul(f2_pack(x[k], x[k + 1]), ks.x), x[k], x[k + 1]);
-        f2_unpack(f2_mul(f2_pack(x[k + 2], x[k + 3]), ks.y), x[k + 2], x[k + 3]);
+        for (int k = 0; k < 32; ++k) x[k] *= r.ks[32 * c + k];
     }
-    if constexpr (CAP) softcap_tile<32>(x, r.qs, r.cap);
+    if constexpr (CAP) softcap_tile<32>(x, r.mul, r.cap);
     if constexpr (!WHOLE) {
         const uint32_t bits = (uint32_t)(r.see >> (32 * c));
 #pragma unroll
@@ -523,45 +545,44 @@ __device__ __forceinline__ void row_scores(const RowTile& r, int c, float (&x)[3
     }
 }
 
-// The online softmax's step: m and l move on, P goes over the scores (keys 32 c
-// .. as f16 hi in 16 columns, lo in 16).  Returns alpha.  The scores are read
-// twice, for the maximum and for the probabilities: 64 of them do not fit the
-// registers at once.
-template <bool CAP, bool WHOLE>
+// The online softmax's step: m and l move on, P (times 2^kPShift, which l has too)
+// goes over the scores (keys 32 c .. as f16 hi in 16 columns, lo in 16).
+// Returns alpha.  The scores are read twice, for the maximum and for the
+// probabilities: 64 of them do not fit the registers at once.
+template <bool CAP, bool WHOLE, bool SCALED>
 __device__ __forceinline__ float row_softmax(const RowTile& r, float& m, float& l) {
     float mt = -INFINITY;
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
         float x[32];
-        row_scores<CAP, WHOLE>(r, c, x);
+        row_scores<CAP, WHOLE, SCALED>(r, c, x);
 #pragma unroll
         for (int k = 0; k < 32; k += 2) mt = fmaxf(fmaxf(mt, x[k]), x[k + 1]);
     }
-    const float mul = CAP ? 1.f : r.qs;
+    const float mul = CAP ? 1.f : r.mul;
     const float mn = fmaxf(m, mt * mul), mu = mn == -INFINITY ? 0.f : mn;
     const float alpha = fast_exp2(m - mu);
     m = mn;
-    const uint64_t mul2 = f2_pack(mul, mul), mu2 = f2_pack(-mu, -mu), v2 = f2_pack(r.v_mul, r.v_mul);
+    const float shift = (float)kPShift - mu;
+    const uint64_t mul2 = f2_pack(mul, mul), shift2 = f2_pack(shift, shift);
     uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
         float x[32];
-        row_scores<CAP, WHOLE>(r, c, x);
+        row_scores<CAP, WHOLE, SCALED>(r, c, x);
         float phi[16], plo[16];
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
-            const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(r.vs + 32 * c + k);
             float e0, e1, e2, e3;
-            f2_unpack(f2_fma(f2_pack(x[k], x[k + 1]), mul2, mu2), e0, e1);
-            f2_unpack(f2_fma(f2_pack(x[k + 2], x[k + 3]), mul2, mu2), e2, e3);
+            f2_unpack(f2_fma(f2_pack(x[k], x[k + 1]), mul2, shift2), e0, e1);
+            f2_unpack(f2_fma(f2_pack(x[k + 2], x[k + 3]), mul2, shift2), e2, e3);
             uint64_t p0 = f2_pack(fast_exp2(e0), fast_exp2(e1)), p1 = f2_pack(fast_exp2(e2), fast_exp2(e3));
             sum0 = f2_add(sum0, p0);
             sum1 = f2_add(sum1, p1);
-            p0 = f2_mul(p0, w.x);
-            p1 = f2_mul(p1, w.y);
-            if constexpr (!WHOLE) {
-                p0 = f2_mul(p0, v2);
-                p1 = f2_mul(p1, v2);
+            if constexpr (SCALED) {
+                const float* w = r.vs + 32 * c + k;
+                p0 = f2_mul(p0, f2_pack(w[0] * r.v_mul, w[1] * r.v_mul));
+                p1 = f2_mul(p1, f2_pack(w[2] * r.v_mul, w[3] * r.v_mul));
             }
             uint32_t h0, l0, h1, l1;
             split2(p0, h0, l0);
@@ -604,14 +625,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // P.V of tile n + 2, which follows the fold of tile n.
     __shared__ __align__(16) float k_scale[8][kKT], v_scale[8][kKT];
     __shared__ __align__(16) uint32_t v_bad[8][4];
-    __shared__ float row_max[2][2][2][kKT];      // by n % 2: keys and values, halves of the rows
+    __shared__ __align__(16) uint32_t k_scaled[8][4], v_scaled[8][4];
     __shared__ float q_scale[4][kM];             // by piece % 4
     __shared__ float2 fold_f[4][kM];             // alpha, output scale
     __shared__ uint64_t row_bad[4][kM];          // values to add that are not finite
     __shared__ int4 tile_at[4];                  // rows of the block (kLast: last tile of its piece), request, first key, KV head
     __shared__ float* row_out[4][kM];            // last tile of a piece: where the row goes
     __shared__ float row_inv[4][kM];
-    __shared__ __align__(16) float v_norm[4][kKT];  // per softmax warp: value scales of a tile all rows see
 
     const PagedDesc& a = g.a;
     const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform, to the compiler too
@@ -633,7 +653,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 1) tmem_alloc(&tmem_base_s, C::kTmemCols);
     if (threadIdx.x == 32) g.head[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (threadIdx.x < 32) (&v_bad[0][0])[threadIdx.x] = 0;
+    if (threadIdx.x < 32)  // headDim 64: two words of a tile's four are never written
+        (&v_bad[0][0])[threadIdx.x] = (&k_scaled[0][0])[threadIdx.x] = (&v_scaled[0][0])[threadIdx.x] = 0;
 
     // The requests' tiles and their running sum.
     long long carry = 0;
@@ -846,33 +867,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 RowTile rt;
                 rt.at = tmem + lanes + C::kColS + bf * kKT;
-                rt.ks = k_scale[n8];
                 rt.see = see;
-                rt.qs = q_scale[piece & 3][i];
+                rt.mul = q_scale[piece & 3][i] * kUnscale;
                 rt.cap = a.cap_log2;
-                // The largest value scale among the keys seen sets the probabilities'.
-                uint32_t vtop;
-                float alpha;
-                if (__all_sync(FULL, see == ~0ull)) {
-                    const float v0 = v_scale[n8][lane], v1 = v_scale[n8][lane + 32];
-                    vtop = __reduce_max_sync(FULL, max(__float_as_uint(v0), __float_as_uint(v1)));
-                    const float c = pow2_of(254u + kPShift - (vtop >> 23));
-                    v_norm[warp & 3][lane] = v0 * c;
-                    v_norm[warp & 3][lane + 32] = v1 * c;
-                    __syncwarp();
-                    rt.vs = v_norm[warp & 3];
-                    rt.v_mul = 1.f;
-                    alpha = row_softmax<CAP, true>(rt, m, l);
-                } else {
-                    vtop = 27u << 23;
-#pragma unroll 4
+                float alpha, o_scale = kUnscale;  // of the tile's output
+                if (any_of(k_scaled[n8]) || any_of(v_scaled[n8])) {  // rare
+                    // The largest value scale among the keys seen sets the probabilities'.
+                    o_scale = 7.888609052210118e-31f;
                     for (int k = 0; k < kKT; ++k)
-                        if ((see >> k) & 1) vtop = max(vtop, __float_as_uint(v_scale[n8][k]));
+                        if ((see >> k) & 1) o_scale = fmaxf(o_scale, v_scale[n8][k]);
+                    rt.mul = q_scale[piece & 3][i];
+                    rt.ks = k_scale[n8];
                     rt.vs = v_scale[n8];
-                    rt.v_mul = pow2_of(254u + kPShift - (vtop >> 23));
-                    alpha = row_softmax<CAP, false>(rt, m, l);
+                    rt.v_mul = __uint_as_float(0x7f000000u - __float_as_uint(o_scale));
+                    alpha = row_softmax<CAP, false, true>(rt, m, l);
+                } else if (__all_sync(FULL, see == ~0ull)) {
+                    alpha = row_softmax<CAP, true, false>(rt, m, l);
+                } else {
+                    alpha = row_softmax<CAP, false, false>(rt, m, l);
                 }
-                fold_f[nb][i] = make_float2(alpha, pow2_of((vtop >> 23) - kPShift));
+                fold_f[nb][i] = make_float2(alpha, o_scale);
                 const uint64_t bad = bad_rows<D>(v_bad[n8]);
                 if (bad) row_bad[nb][i] = bad & see;
                 if (u == s.u1 - 1) {
@@ -979,7 +993,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (count < 0) {
-                const int rows = tile_rows(s, tile_key(s, a.tree, u));
                 // A piece's queries once S(n - 1) is done with the last ones.
                 if (first && side == 0 && n > 0 &&
                     !__all_sync(FULL, wait_for(&freed[(2 * n - 2) % ST], (uint32_t)(((2 * n - 2) / ST) & 1)))) {
@@ -1039,8 +1052,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    split_tile<D>(side != 0, smem_u32(tiles) + st * C::kTile, side ? v_scale[n & 7] : k_scale[n & 7],
-                                  v_bad[n & 7], row_max[n & 1][side], rows, w, lane);
+                    split_tile<D>(a, side != 0, smem_u32(tiles) + st * C::kTile, side ? v_scale[n & 7] : k_scale[n & 7],
+                                  v_bad[n & 7], side ? v_scaled[n & 7] : k_scaled[n & 7], s, tile_key(s, a.tree, u), w, lane);
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ready[st]);
