@@ -35,11 +35,12 @@
 //   1       lane 0 issues the MMAs: S(n) = Q.K^T, then O(n - 1) = P.V;
 //   4 - 7   softmax, thread = virtual row: no exchange between threads; P goes
 //           back to TMEM over S as the A operand of P.V;
-//   8 - 15  split: raw f32 rows to hi and lo in the 128-byte swizzled layout
-//           (K K-major, V MN-major: the same bytes; four warps each), the unit's
-//           Q to TMEM, and the fold o = o alpha + O of the tile before last, 64 columns a thread
-//           (a fresh accumulator per tile: no sum runs long inside the pipe).
-// TMEM: Q hi, lo (D columns), S / P two buffers (128), O two buffers (2 D).
+//   8 - 15  split: f32 rows to f16 hi and lo in place (K K-major, V MN-major: the same
+//           bytes), four warps for the keys and four for the values;
+//   16 - 19 a piece's queries to TMEM, and the fold acc = acc alpha + O of each tile (a
+//           fresh accumulator per tile: no sum runs long inside the pipe); acc
+//           stays in TMEM, so that 20 warps fit the registers.
+// TMEM: Q hi, lo (D columns), S / P two buffers (128), O and its running sum (2 D).
 // Every wait is bounded; a wait that gives up sets a bit of the device flag.
 #include <cstring>
 #include <mutex>
@@ -66,9 +67,9 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kKT = 64;        // keys per tile
 constexpr int kM = 128;        // virtual rows per row block
-constexpr int kThreads = 512;
-constexpr int kFoldWarps = 8;
-constexpr int kLast = 1 << 16;
+constexpr int kThreads = 640;
+constexpr int kFoldWarps = 4;
+constexpr int kFirst = 1 << 16, kLast = 1 << 17;  // a piece's first and last tile
 constexpr int kPShift = 14;    // probabilities are scaled to at most 2^14 in f16
 
 enum : unsigned int {
@@ -94,10 +95,10 @@ struct Cfg {
     static constexpr uint32_t kTile = kKT * D * 4;
     static constexpr uint32_t kBlock = kKT * 128;                 // [64 rows x 128 bytes]: 32 f32, or 64 f16 hi or lo
     static constexpr int kSplitWarps = D == 128 ? 4 : 2;          // warps that split a tile
-    static constexpr uint32_t kColQhi = 0, kColQlo = D / 2, kColS = D, kColO = D + 2 * kKT;
+    static constexpr uint32_t kColQhi = 0, kColQlo = D / 2, kColS = D, kColO = D + 2 * kKT, kColAcc = kColO + D;
     static constexpr uint32_t kTmemCols = 512;
     static constexpr size_t kSmem = 1024 + (size_t)kSlots * kTile + (kPagedMaxRequests + 1) * 8;
-    static_assert(kColO + 2 * D <= kTmemCols, "TMEM budget");
+    static_assert(kColAcc + D <= kTmemCols, "TMEM budget");
     static_assert(kSmem + 25 * 1024 <= 232448, "shared memory budget");
     static_assert(kSlots % 2 == 0, "K in the even slots, V in the odd ones");
 };
@@ -615,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                             ~uintptr_t(1023));  // tile 2 n: K(n), 2 n + 1: V(n)
     long long* prefix = reinterpret_cast<long long*>(tiles + (size_t)ST * C::kTile);
     // A slot is loaded by TMA (full), split in place (ready), read by the MMAs (free).
-    __shared__ __align__(8) uint64_t full[ST], ready[ST], freed[ST], s_full[2], p_full[2], o_full[2], o_free[2];
+    __shared__ __align__(8) uint64_t full[ST], ready[ST], freed[ST], q_full, s_full[2], p_full[2], o_full, o_free;
     __shared__ uint32_t tmem_base_s;
     __shared__ long long scan_s[kThreads / 32];
     __shared__ Seg seg_s[kThreads / 32];
@@ -646,9 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
-            mbar_init(&o_full[i], 1);
-            mbar_init(&o_free[i], kFoldWarps);
         }
+        mbar_init(&q_full, kFoldWarps);
+        mbar_init(&o_full, 1);
+        mbar_init(&o_free, kFoldWarps);
         fence_barrier_init();
     }
     if (warp == 1) tmem_alloc(&tmem_base_s, C::kTmemCols);
@@ -754,18 +756,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t id_s = idesc_f16(kM, kKT, false), id_o = idesc_f16(kM, D, true);
         const uint32_t tm = __shfl_sync(FULL, tmem, 0);
         const uint64_t k0 = smem_desc_sw128(tiles), v0 = smem_desc_mn(tiles, 2 * C::kBlock);
-        int n = 0;
+        int n = 0, piece = 0;
         bool ok = true;
         auto pv = [&](int j) -> bool {  // O(j) = P(j).V(j)
             const int bf = j & 1, it = 2 * j + 1, st = it % ST;
             const uint32_t ph = (uint32_t)((j >> 1) & 1);
             if (!__all_sync(FULL, wait_for(&p_full[bf], ph) && wait_for(&ready[st], (uint32_t)((it / ST) & 1)) &&
-                                      (j < 2 || wait_for(&o_free[bf], ph ^ 1u)))) {
+                                      (j < 1 || wait_for(&o_free, (uint32_t)((j - 1) & 1))))) {
                 raise_device_error(&g_paged_device_error, kErrPgMma);
                 return false;
             }
             tc_fence_after();
-            const uint32_t d = tm + C::kColO + bf * D;
+            const uint32_t d = tm + C::kColO;
             const uint32_t p = tm + C::kColS + bf * kKT;  // 32 keys: hi in 16 columns, lo in 16
             const uint64_t vhi = v0 + st * (C::kTile >> 4);
             const uint64_t vlo = vhi + (C::kBlock >> 4);
@@ -778,16 +780,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_f16_ts(d, phi, vlo + 128 * k, id_o, 1u);
                 }
                 mma_commit(&freed[st]);
-                mma_commit(&o_full[bf]);
+                mma_commit(&o_full);
             }
             __syncwarp();
             return true;
         };
         while (ok && warp_next(g, prefix, s)) {
-            const int u1 = s.u1;
-            for (int u = s.u0; u < u1; ++u, ++n) {
+            const int u0 = s.u0, u1 = s.u1;
+            for (int u = u0; u < u1; ++u, ++n) {
                 const int it = 2 * n, st = it % ST;
-                if (!__all_sync(FULL, wait_for(&ready[st], (uint32_t)((it / ST) & 1)))) {
+                if (!__all_sync(FULL, (u > u0 || wait_for(&q_full, (uint32_t)(piece & 1))) &&
+                                          wait_for(&ready[st], (uint32_t)((it / ST) & 1)))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
                     break;
@@ -812,6 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
             }
+            if (u1 > u0) ++piece;
         }
         if (ok && n > 0) pv(n - 1);
     } else if (warp >= 4 && warp < 8) {
@@ -902,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     row_out[nb][i] = to;
                     row_inv[nb][i] = inv;
                 }
-                if (i == 0) tile_at[nb] = make_int4(rows + (u == s.u1 - 1 ? kLast : 0), s.b, key, s.hk);
+                if (i == 0) tile_at[nb] = make_int4(rows + (u == s.u0 ? kFirst : 0) + (u == s.u1 - 1 ? kLast : 0), s.b, key, s.hk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -914,157 +918,160 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = rows_sync_and(ok);
             ++piece;
         }
-    } else if (warp >= 8) {
-        // ---- split, queries and fold: warps 8 - 11 the keys and the queries, 12 - 15
-        // the values; both fold, each its half of the columns ----
+    } else if (warp >= 8 && warp < 16) {
+        // ---- split: warps 8 - 11 the keys, 12 - 15 the values ------------------------
         const int w = warp & 3, side = (warp - 8) >> 2;
+        int n = 0;
+        bool ok = true;
+        while (ok && warp_next(g, prefix, s)) {
+            const int u1 = s.u1;
+            for (int u = s.u0; u < u1; ++u, ++n) {
+                if (D == 64 && (n & 1) != (w >> 1)) continue;  // a tile's two warps of the four
+                const int it = 2 * n + side, st = it % ST;
+                if (!__all_sync(FULL, wait_for(&full[st], (uint32_t)((it / ST) & 1)))) {
+                    raise_device_error(&g_paged_device_error, kErrPgLoad);
+                    ok = false;
+                    break;
+                }
+                split_tile<D>(a, side != 0, smem_u32(tiles) + st * C::kTile, side ? v_scale[n & 7] : k_scale[n & 7],
+                              v_bad[n & 7], side ? v_scaled[n & 7] : k_scaled[n & 7], s, tile_key(s, a.tree, u), w, lane);
+                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ready[st]);
+            }
+        }
+    } else if (warp >= 16) {
+        // ---- queries and fold: thread = virtual row -----------------------------------
+        const int w = warp & 3, i = 32 * w + lane;
         const uint32_t lanes = (uint32_t)(32 * w) << 16;
-        const int i = 32 * w + lane;
-        float o[D / 2];
-#pragma unroll
-        for (int d = 0; d < D / 2; ++d) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(o[d]));
         int n = 0, piece = 0;
         bool ok = true, odd = false;
+        // Row i of the piece's block: q scaled by qk_mul, then as a row of a tile, with a
+        // power of two of its own; two elements to a column of Q hi and Q lo.
+        auto load_queries = [&]() {
+            const int v = s.rb * kM + i, t = v / a.G;
+            const bool alive = v < s.T * a.G;
+            const float* q = a.q + (((int64_t)s.row0 + t) * a.H + (int64_t)s.hk * a.G + (v - t * a.G)) * D;
+            auto load4 = [&](int d) -> float4 {
+                if (!alive) return make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 y = __ldg(reinterpret_cast<const float4*>(q + d));
+                return make_float4(y.x * a.qk_mul, y.y * a.qk_mul, y.z * a.qk_mul, y.w * a.qk_mul);
+            };
+            float top = 0.f;
+#pragma unroll 8
+            for (int d = 0; d < D; d += 4) {
+                const float4 y = load4(d);
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
+            }
+            const uint32_t e = row_exponent(__float_as_uint(top));
+            const float sc = pow2_of(254u - e);
+            q_scale[piece & 3][i] = pow2_of(e);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D / 2; c0 += 16) {
+                float qh[16], ql[16];
+#pragma unroll
+                for (int c = 0; c < 16; c += 2) {
+                    const float4 y = load4(2 * (c0 + c));
+                    uint32_t h0, l0, h1, l1;
+                    split2(f2_pack(y.x * sc, y.y * sc), h0, l0);
+                    split2(f2_pack(y.z * sc, y.w * sc), h1, l1);
+                    qh[c] = __uint_as_float(h0);
+                    qh[c + 1] = __uint_as_float(h1);
+                    ql[c] = __uint_as_float(l0);
+                    ql[c + 1] = __uint_as_float(l1);
+                }
+                tmem_st16(tmem + lanes + C::kColQhi + c0, qh);
+                tmem_st16(tmem + lanes + C::kColQlo + c0, ql);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full);
+            ++piece;
+        };
+        // acc = acc alpha + O of tile j; after a piece's last tile to where the row goes.
         auto fold = [&](int j) -> bool {
-            const int nb = j & 3, n8 = j & 7, bf = j & 1;
-            if (!__all_sync(FULL, wait_for(&o_full[bf], (uint32_t)((j >> 1) & 1)))) {
+            const int nb = j & 3, n8 = j & 7;
+            if (!__all_sync(FULL, wait_for(&o_full, (uint32_t)(j & 1)))) {
                 raise_device_error(&g_paged_device_error, kErrPgMma);
                 return false;
             }
             tc_fence_after();
             const int4 ta = tile_at[nb];
-            const int rows = ta.x & (kLast - 1);
+            const int rows = ta.x & (kFirst - 1);
+            const bool first = ta.x & kFirst, last = ta.x & kLast;
             if (32 * w < rows) {
                 const float2 f = fold_f[nb][i];
                 const uint64_t fx = f2_pack(f.x, f.x), fy = f2_pack(f.y, f.y);
-                const uint32_t at = tmem + lanes + C::kColO + bf * D + side * (D / 2);
-                float acc[2][16];
-                tmem_ld16(at, acc[0]);
-#pragma unroll
-                for (int c0 = 0; c0 < D / 2; c0 += 16) {
-                    float(&now)[16] = acc[(c0 >> 4) & 1];
+                const uint32_t at = tmem + lanes + C::kColO;
+                float* to = last ? row_out[nb][i] : nullptr;
+                const float inv = last ? row_inv[nb][i] : 1.f;
+                const uint64_t inv2 = f2_pack(inv, inv);
+                if (bad_rows<D>(v_bad[n8]) && i < rows && row_bad[nb][i])  // rare
+                    odd = add_odd_values(a, ta, row_bad[nb][i], g.odd + ((int64_t)blockIdx.x * kM + i) * D, 0, D, odd);
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    float x[32], y[32];
+                    tmem_ld32(at + c0, x);
+                    if (!first) tmem_ld32(at + (C::kColAcc - C::kColO) + c0, y);
                     tmem_wait_ld();
-                    if (c0 + 16 < D / 2) tmem_ld16(at + c0 + 16, acc[((c0 >> 4) & 1) ^ 1]);
+                    if (first) {
 #pragma unroll
-                    for (int d = 0; d < 16; d += 2)
-                        f2_unpack(f2_fma(f2_pack(now[d], now[d + 1]), fy, f2_mul(f2_pack(o[c0 + d], o[c0 + d + 1]), fx)),
-                                  o[c0 + d], o[c0 + d + 1]);
+                        for (int d = 0; d < 32; d += 2) f2_unpack(f2_mul(f2_pack(x[d], x[d + 1]), fy), x[d], x[d + 1]);
+                    } else {
+#pragma unroll
+                        for (int d = 0; d < 32; d += 2)
+                            f2_unpack(f2_fma(f2_pack(x[d], x[d + 1]), fy, f2_mul(f2_pack(y[d], y[d + 1]), fx)), x[d], x[d + 1]);
+                    }
+                    if (!last) {
+                        tmem_st32(at + (C::kColAcc - C::kColO) + c0, x);
+                    } else if (i < rows) {
+#pragma unroll
+                        for (int d = 0; d < 32; d += 4) {
+                            float4 r;
+                            f2_unpack(f2_mul(f2_pack(x[d], x[d + 1]), inv2), r.x, r.y);
+                            f2_unpack(f2_mul(f2_pack(x[d + 2], x[d + 3]), inv2), r.z, r.w);
+                            *reinterpret_cast<float4*>(to + c0 + d) = r;
+                        }
+                    }
                 }
+                tmem_wait_st();
+                if (last && odd) odd = join_odd_values(to, g.odd + ((int64_t)blockIdx.x * kM + i) * D, D);
                 tc_fence_before();
             }
-            if (bad_rows<D>(v_bad[n8]) && i < rows && row_bad[nb][i])  // rare
-                odd = add_odd_values(a, ta, row_bad[nb][i], g.odd + ((int64_t)blockIdx.x * kM + i) * D + side * (D / 2),
-                                     side * (D / 2), D / 2, odd);
-            if (ta.x & kLast) {
-                if (i < rows) {
-                    float* to = row_out[nb][i] + side * (D / 2);
-                    const float inv = row_inv[nb][i];
-#pragma unroll
-                    for (int d = 0; d < D / 2; d += 4)
-                        *reinterpret_cast<float4*>(to + d) =
-                            make_float4(o[d] * inv, o[d + 1] * inv, o[d + 2] * inv, o[d + 3] * inv);
-                    if (odd) odd = join_odd_values(to, g.odd + ((int64_t)blockIdx.x * kM + i) * D + side * (D / 2), D / 2);
-                }
-                // Opaque zeros: as constants they make the compiler keep a second copy of
-                // the loop's registers, and spill.
-#pragma unroll
-                for (int d = 0; d < D / 2; ++d) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(o[d]));
-            }
             __syncwarp();  // after everything that tile j left in shared memory has been read
-            if (lane == 0) mbar_arrive(&o_free[bf]);
+            if (lane == 0) mbar_arrive(&o_free);
             return true;
         };
-        // Tile n is split in step n and folded in step n + 2; the two steps after
-        // the last tile only fold.
-        int u = 0, u1 = 0, count = -1;
-        while (ok && (count < 0 || n < count + 2)) {
-            bool first = false;
-            if (count < 0 && u >= u1) {
-                bool more;
-                do more = warp_next(g, prefix, s);
-                while (more && s.u1 <= s.u0);
-                if (more) {
-                    u = s.u0;
-                    u1 = s.u1;
-                    first = true;
-                } else {
-                    count = n;
-                    if (count == 0) break;
+        auto next_piece = [&]() -> bool {  // the next one that has tiles
+            bool more;
+            do more = warp_next(g, prefix, s);
+            while (more && s.u1 <= s.u0);
+            return more;
+        };
+        bool more = next_piece();
+        if (more) load_queries();
+        while (ok && more) {
+            const int end = n + s.u1 - s.u0;
+            for (; n < end; ++n) {
+                if (n == end - 1) {
+                    // The next piece's queries, once S(n) is done with this one's.
+                    more = next_piece();
+                    if (more) {
+                        if (!__all_sync(FULL, wait_for(&freed[(2 * n) % ST], (uint32_t)(((2 * n) / ST) & 1)))) {
+                            raise_device_error(&g_paged_device_error, kErrPgMma);
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        load_queries();
+                    }
                 }
-            }
-            if (count < 0) {
-                // A piece's queries once S(n - 1) is done with the last ones.
-                if (first && side == 0 && n > 0 &&
-                    !__all_sync(FULL, wait_for(&freed[(2 * n - 2) % ST], (uint32_t)(((2 * n - 2) / ST) & 1)))) {
-                    raise_device_error(&g_paged_device_error, kErrPgMma);
+                if (!fold(n)) {
                     ok = false;
                     break;
                 }
-                if (first && side == 0) {
-                    // Row i of the block: q scaled by qk_mul, then as any row; two
-                    // elements to a column of Q hi and Q lo.
-                    const int v = s.rb * kM + i, t = v / a.G;
-                    const bool alive = v < s.T * a.G;
-                    const float* q = a.q + (((int64_t)s.row0 + t) * a.H + (int64_t)s.hk * a.G + (v - t * a.G)) * D;
-                    auto load4 = [&](int d) -> float4 {
-                        if (!alive) return make_float4(0.f, 0.f, 0.f, 0.f);
-                        const float4 y = __ldg(reinterpret_cast<const float4*>(q + d));
-                        return make_float4(y.x * a.qk_mul, y.y * a.qk_mul, y.z * a.qk_mul, y.w * a.qk_mul);
-                    };
-                    float top = 0.f;
-#pragma unroll 8
-                    for (int d = 0; d < D; d += 4) {
-                        const float4 y = load4(d);
-                        top = fmaxf(top, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
-                    }
-                    const uint32_t e = row_exponent(__float_as_uint(top));
-                    const float sc = pow2_of(254u - e);
-                    q_scale[piece & 3][i] = pow2_of(e);
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D / 2; c0 += 16) {
-                        float qh[16], ql[16];
-#pragma unroll
-                        for (int c = 0; c < 16; c += 2) {
-                            const float4 y = load4(2 * (c0 + c));
-                            uint32_t h0, l0, h1, l1;
-                            split2(f2_pack(y.x * sc, y.y * sc), h0, l0);
-                            split2(f2_pack(y.z * sc, y.w * sc), h1, l1);
-                            qh[c] = __uint_as_float(h0);
-                            qh[c + 1] = __uint_as_float(h1);
-                            ql[c] = __uint_as_float(l0);
-                            ql[c + 1] = __uint_as_float(l1);
-                        }
-                        tmem_st16(tmem + lanes + C::kColQhi + c0, qh);
-                        tmem_st16(tmem + lanes + C::kColQlo + c0, ql);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    ++piece;
-                    // headDim 64: two of the four warps vouch for the tile, and with it for
-                    // the queries of all four.
-                    if (D == 64) asm volatile("bar.sync 6, 128;" ::: "memory");
-                }
-                // headDim 64: the tile's two warps of the four.
-                if (D == 128 || (n & 1) == (w >> 1)) {
-                    const int it = 2 * n + side, st = it % ST;
-                    if (!__all_sync(FULL, wait_for(&full[st], (uint32_t)((it / ST) & 1)))) {
-                        raise_device_error(&g_paged_device_error, kErrPgLoad);
-                        ok = false;
-                        break;
-                    }
-                    split_tile<D>(a, side != 0, smem_u32(tiles) + st * C::kTile, side ? v_scale[n & 7] : k_scale[n & 7],
-                                  v_bad[n & 7], side ? v_scaled[n & 7] : k_scaled[n & 7], s, tile_key(s, a.tree, u), w, lane);
-                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ready[st]);
-                }
-                ++u;
             }
-            if (n >= 2 && !fold(n - 2)) {
-                ok = false;
-                break;
-            }
-            ++n;
         }
     }
 
