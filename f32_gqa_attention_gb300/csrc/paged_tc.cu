@@ -772,13 +772,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t vhi = v0 + st * (C::kTile >> 4);
             const uint64_t vlo = vhi + (C::kBlock >> 4);
             if (elect_one()) {
+                // 16 keys: 8 columns of P, 16 rows (2048 bytes) of V.  The small products
+                // come first: the accumulator's rounding (towards zero, at every step) then
+                // meets the full sum a third as often.
 #pragma unroll
-                for (int k = 0; k < kKT / 16; ++k) {  // 16 keys: 8 columns of P, 16 rows (2048 bytes) of V
+                for (int k = 0; k < kKT / 16; ++k) {
                     const uint32_t phi = p + 32 * (k >> 1) + 8 * (k & 1), plo = phi + 16;
-                    mma_f16_ts(d, phi, vhi + 128 * k, id_o, k > 0 ? 1u : 0u);
-                    mma_f16_ts(d, plo, vhi + 128 * k, id_o, 1u);
+                    mma_f16_ts(d, plo, vhi + 128 * k, id_o, k > 0 ? 1u : 0u);
                     mma_f16_ts(d, phi, vlo + 128 * k, id_o, 1u);
                 }
+#pragma unroll
+                for (int k = 0; k < kKT / 16; ++k)
+                    mma_f16_ts(d, p + 32 * (k >> 1) + 8 * (k & 1), vhi + 128 * k, id_o, 1u);
                 mma_commit(&freed[st]);
                 mma_commit(&o_full);
             }
@@ -799,13 +804,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t d = tm + C::kColS + (n & 1) * kKT;
                 const uint64_t khi = k0 + st * (C::kTile >> 4), klo = khi + (C::kBlock >> 4);
                 if (elect_one()) {
+                    // 16 dims: 8 columns of Q, 32 bytes of a K row.
+                    auto off = [](int k) -> uint64_t { return (uint64_t)(k >> 2) * (2 * C::kBlock >> 4) + 2 * (k & 3); };
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {  // 16 dims: 8 columns of Q, 32 bytes of a K row
-                        const uint64_t off = (uint64_t)(k >> 2) * (2 * C::kBlock >> 4) + 2 * (k & 3);
-                        mma_f16_ts(d, tm + C::kColQhi + 8 * k, khi + off, id_s, k > 0 ? 1u : 0u);
-                        mma_f16_ts(d, tm + C::kColQlo + 8 * k, khi + off, id_s, 1u);
-                        mma_f16_ts(d, tm + C::kColQhi + 8 * k, klo + off, id_s, 1u);
+                    for (int k = 0; k < D / 16; ++k) {
+                        mma_f16_ts(d, tm + C::kColQlo + 8 * k, khi + off(k), id_s, k > 0 ? 1u : 0u);
+                        mma_f16_ts(d, tm + C::kColQhi + 8 * k, klo + off(k), id_s, 1u);
                     }
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) mma_f16_ts(d, tm + C::kColQhi + 8 * k, khi + off(k), id_s, 1u);
                     mma_commit(&freed[st]);
                     mma_commit(&s_full[n & 1]);
                 }
