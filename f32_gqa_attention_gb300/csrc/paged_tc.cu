@@ -38,7 +38,7 @@
 //   8 - 15  split: f32 rows to f16 hi and lo in place (K K-major, V MN-major: the same
 //           bytes), four warps for the keys and four for the values;
 //   16 - 19 a piece's queries to TMEM, and the fold acc = acc alpha + O of each tile (a
-//           fresh accumulator per tile: no sum runs long inside the pipe); acc
+//           fresh accumulator for every two tiles: no sum runs long inside the pipe); acc
 //           stays in TMEM, so that 20 warps fit the registers.
 // TMEM: Q hi, lo (D columns), S / P two buffers (128), O and its running sum (2 D).
 // Every wait is bounded; a wait that gives up sets a bit of the device flag.
@@ -70,7 +70,9 @@ constexpr int kM = 128;        // virtual rows per row block
 constexpr int kThreads = 640;
 constexpr int kFoldWarps = 4;
 constexpr int kFirst = 1 << 16, kLast = 1 << 17;  // a piece's first and last tile
-constexpr int kPShift = 14;    // probabilities are scaled to at most 2^14 in f16
+constexpr int kPShift = 11;    // probabilities are scaled by 2^11 in f16
+constexpr float kLazyLog2 = 4.f;  // and a row's reference maximum moves when beaten by more than 2^4: 2^15 at most
+constexpr int kGroup = 2;      // tiles that one accumulator takes before it is folded
 
 enum : unsigned int {
     kErrPgLoad = 1u << 3,   // the splitters gave up on a loaded tile
@@ -259,13 +261,13 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
-// Barrier over the four softmax warps; the AND of `v` over them.
-__device__ __forceinline__ bool rows_sync_and(bool v) {
+// Barrier `id` over `threads` threads; the AND of `v` over them.
+__device__ __forceinline__ bool sync_and(int id, int threads, bool v) {
     uint32_t r;
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.and.pred p, 1, 128, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+        "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.and.pred p, %2, %3, q;\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(r)
-        : "r"((uint32_t)v)
+        : "r"((uint32_t)v), "r"(id), "r"(threads)
         : "memory");
     return r != 0;
 }
@@ -331,53 +333,33 @@ __device__ __forceinline__ void sts4(uint32_t at, uint32_t x, uint32_t y, uint32
 constexpr float kScale = 64.f, kUnscale = 1.f / 64.f, kTopMost = 512.f, kTopLeast = 1.f / 512.f;
 
 // 64 elements of a row of a tile (two blocks from `at` on, swizzled by sw = (row % 8)
-// 16) times kScale as f16: hi over the first block, lo over the second, in place.
-// hi chunk c (8 elements, 16 bytes) lands on f32 chunk c, whose elements went into
-// hi chunk c / 2 (+ 4 in the second block); the first block is taken upwards with its
-// lo chunks kept, the second downwards, so that nothing is written before it has
-// been read.  Returns the largest |element| (NaN if one is).
+// 16) times kScale as f16: hi over the first block, lo over the second, in place:
+// chunk c (16 bytes) of both takes the elements that chunk c of the two blocks had,
+// 4 c .. 4 c + 3 and 32 + 4 c .. 32 + 4 c + 3.  (So a tile's elements come in
+// another order; the queries are laid out in the same one, and the fold puts the
+// outputs back.)  A short loop on purpose: five warps with code of their own share a
+// scheduler, and unrolled it ran at the rate of instruction fetches.  Returns the
+// largest |element| (NaN if one is).
 __device__ __forceinline__ float row_split(uint32_t at, uint32_t sw) {
     const uint64_t s2 = f2_pack(kScale, kScale);
-    constexpr uint32_t kB = kKT * 128;
-    uint32_t held[16];
     float t = 0.f;
-    // f32 chunks 2 c, 2 c + 1 of step i (c = 0 .. 3 of the first block, 3 .. 0 of the
-    // second); a step's loads are on their way while the last one is converted.
-    float4 x[2][2];
-    auto load = [&](int i) {
-        const int c = i < 4 ? i : 7 - i;
-        const uint32_t from = at + (i < 4 ? 0 : kB);
-        x[i & 1][0] = lds4(from + (((2 * c) << 4) ^ sw));
-        x[i & 1][1] = lds4(from + (((2 * c + 1) << 4) ^ sw));
-    };
-    auto convert = [&](int i, uint32_t (&h)[4], uint32_t* l) {
-        const float4 u = x[i & 1][0], v = x[i & 1][1];
-        t = abs_top(abs_top(t, u), v);
-        split2(f2_mul(f2_pack(u.x, u.y), s2), h[0], l[0]);
-        split2(f2_mul(f2_pack(u.z, u.w), s2), h[1], l[1]);
-        split2(f2_mul(f2_pack(v.x, v.y), s2), h[2], l[2]);
-        split2(f2_mul(f2_pack(v.z, v.w), s2), h[3], l[3]);
-    };
-    load(0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (i < 7) load(i + 1);
+#pragma unroll 2
+    for (uint32_t c = 0; c < 128; c += 16) {
+        const uint32_t to = at + (c ^ sw);
+        const float4 x = lds4(to), y = lds4(to + kKT * 128);
+        t = abs_top(abs_top(t, x), y);
         uint32_t h[4], l[4];
-        if (i < 4) {
-            convert(i, h, held + 4 * i);
-            sts4(at + ((i << 4) ^ sw), h[0], h[1], h[2], h[3]);
-        } else {
-            const int c = 11 - i;  // hi and lo chunk
-            convert(i, h, l);
-            sts4(at + ((c << 4) ^ sw), h[0], h[1], h[2], h[3]);
-            sts4(at + kB + ((c << 4) ^ sw), l[0], l[1], l[2], l[3]);
-        }
+        split2(f2_mul(f2_pack(x.x, x.y), s2), h[0], l[0]);
+        split2(f2_mul(f2_pack(x.z, x.w), s2), h[1], l[1]);
+        split2(f2_mul(f2_pack(y.x, y.y), s2), h[2], l[2]);
+        split2(f2_mul(f2_pack(y.z, y.w), s2), h[3], l[3]);
+        sts4(to, h[0], h[1], h[2], h[3]);
+        sts4(to + kKT * 128, l[0], l[1], l[2], l[3]);
     }
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        sts4(at + kB + ((c << 4) ^ sw), held[4 * c], held[4 * c + 1], held[4 * c + 2], held[4 * c + 3]);
     return t;
 }
+// First element of the c-th (0 .. D / 4 - 1) group of four in a tile's order.
+__device__ __forceinline__ int tile_order(int c) { return (c >> 4) * 64 + (c & 1) * 32 + ((c >> 1) & 7) * 4; }
 
 // Row k of a tile (first key `key` of request b, or its drafted rows) in global memory,
 // KV head hk; null for a page id outside the pool.
@@ -408,7 +390,7 @@ __device__ __noinline__ float row_rescue(const float* row, int D, int half, bool
     for (int c = 0; c < 8; ++c) {
         float x[8];
         for (int i = 0; i < 8; ++i) {
-            x[i] = row[64 * half + 8 * c + i];
+            x[i] = row[tile_order(16 * half + 2 * c + (i >> 2)) + (i & 3)];
             if (values) x[i] = finite_or_zero(x[i]);
         }
         uint32_t h[4], l[4];
@@ -475,6 +457,15 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) {
 }
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
     return mbar_try_wait(bar, parity) || wait_long(bar, parity);
+}
+// A wait of several warps: the first one looks at the mbarrier while the others sleep at
+// barrier `id` (18 warps that all looked took two fifths of the issue slots), then
+// each looks once, for what the mbarrier orders.
+__device__ __forceinline__ bool team_wait(bool leads, int id, int threads, uint64_t* bar, uint32_t parity) {
+    bool ok = true;
+    if (leads) ok = __all_sync(FULL, wait_for(bar, parity));
+    ok = sync_and(id, threads, ok);
+    return ok && (leads || __all_sync(FULL, wait_for(bar, parity)));
 }
 
 // Rows of a value tile with elements that are not finite, from what its warps found.
@@ -546,12 +537,12 @@ __device__ __forceinline__ void row_scores(const RowTile& r, int c, float (&x)[3
     }
 }
 
-// The online softmax's step: m and l move on, P (times 2^kPShift, which l has too)
+// The online softmax's step: l and, where it is beaten, m move on; P (times 2^kPShift, which l has too)
 // goes over the scores (keys 32 c .. as f16 hi in 16 columns, lo in 16).
-// Returns alpha.  The scores are read twice, for the maximum and for the
+// Returns alpha; `moved`: m, the row's reference, is another one now.  The scores are read twice, for the maximum and for the
 // probabilities: 64 of them do not fit the registers at once.
 template <bool CAP, bool WHOLE, bool SCALED>
-__device__ __forceinline__ float row_softmax(const RowTile& r, float& m, float& l) {
+__device__ __forceinline__ float row_softmax(const RowTile& r, float& m, float& l, bool& moved) {
     float mt = -INFINITY;
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
@@ -561,8 +552,9 @@ __device__ __forceinline__ float row_softmax(const RowTile& r, float& m, float& 
         for (int k = 0; k < 32; k += 2) mt = fmaxf(fmaxf(mt, x[k]), x[k + 1]);
     }
     const float mul = CAP ? 1.f : r.mul;
-    const float mn = fmaxf(m, mt * mul), mu = mn == -INFINITY ? 0.f : mn;
-    const float alpha = fast_exp2(m - mu);
+    moved = mt * mul > m + kLazyLog2;
+    const float mn = moved ? mt * mul : m, mu = mn == -INFINITY ? 0.f : mn;
+    const float alpha = moved ? fast_exp2(m - mu) : 1.f;
     m = mn;
     const float shift = (float)kPShift - mu;
     const uint64_t mul2 = f2_pack(mul, mul), shift2 = f2_pack(shift, shift);
@@ -630,6 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ float q_scale[4][kM];             // by piece % 4
     __shared__ float2 fold_f[4][kM];             // alpha, output scale
     __shared__ uint64_t row_bad[4][kM];          // values to add that are not finite
+    __shared__ int group_tag[4];                 // n + 1: tile n begins a group (written by the softmax)
+    __shared__ int2 group_at[2];                 // a group's first and last tile
     __shared__ int4 tile_at[4];                  // rows of the block (kLast: last tile of its piece), request, first key, KV head
     __shared__ float* row_out[4][kM];            // last tile of a piece: where the row goes
     __shared__ float row_inv[4][kM];
@@ -649,12 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&p_full[i], 4);
         }
         mbar_init(&q_full, kFoldWarps);
-        mbar_init(&o_full, 1);
+        mbar_init(&o_full, 2);  // the MMAs' commit, and an arrival that publishes group_at
         mbar_init(&o_free, kFoldWarps);
         fence_barrier_init();
     }
     if (warp == 1) tmem_alloc(&tmem_base_s, C::kTmemCols);
     if (threadIdx.x == 32) g.head[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (threadIdx.x < 4) group_tag[threadIdx.x] = 0;
     if (threadIdx.x < 32)  // headDim 64: two words of a tile's four are never written
         (&v_bad[0][0])[threadIdx.x] = (&k_scaled[0][0])[threadIdx.x] = (&v_scaled[0][0])[threadIdx.x] = 0;
 
@@ -757,14 +752,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tm = __shfl_sync(FULL, tmem, 0);
         const uint64_t k0 = smem_desc_sw128(tiles), v0 = smem_desc_mn(tiles, 2 * C::kBlock);
         int n = 0, piece = 0;
+        // Groups of tiles share an accumulator: `len` tiles in the open one, the first
+        // of them `from`; `groups` are closed.
+        int len = 0, from = 0, groups = 0;
         bool ok = true;
-        auto pv = [&](int j) -> bool {  // O(j) = P(j).V(j)
+        auto close = [&](int j) {
+            if (elect_one()) {
+                group_at[groups & 1] = make_int2(from, j);
+                mbar_arrive(&o_full);
+                mma_commit(&o_full);
+            }
+            __syncwarp();
+            ++groups;
+            len = 0;
+        };
+        auto pv = [&](int j, bool first, bool last) -> bool {  // O (+)= P(j).V(j)
             const int bf = j & 1, it = 2 * j + 1, st = it % ST;
             const uint32_t ph = (uint32_t)((j >> 1) & 1);
-            if (!__all_sync(FULL, wait_for(&p_full[bf], ph) && wait_for(&ready[st], (uint32_t)((it / ST) & 1)) &&
-                                      (j < 1 || wait_for(&o_free, (uint32_t)((j - 1) & 1))))) {
+            if (!__all_sync(FULL, wait_for(&p_full[bf], ph) && wait_for(&ready[st], (uint32_t)((it / ST) & 1)))) {
                 raise_device_error(&g_paged_device_error, kErrPgMma);
                 return false;
+            }
+            if (len > 0 && (first || __shfl_sync(FULL, group_tag[j & 3], 0) == j + 1)) close(j - 1);
+            if (len == 0) {
+                from = j;
+                if (groups > 0 && !__all_sync(FULL, wait_for(&o_free, (uint32_t)((groups - 1) & 1)))) {
+                    raise_device_error(&g_paged_device_error, kErrPgMma);
+                    return false;
+                }
             }
             tc_fence_after();
             const uint32_t d = tm + C::kColO;
@@ -775,21 +790,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // 16 keys: 8 columns of P, 16 rows (2048 bytes) of V.  The small products
                 // come first: the accumulator's rounding (towards zero, at every step) then
                 // meets the full sum a third as often.
-#pragma unroll
+#pragma unroll 2
                 for (int k = 0; k < kKT / 16; ++k) {
                     const uint32_t phi = p + 32 * (k >> 1) + 8 * (k & 1), plo = phi + 16;
-                    mma_f16_ts(d, plo, vhi + 128 * k, id_o, k > 0 ? 1u : 0u);
+                    mma_f16_ts(d, plo, vhi + 128 * k, id_o, k > 0 || len > 0 ? 1u : 0u);
                     mma_f16_ts(d, phi, vlo + 128 * k, id_o, 1u);
                 }
-#pragma unroll
+#pragma unroll 2
                 for (int k = 0; k < kKT / 16; ++k)
                     mma_f16_ts(d, p + 32 * (k >> 1) + 8 * (k & 1), vhi + 128 * k, id_o, 1u);
                 mma_commit(&freed[st]);
-                mma_commit(&o_full);
             }
             __syncwarp();
+            if (++len == kGroup || last) close(j);
             return true;
         };
+        bool prev_first = false, prev_last = false;
         while (ok && warp_next(g, prefix, s)) {
             const int u0 = s.u0, u1 = s.u1;
             for (int u = u0; u < u1; ++u, ++n) {
@@ -806,25 +822,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) {
                     // 16 dims: 8 columns of Q, 32 bytes of a K row.
                     auto off = [](int k) -> uint64_t { return (uint64_t)(k >> 2) * (2 * C::kBlock >> 4) + 2 * (k & 3); };
-#pragma unroll
+#pragma unroll 2
                     for (int k = 0; k < D / 16; ++k) {
                         mma_f16_ts(d, tm + C::kColQlo + 8 * k, khi + off(k), id_s, k > 0 ? 1u : 0u);
                         mma_f16_ts(d, tm + C::kColQhi + 8 * k, klo + off(k), id_s, 1u);
                     }
-#pragma unroll
+#pragma unroll 2
                     for (int k = 0; k < D / 16; ++k) mma_f16_ts(d, tm + C::kColQhi + 8 * k, khi + off(k), id_s, 1u);
                     mma_commit(&freed[st]);
                     mma_commit(&s_full[n & 1]);
                 }
                 __syncwarp();
-                if (n > 0 && !pv(n - 1)) {
+                if (n > 0 && !pv(n - 1, prev_first, prev_last)) {
                     ok = false;
                     break;
                 }
+                prev_first = u == u0;
+                prev_last = u == u1 - 1;
             }
             if (u1 > u0) ++piece;
         }
-        if (ok && n > 0) pv(n - 1);
+        if (ok && n > 0) pv(n - 1, prev_first, prev_last);
     } else if (warp >= 4 && warp < 8) {
         // ---- softmax: thread = virtual row -------------------------------------------
         const int i = threadIdx.x - 128;
@@ -851,14 +869,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int lo = a.window > 0 ? (int)max((int64_t)p - a.window + 1, (int64_t)0) : 0;
             const int sinks = (int)min(a.sinks, (int64_t)s.len);
             float m = -INFINITY, l = 0.f;
+            bool was_scaled = false;
             const int rows = min(s.T * a.G - s.rb * kM, kM), tiles = s.u1 - s.u0;
             // A warp without rows waits at the barrier that ends the piece; the first
             // warp, which always has one, arrives for it.
             const int arrivals = warp == 4 ? 4 - (rows + 31) / 32 + 1 : 1;
             for (int u = s.u0; u < s.u1 && __any_sync(FULL, alive); ++u, ++n) {
                 const int key = tile_key(s, a.tree, u), nb = n & 3, n8 = n & 7, bf = n & 1, it = 2 * n + 1;
-                if (!__all_sync(FULL, wait_for(&s_full[bf], (uint32_t)((n >> 1) & 1)) &&
-                                          wait_for(&ready[it % ST], (uint32_t)((it / ST) & 1)))) {
+                if (!team_wait(warp == 4, 2, (rows + 31) & ~31, &s_full[bf], (uint32_t)((n >> 1) & 1)) ||
+                    !__all_sync(FULL, wait_for(&ready[it % ST], (uint32_t)((it / ST) & 1)))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
                     break;
@@ -882,7 +901,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 rt.mul = q_scale[piece & 3][i] * kUnscale;
                 rt.cap = a.cap_log2;
                 float alpha, o_scale = kUnscale;  // of the tile's output
-                if (any_of(k_scaled[n8]) || any_of(v_scaled[n8])) {  // rare
+                bool moved;
+                const bool scaled = any_of(k_scaled[n8]) || any_of(v_scaled[n8]);
+                if (scaled) {  // rare
                     // The largest value scale among the keys seen sets the probabilities'.
                     o_scale = 7.888609052210118e-31f;
                     for (int k = 0; k < kKT; ++k)
@@ -891,13 +912,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     rt.ks = k_scale[n8];
                     rt.vs = v_scale[n8];
                     rt.v_mul = __uint_as_float(0x7f000000u - __float_as_uint(o_scale));
-                    alpha = row_softmax<CAP, false, true>(rt, m, l);
+                    alpha = row_softmax<CAP, false, true>(rt, m, l, moved);
                 } else if (__all_sync(FULL, see == ~0ull)) {
-                    alpha = row_softmax<CAP, true, false>(rt, m, l);
+                    alpha = row_softmax<CAP, true, false>(rt, m, l, moved);
                 } else {
-                    alpha = row_softmax<CAP, false, false>(rt, m, l);
+                    alpha = row_softmax<CAP, false, false>(rt, m, l, moved);
                 }
                 fold_f[nb][i] = make_float2(alpha, o_scale);
+                // A tile with another reference or scale than the one before begins a group.
+                if (__any_sync(FULL, moved && alive) || scaled || was_scaled) group_tag[nb] = n + 1;
+                was_scaled = scaled;
                 const uint64_t bad = bad_rows<D>(v_bad[n8]);
                 if (bad) row_bad[nb][i] = bad & see;
                 if (u == s.u1 - 1) {
@@ -922,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__any_sync(FULL, alive)) n += tiles;
             // One barrier a piece keeps the four warps' tile counts together; a failed
             // wait ends the role for all of them.
-            ok = rows_sync_and(ok);
+            ok = sync_and(1, 128, ok);
             ++piece;
         }
     } else if (warp >= 8 && warp < 16) {
@@ -935,7 +959,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = s.u0; u < u1; ++u, ++n) {
                 if (D == 64 && (n & 1) != (w >> 1)) continue;  // a tile's two warps of the four
                 const int it = 2 * n + side, st = it % ST;
-                if (!__all_sync(FULL, wait_for(&full[st], (uint32_t)((it / ST) & 1)))) {
+                // The warps that share the tile: four, or a pair.
+                if (!team_wait(D == 128 ? w == 0 : (w & 1) == 0, 3 + side + (D == 128 ? 0 : w & 2), 32 * C::kSplitWarps, &full[st],
+                               (uint32_t)((it / ST) & 1))) {
                     raise_device_error(&g_paged_device_error, kErrPgLoad);
                     ok = false;
                     break;
@@ -978,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float qh[16], ql[16];
 #pragma unroll
                 for (int c = 0; c < 16; c += 2) {
-                    const float4 y = load4(2 * (c0 + c));
+                    const float4 y = load4(tile_order((c0 + c) / 2));
                     uint32_t h0, l0, h1, l1;
                     split2(f2_pack(y.x * sc, y.y * sc), h0, l0);
                     split2(f2_pack(y.z * sc, y.w * sc), h1, l1);
@@ -996,26 +1022,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&q_full);
             ++piece;
         };
-        // acc = acc alpha + O of tile j; after a piece's last tile to where the row goes.
-        auto fold = [&](int j) -> bool {
-            const int nb = j & 3, n8 = j & 7;
-            if (!__all_sync(FULL, wait_for(&o_full, (uint32_t)(j & 1)))) {
+        // acc = acc alpha + O of group k; after a piece's last tile to where the row goes.
+        // Returns the tile after the group (0: a wait gave up).
+        auto fold = [&](int k) -> int {
+            if (!team_wait(w == 0, 7, 128, &o_full, (uint32_t)(k & 1))) {
                 raise_device_error(&g_paged_device_error, kErrPgMma);
-                return false;
+                return 0;
             }
             tc_fence_after();
-            const int4 ta = tile_at[nb];
-            const int rows = ta.x & (kFirst - 1);
-            const bool first = ta.x & kFirst, last = ta.x & kLast;
+            const int2 group = group_at[k & 1];
+            const int nb = group.x & 3;
+            const int rows = tile_at[nb].x & (kFirst - 1);
+            const bool first = tile_at[nb].x & kFirst, last = tile_at[group.y & 3].x & kLast;
             if (32 * w < rows) {
                 const float2 f = fold_f[nb][i];
                 const uint64_t fx = f2_pack(f.x, f.x), fy = f2_pack(f.y, f.y);
                 const uint32_t at = tmem + lanes + C::kColO;
-                float* to = last ? row_out[nb][i] : nullptr;
-                const float inv = last ? row_inv[nb][i] : 1.f;
+                float* to = last ? row_out[group.y & 3][i] : nullptr;
+                const float inv = last ? row_inv[group.y & 3][i] : 1.f;
                 const uint64_t inv2 = f2_pack(inv, inv);
-                if (bad_rows<D>(v_bad[n8]) && i < rows && row_bad[nb][i])  // rare
-                    odd = add_odd_values(a, ta, row_bad[nb][i], g.odd + ((int64_t)blockIdx.x * kM + i) * D, 0, D, odd);
+                for (int j = group.x; j <= group.y; ++j)
+                    if (bad_rows<D>(v_bad[j & 7]) && i < rows && row_bad[j & 3][i])  // rare
+                        odd = add_odd_values(a, tile_at[j & 3], row_bad[j & 3][i],
+                                             g.odd + ((int64_t)blockIdx.x * kM + i) * D, 0, D, odd);
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     float x[32], y[32];
@@ -1038,7 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float4 r;
                             f2_unpack(f2_mul(f2_pack(x[d], x[d + 1]), inv2), r.x, r.y);
                             f2_unpack(f2_mul(f2_pack(x[d + 2], x[d + 3]), inv2), r.z, r.w);
-                            *reinterpret_cast<float4*>(to + c0 + d) = r;
+                            *reinterpret_cast<float4*>(to + tile_order((c0 + d) / 4)) = r;
                         }
                     }
                 }
@@ -1046,9 +1075,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (last && odd) odd = join_odd_values(to, g.odd + ((int64_t)blockIdx.x * kM + i) * D, D);
                 tc_fence_before();
             }
-            __syncwarp();  // after everything that tile j left in shared memory has been read
+            __syncwarp();  // after everything that the group left in shared memory has been read
             if (lane == 0) mbar_arrive(&o_free);
-            return true;
+            return group.y + 1;
         };
         auto next_piece = [&]() -> bool {  // the next one that has tiles
             bool more;
@@ -1058,14 +1087,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         bool more = next_piece();
         if (more) load_queries();
-        while (ok && more) {
+        for (int k = 0; ok && more;) {
             const int end = n + s.u1 - s.u0;
-            for (; n < end; ++n) {
-                if (n == end - 1) {
-                    // The next piece's queries, once S(n) is done with this one's.
+            for (bool loaded = false; n < end; ++k) {
+                if (end - n <= kGroup && !loaded) {
+                    // The next piece's queries, once the last scores with this one's are done
+                    // (which no fold of the tiles that are left holds up).
+                    loaded = true;
                     more = next_piece();
                     if (more) {
-                        if (!__all_sync(FULL, wait_for(&freed[(2 * n) % ST], (uint32_t)(((2 * n) / ST) & 1)))) {
+                        const int it = 2 * (end - 1);
+                        if (!__all_sync(FULL, wait_for(&freed[it % ST], (uint32_t)((it / ST) & 1)))) {
                             raise_device_error(&g_paged_device_error, kErrPgMma);
                             ok = false;
                             break;
@@ -1074,7 +1106,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         load_queries();
                     }
                 }
-                if (!fold(n)) {
+                n = fold(k);
+                if (n == 0) {
                     ok = false;
                     break;
                 }
