@@ -68,7 +68,8 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int kKT = 64;        // keys per tile
 constexpr int kM = 128;        // virtual rows per row block
 constexpr int kThreads = 640;
-constexpr int kFoldWarps = 4;
+// Warps of each role (its TMEM lanes: 32 (warp % 4)).
+constexpr int kFoldWarp = 4, kSoftmaxWarp = 8, kSplitWarp = 12, kFoldWarps = 4;
 constexpr int kFirst = 1 << 16, kLast = 1 << 17;  // a piece's first and last tile
 constexpr int kPShift = 11;    // probabilities are scaled by 2^11 in f16
 constexpr float kLazyLog2 = 4.f;  // and a row's reference maximum moves when beaten by more than 2^4: 2^15 at most
@@ -515,8 +516,6 @@ struct RowTile {
     float mul;            // a score of the MMA times this is one in base-2 units (the argument of tanh with a cap)
     float cap;            // softcap in base-2 units
     const float* ks;      // SCALED: [64] key scales
-    const float* vs;      // SCALED: [64] value scales
-    float v_mul;          // SCALED: 1 / the largest value scale seen
 };
 
 // 32 scores from key 32 c on, masked, in base-2 units with a cap, else still to be
@@ -572,11 +571,6 @@ __device__ __forceinline__ float row_softmax(const RowTile& r, float& m, float& 
             uint64_t p0 = f2_pack(fast_exp2(e0), fast_exp2(e1)), p1 = f2_pack(fast_exp2(e2), fast_exp2(e3));
             sum0 = f2_add(sum0, p0);
             sum1 = f2_add(sum1, p1);
-            if constexpr (SCALED) {
-                const float* w = r.vs + 32 * c + k;
-                p0 = f2_mul(p0, f2_pack(w[0] * r.v_mul, w[1] * r.v_mul));
-                p1 = f2_mul(p1, f2_pack(w[2] * r.v_mul, w[3] * r.v_mul));
-            }
             uint32_t h0, l0, h1, l1;
             split2(p0, h0, l0);
             split2(p1, h1, l1);
@@ -593,6 +587,32 @@ __device__ __forceinline__ float row_softmax(const RowTile& r, float& m, float& 
     f2_unpack(sum1, b0, b1);
     l = fmaf(l, alpha, (a0 + a1) + (b0 + b1));
     return alpha;
+}
+
+// P once more, each key's times weight[key] * mul: for a tile whose values have scales of
+// their own (rare).
+__device__ __noinline__ void row_reweigh(uint32_t at, const float* weight, float mul) {
+    tmem_wait_st();
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+        float phi[16], plo[16];
+        tmem_ld16(at + 32 * c, phi);
+        tmem_ld16(at + 32 * c + 16, plo);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const uint32_t h = __float_as_uint(phi[k]), l = __float_as_uint(plo[k]);
+            const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&l));
+            const float* w = weight + 32 * c + 2 * k;
+            uint32_t h2, l2;
+            split2(f2_pack((fh.x + fl.x) * (w[0] * mul), (fh.y + fl.y) * (w[1] * mul)), h2, l2);
+            phi[k] = __uint_as_float(h2);
+            plo[k] = __uint_as_float(l2);
+        }
+        tmem_st16(at + 32 * c, phi);
+        tmem_st16(at + 32 * c + 16, plo);
+    }
 }
 
 // ---- the kernel -------------------------------------------------------------------------
@@ -843,9 +863,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (u1 > u0) ++piece;
         }
         if (ok && n > 0) pv(n - 1, prev_first, prev_last);
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= kSoftmaxWarp && warp < kSoftmaxWarp + 4) {
         // ---- softmax: thread = virtual row -------------------------------------------
-        const int i = threadIdx.x - 128;
+        const int i = threadIdx.x - 32 * kSoftmaxWarp;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         int n = 0, piece = 0;
         bool ok = true;
@@ -873,11 +893,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rows = min(s.T * a.G - s.rb * kM, kM), tiles = s.u1 - s.u0;
             // A warp without rows waits at the barrier that ends the piece; the first
             // warp, which always has one, arrives for it.
-            const int arrivals = warp == 4 ? 4 - (rows + 31) / 32 + 1 : 1;
+            const int arrivals = warp == kSoftmaxWarp ? 4 - (rows + 31) / 32 + 1 : 1;
             for (int u = s.u0; u < s.u1 && __any_sync(FULL, alive); ++u, ++n) {
                 const int key = tile_key(s, a.tree, u), nb = n & 3, n8 = n & 7, bf = n & 1, it = 2 * n + 1;
-                if (!team_wait(warp == 4, 2, (rows + 31) & ~31, &s_full[bf], (uint32_t)((n >> 1) & 1)) ||
-                    !__all_sync(FULL, wait_for(&ready[it % ST], (uint32_t)((it / ST) & 1)))) {
+                if (!team_wait(warp == kSoftmaxWarp, 2, (rows + 31) & ~31, &s_full[bf], (uint32_t)((n >> 1) & 1))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
                     break;
@@ -902,21 +921,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 rt.cap = a.cap_log2;
                 float alpha, o_scale = kUnscale;  // of the tile's output
                 bool moved;
-                const bool scaled = any_of(k_scaled[n8]) || any_of(v_scaled[n8]);
-                if (scaled) {  // rare
-                    // The largest value scale among the keys seen sets the probabilities'.
-                    o_scale = 7.888609052210118e-31f;
-                    for (int k = 0; k < kKT; ++k)
-                        if ((see >> k) & 1) o_scale = fmaxf(o_scale, v_scale[n8][k]);
+                if (any_of(k_scaled[n8])) {  // rare
                     rt.mul = q_scale[piece & 3][i];
                     rt.ks = k_scale[n8];
-                    rt.vs = v_scale[n8];
-                    rt.v_mul = __uint_as_float(0x7f000000u - __float_as_uint(o_scale));
                     alpha = row_softmax<CAP, false, true>(rt, m, l, moved);
                 } else if (__all_sync(FULL, see == ~0ull)) {
                     alpha = row_softmax<CAP, true, false>(rt, m, l, moved);
                 } else {
                     alpha = row_softmax<CAP, false, false>(rt, m, l, moved);
+                }
+                // Nothing above needs the values, which are often still to come.
+                if (!__all_sync(FULL, wait_for(&ready[it % ST], (uint32_t)((it / ST) & 1)))) {
+                    raise_device_error(&g_paged_device_error, kErrPgMma);
+                    ok = false;
+                    break;
+                }
+                const bool scaled = any_of(v_scaled[n8]);
+                if (scaled) {  // rare: the largest value scale among the keys seen sets the probabilities'
+                    o_scale = 7.888609052210118e-31f;
+                    for (int k = 0; k < kKT; ++k)
+                        if ((see >> k) & 1) o_scale = fmaxf(o_scale, v_scale[n8][k]);
+                    row_reweigh(rt.at, v_scale[n8], __uint_as_float(0x7f000000u - __float_as_uint(o_scale)));
                 }
                 fold_f[nb][i] = make_float2(alpha, o_scale);
                 // A tile with another reference or scale than the one before begins a group.
@@ -949,9 +974,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = sync_and(1, 128, ok);
             ++piece;
         }
-    } else if (warp >= 8 && warp < 16) {
-        // ---- split: warps 8 - 11 the keys, 12 - 15 the values ------------------------
-        const int w = warp & 3, side = (warp - 8) >> 2;
+    } else if (warp >= kSplitWarp) {
+        // ---- split: four warps the keys, four the values ------------------------
+        const int w = warp & 3, side = (warp - kSplitWarp) >> 2;
         int n = 0;
         bool ok = true;
         while (ok && warp_next(g, prefix, s)) {
@@ -973,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&ready[st]);
             }
         }
-    } else if (warp >= 16) {
+    } else if (warp >= kFoldWarp && warp < kFoldWarp + 4) {
         // ---- queries and fold: thread = virtual row -----------------------------------
         const int w = warp & 3, i = 32 * w + lane;
         const uint32_t lanes = (uint32_t)(32 * w) << 16;
