@@ -70,10 +70,11 @@ constexpr int kM = 128;        // virtual rows per row block
 constexpr int kThreads = 640;
 // Warps of each role (its TMEM lanes: 32 (warp % 4)).
 constexpr int kFoldWarp = 4, kSoftmaxWarp = 8, kSplitWarp = 12, kFoldWarps = 4;
-constexpr int kFirst = 1 << 16, kLast = 1 << 17;  // a piece's first and last tile
+constexpr int kFirst = 1 << 16, kLast = 1 << 17, kBad = 1 << 18;  // a piece's first and last tile; values that are not finite
 constexpr int kPShift = 11;    // probabilities are scaled by 2^11 in f16
 constexpr float kLazyLog2 = 4.f;  // and a row's reference maximum moves when beaten by more than 2^4: 2^15 at most
-constexpr int kGroup = 2;      // tiles that one accumulator takes before it is folded
+constexpr int kGroup = 4;      // tiles that one accumulator takes before it is folded
+constexpr int kRing = 8;       // a power of two, at least kGroup + 2 (and 5)
 
 enum : unsigned int {
     kErrPgLoad = 1u << 3,   // the splitters gave up on a loaded tile
@@ -89,6 +90,7 @@ struct PgArgs {
     float* part_l;
     float* part_o;       // [2 CTAs][128][D]
     float* odd;          // [CTAs][128][D]: values that are not finite
+    uint64_t* odd_rows;  // [CTAs][kRing][128]: such rows of a tile that a virtual row sees
     int4* head;          // [CTAs]: the unit that a CTA starts and others go on with
 };
 
@@ -102,7 +104,7 @@ struct Cfg {
     static constexpr uint32_t kTmemCols = 512;
     static constexpr size_t kSmem = 1024 + (size_t)kSlots * kTile + (kPagedMaxRequests + 1) * 8;
     static_assert(kColAcc + D <= kTmemCols, "TMEM budget");
-    static_assert(kSmem + 25 * 1024 <= 232448, "shared memory budget");
+    static_assert(kSmem + 24 * 1024 <= 232448, "shared memory budget");
     static_assert(kSlots % 2 == 0, "K in the even slots, V in the odd ones");
 };
 
@@ -444,20 +446,22 @@ __device__ __forceinline__ void split_tile(const PagedDesc& a, bool values, uint
     }
 }
 
-// mbar_wait, bounded in the same way, that looks at the clock after every 64 tries only:
-// half of the warps wait at any time here, and what they execute takes issue slots
-// from the rest (a look at the clock per try was half of all instructions).
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) {
+// mbar_wait, bounded in the same way, that looks at the clock after 4096 tries and then
+// after every 64: reading the global timer takes as long as a whole hand-over.
+__device__ __noinline__ bool wait_timed(uint64_t* bar, uint32_t parity) {
     const uint64_t t0 = global_ns();
     do {
-#pragma unroll 4
+#pragma unroll 1
         for (int i = 0; i < 64; ++i)
             if (mbar_try_wait(bar, parity)) return true;
     } while (global_ns() - t0 <= kWaitLimitNs);
     return false;
 }
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) || wait_long(bar, parity);
+#pragma unroll 1
+    for (int i = 0; i < 4096; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return wait_timed(bar, parity);
 }
 // A wait of several warps: the first one looks at the mbarrier while the others sleep at
 // barrier `id` (18 warps that all looked took two fifths of the issue slots), then
@@ -632,21 +636,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_base_s;
     __shared__ long long scan_s[kThreads / 32];
     __shared__ Seg seg_s[kThreads / 32];
-    // What tile n leaves for the roles that come later.  From the splitters, at n % 8:
-    // they are at most three tiles ahead of the MMAs, and P.V of tile n + 4 means that
-    // tile n + 2 has been folded.  From the softmax, at n % 4: S(n + 4) follows
-    // P.V of tile n + 2, which follows the fold of tile n.
-    __shared__ __align__(16) float k_scale[8][kKT], v_scale[8][kKT];
-    __shared__ __align__(16) uint32_t v_bad[8][4];
-    __shared__ __align__(16) uint32_t k_scaled[8][4], v_scaled[8][4];
+    // What tile n leaves for the roles that come later, at n % kRing.  The splitters are at
+    // most three tiles ahead of the MMAs; while a group of kGroup tiles waits for its
+    // fold, the softmax gets two tiles further: S(n) is issued before P.V of tile
+    // n - 1, which waits.
+    __shared__ __align__(16) float k_scale[kRing][kKT], v_scale[kRing][kKT];
+    __shared__ __align__(16) uint32_t v_bad[kRing][4], k_scaled[kRing][4], v_scaled[kRing][4];
     __shared__ float q_scale[4][kM];             // by piece % 4
-    __shared__ float2 fold_f[4][kM];             // alpha, output scale
-    __shared__ uint64_t row_bad[4][kM];          // values to add that are not finite
-    __shared__ int group_tag[4];                 // n + 1: tile n begins a group (written by the softmax)
+    __shared__ float2 fold_f[kRing][kM];         // alpha, output scale of a tile that begins a group
+    __shared__ float row_inv[kRing][kM];         // last tile of a piece: 1 / l, or 1
+    __shared__ int group_tag[kRing];             // n + 1: tile n begins a group (written by the softmax)
     __shared__ int2 group_at[2];                 // a group's first and last tile
-    __shared__ int4 tile_at[4];                  // rows of the block (kLast: last tile of its piece), request, first key, KV head
-    __shared__ float* row_out[4][kM];            // last tile of a piece: where the row goes
-    __shared__ float row_inv[4][kM];
+    __shared__ int4 tile_at[kRing];              // rows of the block (kFirst, kLast, kBad), request, first key, KV head
 
     const PagedDesc& a = g.a;
     const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform, to the compiler too
@@ -669,8 +670,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 1) tmem_alloc(&tmem_base_s, C::kTmemCols);
     if (threadIdx.x == 32) g.head[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (threadIdx.x < 4) group_tag[threadIdx.x] = 0;
-    if (threadIdx.x < 32)  // headDim 64: two words of a tile's four are never written
+    if (threadIdx.x < kRing) group_tag[threadIdx.x] = 0;
+    if (threadIdx.x < 4 * kRing)  // headDim 64: two words of a tile's four are never written
         (&v_bad[0][0])[threadIdx.x] = (&k_scaled[0][0])[threadIdx.x] = (&v_scaled[0][0])[threadIdx.x] = 0;
 
     // The requests' tiles and their running sum.
@@ -793,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 raise_device_error(&g_paged_device_error, kErrPgMma);
                 return false;
             }
-            if (len > 0 && (first || __shfl_sync(FULL, group_tag[j & 3], 0) == j + 1)) close(j - 1);
+            if (len > 0 && (first || __shfl_sync(FULL, group_tag[j % kRing], 0) == j + 1)) close(j - 1);
             if (len == 0) {
                 from = j;
                 if (groups > 0 && !__all_sync(FULL, wait_for(&o_free, (uint32_t)((groups - 1) & 1)))) {
@@ -895,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // warp, which always has one, arrives for it.
             const int arrivals = warp == kSoftmaxWarp ? 4 - (rows + 31) / 32 + 1 : 1;
             for (int u = s.u0; u < s.u1 && __any_sync(FULL, alive); ++u, ++n) {
-                const int key = tile_key(s, a.tree, u), nb = n & 3, n8 = n & 7, bf = n & 1, it = 2 * n + 1;
+                const int key = tile_key(s, a.tree, u), nb = n % kRing, bf = n & 1, it = 2 * n + 1;
                 if (!team_wait(warp == kSoftmaxWarp, 2, (rows + 31) & ~31, &s_full[bf], (uint32_t)((n >> 1) & 1))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
@@ -921,9 +922,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 rt.cap = a.cap_log2;
                 float alpha, o_scale = kUnscale;  // of the tile's output
                 bool moved;
-                if (any_of(k_scaled[n8])) {  // rare
+                if (any_of(k_scaled[nb])) {  // rare
                     rt.mul = q_scale[piece & 3][i];
-                    rt.ks = k_scale[n8];
+                    rt.ks = k_scale[nb];
                     alpha = row_softmax<CAP, false, true>(rt, m, l, moved);
                 } else if (__all_sync(FULL, see == ~0ull)) {
                     alpha = row_softmax<CAP, true, false>(rt, m, l, moved);
@@ -936,33 +937,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                const bool scaled = any_of(v_scaled[n8]);
+                const bool scaled = any_of(v_scaled[nb]);
                 if (scaled) {  // rare: the largest value scale among the keys seen sets the probabilities'
                     o_scale = 7.888609052210118e-31f;
                     for (int k = 0; k < kKT; ++k)
-                        if ((see >> k) & 1) o_scale = fmaxf(o_scale, v_scale[n8][k]);
-                    row_reweigh(rt.at, v_scale[n8], __uint_as_float(0x7f000000u - __float_as_uint(o_scale)));
+                        if ((see >> k) & 1) o_scale = fmaxf(o_scale, v_scale[nb][k]);
+                    row_reweigh(rt.at, v_scale[nb], __uint_as_float(0x7f000000u - __float_as_uint(o_scale)));
                 }
-                fold_f[nb][i] = make_float2(alpha, o_scale);
                 // A tile with another reference or scale than the one before begins a group.
                 if (__any_sync(FULL, moved && alive) || scaled || was_scaled) group_tag[nb] = n + 1;
+                fold_f[nb][i] = make_float2(alpha, o_scale * kScale);
                 was_scaled = scaled;
-                const uint64_t bad = bad_rows<D>(v_bad[n8]);
-                if (bad) row_bad[nb][i] = bad & see;
+                const uint64_t bad = bad_rows<D>(v_bad[nb]);
+                if (bad)  // rare: which of them the row sees, for the fold
+                    g.odd_rows[((int64_t)blockIdx.x * kRing + nb) * kM + i] = alive ? bad & see : 0;
                 if (u == s.u1 - 1) {
-                    float* to = g.part_o + prow * D;
                     float inv = 1.f;
                     if (s.slot < 0) {
-                        to = a.out + (((int64_t)s.row0 + t) * a.H + (int64_t)s.hk * a.G + (v - t * a.G)) * D;
                         inv = l != 0.f ? 1.f / l : 0.f;
                     } else {
                         g.part_m[prow] = m;
                         g.part_l[prow] = l;
                     }
-                    row_out[nb][i] = to;
                     row_inv[nb][i] = inv;
                 }
-                if (i == 0) tile_at[nb] = make_int4(rows + (u == s.u0 ? kFirst : 0) + (u == s.u1 - 1 ? kLast : 0), s.b, key, s.hk);
+                if (i == 0)
+                    tile_at[nb] = make_int4(rows + (u == s.u0 ? kFirst : 0) + (u == s.u1 - 1 ? kLast : 0) + (bad ? kBad : 0), s.b,
+                                            key, s.hk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -991,8 +992,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                split_tile<D>(a, side != 0, smem_u32(tiles) + st * C::kTile, side ? v_scale[n & 7] : k_scale[n & 7],
-                              v_bad[n & 7], side ? v_scaled[n & 7] : k_scaled[n & 7], s, tile_key(s, a.tree, u), w, lane);
+                split_tile<D>(a, side != 0, smem_u32(tiles) + st * C::kTile, side ? v_scale[n % kRing] : k_scale[n % kRing],
+                              v_bad[n % kRing], side ? v_scaled[n % kRing] : k_scaled[n % kRing], s,
+                              tile_key(s, a.tree, u), w, lane);
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ready[st]);
@@ -1004,6 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * w) << 16;
         int n = 0, piece = 0;
         bool ok = true, odd = false;
+        float *to = nullptr, *next_to = nullptr;  // where the row goes: this piece's, the next one's
         // Row i of the piece's block: q scaled by qk_mul, then as a row of a tile, with a
         // power of two of its own; two elements to a column of Q hi and Q lo.
         auto load_queries = [&]() {
@@ -1046,9 +1049,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full);
             ++piece;
+            next_to = s.slot < 0 ? a.out + (q - a.q)
+                                 : g.part_o + ((int64_t)(2 * blockIdx.x + (s.slot > 0 ? 1 : 0)) * kM + i) * D;
         };
-        // acc = acc alpha + O of group k; after a piece's last tile to where the row goes.
-        // Returns the tile after the group (0: a wait gave up).
+        // acc = acc alpha + O of group k (times kScale, as the tiles' values are); after a
+        // piece's last tile to where the row goes.  Returns the tile after the group (0:
+        // a wait gave up).
         auto fold = [&](int k) -> int {
             if (!team_wait(w == 0, 7, 128, &o_full, (uint32_t)(k & 1))) {
                 raise_device_error(&g_paged_device_error, kErrPgMma);
@@ -1056,50 +1062,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const int2 group = group_at[k & 1];
-            const int nb = group.x & 3;
+            const int nb = group.x % kRing, ne = group.y % kRing;
             const int rows = tile_at[nb].x & (kFirst - 1);
-            const bool first = tile_at[nb].x & kFirst, last = tile_at[group.y & 3].x & kLast;
+            const bool first = tile_at[nb].x & kFirst, last = tile_at[ne].x & kLast;
             if (32 * w < rows) {
                 const float2 f = fold_f[nb][i];
-                const uint64_t fx = f2_pack(f.x, f.x), fy = f2_pack(f.y, f.y);
+                const float fin = last ? row_inv[ne][i] * kUnscale : 1.f;
+                const bool plain = __all_sync(FULL, (first || f.x == 1.f) && f.y == 1.f && !last);
+                const uint64_t fx = f2_pack(f.x, f.x), fy = f2_pack(f.y, f.y), fin2 = f2_pack(fin, fin);
                 const uint32_t at = tmem + lanes + C::kColO;
-                float* to = last ? row_out[group.y & 3][i] : nullptr;
-                const float inv = last ? row_inv[group.y & 3][i] : 1.f;
-                const uint64_t inv2 = f2_pack(inv, inv);
-                for (int j = group.x; j <= group.y; ++j)
-                    if (bad_rows<D>(v_bad[j & 7]) && i < rows && row_bad[j & 3][i])  // rare
-                        odd = add_odd_values(a, tile_at[j & 3], row_bad[j & 3][i],
-                                             g.odd + ((int64_t)blockIdx.x * kM + i) * D, 0, D, odd);
+                int bad = 0;
+                for (int j = group.x; j <= group.y; ++j) bad |= tile_at[j % kRing].x;
+                if (bad & kBad)  // rare
+                    for (int j = group.x; j <= group.y; ++j) {
+                        const uint64_t mask = g.odd_rows[((int64_t)blockIdx.x * kRing + j % kRing) * kM + i];
+                        if ((tile_at[j % kRing].x & kBad) && i < rows && mask)
+                            odd = add_odd_values(a, tile_at[j % kRing], mask, g.odd + ((int64_t)blockIdx.x * kM + i) * D, 0, D,
+                                                 odd);
+                    }
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     float x[32], y[32];
                     tmem_ld32(at + c0, x);
                     if (!first) tmem_ld32(at + (C::kColAcc - C::kColO) + c0, y);
                     tmem_wait_ld();
-                    if (first) {
+                    if (plain) {
+                        if (!first) {
 #pragma unroll
-                        for (int d = 0; d < 32; d += 2) f2_unpack(f2_mul(f2_pack(x[d], x[d + 1]), fy), x[d], x[d + 1]);
+                            for (int d = 0; d < 32; d += 2)
+                                f2_unpack(f2_add(f2_pack(x[d], x[d + 1]), f2_pack(y[d], y[d + 1])), x[d], x[d + 1]);
+                        }
                     } else {
 #pragma unroll
-                        for (int d = 0; d < 32; d += 2)
-                            f2_unpack(f2_fma(f2_pack(x[d], x[d + 1]), fy, f2_mul(f2_pack(y[d], y[d + 1]), fx)), x[d], x[d + 1]);
+                        for (int d = 0; d < 32; d += 2) {
+                            uint64_t v = f2_mul(f2_pack(x[d], x[d + 1]), fy);
+                            if (!first) v = f2_fma(f2_pack(y[d], y[d + 1]), fx, v);
+                            f2_unpack(f2_mul(v, fin2), x[d], x[d + 1]);
+                        }
                     }
                     if (!last) {
                         tmem_st32(at + (C::kColAcc - C::kColO) + c0, x);
                     } else if (i < rows) {
 #pragma unroll
-                        for (int d = 0; d < 32; d += 4) {
-                            float4 r;
-                            f2_unpack(f2_mul(f2_pack(x[d], x[d + 1]), inv2), r.x, r.y);
-                            f2_unpack(f2_mul(f2_pack(x[d + 2], x[d + 3]), inv2), r.z, r.w);
-                            *reinterpret_cast<float4*>(to + tile_order((c0 + d) / 4)) = r;
-                        }
+                        for (int d = 0; d < 32; d += 4)
+                            *reinterpret_cast<float4*>(to + tile_order((c0 + d) / 4)) = make_float4(x[d], x[d + 1], x[d + 2], x[d + 3]);
                     }
                 }
                 tmem_wait_st();
                 if (last && odd) odd = join_odd_values(to, g.odd + ((int64_t)blockIdx.x * kM + i) * D, D);
                 tc_fence_before();
             }
+            if (last) to = next_to;
             __syncwarp();  // after everything that the group left in shared memory has been read
             if (lane == 0) mbar_arrive(&o_free);
             return group.y + 1;
@@ -1112,30 +1125,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         bool more = next_piece();
         if (more) load_queries();
+        to = next_to;
         for (int k = 0; ok && more;) {
-            const int end = n + s.u1 - s.u0;
-            for (bool loaded = false; n < end; ++k) {
+            const int end = n + s.u1 - s.u0, it = 2 * (end - 1);
+            uint64_t* scores_done = &freed[it % ST];  // of the piece's last tile
+            const uint32_t phase = (uint32_t)((it / ST) & 1);
+            bool loaded = false;
+            while (n < end) {
+                // The next piece's queries go in once the last scores with this one's are done:
+                // before the fold that ends the piece, since its P.V comes after the
+                // next piece's first scores; but those last scores may wait for a fold
+                // that comes first.
                 if (end - n <= kGroup && !loaded) {
-                    // The next piece's queries, once the last scores with this one's are done
-                    // (which no fold of the tiles that are left holds up).
-                    loaded = true;
-                    more = next_piece();
-                    if (more) {
-                        const int it = 2 * (end - 1);
-                        if (!__all_sync(FULL, wait_for(&freed[it % ST], (uint32_t)((it / ST) & 1)))) {
-                            raise_device_error(&g_paged_device_error, kErrPgMma);
-                            ok = false;
-                            break;
-                        }
+                    bool done = false;
+                    for (int i = 0; i < (1 << 20) && !(done = __all_sync(FULL, mbar_try_wait(scores_done, phase))) &&
+                                    !__all_sync(FULL, mbar_try_wait(&o_full, (uint32_t)(k & 1)));
+                         ++i) {
+                    }
+                    if (done) {
+                        loaded = true;
+                        more = next_piece();
                         tc_fence_after();
-                        load_queries();
+                        if (more) load_queries();
                     }
                 }
-                n = fold(k);
+                n = fold(k++);
                 if (n == 0) {
                     ok = false;
                     break;
                 }
+            }
+            if (ok && !loaded) {  // the last fold came first: nothing follows, or the scores are done by now
+                if (!__all_sync(FULL, wait_for(scores_done, phase))) {
+                    raise_device_error(&g_paged_device_error, kErrPgMma);
+                    break;
+                }
+                more = next_piece();
+                tc_fence_after();
+                if (more) load_queries();
+                to = next_to;
             }
         }
     }
@@ -1233,7 +1261,7 @@ bool encode_rows(CUtensorMap* map, const float* p, int64_t rows, int64_t cols, i
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 struct PgScratch {
-    size_t m, l, o, odd, head, total;
+    size_t m, l, o, odd, odd_rows, head, total;
 };
 PgScratch scratch_of(int ctas, int D) {
     PgScratch s;
@@ -1242,7 +1270,8 @@ PgScratch scratch_of(int ctas, int D) {
     s.l = s.m + up256(rows * 4);
     s.o = s.l + up256(rows * 4);
     s.odd = s.o + up256(rows * D * 4);
-    s.head = s.odd + up256(rows / 2 * D * 4);
+    s.odd_rows = s.odd + up256(rows / 2 * D * 4);
+    s.head = s.odd_rows + up256(rows / 2 * kRing * 8);
     s.total = s.head + up256((size_t)ctas * sizeof(int4));
     return s;
 }
@@ -1269,6 +1298,7 @@ cudaError_t launch_d(const PagedDesc& a, int num_sms, void* workspace, cudaStrea
     g.part_l = reinterpret_cast<float*>(ws + sc.l);
     g.part_o = reinterpret_cast<float*>(ws + sc.o);
     g.odd = reinterpret_cast<float*>(ws + sc.odd);
+    g.odd_rows = reinterpret_cast<uint64_t*>(ws + sc.odd_rows);
     g.head = reinterpret_cast<int4*>(ws + sc.head);
     const int64_t cols = (int64_t)a.Hk * D, pool = a.pages * a.page_size;
     CUtensorMap tk, tv, tkn, tvn;
