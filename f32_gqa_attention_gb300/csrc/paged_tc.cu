@@ -28,8 +28,8 @@
 //
 // Tiles of 64 keys, M = 128 virtual rows (padded: a wave of MMAs takes less
 // time than the tile's bytes take from HBM, so padding costs nothing).  Warps:
-//   0       page ids (32 at a time, one per lane) and TMA loads of raw f32 K and
-//           V tiles, one box per page; drafted rows come as one tile of their
+//   0, 2    page ids (32 at a time, one per lane) and TMA loads of f32 K and V tiles, one
+//           box per page; drafted rows come as one tile of their
 //           own from k_new / v_new; rows of no page are read out of bounds, as
 //           zeros;
 //   1       lane 0 issues the MMAs: S(n) = Q.K^T, then O(n - 1) = P.V;
@@ -98,7 +98,10 @@ template <int D>
 struct Cfg {
     static constexpr int kSlots = D == 128 ? 6 : 12;              // tiles: K(n), V(n), K(n + 1), ..
     static constexpr uint32_t kTile = kKT * D * 4;
-    static constexpr uint32_t kBlock = kKT * 128;                 // [64 rows x 128 bytes]: 32 f32, or 64 f16 hi or lo
+    // A tile is a run of groups of 8 rows, a group a run of blocks [8 rows x 128 bytes]
+    // (32 f32, or 64 f16 hi or lo; a swizzle atom), one for each 32 elements of the head.
+    static constexpr int kBlocks = D / 32;
+    static constexpr uint32_t kGroupRows = kBlocks * 1024;
     static constexpr int kSplitWarps = D == 128 ? 4 : 2;          // warps that split a tile
     static constexpr uint32_t kColQhi = 0, kColQlo = D / 2, kColS = D, kColO = D + 2 * kKT, kColAcc = kColO + D;
     static constexpr uint32_t kTmemCols = 512;
@@ -238,19 +241,35 @@ __device__ __forceinline__ int tile_rows(const Seg& s, int key) {
     return key < 0 ? min(s.T, kKT) : max(min(s.len - key, kKT), 0);
 }
 
+// Tiled TMA loads of 3 and 4 dimensions, as tma_load_2d.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];\n" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // ---- f16 operands ---------------------------------------------------------------------
 // Descriptor of an f16 kind MMA: f32 accumulator, A K-major, B K-major or (mn) MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool mn) {
     return (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// Shared-memory descriptor of MN-major blocks of 64 elements (128 bytes, the
-// 128-byte swizzle): rows are K; 8-row atoms 1024 bytes apart, blocks of 64
-// elements `block` bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_mn(const void* tile, uint32_t block) {
+// Shared-memory descriptors of a tile's hi (or lo) blocks with the 128-byte swizzle, groups
+// of 8 rows `group` bytes apart.  K-major: 64 elements of a row along K.  MN-major: the
+// rows are K, and the next 64 elements of a row lie two blocks on.
+__device__ __forceinline__ uint64_t smem_desc_rows(const void* tile, uint32_t group, uint32_t next) {
     const uint64_t addr = smem_u32(tile);
     uint64_t d = (addr >> 4) & 0x3FFFull;
-    d |= (uint64_t)(block >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)(next >> 4) << 16;
+    d |= (uint64_t)(group >> 4) << 32;
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
     return d;
@@ -349,7 +368,7 @@ __device__ __forceinline__ float row_split(uint32_t at, uint32_t sw) {
 #pragma unroll 2
     for (uint32_t c = 0; c < 128; c += 16) {
         const uint32_t to = at + (c ^ sw);
-        const float4 x = lds4(to), y = lds4(to + kKT * 128);
+        const float4 x = lds4(to), y = lds4(to + 1024);
         t = abs_top(abs_top(t, x), y);
         uint32_t h[4], l[4];
         split2(f2_mul(f2_pack(x.x, x.y), s2), h[0], l[0]);
@@ -357,7 +376,7 @@ __device__ __forceinline__ float row_split(uint32_t at, uint32_t sw) {
         split2(f2_mul(f2_pack(y.x, y.y), s2), h[2], l[2]);
         split2(f2_mul(f2_pack(y.z, y.w), s2), h[3], l[3]);
         sts4(to, h[0], h[1], h[2], h[3]);
-        sts4(to + kKT * 128, l[0], l[1], l[2], l[3]);
+        sts4(to + 1024, l[0], l[1], l[2], l[3]);
     }
     return t;
 }
@@ -400,15 +419,15 @@ __device__ __noinline__ float row_rescue(const float* row, int D, int half, bool
 #pragma unroll
         for (int i = 0; i < 4; ++i) split2(f2_pack(x[2 * i] * s, x[2 * i + 1] * s), h[i], l[i]);
         sts4(at + ((c << 4) ^ sw), h[0], h[1], h[2], h[3]);
-        sts4(at + kKT * 128 + ((c << 4) ^ sw), l[0], l[1], l[2], l[3]);
+        sts4(at + 1024 + ((c << 4) ^ sw), l[0], l[1], l[2], l[3]);
     }
     return __uint_as_float(e);
 }
 
 // One tile of f32 rows to f16 hi and lo, in place; the rows' inverse scales to
-// `scale`.  TMA leaves 32 elements (128 bytes) of row r in row r of each block,
-// 128-byte swizzled; a thread takes 64 elements of one row (two blocks, which become
-// their hi and lo), neighbouring lanes neighbouring rows, so that the swizzle makes
+// `scale`.  TMA leaves 32 elements (128 bytes) of a row in a row of each block of its
+// group, 128-byte swizzled; a thread takes 64 elements of one row (two blocks, which
+// become their hi and lo), neighbouring lanes neighbouring rows, so that the swizzle makes
 // its 16-byte accesses free of bank conflicts.  headDim 128: lanes 0 - 15 the first
 // halves of 16 rows, lanes 16 - 31 the second ones.  Rows past `rows` are
 // zeros.  In value tiles elements that are not finite become zeros and `bad` gets the
@@ -419,12 +438,12 @@ template <int D>
 __device__ __forceinline__ void split_tile(const PagedDesc& a, bool values, uint32_t tile, float* scale, uint32_t* bad,
                                            uint32_t* scaled, const Seg& s, int key, int w, int lane) {
     const int half = D == 128 ? lane >> 4 : 0, row = D == 128 ? 16 * w + (lane & 15) : 32 * (w & 1) + lane;
-    uint32_t at = tile + 2 * half * (kKT * 128) + row * 128;
+    uint32_t at = tile + (row >> 3) * Cfg<D>::kGroupRows + half * 2048 + (row & 7) * 128;
     asm volatile("" : "+r"(at));  // addresses are worked out here, not kept over the tile loop
     const uint32_t sw = (row & 7) << 4;
     const int rows = tile_rows(s, key);
     if (rows < kKT && row >= rows) {  // the last tile of a cache, or drafted rows
-        for (int c = 0; c < 16; ++c) sts4(at + (c >> 3) * (kKT * 128) + (c & 7) * 16, 0, 0, 0, 0);
+        for (int c = 0; c < 16; ++c) sts4(at + (c >> 3) * 1024 + (c & 7) * 16, 0, 0, 0, 0);
     }
     float t = row_split(at, sw), unscale = kUnscale;
     if constexpr (D == 128) t = nan_max(t, __shfl_xor_sync(FULL, t, 16));
@@ -710,20 +729,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     Seg& s = seg_s[warp];
     if (lane == 0) walk_start(g, prefix, s);
 
-    if (warp == 0) {
-        // ---- producer: raw K and V tiles --------------------------------------------
-        if (lane == 0) {
-            prefetch_tensormap(&tm_k);
-            prefetch_tensormap(&tm_v);
-        }
-        const int nsub = kKT / g.sub, blk = lane / nsub, k_sub = lane % nsub;
+    if (warp == 0 || warp == 2) {
+        // ---- producers: warp 0 the K tiles, warp 2 the V tiles -------------------------
+        const int kv = warp >> 1;
+        const CUtensorMap *tm = kv ? &tm_v : &tm_k, *tmn = kv ? &tm_vn : &tm_kn;
+        if (lane == 0) prefetch_tensormap(tm);
+        const int nsub = kKT / g.sub;
         const int nowhere = (int)(a.pages * a.page_size);  // a row out of bounds: zeros
-        int it = 0;
+        int n = 0;
         bool ok = true;
         while (ok && warp_next(g, prefix, s)) {
             int batch = -1, y_cur = nowhere;
-            const int subs = (s.len + g.sub - 1) / g.sub;
-            for (int u = s.u0; ok && u < s.u1; ++u) {
+            const int subs = (s.len + g.sub - 1) / g.sub, u1 = s.u1;
+            for (int u = s.u0; u < u1; ++u, ++n) {
                 const int key = tile_key(s, a.tree, u);
                 int y = nowhere;
                 if (key >= 0) {
@@ -738,40 +756,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (page >= 0 && page < a.pages) y_cur = page * a.page_size + row % a.page_size;
                         }
                     }
-                    y = __shfl_sync(FULL, y_cur, (q0 & 31) + k_sub);
+                    y = __shfl_sync(FULL, y_cur, (q0 & 31) + (lane < nsub ? lane : 0));
                 }
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++it) {
-                    const int st = it % ST;
-                    if (it >= ST && !__all_sync(FULL, wait_for(&freed[st], (uint32_t)((it / ST - 1) & 1)))) {
-                        raise_device_error(&g_paged_device_error, kErrPgFree);
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kTile);
-                    __syncwarp();
-                    // A lane for each box of 32 elements x the rows of a page (or of the tile).
-                    unsigned char* dst = tiles + (size_t)st * C::kTile;
-                    if (key < 0) {
-                        if (lane < D / 32)
-                            tma_load_2d(dst + lane * C::kBlock, kv ? &tm_vn : &tm_kn, s.hk * D + 32 * lane, s.row0, &full[st]);
-                    } else if (blk < D / 32) {
-                        tma_load_2d(dst + blk * C::kBlock + k_sub * g.sub * 128, kv ? &tm_v : &tm_k, s.hk * D + 32 * blk, y,
-                                    &full[st]);
-                    }
+                const int it = 2 * n + kv, st = it % ST;
+                if (it >= ST && !__all_sync(FULL, wait_for(&freed[st], (uint32_t)((it / ST - 1) & 1)))) {
+                    raise_device_error(&g_paged_device_error, kErrPgFree);
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kTile);
+                __syncwarp();
+                // A lane for each box: the groups of a page (or of the tile), all their blocks;
+                // drafted rows, which start anywhere, one group at a time.
+                unsigned char* dst = tiles + (size_t)st * C::kTile;
+                if (key < 0) {
+                    if (lane < kKT / 8)
+                        tma_load_3d(dst + lane * C::kGroupRows, tmn, 0, s.row0 + 8 * lane, s.hk * C::kBlocks, &full[st]);
+                } else if (lane < nsub) {
+                    tma_load_4d(dst + lane * (g.sub / 8) * C::kGroupRows, tm, 0, 0, s.hk * C::kBlocks, y >> 3, &full[st]);
                 }
             }
         }
         // No copy may be in flight when the CTA exits.
-        for (int j = it < ST ? 0 : it - ST; j < it; ++j)
-            if (!wait_for(&full[j % ST], (uint32_t)((j / ST) & 1)))
+        const int slots = ST / 2;
+        for (int j = n < slots ? 0 : n - slots; j < n; ++j)
+            if (!wait_for(&full[(2 * j + kv) % ST], (uint32_t)(((2 * j + kv) / ST) & 1)))
                 raise_device_error(&g_paged_device_error, kErrPgFree);
     } else if (warp == 1) {
         // ---- MMAs: the warp stays together and one elected lane issues (behind a
         // lane == 0 test an MMA took 45 cycles to issue, behind elect 10) ----
         constexpr uint32_t id_s = idesc_f16(kM, kKT, false), id_o = idesc_f16(kM, D, true);
         const uint32_t tm = __shfl_sync(FULL, tmem, 0);
-        const uint64_t k0 = smem_desc_sw128(tiles), v0 = smem_desc_mn(tiles, 2 * C::kBlock);
+        const uint64_t k0 = smem_desc_rows(tiles, C::kGroupRows, 16), v0 = smem_desc_rows(tiles, C::kGroupRows, 2048);
         int n = 0, piece = 0;
         // Groups of tiles share an accumulator: `len` tiles in the open one, the first
         // of them `from`; `groups` are closed.
@@ -806,20 +822,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t d = tm + C::kColO;
             const uint32_t p = tm + C::kColS + bf * kKT;  // 32 keys: hi in 16 columns, lo in 16
             const uint64_t vhi = v0 + st * (C::kTile >> 4);
-            const uint64_t vlo = vhi + (C::kBlock >> 4);
+            const uint64_t vlo = vhi + (1024 >> 4);
             if (elect_one()) {
-                // 16 keys: 8 columns of P, 16 rows (2048 bytes) of V.  The small products
+                // 16 keys: 8 columns of P, two groups of V's rows.  The small products
                 // come first: the accumulator's rounding (towards zero, at every step) then
                 // meets the full sum a third as often.
 #pragma unroll 2
                 for (int k = 0; k < kKT / 16; ++k) {
                     const uint32_t phi = p + 32 * (k >> 1) + 8 * (k & 1), plo = phi + 16;
-                    mma_f16_ts(d, plo, vhi + 128 * k, id_o, k > 0 || len > 0 ? 1u : 0u);
-                    mma_f16_ts(d, phi, vlo + 128 * k, id_o, 1u);
+                    mma_f16_ts(d, plo, vhi + (2 * C::kGroupRows >> 4) * k, id_o, k > 0 || len > 0 ? 1u : 0u);
+                    mma_f16_ts(d, phi, vlo + (2 * C::kGroupRows >> 4) * k, id_o, 1u);
                 }
 #pragma unroll 2
                 for (int k = 0; k < kKT / 16; ++k)
-                    mma_f16_ts(d, p + 32 * (k >> 1) + 8 * (k & 1), vhi + 128 * k, id_o, 1u);
+                    mma_f16_ts(d, p + 32 * (k >> 1) + 8 * (k & 1), vhi + (2 * C::kGroupRows >> 4) * k, id_o, 1u);
                 mma_commit(&freed[st]);
             }
             __syncwarp();
@@ -839,10 +855,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tm + C::kColS + (n & 1) * kKT;
-                const uint64_t khi = k0 + st * (C::kTile >> 4), klo = khi + (C::kBlock >> 4);
+                const uint64_t khi = k0 + st * (C::kTile >> 4), klo = khi + (1024 >> 4);
                 if (elect_one()) {
                     // 16 dims: 8 columns of Q, 32 bytes of a K row.
-                    auto off = [](int k) -> uint64_t { return (uint64_t)(k >> 2) * (2 * C::kBlock >> 4) + 2 * (k & 3); };
+                    auto off = [](int k) -> uint64_t { return (uint64_t)(k >> 2) * (2048 >> 4) + 2 * (k & 3); };
 #pragma unroll 2
                     for (int k = 0; k < D / 16; ++k) {
                         mma_f16_ts(d, tm + C::kColQlo + 8 * k, khi + off(k), id_s, k > 0 ? 1u : 0u);
@@ -1243,16 +1259,26 @@ PFN_cuTensorMapEncodeTiled_v12000 pg_encoder() {
     return fn;
 }
 
-// Row-major [rows, cols] f32, boxes of box_rows rows x 32 columns, 128-byte swizzle.
-bool encode_rows(CUtensorMap* map, const float* p, int64_t rows, int64_t cols, int box_rows) {
-    return cached_tensor_map(map, p, rows, cols, 32, box_rows, 3, [&](CUtensorMap* m) {
+// Boxes of a tile's layout out of row-major [rows, cols] f32, 128-byte swizzle.  A pool
+// (rows in whole groups): elements, rows of a group, blocks, groups; a box has the
+// `groups` of a page.  Drafted rows (groups = 0), which start anywhere: elements, rows,
+// blocks; a box is one group.
+bool encode_boxes(CUtensorMap* map, const float* p, int64_t rows, int64_t cols, int blocks, int groups) {
+    return cached_tensor_map(map, p, rows, cols, 32 * blocks, groups, 4, [&](CUtensorMap* m) {
         auto fn = pg_encoder();
         if (!fn) return false;
-        const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-        const cuuint64_t strides[1] = {(cuuint64_t)cols * sizeof(float)};
-        const cuuint32_t box[2] = {32u, (cuuint32_t)box_rows};
-        const cuuint32_t estr[2] = {1, 1};
-        return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(p), dims, strides, box, estr,
+        const cuuint64_t row = (cuuint64_t)cols * sizeof(float), nblk = (cuuint64_t)cols / 32;
+        const cuuint32_t ones[4] = {1, 1, 1, 1};
+        if (groups == 0) {
+            const cuuint64_t dims[3] = {32, (cuuint64_t)rows, nblk}, strides[2] = {row, 128};
+            const cuuint32_t box[3] = {32, 8, (cuuint32_t)blocks};
+            return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(p), dims, strides, box, ones,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+        }
+        const cuuint64_t dims[4] = {32, 8, nblk, (cuuint64_t)rows / 8}, strides[3] = {row, 128, 8 * row};
+        const cuuint32_t box[4] = {32, 8, (cuuint32_t)blocks, (cuuint32_t)groups};
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<float*>(p), dims, strides, box, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     });
@@ -1302,11 +1328,12 @@ cudaError_t launch_d(const PagedDesc& a, int num_sms, void* workspace, cudaStrea
     g.head = reinterpret_cast<int4*>(ws + sc.head);
     const int64_t cols = (int64_t)a.Hk * D, pool = a.pages * a.page_size;
     CUtensorMap tk, tv, tkn, tvn;
-    if (!encode_rows(&tk, a.k_pool, pool, cols, g.sub) || !encode_rows(&tv, a.v_pool, pool, cols, g.sub))
+    constexpr int nb = Cfg<D>::kBlocks;
+    if (!encode_boxes(&tk, a.k_pool, pool, cols, nb, g.sub / 8) || !encode_boxes(&tv, a.v_pool, pool, cols, nb, g.sub / 8))
         return cudaErrorInvalidValue;
     tkn = tk;
     tvn = tv;
-    if (a.tree && (!encode_rows(&tkn, a.k_new, a.rows, cols, kKT) || !encode_rows(&tvn, a.v_new, a.rows, cols, kKT)))
+    if (a.tree && (!encode_boxes(&tkn, a.k_new, a.rows, cols, nb, 0) || !encode_boxes(&tvn, a.v_new, a.rows, cols, nb, 0)))
         return cudaErrorInvalidValue;
     auto kern = a.softcap_on ? paged_tc_kernel<D, true> : paged_tc_kernel<D, false>;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), (int)Cfg<D>::kSmem);
