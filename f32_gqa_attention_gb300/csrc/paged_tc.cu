@@ -530,6 +530,18 @@ __device__ __noinline__ bool join_odd_values(float* to, const float* odd, int n)
     return false;
 }
 
+// Keys of a tile that a row sees: in the cache [lo, hi] and those before `sinks`, among the
+// drafted rows its mask's, with a window those near its position p.
+__device__ __noinline__ uint64_t tile_mask(const PagedDesc& a, const Seg& s, int key, int hi, int lo, int sinks, int p, int t) {
+    auto below = [](int c) -> uint64_t { return c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1; };
+    if (key >= 0) return below(hi - key + 1) & (~below(lo - key) | below(sinks - key));
+    uint64_t see = __ldg(reinterpret_cast<const unsigned long long*>(a.masks) + s.row0 + t) & below(s.T);
+    if (a.window > 0)
+        for (int j = 0; j < s.T; ++j)
+            if (__ldg(a.positions + s.row0 + j) <= p - a.window) see &= ~(1ull << j);
+    return see;
+}
+
 // ---- softmax of one row of a tile -----------------------------------------------------
 // What a thread needs of the tile: its scores (TMEM columns `at`), the keys' and
 // values' scales, the mask.
@@ -913,23 +925,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int arrivals = warp == kSoftmaxWarp ? 4 - (rows + 31) / 32 + 1 : 1;
             for (int u = s.u0; u < s.u1 && __any_sync(FULL, alive); ++u, ++n) {
                 const int key = tile_key(s, a.tree, u), nb = n % kRing, bf = n & 1, it = 2 * n + 1;
-                if (!team_wait(warp == kSoftmaxWarp, 2, (rows + 31) & ~31, &s_full[bf], (uint32_t)((n >> 1) & 1))) {
+                if (!__all_sync(FULL, wait_for(&s_full[bf], (uint32_t)((n >> 1) & 1)))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
                     break;
                 }
-                uint64_t see = ~0ull;  // rows of no request: anything
-                if (alive) {
-                    auto below = [](int c) -> uint64_t { return c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1; };
-                    if (key >= 0) {
-                        see = below(hi - key + 1) & (~below(lo - key) | below(sinks - key));
-                    } else {
-                        see = __ldg(reinterpret_cast<const unsigned long long*>(a.masks) + s.row0 + t) & below(s.T);
-                        if (a.window > 0)
-                            for (int j = 0; j < s.T; ++j)
-                                if (__ldg(a.positions + s.row0 + j) <= p - a.window) see &= ~(1ull << j);
-                    }
-                }
+                // Keys of the tile that the row sees (a row of no request: anything).
+                const bool all = !alive || (key >= 0 && hi - key >= kKT - 1 && lo <= key);
+                const bool whole = __all_sync(FULL, all);
+                uint64_t see = ~0ull;
+                if (!all) see = tile_mask(a, s, key, hi, lo, sinks, p, t);
                 tc_fence_after();
                 RowTile rt;
                 rt.at = tmem + lanes + C::kColS + bf * kKT;
@@ -942,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     rt.mul = q_scale[piece & 3][i];
                     rt.ks = k_scale[nb];
                     alpha = row_softmax<CAP, false, true>(rt, m, l, moved);
-                } else if (__all_sync(FULL, see == ~0ull)) {
+                } else if (whole) {
                     alpha = row_softmax<CAP, true, false>(rt, m, l, moved);
                 } else {
                     alpha = row_softmax<CAP, false, false>(rt, m, l, moved);
@@ -1072,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // piece's last tile to where the row goes.  Returns the tile after the group (0:
         // a wait gave up).
         auto fold = [&](int k) -> int {
-            if (!team_wait(w == 0, 7, 128, &o_full, (uint32_t)(k & 1))) {
+            if (!__all_sync(FULL, wait_for(&o_full, (uint32_t)(k & 1)))) {
                 raise_device_error(&g_paged_device_error, kErrPgMma);
                 return 0;
             }
