@@ -230,11 +230,10 @@ __device__ __forceinline__ bool warp_next(const PgArgs& g, const long long* pref
     return __shfl_sync(FULL, more, 0) != 0;  // orders lane 0's writes before the other lanes' reads
 }
 
-// First key of tile u, or -1 for the drafted rows' tile.
-__device__ __forceinline__ int tile_key(const Seg& s, int tree, int u) {
-    if (u < s.n_sink) return u * kKT;
-    if (u < s.n_ctx) return (s.lo_tile + u - s.n_sink) * kKT;
-    return tree ? -1 : 0;  // 0: a unit without keys
+// First key of tile u, or -1 for the drafted rows' tile (n_sink, n_ctx, lo_tile: Seg's).
+__device__ __forceinline__ int tile_key(int n_sink, int n_ctx, int lo_tile, int tree, int u) {
+    const int key = (u < n_sink ? u : lo_tile + u - n_sink) * kKT;
+    return u < n_ctx ? key : tree ? -1 : 0;  // 0: a unit without keys
 }
 // Rows of the tile that hold keys.
 __device__ __forceinline__ int tile_rows(const Seg& s, int key) {
@@ -433,10 +432,10 @@ __device__ __noinline__ float row_rescue(const float* row, int D, int half, bool
 // zeros.  In value tiles elements that are not finite become zeros and `bad` gets the
 // rows that had one (they are added in the fold, to the rows that see them
 // only); in key tiles they make their own scores not finite, which the mask
-// discards.  `scaled` tells whether a row has a scale of its own.
+// discards.  `rescued` tells whether a row has a scale of its own.
 template <int D>
 __device__ __forceinline__ void split_tile(const PagedDesc& a, bool values, uint32_t tile, float* scale, uint32_t* bad,
-                                           uint32_t* scaled, const Seg& s, int key, int w, int lane) {
+                                           uint8_t* rescued, const Seg& s, int key, int w, int lane) {
     const int half = D == 128 ? lane >> 4 : 0, row = D == 128 ? 16 * w + (lane & 15) : 32 * (w & 1) + lane;
     uint32_t at = tile + (row >> 3) * Cfg<D>::kGroupRows + half * 2048 + (row & 7) * 128;
     asm volatile("" : "+r"(at));  // addresses are worked out here, not kept over the tile loop
@@ -449,8 +448,8 @@ __device__ __forceinline__ void split_tile(const PagedDesc& a, bool values, uint
     if constexpr (D == 128) t = nan_max(t, __shfl_xor_sync(FULL, t, 16));
     uint32_t odd_rows = 0;
     const bool rescue = !(t < kTopMost) || (t < kTopLeast && t > 0.f);
-    const uint32_t rescued = __ballot_sync(FULL, rescue);
-    if (rescued) {
+    const bool any = __any_sync(FULL, rescue);
+    if (any) {
         bool odd = false;
         if (rescue) {
             const float* src = global_row(a, values ? a.v_pool : a.k_pool, values ? a.v_new : a.k_new, s.b, key, row, s.hk);
@@ -460,7 +459,7 @@ __device__ __forceinline__ void split_tile(const PagedDesc& a, bool values, uint
     }
     if (half == 0) scale[row] = unscale;
     if (lane == 0) {
-        scaled[w] = rescued;
+        rescued[w] = any;
         if (values) bad[w] = D == 128 ? odd_rows & 0xffffu : odd_rows;
     }
 }
@@ -498,11 +497,6 @@ __device__ __forceinline__ uint64_t bad_rows(const uint32_t* b) {
     const uint4 v = *reinterpret_cast<const uint4*>(b);
     return D == 128 ? (v.x | v.y << 16) | (uint64_t)(v.z | v.w << 16) << 32 : (v.x | v.z) | (uint64_t)(v.y | v.w) << 32;
 }
-__device__ __forceinline__ bool any_of(const uint32_t* b) {
-    const uint4 v = *reinterpret_cast<const uint4*>(b);
-    return (v.x | v.y | v.z | v.w) != 0;
-}
-
 // Values that are not finite would reach every row of a tile through 0 x inf =
 // NaN, so the tile has zeros in their place and they are added here, to the rows
 // that see them.  `rows_bad`: such keys of the tile; columns col .. col + n of each
@@ -672,11 +666,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // fold, the softmax gets two tiles further: S(n) is issued before P.V of tile
     // n - 1, which waits.
     __shared__ __align__(16) float k_scale[kRing][kKT], v_scale[kRing][kKT];
-    __shared__ __align__(16) uint32_t v_bad[kRing][4], k_scaled[kRing][4], v_scaled[kRing][4];
+    __shared__ __align__(16) uint32_t v_bad[kRing][4];
+    __shared__ __align__(8) uint8_t rescued[kRing][2][4];  // keys, values: a split warp's rows have a scale of their own
     __shared__ float q_scale[4][kM];             // by piece % 4
-    __shared__ float2 fold_f[kRing][kM];         // alpha, output scale of a tile that begins a group
+    __shared__ float2 fold_f[kRing][kM];         // alpha, output scale of such a tile
     __shared__ float row_inv[kRing][kM];         // last tile of a piece: 1 / l, or 1
-    __shared__ int group_tag[kRing];             // n + 1: tile n begins a group (written by the softmax)
+    __shared__ __align__(16) int group_tag[kRing][4];  // by softmax warp, n + 1: tile n begins a group, its fold_f counts
     __shared__ int2 group_at[2];                 // a group's first and last tile
     __shared__ int4 tile_at[kRing];              // rows of the block (kFirst, kLast, kBad), request, first key, KV head
 
@@ -701,9 +696,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 1) tmem_alloc(&tmem_base_s, C::kTmemCols);
     if (threadIdx.x == 32) g.head[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (threadIdx.x < kRing) group_tag[threadIdx.x] = 0;
+    if (threadIdx.x < 4 * kRing) (&group_tag[0][0])[threadIdx.x] = 0;
     if (threadIdx.x < 4 * kRing)  // headDim 64: two words of a tile's four are never written
-        (&v_bad[0][0])[threadIdx.x] = (&k_scaled[0][0])[threadIdx.x] = (&v_scaled[0][0])[threadIdx.x] = 0;
+        (&v_bad[0][0])[threadIdx.x] = (&rescued[0][0][0])[threadIdx.x] = (&rescued[0][0][0])[4 * kRing + threadIdx.x] = 0;
 
     // The requests' tiles and their running sum.
     long long carry = 0;
@@ -752,9 +747,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && warp_next(g, prefix, s)) {
             int batch = -1, y_cur = nowhere;
-            const int subs = (s.len + g.sub - 1) / g.sub, u1 = s.u1;
+            const int subs = (s.len + g.sub - 1) / g.sub, u1 = s.u1, n_sink = s.n_sink, n_ctx = s.n_ctx, lo_tile = s.lo_tile;
             for (int u = s.u0; u < u1; ++u, ++n) {
-                const int key = tile_key(s, a.tree, u);
+                const int key = tile_key(n_sink, n_ctx, lo_tile, a.tree, u);
                 int y = nowhere;
                 if (key >= 0) {
                     const int q0 = key / g.sub;
@@ -822,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 raise_device_error(&g_paged_device_error, kErrPgMma);
                 return false;
             }
-            if (len > 0 && (first || __shfl_sync(FULL, group_tag[j % kRing], 0) == j + 1)) close(j - 1);
+            if (len > 0 && (first || __any_sync(FULL, group_tag[j % kRing][lane & 3] == j + 1))) close(j - 1);
             if (len == 0) {
                 from = j;
                 if (groups > 0 && !__all_sync(FULL, wait_for(&o_free, (uint32_t)((groups - 1) & 1)))) {
@@ -896,7 +891,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- softmax: thread = virtual row -------------------------------------------
         const int i = threadIdx.x - 32 * kSoftmaxWarp;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        int n = 0, piece = 0;
+        int n = 0, piece = 0, v_slot = 1;
+        uint32_t v_phase = 0;
         bool ok = true;
         while (ok && warp_next(g, prefix, s)) {
             const int v = s.rb * kM + i, t = v / a.G;
@@ -919,12 +915,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int sinks = (int)min(a.sinks, (int64_t)s.len);
             float m = -INFINITY, l = 0.f;
             bool was_scaled = false;
-            const int rows = min(s.T * a.G - s.rb * kM, kM), tiles = s.u1 - s.u0;
+            const int rows = min(s.T * a.G - s.rb * kM, kM);
+            const int u0 = s.u0, u1 = s.u1, n_sink = s.n_sink, n_ctx = s.n_ctx, lo_tile = s.lo_tile;
             // A warp without rows waits at the barrier that ends the piece; the first
             // warp, which always has one, arrives for it.
             const int arrivals = warp == kSoftmaxWarp ? 4 - (rows + 31) / 32 + 1 : 1;
-            for (int u = s.u0; u < s.u1 && __any_sync(FULL, alive); ++u, ++n) {
-                const int key = tile_key(s, a.tree, u), nb = n % kRing, bf = n & 1, it = 2 * n + 1;
+            const bool idle = !__any_sync(FULL, alive);
+            for (int u = idle ? u1 : u0; u < u1; ++u, ++n) {
+                const int key = tile_key(n_sink, n_ctx, lo_tile, a.tree, u), nb = n % kRing, bf = n & 1;
                 if (!__all_sync(FULL, wait_for(&s_full[bf], (uint32_t)((n >> 1) & 1)))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
@@ -933,19 +931,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Keys of the tile that the row sees (a row of no request: anything).
                 const bool all = !alive || (key >= 0 && hi - key >= kKT - 1 && lo <= key);
                 const bool whole = __all_sync(FULL, all);
-                uint64_t see = ~0ull;
-                if (!all) see = tile_mask(a, s, key, hi, lo, sinks, p, t);
                 tc_fence_after();
                 RowTile rt;
                 rt.at = tmem + lanes + C::kColS + bf * kKT;
-                rt.see = see;
+                rt.see = ~0ull;
                 rt.mul = q_scale[piece & 3][i] * kUnscale;
                 rt.cap = a.cap_log2;
-                float alpha, o_scale = kUnscale;  // of the tile's output
+                rt.ks = k_scale[nb];
+                if (!all) rt.see = tile_mask(a, s, key, hi, lo, sinks, p, t);
+                float alpha;
                 bool moved;
-                if (any_of(k_scaled[nb])) {  // rare
-                    rt.mul = q_scale[piece & 3][i];
-                    rt.ks = k_scale[nb];
+                if (*reinterpret_cast<const uint32_t*>(rescued[nb][0])) {  // rare
+                    rt.mul *= kScale;
                     alpha = row_softmax<CAP, false, true>(rt, m, l, moved);
                 } else if (whole) {
                     alpha = row_softmax<CAP, true, false>(rt, m, l, moved);
@@ -953,26 +950,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     alpha = row_softmax<CAP, false, false>(rt, m, l, moved);
                 }
                 // Nothing above needs the values, which are often still to come.
-                if (!__all_sync(FULL, wait_for(&ready[it % ST], (uint32_t)((it / ST) & 1)))) {
+                if (!__all_sync(FULL, wait_for(&ready[v_slot], v_phase))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
                     break;
                 }
-                const bool scaled = any_of(v_scaled[nb]);
-                if (scaled) {  // rare: the largest value scale among the keys seen sets the probabilities'
-                    o_scale = 7.888609052210118e-31f;
-                    for (int k = 0; k < kKT; ++k)
-                        if ((see >> k) & 1) o_scale = fmaxf(o_scale, v_scale[nb][k]);
-                    row_reweigh(rt.at, v_scale[nb], __uint_as_float(0x7f000000u - __float_as_uint(o_scale)));
+                if ((v_slot += 2) >= ST) {
+                    v_slot = 1;
+                    v_phase ^= 1;
                 }
+                int flags = rows;
+                const bool scaled = *reinterpret_cast<const uint32_t*>(rescued[nb][1]) != 0;
                 // A tile with another reference or scale than the one before begins a group.
-                if (__any_sync(FULL, moved && alive) || scaled || was_scaled) group_tag[nb] = n + 1;
-                fold_f[nb][i] = make_float2(alpha, o_scale * kScale);
+                if (__any_sync(FULL, moved && alive) || scaled || was_scaled) {
+                    float o_scale = 1.f;  // of the tile's output, times kScale
+                    if (scaled) {         // the largest value scale among the keys seen sets the probabilities'
+                        float top = 7.888609052210118e-31f;
+                        for (int k = 0; k < kKT; ++k)
+                            if ((rt.see >> k) & 1) top = fmaxf(top, v_scale[nb][k]);
+                        row_reweigh(rt.at, v_scale[nb], __uint_as_float(0x7f000000u - __float_as_uint(top)));
+                        o_scale = top * kScale;
+                        const uint64_t bad = bad_rows<D>(v_bad[nb]);
+                        if (bad) {  // which of them the row sees, for the fold
+                            g.odd_rows[((int64_t)blockIdx.x * kRing + nb) * kM + i] = alive ? bad & rt.see : 0;
+                            flags += kBad;
+                        }
+                    }
+                    fold_f[nb][i] = make_float2(alpha, o_scale);
+                    group_tag[nb][warp & 3] = n + 1;
+                }
                 was_scaled = scaled;
-                const uint64_t bad = bad_rows<D>(v_bad[nb]);
-                if (bad)  // rare: which of them the row sees, for the fold
-                    g.odd_rows[((int64_t)blockIdx.x * kRing + nb) * kM + i] = alive ? bad & see : 0;
-                if (u == s.u1 - 1) {
+                if (u == u0) flags += kFirst;
+                if (u == u1 - 1) {
+                    flags += kLast;
                     float inv = 1.f;
                     if (s.slot < 0) {
                         inv = l != 0.f ? 1.f / l : 0.f;
@@ -982,15 +992,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     row_inv[nb][i] = inv;
                 }
-                if (i == 0)
-                    tile_at[nb] = make_int4(rows + (u == s.u0 ? kFirst : 0) + (u == s.u1 - 1 ? kLast : 0) + (bad ? kBad : 0), s.b,
-                                            key, s.hk);
+                if (i == 0) tile_at[nb] = make_int4(flags, s.b, key, s.hk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_n(&p_full[bf], arrivals);
             }
-            if (!__any_sync(FULL, alive)) n += tiles;
+            if (idle) {  // past the tiles of the piece
+                n += u1 - u0;
+                const int it = 2 * n + 1;
+                v_slot = it % ST;
+                v_phase = (uint32_t)((it / ST) & 1);
+            }
             // One barrier a piece keeps the four warps' tile counts together; a failed
             // wait ends the role for all of them.
             ok = sync_and(1, 128, ok);
@@ -1002,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n = 0;
         bool ok = true;
         while (ok && warp_next(g, prefix, s)) {
-            const int u1 = s.u1;
+            const int u1 = s.u1, n_sink = s.n_sink, n_ctx = s.n_ctx, lo_tile = s.lo_tile;
             for (int u = s.u0; u < u1; ++u, ++n) {
                 if (D == 64 && (n & 1) != (w >> 1)) continue;  // a tile's two warps of the four
                 const int it = 2 * n + side, st = it % ST;
@@ -1014,8 +1027,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 split_tile<D>(a, side != 0, smem_u32(tiles) + st * C::kTile, side ? v_scale[n % kRing] : k_scale[n % kRing],
-                              v_bad[n % kRing], side ? v_scaled[n % kRing] : k_scaled[n % kRing], s,
-                              tile_key(s, a.tree, u), w, lane);
+                              v_bad[n % kRing], rescued[n % kRing][side], s,
+                              tile_key(n_sink, n_ctx, lo_tile, a.tree, u), w, lane);
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ready[st]);
@@ -1087,7 +1100,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rows = tile_at[nb].x & (kFirst - 1);
             const bool first = tile_at[nb].x & kFirst, last = tile_at[ne].x & kLast;
             if (32 * w < rows) {
-                const float2 f = fold_f[nb][i];
+                const float2 f = group_tag[nb][w] == group.x + 1 ? fold_f[nb][i] : make_float2(1.f, 1.f);
                 const float fin = last ? row_inv[ne][i] * kUnscale : 1.f;
                 const bool plain = __all_sync(FULL, (first || f.x == 1.f) && f.y == 1.f && !last);
                 const uint64_t fx = f2_pack(f.x, f.x), fy = f2_pack(f.y, f.y), fin2 = f2_pack(fin, fin);
