@@ -1161,22 +1161,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (more) load_queries();
         to = next_to;
         for (int k = 0; ok && more;) {
-            const int end = n + s.u1 - s.u0, it = 2 * (end - 1);
-            uint64_t* scores_done = &freed[it % ST];  // of the piece's last tile
-            const uint32_t phase = (uint32_t)((it / ST) & 1);
+            const int end = n + s.u1 - s.u0;
             bool loaded = false;
+            // The K slot of the piece's last tile is freed once by every kStep-th tile, and a
+            // wait tells two frees of a slot apart only one after the other: `due` is the
+            // first of them that is not known to have come.  (P.V of tile n - 1, folded,
+            // means that S(n) is done.)
+            constexpr int kStep = ST / 2;
+            int due = (end - 1) % kStep;
+            auto due_done = [&]() { return __all_sync(FULL, mbar_try_wait(&freed[(2 * due) % ST], (uint32_t)(((2 * due) / ST) & 1))); };
             while (n < end) {
                 // The next piece's queries go in once the last scores with this one's are done:
                 // before the fold that ends the piece, since its P.V comes after the
                 // next piece's first scores; but those last scores may wait for a fold
                 // that comes first.
                 if (end - n <= kGroup && !loaded) {
-                    bool done = false;
-                    for (int i = 0; i < (1 << 20) && !(done = __all_sync(FULL, mbar_try_wait(scores_done, phase))) &&
-                                    !__all_sync(FULL, mbar_try_wait(&o_full, (uint32_t)(k & 1)));
-                         ++i) {
+                    if (n > 0 && due <= n) due += (n - due + kStep) / kStep * kStep;
+                    for (int i = 0; i < (1 << 20) && due < end; ++i) {
+                        if (due_done())
+                            due += kStep;
+                        else if (__all_sync(FULL, mbar_try_wait(&o_full, (uint32_t)(k & 1))))
+                            break;
                     }
-                    if (done) {
+                    if (due >= end) {
                         loaded = true;
                         more = next_piece();
                         tc_fence_after();
@@ -1189,13 +1196,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
             }
-            if (ok && !loaded) {  // the last fold came first: nothing follows, or the scores are done by now
-                if (!__all_sync(FULL, wait_for(scores_done, phase))) {
-                    raise_device_error(&g_paged_device_error, kErrPgMma);
-                    break;
-                }
+            if (ok && !loaded) {  // the last fold came first: all of the piece's scores are done
                 more = next_piece();
-                tc_fence_after();
                 if (more) load_queries();
                 to = next_to;
             }
