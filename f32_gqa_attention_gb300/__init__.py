@@ -13,6 +13,7 @@ Build it with ``python -m f32_gqa_attention_gb300._build``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -682,9 +683,24 @@ def mla_decode_step(state, state_new, offset: int, q, k_b, v_b, *, heads, qk_nop
 # ------------------------------------------------------------- paged caches
 def _need(name, t, dtype, device=None):
     """A contiguous CUDA tensor of the type, on the call's device."""
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or (device is not None and t.device != device):
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or (device is not None and t.device != device):
         where = "" if device is None else f" on {device}"
         raise ValueError(f"{name} must be a contiguous {str(dtype).removeprefix('torch.')} CUDA tensor{where}")
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device):
+    """The device as the current one; nothing to do where it is (the usual case)."""
+    import torch
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _raw_stream(device) -> int:
+    """The device's current stream as the library takes it."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def page_map(lens, cu_rows, block_table, free_pages, n_free, *, rows: int, pageSize: int, accept=None, stream=None):
@@ -706,12 +722,9 @@ def page_map(lens, cu_rows, block_table, free_pages, n_free, *, rows: int, pageS
             (accept is not None and accept.shape != (n,))):
         raise ValueError("page_map: cu_rows [requests + 1], block_table [requests, maxPages], n_free [1], "
                          "accept [requests]")
-    slots = torch.empty(rows, dtype=i32, device=dev)
-    positions = torch.empty(rows, dtype=i32, device=dev)
-    new_lens = torch.empty(n, dtype=i32, device=dev)
-    left = torch.empty(1, dtype=i32, device=dev)
-    with torch.cuda.device(dev):
-        st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    slots, positions, new_lens, left = torch.empty(2 * rows + n + 1, dtype=i32, device=dev).split([rows, rows, n, 1])
+    with _on(dev):
+        st = _raw_stream(dev) if stream is None else stream
         vtmu_page_map(lens, cu_rows, accept, block_table, free_pages, free_pages.numel(), n_free, slots, positions,
                       new_lens, left, n, rows, pageSize, block_table.shape[1], st)
     return slots, positions, new_lens, left
@@ -729,8 +742,8 @@ def tree_plan(parents, cu_rows, lens, *, stream=None):
         raise ValueError("tree_plan: cu_rows [requests + 1], lens [requests]")
     masks = torch.empty(parents.shape[0], dtype=torch.int64, device=dev)
     positions = torch.empty(parents.shape[0], dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    with _on(dev):
+        st = _raw_stream(dev) if stream is None else stream
         vtmu_tree_plan(parents, cu_rows, lens, masks, positions, lens.shape[0], parents.shape[0], st)
     return masks, positions
 
@@ -749,8 +762,8 @@ def rope_at(x, positions, *, headDim, out=None, stream=None, **params):
     if x.dim() != 2 or x.shape[1] % headDim or positions.shape != (x.shape[0],) or out.shape != x.shape:
         raise ValueError("rope_at: x and out [T, heads*headDim], positions [T]")
     r = make_rope_params(headDim=headDim, **params)
-    with torch.cuda.device(dev):
-        st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    with _on(dev):
+        st = _raw_stream(dev) if stream is None else stream
         vtmu_rope_at(x, out, x.shape[0], x.shape[1] // headDim, positions, r, st)
     return out
 
@@ -768,8 +781,8 @@ def paged_write(k_pool, v_pool, k_new, v_new, slots, *, stream=None):
     if (k_pool.dim() != 2 or v_pool.dim() != 2 or k_pool.shape[0] != v_pool.shape[0] or
             k_new.shape != (n, k_pool.shape[1]) or v_new.shape != (n, v_pool.shape[1])):
         raise ValueError("paged_write: pools [poolRows, width], k_new and v_new [rows, width], slots [rows]")
-    with torch.cuda.device(dev):
-        st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    with _on(dev):
+        st = _raw_stream(dev) if stream is None else stream
         vtmu_paged_write(k_pool, v_pool, k_pool.shape[0], k_pool.shape[1], v_pool.shape[1], k_new, v_new, slots, n, st)
     return k_pool, v_pool
 
@@ -819,10 +832,10 @@ def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, hea
                           head_dim=headDim, tree=0 if tree is None else 1, has_scale=0 if scale is None else 1,
                           scale=0.0 if scale is None else scale, softcap=softcap or 0.0, kernel=kernel,
                           window=window or 0, sinks=sinks or 0)
-    with torch.cuda.device(dev):
+    with _on(dev):
         nbytes = vtmu_paged_workspace_size(p)
         buf, cap = (workspace if workspace is not None else _default_workspace(dev)).get(nbytes)
-        st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+        st = _raw_stream(dev) if stream is None else stream
         vtmu_paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, k_new, v_new, masks, positions, out, p,
                              buf, cap, st)
     return out

@@ -161,9 +161,14 @@ __global__ void __launch_bounds__(32 * kTreeWarps)
 }
 
 // ---- rope_at -----------------------------------------------------------------------
+// As rope.cu, with the row's position from the device: a CTA forms the row's (cos, sin)
+// table (angle in double), then turns its heads.  Memory-bound: VEC (16-byte
+// aligned rows, headDim and rotary_dim / 2 multiples of four) turns four pairs a
+// thread with 16-byte accesses.
+template <bool VEC>
 __global__ void __launch_bounds__(256) rope_at_kernel(const float* x, float* out, int64_t T, int H, int D,
                                                       const int32_t* __restrict__ positions, const RopeDev r) {
-    __shared__ float2 cs[kRopeMaxPairs];
+    __shared__ __align__(16) float2 cs[kRopeMaxPairs];
     const int half = r.half;
     const int64_t row_len = (int64_t)H * D;
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
@@ -174,13 +179,39 @@ __global__ void __launch_bounds__(256) rope_at_kernel(const float* x, float* out
         __syncthreads();
         const float* xr = x + t * row_len;
         float* orow = out + t * row_len;
-        for (int e = threadIdx.x; e < H * half; e += blockDim.x) {
-            const int h = e / half, j = e - h * half;
-            const int ia = r.interleaved ? 2 * j : j;
-            const int ib = r.interleaved ? 2 * j + 1 : j + half;
-            const float a = xr[h * D + ia], b = xr[h * D + ib];
-            orow[h * D + ia] = rope_channel(a, b, true, cs[j]);
-            orow[h * D + ib] = rope_channel(b, a, false, cs[j]);
+        if constexpr (VEC) {
+            const int quads = half / 4;
+            for (int e = threadIdx.x; e < H * quads; e += blockDim.x) {
+                const int h = e / quads, j = 4 * (e - h * quads);
+                const int ia = h * D + (r.interleaved ? 2 * j : j), ib = h * D + (r.interleaved ? 2 * j + 4 : j + half);
+                const float4 u = *reinterpret_cast<const float4*>(xr + ia), v = *reinterpret_cast<const float4*>(xr + ib);
+                const float4 c01 = *reinterpret_cast<const float4*>(&cs[j]), c23 = *reinterpret_cast<const float4*>(&cs[j + 2]);
+                const float2 c0 = make_float2(c01.x, c01.y), c1 = make_float2(c01.z, c01.w), c2 = make_float2(c23.x, c23.y),
+                             c3 = make_float2(c23.z, c23.w);
+                float4 p, q;
+                if (r.interleaved) {
+                    p = make_float4(rope_channel(u.x, u.y, true, c0), rope_channel(u.y, u.x, false, c0),
+                                    rope_channel(u.z, u.w, true, c1), rope_channel(u.w, u.z, false, c1));
+                    q = make_float4(rope_channel(v.x, v.y, true, c2), rope_channel(v.y, v.x, false, c2),
+                                    rope_channel(v.z, v.w, true, c3), rope_channel(v.w, v.z, false, c3));
+                } else {
+                    p = make_float4(rope_channel(u.x, v.x, true, c0), rope_channel(u.y, v.y, true, c1),
+                                    rope_channel(u.z, v.z, true, c2), rope_channel(u.w, v.w, true, c3));
+                    q = make_float4(rope_channel(v.x, u.x, false, c0), rope_channel(v.y, u.y, false, c1),
+                                    rope_channel(v.z, u.z, false, c2), rope_channel(v.w, u.w, false, c3));
+                }
+                *reinterpret_cast<float4*>(orow + ia) = p;
+                *reinterpret_cast<float4*>(orow + ib) = q;
+            }
+        } else {
+            for (int e = threadIdx.x; e < H * half; e += blockDim.x) {
+                const int h = e / half, j = e - h * half;
+                const int ia = h * D + (r.interleaved ? 2 * j : j);
+                const int ib = h * D + (r.interleaved ? 2 * j + 1 : j + half);
+                const float a = xr[ia], b = xr[ib];
+                orow[ia] = rope_channel(a, b, true, cs[j]);
+                orow[ib] = rope_channel(b, a, false, cs[j]);
+            }
         }
         if (out != x) {
             const int pass = D - 2 * half;
@@ -236,7 +267,13 @@ cudaError_t launch_tree_plan(const int32_t* parents, const int32_t* cu_rows, con
 cudaError_t launch_rope_at(const float* x, float* out, int64_t T, int H, int D, const int32_t* positions,
                            const RopeDev& r, cudaStream_t stream) {
     if (T == 0) return cudaSuccess;
-    rope_at_kernel<<<(unsigned)(T < kWave ? T : kWave), 256, 0, stream>>>(x, out, T, H, D, positions, r);
+    const unsigned blocks = (unsigned)(T < kWave ? T : kWave);
+    const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0 && D % 4 == 0 &&
+                     r.half % 4 == 0 && r.half > 0;
+    if (vec)
+        rope_at_kernel<true><<<blocks, 256, 0, stream>>>(x, out, T, H, D, positions, r);
+    else
+        rope_at_kernel<false><<<blocks, 256, 0, stream>>>(x, out, T, H, D, positions, r);
     return cudaGetLastError();
 }
 

@@ -73,7 +73,11 @@ constexpr int kFoldWarp = 4, kSoftmaxWarp = 8, kSplitWarp = 12, kFoldWarps = 4;
 constexpr int kFirst = 1 << 16, kLast = 1 << 17, kBad = 1 << 18;  // a piece's first and last tile; values that are not finite
 constexpr int kPShift = 11;    // probabilities are scaled by 2^11 in f16
 constexpr float kLazyLog2 = 4.f;  // and a row's reference maximum moves when beaten by more than 2^4: 2^15 at most
-constexpr int kGroup = 4;      // tiles that one accumulator takes before it is folded
+// Tiles that one accumulator takes before it is folded.  The tensor cores round their sums
+// towards zero at every step: on 32 single-token requests the error against 64 bits is
+// 5.6e-7 with one tile, 7.8e-7 with two, 9.3e-7 with three, 1.1e-6 with four, at
+// 281, 258, 257 and 249 us.
+constexpr int kGroup = 2;
 constexpr int kRing = 8;       // a power of two, at least kGroup + 2 (and 5)
 
 enum : unsigned int {
