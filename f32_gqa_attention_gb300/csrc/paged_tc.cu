@@ -639,7 +639,8 @@ __device__ __noinline__ void row_reweigh(uint32_t at, const float* weight, float
             const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&l));
             const float* w = weight + 32 * c + 2 * k;
             uint32_t h2, l2;
-            split2(f2_pack((fh.x + fl.x) * (w[0] * mul), (fh.y + fl.y) * (w[1] * mul)), h2, l2);
+            // At most 1 for a key that is seen; one that is not may be larger, times p = 0.
+            split2(f2_pack((fh.x + fl.x) * fminf(w[0] * mul, 1.f), (fh.y + fl.y) * fminf(w[1] * mul, 1.f)), h2, l2);
             phi[k] = __uint_as_float(h2);
             plo[k] = __uint_as_float(l2);
         }
