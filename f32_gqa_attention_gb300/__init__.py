@@ -759,7 +759,7 @@ def rope_at(x, positions, *, headDim, out=None, stream=None, **params):
     if out is None:
         out = torch.empty_like(x)
     _need("out", out, torch.float32, dev)
-    if x.dim() != 2 or x.shape[1] % headDim or positions.shape != (x.shape[0],) or out.shape != x.shape:
+    if headDim < 1 or x.dim() != 2 or x.shape[1] % headDim or positions.shape != (x.shape[0],) or out.shape != x.shape:
         raise ValueError("rope_at: x and out [T, heads*headDim], positions [T]")
     r = make_rope_params(headDim=headDim, **params)
     with _on(dev):
@@ -806,7 +806,7 @@ def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, hea
         _need(name, t, i32, dev)
     hk = heads if kvHeads is None else kvHeads
     rows, n = q.shape[0], lens.shape[0]
-    if (q.shape != (rows, heads * headDim) or k_pool.dim() != 2 or k_pool.shape[1] != hk * headDim or
+    if (pageSize < 1 or q.shape != (rows, heads * headDim) or k_pool.dim() != 2 or k_pool.shape[1] != hk * headDim or
             k_pool.shape != v_pool.shape or k_pool.shape[0] % pageSize or block_table.dim() != 2 or
             block_table.shape[0] != n or cu_rows.shape != (n + 1,)):
         raise ValueError("paged_attention: q [rows, heads*headDim], pools [pages*pageSize, kvHeads*headDim], "

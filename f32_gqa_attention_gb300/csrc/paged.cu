@@ -18,7 +18,9 @@ constexpr int64_t kWave = 152 * 8;  // CTAs of 256 threads that are resident at 
 // that one launch with no ordering between CTAs does: a CTA never reads a table
 // entry that another one writes, new pages being read off the stack.  CTA
 // (b, y) serves every gridDim.y-th chunk of request b's rows; the CTAs of b ==
-// requests clear the rows behind the last request.
+// requests clear the rows behind the last request.  Bound by the launch: the
+// accepted rows of 7 trees and 256 prompts of 1 to 1021 rows take the same 25 us
+// from the host; the first 3.1 us a call in a replayed graph.
 constexpr int kMapThreads = 256;
 
 struct Need {
@@ -99,6 +101,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const PageMapArgs
 // row starts with its own bit and its parent; each of six steps adds the mask
 // of the row it points to and moves the pointer there, so the path a mask
 // covers doubles and 64 rows are done in 6 steps whatever the tree's depth.
+// Bound by the launch: 1.4 us a call in a replayed graph for one tree, 1.7 us for many.
 constexpr int kTreeWarps = 4;
 
 __global__ void __launch_bounds__(32 * kTreeWarps)
@@ -164,7 +167,8 @@ __global__ void __launch_bounds__(32 * kTreeWarps)
 // As rope.cu, with the row's position from the device: a CTA forms the row's (cos, sin)
 // table (angle in double), then turns its heads.  Memory-bound: VEC (16-byte
 // aligned rows, headDim and rotary_dim / 2 multiples of four) turns four pairs a
-// thread with 16-byte accesses.
+// thread with 16-byte accesses: 8111 rows of 40 heads of 128 take 57.6 us, 5.8 TB/s
+// (one pair a thread: 70 us).
 template <bool VEC>
 __global__ void __launch_bounds__(256) rope_at_kernel(const float* x, float* out, int64_t T, int H, int D,
                                                       const int32_t* __restrict__ positions, const RopeDev r) {
@@ -225,7 +229,9 @@ __global__ void __launch_bounds__(256) rope_at_kernel(const float* x, float* out
 
 // ---- paged_write --------------------------------------------------------------------
 // A memory-bound copy: one CTA per packed row at a time, K and V of the row in
-// flight together.  VEC floats per access: 4 where pointers and widths allow.
+// flight together, 16 bytes an access where pointers and widths allow.  A call of
+// 514 MB takes 81 us, 6.3 TB/s (94 % of the copy rate); a few rows 1.8 us in a
+// replayed graph.
 template <typename V>
 __global__ void __launch_bounds__(256)
     paged_write_kernel(V* __restrict__ k_pool, V* __restrict__ v_pool, int64_t pool_rows, int64_t kw, int64_t vw,

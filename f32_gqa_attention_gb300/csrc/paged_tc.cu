@@ -6,16 +6,18 @@
 // are virtual rows v = t G + g; up to 128 of them (a row block) meet the same
 // keys:   x2[v, s] = log2 e * softcap(scale q_v.k_s),  m = running max,
 //         p = 2^(x2 - m),  l = sum p,  o = sum p v_s,  out = o / l.
-// Both products run on f16 operands that carry 22 bits of an f32: a row x of Q,
-// K or V is brought to |x| < 2 by a power of two e_x of its own (exact), then
-// x = hi + lo with hi, lo in f16, and x.y = hi.hi + hi.lo + lo.hi, each summed
-// in f32.  What is dropped or rounded is at most 2^-22 of the row's largest
-// element.  Three f16 products cost 1.5 passes of a tf32 one, so this is twice
-// as fast as splitting into tf32 halves, at the same precision, and halves
-// the bytes that the MMAs read from shared memory.  Key scales multiply the
-// scores, value scales the probabilities: p'_s = p_s 2^(e_s - e_max + 14) with
-// e_max over the keys that the row sees in the tile, so that p' fills f16's
-// range, and the tile's output is multiplied by 2^(e_max - 14).
+// Both products run on f16 operands that carry 22 bits of an f32: an element x
+// times a power of two (exact) is hi + lo with hi, lo in f16, and x.y = lo.hi +
+// hi.lo + hi.hi, summed in f32.  What is dropped or rounded is at most 2^-22
+// of the row's largest element.  Three f16 products cost 1.5 passes of a tf32
+// one, so this is twice as fast as splitting into tf32 halves, at the same
+// precision, and halves the bytes that the MMAs read from shared memory.  The
+// power is 2^6 for a row of K or V whose largest element lies in [2^-9, 2^9), and
+// one of its own for a row of Q and for any other row of K or V; those
+// multiply the scores and, brought to at most 1, the probabilities.  P has
+// 2^11 as a factor, so that f16 holds small ones too; l has it as well.  A
+// row's reference maximum moves only when it is beaten by more than 2^4, so
+// that the output seldom needs to be multiplied by alpha.
 //
 // Split of the work.  The lengths are on the device, so the launch is one
 // persistent CTA per SM and the CTAs divide the 64-key tiles of all (request,
@@ -26,22 +28,30 @@
 // With more than 128 virtual rows per KV head, teams of R CTAs walk the same
 // tiles for R row blocks at the same time, so the tiles come from HBM once.
 //
-// Tiles of 64 keys, M = 128 virtual rows (padded: a wave of MMAs takes less
-// time than the tile's bytes take from HBM, so padding costs nothing).  Warps:
+// Tiles of 64 keys, M = 128 virtual rows (padded: the MMAs of a tile take 1540
+// cycles, its 64 KB 2800 at this SM's share of HBM, so padding costs no
+// bandwidth).  Warps:
 //   0, 2    page ids (32 at a time, one per lane) and TMA loads of f32 K and V tiles, one
-//           box per page; drafted rows come as one tile of their
-//           own from k_new / v_new; rows of no page are read out of bounds, as
-//           zeros;
-//   1       lane 0 issues the MMAs: S(n) = Q.K^T, then O(n - 1) = P.V;
-//   4 - 7   softmax, thread = virtual row: no exchange between threads; P goes
+//           box per page (with a box for each group of 8 rows the one warp that issued
+//           them fell behind on pages of 16); drafted rows come as one tile of their own from k_new / v_new; rows of
+//           no page are read out of bounds, as zeros;
+//   1       the MMAs: S(n) = Q.K^T, then O(n - 1) = P.V;
+//   4 - 7   a piece's queries to TMEM, and the fold acc = acc alpha + O of every two tiles
+//           (kGroup: no sum runs long inside the pipe); acc stays in TMEM, so that 20
+//           warps fit the registers;
+//   8 - 11  softmax, thread = virtual row: no exchange between threads; P goes
 //           back to TMEM over S as the A operand of P.V;
-//   8 - 15  split: f32 rows to f16 hi and lo in place (K K-major, V MN-major: the same
-//           bytes), four warps for the keys and four for the values;
-//   16 - 19 a piece's queries to TMEM, and the fold acc = acc alpha + O of each tile (a
-//           fresh accumulator for every two tiles: no sum runs long inside the pipe); acc
-//           stays in TMEM, so that 20 warps fit the registers.
+//   12 - 19 split: f32 rows to f16 hi and lo in place (K K-major, V MN-major: the same
+//           bytes), four warps for the keys and four for the values.
 // TMEM: Q hi, lo (D columns), S / P two buffers (128), O and its running sum (2 D).
 // Every wait is bounded; a wait that gives up sets a bit of the device flag.
+//
+// Measured, headDim 128, 32 heads over 8: one row for each of 32 requests of 517 to 8111
+// rows, pages of 16: 258 us for 1.176 GB, 4.6 TB/s (67 % of the copy rate).  Trees
+// of 64 rows on 8 requests of 16384 to 32704, pages of 64: 647 us for 217 GFLOP,
+// 335 TFLOP/s of f32 products, 52 % of a third of the f16 rate.  What bounds it: a
+// tile's softmax is one thread per row, about 2000 cycles with its hand-overs
+// against 1540 of MMAs, and at a group's end P.V waits for the fold.
 #include <cstring>
 #include <mutex>
 
@@ -78,7 +88,8 @@ constexpr float kLazyLog2 = 4.f;  // and a row's reference maximum moves when be
 // 5.6e-7 with one tile, 7.8e-7 with two, 9.3e-7 with three, 1.1e-6 with four, at
 // 281, 258, 257 and 249 us.
 constexpr int kGroup = 2;
-constexpr int kRing = 8;       // a power of two, at least kGroup + 2 (and 5)
+constexpr int kRing = 8;       // what a tile leaves for later roles
+static_assert(kRing >= kGroup + 2 && kRing >= 5 && (kRing & (kRing - 1)) == 0, "a slot outlives its last reader");
 
 enum : unsigned int {
     kErrPgLoad = 1u << 3,   // the splitters gave up on a loaded tile
@@ -485,9 +496,9 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return true;
     return wait_timed(bar, parity);
 }
-// A wait of several warps: the first one looks at the mbarrier while the others sleep at
-// barrier `id` (18 warps that all looked took two fifths of the issue slots), then
-// each looks once, for what the mbarrier orders.
+// A wait of the warps that share a tile: the first one looks at the mbarrier while the
+// others sleep at barrier `id` and leave it the issue slots, then each looks
+// once, for what the mbarrier orders.
 __device__ __forceinline__ bool team_wait(bool leads, int id, int threads, uint64_t* bar, uint32_t parity) {
     bool ok = true;
     if (leads) ok = __all_sync(FULL, wait_for(bar, parity));
@@ -1182,11 +1193,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // that comes first.
                 if (end - n <= kGroup && !loaded) {
                     if (n > 0 && due <= n) due += (n - due + kStep) / kStep * kStep;
-                    for (int i = 0; i < (1 << 20) && due < end; ++i) {
+                    uint64_t t0 = 0;
+                    for (int i = 1; due < end; ++i) {
                         if (due_done())
                             due += kStep;
                         else if (__all_sync(FULL, mbar_try_wait(&o_full, (uint32_t)(k & 1))))
                             break;
+                        if ((i & 1023) == 0) {  // bounded as wait_for is; the fold's own wait reports it
+                            const uint64_t now = __shfl_sync(FULL, global_ns(), 0);
+                            if (t0 == 0) t0 = now;
+                            if (now - t0 > kWaitLimitNs) break;
+                        }
                     }
                     if (due >= end) {
                         loaded = true;
@@ -1220,7 +1237,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partials of the unit that CTA blockIdx.x started and its team's
 // successors went on with: m* = max m_i, out = sum 2^(m_i - m*) o_i / sum 2^(m_i - m*) l_i.
-// A warp per virtual row.
+// A warp per virtual row.  Its launch overlaps the pieces' kernel; it reads at most
+// 20 MB of partials out of L2 and is a few microseconds of any call.
 template <int D>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PgArgs g) {
     pdl_wait();

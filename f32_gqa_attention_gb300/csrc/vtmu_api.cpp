@@ -399,7 +399,8 @@ vtmu_status resolve_paged(const vtmu_paged_params* p, vtmu::PagedDesc* a) {
         return fail(VTMU_ERR_UNSUPPORTED, "paged: max_rows x group size must be below 2^31");
     a->rows = p->rows;
     a->pages = p->pages;
-    a->window = p->window;
+    const int64_t far = (int64_t)1 << 40;  // beyond any two positions, and small enough to subtract
+    a->window = p->window < far ? p->window : far;
     a->sinks = p->window > 0 ? p->sinks : 0;  // without a window no key is dropped
     a->B = p->requests;
     a->H = p->heads;
@@ -408,7 +409,7 @@ vtmu_status resolve_paged(const vtmu_paged_params* p, vtmu::PagedDesc* a) {
     a->D = p->head_dim;
     a->page_size = p->page_size;
     a->max_pages = p->max_pages;
-    a->max_rows = p->max_rows;
+    a->max_rows = (int32_t)(p->max_rows < p->rows ? p->max_rows : p->rows);
     a->tree = p->tree;
     const double scale = p->has_scale ? (double)p->scale : 1.0 / std::sqrt((double)p->head_dim);
     a->softcap_on = p->softcap > 0.f ? 1 : 0;
@@ -1060,7 +1061,8 @@ vtmu_status vtmu_page_map(const int32_t* lens, const int32_t* cu_rows, const uin
                     (long long)rows, (long long)free_capacity);
     if (page_size < 1 || max_pages < 1)
         return fail(VTMU_ERR_INVALID, "page_map: page_size %d and max_pages %d must be > 0", page_size, max_pages);
-    if (requests == ((int32_t)1 << 31) - 1) return fail(VTMU_ERR_INVALID, "page_map: too many requests");
+    if (requests > 65536)  // every CTA adds up the requests before its own
+        return fail(VTMU_ERR_UNSUPPORTED, "page_map: %d requests, 65536 at most", requests);
     if (!cu_rows || !n_free || !n_free_out || (requests > 0 && (!lens || !block_table || !new_lens)) ||
         (rows > 0 && !slots) || (free_capacity > 0 && !free_pages))
         return fail(VTMU_ERR_INVALID, "page_map: a pointer is NULL");
@@ -1103,6 +1105,8 @@ vtmu_status vtmu_rope_at(const float* x, float* out, int64_t T, int32_t heads, c
     if (st != VTMU_OK) return st;
     if (T < 0 || heads <= 0)
         return fail(VTMU_ERR_INVALID, "rope_at: T %lld and heads %d must be >= 0 and > 0", (long long)T, heads);
+    if ((int64_t)heads * rp->head_dim >= ((int64_t)1 << 31))
+        return fail(VTMU_ERR_UNSUPPORTED, "rope_at: heads x headDim must be below 2^31");
     if (T == 0) return ok();
     if (!x || !out || !positions) return fail(VTMU_ERR_INVALID, "rope_at: x, out or positions is NULL");
     if (misaligned({x, out, positions}, 3u)) return fail(VTMU_ERR_INVALID, "rope_at: pointers must be 4-byte aligned");
@@ -1120,6 +1124,8 @@ vtmu_status vtmu_paged_write(float* k_pool, float* v_pool, int64_t pool_rows, in
     if (pool_rows < 0 || k_width < 0 || v_width < 0 || rows < 0)
         return fail(VTMU_ERR_INVALID, "paged_write: negative size (pool_rows %lld, widths %lld and %lld, rows %lld)",
                     (long long)pool_rows, (long long)k_width, (long long)v_width, (long long)rows);
+    if ((pool_rows | k_width | v_width | rows) >> 31)
+        return fail(VTMU_ERR_UNSUPPORTED, "paged_write: sizes must be below 2^31");
     if (rows == 0 || pool_rows == 0) return ok();
     if (!slots || (k_width > 0 && (!k_pool || !k_new)) || (v_width > 0 && (!v_pool || !v_new)))
         return fail(VTMU_ERR_INVALID, "paged_write: a pointer is NULL");

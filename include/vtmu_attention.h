@@ -531,7 +531,8 @@ VTMU_API vtmu_status vtmu_mla_decode_step_host(float* state, int64_t max_rows, c
  * writing its id at free_pages[*n_free_out] and counting one more (a finished
  * request's ids are the first ceil(lens[b] / page_size) of its table row).
  * Errors: VTMU_ERR_INVALID (null pointer, negative size, page_size or
- * max_pages < 1, a misaligned pointer, overlapping buffers), VTMU_ERR_CUDA.
+ * max_pages < 1, a misaligned pointer, overlapping buffers),
+ * VTMU_ERR_UNSUPPORTED (more than 65536 requests), VTMU_ERR_CUDA.
  */
 VTMU_API vtmu_status vtmu_page_map(const int32_t* lens, const int32_t* cu_rows, const uint64_t* accept,
                                    int32_t* block_table, const int32_t* free_pages, int64_t free_capacity,
@@ -575,7 +576,8 @@ VTMU_API vtmu_status vtmu_rope_at(const float* x, float* out, int64_t T, int32_t
  *     k_width], v_new [rows, v_width]: row-major f32, DEVICE; slots [rows]:
  *     int32, DEVICE.  None may overlap another.
  * Errors: VTMU_ERR_INVALID (null pointer with rows > 0, negative size,
- * misaligned or overlapping buffers), VTMU_ERR_CUDA.
+ * misaligned or overlapping buffers), VTMU_ERR_UNSUPPORTED (a size of 2^31 or
+ * more), VTMU_ERR_CUDA.
  */
 VTMU_API vtmu_status vtmu_paged_write(float* k_pool, float* v_pool, int64_t pool_rows, int64_t k_width,
                                       int64_t v_width, const float* k_new, const float* v_new,
@@ -636,7 +638,8 @@ VTMU_API vtmu_status vtmu_paged_workspace_size(const vtmu_paged_params* p, size_
  * own positions), or among the first `sinks` cache rows.  Scores are scale *
  * q.k, then softcap; the output is the max-subtracted softmax applied to the
  * values.  A row that sees no key is written as zeros; keys and values that a
- * row does not see do not enter it, whatever they hold.
+ * row does not see do not enter it, whatever they hold.  A score with a factor
+ * that is not finite may come out as NaN.
  *   q, out [rows, heads*headDim]; lens, cu_rows, block_table as for
  *   vtmu_page_map.  Rows behind the last request, and a request's rows past
  *   max_rows, are left as they were in out.  Lengths are clamped to 0 ..
