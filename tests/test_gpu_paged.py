@@ -581,3 +581,79 @@ def test_serving_loop(D):
         assert lens.cpu().tolist() == [len(x[0]) for x in dense]
     assert int(left) == pages - sum(-(-len(x[0]) // P) for x in dense)
     assert vtmu.vtmu_device_error() == 0
+
+
+# --------------------------------------------------------------- far corners
+@BOTH
+@pytest.mark.parametrize("c", [
+    ([100, 70], [64, 40], 64, 1, 128, 16, True, {}),     # 4096 virtual rows per KV head: four rounds of a team
+    ([100, 70], [64, 3], 71, 1, 64, 32, True, {}),        # a prime group
+    ([1300], [1100], 8, 1, 64, 64, False, {}),            # a prompt's chunk
+    ([40, 90], [3, 5], 130, 1, 128, 8, False, {}),        # more heads than a row block has rows
+])
+def test_many_virtual_rows(kernel, c):
+    run_case(c, kernel, seed=31)
+
+
+@BOTH
+@pytest.mark.parametrize("tree", [False, True])
+def test_a_window_beyond_every_position_is_none(kernel, tree):
+    d = ref.batch(32, [150, 20], [5, 9], tree=tree, **KW)
+    whole = attend(d, kernel=kernel, **KW)
+    for window in (1 << 20, (1 << 63) - 1):
+        assert np.array_equal(attend(d, kernel=kernel, window=window, sinks=3, **KW), whole)
+
+
+@BOTH
+def test_max_rows_far_above_the_rows(kernel):
+    d = ref.batch(33, [150, 20], [1, 1], **KW)
+    check(attend(d, kernel=kernel, maxRows=1 << 27, **KW), expect(d, **KW))
+
+
+def test_paged_write_of_one_slot_twice():
+    kp, vp = torch.zeros(4, 1024, device="cuda"), torch.zeros(4, 1024, device="cuda")
+    kn = torch.arange(1., 4., device="cuda")[:, None].expand(3, 1024).contiguous()
+    vtmu.paged_write(kp, vp, kn, -kn, dev(np.array([2, 2, 0], np.int32)))
+    k, v = kp.cpu().numpy(), vp.cpu().numpy()
+    assert np.all((k[2] == 1) | (k[2] == 2)) and np.all((v[2] == -1) | (v[2] == -2))
+    assert np.all(k[0] == 3) and np.all(v[0] == -3) and not k[[1, 3]].any() and not v[[1, 3]].any()
+
+
+def test_helpers_captured_and_replayed():
+    """page_map, tree_plan, rope_at and paged_write in one graph, replayed with another step's inputs."""
+    H, D, P, cols = 2, 64, 16, 6
+    kw = dict(rows=9, pageSize=P)
+    steps = [([5, 30], [0, 4, 9]), ([0, 47], [0, 1, 6])]
+    lens, cu = dev(np.zeros(2, np.int32)), dev(np.zeros(3, np.int32))
+    table0 = np.array([[0, 1, -1, -1, -1, -1], [2, 3, 4, -1, -1, -1]], np.int32)
+    table, free, n_free = dev(table0), dev(np.arange(5, 13, dtype=np.int32)), dev(np.array([8], np.int32))
+    parents = dev(np.array([-1, 0, 0, 1, -1, 0, 1, 2, 3], np.int32))
+    x = torch.randn(9, H * D, device="cuda")
+    kp, vp = torch.zeros(13 * P, H * D, device="cuda"), torch.zeros(13 * P, H * D, device="cuda")
+
+    def step():
+        slots, pos, new, left = vtmu.page_map(lens, cu, table, free, n_free, **kw)
+        masks, tpos = vtmu.tree_plan(parents, cu, lens)
+        turned = vtmu.rope_at(x, pos, headDim=D, out=x.clone())
+        vtmu.paged_write(kp, vp, turned, x, slots)
+        return slots, pos, new, left, masks, tpos, turned
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        got = step()
+    for l, c in steps + steps[:1]:
+        lens.copy_(dev(np.array(l, np.int32)))
+        cu.copy_(dev(np.array(c, np.int32)))
+        outs, pools = [], []
+        for run in (step, lambda: (g.replay(), got)[1]):
+            table.copy_(dev(table0))
+            kp.zero_()
+            vp.zero_()
+            outs.append([t.cpu().numpy() for t in run()])
+            pools.append((kp.cpu().numpy(), vp.cpu().numpy(), table.cpu().numpy()))
+        for a, b in zip(outs[0] + list(pools[0]), outs[1] + list(pools[1])):
+            assert np.array_equal(a, b)
+        want = ref.page_map(l, c, table0, np.arange(5, 13), 8, 9, P)
+        assert np.array_equal(outs[0][0], want[0]) and np.array_equal(pools[0][2], want[4])
