@@ -1113,17 +1113,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const int2 group = group_at[k & 1];
             const int nb = group.x % kRing, ne = group.y % kRing;
-            const int rows = tile_at[nb].x & (kFirst - 1);
-            const bool first = tile_at[nb].x & kFirst, last = tile_at[ne].x & kLast;
+            static_assert(kGroup <= 2, "nb and ne are all of the group's tiles");
+            const int flags = tile_at[nb].x, flags_e = tile_at[ne].x, rows = flags & (kFirst - 1);
+            const bool first = flags & kFirst, last = flags_e & kLast;
             if (32 * w < rows) {
                 const float2 f = group_tag[nb][w] == group.x + 1 ? fold_f[nb][i] : make_float2(1.f, 1.f);
                 const float fin = last ? row_inv[ne][i] * kUnscale : 1.f;
                 const bool plain = __all_sync(FULL, (first || f.x == 1.f) && f.y == 1.f && !last);
                 const uint64_t fx = f2_pack(f.x, f.x), fy = f2_pack(f.y, f.y), fin2 = f2_pack(fin, fin);
                 const uint32_t at = tmem + lanes + C::kColO;
-                int bad = 0;
-                for (int j = group.x; j <= group.y; ++j) bad |= tile_at[j % kRing].x;
-                if (bad & kBad)  // rare
+                if ((flags | flags_e) & kBad)  // rare
                     for (int j = group.x; j <= group.y; ++j) {
                         const uint64_t mask = g.odd_rows[((int64_t)blockIdx.x * kRing + j % kRing) * kM + i];
                         if ((tile_at[j % kRing].x & kBad) && i < rows && mask)
@@ -1136,6 +1135,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32(at + c0, x);
                     if (!first) tmem_ld32(at + (C::kColAcc - C::kColO) + c0, y);
                     tmem_wait_ld();
+                    if (c0 == D - 32) {  // the accumulator, and what the group left in shared memory, have been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&o_free);
+                    }
                     if (plain) {
                         if (!first) {
 #pragma unroll
@@ -1160,11 +1164,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tmem_wait_st();
                 if (last && odd) odd = join_odd_values(to, g.odd + ((int64_t)blockIdx.x * kM + i) * D, D);
-                tc_fence_before();
+            } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_free);
             }
             if (last) to = next_to;
-            __syncwarp();  // after everything that the group left in shared memory has been read
-            if (lane == 0) mbar_arrive(&o_free);
             return group.y + 1;
         };
         auto next_piece = [&]() -> bool {  // the next one that has tiles
