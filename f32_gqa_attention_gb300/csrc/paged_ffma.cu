@@ -15,8 +15,8 @@
 // are known to the device alone, and this kernel needs no workspace.  Where both
 // kernels cover a call the tensor cores win at every size measured: one token
 // of a chat of 211 rows 36.9 us here and 28 there, small trees 99 and 32, one row
-// for each of 32 requests of up to 8111 rows 2134 and 258, trees of 64 rows on 8
-// requests of up to 32704 72.9 ms and 0.65.  Bound by the lanes' scattered reads of
+// for each of 32 requests of up to 8111 rows 2134 and 255, trees of 64 rows on 8
+// requests of up to 32704 72.9 ms and 0.60.  Bound by the lanes' scattered reads of
 // key rows and by the few CTAs of a small batch.
 #include "attn_common.cuh"
 #include "kernels.h"

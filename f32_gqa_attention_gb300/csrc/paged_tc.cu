@@ -47,11 +47,12 @@
 // Every wait is bounded; a wait that gives up sets a bit of the device flag.
 //
 // Measured, headDim 128, 32 heads over 8: one row for each of 32 requests of 517 to 8111
-// rows, pages of 16: 258 us for 1.176 GB, 4.6 TB/s (67 % of the copy rate).  Trees
-// of 64 rows on 8 requests of 16384 to 32704, pages of 64: 647 us for 217 GFLOP,
-// 335 TFLOP/s of f32 products, 52 % of a third of the f16 rate.  What bounds it: a
-// tile's softmax is one thread per row, about 2000 cycles with its hand-overs
-// against 1540 of MMAs, and at a group's end P.V waits for the fold.
+// rows, pages of 16: 250-275 us for 1.176 GB, 4.3-4.7 TB/s (63-69 % of the copy
+// rate).  Trees of 64 rows on 8 requests of 16384 to 32704, pages of 64: 595-623 us
+// for 217 GFLOP, 348-364 TFLOP/s of f32 products, 54-56 % of a third of the f16 rate.
+// What bounds it: the chain P.V(n - 1), S(n + 1), softmax(n + 1) on two score buffers:
+// 1900-2300 cycles of softmax a tile, one thread per row, against 1540 of MMAs and
+// the hand-overs between them.
 #include <cstring>
 #include <mutex>
 
@@ -85,8 +86,9 @@ constexpr int kPShift = 11;    // probabilities are scaled by 2^11 in f16
 constexpr float kLazyLog2 = 4.f;  // and a row's reference maximum moves when beaten by more than 2^4: 2^15 at most
 // Tiles that one accumulator takes before it is folded.  The tensor cores round their sums
 // towards zero at every step: on 32 single-token requests the error against 64 bits is
-// 5.6e-7 with one tile, 7.8e-7 with two, 9.3e-7 with three, 1.1e-6 with four, at
-// 281, 258, 257 and 249 us.
+// 5.6e-7 with one tile, 7.8e-7 with two, 9.3e-7 with three, 1.1e-6 with four.  One tile
+// takes 2 % longer than two there (282 and 276 us side by side) and as long on large
+// trees; four were 4 % faster than two.
 constexpr int kGroup = 2;
 constexpr int kRing = 8;       // what a tile leaves for later roles
 static_assert(kRing >= kGroup + 2 && kRing >= 5 && (kRing & (kRing - 1)) == 0, "a slot outlives its last reader");
@@ -1135,7 +1137,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32(at + c0, x);
                     if (!first) tmem_ld32(at + (C::kColAcc - C::kColO) + c0, y);
                     tmem_wait_ld();
-                    if (c0 == D - 32) {  // the accumulator, and what the group left in shared memory, have been read
+                    // The accumulator, and what the group left in shared memory, have been read: the
+                    // next P.V need not wait for the rest (288 -> 275 us and 638 -> 590 us side by side).
+                    if (c0 == D - 32) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&o_free);
