@@ -1,8 +1,8 @@
 // paged.cu -- the small operators of the paged cache: page maps, plans of
 // drafted trees, op "rope" at given positions and op "cache_write" through a
 // slot map (op catalog, vtmu.mpakt.dev/api/ops, for the two ops' arithmetic).
-#include "kernels.h"
 #include "paged.cuh"
+#include "paged_kernels.h"
 #include "rope.cuh"
 
 namespace vtmu {

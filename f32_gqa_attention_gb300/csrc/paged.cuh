@@ -4,7 +4,7 @@
 
 #include <cstdint>
 
-#include "kernels.h"
+#include "paged_kernels.h"
 
 namespace vtmu {
 

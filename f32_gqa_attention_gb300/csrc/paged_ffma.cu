@@ -19,8 +19,8 @@
 // requests of up to 32704 72.9 ms and 0.60.  Bound by the lanes' scattered reads of
 // key rows and by the few CTAs of a small batch.
 #include "attn_common.cuh"
-#include "kernels.h"
 #include "paged.cuh"
+#include "paged_kernels.h"
 
 namespace vtmu {
 namespace {

@@ -61,9 +61,9 @@
 #include <cuda_fp16.h>
 
 #include "attn_common.cuh"
-#include "kernels.h"
 #include "launch_cache.h"
 #include "paged.cuh"
+#include "paged_kernels.h"
 #include "pdl.cuh"
 #include "softcap.cuh"
 #include "tcgen05_ops.cuh"

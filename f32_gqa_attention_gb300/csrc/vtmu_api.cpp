@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include "kernels.h"
+#include "paged_kernels.h"
 #include "vtmu_attention.h"
 
 namespace {

@@ -599,7 +599,8 @@ typedef struct vtmu_paged_params {
     int64_t rows;        /* packed query rows that the buffers hold (0 is a no-op) */
     int64_t pages;       /* pages of the pools */
     int32_t requests;    /* 1..1024 */
-    int32_t max_rows;    /* most rows of one request; with a tree at most 64 */
+    int32_t max_rows;    /* most rows of one request; with a tree at most 64.  A bound far above
+                            the rows that come costs time: work is laid out for it */
     int32_t page_size;   /* cache rows per page, > 0 */
     int32_t max_pages;   /* columns of the block table, > 0 */
     int32_t heads;       /* query heads, > 0 */

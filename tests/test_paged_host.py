@@ -153,6 +153,16 @@ def test_paged_write_refusals(lib, args, status, word):  # noqa: F811
     assert e.status == status and word in str(e), str(e)
 
 
+def test_other_kernels_do_not_include_the_paged_ones():
+    """The profiles that the bench quotes record the sources of their kernels, headers included."""
+    import glob
+    import os
+    csrc = os.path.join(os.path.dirname(vtmu.__file__), "csrc")
+    for path in glob.glob(os.path.join(csrc, "*")):
+        if not os.path.basename(path).startswith("paged") and path.endswith((".cu", ".cuh", ".h")):
+            assert '#include "paged' not in open(path).read(), path
+
+
 # -------------------------------------------------- the plain implementations
 def test_plain_tree_plan_by_hand():
     #    0 -> 1 -> 3, 0 -> 2, and a second root 4 -> 5
