@@ -136,7 +136,7 @@ struct Req {
 };
 struct Tiles {
     int lo_tile;  // first tile of the window's range
-    int n_sink;   // tiles of sinks before it
+    int n_sink;   // tiles of sinks before it, or all of them without a main tile
     int n_main;
     int nt;       // with the drafted rows' tile; at least 1 when there are rows
 };
@@ -155,8 +155,11 @@ __device__ __forceinline__ Tiles tiles_of(const PagedDesc& a, const Req& r) {
     int64_t lo = 0;
     if (a.window > 0) lo = clamp64((a.tree ? (int64_t)r.len : (int64_t)r.len - r.n) - a.window + 1, 0, r.len);
     t.lo_tile = (int)(lo / kKT);
-    t.n_sink = (int)min((min(a.sinks, (int64_t)r.len) + kKT - 1) / kKT, (int64_t)t.lo_tile);
     t.n_main = lo < r.len ? (r.len + kKT - 1) / kKT - t.lo_tile : 0;
+    // Where the window leaves nothing of the cache (a tree's, at most 1), no main tile holds
+    // the sinks of the cache's last tile.
+    const int64_t sink_tiles = (min(a.sinks, (int64_t)r.len) + kKT - 1) / kKT;
+    t.n_sink = (int)(t.n_main > 0 ? min(sink_tiles, (int64_t)t.lo_tile) : sink_tiles);
     t.nt = t.n_sink + t.n_main + a.tree;
     if (r.T == 0) t.nt = 0;
     else if (t.nt == 0) t.nt = 1;
