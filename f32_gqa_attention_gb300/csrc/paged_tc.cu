@@ -14,8 +14,10 @@
 // precision, and halves the bytes that the MMAs read from shared memory.  The
 // power is 2^6 for a row of K or V whose largest element lies in [2^-9, 2^9), and
 // one of its own for a row of Q and for any other row of K or V; those
-// multiply the scores and, brought to at most 1, the probabilities.  P has
-// 2^11 as a factor, so that f16 holds small ones too; l has it as well.  A
+// multiply the scores and the probabilities.  P has
+// 2^11 as a factor, so that f16 holds small ones too; l has it as well.  (A weight is so
+// kept to 2^-36 of the row's largest; in a tile with value rows that have a power of
+// their own, the product of weight and value to 2^-36 of the tile's largest one.)  A
 // row's reference maximum moves only when it is beaten by more than 2^4, so
 // that the output seldom needs to be multiplied by alpha.
 //
@@ -564,19 +566,14 @@ struct RowTile {
     uint64_t see;         // keys that the row sees (not read when WHOLE)
     float mul;            // a score of the MMA times this is one in base-2 units (the argument of tanh with a cap)
     float cap;            // softcap in base-2 units
-    const float* ks;      // SCALED: [64] key scales
 };
 
 // 32 scores from key 32 c on, masked, in base-2 units with a cap, else still to be
 // multiplied by r.mul (in the exponent's FMA).
-template <bool CAP, bool WHOLE, bool SCALED>
+template <bool CAP, bool WHOLE>
 __device__ __forceinline__ void row_scores(const RowTile& r, int c, float (&x)[32]) {
     tmem_ld32(r.at + 32 * c, x);
     tmem_wait_ld();
-    if constexpr (SCALED) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] *= r.ks[32 * c + k];
-    }
     if constexpr (CAP) softcap_tile<32>(x, r.mul, r.cap);
     if constexpr (!WHOLE) {
         const uint32_t bits = (uint32_t)(r.see >> (32 * c));
@@ -585,84 +582,134 @@ __device__ __forceinline__ void row_scores(const RowTile& r, int c, float (&x)[3
     }
 }
 
-// The online softmax's step: l and, where it is beaten, m move on; P (times 2^kPShift, which l has too)
-// goes over the scores (keys 32 c .. as f16 hi in 16 columns, lo in 16).
-// Returns alpha; `moved`: m, the row's reference, is another one now.  The scores are read twice, for the maximum and for the
-// probabilities: 64 of them do not fit the registers at once.
-template <bool CAP, bool WHOLE, bool SCALED>
-__device__ __forceinline__ float row_softmax(const RowTile& r, float& m, float& l, bool& moved) {
+// The online softmax's step in two passes over the scores (64 of them do not fit the
+// registers at once).  First the largest one, in base-2 units.
+template <bool CAP, bool WHOLE>
+__device__ __forceinline__ float row_max(const RowTile& r) {
     float mt = -INFINITY;
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
         float x[32];
-        row_scores<CAP, WHOLE, SCALED>(r, c, x);
+        row_scores<CAP, WHOLE>(r, c, x);
 #pragma unroll
         for (int k = 0; k < 32; k += 2) mt = fmaxf(fmaxf(mt, x[k]), x[k + 1]);
     }
-    const float mul = CAP ? 1.f : r.mul;
-    moved = mt * mul > m + kLazyLog2;
-    const float mn = moved ? mt * mul : m, mu = mn == -INFINITY ? 0.f : mn;
-    const float alpha = moved ? fast_exp2(m - mu) : 1.f;
-    m = mn;
-    const float shift = (float)kPShift - mu;
+    return CAP ? mt : mt * r.mul;
+}
+
+// 32 probabilities as f16 hi and lo over their scores' columns.
+__device__ __forceinline__ void store_probs(uint32_t at, const float (&phi)[16], const float (&plo)[16]) {
+    tmem_st16(at, phi);
+    tmem_st16(at + 16, plo);
+}
+__device__ __forceinline__ void split_probs(uint64_t p, float& hi, float& lo) {
+    uint32_t h, l;
+    split2(p, h, l);
+    hi = __uint_as_float(h);
+    lo = __uint_as_float(l);
+}
+
+// Then P = 2^(score - mu + kPShift), which goes over the scores (keys 32 c .. as f16 hi in
+// 16 columns, lo in 16).  Returns its sum.
+template <bool CAP, bool WHOLE>
+__device__ __forceinline__ float row_probs(const RowTile& r, float mu) {
+    const float mul = CAP ? 1.f : r.mul, shift = (float)kPShift - mu;
     const uint64_t mul2 = f2_pack(mul, mul), shift2 = f2_pack(shift, shift);
     uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
         float x[32];
-        row_scores<CAP, WHOLE, SCALED>(r, c, x);
+        row_scores<CAP, WHOLE>(r, c, x);
         float phi[16], plo[16];
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
             float e0, e1, e2, e3;
             f2_unpack(f2_fma(f2_pack(x[k], x[k + 1]), mul2, shift2), e0, e1);
             f2_unpack(f2_fma(f2_pack(x[k + 2], x[k + 3]), mul2, shift2), e2, e3);
-            uint64_t p0 = f2_pack(fast_exp2(e0), fast_exp2(e1)), p1 = f2_pack(fast_exp2(e2), fast_exp2(e3));
+            const uint64_t p0 = f2_pack(fast_exp2(e0), fast_exp2(e1)), p1 = f2_pack(fast_exp2(e2), fast_exp2(e3));
             sum0 = f2_add(sum0, p0);
             sum1 = f2_add(sum1, p1);
-            uint32_t h0, l0, h1, l1;
-            split2(p0, h0, l0);
-            split2(p1, h1, l1);
-            phi[k / 2] = __uint_as_float(h0);
-            phi[k / 2 + 1] = __uint_as_float(h1);
-            plo[k / 2] = __uint_as_float(l0);
-            plo[k / 2 + 1] = __uint_as_float(l1);
+            split_probs(p0, phi[k / 2], plo[k / 2]);
+            split_probs(p1, phi[k / 2 + 1], plo[k / 2 + 1]);
         }
-        tmem_st16(r.at + 32 * c, phi);
-        tmem_st16(r.at + 32 * c + 16, plo);
+        store_probs(r.at + 32 * c, phi, plo);
     }
     float a0, a1, b0, b1;
     f2_unpack(sum0, a0, a1);
     f2_unpack(sum1, b0, b1);
-    l = fmaf(l, alpha, (a0 + a1) + (b0 + b1));
-    return alpha;
+    return (a0 + a1) + (b0 + b1);
 }
 
-// P once more, each key's times weight[key] * mul: for a tile whose values have scales of
-// their own (rare).
-__device__ __noinline__ void row_reweigh(uint32_t at, const float* weight, float mul) {
-    tmem_wait_st();
+// The same two passes for a tile that has rows with scales of their own (rare).  Keys:
+// their scores times `ks` (null: keys without one).
+template <bool CAP>
+__device__ __forceinline__ void scaled_scores(const RowTile& r, const float* ks, int c, float (&x)[32]) {
+    tmem_ld32(r.at + 32 * c, x);
+    tmem_wait_ld();
+    if (ks) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] *= ks[32 * c + k];
+    }
+    if constexpr (CAP) {
+        softcap_tile<32>(x, r.mul, r.cap);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] *= r.mul;
+    }
+    const uint32_t bits = (uint32_t)(r.see >> (32 * c));
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = (bits >> k) & 1u ? x[k] : -INFINITY;
+}
+template <bool CAP>
+__device__ __noinline__ float scaled_max(const RowTile& r, const float* ks) {
+    float mt = -INFINITY;
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
-        float phi[16], plo[16];
-        tmem_ld16(at + 32 * c, phi);
-        tmem_ld16(at + 32 * c + 16, plo);
-        tmem_wait_ld();
+        float x[32];
+        scaled_scores<CAP>(r, ks, c, x);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const uint32_t h = __float_as_uint(phi[k]), l = __float_as_uint(plo[k]);
-            const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&l));
-            const float* w = weight + 32 * c + 2 * k;
-            uint32_t h2, l2;
-            // At most 1 for a key that is seen; one that is not may be larger, times p = 0.
-            split2(f2_pack((fh.x + fl.x) * fminf(w[0] * mul, 1.f), (fh.y + fl.y) * fminf(w[1] * mul, 1.f)), h2, l2);
-            phi[k] = __uint_as_float(h2);
-            plo[k] = __uint_as_float(l2);
-        }
-        tmem_st16(at + 32 * c, phi);
-        tmem_st16(at + 32 * c + 16, plo);
+        for (int k = 0; k < 32; ++k) mt = fmaxf(mt, x[k]);
     }
+    return mt;
+}
+// Values (`vs` their scales, powers of two; null: values without one): the products
+// p v decide, not the scales, since a value row of any size may weigh nothing, and one that
+// weighs little may count.  So P takes the exponent E of its value row's scale, less the
+// largest (score - mu + E) of the keys that are seen, rounded up: `lift`, which the
+// tile's output gets back.  The sum of the probabilities has no part in it.
+template <bool CAP>
+__device__ __noinline__ float scaled_probs(const RowTile& r, const float* ks, const float* vs, float mu, float* lift) {
+    auto exponent = [&](int k) -> float { return (float)((int)(__float_as_uint(vs[k]) >> 23) - 127); };
+    float top = 0.f;
+    if (vs) {
+        top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+            float x[32];
+            scaled_scores<CAP>(r, ks, c, x);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) top = fmaxf(top, (x[k] - mu) + exponent(32 * c + k));
+        }
+        top = ceilf(fmaxf(top, -300.f));  // nothing seen: any number does
+    }
+    *lift = top;
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+        float x[32], phi[16], plo[16];
+        scaled_scores<CAP>(r, ks, c, x);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            const float e0 = (x[k] - mu) + (float)kPShift, e1 = (x[k + 1] - mu) + (float)kPShift;
+            const float p0 = fast_exp2(e0), p1 = fast_exp2(e1);
+            sum += p0 + p1;
+            split_probs(vs ? f2_pack(fast_exp2(e0 + (exponent(32 * c + k) - top)), fast_exp2(e1 + (exponent(32 * c + k + 1) - top)))
+                           : f2_pack(p0, p1),
+                        phi[k / 2], plo[k / 2]);
+        }
+        store_probs(r.at + 32 * c, phi, plo);
+    }
+    return sum;
 }
 
 // ---- the kernel -------------------------------------------------------------------------
@@ -958,19 +1005,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 rt.see = ~0ull;
                 rt.mul = q_scale[piece & 3][i] * kUnscale;
                 rt.cap = a.cap_log2;
-                rt.ks = k_scale[nb];
                 if (!all) rt.see = tile_mask(a, s, key, hi, lo, sinks, p, t);
-                float alpha;
-                bool moved;
+                const float* ks = nullptr;
+                float mt;
                 if (*reinterpret_cast<const uint32_t*>(rescued[nb][0])) {  // rare
+                    ks = k_scale[nb];
                     rt.mul *= kScale;
-                    alpha = row_softmax<CAP, false, true>(rt, m, l, moved);
-                } else if (whole) {
-                    alpha = row_softmax<CAP, true, false>(rt, m, l, moved);
+                    mt = scaled_max<CAP>(rt, ks);
                 } else {
-                    alpha = row_softmax<CAP, false, false>(rt, m, l, moved);
+                    mt = whole ? row_max<CAP, true>(rt) : row_max<CAP, false>(rt);
                 }
-                // Nothing above needs the values, which are often still to come.
+                // m, the row's reference, moves when it is beaten.
+                const bool moved = mt > m + kLazyLog2;
+                const float mn = moved ? mt : m, mu = mn == -INFINITY ? 0.f : mn;
+                const float alpha = moved ? fast_exp2(m - mu) : 1.f;
+                m = mn;
+                // The values' scales go into P.
                 if (!__all_sync(FULL, wait_for(&ready[v_slot], v_phase))) {
                     raise_device_error(&g_paged_device_error, kErrPgMma);
                     ok = false;
@@ -980,17 +1030,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v_slot = 1;
                     v_phase ^= 1;
                 }
-                int flags = rows;
                 const bool scaled = *reinterpret_cast<const uint32_t*>(rescued[nb][1]) != 0;
+                float lift = 0.f, sum;
+                if (ks || scaled)  // rare
+                    sum = scaled_probs<CAP>(rt, ks, scaled ? v_scale[nb] : nullptr, mu, &lift);
+                else
+                    sum = whole ? row_probs<CAP, true>(rt, mu) : row_probs<CAP, false>(rt, mu);
+                l = fmaf(l, alpha, sum);
+                int flags = rows;
                 // A tile with another reference or scale than the one before begins a group.
                 if (__any_sync(FULL, moved && alive) || scaled || was_scaled) {
                     float o_scale = 1.f;  // of the tile's output, times kScale
-                    if (scaled) {         // the largest value scale among the keys seen sets the probabilities'
-                        float top = 7.888609052210118e-31f;
-                        for (int k = 0; k < kKT; ++k)
-                            if ((rt.see >> k) & 1) top = fmaxf(top, v_scale[nb][k]);
-                        row_reweigh(rt.at, v_scale[nb], __uint_as_float(0x7f000000u - __float_as_uint(top)));
-                        o_scale = top * kScale;
+                    if (scaled) {
+                        o_scale = fast_exp2(lift) * kScale;
                         const uint64_t bad = bad_rows<D>(v_bad[nb]);
                         if (bad) {  // which of them the row sees, for the fold
                             g.odd_rows[((int64_t)blockIdx.x * kRing + nb) * kM + i] = alive ? bad & rt.see : 0;

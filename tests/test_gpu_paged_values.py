@@ -1,0 +1,98 @@
+"""Paged attention on rows of very different size, scores past what 16 bits hold and
+numbers that are not finite, on both kernels, against plain 64-bit implementations.
+
+Tolerance: NORM of test_gpu_paged in the 2-norm of a request's output.  It is for
+scores of up to 2^3; where a test's weights come from larger ones, a score x is off by
+at most 2^-20 sum |q k| scale, so its weight by that of itself: `far` adds 2^-20 |x|
+for keys that point along the query (sum |q k| scale = |x|)."""
+import numpy as np
+import pytest
+
+import paged_ref as ref
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from test_gpu_paged import BOTH, NORM, attend, expect, kw_of  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+# A row's context: inside one CTA, and cut into pieces by many.
+WHOLE, CUT = 130, 64 * 400 + 7
+
+
+def close(got, want, extra=0.0):
+    assert np.all(np.isfinite(got))
+    size = np.max(np.abs(want))
+    err = np.linalg.norm((got.astype(np.float64) - want) / size) / np.linalg.norm(want / size)
+    assert err <= NORM + extra, f"relative error {err:.3e}"
+
+
+def cache_rows(d, b, page):
+    s = np.arange(int(d["lens"][b]))
+    return d["table"][b, s // page].astype(np.int64) * page + s % page
+
+
+def aim(d, kw, b, key, log2_weight):
+    """Points the first KV head's key `key` of request b along row 0, head 0 of its query,
+    with a score of log2_weight * ln 2."""
+    D, page = kw["headDim"], kw["pageSize"]
+    q = d["q"][d["cu"][b], :D].astype(np.float64)
+    x = log2_weight * np.log(2.0)
+    d["k_pool"][cache_rows(d, b, page)[key], :D] = q * (x / (q @ q) * D ** 0.5)
+
+
+# ---------------------------------------------------------- values of any size
+@BOTH
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [WHOLE, CUT])
+@pytest.mark.parametrize("size", [1.0, 600.0, 1e4, 1e5, 1e6, 1e9, 1e20])
+def test_a_large_value_row_that_weighs_nothing(kernel, D, n, size):
+    """It is seen, and its product with its weight is far below the output."""
+    kw = kw_of(2, 2, D, 16)
+    d = ref.batch(41, [n, 40], [1, 1], **kw)
+    for b, key in ((0, 5), (0, 70), (1, 33)):
+        aim(d, kw, b, key, -120.0)
+        d["v_pool"][cache_rows(d, b, 16)[key], :D] *= np.float32(size)
+    close(attend(d, kernel=kernel, **kw), expect(d, **kw))
+
+
+@BOTH
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [WHOLE, CUT])
+@pytest.mark.parametrize("bits", [12, 20, 30, 60, 90])
+def test_a_large_value_row_whose_product_counts(kernel, D, n, bits):
+    """A weight of 2^-bits times a value of 2^bits: as large as the ordinary products."""
+    kw = kw_of(2, 2, D, 16)
+    d = ref.batch(42, [n, 40], [1, 1], **kw)
+    for b, key in ((0, 5), (0, 70), (1, 33)):
+        aim(d, kw, b, key, -float(bits))
+        d["v_pool"][cache_rows(d, b, 16)[key], :D] *= np.float32(2.0 ** bits)
+    close(attend(d, kernel=kernel, **kw), expect(d, **kw), extra=bits * np.log(2.0) * 2.0 ** -20)
+
+
+@BOTH
+@pytest.mark.parametrize("small", [1e-4, 1e-12, 1e-30])
+def test_a_tile_of_which_the_heaviest_key_has_a_small_value(kernel, small):
+    """One key takes nearly all of the weight and brings next to nothing."""
+    kw = kw_of(2, 2, 128, 16)
+    d = ref.batch(43, [WHOLE, 40], [1, 1], **kw)
+    for b, key in ((0, 0), (1, 0)):
+        aim(d, kw, b, key, 14.0)
+        d["v_pool"][cache_rows(d, b, 16)[key], :128] *= np.float32(small)
+    close(attend(d, kernel=kernel, **kw), expect(d, **kw), extra=14 * np.log(2.0) * 2.0 ** -20)
+
+
+@BOTH
+def test_large_value_rows_in_trees(kernel):
+    """Context and drafted rows of the trees, seen with weights of every size."""
+    kw = kw_of(8, 2, 128, 32)
+    d = ref.batch(44, [300, 70], [30, 64], tree=True, **kw)
+    g = np.random.default_rng(44)
+    for v, rows in ((d["v_pool"], len(d["v_pool"])), (d["tree"][1], len(d["q"]))):
+        v *= np.where(g.random((rows, 1)) < 0.1, 10.0 ** g.uniform(2, 6, (rows, 1)), 1.0).astype(np.float32)
+    got, want = attend(d, kernel=kernel, **kw), expect(d, **kw)
+    for t in range(94):  # row by row: the large ones do not hide the others
+        for h in range(8):
+            close(got[t, h * 128:(h + 1) * 128], want[t, h * 128:(h + 1) * 128], extra=2.0 ** -17)
