@@ -25,7 +25,7 @@
 // persistent CTA per SM and the CTAs divide the 64-key tiles of all (request,
 // KV head, row block) units evenly among themselves: CTA c takes tiles
 // [total c / n, total (c + 1) / n) of their concatenation.  A unit inside one
-// CTA is finished there; a unit cut by a boundary leaves partials (m, l, o) that
+// CTA is finished there; a unit cut by a boundary leaves partials (m, l, o / l) that
 // paged_merge_kernel joins by the log-sum-exp rule, always in the same order.
 // With more than 128 virtual rows per KV head, teams of R CTAs walk the same
 // tiles for R row blocks at the same time, so the tiles come from HBM once.
@@ -107,7 +107,7 @@ struct PgArgs {
     int32_t sub;         // rows per TMA box: min(page_size, 64)
     float* part_m;       // [2 CTAs][128]
     float* part_l;
-    float* part_o;       // [2 CTAs][128][D]
+    float* part_o;       // [2 CTAs][128][D], divided by l: of the output's size
     float* odd;          // [CTAs][128][D]: values that are not finite
     uint64_t* odd_rows;  // [CTAs][kRing][128]: such rows of a tile that a virtual row sees
     int4* head;          // [CTAs]: the unit that a CTA starts and others go on with
@@ -374,6 +374,11 @@ __device__ __forceinline__ void sts4(uint32_t at, uint32_t x, uint32_t y, uint32
 // global memory: rare). One pass over the tile instead of two: its shared-memory
 // traffic is what bounds the kernel.
 constexpr float kScale = 64.f, kUnscale = 1.f / 64.f, kTopMost = 512.f, kTopLeast = 1.f / 512.f;
+// The running output has the factors of P and V, 2^17, and up to 2^4 and the number of keys
+// more: from the first tile on whose largest product of weight and value passes 2^kBigLog2 a row's is
+// kept times kBigUnit, where the largest products, 2^132, fit and ordinary ones are far from the smallest
+// normal number.
+constexpr float kBigLog2 = 50.f, kBigUnit = 0x1p-64f;
 
 // 64 elements of a row of a tile (two blocks from `at` on, swizzled by sw = (row % 8)
 // 16) times kScale as f16: hi over the first block, lo over the second, in place:
@@ -427,7 +432,7 @@ __device__ __noinline__ float row_rescue(const float* row, int D, int half, bool
     }
     *odd = !(all < __int_as_float(0x7f800000));
     if (*odd && !values) t = 1.f;
-    t = fminf(fmaxf(t, 7.888609052210118e-31f), 8.507059173023462e37f);  // 2^-100 .. 2^126
+    t = fminf(fmaxf(t, 0x1p-125f), 0x1p126f);  // the scale and its inverse are normal numbers
     const uint32_t e = __float_as_uint(t) & 0x7f800000u;  // 2^E in f32; 2^-E is 0x7f000000 - e
     const float s = __uint_as_float(0x7f000000u - e);
     for (int c = 0; c < 8; ++c) {
@@ -738,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint8_t rescued[kRing][2][4];  // keys, values: a split warp's rows have a scale of their own
     __shared__ float q_scale[4][kM];             // by piece % 4
     __shared__ float2 fold_f[kRing][kM];         // alpha, output scale of such a tile
-    __shared__ float row_inv[kRing][kM];         // last tile of a piece: 1 / l, or 1
+    __shared__ float row_inv[kRing][kM];         // last tile of a piece: 1 / l
     __shared__ __align__(16) int group_tag[kRing][4];  // by softmax warp, n + 1: tile n begins a group, its fold_f counts
     __shared__ int2 group_at[2];                 // a group's first and last tile
     __shared__ int4 tile_at[kRing];              // rows of the block (kFirst, kLast, kBad), request, first key, KV head
@@ -981,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int hi = a.tree ? s.len - 1 : min(p, s.len - 1);
             const int lo = a.window > 0 ? (int)max((int64_t)p - a.window + 1, (int64_t)0) : 0;
             const int sinks = (int)min(a.sinks, (int64_t)s.len);
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, unit = 1.f;  // of the running output: 1 or kBigUnit
             bool was_scaled = false;
             const int rows = min(s.T * a.G - s.rb * kM, kM);
             const int u0 = s.u0, u1 = s.u1, n_sink = s.n_sink, n_ctx = s.n_ctx, lo_tile = s.lo_tile;
@@ -1018,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // m, the row's reference, moves when it is beaten.
                 const bool moved = mt > m + kLazyLog2;
                 const float mn = moved ? mt : m, mu = mn == -INFINITY ? 0.f : mn;
-                const float alpha = moved ? fast_exp2(m - mu) : 1.f;
+                float alpha = moved ? fast_exp2(m - mu) : 1.f;
                 m = mn;
                 // The values' scales go into P.
                 if (!__all_sync(FULL, wait_for(&ready[v_slot], v_phase))) {
@@ -1039,10 +1044,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = fmaf(l, alpha, sum);
                 int flags = rows;
                 // A tile with another reference or scale than the one before begins a group.
-                if (__any_sync(FULL, moved && alive) || scaled || was_scaled) {
-                    float o_scale = 1.f;  // of the tile's output, times kScale
+                if (__any_sync(FULL, (moved && alive) || unit != 1.f) || scaled || was_scaled) {
+                    if (lift > kBigLog2 && unit == 1.f) alpha *= unit = kBigUnit;
+                    float o_scale = unit;  // of the tile's output, times kScale
                     if (scaled) {
-                        o_scale = fast_exp2(lift) * kScale;
+                        // Below 2^-126 the tile's output is lost, as its sums would be.
+                        o_scale = fast_exp2(lift + (unit == 1.f ? 6.f : -58.f));
+                        static_assert(kScale == 64.f && kBigUnit == 0x1p-64f, "their exponents");
                         const uint64_t bad = bad_rows<D>(v_bad[nb]);
                         if (bad) {  // which of them the row sees, for the fold
                             g.odd_rows[((int64_t)blockIdx.x * kRing + nb) * kM + i] = alive ? bad & rt.see : 0;
@@ -1056,14 +1064,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (u == u0) flags += kFirst;
                 if (u == u1 - 1) {
                     flags += kLast;
-                    float inv = 1.f;
-                    if (s.slot < 0) {
-                        inv = l != 0.f ? 1.f / l : 0.f;
-                    } else {
+                    if (s.slot >= 0) {
                         g.part_m[prow] = m;
                         g.part_l[prow] = l;
                     }
-                    row_inv[nb][i] = inv;
+                    row_inv[nb][i] = l != 0.f ? 1.f / l / unit : 0.f;
                 }
                 if (i == 0) tile_at[nb] = make_int4(flags, s.b, key, s.hk);
                 tmem_wait_st();
@@ -1299,7 +1304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partials of the unit that CTA blockIdx.x started and its team's
-// successors went on with: m* = max m_i, out = sum 2^(m_i - m*) o_i / sum 2^(m_i - m*) l_i.
+// successors went on with: m* = max m_i, out = sum w_i o_i / sum w_i, w_i = 2^(m_i - m*) l_i,
+// o_i the pieces' own outputs, so that nothing on the way is larger than they are.
 // A warp per virtual row.  Its launch overlaps the pieces' kernel; it reads at most
 // 20 MB of partials out of L2 and is a few microseconds of any call.
 template <int D>
@@ -1320,35 +1326,34 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PgArgs g) {
     for (int k = lane; k < count; k += 32) m = fmaxf(m, __ldcg(g.part_m + slot_row(k)));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, off));
+    auto weight = [&](int k) -> float {  // piece k's
+        if (k >= count) return 0.f;
+        const float mi = __ldcg(g.part_m + slot_row(k));
+        return mi != -INFINITY ? fast_exp2(mi - m) * __ldcg(g.part_l + slot_row(k)) : 0.f;
+    };
+    float den = 0.f;
+    for (int k = lane; k < count; k += 32) den += weight(k);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(FULL, den, off);
+    const float inv = den != 0.f ? 1.f / den : 0.f;
     constexpr int kPer = D / 32;
-    float acc[kPer], den = 0.f;
+    float acc[kPer];
 #pragma unroll
     for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
     for (int k0 = 0; k0 < count; k0 += 32) {
-        float wgt = 0.f, ll = 0.f;
-        if (k0 + lane < count) {
-            const float mi = __ldcg(g.part_m + slot_row(k0 + lane));
-            if (mi != -INFINITY) {  // a piece that saw nothing has no output to read
-                wgt = fast_exp2(mi - m);
-                ll = wgt * __ldcg(g.part_l + slot_row(k0 + lane));
-            }
-        }
-        den += ll;
+        const float wgt = weight(k0 + lane) * inv;
         const int here = min(count - k0, 32);
         for (int k = 0; k < here; ++k) {
             const float f = __shfl_sync(FULL, wgt, k);
-            if (f == 0.f) continue;
+            if (f == 0.f) continue;  // a piece that saw nothing has no output to read
             const float* src = g.part_o + slot_row(k0 + k) * D;
 #pragma unroll
             for (int c = 0; c < kPer; ++c) acc[c] = fmaf(f, __ldcg(src + lane + 32 * c), acc[c]);
         }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(FULL, den, off);
-    const float inv = den != 0.f ? 1.f / den : 0.f;
     float* out = a.out + (((int64_t)r.row0 + v / a.G) * a.H + (int64_t)hk * a.G + v % a.G) * D;
 #pragma unroll
-    for (int c = 0; c < kPer; ++c) out[lane + 32 * c] = acc[c] * inv;
+    for (int c = 0; c < kPer; ++c) out[lane + 32 * c] = acc[c];
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 pg_encoder() {

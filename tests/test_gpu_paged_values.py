@@ -14,7 +14,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
-from test_gpu_paged import BOTH, NORM, attend, expect, kw_of  # noqa: E402
+from test_gpu_paged import BOTH, NORM, TENSOR, attend, check, expect, kw_of  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +96,62 @@ def test_large_value_rows_in_trees(kernel):
     for t in range(94):  # row by row: the large ones do not hide the others
         for h in range(8):
             close(got[t, h * 128:(h + 1) * 128], want[t, h * 128:(h + 1) * 128], extra=2.0 ** -17)
+
+
+# ----------------------------------------------------- values at f32's far end
+@BOTH
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [30, 60])
+@pytest.mark.parametrize("size", [1e30, 1e33, 1e36])
+def test_values_near_the_largest(kernel, D, n, size):
+    """At most 60 keys and |N(0, 1)| below 4.5: sums of weights times values stay below 2.7e38."""
+    kw = kw_of(4, 2, D, 16)
+    d = ref.batch(45, [n], [2], **kw)
+    d["v_pool"] = np.clip(d["v_pool"], -4.5, 4.5) * np.float32(size)
+    close(attend(d, kernel=kernel, **kw), expect(d, **kw))
+
+
+@BOTH
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [1e-30, 1e-34, 1e-36])
+def test_values_near_the_smallest(kernel, D, size):
+    """Products of weights and values go down to 2^-149 in steps of that: below 2^-24 of these outputs."""
+    kw = kw_of(4, 2, D, 16)
+    d = ref.batch(53, [WHOLE, 40], [2, 1], **kw)
+    d["v_pool"] *= np.float32(size)
+    close(attend(d, kernel=kernel, **kw), expect(d, **kw))
+
+
+@pytest.mark.parametrize("size", [1e30, 1e33, 1e37])
+def test_values_near_the_largest_on_many_tiles(size):
+    """The tensor cores' sums are kept in units that such values fit, whatever their number;
+    ordinary rows come before and after."""
+    kw = kw_of(4, 2, 64, 64)
+    d = ref.batch(46, [CUT, 300], [2, 2], **kw)
+    rows = cache_rows(d, 0, 64)
+    d["v_pool"][rows[1000:9000]] = np.clip(d["v_pool"][rows[1000:9000]], -4.5, 4.5) * np.float32(size)
+    close(attend(d, kernel=TENSOR, **kw)[:2], expect(d, **kw)[:2])
+    check(attend(d, kernel=TENSOR, **kw)[2:], expect(d, **kw)[2:])
+
+
+@BOTH
+@pytest.mark.parametrize("n", [WHOLE, CUT])
+@pytest.mark.parametrize("weight", [-100.0, -200.0])
+def test_the_largest_values_with_a_negligible_weight(kernel, n, weight):
+    kw = kw_of(2, 2, 128, 16)
+    d = ref.batch(47, [n, 40], [1, 1], **kw)
+    for b, key in ((0, 5), (0, 70), (1, 33)):
+        aim(d, kw, b, key, weight)
+        d["v_pool"][cache_rows(d, b, 16)[key], :128] = np.float32(1e37)
+    close(attend(d, kernel=kernel, **kw), expect(d, **kw), extra=-weight * np.log(2.0) * 2.0 ** -20)
+
+
+def test_a_large_row_that_later_keys_leave_behind():
+    """It sets the units of the running sum, then rising scores take its weight away."""
+    kw = kw_of(2, 2, 128, 64)
+    d = ref.batch(48, [64 * 6], [1], **kw)
+    aim(d, kw, 0, 3, 10.0)
+    d["v_pool"][cache_rows(d, 0, 64)[3], :128] *= np.float32(2.0 ** 100)
+    for i, bits in enumerate((60.0, 110.0, 160.0)):
+        aim(d, kw, 0, 64 * (i + 2) + 9, bits)
+    close(attend(d, kernel=TENSOR, **kw), expect(d, **kw), extra=160 * np.log(2.0) * 2.0 ** -20)
