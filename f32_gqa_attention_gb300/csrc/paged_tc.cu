@@ -85,6 +85,7 @@ constexpr int kThreads = 640;
 constexpr int kFoldWarp = 4, kSoftmaxWarp = 8, kSplitWarp = 12, kFoldWarps = 4;
 constexpr int kFirst = 1 << 16, kLast = 1 << 17, kBad = 1 << 18;  // a piece's first and last tile; values that are not finite
 constexpr int kPShift = 11;    // probabilities are scaled by 2^11 in f16
+constexpr float kFar = 0x1p20f;  // base-2 scores from here on take the exact route
 constexpr float kLazyLog2 = 4.f;  // and a row's reference maximum moves when beaten by more than 2^4: 2^15 at most
 // Tiles that one accumulator takes before it is folded.  The tensor cores round their sums
 // towards zero at every step: on 32 single-token requests the error against 64 bits is
@@ -645,8 +646,8 @@ __device__ __forceinline__ float row_probs(const RowTile& r, float mu) {
     return (a0 + a1) + (b0 + b1);
 }
 
-// The same two passes for a tile that has rows with scales of their own (rare).  Keys:
-// their scores times `ks` (null: keys without one).
+// The same two passes for a tile that has rows with scales of their own, or for rows
+// with a far reference (both rare).  Keys: their scores times `ks` (null: keys without one).
 template <bool CAP>
 __device__ __forceinline__ void scaled_scores(const RowTile& r, const float* ks, int c, float (&x)[32]) {
     tmem_ld32(r.at + 32 * c, x);
@@ -1036,8 +1037,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v_phase ^= 1;
                 }
                 const bool scaled = *reinterpret_cast<const uint32_t*>(rescued[nb][1]) != 0;
+                // kPShift - mu rounds to a multiple that grows with mu: from 2^24 on P would
+                // leave f16.  Past kFar the difference to mu comes before kPShift.
+                const bool far = __any_sync(FULL, fabsf(mu) > kFar);
                 float lift = 0.f, sum;
-                if (ks || scaled)  // rare
+                if (ks || scaled || far)  // rare
                     sum = scaled_probs<CAP>(rt, ks, scaled ? v_scale[nb] : nullptr, mu, &lift);
                 else
                     sum = whole ? row_probs<CAP, true>(rt, mu) : row_probs<CAP, false>(rt, mu);

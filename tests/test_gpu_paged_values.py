@@ -155,3 +155,42 @@ def test_a_large_row_that_later_keys_leave_behind():
     for i, bits in enumerate((60.0, 110.0, 160.0)):
         aim(d, kw, 0, 64 * (i + 2) + 9, bits)
     close(attend(d, kernel=TENSOR, **kw), expect(d, **kw), extra=160 * np.log(2.0) * 2.0 ** -20)
+
+
+# ------------------------------------------------------------------ far scores
+def best_key_leads(d, D, cap):
+    """True where in every row the best score leads the runner-up by more than 2^10, and by
+    more than 2^-17 of itself, which no rounding of a score turns round."""
+    for b in range(len(d["lens"])):
+        k = d["k_pool"][cache_rows(d, b, 16)].astype(np.float64)
+        for t in range(int(d["cu"][b]), int(d["cu"][b + 1])):
+            lim = len(k) - (int(d["cu"][b + 1]) - 1 - t)
+            for h in range(4):
+                x = k[:lim, (h // 2) * D:(h // 2 + 1) * D] @ d["q"][t, h * D:(h + 1) * D].astype(np.float64) * D ** -0.5
+                x = np.unique(cap * np.tanh(x / cap) if cap else x)
+                if not x[-1] - x[-2] > max(2.0 ** 10, 2.0 ** -17 * abs(x[-1])):
+                    return False
+    return True
+
+
+@BOTH
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [50, CUT])
+@pytest.mark.parametrize("q_size,k_size", [
+    (2e3, 1e3), (3e3, 2e3), (3e3, 4e3), (5e3, 5e3), (1e4, 1e4), (5e5, 20.0), (1e7, 40.0), (1e15, 1e15), (1e30, 1.0)])
+@pytest.mark.parametrize("capped", [False, True])
+def test_far_scores_take_one_key(kernel, D, n, q_size, k_size, capped):
+    """Scores of q_size * k_size: the output is the value of the best key, half of each where
+    two keys are the same (some are, in one tile, in two and in two pieces of a unit)."""
+    kw = kw_of(4, 2, D, 16)
+    d = ref.batch(49, [n, 40], [2, 1], **kw)
+    d["q"] *= np.float32(q_size)
+    d["k_pool"] *= np.float32(k_size)
+    for b, i, j in ((0, 7, 33), (0, 9, n - 5), (1, 2, 35)):
+        rows = cache_rows(d, b, 16)
+        d["k_pool"][rows[i]] *= np.float32(3)
+        d["k_pool"][rows[j]] = d["k_pool"][rows[i]]
+    if capped:  # a cap that the scores do not come near
+        kw["softcap"] = 1e3 * q_size * k_size
+    assert best_key_leads(d, D, kw.get("softcap"))
+    close(attend(d, kernel=kernel, **kw), expect(d, **kw))
