@@ -201,14 +201,12 @@ __global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm[w][r]);
         float den = 0.f, acc = 0.f;
-        if (mx != -INFINITY) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (sm[w][r] == -INFINITY) continue;
-                const float f = exp2f(sm[w][r] - mx);
-                den = fmaf(sl[w][r], f, den);
-                acc = fmaf(so[w][r][d], f, acc);
-            }
+        for (int w = 0; w < kWarps; ++w) {
+            if (sl[w][r] == 0.f) continue;  // nothing seen; NaN scores leave the maximum at -inf, but not l at 0
+            const float f = exp2f(sm[w][r] - mx);
+            den = fmaf(sl[w][r], f, den);
+            acc = fmaf(so[w][r][d], f, acc);
         }
         a.out[((pr.row0 + v / a.G) * a.H + (int64_t)hk * a.G + v % a.G) * D + d] = den != 0.f ? acc / den : 0.f;
     }

@@ -1330,10 +1330,9 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PgArgs g) {
     for (int k = lane; k < count; k += 32) m = fmaxf(m, __ldcg(g.part_m + slot_row(k)));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, off));
-    auto weight = [&](int k) -> float {  // piece k's
-        if (k >= count) return 0.f;
-        const float mi = __ldcg(g.part_m + slot_row(k));
-        return mi != -INFINITY ? fast_exp2(mi - m) * __ldcg(g.part_l + slot_row(k)) : 0.f;
+    auto weight = [&](int k) -> float {  // piece k's; l, not m, tells that it saw nothing: NaN scores leave m at -inf
+        const float l = k < count ? __ldcg(g.part_l + slot_row(k)) : 0.f;
+        return l != 0.f ? fast_exp2(__ldcg(g.part_m + slot_row(k)) - m) * l : 0.f;
     };
     float den = 0.f;
     for (int k = lane; k < count; k += 32) den += weight(k);

@@ -194,3 +194,27 @@ def test_far_scores_take_one_key(kernel, D, n, q_size, k_size, capped):
         kw["softcap"] = 1e3 * q_size * k_size
     assert best_key_leads(d, D, kw.get("softcap"))
     close(attend(d, kernel=kernel, **kw), expect(d, **kw))
+
+
+# ------------------------------------------------------ numbers that are not finite
+@BOTH
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [WHOLE, CUT])
+@pytest.mark.parametrize("where", ["query", "a key", "an early key", "every key"])
+def test_nan_scores_make_their_rows_nan(kernel, D, n, where):
+    """Whether the row's unit is cut or not, and no other row or head."""
+    kw = kw_of(4, 2, D, 16)
+    d = ref.batch(50, [n, 90], [3, 2], **kw)
+    want = expect(d, **kw)
+    nan = np.zeros(want.shape, bool)
+    if where == "query":
+        d["q"][1, D + 3] = np.nan
+        nan[1, D:2 * D] = True
+    else:
+        rows = cache_rows(d, 0, 16)
+        rows = {"a key": rows[n - 40:n - 39], "an early key": rows[:1], "every key": rows}[where]
+        d["k_pool"][rows, D + 5] = np.nan
+        nan[:3, 2 * D:] = True
+    got = attend(d, kernel=kernel, **kw)
+    assert np.array_equal(np.isnan(got), nan)
+    check(np.where(nan, 0.0, got), np.where(nan, 0.0, want))
