@@ -9,9 +9,9 @@
 // the chunks of 32 keys in turn and are joined at the end by the log-sum-exp
 // rule.  Scores: lane = key, the lane reads its whole key row (served by L1
 // after the first touch of a line) against the kR queries in shared memory.
-// Values: lane = dims, one coalesced row per key; a key whose probability is
-// zero for all rows is not read, and one that is zero for a row does not
-// enter that row.  The keys of one request are not split over CTAs: lengths
+// Values: lane = dims, one coalesced row per key; a key that no row sees is not
+// read, and does not enter a row that does not see it: its probability there is -0,
+// which exp2f never gives (one that is seen counts, were its weight +0: 0 x inf).  The keys of one request are not split over CTAs: lengths
 // are known to the device alone, and this kernel needs no workspace.  Where both
 // kernels cover a call the tensor cores win at every size measured: one token
 // of a chat of 211 rows 36.9 us here and 28 there, small trees 99 and 32, one row
@@ -30,6 +30,7 @@ constexpr int kWarps = 8;
 constexpr int kMaxD = 256;
 constexpr int kPer = kMaxD / 32;
 constexpr unsigned FULL = 0xffffffffu;
+constexpr unsigned kUnseen = 0x80000000u;  // -0
 
 __device__ __forceinline__ float apply_cap(const PagedDesc& a, float dot) {
     return a.softcap_on ? a.cap_log2 * softcap_tanh(dot * a.qk_mul) : dot * a.qk_mul;
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc
             for (int off = 16; off > 0; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, off));
             const float mn = fmaxf(m[r], mt), mu = mn == -INFINITY ? 0.f : mn;
             const float alpha = exp2f(m[r] - mu);
-            p[r] = see[r] ? exp2f(x2 - mu) : 0.f;
+            p[r] = see[r] ? exp2f(x2 - mu) : -0.f;
             m[r] = mn;
             l[r] = fmaf(l[r], alpha, p[r]);  // this lane's keys
             if (alpha != 1.f) {
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
                 w[r] = __shfl_sync(FULL, p[r], kk);
-                need = need || w[r] != 0.f;  // a NaN weight is passed on
+                need = need || __float_as_uint(w[r]) != kUnseen;
             }
             const float* vr = reinterpret_cast<const float*>(
                 __shfl_sync(FULL, reinterpret_cast<unsigned long long>(vrow), kk));
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc
                     const float vv = __ldg(vr + d);
 #pragma unroll
                     for (int r = 0; r < kR; ++r)
-                        if (w[r] != 0.f) o[r][i] = fmaf(w[r], vv, o[r][i]);
+                        if (__float_as_uint(w[r]) != kUnseen) o[r][i] = fmaf(w[r], vv, o[r][i]);
                 }
             }
         }

@@ -1330,9 +1330,11 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PgArgs g) {
     for (int k = lane; k < count; k += 32) m = fmaxf(m, __ldcg(g.part_m + slot_row(k)));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, off));
-    auto weight = [&](int k) -> float {  // piece k's; l, not m, tells that it saw nothing: NaN scores leave m at -inf
+    // Piece k's; -0 where it saw nothing and left no output (l tells that, not m: NaN scores
+    // leave m at -inf).  A weight that comes to +0 counts: 0 x inf is NaN, as in the other rows.
+    auto weight = [&](int k) -> float {
         const float l = k < count ? __ldcg(g.part_l + slot_row(k)) : 0.f;
-        return l != 0.f ? fast_exp2(__ldcg(g.part_m + slot_row(k)) - m) * l : 0.f;
+        return l != 0.f ? fast_exp2(__ldcg(g.part_m + slot_row(k)) - m) * l : -0.f;
     };
     float den = 0.f;
     for (int k = lane; k < count; k += 32) den += weight(k);
@@ -1348,7 +1350,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PgArgs g) {
         const int here = min(count - k0, 32);
         for (int k = 0; k < here; ++k) {
             const float f = __shfl_sync(FULL, wgt, k);
-            if (f == 0.f) continue;  // a piece that saw nothing has no output to read
+            if (__float_as_uint(f) == 0x80000000u) continue;
             const float* src = g.part_o + slot_row(k0 + k) * D;
 #pragma unroll
             for (int c = 0; c < kPer; ++c) acc[c] = fmaf(f, __ldcg(src + lane + 32 * c), acc[c]);

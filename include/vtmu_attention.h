@@ -641,7 +641,8 @@ VTMU_API vtmu_status vtmu_paged_workspace_size(const vtmu_paged_params* p, size_
  * values.  A row that sees no key is written as zeros; keys and values that a
  * row does not see do not enter it, whatever they hold.  A NaN in a row's
  * query, or in a key that it sees, makes that head of the row NaN; other
- * scores that are not finite may do so.
+ * scores that are not finite may do so.  A value that is not finite makes its
+ * column of the rows that see it not finite, whatever its weight.
  *   q, out [rows, heads*headDim]; lens, cu_rows, block_table as for
  *   vtmu_page_map.  Rows behind the last request, and a request's rows past
  *   max_rows, are left as they were in out.  Lengths are clamped to 0 ..

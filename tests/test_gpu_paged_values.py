@@ -201,10 +201,12 @@ def test_far_scores_take_one_key(kernel, D, n, q_size, k_size, capped):
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("n", [WHOLE, CUT])
 @pytest.mark.parametrize("where", ["query", "a key", "an early key", "every key"])
-def test_nan_scores_make_their_rows_nan(kernel, D, n, where):
+@pytest.mark.parametrize("softcap", [None, 3.0])
+def test_nan_scores_make_their_rows_nan(kernel, D, n, where, softcap):
     """Whether the row's unit is cut or not, and no other row or head."""
     kw = kw_of(4, 2, D, 16)
     d = ref.batch(50, [n, 90], [3, 2], **kw)
+    kw["softcap"] = softcap
     want = expect(d, **kw)
     nan = np.zeros(want.shape, bool)
     if where == "query":
@@ -218,3 +220,25 @@ def test_nan_scores_make_their_rows_nan(kernel, D, n, where):
     got = attend(d, kernel=kernel, **kw)
     assert np.array_equal(np.isnan(got), nan)
     check(np.where(nan, 0.0, got), np.where(nan, 0.0, want))
+
+
+@BOTH
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [WHOLE, CUT])
+@pytest.mark.parametrize("weight", [-20.0, -400.0])
+@pytest.mark.parametrize("others", [False, True])
+def test_a_value_that_is_not_finite_counts_whatever_its_weight(kernel, D, n, weight, others):
+    """Its column of the row that sees it is not finite, whether the unit is cut or not."""
+    kw = kw_of(2, 2, D, 16)
+    d = ref.batch(51, [n, 40], [2, 1], **kw)
+    for key in (*range(min(n - 20, 1000) if others else 0), 5, n - 1):  # whole tiles and pieces with it; the last key
+        aim(d, kw, 0, key, weight)                                        # is the second row's alone
+    want = expect(d, **kw)
+    d["v_pool"][cache_rows(d, 0, 16)[5], 9] = np.inf
+    d["v_pool"][cache_rows(d, 0, 16)[n - 1], 11] = np.nan
+    lost = np.zeros(want.shape, bool)
+    lost[:2, 9] = lost[1, 11] = True
+    got = attend(d, kernel=kernel, **kw)
+    assert np.array_equal(~np.isfinite(got), lost)
+    extra = -weight * np.log(2.0) * 2.0 ** -20
+    close(np.where(lost, 0.0, got), np.where(lost, 0.0, want), extra=extra)
