@@ -492,32 +492,91 @@ def make_rope_params(*, headDim, base=None, rotaryDim=None, interleaved=False, s
     return r
 
 
+_HERE = contextlib.nullcontext()
+WORKSPACE_HEADER_BYTES = 64 << 10  # the decode kernels' arrival counters, zero between calls
+
+
+def _on(device):
+    """The device as the current one; nothing to do where it is (the usual case)."""
+    import torch
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _raw_stream(device) -> int:
+    """The device's current stream as the library takes it."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _at(device, stream: int):
+    """The stream as torch's current one."""
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
+                             else torch.cuda.default_stream(device))
+
+
 class Workspace:
     """A zero-initialised device scratch buffer (torch-allocated) that grows
-    on demand.  One per concurrent stream."""
+    on demand.  One per concurrent stream, and one for each captured graph
+    whose replays may overlap other calls.  Inside a capture it does not grow:
+    a call that needs more gets a buffer of the graph's own.  A buffer that a
+    graph was captured with stays allocated as long as the Workspace."""
 
     def __init__(self, device=None):
         import torch
         self.device = torch.device("cuda") if device is None else torch.device(device)
         self.buf = None
+        self._captured = False  # a graph holds buf's address
+        self._kept = []
 
     def get(self, nbytes: int):
         import torch
         if nbytes == 0:
             return None, 0
+        capturing = torch.cuda.is_current_stream_capturing()
         if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            if capturing:
+                return _graph_scratch(self.device, nbytes)
+            if self._captured:
+                self._kept.append(self.buf)
+            self.buf, self._captured = torch.zeros(nbytes, dtype=torch.uint8, device=self.device), False
+        self._captured = self._captured or capturing
         return self.buf, self.buf.numel()
 
 
-_ws = {}
+def _graph_scratch(device, nbytes: int):
+    """A buffer out of the memory of the graph that is being captured, its counters cleared
+    by the graph.  Given back at the end of the call, it serves later calls on the stream."""
+    import torch
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    buf[:WORKSPACE_HEADER_BYTES].zero_()
+    return buf, nbytes
 
 
-def _default_workspace(device):
-    key = (device.type, device.index)
-    if key not in _ws:
-        _ws[key] = Workspace(device)
-    return _ws[key]
+_ws = threading.local()  # per host thread: two threads' launches on one stream may alternate
+
+
+def _default_scratch(device, stream: int, nbytes: int):
+    """The scratch of a call without a workspace: the buffer that this thread has for the
+    stream; in a capture one of the graph's, so that no graph shares it with other calls."""
+    import torch
+    if nbytes == 0:
+        return None, 0
+    if torch.cuda.current_device() != device.index or stream != _raw_stream(device):
+        with _on(device), _at(device, stream):
+            return _default_scratch(device, stream, nbytes)
+    if torch.cuda.is_current_stream_capturing():
+        return _graph_scratch(device, nbytes)
+    spaces = _ws.__dict__
+    key = (device.index, stream)
+    if key not in spaces:
+        spaces[key] = Workspace(device)
+    return spaces[key].get(nbytes)
+
+
+def _scratch(workspace, device, stream: int, nbytes: int):
+    """(buffer, its bytes) of a call: the caller's workspace, or the default one."""
+    return workspace.get(nbytes) if workspace is not None else _default_scratch(device, stream, nbytes)
 
 
 def attention(q, k, v, bias=None, *, heads, headDim, out=None, workspace=None, stream=None, **params):
@@ -537,9 +596,8 @@ def attention(q, k, v, bias=None, *, heads, headDim, out=None, workspace=None, s
     if out is None:
         out = torch.empty((T, heads * vhd), dtype=torch.float32, device=q.device)
     nbytes = vtmu_attention_workspace_size(p)
-    ws = workspace if workspace is not None else _default_workspace(q.device)
-    buf, cap = ws.get(nbytes)
     st = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
+    buf, cap = _scratch(workspace, q.device, st, nbytes)
     vtmu_attention(q, k, v, bias, out, p, buf, cap, st)
     return out
 
@@ -561,9 +619,8 @@ def decode_step(k_cache, v_cache, k_new, v_new, offset: int, q, bias=None, *, he
     if out is None:
         out = torch.empty((T, heads * vhd), dtype=torch.float32, device=q.device)
     nbytes = vtmu_attention_workspace_size(p)
-    ws = workspace if workspace is not None else _default_workspace(q.device)
-    buf, cap = ws.get(nbytes)
     st = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
+    buf, cap = _scratch(workspace, q.device, st, nbytes)
     vtmu_decode_step(k_cache, v_cache, S, k_new, v_new, k_new.shape[0], offset, q, bias, out, p, buf, cap, st)
     return out
 
@@ -598,9 +655,8 @@ def decode_step_rope(k_cache, v_cache, k_new, v_new, offset: int, q, bias=None, 
     if out is None:
         out = torch.empty((T, heads * vhd), dtype=torch.float32, device=q.device)
     nbytes = vtmu_attention_workspace_size(p)
-    ws = workspace if workspace is not None else _default_workspace(q.device)
-    buf, cap = ws.get(nbytes)
     st = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
+    buf, cap = _scratch(workspace, q.device, st, nbytes)
     vtmu_decode_step_rope(k_cache, v_cache, S, k_new, v_new, k_new.shape[0], offset, q, bias, out, p, r, buf, cap,
                           st)
     return out
@@ -653,9 +709,8 @@ def mla_attention(q, state, k_b, v_b, *, heads, qk_nope, v_head_dim, out=None, w
     if out is None:
         out = torch.empty((T, heads * v_head_dim), dtype=torch.float32, device=q.device)
     nbytes = vtmu_mla_workspace_size(p)
-    ws = workspace if workspace is not None else _default_workspace(q.device)
-    buf, cap = ws.get(nbytes)
     st = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
+    buf, cap = _scratch(workspace, q.device, st, nbytes)
     vtmu_mla_attention(q, state, k_b, v_b, out, p, buf, cap, st)
     return out
 
@@ -673,9 +728,8 @@ def mla_decode_step(state, state_new, offset: int, q, k_b, v_b, *, heads, qk_nop
     if out is None:
         out = torch.empty((T, heads * v_head_dim), dtype=torch.float32, device=q.device)
     nbytes = vtmu_mla_workspace_size(p)
-    ws = workspace if workspace is not None else _default_workspace(q.device)
-    buf, cap = ws.get(nbytes)
     st = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
+    buf, cap = _scratch(workspace, q.device, st, nbytes)
     vtmu_mla_decode_step(state, state.shape[0], state_new, R, offset, q, k_b, v_b, out, p, buf, cap, st)
     return out
 
@@ -686,21 +740,6 @@ def _need(name, t, dtype, device=None):
     if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or (device is not None and t.device != device):
         where = "" if device is None else f" on {device}"
         raise ValueError(f"{name} must be a contiguous {str(dtype).removeprefix('torch.')} CUDA tensor{where}")
-
-
-_HERE = contextlib.nullcontext()
-
-
-def _on(device):
-    """The device as the current one; nothing to do where it is (the usual case)."""
-    import torch
-    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-def _raw_stream(device) -> int:
-    """The device's current stream as the library takes it."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def page_map(lens, cu_rows, block_table, free_pages, n_free, *, rows: int, pageSize: int, accept=None, stream=None):
@@ -834,8 +873,8 @@ def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, hea
                           window=window or 0, sinks=sinks or 0)
     with _on(dev):
         nbytes = vtmu_paged_workspace_size(p)
-        buf, cap = (workspace if workspace is not None else _default_workspace(dev)).get(nbytes)
         st = _raw_stream(dev) if stream is None else stream
+        buf, cap = _scratch(workspace, dev, st, nbytes)
         vtmu_paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, k_new, v_new, masks, positions, out, p,
                              buf, cap, st)
     return out
