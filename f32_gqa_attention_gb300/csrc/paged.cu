@@ -18,9 +18,9 @@ constexpr int64_t kWave = 152 * 8;  // CTAs of 256 threads that are resident at 
 // that one launch with no ordering between CTAs does: a CTA never reads a table
 // entry that another one writes, new pages being read off the stack.  CTA
 // (b, y) serves every gridDim.y-th chunk of request b's rows; the CTAs of b ==
-// requests clear the rows behind the last request.  Bound by the launch: the
-// accepted rows of 7 trees and 256 prompts of 1 to 1021 rows take the same 25 us
-// from the host; the first 3.1 us a call in a replayed graph.
+// requests clear the rows before the first request and behind the last one.  Bound
+// by the launch: the accepted rows of 7 trees and 256 prompts of 1 to 1021 rows take
+// the same 25 us from the host; the first 3.1 us a call in a replayed graph.
 constexpr int kMapThreads = 256;
 
 struct Need {
@@ -28,7 +28,7 @@ struct Need {
 };
 __device__ __forceinline__ Need page_need(const PageMapArgs& a, int b) {
     Need n;
-    const PackedRows r = packed_rows(a.cu_rows, b, a.rows);
+    const PackedRows r = packed_rows(a.cu_rows, b, a.requests, a.rows);
     n.len = max(__ldg(a.lens + b), 0);
     n.added = r.n;
     if (a.accept) {
@@ -61,14 +61,19 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const PageMapArgs
 
     if (b == a.requests) {
         if (at == 0) *a.n_free_out = (int32_t)clamp64(n_free - before, INT32_MIN, INT32_MAX);
-        for (int64_t r = clamp64(__ldg(a.cu_rows + b), 0, a.rows) + at; r < a.rows; r += step) {
-            a.slots[r] = -1;
-            if (a.positions) a.positions[r] = -1;
-        }
+        const RowRange all = rows_of_all(a.cu_rows, a.requests, a.rows);
+        auto clear = [&](int64_t from, int64_t to) {
+            for (int64_t r = from + at; r < to; r += step) {
+                a.slots[r] = -1;
+                if (a.positions) a.positions[r] = -1;
+            }
+        };
+        clear(0, all.first);
+        clear(all.last, a.rows);
         return;
     }
     const Need n = page_need(a, b);
-    const PackedRows r = packed_rows(a.cu_rows, b, a.rows);
+    const PackedRows r = packed_rows(a.cu_rows, b, a.requests, a.rows);
     int32_t* table = a.block_table + (int64_t)b * a.max_pages;
     auto new_page = [&](int64_t col) -> int32_t {  // col in [held, want)
         const int64_t k = before + col - n.held;
@@ -112,7 +117,7 @@ __global__ void __launch_bounds__(32 * kTreeWarps)
     const int lane = threadIdx.x & 31;
     const int b = blockIdx.x * kTreeWarps + (threadIdx.x >> 5);
     if (b < requests) {
-        const PackedRows r = packed_rows(cu_rows, b, rows);
+        const PackedRows r = packed_rows(cu_rows, b, requests, rows);
         const int n = (int)min(r.n, (int64_t)kTreeMaxRows);
         const int len = max(__ldg(lens + b), 0);
         uint64_t mask[2];
@@ -155,12 +160,17 @@ __global__ void __launch_bounds__(32 * kTreeWarps)
             positions[r.row0 + j] = -1;
         }
     }
-    // Rows behind the last request.
-    const int64_t tail = clamp64(__ldg(cu_rows + requests), 0, rows);
-    for (int64_t j = tail + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; j < rows; j += (int64_t)gridDim.x * blockDim.x) {
-        masks[j] = 0;
-        positions[j] = -1;
-    }
+    // Rows before the first request and behind the last one.
+    const RowRange all = rows_of_all(cu_rows, requests, rows);
+    const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
+    auto clear = [&](int64_t from, int64_t to) {
+        for (int64_t j = from + at; j < to; j += step) {
+            masks[j] = 0;
+            positions[j] = -1;
+        }
+    };
+    clear(0, all.first);
+    clear(all.last, rows);
 }
 
 // ---- rope_at -----------------------------------------------------------------------

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc
     __shared__ float so[kWarps][kR][kMaxD];
     __shared__ float sm[kWarps][kR], sl[kWarps][kR];
     const int b = blockIdx.z, hk = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PackedRows pr = packed_rows(a.cu_rows, b, a.rows);
+    const PackedRows pr = packed_rows(a.cu_rows, b, a.B, a.rows);
     const int64_t nt = min(pr.n, (int64_t)a.max_rows);
     const int64_t v0 = (int64_t)blockIdx.x * kR, nv = nt * a.G;
     if (v0 >= nv) return;

@@ -145,7 +145,7 @@ struct Tiles {
 };
 
 __device__ __forceinline__ Req load_req(const PagedDesc& a, int b) {
-    const PackedRows pr = packed_rows(a.cu_rows, b, a.rows);
+    const PackedRows pr = packed_rows(a.cu_rows, b, a.B, a.rows);
     Req r;
     r.row0 = (int)pr.row0;
     r.n = (int)pr.n;
@@ -414,7 +414,7 @@ __device__ __forceinline__ int tile_order(int c) { return (c >> 4) * 64 + (c & 1
 // KV head hk; null for a page id outside the pool.
 __device__ __forceinline__ const float* global_row(const PagedDesc& a, const float* pool, const float* fresh, int b, int key,
                                                    int k, int hk) {
-    if (key < 0) return fresh + ((packed_rows(a.cu_rows, b, a.rows).row0 + k) * a.Hk + hk) * a.D;
+    if (key < 0) return fresh + ((packed_rows(a.cu_rows, b, a.B, a.rows).row0 + k) * a.Hk + hk) * a.D;
     const int64_t page = __ldg(a.block_table + (int64_t)b * a.max_pages + (key + k) / a.page_size);
     if (page < 0 || page >= a.pages) return nullptr;
     return pool + ((page * a.page_size + (key + k) % a.page_size) * a.Hk + hk) * a.D;

@@ -486,12 +486,16 @@ VTMU_API vtmu_status vtmu_mla_decode_step_host(float* state, int64_t max_rows, c
  * of request b is pool row block_table[b, s / page_size] * page_size + s %
  * page_size.  The rows that a step adds are packed request after request:
  * request b owns rows cu_rows[b] .. cu_rows[b + 1] - 1 of q, out, the new K/V
- * rows and every per-row array; rows behind cu_rows[requests] belong to no
- * request.  Lengths and tables are DEVICE memory and read by the kernels
+ * rows and every per-row array; rows before cu_rows[0] and from
+ * cu_rows[requests] on belong to no request (cu_rows may be a part of a larger
+ * batch's).  Lengths and tables are DEVICE memory and read by the kernels
  * alone, so a captured graph serves every later step whose rows and pages fit
  * the sizes it was captured with.  Values outside their range on the device
  * (a negative length, a page id outside the pool, a decreasing cu_rows) are
  * clamped or skipped as each entry point says; none leads out of a buffer.
+ * cu_rows is clamped to 0 .. rows and its inner entries to its ends, and a
+ * decreasing pair holds no rows; where later requests then claim a row again, it
+ * holds what one of its requests makes of it.
  *
  * A step of tokens that are already decided: vtmu_page_map, vtmu_rope_at on q
  * and the new keys, vtmu_paged_write, vtmu_paged_attention without a tree.
@@ -512,8 +516,7 @@ VTMU_API vtmu_status vtmu_mla_decode_step_host(float* state, int64_t max_rows, c
  * taken from the top of the stack free_pages[0 .. *n_free) in the order of
  * (request, page): the k-th new page of the call is free_pages[*n_free-1-k].
  *   lens [requests], cu_rows [requests + 1]: int32, DEVICE.  A negative length
- *     counts as 0; cu_rows entries are clamped to 0 .. rows and a decreasing
- *     pair holds no rows.
+ *     counts as 0.
  *   accept [requests]: uint64, DEVICE, or NULL (every packed row is added).
  *   block_table [requests, max_pages]: int32, DEVICE; entries of pages that
  *     the call adds are written, the others left.  A request's rows past
@@ -521,7 +524,7 @@ VTMU_API vtmu_status vtmu_mla_decode_step_host(float* state, int64_t max_rows, c
  *   free_pages [free_capacity], n_free [1]: int32, DEVICE; not changed.
  *     *n_free is clamped to 0 .. free_capacity.
  *   slots [rows]: int32 out: the pool row of each packed row; -1 for a row
- *     that is not added, behind the last request, or without a page.
+ *     that is not added, of no request, or without a page.
  *   positions [rows]: int32 out or NULL: the row's place in its request (its
  *     token position), -1 where it is not added.
  *   new_lens [requests]: int32 out: lens + a_b.
@@ -548,7 +551,7 @@ VTMU_API vtmu_status vtmu_page_map(const int32_t* lens, const int32_t* cu_rows, 
  *   parents [rows], cu_rows [requests + 1], lens [requests] (rows of context,
  *     a negative one counts as 0): int32, DEVICE.
  *   masks [rows]: uint64 out; positions [rows]: int32 out.  Rows past a
- *     request's 64th and rows behind the last request get mask 0, position -1.
+ *     request's 64th and rows of no request get mask 0, position -1.
  * Errors: VTMU_ERR_INVALID (null or misaligned pointer, negative size,
  * overlapping buffers), VTMU_ERR_CUDA.
  */
@@ -644,8 +647,8 @@ VTMU_API vtmu_status vtmu_paged_workspace_size(const vtmu_paged_params* p, size_
  * scores that are not finite may do so.  A value that is not finite makes its
  * column of the rows that see it not finite, whatever its weight.
  *   q, out [rows, heads*headDim]; lens, cu_rows, block_table as for
- *   vtmu_page_map.  Rows behind the last request, and a request's rows past
- *   max_rows, are left as they were in out.  Lengths are clamped to 0 ..
+ *   vtmu_page_map.  Rows of no request, and a request's rows past max_rows, are
+ *   left as they were in out.  Lengths are clamped to 0 ..
  *   max_pages * page_size; a page id outside 0 .. pages - 1 stands for rows of
  *   zeros.  out must not overlap an input; k_new, v_new, masks and positions
  *   are NULL without a tree.
