@@ -1326,18 +1326,20 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PgArgs g) {
     auto slot_row = [&](int k) -> int64_t {  // piece k of the unit
         return (int64_t)(2 * (first + k * g.team) + (k == 0 ? 1 : 0)) * kM + i;
     };
-    float m = -INFINITY;
-    for (int k = lane; k < count; k += 32) m = fmaxf(m, __ldcg(g.part_m + slot_row(k)));
+    auto load = [&](int k) -> float2 {  // m and l of piece k
+        return k < count ? make_float2(__ldcg(g.part_m + slot_row(k)), __ldcg(g.part_l + slot_row(k)))
+                         : make_float2(-INFINITY, 0.f);
+    };
+    const float2 own = load(lane);  // more than 32 pieces: the others are loaded at every use
+    float m = own.x;
+    for (int k = lane + 32; k < count; k += 32) m = fmaxf(m, __ldcg(g.part_m + slot_row(k)));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, off));
-    // Piece k's; -0 where it saw nothing and left no output (l tells that, not m: NaN scores
-    // leave m at -inf).  A weight that comes to +0 counts: 0 x inf is NaN, as in the other rows.
-    auto weight = [&](int k) -> float {
-        const float l = k < count ? __ldcg(g.part_l + slot_row(k)) : 0.f;
-        return l != 0.f ? fast_exp2(__ldcg(g.part_m + slot_row(k)) - m) * l : -0.f;
-    };
-    float den = 0.f;
-    for (int k = lane; k < count; k += 32) den += weight(k);
+    // A piece's weight; -0 where it saw nothing and left no output (l tells that, not m: NaN
+    // scores leave m at -inf).  One that comes to +0 counts: 0 x inf is NaN, as in the other rows.
+    auto weight = [&](float2 p) -> float { return p.y != 0.f ? fast_exp2(p.x - m) * p.y : -0.f; };
+    float den = weight(own);
+    for (int k = lane + 32; k < count; k += 32) den += weight(load(k));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(FULL, den, off);
     const float inv = den != 0.f ? 1.f / den : 0.f;
@@ -1346,7 +1348,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PgArgs g) {
 #pragma unroll
     for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
     for (int k0 = 0; k0 < count; k0 += 32) {
-        const float wgt = weight(k0 + lane) * inv;
+        const float wgt = weight(k0 == 0 ? own : load(k0 + lane)) * inv;
         const int here = min(count - k0, 32);
         for (int k = 0; k < here; ++k) {
             const float f = __shfl_sync(FULL, wgt, k);
