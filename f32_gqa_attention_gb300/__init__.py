@@ -544,19 +544,20 @@ class Workspace:
         return self.buf, self.buf.numel()
 
 
-def _graph_scratch(device, nbytes: int):
+def _graph_scratch(device, nbytes: int, counters: bool = True):
     """A buffer out of the memory of the graph that is being captured, its counters cleared
     by the graph.  Given back at the end of the call, it serves later calls on the stream."""
     import torch
     buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    buf[:WORKSPACE_HEADER_BYTES].zero_()
+    if counters:
+        buf[:WORKSPACE_HEADER_BYTES].zero_()
     return buf, nbytes
 
 
 _ws = threading.local()  # per host thread: two threads' launches on one stream may alternate
 
 
-def _default_scratch(device, stream: int, nbytes: int):
+def _default_scratch(device, stream: int, nbytes: int, counters: bool):
     """The scratch of a call without a workspace: the buffer that this thread has for the
     stream; in a capture one of the graph's, so that no graph shares it with other calls."""
     import torch
@@ -564,9 +565,9 @@ def _default_scratch(device, stream: int, nbytes: int):
         return None, 0
     if torch.cuda.current_device() != device.index or stream != _raw_stream(device):
         with _on(device), _at(device, stream):
-            return _default_scratch(device, stream, nbytes)
+            return _default_scratch(device, stream, nbytes, counters)
     if torch.cuda.is_current_stream_capturing():
-        return _graph_scratch(device, nbytes)
+        return _graph_scratch(device, nbytes, counters)
     spaces = _ws.__dict__
     key = (device.index, stream)
     if key not in spaces:
@@ -574,9 +575,10 @@ def _default_scratch(device, stream: int, nbytes: int):
     return spaces[key].get(nbytes)
 
 
-def _scratch(workspace, device, stream: int, nbytes: int):
-    """(buffer, its bytes) of a call: the caller's workspace, or the default one."""
-    return workspace.get(nbytes) if workspace is not None else _default_scratch(device, stream, nbytes)
+def _scratch(workspace, device, stream: int, nbytes: int, counters: bool = True):
+    """(buffer, its bytes) of a call: the caller's workspace, or the default one
+    (`counters`: with the decode kernels' arrival counters, cleared)."""
+    return workspace.get(nbytes) if workspace is not None else _default_scratch(device, stream, nbytes, counters)
 
 
 def attention(q, k, v, bias=None, *, heads, headDim, out=None, workspace=None, stream=None, **params):
@@ -710,7 +712,7 @@ def mla_attention(q, state, k_b, v_b, *, heads, qk_nope, v_head_dim, out=None, w
         out = torch.empty((T, heads * v_head_dim), dtype=torch.float32, device=q.device)
     nbytes = vtmu_mla_workspace_size(p)
     st = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
-    buf, cap = _scratch(workspace, q.device, st, nbytes)
+    buf, cap = _scratch(workspace, q.device, st, nbytes, counters=False)
     vtmu_mla_attention(q, state, k_b, v_b, out, p, buf, cap, st)
     return out
 
@@ -729,7 +731,7 @@ def mla_decode_step(state, state_new, offset: int, q, k_b, v_b, *, heads, qk_nop
         out = torch.empty((T, heads * v_head_dim), dtype=torch.float32, device=q.device)
     nbytes = vtmu_mla_workspace_size(p)
     st = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
-    buf, cap = _scratch(workspace, q.device, st, nbytes)
+    buf, cap = _scratch(workspace, q.device, st, nbytes, counters=False)
     vtmu_mla_decode_step(state, state.shape[0], state_new, R, offset, q, k_b, v_b, out, p, buf, cap, st)
     return out
 
@@ -874,7 +876,7 @@ def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, hea
     with _on(dev):
         nbytes = vtmu_paged_workspace_size(p)
         st = _raw_stream(dev) if stream is None else stream
-        buf, cap = _scratch(workspace, dev, st, nbytes)
+        buf, cap = _scratch(workspace, dev, st, nbytes, counters=False)
         vtmu_paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, k_new, v_new, masks, positions, out, p,
                              buf, cap, st)
     return out

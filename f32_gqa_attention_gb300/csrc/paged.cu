@@ -26,9 +26,9 @@ constexpr int kMapThreads = 256;
 struct Need {
     int64_t len, added, held, want;
 };
-__device__ __forceinline__ Need page_need(const PageMapArgs& a, int b) {
+__device__ __forceinline__ Need page_need(const PageMapArgs& a, const RowRange& all, int b) {
     Need n;
-    const PackedRows r = packed_rows(a.cu_rows, b, a.requests, a.rows);
+    const PackedRows r = packed_rows(a.cu_rows, b, all, a.rows);
     n.len = max(__ldg(a.lens + b), 0);
     n.added = r.n;
     if (a.accept) {
@@ -44,10 +44,11 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const PageMapArgs
     __shared__ long long s_sum[kMapThreads / 32];
     const int b = blockIdx.x;
     const int64_t step = (int64_t)gridDim.y * kMapThreads, at = (int64_t)blockIdx.y * kMapThreads + threadIdx.x;
+    const RowRange all = rows_of_all(a.cu_rows, a.requests, a.rows);
     // Pages taken by the requests before b (by all of them for b == requests).
     long long before = 0;
     for (int i = threadIdx.x; i < b; i += kMapThreads) {
-        const Need n = page_need(a, i);
+        const Need n = page_need(a, all, i);
         before += n.want - n.held;
     }
 #pragma unroll
@@ -61,7 +62,6 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const PageMapArgs
 
     if (b == a.requests) {
         if (at == 0) *a.n_free_out = (int32_t)clamp64(n_free - before, INT32_MIN, INT32_MAX);
-        const RowRange all = rows_of_all(a.cu_rows, a.requests, a.rows);
         auto clear = [&](int64_t from, int64_t to) {
             for (int64_t r = from + at; r < to; r += step) {
                 a.slots[r] = -1;
@@ -72,8 +72,8 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const PageMapArgs
         clear(all.last, a.rows);
         return;
     }
-    const Need n = page_need(a, b);
-    const PackedRows r = packed_rows(a.cu_rows, b, a.requests, a.rows);
+    const Need n = page_need(a, all, b);
+    const PackedRows r = packed_rows(a.cu_rows, b, all, a.rows);
     int32_t* table = a.block_table + (int64_t)b * a.max_pages;
     auto new_page = [&](int64_t col) -> int32_t {  // col in [held, want)
         const int64_t k = before + col - n.held;
@@ -116,8 +116,9 @@ __global__ void __launch_bounds__(32 * kTreeWarps)
     constexpr unsigned FULL = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     const int b = blockIdx.x * kTreeWarps + (threadIdx.x >> 5);
+    const RowRange all = rows_of_all(cu_rows, requests, rows);
     if (b < requests) {
-        const PackedRows r = packed_rows(cu_rows, b, requests, rows);
+        const PackedRows r = packed_rows(cu_rows, b, all, rows);
         const int n = (int)min(r.n, (int64_t)kTreeMaxRows);
         const int len = max(__ldg(lens + b), 0);
         uint64_t mask[2];
@@ -161,7 +162,6 @@ __global__ void __launch_bounds__(32 * kTreeWarps)
         }
     }
     // Rows before the first request and behind the last one.
-    const RowRange all = rows_of_all(cu_rows, requests, rows);
     const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
     auto clear = [&](int64_t from, int64_t to) {
         for (int64_t j = from + at; j < to; j += step) {

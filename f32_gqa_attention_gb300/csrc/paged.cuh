@@ -25,12 +25,14 @@ struct PackedRows {
     int64_t row0;
     int64_t n;
 };
-__device__ __forceinline__ PackedRows packed_rows(const int32_t* cu_rows, int b, int requests, int64_t rows) {
-    const RowRange all = rows_of_all(cu_rows, requests, rows);
+__device__ __forceinline__ PackedRows packed_rows(const int32_t* cu_rows, int b, const RowRange& all, int64_t rows) {
     PackedRows r;
     r.row0 = max(clamp64(__ldg(cu_rows + b), 0, rows), all.first);
     r.n = max(min((int64_t)__ldg(cu_rows + b + 1), all.last) - r.row0, (int64_t)0);
     return r;
+}
+__device__ __forceinline__ PackedRows packed_rows(const int32_t* cu_rows, int b, int requests, int64_t rows) {
+    return packed_rows(cu_rows, b, rows_of_all(cu_rows, requests, rows), rows);
 }
 
 }  // namespace vtmu
