@@ -158,7 +158,7 @@ __device__ __forceinline__ Tiles tiles_of(const PagedDesc& a, const Req& r) {
     int64_t lo = 0;
     if (a.window > 0) lo = clamp64((a.tree ? (int64_t)r.len : (int64_t)r.len - r.n) - a.window + 1, 0, r.len);
     t.lo_tile = (int)(lo / kKT);
-    t.n_main = lo < r.len ? (r.len + kKT - 1) / kKT - t.lo_tile : 0;
+    t.n_main = lo < r.len ? (int)(((int64_t)r.len + kKT - 1) / kKT) - t.lo_tile : 0;
     // Where the window leaves nothing of the cache (a tree's, at most 1), no main tile holds
     // the sinks of the cache's last tile.
     const int64_t sink_tiles = (min(a.sinks, (int64_t)r.len) + kKT - 1) / kKT;
@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && warp_next(g, prefix, s)) {
             int batch = -1, y_cur = nowhere;
-            const int subs = (s.len + g.sub - 1) / g.sub, u1 = s.u1, n_sink = s.n_sink, n_ctx = s.n_ctx, lo_tile = s.lo_tile;
+            const int subs = (int)(((int64_t)s.len + g.sub - 1) / g.sub), u1 = s.u1, n_sink = s.n_sink, n_ctx = s.n_ctx, lo_tile = s.lo_tile;
             for (int u = s.u0; u < u1; ++u, ++n) {
                 const int key = tile_key(n_sink, n_ctx, lo_tile, a.tree, u);
                 int y = nowhere;
