@@ -760,9 +760,9 @@ def page_map(lens, cu_rows, block_table, free_pages, n_free, *, rows: int, pageS
     if accept is not None:
         _need("accept", accept, torch.int64, dev)
     if (cu_rows.shape != (n + 1,) or block_table.dim() != 2 or block_table.shape[0] != n or n_free.numel() != 1 or
-            (accept is not None and accept.shape != (n,))):
-        raise ValueError("page_map: cu_rows [requests + 1], block_table [requests, maxPages], n_free [1], "
-                         "accept [requests]")
+            (accept is not None and accept.shape != (n,)) or pageSize >= 1 << 31):
+        raise ValueError("page_map: pageSize below 2^31, cu_rows [requests + 1], block_table [requests, maxPages], "
+                         "n_free [1], accept [requests]")
     slots, positions, new_lens, left = torch.empty(2 * rows + n + 1, dtype=i32, device=dev).split([rows, rows, n, 1])
     with _on(dev):
         st = _raw_stream(dev) if stream is None else stream
@@ -847,11 +847,11 @@ def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, hea
         _need(name, t, i32, dev)
     hk = heads if kvHeads is None else kvHeads
     rows, n = q.shape[0], lens.shape[0]
-    if (pageSize < 1 or q.shape != (rows, heads * headDim) or k_pool.dim() != 2 or k_pool.shape[1] != hk * headDim or
+    if (not 0 < pageSize < 1 << 31 or q.shape != (rows, heads * headDim) or k_pool.dim() != 2 or k_pool.shape[1] != hk * headDim or
             k_pool.shape != v_pool.shape or k_pool.shape[0] % pageSize or block_table.dim() != 2 or
             block_table.shape[0] != n or cu_rows.shape != (n + 1,)):
-        raise ValueError("paged_attention: q [rows, heads*headDim], pools [pages*pageSize, kvHeads*headDim], "
-                         "block_table [requests, maxPages], lens [requests], cu_rows [requests + 1]")
+        raise ValueError("paged_attention: pageSize in 1 .. 2^31 - 1, q [rows, heads*headDim], pools [pages*pageSize, "
+                         "kvHeads*headDim], block_table [requests, maxPages], lens [requests], cu_rows [requests + 1]")
     k_new = v_new = masks = positions = None
     if tree is not None:
         k_new, v_new, masks, positions = tree
@@ -868,8 +868,8 @@ def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, hea
     _need("out", out, f32, dev)
     if out.shape != q.shape:
         raise ValueError("paged_attention: out [rows, heads*headDim]")
-    p = vtmu_paged_params(rows=rows, pages=k_pool.shape[0] // pageSize, requests=n, max_rows=maxRows,
-                          page_size=pageSize, max_pages=block_table.shape[1], heads=heads, kv_heads=hk,
+    p = vtmu_paged_params(rows=rows, pages=k_pool.shape[0] // pageSize, requests=n,
+                          max_rows=max(min(maxRows, rows), -1), page_size=pageSize, max_pages=block_table.shape[1], heads=heads, kv_heads=hk,
                           head_dim=headDim, tree=0 if tree is None else 1, has_scale=0 if scale is None else 1,
                           scale=0.0 if scale is None else scale, softcap=softcap or 0.0, kernel=kernel,
                           window=window or 0, sinks=sinks or 0)

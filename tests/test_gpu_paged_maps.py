@@ -10,7 +10,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import f32_gqa_attention_gb300 as vtmu  # noqa: E402
-from test_gpu_paged import BOTH, KW, attend, check, dev, expect  # noqa: E402
+from test_gpu_paged import BOTH, CUDA, KW, attend, check, dev, expect  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +104,23 @@ def test_attention_writes_the_requests_rows_alone(kernel, tree):
         d["cu"] = np.array([0, 2], np.int32)
         d["q"], d["lens"], d["table"] = d["q"][7:9], d["lens"][:1], d["table"][:1]
         check(got[7:9], expect(d, **KW))
+
+
+@BOTH
+@pytest.mark.parametrize("most", [(1 << 31) - 1, 1 << 31, 1 << 32, (1 << 40) + 1])
+def test_max_rows_past_32_bits(kernel, most):
+    """A bound is a bound, whatever its size; a negative one is refused."""
+    d = ref.batch(35, [150, 20], [4, 1], **KW)
+    check(attend(d, kernel=kernel, maxRows=most, **KW), expect(d, **KW))
+    with pytest.raises(vtmu.VtmuError):
+        attend(d, kernel=kernel, maxRows=-most, **KW)
+
+
+@pytest.mark.parametrize("page", [0, -16, 1 << 31, (1 << 32) + 16])
+def test_page_sizes_out_of_range_are_refused(page):
+    d = ref.batch(36, [150, 20], [4, 1], **KW)
+    with pytest.raises((ValueError, vtmu.VtmuError)):
+        vtmu.page_map(dev(d["lens"]), dev(d["cu"]), dev(d["table"]), dev(np.arange(9, dtype=np.int32)),
+                      dev(np.array([9], np.int32)), rows=5, pageSize=page)
+    with pytest.raises((ValueError, vtmu.VtmuError)):
+        attend(dict(d, k_pool=d["k_pool"][:0], v_pool=d["v_pool"][:0]), kernel=CUDA, **dict(KW, pageSize=page))
