@@ -750,7 +750,9 @@ def page_map(lens, cu_rows, block_table, free_pages, n_free, *, rows: int, pageS
     block_table [requests, maxPages] int32 (completed in place), the stack
     free_pages [n] with n_free [1] pages on it, accept [requests] int64 bit
     masks of the rows to add (None: all).  Returns (slots [rows],
-    positions [rows], new_lens [requests], n_free [1]), all int32."""
+    positions [rows], new_lens [requests], n_free [1]), all int32.  A negative
+    n_free says that as many pages were missing: call again with the same
+    lens and n_free once pages are back on the stack."""
     import torch
     dev, n = lens.device, lens.shape[0]
     i32 = torch.int32
@@ -847,9 +849,9 @@ def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, hea
         _need(name, t, i32, dev)
     hk = heads if kvHeads is None else kvHeads
     rows, n = q.shape[0], lens.shape[0]
-    if (not 0 < pageSize < 1 << 31 or q.shape != (rows, heads * headDim) or k_pool.dim() != 2 or k_pool.shape[1] != hk * headDim or
-            k_pool.shape != v_pool.shape or k_pool.shape[0] % pageSize or block_table.dim() != 2 or
-            block_table.shape[0] != n or cu_rows.shape != (n + 1,)):
+    if (not 0 < pageSize < 1 << 31 or q.shape != (rows, heads * headDim) or k_pool.dim() != 2 or
+            k_pool.shape[1] != hk * headDim or k_pool.shape != v_pool.shape or k_pool.shape[0] % pageSize or
+            block_table.dim() != 2 or block_table.shape[0] != n or cu_rows.shape != (n + 1,)):
         raise ValueError("paged_attention: pageSize in 1 .. 2^31 - 1, q [rows, heads*headDim], pools [pages*pageSize, "
                          "kvHeads*headDim], block_table [requests, maxPages], lens [requests], cu_rows [requests + 1]")
     k_new = v_new = masks = positions = None
@@ -869,8 +871,9 @@ def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, hea
     if out.shape != q.shape:
         raise ValueError("paged_attention: out [rows, heads*headDim]")
     p = vtmu_paged_params(rows=rows, pages=k_pool.shape[0] // pageSize, requests=n,
-                          max_rows=max(min(maxRows, rows), -1), page_size=pageSize, max_pages=block_table.shape[1], heads=heads, kv_heads=hk,
-                          head_dim=headDim, tree=0 if tree is None else 1, has_scale=0 if scale is None else 1,
+                          max_rows=max(min(maxRows, rows), -1), page_size=pageSize,
+                          max_pages=block_table.shape[1], heads=heads, kv_heads=hk, head_dim=headDim,
+                          tree=0 if tree is None else 1, has_scale=0 if scale is None else 1,
                           scale=0.0 if scale is None else scale, softcap=softcap or 0.0, kernel=kernel,
                           window=window or 0, sinks=sinks or 0)
     with _on(dev):

@@ -531,8 +531,15 @@ VTMU_API vtmu_status vtmu_mla_decode_step_host(float* state, int64_t max_rows, c
  *   n_free_out [1]: int32 out: pages left; negative when that many pages were
  *     missing: entries and slots of missing pages are -1.
  * The outputs may not overlap an input or each other.  A page goes back by
- * writing its id at free_pages[*n_free_out] and counting one more (a finished
+ * writing its id at free_pages[n] and counting one more, n the pages on the
+ * stack: *n_free_out, or *n_free where the call is not gone on with (a finished
  * request's ids are the first ceil(lens[b] / page_size) of its table row).
+ * A call that ran out of pages (*n_free_out < 0) is not gone on with: lens,
+ * n_free and the stack are as they were, so once pages have come back on top of
+ * it the same call gives every row its page, over the -1 entries.  A caller
+ * that takes new_lens all the same keeps the holes: a page below a request's
+ * length counts as held, so no later call fills it, and the stack is empty (a
+ * negative *n_free counts as 0).
  * Errors: VTMU_ERR_INVALID (null pointer, negative size, page_size or
  * max_pages < 1, a misaligned pointer, overlapping buffers),
  * VTMU_ERR_UNSUPPORTED (more than 65536 requests), VTMU_ERR_CUDA.

@@ -1,5 +1,5 @@
-"""Requests' rows from offsets that do not start at 0 or that fall, against what the
-definitions say.  Whole numbers are exact, attention as in test_gpu_paged."""
+"""Requests' rows from offsets that do not start at 0 or that fall, sizes past 32 bits,
+and page_map after a call that ran out of pages, against what the definitions say.  Whole numbers are exact, attention as in test_gpu_paged."""
 import numpy as np
 import pytest
 
@@ -124,3 +124,28 @@ def test_page_sizes_out_of_range_are_refused(page):
                       dev(np.array([9], np.int32)), rows=5, pageSize=page)
     with pytest.raises((ValueError, vtmu.VtmuError)):
         attend(dict(d, k_pool=d["k_pool"][:0], v_pool=d["v_pool"][:0]), kernel=CUDA, **dict(KW, pageSize=page))
+
+
+def test_page_map_again_after_a_shortage():
+    """A call that ran out of pages reads its inputs alone: once pages have come back, the same
+    lengths and the same stack give every row its page, over the entries that were -1."""
+    page, rows = 4, 40
+    lens, cu = [6, 9, 0], [0, 15, 22, 40]
+    ids = np.random.default_rng(3).permutation(40).astype(np.int32)
+    table = np.full((3, 8), -1, np.int32)
+    table[0, :2], table[1, :3] = ids[:2], ids[2:5]
+    free = ids[5:].copy()
+    t = dev(table)
+    got = call_page_map(lens, cu, t, free, 5, rows, page)
+    want = ref.page_map(lens, cu, table, free, 5, rows, page)
+    assert got[3] == want[3] == -5  # pages for 21, 16 and 18 rows, less those held: 4 + 1 + 5, of 5
+    assert all(np.array_equal(a, b) for a, b in zip(got[:3] + got[4:], want[:3] + want[4:]))
+    assert (got[0][:40] == -1).sum() == (want[0] == -1).sum() > 0
+    left = 5
+    for page_id in free[30:35]:  # the pages come back, to the top of the stack
+        free[left] = page_id
+        left += 1
+    got = call_page_map(lens, cu, t, free, left, rows, page)
+    want = ref.page_map(lens, cu, table, free, left, rows, page)
+    assert got[3] == want[3] == 0 and np.all(got[0] >= 0)
+    assert all(np.array_equal(a, b) for a, b in zip(got[:3] + got[4:], want[:3] + want[4:]))
