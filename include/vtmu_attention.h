@@ -622,7 +622,7 @@ typedef struct vtmu_paged_params {
     float softcap;       /* 0 = off; > 0: x = softcap * tanh(x / softcap) */
     int32_t kernel;      /* vtmu_paged_kernel */
     int64_t window;      /* 0 = off; a key at position s needs s > p - window */
-    int64_t sinks;       /* with a window: cache rows s < sinks stay visible */
+    int64_t sinks;       /* with a window: cache rows s < sinks stay visible (drafted ones do not) */
 } vtmu_paged_params;
 
 /* Writes the defaults: everything 0 / off / AUTO. */
@@ -646,7 +646,10 @@ VTMU_API vtmu_status vtmu_paged_workspace_size(const vtmu_paged_params* p, size_
  *     as vtmu_tree_plan writes them; positions is read with a window only and
  *     may be NULL without one).
  * With a window a key must also lie at s > p - window (drafted rows at their
- * own positions), or among the first `sinks` cache rows.  Scores are scale *
+ * own positions), or among the first `sinks` cache rows; a drafted row is no
+ * sink, wherever it lies, so where a context is shorter than `sinks` a tree
+ * that is deeper than the window sees less than the same rows once they are
+ * in the cache.  Scores are scale *
  * q.k, then softcap; the output is the max-subtracted softmax applied to the
  * values.  A row that sees no key is written as zeros; keys and values that a
  * row does not see do not enter it, whatever they hold.  A NaN in a row's

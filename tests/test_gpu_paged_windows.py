@@ -9,7 +9,7 @@ if not torch.cuda.is_available():
 
 import f32_gqa_attention_gb300 as vtmu  # noqa: E402
 import paged_ref as ref  # noqa: E402
-from test_gpu_paged import BOTH, check, dev, expect, kw_of, run_case  # noqa: E402
+from test_gpu_paged import BOTH, attend, check, dev, expect, kw_of, run_case  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,25 @@ def test_a_request_as_long_as_its_table_allows(kernel, page, tree):
                                tree=drafted, maxRows=3, kernel=kernel, **kw)
     check(got.cpu().numpy(), want)
     assert vtmu.vtmu_device_error() == 0
+
+
+@BOTH
+@pytest.mark.parametrize("n", [0, 2, 5, 6, 70])
+def test_drafted_rows_are_no_sinks(kernel, n):
+    """Only rows of the cache are, in a chain that is deeper than the window too."""
+    kw = kw_of(4, 2, 64, 16, window=3, sinks=6)
+    d = ref.batch(55, [n, 40], [9, 4], heads=4, kvHeads=2, headDim=64, pageSize=16, tree=True)
+    kn, vn, masks, positions = d["tree"]
+    masks[:9] = [(2 << j) - 1 for j in range(9)]  # a chain
+    positions[:9] = n + np.arange(9)
+    got = attend(d, kernel=kernel, **kw)
+    check(got, expect(d, **kw))
+    # Row 8 at position n + 8 sees its window, drafted rows 6 to 8, and the cache's first rows.
+    keys = min(n, 6)
+    at = d["table"][0, np.arange(keys) // 16].astype(np.int64) * 16 + np.arange(keys) % 16
+    k, v = np.concatenate([d["k_pool"][at], kn[6:9]]), np.concatenate([d["v_pool"][at], vn[6:9]])
+    for h in range(4):
+        c = (h // 2) * 64
+        x = k[:, c:c + 64].astype(np.float64) @ d["q"][8, 64 * h:64 * h + 64].astype(np.float64) / 8.0
+        w = np.exp(x - x.max())
+        assert np.max(np.abs(got[8, 64 * h:64 * h + 64] - w @ v[:, c:c + 64] / w.sum())) <= 1e-4
