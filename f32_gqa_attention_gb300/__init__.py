@@ -838,8 +838,9 @@ def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, hea
     kvHeads*headDim], block_table [requests, maxPages], lens [requests] and
     cu_rows [requests + 1] int32; maxRows bounds the rows of one request.
     ``tree=(k_new, v_new, masks, positions)`` attends to drafted rows beside
-    the cache (positions may be None without a window).  Returns out [rows,
-    heads*headDim]; rows of no request are not written."""
+    the cache (positions may be None without a window); with a window the
+    cache's first ``sinks`` rows stay visible, drafted ones do not.  Returns
+    out [rows, heads*headDim]; rows of no request are not written."""
     import torch
     dev = q.device
     f32, i32 = torch.float32, torch.int32

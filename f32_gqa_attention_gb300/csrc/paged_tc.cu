@@ -94,7 +94,7 @@ constexpr float kLazyLog2 = 4.f;  // and a row's reference maximum moves when be
 // trees; four were 4 % faster than two.
 constexpr int kGroup = 2;
 constexpr int kRing = 8;       // what a tile leaves for later roles
-static_assert(kRing >= kGroup + 2 && kRing >= 5 && (kRing & (kRing - 1)) == 0, "a slot outlives its last reader");
+static_assert(kRing >= kGroup + 2 && (kRing & (kRing - 1)) == 0, "a slot outlives its last reader");
 
 enum : unsigned int {
     kErrPgLoad = 1u << 3,   // the splitters gave up on a loaded tile
@@ -129,6 +129,7 @@ struct Cfg {
     static_assert(kColAcc + D <= kTmemCols, "TMEM budget");
     static_assert(kSmem + 24 * 1024 <= 232448, "shared memory budget");
     static_assert(kSlots % 2 == 0, "K in the even slots, V in the odd ones");
+    static_assert(kRing >= kSlots / 2 + 2, "the splitters are kSlots / 2 tiles ahead of scores that the softmax is behind by one");
 };
 
 // ---- the list of tiles --------------------------------------------------------------
@@ -735,10 +736,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_base_s;
     __shared__ long long scan_s[kThreads / 32];
     __shared__ Seg seg_s[kThreads / 32];
-    // What tile n leaves for the roles that come later, at n % kRing.  The splitters are at
-    // most three tiles ahead of the MMAs; while a group of kGroup tiles waits for its
-    // fold, the softmax gets two tiles further: S(n) is issued before P.V of tile
-    // n - 1, which waits.
+    // What tile n leaves for the roles that come later, at n % kRing.  The splitters get to
+    // tile n once S(n - kSlots / 2) is done, three tiles (headDim 128) or six (64), while the
+    // softmax may still read the tile before that one; while a group of kGroup tiles waits
+    // for its fold, the softmax gets two tiles further: S(n) is issued before P.V of
+    // tile n - 1, which waits.
     __shared__ __align__(16) float k_scale[kRing][kKT], v_scale[kRing][kKT];
     __shared__ __align__(16) uint32_t v_bad[kRing][4];
     __shared__ __align__(8) uint8_t rescued[kRing][2][4];  // keys, values: a split warp's rows have a scale of their own

@@ -656,6 +656,14 @@ VTMU_API vtmu_status vtmu_paged_workspace_size(const vtmu_paged_params* p, size_
  * query, or in a key that it sees, makes that head of the row NaN; other
  * scores that are not finite may do so.  A value that is not finite makes its
  * column of the rows that see it not finite, whatever its weight.
+ * Of op "attention" there is no ALiBi, bias, non-causal form or vHeadDim here.
+ * Precision: both kernels sum in f32.  The CUDA cores keep q, k, v and the
+ * weights in f32; their sums of weight x value overflow where the keys' number
+ * times |value| passes 3.4e38.  The tensor cores (AUTO's choice where they cover
+ * the call) keep 22 bits of the largest element of each row and head of q, k
+ * and v, so fewer of an element that is far below it, and weights, or products
+ * of weight and value where values reach 512 or stay below 2^-9, to 2^-36 of
+ * the largest.  Force VTMU_PAGED_CUDA_CORES where that matters more than time.
  *   q, out [rows, heads*headDim]; lens, cu_rows, block_table as for
  *   vtmu_page_map.  Rows of no request, and a request's rows past max_rows, are
  *   left as they were in out.  Lengths are clamped to 0 ..
