@@ -20,7 +20,7 @@ constexpr int64_t kWave = 152 * 8;  // CTAs of 256 threads that are resident at 
 // (b, y) serves every gridDim.y-th chunk of request b's rows; the CTAs of b ==
 // requests clear the rows before the first request and behind the last one.  Bound
 // by the launch: the accepted rows of 7 trees and 256 prompts of 1 to 1021 rows take
-// the same 25 us from the host; the first 3.1 us a call in a replayed graph.
+// the same 25 us from the host; 3.1-3.9 and 6.6-7.3 us a call in a replayed graph.
 constexpr int kMapThreads = 256;
 
 struct Need {
@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const PageMapArgs
 // row starts with its own bit and its parent; each of six steps adds the mask
 // of the row it points to and moves the pointer there, so the path a mask
 // covers doubles and 64 rows are done in 6 steps whatever the tree's depth.
-// Bound by the launch: 1.4 us a call in a replayed graph for one tree, 1.7 us for many.
+// Bound by the launch: 1.4-1.9 us a call in a replayed graph for one tree, 1.7-2.6 us for
+// many (one call a graph, and ten).
 constexpr int kTreeWarps = 4;
 
 __global__ void __launch_bounds__(32 * kTreeWarps)

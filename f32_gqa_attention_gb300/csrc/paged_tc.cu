@@ -28,7 +28,8 @@
 // CTA is finished there; a unit cut by a boundary leaves partials (m, l, o / l) that
 // paged_merge_kernel joins by the log-sum-exp rule, always in the same order.
 // With more than 128 virtual rows per KV head, teams of R CTAs walk the same
-// tiles for R row blocks at the same time, so the tiles come from HBM once.
+// tiles for R row blocks at the same time, so the tiles come from HBM once (two blocks,
+// 0.95 GB of cache: 0.97 GB read).
 //
 // Tiles of 64 keys, M = 128 virtual rows (padded: the MMAs of a tile take 1540
 // cycles, its 64 KB 2800 at this SM's share of HBM, so padding costs no
@@ -42,16 +43,18 @@
 //           (kGroup: no sum runs long inside the pipe); acc stays in TMEM, so that 20
 //           warps fit the registers;
 //   8 - 11  softmax, thread = virtual row: no exchange between threads; P goes
-//           back to TMEM over S as the A operand of P.V;
+//           back to TMEM over S as the A operand of P.V.  It waits for the values between the
+//           maximum and the probabilities, since their scales go into P (waiting after
+//           both was 1 to 2 % faster, but then a scale met weights that f16 had lost);
 //   12 - 19 split: f32 rows to f16 hi and lo in place (K K-major, V MN-major: the same
 //           bytes), four warps for the keys and four for the values.
 // TMEM: Q hi, lo (D columns), S / P two buffers (128), O and its running sum (2 D).
 // Every wait is bounded; a wait that gives up sets a bit of the device flag.
 //
 // Measured, headDim 128, 32 heads over 8: one row for each of 32 requests of 517 to 8111
-// rows, pages of 16: 250-275 us for 1.176 GB, 4.3-4.7 TB/s (63-69 % of the copy
-// rate).  Trees of 64 rows on 8 requests of 16384 to 32704, pages of 64: 595-623 us
-// for 217 GFLOP, 348-364 TFLOP/s of f32 products, 54-56 % of a third of the f16 rate.
+// rows, pages of 16: 251-283 us for 1.176 GB, 4.2-4.7 TB/s (61-69 % of the copy
+// rate).  Trees of 64 rows on 8 requests of 16384 to 32704, pages of 64: 579-622 us
+// for 217 GFLOP, 348-374 TFLOP/s of f32 products, 54-58 % of a third of the f16 rate.
 // What bounds it: the chain P.V(n - 1), S(n + 1), softmax(n + 1) on two score buffers:
 // 1900-2300 cycles of softmax a tile, one thread per row, against 1540 of MMAs and
 // the hand-overs between them.
