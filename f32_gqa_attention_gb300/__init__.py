@@ -794,7 +794,7 @@ def tree_plan(parents, cu_rows, lens, *, stream=None):
 def rope_at(x, positions, *, headDim, out=None, stream=None, **params):
     """op "rope" on a CUDA tensor x [T, heads*headDim] whose row t sits at
     positions[t] (int32; a row at a negative position is left as it was in
-    out); ``out=x`` turns it in place.  Params as make_rope_params."""
+    out, so without ``out`` it is unset); ``out=x`` turns it in place.  Params as make_rope_params."""
     import torch
     dev = x.device
     _need("x", x, torch.float32)
