@@ -40,7 +40,8 @@ EXPORTED = ("vtmu_attention_params_init", "vtmu_attention_workspace_size", "vtmu
             "vtmu_mla_params_init", "vtmu_mla_workspace_size", "vtmu_mla_attention", "vtmu_mla_decode_step",
             "vtmu_mla_decode_step_host_workspace_size", "vtmu_mla_decode_step_host",
             "vtmu_page_map", "vtmu_tree_plan", "vtmu_rope_at", "vtmu_paged_write", "vtmu_paged_params_init",
-            "vtmu_paged_workspace_size", "vtmu_paged_attention")
+            "vtmu_paged_workspace_size", "vtmu_paged_attention", "vtmu_paged_write_q8", "vtmu_paged_read_q8",
+            "vtmu_paged_q8_workspace_size", "vtmu_paged_attention_q8", "vtmu_norm_rope_params_init", "vtmu_norm_rope")
 NOALLOC_SCRATCH_BYTES = 8 << 20  # VTMU_NOALLOC_SCRATCH_BYTES
 
 
@@ -134,6 +135,23 @@ class vtmu_paged_params(ctypes.Structure):
     ]
 
 
+MAX_AXES = 4  # VTMU_MAX_AXES
+
+
+class vtmu_norm_rope_params(ctypes.Structure):
+    """Mirror of ``vtmu_norm_rope_params`` (include/vtmu_attention.h)."""
+    _fields_ = [
+        ("rope", vtmu_rope_params),
+        ("norm", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+        ("axes", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * MAX_AXES),
+        ("dealt", ctypes.c_int32),
+    ]
+
+
+VTMU_KV_INT8, VTMU_KV_E4M3 = 1, 2
 VTMU_PAGED_AUTO, VTMU_PAGED_CUDA_CORES, VTMU_PAGED_TENSOR_CORES = 0, 1, 2
 TREE_MAX_ROWS = 64  # VTMU_TREE_MAX_ROWS
 
@@ -218,6 +236,19 @@ def load_library():
         lib.vtmu_paged_workspace_size.restype = ctypes.c_int
         lib.vtmu_paged_attention.argtypes = [vp] * 11 + [G, vp, ctypes.c_size_t, vp]
         lib.vtmu_paged_attention.restype = ctypes.c_int
+        lib.vtmu_paged_write_q8.argtypes = [vp] * 4 + [i64, i32, i32, i32, vp, vp, vp, i64, vp]
+        lib.vtmu_paged_write_q8.restype = ctypes.c_int
+        lib.vtmu_paged_read_q8.argtypes = [vp] * 4 + [i64, i32, i32, i32, vp, vp, vp, i64, vp]
+        lib.vtmu_paged_read_q8.restype = ctypes.c_int
+        lib.vtmu_paged_q8_workspace_size.argtypes = [G, ctypes.POINTER(ctypes.c_size_t)]
+        lib.vtmu_paged_q8_workspace_size.restype = ctypes.c_int
+        lib.vtmu_paged_attention_q8.argtypes = [vp] * 5 + [i32] + [vp] * 8 + [G, vp, ctypes.c_size_t, vp]
+        lib.vtmu_paged_attention_q8.restype = ctypes.c_int
+        N = ctypes.POINTER(vtmu_norm_rope_params)
+        lib.vtmu_norm_rope_params_init.argtypes = [N]
+        lib.vtmu_norm_rope_params_init.restype = None
+        lib.vtmu_norm_rope.argtypes = [vp] * 6 + [i64, i32, i32, vp, N, vp]
+        lib.vtmu_norm_rope.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -417,6 +448,49 @@ def vtmu_paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, k_new, v
                                                _addr(lens), _addr(cu_rows), _addr(k_new), _addr(v_new),
                                                _addr(masks), _addr(positions), _addr(out), ctypes.byref(p),
                                                _addr(workspace), int(workspace_bytes), stream or None))
+
+
+def vtmu_paged_write_q8(k_pool, v_pool, k_scale, v_scale, pool_rows: int, kv_heads: int, head_dim: int, format: int,
+                        k_new, v_new, slots, rows: int, stream: int = 0) -> None:
+    _check(load_library().vtmu_paged_write_q8(_addr(k_pool), _addr(v_pool), _addr(k_scale), _addr(v_scale),
+                                              int(pool_rows), int(kv_heads), int(head_dim), int(format), _addr(k_new),
+                                              _addr(v_new), _addr(slots), int(rows), stream or None))
+
+
+def vtmu_paged_read_q8(k_pool, v_pool, k_scale, v_scale, pool_rows: int, kv_heads: int, head_dim: int, format: int,
+                       slots, k_out, v_out, rows: int, stream: int = 0) -> None:
+    _check(load_library().vtmu_paged_read_q8(_addr(k_pool), _addr(v_pool), _addr(k_scale), _addr(v_scale),
+                                             int(pool_rows), int(kv_heads), int(head_dim), int(format), _addr(slots),
+                                             _addr(k_out), _addr(v_out), int(rows), stream or None))
+
+
+def vtmu_paged_q8_workspace_size(p: vtmu_paged_params) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().vtmu_paged_q8_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+    return int(n.value)
+
+
+def vtmu_paged_attention_q8(q, k_pool, v_pool, k_scale, v_scale, format: int, block_table, lens, cu_rows, k_new, v_new,
+                            masks, positions, out, p: vtmu_paged_params, workspace, workspace_bytes: int,
+                            stream: int = 0) -> None:
+    _check(load_library().vtmu_paged_attention_q8(_addr(q), _addr(k_pool), _addr(v_pool), _addr(k_scale),
+                                                  _addr(v_scale), int(format), _addr(block_table), _addr(lens),
+                                                  _addr(cu_rows), _addr(k_new), _addr(v_new), _addr(masks),
+                                                  _addr(positions), _addr(out), ctypes.byref(p), _addr(workspace),
+                                                  int(workspace_bytes), stream or None))
+
+
+def vtmu_norm_rope_params_init() -> vtmu_norm_rope_params:
+    p = vtmu_norm_rope_params()
+    load_library().vtmu_norm_rope_params_init(ctypes.byref(p))
+    return p
+
+
+def vtmu_norm_rope(q, k, q_weight, k_weight, q_out, k_out, T: int, heads: int, kv_heads: int, positions,
+                   p: vtmu_norm_rope_params, stream: int = 0) -> None:
+    _check(load_library().vtmu_norm_rope(_addr(q), _addr(k), _addr(q_weight), _addr(k_weight), _addr(q_out),
+                                         _addr(k_out), int(T), int(heads), int(kv_heads), _addr(positions),
+                                         ctypes.byref(p), stream or None))
 
 
 def vtmu_device_error() -> int:
@@ -830,29 +904,19 @@ def paged_write(k_pool, v_pool, k_new, v_new, slots, *, stream=None):
     return k_pool, v_pool
 
 
-def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, headDim, pageSize, maxRows, kvHeads=None,
-                    tree=None, scale=None, softcap=None, window=None, sinks=None, kernel=VTMU_PAGED_AUTO, out=None,
-                    workspace=None, stream=None):
-    """op "attention" of a ragged batch over a paged cache on CUDA tensors
-    (vtmu_paged_attention): q [rows, heads*headDim], pools [pages*pageSize,
-    kvHeads*headDim], block_table [requests, maxPages], lens [requests] and
-    cu_rows [requests + 1] int32; maxRows bounds the rows of one request.
-    ``tree=(k_new, v_new, masks, positions)`` attends to drafted rows beside
-    the cache (positions may be None without a window); with a window the
-    cache's first ``sinks`` rows stay visible, drafted ones do not.  Returns
-    out [rows, heads*headDim]; rows of no request are not written."""
+def _paged_call(q, width, pool_rows, block_table, lens, cu_rows, heads, headDim, pageSize, maxRows, kvHeads, tree, scale,
+                softcap, window, sinks, kernel, out):
+    """What the paged attentions check and lay out alike: (params, out, k_new, v_new, masks, positions)."""
     import torch
     dev = q.device
     f32, i32 = torch.float32, torch.int32
-    for name, t in (("q", q), ("k_pool", k_pool), ("v_pool", v_pool)):
-        _need(name, t, f32, dev)
+    _need("q", q, f32, dev)
     for name, t in (("block_table", block_table), ("lens", lens), ("cu_rows", cu_rows)):
         _need(name, t, i32, dev)
     hk = heads if kvHeads is None else kvHeads
     rows, n = q.shape[0], lens.shape[0]
-    if (not 0 < pageSize < 1 << 31 or q.shape != (rows, heads * headDim) or k_pool.dim() != 2 or
-            k_pool.shape[1] != hk * headDim or k_pool.shape != v_pool.shape or k_pool.shape[0] % pageSize or
-            block_table.dim() != 2 or block_table.shape[0] != n or cu_rows.shape != (n + 1,)):
+    if (not 0 < pageSize < 1 << 31 or q.shape != (rows, heads * headDim) or width != hk * headDim or
+            pool_rows % pageSize or block_table.dim() != 2 or block_table.shape[0] != n or cu_rows.shape != (n + 1,)):
         raise ValueError("paged_attention: pageSize in 1 .. 2^31 - 1, q [rows, heads*headDim], pools [pages*pageSize, "
                          "kvHeads*headDim], block_table [requests, maxPages], lens [requests], cu_rows [requests + 1]")
     k_new = v_new = masks = positions = None
@@ -871,12 +935,35 @@ def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, hea
     _need("out", out, f32, dev)
     if out.shape != q.shape:
         raise ValueError("paged_attention: out [rows, heads*headDim]")
-    p = vtmu_paged_params(rows=rows, pages=k_pool.shape[0] // pageSize, requests=n,
+    p = vtmu_paged_params(rows=rows, pages=pool_rows // pageSize, requests=n,
                           max_rows=max(min(maxRows, rows), -1), page_size=pageSize,
                           max_pages=block_table.shape[1], heads=heads, kv_heads=hk, head_dim=headDim,
                           tree=0 if tree is None else 1, has_scale=0 if scale is None else 1,
                           scale=0.0 if scale is None else scale, softcap=softcap or 0.0, kernel=kernel,
                           window=window or 0, sinks=sinks or 0)
+    return p, out, k_new, v_new, masks, positions
+
+
+def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, headDim, pageSize, maxRows, kvHeads=None,
+                    tree=None, scale=None, softcap=None, window=None, sinks=None, kernel=VTMU_PAGED_AUTO, out=None,
+                    workspace=None, stream=None):
+    """op "attention" of a ragged batch over a paged cache on CUDA tensors
+    (vtmu_paged_attention): q [rows, heads*headDim], pools [pages*pageSize,
+    kvHeads*headDim], block_table [requests, maxPages], lens [requests] and
+    cu_rows [requests + 1] int32; maxRows bounds the rows of one request.
+    ``tree=(k_new, v_new, masks, positions)`` attends to drafted rows beside
+    the cache (positions may be None without a window); with a window the
+    cache's first ``sinks`` rows stay visible, drafted ones do not.  Returns
+    out [rows, heads*headDim]; rows of no request are not written."""
+    import torch
+    dev = q.device
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+        _need(name, t, torch.float32, dev)
+    if k_pool.dim() != 2 or k_pool.shape != v_pool.shape:
+        raise ValueError("paged_attention: pools [pages*pageSize, kvHeads*headDim]")
+    p, out, k_new, v_new, masks, positions = _paged_call(
+        q, k_pool.shape[1], k_pool.shape[0], block_table, lens, cu_rows, heads, headDim, pageSize, maxRows, kvHeads, tree,
+        scale, softcap, window, sinks, kernel, out)
     with _on(dev):
         nbytes = vtmu_paged_workspace_size(p)
         st = _raw_stream(dev) if stream is None else stream
@@ -884,3 +971,146 @@ def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, hea
         vtmu_paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, k_new, v_new, masks, positions, out, p,
                              buf, cap, st)
     return out
+
+
+# -------------------------------------------------------- 8-bit paged caches
+def _q8_format(dtype):
+    import torch
+    kind = {torch.int8: VTMU_KV_INT8, torch.float8_e4m3fn: VTMU_KV_E4M3}.get(dtype)
+    if kind is None:
+        raise ValueError("an 8-bit pool is an int8 or a float8_e4m3fn tensor")
+    return kind
+
+
+def _q8_pools(what, k_pool, v_pool, k_scale, v_scale):
+    """(format, pool rows, KV heads, headDim) of a cache's four tensors."""
+    import torch
+    dev = k_pool.device
+    kind = _q8_format(k_pool.dtype)
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+        _need(name, t, k_pool.dtype, dev)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _need(name, t, torch.float32, dev)
+    if (k_pool.dim() != 2 or v_pool.shape != k_pool.shape or k_scale.dim() != 2 or v_scale.shape != k_scale.shape or
+            k_scale.shape[0] != k_pool.shape[0] or k_scale.shape[1] < 1 or k_pool.shape[1] < k_scale.shape[1] or
+            k_pool.shape[1] % k_scale.shape[1]):
+        raise ValueError(f"{what}: pools [poolRows, kvHeads*headDim], scales [poolRows, kvHeads]")
+    return kind, k_pool.shape[0], k_scale.shape[1], k_pool.shape[1] // k_scale.shape[1]
+
+
+def paged_write_q8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slots, *, stream=None):
+    """paged_write into an 8-bit cache (vtmu_paged_write_q8): rows of k_new and v_new
+    (float32) are quantised, a scale for each KV head, into the pools (int8 or
+    float8_e4m3fn [poolRows, kvHeads*headDim], scales [poolRows, kvHeads]) at the
+    rows that slots (int32) names; rows whose slot is outside the pool are
+    skipped.  Returns (k_pool, v_pool, k_scale, v_scale)."""
+    import torch
+    dev = k_pool.device
+    kind, total, hk, d = _q8_pools("paged_write_q8", k_pool, v_pool, k_scale, v_scale)
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        _need(name, t, torch.float32, dev)
+    _need("slots", slots, torch.int32, dev)
+    n = slots.shape[0]
+    if slots.dim() != 1 or k_new.shape != (n, hk * d) or v_new.shape != k_new.shape:
+        raise ValueError("paged_write_q8: k_new and v_new [rows, kvHeads*headDim], slots [rows]")
+    with _on(dev):
+        st = _raw_stream(dev) if stream is None else stream
+        vtmu_paged_write_q8(k_pool, v_pool, k_scale, v_scale, total, hk, d, kind, k_new, v_new, slots, n, st)
+    return k_pool, v_pool, k_scale, v_scale
+
+
+def paged_read_q8(k_pool, v_pool, k_scale, v_scale, slots, *, out=None, stream=None):
+    """Rows of an 8-bit cache as float32 (vtmu_paged_read_q8): (k, v) [rows,
+    kvHeads*headDim] of the pool rows that slots (int32) names, zeros for slots
+    outside the pool.  ``out=(k, v)`` writes there."""
+    import torch
+    dev = k_pool.device
+    kind, total, hk, d = _q8_pools("paged_read_q8", k_pool, v_pool, k_scale, v_scale)
+    _need("slots", slots, torch.int32, dev)
+    n = slots.shape[0]
+    if out is None:
+        k, v = (torch.empty((n, hk * d), dtype=torch.float32, device=dev) for _ in range(2))
+    else:
+        k, v = out
+    for name, t in (("k", k), ("v", v)):
+        _need(name, t, torch.float32, dev)
+    if slots.dim() != 1 or k.shape != (n, hk * d) or v.shape != k.shape:
+        raise ValueError("paged_read_q8: slots [rows], out [rows, kvHeads*headDim]")
+    with _on(dev):
+        st = _raw_stream(dev) if stream is None else stream
+        vtmu_paged_read_q8(k_pool, v_pool, k_scale, v_scale, total, hk, d, kind, slots, k, v, n, st)
+    return k, v
+
+
+def paged_attention_q8(q, k_pool, v_pool, k_scale, v_scale, block_table, lens, cu_rows, *, heads, headDim, pageSize,
+                       maxRows, kvHeads=None, tree=None, scale=None, softcap=None, window=None, sinks=None,
+                       kernel=VTMU_PAGED_AUTO, out=None, workspace=None, stream=None):
+    """paged_attention over an 8-bit cache (vtmu_paged_attention_q8): pools int8 or
+    float8_e4m3fn [pages*pageSize, kvHeads*headDim] with scales [pages*pageSize,
+    kvHeads]; the drafted rows of a ``tree`` are float32.  Everything else as
+    paged_attention."""
+    dev = q.device
+    kind, total, hk, d = _q8_pools("paged_attention_q8", k_pool, v_pool, k_scale, v_scale)
+    if k_pool.device != dev or hk != (heads if kvHeads is None else kvHeads) or d != headDim:
+        raise ValueError("paged_attention_q8: pools on q's device, kvHeads scales and kvHeads*headDim codes a row")
+    p, out, k_new, v_new, masks, positions = _paged_call(
+        q, k_pool.shape[1], total, block_table, lens, cu_rows, heads, headDim, pageSize, maxRows, kvHeads, tree, scale,
+        softcap, window, sinks, kernel, out)
+    with _on(dev):
+        nbytes = vtmu_paged_q8_workspace_size(p)
+        st = _raw_stream(dev) if stream is None else stream
+        buf, cap = _scratch(workspace, dev, st, nbytes, counters=False)
+        vtmu_paged_attention_q8(q, k_pool, v_pool, k_scale, v_scale, kind, block_table, lens, cu_rows, k_new, v_new,
+                                masks, positions, out, p, buf, cap, st)
+    return out
+
+
+def make_norm_rope_params(*, headDim, norm=True, eps=1e-6, weightOffset=0.0, sections=None, dealt=False, **rope):
+    """A norm_rope params struct; rope parameters as make_rope_params."""
+    p = vtmu_norm_rope_params_init()
+    r = make_rope_params(headDim=headDim, **rope)
+    p.rope = r
+    p._rope = r  # keeps an invFreq array alive
+    p.norm = 1 if norm else 0
+    p.eps = float(eps)
+    p.weight_offset = float(weightOffset)
+    if sections is not None:
+        p.axes = len(sections)
+        for i, n in enumerate(sections[:MAX_AXES]):
+            p.sections[i] = int(n)
+    p.dealt = 1 if dealt else 0
+    return p
+
+
+def norm_rope(q, k, positions, *, headDim, qWeight=None, kWeight=None, norm=True, eps=1e-6, weightOffset=0.0,
+              sections=None, dealt=False, out=None, stream=None, **rope):
+    """An RMS norm of every head of q [T, heads*headDim] and k [T, kvHeads*headDim]
+    and op "rope" at positions [T], in one pass (vtmu_norm_rope).  ``k`` may be None.
+    With ``sections`` (pairs per axis) positions is [axes, T]; ``dealt``: the pairs
+    are dealt out to the axes in turn.  ``norm=False`` rotates only.
+    ``out=(q, k)`` works in place.  Rope parameters as make_rope_params.
+    Returns (q, k); rows at negative positions are left as they were in out."""
+    import torch
+    dev = q.device
+    f32 = torch.float32
+    _need("q", q, f32)
+    _need("positions", positions, torch.int32, dev)
+    q_out, k_out = (torch.empty_like(q), None if k is None else torch.empty_like(k)) if out is None else out
+    for name, t in (("k", k), ("qWeight", qWeight), ("kWeight", kWeight), ("q of out", q_out), ("k of out", k_out)):
+        if t is not None:
+            _need(name, t, f32, dev)
+    T = q.shape[0]
+    axes = 1 if sections is None else len(sections)
+    if (headDim < 1 or q.dim() != 2 or q.shape[1] % headDim or positions.numel() != axes * T or
+            positions.shape not in ((T,), (axes, T)) or q_out is None or q_out.shape != q.shape or
+            (k is None) != (k_out is None) or
+            (k is not None and (k.dim() != 2 or k.shape[0] != T or k.shape[1] % headDim or k_out.shape != k.shape)) or
+            any(w is not None and w.shape != (headDim,) for w in (qWeight, kWeight))):
+        raise ValueError("norm_rope: q and k [T, heads*headDim], positions [T] or [axes, T], weights [headDim], out as q and k")
+    p = make_norm_rope_params(headDim=headDim, norm=norm, eps=eps, weightOffset=weightOffset, sections=sections, dealt=dealt,
+                              **rope)
+    with _on(dev):
+        st = _raw_stream(dev) if stream is None else stream
+        vtmu_norm_rope(q, k, qWeight, kWeight, q_out, k_out, T, q.shape[1] // headDim,
+                       0 if k is None else k.shape[1] // headDim, positions, p, st)
+    return q_out, k_out

@@ -1,6 +1,7 @@
 // paged_ffma.cu -- attention of a ragged batch over a paged cache on the CUDA
-// cores: any headDim to 256, any page size, f32 throughout.  It serves the
-// shapes that the tensor-core kernel does not cover.
+// cores: any headDim to 256, any page size, f32 arithmetic throughout; the cache's rows
+// are f32, or 8-bit codes with a scale (paged_q8.h).  It serves the shapes that the
+// tensor-core kernels do not cover.
 //
 // For request b, query row t and head h, with virtual row v = t G + h % G of
 // KV head h / G:  x2_s = log2 e * softcap(scale q.k_s), p_s = 2^(x2_s - m),
@@ -21,6 +22,7 @@
 #include "attn_common.cuh"
 #include "paged.cuh"
 #include "paged_kernels.h"
+#include "paged_q8.cuh"
 
 namespace vtmu {
 namespace {
@@ -36,8 +38,10 @@ __device__ __forceinline__ float apply_cap(const PagedDesc& a, float dot) {
     return a.softcap_on ? a.cap_log2 * softcap_tanh(dot * a.qk_mul) : dot * a.qk_mul;
 }
 
-template <bool VEC4>
-__global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc a) {
+// FORM: what the pool holds.  Codes are taken as the numbers they stand for, a row's
+// scale multiplies its score and its value; drafted rows are f32 all the same.
+template <bool VEC4, int FORM>
+__global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc a, const Q8Pools p8) {
     __shared__ __align__(16) float sq[kR][kMaxD];
     __shared__ float so[kWarps][kR][kMaxD];
     __shared__ float sm[kWarps][kR], sl[kWarps][kR];
@@ -90,6 +94,8 @@ __global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc
         const int64_t s = c0 + lane;
         const float* krow = nullptr;  // null: rows of zeros (a page id outside the pool)
         const float* vrow = nullptr;
+        const uint8_t* kcode = nullptr;  // the same for rows of codes
+        int64_t coded = -1;
         const bool drafted = s >= len;
         if (s < total) {
             if (drafted) {
@@ -100,8 +106,13 @@ __global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc
                 const int64_t page = __ldg(a.block_table + (int64_t)b * a.max_pages + s / a.page_size);
                 if (page >= 0 && page < a.pages) {
                     const int64_t r = page * a.page_size + s % a.page_size;
-                    krow = a.k_pool + (r * a.Hk + hk) * D;
-                    vrow = a.v_pool + (r * a.Hk + hk) * D;
+                    if constexpr (FORM == kFormF32) {
+                        krow = a.k_pool + (r * a.Hk + hk) * D;
+                        vrow = a.v_pool + (r * a.Hk + hk) * D;
+                    } else {
+                        coded = r * a.Hk + hk;
+                        kcode = p8.k + coded * D;
+                    }
                 }
             }
         }
@@ -140,6 +151,29 @@ __global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc
                 }
             }
         }
+        if constexpr (FORM != kFormF32) {
+            if (any && kcode) {
+                if constexpr (VEC4) {
+                    for (int d = 0; d < D; d += 4) {
+                        const float4 kv = q8_values4<FORM>(__ldg(reinterpret_cast<const uint32_t*>(kcode + d)), 1.f);
+#pragma unroll
+                        for (int r = 0; r < kR; ++r) {
+                            const float4 qv = *reinterpret_cast<const float4*>(&sq[r][d]);
+                            x[r] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, x[r]))));
+                        }
+                    }
+                } else {
+                    for (int d = 0; d < D; ++d) {
+                        const float kv = q8_value<FORM>(__ldg(kcode + d));
+#pragma unroll
+                        for (int r = 0; r < kR; ++r) x[r] = fmaf(sq[r][d], kv, x[r]);
+                    }
+                }
+                const float ks = __ldg(p8.k_scale + coded);
+#pragma unroll
+                for (int r = 0; r < kR; ++r) x[r] *= ks;
+            }
+        }
         float p[kR];
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
@@ -167,12 +201,25 @@ __global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc
             }
             const float* vr = reinterpret_cast<const float*>(
                 __shfl_sync(FULL, reinterpret_cast<unsigned long long>(vrow), kk));
-            if (!need || !vr) continue;
+            const uint8_t* vc = nullptr;
+            float vs = 1.f;
+            if constexpr (FORM != kFormF32) {
+                const int64_t at = __shfl_sync(FULL, (long long)coded, kk);
+                if (at >= 0) {
+                    vc = p8.v + at * D;
+                    vs = __ldg(p8.v_scale + at);
+                }
+            }
+            if (!need || (!vr && !vc)) continue;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const int d = lane + 32 * i;
                 if (d < D) {
-                    const float vv = __ldg(vr + d);
+                    float vv;
+                    if constexpr (FORM == kFormF32)
+                        vv = __ldg(vr + d);
+                    else
+                        vv = vc ? q8_value<FORM>(__ldg(vc + d)) * vs : __ldg(vr + d);
 #pragma unroll
                     for (int r = 0; r < kR; ++r)
                         if (__float_as_uint(w[r]) != kUnseen) o[r][i] = fmaf(w[r], vv, o[r][i]);
@@ -215,16 +262,30 @@ __global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc
 
 }  // namespace
 
-cudaError_t launch_paged_ffma(const PagedDesc& a, cudaStream_t stream) {
+namespace {
+
+template <int FORM>
+cudaError_t launch_form(const PagedDesc& a, const Q8Pools& p, cudaStream_t stream) {
     const int64_t tiles = ((int64_t)a.max_rows * a.G + kR - 1) / kR;
     const dim3 grid((unsigned)tiles, (unsigned)a.Hk, (unsigned)a.B);
     const uintptr_t mis = reinterpret_cast<uintptr_t>(a.k_pool) | reinterpret_cast<uintptr_t>(a.v_pool) |
                           reinterpret_cast<uintptr_t>(a.k_new) | reinterpret_cast<uintptr_t>(a.v_new);
-    if (a.D % 4 == 0 && (mis & 15u) == 0)
-        paged_ffma_kernel<true><<<grid, 32 * kWarps, 0, stream>>>(a);
+    const uintptr_t mis4 = reinterpret_cast<uintptr_t>(p.k);  // codes of K: four a load
+    if (a.D % 4 == 0 && (mis & 15u) == 0 && (mis4 & 3u) == 0)
+        paged_ffma_kernel<true, FORM><<<grid, 32 * kWarps, 0, stream>>>(a, p);
     else
-        paged_ffma_kernel<false><<<grid, 32 * kWarps, 0, stream>>>(a);
+        paged_ffma_kernel<false, FORM><<<grid, 32 * kWarps, 0, stream>>>(a, p);
     return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_ffma(const PagedDesc& a, cudaStream_t stream) {
+    return launch_form<kFormF32>(a, Q8Pools{}, stream);
+}
+
+cudaError_t launch_paged_q8_ffma(const PagedDesc& a, const Q8Pools& p, cudaStream_t stream) {
+    return p.form == kFormInt8 ? launch_form<kFormInt8>(a, p, stream) : launch_form<kFormE4m3>(a, p, stream);
 }
 
 }  // namespace vtmu

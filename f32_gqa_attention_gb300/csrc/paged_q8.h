@@ -1,0 +1,48 @@
+// paged_q8.h -- the 8-bit paged cache: its formats and the launchers of the
+// kernels that write it, read it back and attend over it.
+#pragma once
+
+#include "paged_kernels.h"
+
+namespace vtmu {
+
+// An element is code x scale, one scale per pool row and KV head (the values
+// are vtmu_kv_format's).
+enum KvForm : int32_t { kFormF32 = 0, kFormInt8 = 1, kFormE4m3 = 2 };
+
+// The pools of one call: codes [pool rows, Hk * D], scales [pool rows, Hk].
+struct Q8Pools {
+    const uint8_t* k;
+    const uint8_t* v;
+    const float* k_scale;
+    const float* v_scale;
+    int32_t form;
+};
+
+struct Q8WriteArgs {
+    uint8_t* k_pool;
+    uint8_t* v_pool;
+    float* k_scale;
+    float* v_scale;
+    const float* k_new;
+    const float* v_new;
+    const int32_t* slots;
+    int64_t pool_rows, rows;
+    int32_t Hk, D, form;
+};
+cudaError_t launch_paged_write_q8(const Q8WriteArgs& a, cudaStream_t stream);
+
+struct Q8ReadArgs {
+    Q8Pools p;
+    const int32_t* slots;
+    float* k_out;
+    float* v_out;
+    int64_t pool_rows, rows;
+    int32_t Hk, D;
+};
+cudaError_t launch_paged_read_q8(const Q8ReadArgs& a, cudaStream_t stream);
+
+// a.k_pool and a.v_pool are not read.
+cudaError_t launch_paged_q8_ffma(const PagedDesc& a, const Q8Pools& p, cudaStream_t stream);
+
+}  // namespace vtmu

@@ -17,7 +17,9 @@
 #include <cuda_runtime.h>
 
 #include "kernels.h"
+#include "norm_rope.h"
 #include "paged_kernels.h"
+#include "paged_q8.h"
 #include "vtmu_attention.h"
 
 namespace {
@@ -1216,6 +1218,206 @@ vtmu_status vtmu_paged_attention(const float* q, const float* k_pool, const floa
     const cudaError_t e =
         tc ? vtmu::launch_paged_tc(a, device_sm_count(), workspace, stream) : vtmu::launch_paged_ffma(a, stream);
     if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+    return ok();
+}
+
+// Checks that the write and the read of an 8-bit cache share.
+static vtmu_status check_q8(const char* what, int64_t pool_rows, int32_t kv_heads, int32_t head_dim, int32_t format,
+                            int64_t rows) {
+    if (pool_rows < 0 || rows < 0 || kv_heads < 1 || head_dim < 1)
+        return fail(VTMU_ERR_INVALID, "%s: bad size (pool_rows %lld, rows %lld, kv_heads %d, head_dim %d)", what,
+                    (long long)pool_rows, (long long)rows, kv_heads, head_dim);
+    if (format != VTMU_KV_INT8 && format != VTMU_KV_E4M3)
+        return fail(VTMU_ERR_INVALID, "%s: format %d is not a vtmu_kv_format", what, format);
+    if (head_dim > 256) return fail(VTMU_ERR_UNSUPPORTED, "%s: head_dim %d > 256 is not supported", what, head_dim);
+    if ((pool_rows | rows | (int64_t)kv_heads * head_dim) >> 31 || rows * kv_heads >= ((int64_t)1 << 31))
+        return fail(VTMU_ERR_UNSUPPORTED, "%s: sizes must be below 2^31", what);
+    return VTMU_OK;
+}
+
+vtmu_status vtmu_paged_write_q8(void* k_pool, void* v_pool, float* k_scale, float* v_scale, int64_t pool_rows,
+                                int32_t kv_heads, int32_t head_dim, int32_t format, const float* k_new,
+                                const float* v_new, const int32_t* slots, int64_t rows, cudaStream_t stream) {
+    const vtmu_status st = check_q8("paged_write_q8", pool_rows, kv_heads, head_dim, format, rows);
+    if (st != VTMU_OK) return st;
+    if (rows == 0 || pool_rows == 0) return ok();
+    if (!k_pool || !v_pool || !k_scale || !v_scale || !k_new || !v_new || !slots)
+        return fail(VTMU_ERR_INVALID, "paged_write_q8: a pointer is NULL");
+    if (misaligned({k_scale, v_scale, k_new, v_new, slots}, 3u))
+        return fail(VTMU_ERR_INVALID, "paged_write_q8: scales, new rows and slots must be 4-byte aligned");
+    const size_t width = (size_t)kv_heads * head_dim, pb = (size_t)pool_rows * width, sb = (size_t)pool_rows * kv_heads * 4;
+    const Span spans[] = {{k_pool, pb}, {v_pool, pb}, {k_scale, sb}, {v_scale, sb}, {k_new, (size_t)rows * width * 4},
+                          {v_new, (size_t)rows * width * 4}, {slots, (size_t)rows * 4}};
+    if (outputs_overlap(spans, 4, 7)) return fail(VTMU_ERR_INVALID, "paged_write_q8: a pool overlaps another buffer");
+    const vtmu::Q8WriteArgs a{static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool), k_scale, v_scale, k_new, v_new,
+                              slots, pool_rows, rows, kv_heads, head_dim, format};
+    const cudaError_t e = vtmu::launch_paged_write_q8(a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "paged_write_q8 launch");
+    return ok();
+}
+
+vtmu_status vtmu_paged_read_q8(const void* k_pool, const void* v_pool, const float* k_scale, const float* v_scale,
+                               int64_t pool_rows, int32_t kv_heads, int32_t head_dim, int32_t format,
+                               const int32_t* slots, float* k_out, float* v_out, int64_t rows, cudaStream_t stream) {
+    const vtmu_status st = check_q8("paged_read_q8", pool_rows, kv_heads, head_dim, format, rows);
+    if (st != VTMU_OK) return st;
+    if (rows == 0) return ok();
+    if ((pool_rows > 0 && (!k_pool || !v_pool || !k_scale || !v_scale)) || !slots || !k_out || !v_out)
+        return fail(VTMU_ERR_INVALID, "paged_read_q8: a pointer is NULL");
+    if (misaligned({k_scale, v_scale, slots, k_out, v_out}, 3u))
+        return fail(VTMU_ERR_INVALID, "paged_read_q8: scales, slots and outputs must be 4-byte aligned");
+    const size_t width = (size_t)kv_heads * head_dim, pb = (size_t)pool_rows * width, sb = (size_t)pool_rows * kv_heads * 4,
+                 ob = (size_t)rows * width * 4;
+    const Span spans[] = {{k_out, ob}, {v_out, ob}, {k_pool, pb}, {v_pool, pb}, {k_scale, sb}, {v_scale, sb},
+                          {slots, (size_t)rows * 4}};
+    if (outputs_overlap(spans, 2, 7)) return fail(VTMU_ERR_INVALID, "paged_read_q8: an output overlaps another buffer");
+    const vtmu::Q8ReadArgs a{{static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), k_scale, v_scale,
+                              format},
+                             slots, k_out, v_out, pool_rows, rows, kv_heads, head_dim};
+    const cudaError_t e = vtmu::launch_paged_read_q8(a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "paged_read_q8 launch");
+    return ok();
+}
+
+vtmu_status vtmu_paged_q8_workspace_size(const vtmu_paged_params* p, size_t* bytes) {
+    if (!bytes) return fail(VTMU_ERR_INVALID, "bytes is NULL");
+    vtmu::PagedDesc a;
+    const vtmu_status st = resolve_paged(p, &a);
+    if (st != VTMU_OK) return st;
+    if (p->kernel == VTMU_PAGED_TENSOR_CORES)
+        return fail(VTMU_ERR_UNSUPPORTED, "paged q8: kernel TENSOR_CORES does not cover headDim %d", a.D);
+    *bytes = 0;
+    return ok();
+}
+
+vtmu_status vtmu_paged_attention_q8(const float* q, const void* k_pool, const void* v_pool, const float* k_scale,
+                                    const float* v_scale, int32_t format, const int32_t* block_table,
+                                    const int32_t* lens, const int32_t* cu_rows, const float* k_new, const float* v_new,
+                                    const uint64_t* masks, const int32_t* positions, float* out,
+                                    const vtmu_paged_params* p, void* workspace, size_t workspace_bytes,
+                                    cudaStream_t stream) {
+    vtmu::PagedDesc a;
+    const vtmu_status st = resolve_paged(p, &a);
+    if (st != VTMU_OK) return st;
+    if (format != VTMU_KV_INT8 && format != VTMU_KV_E4M3)
+        return fail(VTMU_ERR_INVALID, "paged q8: format %d is not a vtmu_kv_format", format);
+    if (a.rows == 0 || a.max_rows == 0) return ok();
+    if (!q || !out || !lens || !cu_rows || !block_table || (a.pages > 0 && (!k_pool || !v_pool || !k_scale || !v_scale)))
+        return fail(VTMU_ERR_INVALID, "paged q8: q, out, lens, cu_rows, block_table, a pool or its scales are NULL");
+    if (a.tree ? (!k_new || !v_new || !masks || (a.window > 0 && !positions))
+               : (k_new || v_new || masks || positions))
+        return fail(VTMU_ERR_INVALID, "paged q8: tree arguments (k_new, v_new, masks, positions with a window) and "
+                                      "params.tree disagree");
+    if (misaligned({q, k_scale, v_scale, block_table, lens, cu_rows, k_new, v_new, positions, out}, 3u) ||
+        misaligned({masks}, 7u))
+        return fail(VTMU_ERR_INVALID, "paged q8: a pointer is misaligned");
+    const size_t qb = (size_t)a.rows * a.H * a.D * 4, nb = (size_t)a.rows * a.Hk * a.D * 4,
+                 sb = (size_t)a.pages * a.page_size * a.Hk * 4, pb = sb / 4 * a.D, b4 = (size_t)a.B * 4;
+    const Span spans[] = {{out, qb}, {q, qb}, {k_pool, pb}, {v_pool, pb}, {k_scale, sb}, {v_scale, sb},
+                          {block_table, b4 * (size_t)a.max_pages}, {lens, b4}, {cu_rows, b4 + 4}, {k_new, nb}, {v_new, nb},
+                          {masks, (size_t)a.rows * 8}, {positions, (size_t)a.rows * 4}};
+    if (outputs_overlap(spans, 1, 13)) return fail(VTMU_ERR_INVALID, "paged q8: out overlaps an input");
+    a.q = q;
+    a.block_table = block_table;
+    a.lens = lens;
+    a.cu_rows = cu_rows;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.masks = masks;
+    a.positions = positions;
+    a.out = out;
+    const vtmu::Q8Pools pools{static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), k_scale, v_scale,
+                              format};
+    if (p->kernel == VTMU_PAGED_TENSOR_CORES)
+        return fail(VTMU_ERR_UNSUPPORTED, "paged q8: kernel TENSOR_CORES does not cover headDim %d", a.D);
+    (void)workspace;
+    (void)workspace_bytes;
+    const cudaError_t e = vtmu::launch_paged_q8_ffma(a, pools, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "paged q8 attention launch");
+    return ok();
+}
+
+void vtmu_norm_rope_params_init(vtmu_norm_rope_params* p) {
+    if (!p) return;
+    std::memset(p, 0, sizeof(*p));
+    vtmu_rope_params_init(&p->rope);
+    p->norm = 1;
+    p->eps = 1e-6f;
+    p->axes = 1;
+}
+
+vtmu_status vtmu_norm_rope(const float* q, const float* k, const float* q_weight, const float* k_weight, float* q_out,
+                           float* k_out, int64_t T, int32_t heads, int32_t kv_heads, const int32_t* positions,
+                           const vtmu_norm_rope_params* p, cudaStream_t stream) {
+    if (!p) return fail(VTMU_ERR_INVALID, "norm_rope params is NULL");
+    vtmu::NormRopeArgs a;
+    std::memset(&a, 0, sizeof(a));
+    const vtmu_status st = resolve_rope(&p->rope, &a.r);
+    if (st != VTMU_OK) return st;
+    if (T < 0 || heads <= 0 || kv_heads < 0)
+        return fail(VTMU_ERR_INVALID, "norm_rope: T %lld, heads %d and kv_heads %d must be >= 0, > 0 and >= 0",
+                    (long long)T, heads, kv_heads);
+    if (p->norm != 0 && p->norm != 1) return fail(VTMU_ERR_INVALID, "norm_rope: norm %d is not 0 or 1", p->norm);
+    if (!(p->eps >= 0.f) || !std::isfinite(p->eps)) return fail(VTMU_ERR_INVALID, "norm_rope: eps must be finite and >= 0");
+    if (!std::isfinite(p->weight_offset)) return fail(VTMU_ERR_INVALID, "norm_rope: weight_offset must be finite");
+    if (p->axes < 1 || p->axes > VTMU_MAX_AXES)
+        return fail(VTMU_ERR_INVALID, "norm_rope: axes %d outside 1..%d", p->axes, VTMU_MAX_AXES);
+    if (p->axes > 1) {
+        int64_t sum = 0;
+        for (int i = 0; i < p->axes; ++i) {
+            if (p->sections[i] < 0) return fail(VTMU_ERR_INVALID, "norm_rope: sections[%d] is negative", i);
+            sum += p->sections[i];
+        }
+        if (sum != a.r.half)
+            return fail(VTMU_ERR_INVALID, "norm_rope: sections add up to %lld pairs of %d", (long long)sum, a.r.half);
+        int dealt[VTMU_MAX_AXES] = {0, 0, 0, 0};
+        for (int j = 0, run = 0, left = p->sections[0]; j < a.r.half; ++j) {
+            if (p->dealt) {
+                const int i = j % p->axes;
+                a.axis[j] = (uint8_t)(j < p->axes * (int64_t)p->sections[i] ? i : 0);
+            } else {
+                while (left == 0) left = p->sections[++run];
+                --left;
+                a.axis[j] = (uint8_t)run;
+            }
+            ++dealt[a.axis[j]];
+        }
+        for (int i = 1; i < p->axes; ++i)
+            if (dealt[i] != p->sections[i])
+                return fail(VTMU_ERR_INVALID, "norm_rope: sections[%d] = %d pairs do not fit when dealt out in turn", i,
+                            p->sections[i]);
+    }
+    if (!p->norm && (q_weight || k_weight)) return fail(VTMU_ERR_INVALID, "norm_rope: weights without a norm");
+    if ((int64_t)heads * p->rope.head_dim >= ((int64_t)1 << 31) || (int64_t)kv_heads * p->rope.head_dim >= ((int64_t)1 << 31) ||
+        (int64_t)heads + kv_heads >= ((int64_t)1 << 31) - 256)
+        return fail(VTMU_ERR_UNSUPPORTED, "norm_rope: heads x headDim must be below 2^31");
+    if (T == 0) return ok();
+    if (!q || !q_out || !positions || (kv_heads > 0 ? !k || !k_out : k || k_out || k_weight))
+        return fail(VTMU_ERR_INVALID, "norm_rope: q, q_out, positions, and k, k_out exactly with kv_heads, must be given");
+    if (misaligned({q, k, q_weight, k_weight, q_out, k_out, positions}, 3u))
+        return fail(VTMU_ERR_INVALID, "norm_rope: pointers must be 4-byte aligned");
+    const size_t wb = (size_t)p->rope.head_dim * 4, qb = (size_t)T * heads * wb, kb = (size_t)T * kv_heads * wb;
+    const Span spans[] = {{q_out, qb}, {k_out, kb}, {q_out == q ? nullptr : q, qb}, {k_out == k ? nullptr : k, kb},
+                          {q_weight, wb}, {k_weight, wb}, {positions, (size_t)p->axes * T * 4}};
+    if (outputs_overlap(spans, 2, 7))
+        return fail(VTMU_ERR_INVALID, "norm_rope: an output overlaps another buffer (other than its own input, in place)");
+    a.q = q;
+    a.k = k;
+    a.qw = q_weight;
+    a.kw = k_weight;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.positions = positions;
+    a.T = T;
+    a.H = heads;
+    a.Hk = kv_heads;
+    a.D = p->rope.head_dim;
+    a.axes = p->axes;
+    a.norm = p->norm;
+    a.eps = p->eps;
+    a.weight_offset = p->weight_offset;
+    const cudaError_t e = vtmu::launch_norm_rope(a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "norm_rope launch");
     return ok();
 }
 

@@ -688,6 +688,126 @@ VTMU_API vtmu_status vtmu_paged_attention(const float* q, const float* k_pool, c
                                           size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * ---- 8-bit paged caches ------------------------------------------------------
+ *
+ * A paged cache whose rows are codes of 8 bits with an f32 scale for each pool
+ * row and KV head: k_pool, v_pool [pages * page_size, kvHeads * headDim] bytes,
+ * k_scale, v_scale [pages * page_size, kvHeads] f32; an element is code x scale.
+ * It holds what an f32 pool of (almost) four times its size does.  Pages, tables,
+ * slots, packed rows and lengths are those of the f32 paged cache, and
+ * vtmu_page_map and vtmu_tree_plan serve both.  A step: vtmu_norm_rope (or
+ * vtmu_rope_at) on q and the new keys, vtmu_paged_write_q8, and
+ * vtmu_paged_attention_q8; drafted rows of a tree stay f32 beside the cache until
+ * their acceptance writes them.
+ */
+typedef enum vtmu_kv_format {
+    VTMU_KV_INT8 = 1, /* -127..127; scale = max|x| / 127 rounded to f32 */
+    VTMU_KV_E4M3 = 2  /* OCP e4m3; scale = the least power of two with max|x| <= 448 scale */
+} vtmu_kv_format;
+
+/*
+ * vtmu_paged_write into an 8-bit cache: for r < rows, the KV heads of k_new[r, :]
+ * and v_new[r, :] are quantised and become row slots[r] of the pools.  For each
+ * head x of headDim elements the scale is the format's, but at least 2^-126, and a
+ * code is the nearest one to x / scale, ties to even (the exact quotient).  A head with an
+ * element that is not finite is stored as NaN: scale NaN, codes 0.  A row whose
+ * slot is outside 0 .. pool_rows - 1 is skipped, pool rows without a slot are
+ * untouched; the slots of one call are distinct.
+ *   k_new, v_new [rows, kv_heads*head_dim]: f32, DEVICE; slots [rows]: int32,
+ *   DEVICE.  None may overlap another.  head_dim 1..256.
+ * Errors: VTMU_ERR_INVALID (null pointer with rows > 0, bad size or format,
+ * misaligned or overlapping buffers), VTMU_ERR_UNSUPPORTED (head_dim above 256,
+ * a size of 2^31 or more), VTMU_ERR_CUDA.
+ */
+VTMU_API vtmu_status vtmu_paged_write_q8(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                                         int64_t pool_rows, int32_t kv_heads, int32_t head_dim, int32_t format,
+                                         const float* k_new, const float* v_new, const int32_t* slots, int64_t rows,
+                                         cudaStream_t stream);
+
+/*
+ * Rows of an 8-bit cache as f32: k_out[r, :] and v_out[r, :] get code x scale
+ * (one rounding to f32) of pool row slots[r], and zeros where the slot is
+ * outside 0 .. pool_rows - 1.  A slot may come more than once.
+ *   k_out, v_out [rows, kv_heads*head_dim]: f32, DEVICE, overlapping nothing.
+ * Errors: as vtmu_paged_write_q8.
+ */
+VTMU_API vtmu_status vtmu_paged_read_q8(const void* k_pool, const void* v_pool, const float* k_scale,
+                                        const float* v_scale, int64_t pool_rows, int32_t kv_heads, int32_t head_dim,
+                                        int32_t format, const int32_t* slots, float* k_out, float* v_out, int64_t rows,
+                                        cudaStream_t stream);
+
+/* Scratch bytes that vtmu_paged_attention_q8 needs for `p`.  Errors: those of
+ * vtmu_paged_attention's parameter checks. */
+VTMU_API vtmu_status vtmu_paged_q8_workspace_size(const vtmu_paged_params* p, size_t* bytes);
+
+/*
+ * vtmu_paged_attention over an 8-bit cache: the same rows, masks, positions,
+ * window, sinks, softcap and errors, with K and V of the cache code x scale
+ * (k_new and v_new of a tree are f32).  A head whose scale is NaN is a key or a value
+ * that is not finite.  `format`: vtmu_kv_format.
+ * Kernels: p->kernel forces the CUDA cores or the tensor cores; AUTO takes the tensor
+ * cores where they cover the call (headDim 64 or 128, 16-byte aligned q, out, pools and, in
+ * a tree, k_new and v_new).  Scores and sums are f32 in both.  The tensor cores
+ * take the codes as they are, keep 22 bits of the largest element of each row and head of q
+ * and of drafted rows, and weights, or the products of weight and value scale, to 2^-36
+ * of the largest among a tile's keys.
+ */
+VTMU_API vtmu_status vtmu_paged_attention_q8(const float* q, const void* k_pool, const void* v_pool,
+                                             const float* k_scale, const float* v_scale, int32_t format,
+                                             const int32_t* block_table, const int32_t* lens, const int32_t* cu_rows,
+                                             const float* k_new, const float* v_new, const uint64_t* masks,
+                                             const int32_t* positions, float* out, const vtmu_paged_params* p,
+                                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Most position axes of vtmu_norm_rope. */
+#define VTMU_MAX_AXES 4
+
+/*
+ * Parameters of vtmu_norm_rope; fill with vtmu_norm_rope_params_init(), then set
+ * fields (rope.head_dim at least).
+ */
+typedef struct vtmu_norm_rope_params {
+    vtmu_rope_params rope;   /* as for vtmu_rope */
+    int32_t norm;            /* 1: the norm below comes before the rotation; 0: no norm, no weights */
+    float eps;               /* added to the mean of the squares; >= 0, finite */
+    float weight_offset;     /* added to every weight (1 where a checkpoint stores weight - 1) */
+    int32_t axes;            /* position axes, 1..VTMU_MAX_AXES */
+    int32_t sections[VTMU_MAX_AXES]; /* pairs that each axis turns, rotary_dim / 2 in all; not read with one axis */
+    int32_t dealt;           /* 0: the pairs of an axis follow one another; 1: dealt out in turn (below) */
+} vtmu_norm_rope_params;
+
+/* Writes the defaults: rope's (vtmu_rope_params_init), norm 1, eps 1e-6,
+ * weight_offset 0, one axis. */
+VTMU_API void vtmu_norm_rope_params_init(vtmu_norm_rope_params* p);
+
+/*
+ * The norm of every head of a step's queries and keys and op "rope" at given
+ * positions, in one launch: for each row t and head x of q and of k,
+ *   y = x / sqrt(mean(x^2) + eps) * (weight + weight_offset)   (norm == 1)
+ * and then pair j of y turns by positions[axis(j)][t] * inv_freq[j] as in
+ * vtmu_rope.  With several axes (time, height and width of an image's patch, say)
+ * the pairs are shared out: sections[0] pairs for axis 0, then sections[1] for axis 1, and
+ * so on; or `dealt`, in turn: pair j turns by axis a = j % axes where j < axes *
+ * sections[a], and by axis 0 elsewhere (the sections of the axes from 1 on must fit in:
+ * each then has its number of pairs).
+ *   q, q_out [T, heads*head_dim], k, k_out [T, kv_heads*head_dim]: f32, DEVICE;
+ *   q_out == q and k_out == k work in place, otherwise nothing may overlap.
+ *   kv_heads == 0: queries alone, k and k_out are NULL.
+ *   q_weight, k_weight [head_dim]: f32, DEVICE, or NULL for weights of one (then
+ *   weight_offset is not added); NULL without a norm.
+ *   positions [axes, T]: int32, DEVICE.  A row with a negative position on an axis
+ *   is left as it was in q_out and k_out.
+ * Squares are summed in f32, of elements scaled where their squares leave its range.  A
+ * head of zeros with eps == 0 is 0 / 0, NaN.
+ * Errors: those of vtmu_rope, VTMU_ERR_INVALID (axes, sections, eps or
+ * weight_offset out of range, weights without a norm, null, misaligned or
+ * overlapping buffers), VTMU_ERR_CUDA.
+ */
+VTMU_API vtmu_status vtmu_norm_rope(const float* q, const float* k, const float* q_weight, const float* k_weight,
+                                    float* q_out, float* k_out, int64_t T, int32_t heads, int32_t kv_heads,
+                                    const int32_t* positions, const vtmu_norm_rope_params* p, cudaStream_t stream);
+
+/*
  * Kernel-side failures.  Every wait inside a kernel (TMA stage arrival,
  * stage release) gives up after one second instead of hanging the GPU; the
  * kernel then sets a bit in a device flag, abandons its output and returns.
