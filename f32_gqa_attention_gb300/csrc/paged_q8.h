@@ -44,5 +44,9 @@ cudaError_t launch_paged_read_q8(const Q8ReadArgs& a, cudaStream_t stream);
 
 // a.k_pool and a.v_pool are not read.
 cudaError_t launch_paged_q8_ffma(const PagedDesc& a, const Q8Pools& p, cudaStream_t stream);
+// Warp-wide f16 products: headDim 64 or 128; q, out, pools and new rows 16-byte aligned.
+bool paged_q8_mma_supported(const PagedDesc& a);
+size_t paged_q8_mma_workspace(const PagedDesc& a);
+cudaError_t launch_paged_q8_mma(const PagedDesc& a, const Q8Pools& p, int num_sms, void* workspace, cudaStream_t stream);
 
 }  // namespace vtmu

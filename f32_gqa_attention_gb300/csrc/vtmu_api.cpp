@@ -1284,9 +1284,11 @@ vtmu_status vtmu_paged_q8_workspace_size(const vtmu_paged_params* p, size_t* byt
     vtmu::PagedDesc a;
     const vtmu_status st = resolve_paged(p, &a);
     if (st != VTMU_OK) return st;
-    if (p->kernel == VTMU_PAGED_TENSOR_CORES)
-        return fail(VTMU_ERR_UNSUPPORTED, "paged q8: kernel TENSOR_CORES does not cover headDim %d", a.D);
-    *bytes = 0;
+    // AUTO may fall back to the CUDA cores by the pointers' alignment.
+    const bool tc = p->kernel != VTMU_PAGED_CUDA_CORES && vtmu::paged_q8_mma_supported(a);
+    if (!tc && p->kernel == VTMU_PAGED_TENSOR_CORES)
+        return fail(VTMU_ERR_UNSUPPORTED, "paged q8: kernel TENSOR_CORES covers headDim 64 and 128 (got headDim %d)", a.D);
+    *bytes = tc ? vtmu::paged_q8_mma_workspace(a) : 0;
     return ok();
 }
 
@@ -1328,11 +1330,23 @@ vtmu_status vtmu_paged_attention_q8(const float* q, const void* k_pool, const vo
     a.out = out;
     const vtmu::Q8Pools pools{static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), k_scale, v_scale,
                               format};
-    if (p->kernel == VTMU_PAGED_TENSOR_CORES)
-        return fail(VTMU_ERR_UNSUPPORTED, "paged q8: kernel TENSOR_CORES does not cover headDim %d", a.D);
-    (void)workspace;
-    (void)workspace_bytes;
-    const cudaError_t e = vtmu::launch_paged_q8_ffma(a, pools, stream);
+    bool tc = p->kernel != VTMU_PAGED_CUDA_CORES && vtmu::paged_q8_mma_supported(a);
+    if (tc && misaligned({q, k_pool, v_pool, k_new, v_new, out}, 15u)) tc = false;
+    if (!tc && p->kernel == VTMU_PAGED_TENSOR_CORES)
+        return fail(VTMU_ERR_UNSUPPORTED,
+                    "paged q8: kernel TENSOR_CORES covers headDim 64 and 128 with 16-byte aligned q, pools, k_new, v_new and "
+                    "out (got headDim %d)",
+                    a.D);
+    if (tc) {
+        const size_t need = vtmu::paged_q8_mma_workspace(a);
+        if (!workspace || workspace_bytes < need)
+            return fail(VTMU_ERR_WORKSPACE, "paged q8 attention needs a workspace of %zu bytes (got %zu)", need,
+                        workspace ? workspace_bytes : (size_t)0);
+        if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+            return fail(VTMU_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    }
+    const cudaError_t e = tc ? vtmu::launch_paged_q8_mma(a, pools, device_sm_count(), workspace, stream)
+                             : vtmu::launch_paged_q8_ffma(a, pools, stream);
     if (e != cudaSuccess) return cuda_fail(e, "paged q8 attention launch");
     return ok();
 }

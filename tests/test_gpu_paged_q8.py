@@ -27,7 +27,7 @@ from test_gpu_paged import check, dev  # noqa: E402
 
 FORMS = [q8.INT8, q8.E4M3]
 DTYPE = {q8.INT8: torch.int8, q8.E4M3: torch.float8_e4m3fn}
-CUDA = vtmu.VTMU_PAGED_CUDA_CORES
+CUDA, TENSOR = vtmu.VTMU_PAGED_CUDA_CORES, vtmu.VTMU_PAGED_TENSOR_CORES
 
 
 def codes(a, form):
@@ -267,7 +267,7 @@ SHAPES = [  # lens, counts, heads, kvHeads, D, page, tree, attention arguments
 
 
 def kernels_of(D):
-    return [CUDA]
+    return [CUDA, TENSOR] if D in (64, 128) else [CUDA, vtmu.VTMU_PAGED_AUTO]
 
 
 @pytest.mark.parametrize("form", FORMS)
