@@ -18,20 +18,23 @@
 // a weight is at most 2^5, and has 2^10 as a factor in f16: kept to 2^-35 of the
 // largest product.
 //
-// Work.  A worker is a warp; Hk neighbouring ones (a team) walk the same keys for
-// their KV heads, so that a pool row is read whole by warps that run side by side.
-// Lengths are known to the device alone: the teams of one wave of CTAs divide the tiles
-// of all (request, row block) units evenly.  A unit cut by a team's end leaves
-// partials (m, l, o / l) that q8_merge_kernel joins in a fixed order.  Nothing is
-// shared between warps but the request table: no barrier after it.
+// Work.  Lengths are known to the device alone, so the launch is one persistent CTA per
+// SM, and the CTAs divide the tiles of all (request, head block, row block) units
+// evenly.  A tile is 32 keys for each of kg key groups, hb KV heads wide (all of them up
+// to eight), hb kg <= 8: a consumer warp per head and key group, which shares nothing with
+// the others until the piece ends.  A CTA so reads whole rows of the pool; with a worker
+// per head that loaded its own 128 bytes of each row, the heads drifted apart and HBM
+// gave 3.2 TB/s.  Key groups are joined inside the CTA; a unit cut by a CTA's end leaves
+// partials (m, l, o / l) that q8_merge_kernel joins in a fixed order: no atomics.
 //
-// Memory.  A warp keeps kStages tiles of K and V codes and scales in flight by 16-byte
-// asynchronous copies, a row index per lane looked up a tile ahead.  Fragments come from
-// shared memory 16 bytes a lane: the order of the contraction is free, so a lane takes
+// Memory.  Producer warps look up pages and copy rows and scales kStages tiles ahead, in
+// 16-byte asynchronous copies: 6.2 TB/s with nothing else to do, where bulk copies of a row
+// (1 KB) gave 4.5 TB/s, of a head (128 bytes) 0.7, and only whole pages 6.3.  Consumers
+// read fragments 16 bytes a lane: the order of the contraction is free, so a lane takes
 // 16 neighbouring channels of a K row (its channels of four k-steps), and of V rows the
-// channels that are its rows of the transposed product: O^T = V^T P^T, S^T = K q^T, keys
-// and channels fill the 16-row side, 8 virtual rows the other.  P^T changes layout by
-// movmatrix.
+// channels that are its rows of the transposed product: S^T = K q^T, O^T = V^T P^T, keys and
+// channels fill the 16-row side, 8 virtual rows the other.  P^T changes layout by movmatrix.
+// Every wait is bounded; one that gives up sets a bit of the device flag.
 #include <cstring>
 
 #include "attn_common.cuh"
@@ -40,38 +43,45 @@
 #include "paged_q8.cuh"
 #include "paged_q8_mma.cuh"
 #include "pdl.cuh"
+#include "softcap.cuh"
+#include "tma_sync.cuh"
 
 namespace vtmu {
+
+__device__ unsigned int g_q8_device_error;
+
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int kKT = 32;  // keys per tile
+constexpr int kKT = 32;  // keys of a warp's tile
 constexpr float kLazy = 3.f;     // log2 by which a maximum is beaten before it moves
 constexpr float kSlack = 4.f;    // a scale may be this times 2^r
 constexpr float kShift = 10.f;   // weights in f16: times 2^10
 constexpr float kLeastRef = -116.f;
-enum : int { kFirst = 1, kLast = 2, kSlotShift = 2 };  // of a tile; slot + 1 above them
 
 struct MmaArgs {
     PagedDesc a;
     Q8Pools p;
     int32_t page_shift;  // log2 page_size, or -1
-    float* part_m;       // [2 teams][Hk][NV]: slot 0 goes on with a unit, slot 1 starts one
+    int32_t hb, blocks;  // heads of a block, head blocks
+    int32_t kg;          // key groups
+    int32_t wide;        // four scales of a row may be one copy
+    int32_t stage;       // bytes of one
+    float* part_m;       // [3 CTAs][8 warps][NV]: slot 0 goes on with a unit, slot 1 starts one, 2: key groups
     float* part_l;
-    float* part_o;       // [2 teams][Hk][NV][D], divided by l
-    int4* head;          // [teams]: last team, row block and request of the unit a team starts
+    float* part_o;       // [3 CTAs][8 warps][NV][D], divided by l
+    int4* head;          // [2 CTAs]: the unit a CTA starts: last CTA, virtual rows [y, z), first packed row; first head
 };
 
-template <int D, int NT>
-struct Cfg {
-    static constexpr int kWarps = 8, kStages = 3;
-    static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kTileBytes = kKT * D;                      // of K or V
-    static constexpr int kStage = 2 * kTileBytes + 2 * kKT * 4 + 16;  // and scales, and what the tile is
-    static constexpr size_t smem(int requests) {
-        return (size_t)kWarps * kStages * kStage + (size_t)(requests + 1) * 8;
-    }
-    static_assert(kStage % 16 == 0, "16-byte copies");
+// A tile in shared memory: K rows, V rows, scales [row][head] of K and of V, what it is.
+constexpr int kConsumers = 8;  // at most
+constexpr int kProducers = 4;
+constexpr int kStages = 3, kThreads = 32 * (kConsumers + kProducers);
+constexpr size_t kSmemMost = 232448 - 1024;  // less the static part
+
+enum : unsigned int {
+    kErrQ8Load = 1u << 3,  // the paged kernels' bits: a tile that did not come,
+    kErrQ8Free = 1u << 4,  // a stage that was not given back
 };
 
 // ---- the list of tiles: as in the f32 kernel, with 32 keys a tile and the drafted rows'
@@ -91,7 +101,7 @@ __device__ __forceinline__ Req load_req(const PagedDesc& a, int b) {
     r.len = (int)clamp64(__ldg(a.lens + b), 0, (int64_t)a.max_pages * a.page_size);
     return r;
 }
-__device__ __forceinline__ Units units_of(const PagedDesc& a, const Req& r) {
+__device__ __forceinline__ Units units_of(const PagedDesc& a, const Req& r, int kKT) {
     Units t;
     int64_t lo = 0;
     if (a.window > 0) lo = clamp64((a.tree ? (int64_t)r.len : (int64_t)r.len - r.n) - a.window + 1, 0, r.len);
@@ -110,20 +120,26 @@ __device__ __forceinline__ Units units_of(const PagedDesc& a, const Req& r) {
 struct Tile {
     int b, rb, key, flags;
 };
+enum : int { kFirst = 1, kLast = 2, kStop = 4, kSlotShift = 3, kBlockShift = 5 };  // flags; slot + 1, head block above them
 
-// A team's place in the list; the same in every lane.
+// A CTA's place in the list; the same in every lane of the producer.
 template <int NV>
 struct Walk {
-    long long pos, end, total, teams;
-    int b, rb, u, u1, len, lo_tile, n_sink, n_ctx, slot;
+    long long pos, end, total, ctas;
+    int kt;  // keys of a tile
+    int b, rb, hblock, u, u1, len, lo_tile, n_sink, n_ctx, slot;
     bool first;
-    int4 starts;  // the cut unit that this team starts (x < 0: none)
+    int4 starts;  // the cut unit that this CTA starts (x < 0: none)
+    int starts_block;
 
-    __device__ void start(const PagedDesc& a, const long long* prefix, int team, int most) {
+    __device__ void start(const MmaArgs& g, const long long* prefix) {
+        const PagedDesc& a = g.a;
+        kt = 32 * g.kg;
         total = prefix[a.B];
-        teams = max(min((long long)most, total), 1ll);
-        pos = team < teams ? total * team / teams : 0;
-        end = team < teams ? total * (team + 1) / teams : 0;
+        ctas = max(min((long long)gridDim.x, total), 1ll);
+        const int c = blockIdx.x;
+        pos = c < ctas ? total * c / ctas : 0;
+        end = c < ctas ? total * (c + 1) / ctas : 0;
         int hi = a.B;
         b = 0;  // the last request whose prefix is at most pos
         while (hi - b > 1) {
@@ -132,27 +148,34 @@ struct Walk {
         }
         u = u1 = 0;
         starts = make_int4(-1, 0, 0, 0);
+        starts_block = 0;
     }
     // The next tile; `empty(slot)` for a piece that causality leaves without one.
     template <class Empty>
-    __device__ bool next(const PagedDesc& a, const long long* prefix, Tile& t, Empty empty) {
+    __device__ bool next(const MmaArgs& g, const long long* prefix, Tile& t, Empty empty) {
+        const PagedDesc& a = g.a;
         while (u >= u1) {
             if (pos >= end) return false;
             while (prefix[b + 1] <= pos) ++b;
             const Req r = load_req(a, b);
-            const Units w = units_of(a, r);
+            const Units w = units_of(a, r, kt);
             const long long rel = pos - prefix[b], unit = rel / w.nt;
-            rb = (int)unit;
+            const int rows = (r.T * a.G + NV - 1) / NV;  // row blocks
+            hblock = (int)(unit / rows);
+            rb = (int)(unit - (long long)hblock * rows);
             u = (int)(rel - unit * w.nt);
             u1 = (int)min((long long)w.nt, u + (end - pos));
             const long long from = pos - u;
             pos += u1 - u;
             slot = u > 0 ? 0 : u1 < w.nt ? 1 : -1;
-            if (slot == 1) starts = make_int4((int)(((from + w.nt) * teams - 1) / total), rb, b, 0);
+            if (slot == 1) {
+                starts = make_int4((int)(((from + w.nt) * ctas - 1) / total), rb * NV, r.T * a.G, r.row0);
+                starts_block = hblock;
+            }
             if (!a.tree) {  // tiles past the block's last row's position
                 const int t_last = (min((rb + 1) * NV, r.T * a.G) - 1) / a.G;
                 const int p_last = r.len - r.n + t_last;
-                const int seen = p_last < 0 ? 0 : p_last / kKT + 1 - w.lo_tile;
+                const int seen = p_last < 0 ? 0 : p_last / kt + 1 - w.lo_tile;
                 u1 = min(u1, max(w.n_sink + max(seen, 0), 1));  // a unit has a first tile, so that its rows are written
             }
             len = r.len;
@@ -164,46 +187,56 @@ struct Walk {
         }
         t.b = b;
         t.rb = rb;
-        t.key = u < n_ctx ? (u < n_sink ? u : lo_tile + u - n_sink) * kKT : a.tree ? -1 - (u - n_ctx) : 0;
-        t.flags = (first ? kFirst : 0) | (u + 1 == u1 ? kLast : 0) | (slot + 1) << kSlotShift;
+        t.key = u < n_ctx ? (u < n_sink ? u : lo_tile + u - n_sink) * kt : a.tree ? -1 - (u - n_ctx) : 0;
+        t.flags = (first ? kFirst : 0) | (u + 1 == u1 ? kLast : 0) | (slot + 1) << kSlotShift | hblock << kBlockShift;
         first = false;
         ++u;
         return true;
     }
 };
 
-// 16-byte chunk c of row `row` of a tile in shared memory.  K: lanes read rows g, g + 1
-// side by side, 64 bytes of each; V: rows 2 t, the same two chunks of each.  The order
-// makes both free of bank conflicts at headDim 128.
+// Chunk c (16 bytes) of a row of hb D bytes in shared memory.  A K fragment's load takes 64
+// bytes of each of two neighbouring rows, a V fragment's 32 (16 at headDim 64) of every other
+// row; in this order they meet no bank twice (V at headDim 64: twice).
 template <int D>
-__device__ __forceinline__ int k_chunk(int row, int c) {
-    return D == 128 ? c ^ ((row & 1) << 2) : c;
+__device__ __forceinline__ int k_chunk(int row, int c, int hb) {
+    return D == 128 || (hb & 1) == 0 ? c ^ ((row & 1) << 2) : c;
 }
 template <int D>
 __device__ __forceinline__ int v_chunk(int row, int c) {
-    return D == 128 ? c ^ (((row >> 1) & 3) << 1) : c ^ ((row >> 1) & 3);
+    return c ^ (D == 128 ? ((row >> 1) & 3) << 1 : (row >> 1) & 3);
 }
 
-template <int D, int NT, int FORM>
-__global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const __grid_constant__ MmaArgs g) {
-    using C = Cfg<D, NT>;
-    constexpr int NV = 8 * NT, S = C::kStages, CH = D / 16, KC = D / 64, MT = D / 16;
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ long long scan_s[C::kWarps];
+template <int D, int NT, int FORM, bool TREE>
+__global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_constant__ MmaArgs g) {
+    constexpr int NV = 8 * NT, S = kStages, KC = D / 64, MT = D / 16;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ long long scan_s[kConsumers + kProducers];
+    __shared__ __align__(8) uint64_t full[S], freed[S], x_put, x_got;
+    __shared__ __align__(16) Tile tile_s[S];
     const PagedDesc& a = g.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t4 = lane & 3;
-    unsigned char* mine = smem + (size_t)warp * S * C::kStage;
-    long long* prefix = reinterpret_cast<long long*>(smem + (size_t)C::kWarps * S * C::kStage);
+    const int warps = blockDim.x >> 5, consumers = warps - kProducers;  // hb kg of them, and the producers
+    long long* prefix = reinterpret_cast<long long*>(smem + (size_t)S * g.stage);
 
     pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 32 * kProducers);  // every producer lane's copies
+            mbar_init(&freed[i], consumers);
+        }
+        mbar_init(&x_put, consumers - g.hb > 0 ? consumers - g.hb : 1);
+        mbar_init(&x_got, g.hb);
+        fence_barrier_init();
+    }
     // The requests' tiles and their running sum.
     long long carry = 0;
-    for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
+    for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
         const int b = b0 + threadIdx.x;
         long long v = 0;
         if (b < a.B) {
             const Req r = load_req(a, b);
-            v = ((long long)r.T * a.G + NV - 1) / NV * units_of(a, r).nt;
+            v = ((long long)r.T * a.G + NV - 1) / NV * g.blocks * units_of(a, r, 32 * g.kg).nt;
         }
         long long s = v;
 #pragma unroll
@@ -214,7 +247,7 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const
         if (lane == 31) scan_s[warp] = s;
         __syncthreads();
         long long before = carry, all = carry;
-        for (int w = 0; w < C::kWarps; ++w) {
+        for (int w = 0; w < warps; ++w) {
             if (w < warp) before += scan_s[w];
             all += scan_s[w];
         }
@@ -225,81 +258,163 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const
     if (threadIdx.x == 0) prefix[a.B] = carry;
     __syncthreads();
 
-    const int worker = blockIdx.x * C::kWarps + warp, most = gridDim.x * C::kWarps / a.Hk;
-    const int team = worker / a.Hk, hk = worker - team * a.Hk;
-    if (team >= most) return;
-    Walk<NV> walk;
-    walk.start(a, prefix, team, most);
-    auto part_row = [&](int slot, int i) -> int64_t { return (((int64_t)2 * team + slot) * a.Hk + hk) * NV + i; };
-    auto empty = [&](int slot) {
-        if (slot >= 0 && lane < NV) {
-            g.part_m[part_row(slot, lane)] = -INFINITY;
-            g.part_l[part_row(slot, lane)] = 0.f;
-        }
-    };
+    const int rows_stage = 32 * g.kg;
+    const int width = g.hb * D;  // of a row
+    const int scales_k = 2 * rows_stage * width, scales_v = scales_k + rows_stage * g.hb * 4;
+    auto part_row = [&](int slot, int w, int i) -> int64_t { return ((int64_t)(3 * blockIdx.x + slot) * kConsumers + w) * NV + i; };
 
-    // ---- loads: a tile's rows are looked up one tile before its copies are issued ----
-    Tile ahead;
-    bool have = walk.next(a, prefix, ahead, empty);
-    int row_ahead = -1;  // pool row of key `lane` of that tile; -1: zeros
-    auto look_up = [&]() {
-        row_ahead = -1;
-        if (!have || ahead.key < 0) return;
-        const int key = ahead.key + lane;
-        if (key >= walk.len) return;
-        const int col = g.page_shift >= 0 ? key >> g.page_shift : key / a.page_size;
-        const int page = __ldg(a.block_table + (int64_t)ahead.b * a.max_pages + col);
-        if (page >= 0 && page < a.pages) row_ahead = page * a.page_size + (key - col * a.page_size);
-    };
-    look_up();
-    auto issue = [&](int st) {  // the copies of `ahead`, which moves on; one commit in any case
-        unsigned char* to = mine + st * C::kStage;
-        if (have) {
-            const int row = row_ahead;
-            if (lane == 0) *reinterpret_cast<Tile*>(to + 2 * C::kTileBytes + 2 * kKT * 4) = ahead;
-            if (ahead.key >= 0) {
-                constexpr int kLanes = CH, kRows = 32 / CH;  // lanes a row, rows a round
-#pragma unroll
-                for (int i = 0; i < kKT / kRows; ++i) {
-                    const int r = i * kRows + lane / kLanes, c = lane % kLanes;
-                    const int from = __shfl_sync(FULL, row, r);
-                    const int64_t at = ((int64_t)max(from, 0) * a.Hk + hk) * D + 16 * c;
-                    cp_async16(to + r * D + 16 * k_chunk<D>(r, c), g.p.k + at, from >= 0 ? 16 : 0);
-                    cp_async16(to + C::kTileBytes + r * D + 16 * v_chunk<D>(r, c), g.p.v + at, from >= 0 ? 16 : 0);
-                }
-                const int64_t at = (int64_t)max(row, 0) * a.Hk + hk;
-                cp_async4(to + 2 * C::kTileBytes + 4 * lane, g.p.k_scale + at, row >= 0 ? 4 : 0);
-                cp_async4(to + 2 * C::kTileBytes + 4 * kKT + 4 * lane, g.p.v_scale + at, row >= 0 ? 4 : 0);
+    if (warp >= consumers) {
+        // ---- producers: each a quarter of a tile's rows, 8 of every 32 ----------------------
+        const int pw = warp - consumers;
+        Walk<NV> walk;
+        walk.start(g, prefix);
+        auto empty = [&](int slot) {
+            if (slot < 0 || pw > 0) return;
+            for (int i = lane; i < g.hb * NV; i += 32) {  // key group 0's warps have the piece's partials
+                g.part_m[part_row(slot, 0, i)] = -INFINITY;
+                g.part_l[part_row(slot, 0, i)] = 0.f;
             }
-            have = walk.next(a, prefix, ahead, empty);
-            look_up();
-        }
-        cp_async_commit();
-    };
-    int issued = 0;
+        };
+        // Lane i looks up row i of this warp's 8 kg of a tile: row 32 (i / 8) + 8 pw + i % 8 (kg of
+        // more than 4: lane i row i + 32 too).  A tile ahead of its copies.
+        Tile t, ahead;
+        int len = 0, len_ahead = 0, h0 = 0, h0_ahead = 0, page[2], page_ahead[2];
+        bool more = true;
+        auto place = [&](int i) { return 32 * (i >> 3) + 8 * pw + (i & 7); };
+        auto look = [&]() {
+            more = walk.next(g, prefix, ahead, empty);
+            if (!more) ahead.flags = kStop, ahead.key = -1;
+            len_ahead = walk.len;
+            h0_ahead = walk.hblock * g.hb;
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
-        issued += have;
-        issue(i);
+            for (int j = 0; j < 2; ++j) {
+                page_ahead[j] = -1;
+                const int i = lane + 32 * j, key = ahead.key + place(i);
+                if (ahead.key >= 0 && i < 8 * g.kg && key < len_ahead)
+                    page_ahead[j] = __ldg(a.block_table + (int64_t)ahead.b * a.max_pages +
+                                          (g.page_shift >= 0 ? key >> g.page_shift : key / a.page_size));
+            }
+        };
+        look();
+        int n = 0;
+        for (;; ++n) {
+            t = ahead;
+            len = len_ahead;
+            h0 = h0_ahead;
+            page[0] = page_ahead[0];
+            page[1] = page_ahead[1];
+            if (more) look();
+            const int st = n % S;
+            if (n >= S && !__all_sync(FULL, mbar_wait(&freed[st], (uint32_t)((n / S - 1) & 1)))) {
+                raise_device_error(&g_q8_device_error, kErrQ8Free);
+                break;
+            }
+            unsigned char* to = smem + (size_t)st * g.stage;
+            if (pw == 0 && lane == 0) tile_s[st] = t;
+            if (t.key >= 0) {
+                const int hb = min(g.hb, a.Hk - h0), chunks = hb * (D / 16);  // of a row
+                int row[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int key = t.key + place(lane + 32 * j);
+                    row[j] = (unsigned)page[j] < (unsigned)a.pages
+                                 ? page[j] * a.page_size + (g.page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size)
+                                 : -1;
+                }
+                const uint8_t* ks = g.p.k + (int64_t)h0 * D;
+                const uint8_t* vs = g.p.v + (int64_t)h0 * D;
+                const int64_t pitch = (int64_t)a.Hk * D;
+                // 8 kg rows of `chunks` chunks each.
+                if (chunks == 64) {  // two accesses a row
+#pragma unroll 8
+                    for (int i = 0; i < 8; ++i) {
+                        const int from = __shfl_sync(FULL, row[0], i), r = 8 * pw + i, bytes = from >= 0 ? 16 : 0;
+                        const int64_t at = max(from, 0) * pitch + 16 * lane;
+                        unsigned char* tk = to + r * 1024 + 16 * k_chunk<D>(r, lane, 8);
+                        unsigned char* tv = to + 32768 + r * 1024 + 16 * v_chunk<D>(r, lane);
+                        cp_async16(tk, ks + at, bytes);
+                        cp_async16(tk + 512, ks + at + 512, bytes);
+                        cp_async16(tv, vs + at, bytes);
+                        cp_async16(tv + 512, vs + at + 512, bytes);
+                    }
+                } else {
+                    for (int e = lane; e < 8 * g.kg * chunks; e += 32) {  // a multiple of 32
+                        const int i = e / chunks, c = e - i * chunks, r = place(i);
+                        const int from0 = __shfl_sync(FULL, row[0], i & 31), from1 = __shfl_sync(FULL, row[1], i & 31);
+                        const int from = i < 32 ? from0 : from1, bytes = from >= 0 ? 16 : 0;
+                        const int64_t at = max(from, 0) * pitch + 16 * c;
+                        cp_async16(to + r * width + 16 * k_chunk<D>(r, c, g.hb), ks + at, bytes);
+                        cp_async16(to + rows_stage * width + r * width + 16 * v_chunk<D>(r, c), vs + at, bytes);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int i = lane + 32 * j;
+                    if (i >= 8 * g.kg) break;
+                    const int r = place(i);
+                    const int64_t at = (int64_t)max(row[j], 0) * a.Hk + h0;
+                    float* sk = reinterpret_cast<float*>(to + scales_k) + r * g.hb;
+                    float* sv = reinterpret_cast<float*>(to + scales_v) + r * g.hb;
+                    if (g.wide && (hb & 3) == 0) {
+                        for (int h = 0; h < hb; h += 4) {
+                            cp_async16(sk + h, g.p.k_scale + at + h, row[j] >= 0 ? 16 : 0);
+                            cp_async16(sv + h, g.p.v_scale + at + h, row[j] >= 0 ? 16 : 0);
+                        }
+                    } else {
+                        for (int h = 0; h < hb; ++h) {
+                            cp_async4(sk + h, g.p.k_scale + at + h, row[j] >= 0 ? 4 : 0);
+                            cp_async4(sv + h, g.p.v_scale + at + h, row[j] >= 0 ? 4 : 0);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            cp_async_arrive(&full[st]);
+            if (t.flags & kStop) break;
+        }
+        if (pw == 0 && lane == 0) {
+            g.head[2 * blockIdx.x] = walk.starts;
+            g.head[2 * blockIdx.x + 1] = make_int4(walk.starts_block * g.hb, 0, 0, 0);
+        }
+        cp_async_wait_all();  // no copy may be in flight when the CTA exits
+        return;
     }
 
-    // ---- state of a piece: this lane's virtual rows are 2 t4, 2 t4 + 1 of each eight ----
+    // ---- consumers: head `hi_warp` of the block, key group `group`; this lane's virtual rows are 2 t4,
+    // 2 t4 + 1 of each eight ----
+    const int group = warp / g.hb, head_w = warp - group * g.hb;
     uint32_t qf[KC][4][NT][4];  // hi and lo, two registers each, of k-step s of chunk c
     float o[MT][NT][4], m[NT][2], l[NT][2], r[NT][2], unit[NT][2], rf[NT][2];
     int hi[NT][2], lo[NT][2];
     float limit = -1.f;  // a tile whose scales are at most this takes the fast way
     Req rq{};
-    int sinks = 0;
-    int st = 0, nx = S - 1;
-    for (int n = 0; n < issued; ++n, st = st + 1 < S ? st + 1 : 0, nx = nx + 1 < S ? nx + 1 : 0) {
-        issued += have;
-        issue(nx);
-        cp_async_wait<S - 1>();
-        __syncwarp();
-        const unsigned char* from = mine + st * C::kStage;
-        const Tile tile = *reinterpret_cast<const Tile*>(from + 2 * C::kTileBytes + 2 * kKT * 4);
-        const float* sks = reinterpret_cast<const float*>(from + 2 * C::kTileBytes);
-        const float* svs = sks + kKT;
+    int sinks = 0, pieces = 0;
+    for (int n = 0;; ++n) {
+        const int st = n % S;
+        if (!__all_sync(FULL, mbar_wait(&full[st], (uint32_t)((n / S) & 1)))) {
+            raise_device_error(&g_q8_device_error, kErrQ8Load);
+            break;
+        }
+        Tile tile = tile_s[st];
+        if (tile.flags & kStop) break;
+        const int hk = (tile.flags >> kBlockShift) * g.hb + head_w;
+        const unsigned char* from = smem + (size_t)st * g.stage;
+        const unsigned char* kt = from + group * 32 * width;
+        const unsigned char* vt = from + (rows_stage + group * 32) * width;
+        const float* sks = reinterpret_cast<const float*>(from + scales_k) + group * 32 * g.hb + head_w;
+        const float* svs = reinterpret_cast<const float*>(from + scales_v) + group * 32 * g.hb + head_w;
+        auto give_back = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&freed[st]);
+        };
+        if (hk >= a.Hk) {  // the last block's missing heads
+            give_back();
+            continue;
+        }
+        // This warp's keys: from tile.key on, or drafted rows from d0 on.
+        int d0 = 0;
+        if (!TREE || tile.key >= 0) tile.key += 32 * group;
+        else d0 = (-1 - tile.key) * rows_stage + 32 * group;
 
         if (tile.flags & kFirst) {
             rq = load_req(a, tile.b);
@@ -363,7 +478,7 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const
         float vs[2][2];  // value scales of keys gr, gr + 8
         const float* vrow[2][4];  // drafted value rows
         float vinv[2][4];
-        if (tile.key >= 0) {
+        if (!TREE || tile.key >= 0) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
 #pragma unroll
@@ -373,8 +488,8 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const
                 const int r0 = 16 * b + gr, r1 = r0 + 8;
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
-                    const uint4 w0 = *reinterpret_cast<const uint4*>(from + r0 * D + 16 * k_chunk<D>(r0, 4 * c + t4));
-                    const uint4 w1 = *reinterpret_cast<const uint4*>(from + r1 * D + 16 * k_chunk<D>(r1, 4 * c + t4));
+                    const uint4 w0 = *reinterpret_cast<const uint4*>(kt + r0 * width + 16 * k_chunk<D>(gr, head_w * (D / 16) + 4 * c + t4, g.hb));
+                    const uint4 w1 = *reinterpret_cast<const uint4*>(kt + r1 * width + 16 * k_chunk<D>(gr, head_w * (D / 16) + 4 * c + t4, g.hb));
                     const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
                     uint32_t f[4][4];
 #pragma unroll
@@ -389,9 +504,9 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) mma_16816(x[b][nt], f[s], qf[c][s][nt][0], qf[c][s][nt][1]);
                 }
-                const float ks[2] = {sks[r0], sks[r1]};
-                vs[b][0] = svs[r0];
-                vs[b][1] = svs[r1];
+                const float ks[2] = {sks[r0 * g.hb], sks[r1 * g.hb]};
+                vs[b][0] = svs[r0 * g.hb];
+                vs[b][1] = svs[r1 * g.hb];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -399,7 +514,6 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const
             }
         } else {
             // Drafted rows: f32, as f16 hi + lo after a power of two per row, straight from memory.
-            const int d0 = kKT * (-1 - tile.key);
 #pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 float xx[NT][4], inv[2], vsc[2], ksc[2];
@@ -487,7 +601,8 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) whole = whole && hi[nt][e] - tile.key >= kKT - 1 && lo[nt][e] <= tile.key;
-        if (!__all_sync(FULL, whole)) {
+        whole = __all_sync(FULL, whole);
+        if (!whole) {
             see = 0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -495,7 +610,7 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const
                 for (int e = 0; e < 2; ++e) {
                     uint64_t mask = 0;
                     int p = 0;
-                    if (tile.key < 0) {
+                    if (TREE && tile.key < 0) {
                         const int w = tile.rb * NV + 8 * nt + 2 * t4 + e, tw = w / a.G;
                         if (w < rq.T * a.G) {
                             mask = __ldg(reinterpret_cast<const unsigned long long*>(a.masks) + rq.row0 + tw);
@@ -508,11 +623,11 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const
                         for (int h = 0; h < 2; ++h) {
                             const int k = 16 * b + gr + 8 * h;
                             bool on;
-                            if (tile.key >= 0) {
+                            if (!TREE || tile.key >= 0) {
                                 const int key = tile.key + k;
                                 on = key <= hi[nt][e] && (key >= lo[nt][e] || key < sinks);
                             } else {
-                                const int j = kKT * (-1 - tile.key) + k;
+                                const int j = d0 + k;
                                 on = j < rq.T && ((mask >> (j & 63)) & 1);
                                 if (on && a.window > 0) on = (int64_t)__ldg(a.positions + rq.row0 + j) > (int64_t)p - a.window;
                             }
@@ -570,13 +685,13 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const
         float tile_top;  // the largest scale: as bits, so that a NaN is the largest
         {
             uint32_t bits = 0;
-            if (tile.key >= 0)
-                bits = __float_as_uint(svs[lane]) & 0x7fffffffu;
+            if (!TREE || tile.key >= 0)
+                bits = __float_as_uint(svs[lane * g.hb]) & 0x7fffffffu;
             else
                 bits = 0x7fc00000u;  // drafted rows take the slow way
             tile_top = __uint_as_float(__reduce_max_sync(FULL, bits));
         }
-        uint32_t ph[2][NT][2], pl[2][NT][2];
+        uint32_t ph[2][NT][2], pl[2][NT][2];  // hi, lo
         const bool fast = tile_top <= limit;
         float w[2][NT][4];
         if (fast) {
@@ -633,34 +748,39 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const
             for (int off = 1; off < 32; off <<= 1) lim = fminf(lim, __shfl_xor_sync(FULL, lim, off));
             limit = lim;
         }
+        if (!whole) {  // the scale of a key that is not seen may be anything
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!((see >> ((b * NT + nt) * 4 + e)) & 1)) w[b][nt][e] = 0.f;
+        }
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    // A scale of a key that is not seen may be anything.
-                    const int at = (b * NT + nt) * 4 + 2 * h;
-                    const float u = (see >> at) & 1 ? w[b][nt][2 * h] : 0.f, v = (see >> (at + 1)) & 1 ? w[b][nt][2 * h + 1] : 0.f;
-                    mma_split(u, v, ph[b][nt][h], pl[b][nt][h]);
+                    mma_split(w[b][nt][2 * h], w[b][nt][2 * h + 1], ph[b][nt][h], pl[b][nt][h]);
                     ph[b][nt][h] = mma_transpose(ph[b][nt][h]);
                     pl[b][nt][h] = mma_transpose(pl[b][nt][h]);
                 }
         // ---- O^T += V^T P^T: row gr of product i is channel (D / 8) gr + 2 i, row gr + 8 the next ----
-        if (tile.key >= 0) {
+        if (!TREE || tile.key >= 0) {
             constexpr int W = D / 32;  // words of a lane's channels of one key
             uint32_t vw[2][4][W];
-            const unsigned char* vt = from + C::kTileBytes;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int row = 16 * b + 2 * t4 + (j & 1) + 8 * (j >> 1);
                     if constexpr (D == 128) {
-                        const uint4 y = *reinterpret_cast<const uint4*>(vt + row * D + 16 * v_chunk<D>(row, gr));
+                        const uint4 y = *reinterpret_cast<const uint4*>(vt + row * width + 16 * v_chunk<D>(2 * t4, head_w * (D / 16) + gr));
                         vw[b][j][0] = y.x; vw[b][j][1] = y.y; vw[b][j][2] = y.z; vw[b][j][3] = y.w;
                     } else {
-                        const uint2 y = *reinterpret_cast<const uint2*>(vt + row * D + 16 * v_chunk<D>(row, gr >> 1) + 8 * (gr & 1));
+                        const uint2 y = *reinterpret_cast<const uint2*>(vt + row * width + 16 * v_chunk<D>(2 * t4, head_w * (D / 16) + (gr >> 1)) + 8 * (gr & 1));
                         vw[b][j][0] = y.x; vw[b][j][1] = y.y;
                     }
                 }
@@ -682,7 +802,9 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const
                         mma_16816(acc, f[i][0], ph[0][nt][0], ph[0][nt][1]);
                         mma_16816(acc, f[i][1], ph[1][nt][0], ph[1][nt][1]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[2 * k + i][nt][e] += acc[e];
+                        for (int e = 0; e < 4; e += 2)
+                            f2_unpack(f2_add(f2_pack(o[2 * k + i][nt][e], o[2 * k + i][nt][e + 1]), f2_pack(acc[e], acc[e + 1])),
+                                      o[2 * k + i][nt][e], o[2 * k + i][nt][e + 1]);
                     }
             }
         } else {
@@ -719,137 +841,199 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) q8_mma_kernel(const
                     for (int e = 0; e < 4; ++e) o[i][nt][e] += acc[nt][e];
             }
         }
-        __syncwarp();  // the stage may be filled again
+        give_back();
         // ---- the end of a piece ----
         if (tile.flags & kLast) {
-            const int slot = (tile.flags >> kSlotShift) - 1;
+            const int slot = ((tile.flags >> kSlotShift) & 3) - 1;
+            // Key groups: the others leave theirs as partials in slot 2, group 0 takes them in.
+            const uint32_t turn = (uint32_t)(pieces++ & 1);
+            if (g.kg > 1) {
+                uint64_t* bar = group ? &x_got : &x_put;
+                if ((group == 0 || pieces > 1) && !__all_sync(FULL, mbar_wait(bar, group ? turn ^ 1 : turn))) {
+                    raise_device_error(&g_q8_device_error, kErrQ8Load);
+                    break;
+                }
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float sum = l[nt][e];
+                    float sum = l[nt][e], top = m[nt][e];
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(FULL, sum, off);
-                    const float inv = sum != 0.f ? 1.f / sum : 0.f, back = exp2f(r[nt][e] - kShift);
                     const int i = 8 * nt + 2 * t4 + e, v = tile.rb * NV + i, t = v / a.G;
-                    float* to;
-                    if (slot < 0) {
-                        if (v >= rq.T * a.G) continue;
-                        to = a.out + (((int64_t)rq.row0 + t) * a.H + (int64_t)hk * a.G + (v - t * a.G)) * D;
-                    } else {
-                        to = g.part_o + part_row(slot, i) * D;
-                        if (gr == 0) {
-                            g.part_m[part_row(slot, i)] = m[nt][e];
-                            g.part_l[part_row(slot, i)] = sum;
+                    float y[D / 8];
+                    {
+                        const float inv = sum != 0.f ? 1.f / sum : 0.f, back = exp2f(r[nt][e] - kShift);
+#pragma unroll
+                        for (int k = 0; k < MT; ++k) {
+                            y[2 * k] = o[k][nt][e] * inv * back;
+                            y[2 * k + 1] = o[k][nt][2 + e] * inv * back;
                         }
                     }
-                    to += (D / 8) * gr;
+                    if (g.kg > 1 && group == 0) {  // by the log-sum-exp rule, in the groups' order
+                        float all = top;
+                        for (int k = 1; k < g.kg; ++k) all = fmaxf(all, __ldcg(g.part_m + part_row(2, k * g.hb + head_w, i)));
+                        // A part that saw nothing has no weight; one that comes to 0 counts (0 x inf is NaN).
+                        float den = sum != 0.f ? fast_exp2(top - all) * sum : 0.f;
 #pragma unroll
-                    for (int k = 0; k < MT; k += 2)
-                        *reinterpret_cast<float4*>(to + 2 * k) =
-                            make_float4(o[k][nt][e] * inv * back, o[k][nt][2 + e] * inv * back, o[k + 1][nt][e] * inv * back,
-                                        o[k + 1][nt][2 + e] * inv * back);
+                        for (int k = 0; k < D / 8; ++k) y[k] = sum != 0.f ? y[k] * den : 0.f;
+                        for (int k = 1; k < g.kg; ++k) {
+                            const int64_t at = part_row(2, k * g.hb + head_w, i);
+                            const float lk = __ldcg(g.part_l + at);
+                            if (lk == 0.f) continue;
+                            const float w = fast_exp2(__ldcg(g.part_m + at) - all) * lk;
+                            den += w;
+#pragma unroll
+                            for (int d = 0; d < D / 8; d += 4) {
+                                const float4 z = __ldcg(reinterpret_cast<const float4*>(g.part_o + at * D + (D / 8) * gr + d));
+                                y[d] = fmaf(w, z.x, y[d]);
+                                y[d + 1] = fmaf(w, z.y, y[d + 1]);
+                                y[d + 2] = fmaf(w, z.z, y[d + 2]);
+                                y[d + 3] = fmaf(w, z.w, y[d + 3]);
+                            }
+                        }
+                        const float inv = den != 0.f ? 1.f / den : 0.f;
+#pragma unroll
+                        for (int k = 0; k < D / 8; ++k) y[k] *= inv;
+                        sum = den;
+                        top = all;
+                    }
+                    float* to = nullptr;
+                    const int where = group ? 2 : slot;
+                    if (where < 0) {
+                        if (v < rq.T * a.G) to = a.out + (((int64_t)rq.row0 + t) * a.H + (int64_t)hk * a.G + (v - t * a.G)) * D;
+                    } else {
+                        const int64_t at = part_row(where, warp, i);
+                        to = g.part_o + at * D;
+                        if (gr == 0) {
+                            g.part_m[at] = top;
+                            g.part_l[at] = sum;
+                        }
+                    }
+                    if (to) {
+                        to += (D / 8) * gr;
+#pragma unroll
+                        for (int d = 0; d < D / 8; d += 4)
+                            *reinterpret_cast<float4*>(to + d) = make_float4(y[d], y[d + 1], y[d + 2], y[d + 3]);
+                    }
                 }
+            if (g.kg > 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(group ? &x_put : &x_got);
+            }
         }
     }
-    cp_async_wait<0>();
-    if (hk == 0 && lane == 0) g.head[team] = walk.starts;
 }
 
-// Joins the partials of the unit that team blockIdx.x starts: as the f32 kernel's merge.  A
-// warp per virtual row of KV head blockIdx.y.
+// Joins the partials of the unit that CTA blockIdx.x starts by the log-sum-exp rule, always in
+// the same order: a warp per (head, virtual row).
 template <int D, int NT>
-__global__ void __launch_bounds__(256) q8_merge_kernel(const __grid_constant__ MmaArgs g) {
+__global__ void __launch_bounds__(256) q8_merge_kernel(const __grid_constant__ MmaArgs g, int rows) {
     constexpr int NV = 8 * NT, kPer = D / 32;
     pdl_wait();
     const PagedDesc& a = g.a;
-    const int4 h = __ldcg(&g.head[blockIdx.x]);
-    if (h.x < 0) return;
-    const int first = blockIdx.x, hk = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rb = h.y, count = h.x - first + 1;
-    const Req r = load_req(a, h.z);
-    for (int i = warp; i < NV; i += 8) {
-        const int v = rb * NV + i;
-        if (v >= r.T * a.G) return;
-        auto row = [&](int k) -> int64_t {
-            return (((int64_t)2 * (first + k) + (k == 0 ? 1 : 0)) * a.Hk + hk) * NV + i;
-        };
-        auto load = [&](int k) -> float2 {
-            return k < count ? make_float2(__ldcg(g.part_m + row(k)), __ldcg(g.part_l + row(k))) : make_float2(-INFINITY, 0.f);
-        };
-        const float2 own = load(lane);
-        float m = own.x;
-        for (int k = lane + 32; k < count; k += 32) m = fmaxf(m, __ldcg(g.part_m + row(k)));
+    const int4 h = __ldcg(&g.head[2 * blockIdx.x]);
+    const int h0 = __ldcg(&g.head[2 * blockIdx.x + 1].x);
+    const int lane = threadIdx.x & 31, job = blockIdx.y * 8 + (threadIdx.x >> 5), head = job / rows, i = job - head * rows;
+    const int v = h.y + i, hk = h0 + head;
+    if (h.x < 0 || head >= g.hb || hk >= a.Hk || v >= h.z) return;
+    const int count = h.x - blockIdx.x + 1;
+    auto row = [&](int k) -> int64_t {
+        return ((int64_t)(3 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * kConsumers + head) * NV + i;
+    };
+    auto load = [&](int k) -> float2 {
+        return k < count ? make_float2(__ldcg(g.part_m + row(k)), __ldcg(g.part_l + row(k))) : make_float2(-INFINITY, 0.f);
+    };
+    const float2 own = load(lane);
+    float m = own.x;
+    for (int k = lane + 32; k < count; k += 32) m = fmaxf(m, __ldcg(g.part_m + row(k)));
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, off));
-        // -0 where a piece saw nothing and left no output; +0 counts (0 x inf is NaN).
-        auto weight = [&](float2 p) -> float { return p.y != 0.f ? fast_exp2(p.x - m) * p.y : -0.f; };
-        float den = weight(own);
-        for (int k = lane + 32; k < count; k += 32) den += weight(load(k));
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, off));
+    // -0 where a piece saw nothing and left no output; +0 counts (0 x inf is NaN).
+    auto weight = [&](float2 p) -> float { return p.y != 0.f ? fast_exp2(p.x - m) * p.y : -0.f; };
+    float den = weight(own);
+    for (int k = lane + 32; k < count; k += 32) den += weight(load(k));
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(FULL, den, off);
-        const float inv = den != 0.f ? 1.f / den : 0.f;
-        float acc[kPer];
+    for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(FULL, den, off);
+    const float inv = den != 0.f ? 1.f / den : 0.f;
+    float acc[kPer];
 #pragma unroll
-        for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
-        for (int k0 = 0; k0 < count; k0 += 32) {
-            const float wgt = weight(k0 == 0 ? own : load(k0 + lane)) * inv;
-            const int here = min(count - k0, 32);
-            for (int k = 0; k < here; ++k) {
-                const float f = __shfl_sync(FULL, wgt, k);
-                if (__float_as_uint(f) == 0x80000000u) continue;
-                const float* src = g.part_o + row(k0 + k) * D;
+    for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
+    for (int k0 = 0; k0 < count; k0 += 32) {
+        const float wgt = weight(k0 == 0 ? own : load(k0 + lane)) * inv;
+        const int here = min(count - k0, 32);
+#pragma unroll 4
+        for (int k = 0; k < here; ++k) {
+            const float f = __shfl_sync(FULL, wgt, k);
+            if (__float_as_uint(f) == 0x80000000u) continue;
+            const float* src = g.part_o + row(k0 + k) * D;
 #pragma unroll
-                for (int c = 0; c < kPer; ++c) acc[c] = fmaf(f, __ldcg(src + lane + 32 * c), acc[c]);
-            }
+            for (int c = 0; c < kPer; ++c) acc[c] = fmaf(f, __ldcg(src + lane + 32 * c), acc[c]);
         }
-        float* out = a.out + (((int64_t)r.row0 + v / a.G) * a.H + (int64_t)hk * a.G + v % a.G) * D;
-#pragma unroll
-        for (int c = 0; c < kPer; ++c) out[lane + 32 * c] = acc[c];
     }
+    const int t = v / a.G;
+    float* out = a.out + (((int64_t)h.w + t) * a.H + (int64_t)hk * a.G + (v - t * a.G)) * D;
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) out[lane + 32 * c] = acc[c];
 }
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Row blocks of 8 virtual rows where they hold a request's, else 16.
 int blocks_of(const PagedDesc& a) { return (int64_t)a.max_rows * a.G <= 8 ? 1 : 2; }
-constexpr int kMmaWarps = 8;
 
 struct Scratch {
     size_t m, l, o, head, total;
 };
-int ctas_of(int sms, int Hk) {
-    const int need = (Hk + kMmaWarps - 1) / kMmaWarps, n = sms < kPagedMaxCtas ? sms : kPagedMaxCtas;
-    return n < need ? need : n;
-}
-Scratch scratch_of(int ctas, int Hk, int NV, int D) {
-    const size_t teams = (size_t)ctas * kMmaWarps / Hk, rows = 2 * teams * Hk * NV;
+Scratch scratch_of(int NV, int D) {
+    const size_t rows = (size_t)3 * kPagedMaxCtas * kConsumers * NV;
     Scratch s;
     s.m = kWorkspaceHeader;
     s.l = s.m + up256(rows * 4);
     s.o = s.l + up256(rows * 4);
     s.head = s.o + up256(rows * D * 4);
-    s.total = s.head + up256(teams * sizeof(int4));
+    s.total = s.head + up256((size_t)2 * kPagedMaxCtas * sizeof(int4));
     return s;
 }
 
-template <int D, int NT, int FORM>
-cudaError_t launch_form(const MmaArgs& g, int ctas, cudaStream_t stream) {
-    using C = Cfg<D, NT>;
-    static_assert(C::kWarps == kMmaWarps, "the workspace counts them");
-    auto kern = q8_mma_kernel<D, NT, FORM>;
-    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), (int)C::smem(kPagedMaxRequests));
+template <int D, int NT, int FORM, bool TREE>
+cudaError_t launch_form(MmaArgs& g, int num_sms, void* workspace, cudaStream_t stream) {
+    const PagedDesc& a = g.a;
+    g.blocks = (a.Hk + kConsumers - 1) / kConsumers;
+    g.hb = (a.Hk + g.blocks - 1) / g.blocks;
+    g.kg = kConsumers / g.hb;
+    if (g.kg == 3) g.kg = 2;  // tiles of a power of two
+    g.wide = (a.Hk | g.hb) % 4 == 0 &&
+             ((reinterpret_cast<uintptr_t>(g.p.k_scale) | reinterpret_cast<uintptr_t>(g.p.v_scale)) & 15u) == 0;
+    g.stage = 32 * g.kg * g.hb * (2 * D + 8);
+    const int ctas = num_sms < kPagedMaxCtas ? num_sms : kPagedMaxCtas;
+    const Scratch s = scratch_of(8 * NT, D);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    g.part_m = reinterpret_cast<float*>(ws + s.m);
+    g.part_l = reinterpret_cast<float*>(ws + s.l);
+    g.part_o = reinterpret_cast<float*>(ws + s.o);
+    g.head = reinterpret_cast<int4*>(ws + s.head);
+    auto kern = q8_mma_kernel<D, NT, FORM, TREE>;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), (int)kSmemMost);
     if (e != cudaSuccess) return e;
-    kern<<<ctas, C::kThreads, C::smem(g.a.B), stream>>>(g);
+    const size_t smem = (size_t)kStages * g.stage + (size_t)(a.B + 1) * 8;
+    if (smem > kSmemMost) return cudaErrorInvalidConfiguration;
+    kern<<<ctas, 32 * (g.hb * g.kg + kProducers), smem, stream>>>(g);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_pdl(q8_merge_kernel<D, NT>, dim3((unsigned)(ctas * C::kWarps / g.a.Hk), (unsigned)g.a.Hk), dim3(256), 0,
-                      stream, g);
+    const int64_t most = (int64_t)a.max_rows * a.G;
+    const int live = most < 8 * NT ? (int)most : 8 * NT;
+    return launch_pdl(q8_merge_kernel<D, NT>, dim3((unsigned)ctas, (unsigned)(g.hb * live + 7) / 8), dim3(256), 0, stream, g,
+                      live);
 }
 template <int D, int NT>
-cudaError_t launch_nt(const MmaArgs& g, int ctas, cudaStream_t stream) {
-    return g.p.form == kFormInt8 ? launch_form<D, NT, kFormInt8>(g, ctas, stream)
-                                 : launch_form<D, NT, kFormE4m3>(g, ctas, stream);
+cudaError_t launch_nt(MmaArgs& g, int num_sms, void* ws, cudaStream_t stream) {
+    if (g.p.form == kFormInt8)
+        return g.a.tree ? launch_form<D, NT, kFormInt8, true>(g, num_sms, ws, stream)
+                        : launch_form<D, NT, kFormInt8, false>(g, num_sms, ws, stream);
+    return g.a.tree ? launch_form<D, NT, kFormE4m3, true>(g, num_sms, ws, stream)
+                    : launch_form<D, NT, kFormE4m3, false>(g, num_sms, ws, stream);
 }
 
 }  // namespace
@@ -858,9 +1042,7 @@ bool paged_q8_mma_supported(const PagedDesc& a) {
     return (a.D == 64 || a.D == 128) && a.pages > 0 && (int64_t)a.max_rows * a.G < ((int64_t)1 << 30);
 }
 
-size_t paged_q8_mma_workspace(const PagedDesc& a) {
-    return scratch_of(ctas_of(kPagedMaxCtas, a.Hk), a.Hk, 8 * blocks_of(a), a.D).total;
-}
+size_t paged_q8_mma_workspace(const PagedDesc& a) { return scratch_of(8 * blocks_of(a), a.D).total; }
 
 cudaError_t launch_paged_q8_mma(const PagedDesc& a, const Q8Pools& p, int num_sms, void* workspace, cudaStream_t stream) {
     MmaArgs g;
@@ -870,15 +1052,20 @@ cudaError_t launch_paged_q8_mma(const PagedDesc& a, const Q8Pools& p, int num_sm
     g.page_shift = -1;
     for (int i = 0; i < 31; ++i)
         if (a.page_size == 1 << i) g.page_shift = i;
-    const int ctas = ctas_of(num_sms, a.Hk), nt = blocks_of(a);
-    const Scratch s = scratch_of(ctas, a.Hk, 8 * nt, a.D);
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
-    g.part_m = reinterpret_cast<float*>(ws + s.m);
-    g.part_l = reinterpret_cast<float*>(ws + s.l);
-    g.part_o = reinterpret_cast<float*>(ws + s.o);
-    g.head = reinterpret_cast<int4*>(ws + s.head);
-    if (a.D == 128) return nt == 1 ? launch_nt<128, 1>(g, ctas, stream) : launch_nt<128, 2>(g, ctas, stream);
-    return nt == 1 ? launch_nt<64, 1>(g, ctas, stream) : launch_nt<64, 2>(g, ctas, stream);
+    const int nt = blocks_of(a);
+    if (a.D == 128)
+        return nt == 1 ? launch_nt<128, 1>(g, num_sms, workspace, stream) : launch_nt<128, 2>(g, num_sms, workspace, stream);
+    return nt == 1 ? launch_nt<64, 1>(g, num_sms, workspace, stream) : launch_nt<64, 2>(g, num_sms, workspace, stream);
+}
+
+unsigned int paged_q8_take_device_error() {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_q8_device_error, sizeof(v)) != cudaSuccess) return 0;
+    if (v) {
+        const unsigned int zero = 0;
+        cudaMemcpyToSymbol(g_q8_device_error, &zero, sizeof(zero));
+    }
+    return v;
 }
 
 }  // namespace vtmu

@@ -4,15 +4,17 @@
 
 #include <cstdint>
 
+#include "attn_common.cuh"
 #include "paged_q8.cuh"
 
 namespace vtmu {
 
-__device__ __forceinline__ float fast_exp2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
+// One of the arrivals that `bar` counts, once this thread's earlier cp.async have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
+
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
 
 // The power of two that brings a row's largest |element| to [2^bits, 2^(bits + 1)); it
 // and its inverse are normal numbers.

@@ -1449,7 +1449,8 @@ vtmu_status vtmu_device_error(unsigned int* flags) {
     if (e != cudaSuccess) return cuda_fail(e, "device_error: synchronize");
     *flags = vtmu::decode_take_device_error() | vtmu::decode_tc_take_device_error() | vtmu::tc_take_device_error() |
              vtmu::mla_take_device_error() |
-             vtmu::mla_tc_take_device_error() | vtmu::paged_take_device_error();
+             vtmu::mla_tc_take_device_error() | vtmu::paged_take_device_error() |
+             vtmu::paged_q8_take_device_error();
     return ok();
 }
 
