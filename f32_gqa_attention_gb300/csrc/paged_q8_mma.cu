@@ -216,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
     __shared__ __align__(16) Tile tile_s[S];
     const PagedDesc& a = g.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t4 = lane & 3;
-    const int warps = blockDim.x >> 5, consumers = warps - kProducers;  // hb kg of them, and the producers
+    constexpr int warps = kConsumers + kProducers;
+    const int consumers = g.hb * g.kg;  // that work
     long long* prefix = reinterpret_cast<long long*>(smem + (size_t)S * g.stage);
 
     pdl_launch_dependents();
@@ -263,9 +264,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
     const int scales_k = 2 * rows_stage * width, scales_v = scales_k + rows_stage * g.hb * 4;
     auto part_row = [&](int slot, int w, int i) -> int64_t { return ((int64_t)(3 * blockIdx.x + slot) * kConsumers + w) * NV + i; };
 
-    if (warp >= consumers) {
+    if (warp >= kConsumers) {
         // ---- producers: each a quarter of a tile's rows, 8 of every 32 ----------------------
-        const int pw = warp - consumers;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        const int pw = warp - kConsumers;
         Walk<NV> walk;
         walk.start(g, prefix);
         auto empty = [&](int slot) {
@@ -382,6 +384,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
 
     // ---- consumers: head `hi_warp` of the block, key group `group`; this lane's virtual rows are 2 t4,
     // 2 t4 + 1 of each eight ----
+    // Shares of the launch's registers: 8 x 224 + 4 x 56 = 12 x 168 a lane.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if (warp >= consumers) return;
     const int group = warp / g.hb, head_w = warp - group * g.hb;
     uint32_t qf[KC][4][NT][4];  // hi and lo, two registers each, of k-step s of chunk c
     float o[MT][NT][4], m[NT][2], l[NT][2], r[NT][2], unit[NT][2], rf[NT][2];
@@ -1019,7 +1024,7 @@ cudaError_t launch_form(MmaArgs& g, int num_sms, void* workspace, cudaStream_t s
     if (e != cudaSuccess) return e;
     const size_t smem = (size_t)kStages * g.stage + (size_t)(a.B + 1) * 8;
     if (smem > kSmemMost) return cudaErrorInvalidConfiguration;
-    kern<<<ctas, 32 * (g.hb * g.kg + kProducers), smem, stream>>>(g);
+    kern<<<ctas, kThreads, smem, stream>>>(g);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t most = (int64_t)a.max_rows * a.G;
