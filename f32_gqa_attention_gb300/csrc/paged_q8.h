@@ -48,6 +48,8 @@ cudaError_t launch_paged_q8_ffma(const PagedDesc& a, const Q8Pools& p, cudaStrea
 bool paged_q8_mma_supported(const PagedDesc& a);
 size_t paged_q8_mma_workspace(const PagedDesc& a);
 cudaError_t launch_paged_q8_mma(const PagedDesc& a, const Q8Pools& p, int num_sms, void* workspace, cudaStream_t stream);
+// The drafted rows' part of every row: its output to a.out, its maximum and sum to ml [rows][H].
+cudaError_t launch_paged_q8_draft(const PagedDesc& a, float2* ml, cudaStream_t stream);
 unsigned int paged_q8_take_device_error();
 
 }  // namespace vtmu

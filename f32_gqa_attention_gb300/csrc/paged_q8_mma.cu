@@ -39,8 +39,7 @@
 
 #include "attn_common.cuh"
 #include "launch_cache.h"
-#include "paged.cuh"
-#include "paged_q8.cuh"
+#include "paged_q8_list.cuh"
 #include "paged_q8_mma.cuh"
 #include "pdl.cuh"
 #include "softcap.cuh"
@@ -70,6 +69,7 @@ struct MmaArgs {
     float* part_m;       // [3 CTAs][8 warps][NV]: slot 0 goes on with a unit, slot 1 starts one, 2: key groups
     float* part_l;
     float* part_o;       // [3 CTAs][8 warps][NV][D], divided by l
+    const float2* draft; // [rows][H]: maximum and sum over the drafted rows, whose output is in a.out
     int4* head;          // [2 CTAs]: the unit a CTA starts: last CTA, virtual rows [y, z), first packed row; first head
 };
 
@@ -84,39 +84,7 @@ enum : unsigned int {
     kErrQ8Free = 1u << 4,  // a stage that was not given back
 };
 
-// ---- the list of tiles: as in the f32 kernel, with 32 keys a tile and the drafted rows'
-// tiles behind the cache's ----
-struct Req {
-    int row0, T, len, n;
-};
-struct Units {
-    int lo_tile, n_sink, n_ctx, nt;
-};
-__device__ __forceinline__ Req load_req(const PagedDesc& a, int b) {
-    const PackedRows pr = packed_rows(a.cu_rows, b, a.B, a.rows);
-    Req r;
-    r.row0 = (int)pr.row0;
-    r.n = (int)pr.n;
-    r.T = min(r.n, a.max_rows);
-    r.len = (int)clamp64(__ldg(a.lens + b), 0, (int64_t)a.max_pages * a.page_size);
-    return r;
-}
-__device__ __forceinline__ Units units_of(const PagedDesc& a, const Req& r, int kKT) {
-    Units t;
-    int64_t lo = 0;
-    if (a.window > 0) lo = clamp64((a.tree ? (int64_t)r.len : (int64_t)r.len - r.n) - a.window + 1, 0, r.len);
-    t.lo_tile = (int)(lo / kKT);
-    const int n_main = lo < r.len ? (int)(((int64_t)r.len + kKT - 1) / kKT) - t.lo_tile : 0;
-    const int64_t sink_tiles = (min(a.sinks, (int64_t)r.len) + kKT - 1) / kKT;
-    t.n_sink = (int)(n_main > 0 ? min(sink_tiles, (int64_t)t.lo_tile) : sink_tiles);
-    t.n_ctx = t.n_sink + n_main;
-    t.nt = t.n_ctx + (a.tree ? (r.T + kKT - 1) / kKT : 0);
-    if (r.T == 0) t.nt = 0;
-    else if (t.nt == 0) t.nt = 1;
-    return t;
-}
-
-// A tile: first key, or -1 - i for the i-th tile of drafted rows.
+// A tile: its first key.
 struct Tile {
     int b, rb, key, flags;
 };
@@ -127,7 +95,7 @@ template <int NV>
 struct Walk {
     long long pos, end, total, ctas;
     int kt;  // keys of a tile
-    int b, rb, hblock, u, u1, len, lo_tile, n_sink, n_ctx, slot;
+    int b, rb, hblock, u, u1, len, lo_tile, n_sink, slot;
     bool first;
     int4 starts;  // the cut unit that this CTA starts (x < 0: none)
     int starts_block;
@@ -157,8 +125,8 @@ struct Walk {
         while (u >= u1) {
             if (pos >= end) return false;
             while (prefix[b + 1] <= pos) ++b;
-            const Req r = load_req(a, b);
-            const Units w = units_of(a, r, kt);
+            const Q8Req r = q8_load_req(a, b);
+            const Q8Units w = q8_units(a, r, kt);
             const long long rel = pos - prefix[b], unit = rel / w.nt;
             const int rows = (r.T * a.G + NV - 1) / NV;  // row blocks
             hblock = (int)(unit / rows);
@@ -174,20 +142,17 @@ struct Walk {
             }
             if (!a.tree) {  // tiles past the block's last row's position
                 const int t_last = (min((rb + 1) * NV, r.T * a.G) - 1) / a.G;
-                const int p_last = r.len - r.n + t_last;
-                const int seen = p_last < 0 ? 0 : p_last / kt + 1 - w.lo_tile;
-                u1 = min(u1, max(w.n_sink + max(seen, 0), 1));  // a unit has a first tile, so that its rows are written
+                u1 = min(u1, q8_seen_tiles(r, w, t_last, kt));
             }
             len = r.len;
             lo_tile = w.lo_tile;
             n_sink = w.n_sink;
-            n_ctx = w.n_ctx;
             first = true;
             if (u >= u1) empty(slot);
         }
         t.b = b;
         t.rb = rb;
-        t.key = u < n_ctx ? (u < n_sink ? u : lo_tile + u - n_sink) * kt : a.tree ? -1 - (u - n_ctx) : 0;
+        t.key = (u < n_sink ? u : lo_tile + u - n_sink) * kt;
         t.flags = (first ? kFirst : 0) | (u + 1 == u1 ? kLast : 0) | (slot + 1) << kSlotShift | hblock << kBlockShift;
         first = false;
         ++u;
@@ -207,7 +172,7 @@ __device__ __forceinline__ int v_chunk(int row, int c) {
     return c ^ (D == 128 ? ((row >> 1) & 3) << 1 : (row >> 1) & 3);
 }
 
-template <int D, int NT, int FORM, bool TREE>
+template <int D, int NT, int FORM>
 __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_constant__ MmaArgs g) {
     constexpr int NV = 8 * NT, S = kStages, KC = D / 64, MT = D / 16;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -236,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
         const int b = b0 + threadIdx.x;
         long long v = 0;
         if (b < a.B) {
-            const Req r = load_req(a, b);
-            v = ((long long)r.T * a.G + NV - 1) / NV * g.blocks * units_of(a, r, 32 * g.kg).nt;
+            const Q8Req r = q8_load_req(a, b);
+            v = ((long long)r.T * a.G + NV - 1) / NV * g.blocks * q8_units(a, r, 32 * g.kg).nt;
         }
         long long s = v;
 #pragma unroll
@@ -379,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
             g.head[2 * blockIdx.x + 1] = make_int4(walk.starts_block * g.hb, 0, 0, 0);
         }
         cp_async_wait_all();  // no copy may be in flight when the CTA exits
+        pdl_wait();           // nor this grid be done before the one that it overlaps
         return;
     }
 
@@ -392,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
     float o[MT][NT][4], m[NT][2], l[NT][2], r[NT][2], unit[NT][2], rf[NT][2];
     int hi[NT][2], lo[NT][2];
     float limit = -1.f;  // a tile whose scales are at most this takes the fast way
-    Req rq{};
+    Q8Req rq{};
     int sinks = 0, pieces = 0;
     for (int n = 0;; ++n) {
         const int st = n % S;
@@ -416,13 +382,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
             give_back();
             continue;
         }
-        // This warp's keys: from tile.key on, or drafted rows from d0 on.
-        int d0 = 0;
-        if (!TREE || tile.key >= 0) tile.key += 32 * group;
-        else d0 = (-1 - tile.key) * rows_stage + 32 * group;
+        tile.key += 32 * group;  // this warp's keys
 
         if (tile.flags & kFirst) {
-            rq = load_req(a, tile.b);
+            rq = q8_load_req(a, tile.b);
             sinks = (int)min(a.sinks, (int64_t)rq.len);
             limit = -1.f;
 #pragma unroll
@@ -481,9 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
         // ---- scores: x[block of 16 keys][nt]: keys gr (0, 1) and gr + 8 (2, 3), rows 2 t4 and + 1 ----
         float x[2][NT][4];
         float vs[2][2];  // value scales of keys gr, gr + 8
-        const float* vrow[2][4];  // drafted value rows
-        float vinv[2][4];
-        if (!TREE || tile.key >= 0) {
+        {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
 #pragma unroll
@@ -517,79 +478,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[b][nt][e] *= ks[e >> 1] * rf[nt][e & 1];
             }
-        } else {
-            // Drafted rows: f32, as f16 hi + lo after a power of two per row, straight from memory.
-#pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
-                float xx[NT][4], inv[2], vsc[2], ksc[2];
-                const float* kr[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int j = d0 + 16 * b + gr + 8 * h;
-                    const int64_t at = ((int64_t)(rq.row0 + min(j, rq.T - 1)) * a.Hk + hk) * D;
-                    float top[2];
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const float* row = (kv ? a.v_new : a.k_new) + at;
-                        float tp = 0.f;
-                        for (int d = 4 * t4; d < D; d += 16) tp = q8_abs_top(tp, __ldg(reinterpret_cast<const float4*>(row + d)));
-                        tp = q8_nan_max(tp, __shfl_xor_sync(FULL, tp, 1));
-                        top[kv] = q8_nan_max(tp, __shfl_xor_sync(FULL, tp, 2));
-                    }
-                    kr[h] = a.k_new + at;
-                    const bool kfine = top[0] < INFINITY, vfine = top[1] < INFINITY;
-                    inv[h] = kfine ? mma_row_scale(top[0], 8) : 0.f;
-                    ksc[h] = kfine ? 1.f / inv[h] : __int_as_float(0x7fc00000);
-                    const float vi = vfine ? mma_row_scale(top[1], 8) : 0.f;
-                    vsc[h] = vfine ? 1.f / vi : __int_as_float(0x7fc00000);
-                    // value rows 2 t4 + e + 8 h, whose scales rows gr = 2 t4 + e know
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float w = __shfl_sync(FULL, vi, 4 * (2 * t4 + e));
-                        const int jv = min(d0 + 16 * b + 2 * t4 + e + 8 * h, rq.T - 1);
-                        const float* pv = a.v_new + ((int64_t)(rq.row0 + jv) * a.Hk + hk) * D;
-                        if (b == 0) {
-                            vinv[0][2 * h + e] = w;
-                            vrow[0][2 * h + e] = pv;
-                        } else {
-                            vinv[1][2 * h + e] = w;
-                            vrow[1][2 * h + e] = pv;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) xx[nt][e] = 0.f;
-#pragma unroll
-                for (int c = 0; c < KC; ++c)
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        uint32_t fh[4], fl[4];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float4 y = __ldg(reinterpret_cast<const float4*>(kr[h] + 64 * c + 16 * t4 + 4 * s));
-                            if (inv[h] == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
-                            mma_split(y.x * inv[h], y.y * inv[h], fh[h], fl[h]);
-                            mma_split(y.z * inv[h], y.w * inv[h], fh[2 + h], fl[2 + h]);
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma_16816(xx[nt], fh, qf[c][s][nt][2], qf[c][s][nt][3]);
-                            mma_16816(xx[nt], fl, qf[c][s][nt][0], qf[c][s][nt][1]);
-                            mma_16816(xx[nt], fh, qf[c][s][nt][0], qf[c][s][nt][1]);
-                        }
-                    }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float y = xx[nt][e] * (ksc[e >> 1] * rf[nt][e & 1]);
-                        if (b == 0) x[0][nt][e] = y; else x[1][nt][e] = y;
-                    }
-                if (b == 0) vs[0][0] = vsc[0], vs[0][1] = vsc[1];
-                else vs[1][0] = vsc[0], vs[1][1] = vsc[1];
-            }
         }
         if (a.softcap_on) {
 #pragma unroll
@@ -601,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
         }
         // ---- mask: bit (b, nt, e) of `see` ----
         uint32_t see = FULL;
-        bool whole = tile.key >= 0;
+        bool whole = true;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -613,29 +501,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    uint64_t mask = 0;
-                    int p = 0;
-                    if (TREE && tile.key < 0) {
-                        const int w = tile.rb * NV + 8 * nt + 2 * t4 + e, tw = w / a.G;
-                        if (w < rq.T * a.G) {
-                            mask = __ldg(reinterpret_cast<const unsigned long long*>(a.masks) + rq.row0 + tw);
-                            if (a.window > 0) p = __ldg(a.positions + rq.row0 + tw);
-                        }
-                    }
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const int k = 16 * b + gr + 8 * h;
-                            bool on;
-                            if (!TREE || tile.key >= 0) {
-                                const int key = tile.key + k;
-                                on = key <= hi[nt][e] && (key >= lo[nt][e] || key < sinks);
-                            } else {
-                                const int j = d0 + k;
-                                on = j < rq.T && ((mask >> (j & 63)) & 1);
-                                if (on && a.window > 0) on = (int64_t)__ldg(a.positions + rq.row0 + j) > (int64_t)p - a.window;
-                            }
+                            const int key = tile.key + 16 * b + gr + 8 * h;
+                            const bool on = key <= hi[nt][e] && (key >= lo[nt][e] || key < sinks);
                             if (on) see |= 1u << ((b * NT + nt) * 4 + 2 * h + e);
                         }
                 }
@@ -687,15 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
                 }
         }
         // ---- weights, as B fragments: P^T ----
-        float tile_top;  // the largest scale: as bits, so that a NaN is the largest
-        {
-            uint32_t bits = 0;
-            if (!TREE || tile.key >= 0)
-                bits = __float_as_uint(svs[lane * g.hb]) & 0x7fffffffu;
-            else
-                bits = 0x7fc00000u;  // drafted rows take the slow way
-            tile_top = __uint_as_float(__reduce_max_sync(FULL, bits));
-        }
+        // The largest scale, as bits, so that a NaN is the largest.
+        const float tile_top = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(svs[lane * g.hb]) & 0x7fffffffu));
         uint32_t ph[2][NT][2], pl[2][NT][2];  // hi, lo
         const bool fast = tile_top <= limit;
         float w[2][NT][4];
@@ -773,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
                     pl[b][nt][h] = mma_transpose(pl[b][nt][h]);
                 }
         // ---- O^T += V^T P^T: row gr of product i is channel (D / 8) gr + 2 i, row gr + 8 the next ----
-        if (!TREE || tile.key >= 0) {
+        {
             constexpr int W = D / 32;  // words of a lane's channels of one key
             uint32_t vw[2][4][W];
 #pragma unroll
@@ -812,43 +676,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
                                       o[2 * k + i][nt][e], o[2 * k + i][nt][e + 1]);
                     }
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                float acc[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    uint32_t fh[4], fl[4];
-                    float2 y[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        y[j] = __ldg(reinterpret_cast<const float2*>(vrow[b][j] + (D / 8) * gr + 2 * i));
-                        y[j] = vinv[b][j] == 0.f ? make_float2(0.f, 0.f) : make_float2(y[j].x * vinv[b][j], y[j].y * vinv[b][j]);
-                    }
-                    mma_split(y[0].x, y[1].x, fh[0], fl[0]);
-                    mma_split(y[0].y, y[1].y, fh[1], fl[1]);
-                    mma_split(y[2].x, y[3].x, fh[2], fl[2]);
-                    mma_split(y[2].y, y[3].y, fh[3], fl[3]);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_16816(acc[nt], fh, pl[b][nt][0], pl[b][nt][1]);
-                        mma_16816(acc[nt], fl, ph[b][nt][0], ph[b][nt][1]);
-                        mma_16816(acc[nt], fh, ph[b][nt][0], ph[b][nt][1]);
-                    }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[i][nt][e] += acc[nt][e];
-            }
         }
         give_back();
         // ---- the end of a piece ----
         if (tile.flags & kLast) {
+            if (a.tree) pdl_wait();  // the drafted rows' part
             const int slot = ((tile.flags >> kSlotShift) & 3) - 1;
             // Key groups: the others leave theirs as partials in slot 2, group 0 takes them in.
             const uint32_t turn = (uint32_t)(pieces++ & 1);
@@ -907,7 +739,22 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
                     float* to = nullptr;
                     const int where = group ? 2 : slot;
                     if (where < 0) {
-                        if (v < rq.T * a.G) to = a.out + (((int64_t)rq.row0 + t) * a.H + (int64_t)hk * a.G + (v - t * a.G)) * D;
+                        if (v < rq.T * a.G) {
+                            const int64_t row = ((int64_t)rq.row0 + t) * a.H + (int64_t)hk * a.G + (v - t * a.G);
+                            to = a.out + row * D;
+                            if (a.tree) {
+                                const Q8Share w = q8_share(top, sum, __ldcg(g.draft + row));
+#pragma unroll
+                                for (int d = 0; d < D / 8; d += 4) {
+                                    float4 z = __ldcg(reinterpret_cast<const float4*>(to + (D / 8) * gr + d));
+                                    if (q8_nothing(w.draft)) z = make_float4(0.f, 0.f, 0.f, 0.f);
+                                    y[d] = fmaf(w.own, y[d], w.draft * z.x);
+                                    y[d + 1] = fmaf(w.own, y[d + 1], w.draft * z.y);
+                                    y[d + 2] = fmaf(w.own, y[d + 2], w.draft * z.z);
+                                    y[d + 3] = fmaf(w.own, y[d + 3], w.draft * z.w);
+                                }
+                            }
+                        }
                     } else {
                         const int64_t at = part_row(where, warp, i);
                         to = g.part_o + at * D;
@@ -978,7 +825,16 @@ __global__ void __launch_bounds__(256) q8_merge_kernel(const __grid_constant__ M
         }
     }
     const int t = v / a.G;
-    float* out = a.out + (((int64_t)h.w + t) * a.H + (int64_t)hk * a.G + (v - t * a.G)) * D;
+    const int64_t at = ((int64_t)h.w + t) * a.H + (int64_t)hk * a.G + (v - t * a.G);
+    float* out = a.out + at * D;
+    if (a.tree) {
+        const Q8Share w = q8_share(m, den, __ldcg(g.draft + at));
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) {
+            const float z = q8_nothing(w.draft) ? 0.f : __ldcg(out + lane + 32 * c);
+            acc[c] = fmaf(w.own, acc[c], w.draft * z);
+        }
+    }
 #pragma unroll
     for (int c = 0; c < kPer; ++c) out[lane + 32 * c] = acc[c];
 }
@@ -989,20 +845,21 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 int blocks_of(const PagedDesc& a) { return (int64_t)a.max_rows * a.G <= 8 ? 1 : 2; }
 
 struct Scratch {
-    size_t m, l, o, head, total;
+    size_t m, l, o, head, draft, total;
 };
-Scratch scratch_of(int NV, int D) {
+Scratch scratch_of(int NV, int D, int64_t draft_rows) {
     const size_t rows = (size_t)3 * kPagedMaxCtas * kConsumers * NV;
     Scratch s;
     s.m = kWorkspaceHeader;
     s.l = s.m + up256(rows * 4);
     s.o = s.l + up256(rows * 4);
     s.head = s.o + up256(rows * D * 4);
-    s.total = s.head + up256((size_t)2 * kPagedMaxCtas * sizeof(int4));
+    s.draft = s.head + up256((size_t)2 * kPagedMaxCtas * sizeof(int4));
+    s.total = s.draft + up256((size_t)draft_rows * sizeof(float2));
     return s;
 }
 
-template <int D, int NT, int FORM, bool TREE>
+template <int D, int NT, int FORM>
 cudaError_t launch_form(MmaArgs& g, int num_sms, void* workspace, cudaStream_t stream) {
     const PagedDesc& a = g.a;
     g.blocks = (a.Hk + kConsumers - 1) / kConsumers;
@@ -1013,19 +870,26 @@ cudaError_t launch_form(MmaArgs& g, int num_sms, void* workspace, cudaStream_t s
              ((reinterpret_cast<uintptr_t>(g.p.k_scale) | reinterpret_cast<uintptr_t>(g.p.v_scale)) & 15u) == 0;
     g.stage = 32 * g.kg * g.hb * (2 * D + 8);
     const int ctas = num_sms < kPagedMaxCtas ? num_sms : kPagedMaxCtas;
-    const Scratch s = scratch_of(8 * NT, D);
+    const Scratch s = scratch_of(8 * NT, D, 0);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     g.part_m = reinterpret_cast<float*>(ws + s.m);
     g.part_l = reinterpret_cast<float*>(ws + s.l);
     g.part_o = reinterpret_cast<float*>(ws + s.o);
     g.head = reinterpret_cast<int4*>(ws + s.head);
-    auto kern = q8_mma_kernel<D, NT, FORM, TREE>;
+    float2* draft = reinterpret_cast<float2*>(ws + s.draft);
+    g.draft = draft;
+    auto kern = q8_mma_kernel<D, NT, FORM>;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), (int)kSmemMost);
     if (e != cudaSuccess) return e;
     const size_t smem = (size_t)kStages * g.stage + (size_t)(a.B + 1) * 8;
     if (smem > kSmemMost) return cudaErrorInvalidConfiguration;
-    kern<<<ctas, kThreads, smem, stream>>>(g);
-    e = cudaGetLastError();
+    if (a.tree) {  // the cached part runs beside the drafted one and waits for it at the end
+        e = launch_paged_q8_draft(a, draft, stream);
+        if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, g);
+    } else {
+        kern<<<ctas, kThreads, smem, stream>>>(g);
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return e;
     const int64_t most = (int64_t)a.max_rows * a.G;
     const int live = most < 8 * NT ? (int)most : 8 * NT;
@@ -1034,11 +898,8 @@ cudaError_t launch_form(MmaArgs& g, int num_sms, void* workspace, cudaStream_t s
 }
 template <int D, int NT>
 cudaError_t launch_nt(MmaArgs& g, int num_sms, void* ws, cudaStream_t stream) {
-    if (g.p.form == kFormInt8)
-        return g.a.tree ? launch_form<D, NT, kFormInt8, true>(g, num_sms, ws, stream)
-                        : launch_form<D, NT, kFormInt8, false>(g, num_sms, ws, stream);
-    return g.a.tree ? launch_form<D, NT, kFormE4m3, true>(g, num_sms, ws, stream)
-                    : launch_form<D, NT, kFormE4m3, false>(g, num_sms, ws, stream);
+    return g.p.form == kFormInt8 ? launch_form<D, NT, kFormInt8>(g, num_sms, ws, stream)
+                                 : launch_form<D, NT, kFormE4m3>(g, num_sms, ws, stream);
 }
 
 }  // namespace
@@ -1047,7 +908,9 @@ bool paged_q8_mma_supported(const PagedDesc& a) {
     return (a.D == 64 || a.D == 128) && a.pages > 0 && (int64_t)a.max_rows * a.G < ((int64_t)1 << 30);
 }
 
-size_t paged_q8_mma_workspace(const PagedDesc& a) { return scratch_of(8 * blocks_of(a), a.D).total; }
+size_t paged_q8_mma_workspace(const PagedDesc& a) {
+    return scratch_of(8 * blocks_of(a), a.D, a.tree ? a.rows * a.H : 0).total;
+}
 
 cudaError_t launch_paged_q8_mma(const PagedDesc& a, const Q8Pools& p, int num_sms, void* workspace, cudaStream_t stream) {
     MmaArgs g;
