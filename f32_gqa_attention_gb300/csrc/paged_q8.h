@@ -48,6 +48,13 @@ cudaError_t launch_paged_q8_ffma(const PagedDesc& a, const Q8Pools& p, cudaStrea
 bool paged_q8_mma_supported(const PagedDesc& a);
 size_t paged_q8_mma_workspace(const PagedDesc& a);
 cudaError_t launch_paged_q8_mma(const PagedDesc& a, const Q8Pools& p, int num_sms, void* workspace, cudaStream_t stream);
+// tcgen05 products of 128-row blocks, for the same calls.
+size_t paged_q8_tc_workspace(const PagedDesc& a);
+cudaError_t launch_paged_q8_tc(const PagedDesc& a, const Q8Pools& p, int num_sms, void* workspace, cudaStream_t stream);
+unsigned int paged_q8_tc_take_device_error();
+// Which of the two: virtual rows (rows of a request x heads of a group) above this take the blocks of 128.
+constexpr int kQ8FewRows = 16;
+inline bool paged_q8_few_rows(const PagedDesc& a) { return (int64_t)a.max_rows * a.G <= kQ8FewRows; }
 // The drafted rows' part of every row: its output to a.out, its maximum and sum to ml [rows][H].
 cudaError_t launch_paged_q8_draft(const PagedDesc& a, float2* ml, cudaStream_t stream);
 unsigned int paged_q8_take_device_error();

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], 32 * kProducers);  // every producer lane's copies
+            mbar_init(&full[i], 32 * kProducers + 1);  // every producer lane's copies, and what the tile is
             mbar_init(&freed[i], consumers);
         }
         mbar_init(&x_put, consumers - g.hb > 0 ? consumers - g.hb : 1);
@@ -277,7 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
                 break;
             }
             unsigned char* to = smem + (size_t)st * g.stage;
-            if (pw == 0 && lane == 0) tile_s[st] = t;
+            if (pw == 0 && lane == 0) {
+                tile_s[st] = t;
+                mbar_arrive(&full[st]);
+            }
             if (t.key >= 0) {
                 const int hb = min(g.hb, a.Hk - h0), chunks = hb * (D / 16);  // of a row
                 int row[2];

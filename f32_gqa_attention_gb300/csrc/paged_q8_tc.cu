@@ -1,0 +1,922 @@
+// paged_q8_tc.cu -- attention of many query rows per request over an 8-bit paged cache on
+// the tcgen05 tensor cores, headDim 64 or 128: trees of drafted tokens, chunks of prompts.
+//
+// Mathematics as in paged_q8_mma.cu, for row blocks of 128 virtual rows (t G + g) and tiles of
+// 64 keys.  Codes are exact in f16, so S = Q K^T and O = P V are two f16 products each: hi and
+// lo of the queries and of the weights, lo first.  Every tile stands alone: its weights are
+// 2^(x2 - m_t), m_t the row's largest score in the tile, times the value's scale over 2^E, E
+// the largest scale's exponent; its output O_t and sum l_t come with m_t and E, and the
+// fold joins them in f32 by the log-sum-exp rule,
+//   acc = acc 2^(M - M') + O_t 2^(m_t + E - M'),  M' = max(M, m_t).
+// So no tile waits for another one's maximum, two softmax warpgroups take tiles in turn, and
+// no sum runs long inside the tensor cores, which round towards zero at every step.
+// A weight has 2^14 as a factor: kept to 2^-39 of the largest scale times 1.  Where a tile's
+// scales differ by more than 2^6 a small one may be what counts, so each row of such a tile
+// takes the exponent of its own largest product instead (rare).
+//
+// Work.  One persistent CTA per SM; the CTAs divide the tiles of all (request, KV head, row
+// block) units evenly.  A unit cut by a CTA's end leaves partials (m, l, o / l) that
+// q8_tc_merge_kernel joins in a fixed order.
+//
+// Warps, with their share of the 480 registers a lane that five warpgroups launch with:
+//   0, 2    page ids and 16-byte asynchronous copies of K and of V codes and scales
+//   1       MMAs: S(n), then O(n - 1); one elected lane issues                      (56)
+//   4 - 7   queries to TMEM, and the fold; a thread is a row, acc in registers     (184)
+//   8 - 15  softmax of even and of odd tiles; a thread is a row                  (2 x 96)
+//   16 - 19 codes to f16 tiles, and the scales' range                               (48)
+// TMEM: Q hi, lo (D columns), two S / P buffers (128), two O buffers (2 D).
+// Every wait is bounded; one that gives up sets a bit of the device flag.
+#include <cstring>
+
+#include "attn_common.cuh"
+#include "launch_cache.h"
+#include "paged_q8_list.cuh"
+#include "paged_q8_mma.cuh"
+#include "pdl.cuh"
+#include "softcap.cuh"
+#include "tcgen05_ops.cuh"
+#include "tma_sync.cuh"
+
+namespace vtmu {
+
+__device__ unsigned int g_q8_tc_device_error;
+
+namespace {
+
+constexpr unsigned FULL = 0xffffffffu;
+constexpr int kKT = 64, kM = 128, kThreads = 640;
+constexpr int kStages = 4;  // tiles of codes
+constexpr int kSlots = 3;   // tiles of f16, of K and of V
+constexpr int kRing = 8;    // scales of a tile: stage n is loaded once PV(n - 7) is done, so softmax(n - 8) is
+constexpr int kTiles = 16;  // what it is: the fold of a tile that far back may not have begun
+constexpr int kShift = 14;  // of weights in f16
+constexpr int kFar = 6;     // log2 by which a tile's scales may differ on the short way
+enum : int { kFirst = 1, kLast = 2, kStop = 4, kSlotShift = 3 };  // flags of a tile; slot + 1 above them
+enum : unsigned int {
+    kErrQ8Load = 1u << 3,  // the paged kernels' bits: a tile that did not come,
+    kErrQ8Free = 1u << 4,  // a buffer that was not given back,
+    kErrQ8Mma = 1u << 5,   // a wait around the MMAs
+};
+
+struct TcArgs {
+    PagedDesc a;
+    Q8Pools p;
+    int32_t page_shift;
+    float* part_m;  // [2 CTAs][128]: slot 0 goes on with a unit, slot 1 starts one
+    float* part_l;
+    float* part_o;  // [2 CTAs][128][D], divided by l
+    const float2* draft;
+    int4* head;     // [2 CTAs]: the unit a CTA starts: last CTA, first virtual row, rows x group, first packed row; KV head
+};
+
+template <int D>
+struct Cfg {
+    static constexpr uint32_t kCodes = kKT * D, kTile = 2 * kCodes;  // bytes of a tile, as codes and as f16
+    static constexpr size_t kSmem = 1024 + 2 * kSlots * kTile + kStages * 2 * kCodes + (kPagedMaxRequests + 1) * 8;
+    static constexpr uint32_t kColQhi = 0, kColQlo = D / 2, kColS = D, kColO = D + 2 * kKT;
+    static_assert(kColO + 2 * D <= 512, "TMEM budget");
+    static_assert(kSmem + 16 * 1024 <= 232448, "shared memory budget");
+};
+
+struct Tile {
+    int b, rb, key, flags, hk, piece, pad0, pad1;
+};
+
+// A CTA's place in the list, for the producers.
+struct Walk {
+    long long pos, end, total, ctas;
+    int b, rb, hk, u, u1, len, lo_tile, n_sink, slot, piece;
+    bool first;
+    int4 starts;  // the cut unit that this CTA starts (x < 0: none)
+    int starts_head;
+
+    __device__ void start(const PagedDesc& a, const long long* prefix) {
+        total = prefix[a.B];
+        ctas = max(min((long long)gridDim.x, total), 1ll);
+        const int c = blockIdx.x;
+        pos = c < ctas ? total * c / ctas : 0;
+        end = c < ctas ? total * (c + 1) / ctas : 0;
+        int hi = a.B;
+        b = 0;  // the last request whose prefix is at most pos
+        while (hi - b > 1) {
+            const int mid = (b + hi) >> 1;
+            if (prefix[mid] <= pos) b = mid; else hi = mid;
+        }
+        u = u1 = 0;
+        piece = -1;
+        starts = make_int4(-1, 0, 0, 0);
+        starts_head = 0;
+    }
+    template <class Empty>
+    __device__ bool next(const PagedDesc& a, const long long* prefix, Tile& t, Empty empty) {
+        while (u >= u1) {
+            if (pos >= end) return false;
+            while (prefix[b + 1] <= pos) ++b;
+            const Q8Req r = q8_load_req(a, b);
+            const Q8Units w = q8_units(a, r, kKT);
+            const long long rel = pos - prefix[b], unit = rel / w.nt;
+            const int blocks = (r.T * a.G + kM - 1) / kM;
+            hk = (int)(unit / blocks);
+            rb = (int)(unit - (long long)hk * blocks);
+            u = (int)(rel - unit * w.nt);
+            u1 = (int)min((long long)w.nt, u + (end - pos));
+            const long long from = pos - u;
+            pos += u1 - u;
+            slot = u > 0 ? 0 : u1 < w.nt ? 1 : -1;
+            if (slot == 1) {
+                starts = make_int4((int)(((from + w.nt) * ctas - 1) / total), rb * kM, r.T * a.G, r.row0);
+                starts_head = hk;
+            }
+            if (!a.tree) u1 = min(u1, q8_seen_tiles(r, w, (min((rb + 1) * kM, r.T * a.G) - 1) / a.G, kKT));
+            len = r.len;
+            lo_tile = w.lo_tile;
+            n_sink = w.n_sink;
+            first = true;
+            if (u >= u1) empty(slot);
+            else ++piece;
+        }
+        t.b = b;
+        t.rb = rb;
+        t.hk = hk;
+        t.piece = piece;
+        t.key = (u < n_sink ? u : lo_tile + u - n_sink) * kKT;
+        t.flags = (first ? kFirst : 0) | (u + 1 == u1 ? kLast : 0) | (slot + 1) << kSlotShift;
+        first = false;
+        ++u;
+        return true;
+    }
+};
+
+// ---- f16 MMAs (as the f32 cache's kernel) ---------------------------------------------------
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool mn) {
+    return (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// A tile's blocks of 64 channels, [64 rows][128 bytes] with the 128-byte swizzle, 8 KB apart.
+// K-major: a row's channels along K.  MN-major: the rows are K, the next 64 channels a block on.
+__device__ __forceinline__ uint64_t smem_desc(const void* tile, uint32_t next) {
+    const uint64_t addr = smem_u32(tile);
+    uint64_t d = (addr >> 4) & 0x3FFFull;
+    d |= (uint64_t)(next >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+// mbar_wait, bounded in the same way, that looks at the clock late and seldom: reading the
+// global timer takes as long as a whole hand-over.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < 4096; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    do {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+    } while (global_ns() - t0 <= kWaitLimitNs);
+    return false;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase, unsigned int error) {
+    if (__all_sync(FULL, wait_for(bar, (uint32_t)(phase & 1)))) return true;
+    raise_device_error(&g_q8_tc_device_error, error);
+    return false;
+}
+
+// Chunk c (16 bytes) of row `row` of a tile of codes: the converting lanes read 64 bytes of
+// two neighbouring rows at a time.
+template <int D>
+__device__ __forceinline__ int code_chunk(int row, int c) {
+    return D == 128 ? c ^ ((row & 1) << 2) : c;
+}
+
+// Codes of a tile to f16: four warps, 16 rows each, a lane 16 codes at a time.
+template <int D, int FORM>
+__device__ __forceinline__ void convert(const unsigned char* codes, unsigned char* tile, int w, int lane) {
+    const int sub = lane & 7;
+#pragma unroll
+    for (int i = 0; i < (D == 128 ? 4 : 2); ++i) {
+        const int row = 16 * w + 8 * (i & 1) + 2 * (lane >> 3) + (sub >> 2), c = (sub & 3) + 4 * (i >> 1);
+        const uint4 x = *reinterpret_cast<const uint4*>(codes + row * D + 16 * code_chunk<D>(row, c));
+        uint32_t h[8];
+        q8_halves<FORM>(x.x, h[0], h[1]);
+        q8_halves<FORM>(x.y, h[2], h[3]);
+        q8_halves<FORM>(x.z, h[4], h[5]);
+        q8_halves<FORM>(x.w, h[6], h[7]);
+        unsigned char* to = tile + (c >> 2) * 8192 + row * 128;
+        const int j = 2 * (c & 3), sw = row & 7;
+        *reinterpret_cast<uint4*>(to + 16 * (j ^ sw)) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(to + 16 * ((j + 1) ^ sw)) = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+}
+
+// What a softmax thread needs of its row and tile.
+struct RowTile {
+    uint32_t at;       // TMEM of its scores
+    const float* ks;   // the keys' scales
+    uint64_t see;      // keys that it sees (not read when WHOLE)
+    float rf, cap;     // a score of the MMA times ks rf is one in base-2 units (the argument of tanh with a cap)
+};
+// 32 scores from key 32 c on: in base-2 units with a cap, else still to be multiplied by rf.
+template <bool CAP, bool WHOLE>
+__device__ __forceinline__ void row_scores(const RowTile& r, int c, float (&x)[32]) {
+    tmem_ld32(r.at + 32 * c, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+        const float4 s = *reinterpret_cast<const float4*>(r.ks + 32 * c + k);
+        f2_unpack(f2_mul(f2_pack(x[k], x[k + 1]), f2_pack(s.x, s.y)), x[k], x[k + 1]);
+        f2_unpack(f2_mul(f2_pack(x[k + 2], x[k + 3]), f2_pack(s.z, s.w)), x[k + 2], x[k + 3]);
+    }
+    if constexpr (CAP) softcap_tile<32>(x, r.rf, r.cap);
+    if constexpr (!WHOLE) {
+        const uint32_t bits = (uint32_t)(r.see >> (32 * c));
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = (bits >> k) & 1u ? x[k] : -INFINITY;
+    }
+}
+template <bool CAP, bool WHOLE>
+__device__ __forceinline__ float row_max(const RowTile& r) {
+    float mt = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+        float x[32];
+        row_scores<CAP, WHOLE>(r, c, x);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) mt = fmaxf(fmaxf(mt, x[k]), x[k + 1]);
+    }
+    return CAP ? mt : mt * r.rf;
+}
+// 32 weights as f16 hi (16 columns) and lo (16) over their scores.
+__device__ __forceinline__ void store_weights(uint32_t at, const float (&w)[32]) {
+    float hi[16], lo[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+        uint32_t h, l;
+        mma_split(w[k], w[k + 1], h, l);
+        hi[k / 2] = __uint_as_float(h);
+        lo[k / 2] = __uint_as_float(l);
+    }
+    tmem_st16(at, hi);
+    tmem_st16(at + 16, lo);
+}
+// Weights 2^(x2 - mu) vn over the scores; returns the sum of the exponentials.  vn: the values'
+// scales times 2^(kShift - E).
+template <bool CAP, bool WHOLE>
+__device__ __forceinline__ float row_weights(const RowTile& r, const float* vn, float mu) {
+    const float mul = CAP ? 1.f : r.rf;
+    const uint64_t mul2 = f2_pack(mul, mul), sub2 = f2_pack(-mu, -mu);
+    uint64_t sum = 0;
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+        float x[32];
+        row_scores<CAP, WHOLE>(r, c, x);
+        const uint32_t bits = (uint32_t)(r.see >> (32 * c));
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(vn + 32 * c + k);
+            const float vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                float e0, e1;
+                f2_unpack(f2_fma(f2_pack(x[k + j], x[k + j + 1]), mul2, sub2), e0, e1);
+                const uint64_t p = f2_pack(fast_exp2(e0), fast_exp2(e1));
+                sum = f2_add(sum, p);
+                f2_unpack(f2_mul(p, f2_pack(vv[j], vv[j + 1])), x[k + j], x[k + j + 1]);
+                if constexpr (!WHOLE) {  // the scale of a key that is not seen may be anything
+                    if (!((bits >> (k + j)) & 1u)) x[k + j] = 0.f;
+                    if (!((bits >> (k + j + 1)) & 1u)) x[k + j + 1] = 0.f;
+                }
+            }
+        }
+        store_weights(r.at + 32 * c, x);
+    }
+    float a, b;
+    f2_unpack(sum, a, b);
+    return a + b;
+}
+// The same with scales of very different size: relative to the row's largest product
+// 2^(x2 - mu) 2^e, e the scales' exponents.  Returns the sum, and that product's exponent.
+template <bool CAP>
+__device__ __noinline__ float far_weights(const RowTile& r, const float* vs, float mu, float* lift) {
+    auto power = [](float v) -> float { return (float)((int)((__float_as_uint(v) >> 23) & 255u) - 127); };
+    const float mul = CAP ? 1.f : r.rf;
+    float top = -300.f;
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+        float x[32];
+        row_scores<CAP, false>(r, c, x);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) top = fmaxf(top, fmaf(x[k], mul, -mu) + power(vs[32 * c + k]));
+    }
+    top = ceilf(fminf(top, 126.f));
+    *lift = top;
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+        float x[32];
+        row_scores<CAP, false>(r, c, x);
+        const uint32_t bits = (uint32_t)(r.see >> (32 * c));
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            const float v = vs[32 * c + k], e = power(v), y = fmaf(x[k], mul, -mu);
+            const float part = v * (e > 0.f ? exp2f(-e) : exp2f(-e - 1.f) * 2.f);  // the scale's mantissa; 0 stays 0
+            sum += fast_exp2(y);
+            const float w = fast_exp2(y + (e - top)) * part * (float)(1 << kShift);
+            x[k] = (bits >> k) & 1u ? w : 0.f;
+        }
+        store_weights(r.at + 32 * c, x);
+    }
+    return sum;
+}
+
+template <int D, int FORM, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constant__ TcArgs g) {
+    using C = Cfg<D>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* ktiles = tiles;
+    unsigned char* vtiles = tiles + kSlots * C::kTile;
+    unsigned char* codes = tiles + 2 * kSlots * C::kTile;  // stage: K, V
+    long long* prefix = reinterpret_cast<long long*>(codes + (size_t)kStages * 2 * C::kCodes);
+    __shared__ __align__(8) uint64_t staged[kStages], unstaged[kStages], k_ready[kSlots], k_free[kSlots], v_ready[kSlots],
+        v_free[kSlots], q_full, s_full[2], p_full[2], o_full[2], o_free[2];
+    __shared__ uint32_t tmem_base_s;
+    __shared__ long long scan_s[kThreads / 32];
+    __shared__ __align__(16) float k_scale[kRing][kKT], v_scale[kRing][kKT], v_norm[kRing][kKT];
+    __shared__ float v_back[kRing];              // 2^(E - kShift); 0: the scales differ too much
+    __shared__ __align__(16) Tile tile_s[kTiles];
+    __shared__ float q_back[4][kM];              // by piece: what the queries' power of two takes back
+    __shared__ __align__(16) float4 stat[4][kM]; // by tile: m, l, factor of its output
+
+    const PagedDesc& a = g.a;
+    const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&staged[i], 2 * 32 + 1);  // two warps' copies, and what the tile is
+            mbar_init(&unstaged[i], 4);
+        }
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&k_ready[i], 4);
+            mbar_init(&v_ready[i], 4);
+            mbar_init(&k_free[i], 1);
+            mbar_init(&v_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_full[i], 1);
+            mbar_init(&o_free[i], 4);
+        }
+        mbar_init(&q_full, 4);
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc(&tmem_base_s, 512);
+    // The requests' tiles and their running sum.
+    long long carry = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        long long v = 0;
+        if (b < a.B) {
+            const Q8Req r = q8_load_req(a, b);
+            v = ((long long)r.T * a.G + kM - 1) / kM * a.Hk * q8_units(a, r, kKT).nt;
+        }
+        long long s = v;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long u = __shfl_up_sync(FULL, s, off);
+            if (lane >= off) s += u;
+        }
+        if (lane == 31) scan_s[warp] = s;
+        __syncthreads();
+        long long before = carry, all = carry;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += scan_s[w];
+            all += scan_s[w];
+        }
+        if (b < a.B) prefix[b] = before + s - v;
+        carry = all;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) prefix[a.B] = carry;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+    auto part_row = [&](int slot, int i) -> int64_t { return (int64_t)(2 * blockIdx.x + slot) * kM + i; };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0 || warp == 2) {
+            // ---- producers: K and V ---------------------------------------------------------
+            const bool values = warp == 2;
+            Walk walk;
+            walk.start(a, prefix);
+            auto empty = [&](int slot) {
+                if (slot < 0 || values) return;
+                for (int i = lane; i < kM; i += 32) {
+                    g.part_m[part_row(slot, i)] = -INFINITY;
+                    g.part_l[part_row(slot, i)] = 0.f;
+                }
+            };
+            const uint8_t* pool = values ? g.p.v : g.p.k;
+            const float* scales = values ? g.p.v_scale : g.p.k_scale;
+            // Lane i looks up rows i and i + 32, a tile ahead of its copies.
+            Tile t, ahead;
+            int page[2], page_ahead[2];
+            auto look = [&]() {
+                if (!walk.next(a, prefix, ahead, empty)) {
+                    ahead.flags = kStop;
+                    ahead.key = 0;
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    page_ahead[j] = -1;
+                    const int key = ahead.key + lane + 32 * j;
+                    if (!(ahead.flags & kStop) && key < walk.len)
+                        page_ahead[j] = __ldg(a.block_table + (int64_t)ahead.b * a.max_pages +
+                                              (g.page_shift >= 0 ? key >> g.page_shift : key / a.page_size));
+                }
+            };
+            look();
+            for (int n = 0;; ++n) {
+                t = ahead;
+                page[0] = page_ahead[0];
+                page[1] = page_ahead[1];
+                const bool stop = t.flags & kStop;
+                if (!stop) look();
+                const int st = n % kStages;
+                if (n >= kStages && !warp_wait(&unstaged[st], n / kStages - 1, kErrQ8Free)) break;
+                if (!values && lane == 0) {
+                    tile_s[n % kTiles] = t;
+                    if (stop) tile_s[(n + 1) % kTiles] = t;  // for the other softmax warps
+                    mbar_arrive(&staged[st]);
+                }
+                if (!stop) {
+                    unsigned char* to = codes + (size_t)(2 * st + (values ? 1 : 0)) * C::kCodes;
+                    int row[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int key = t.key + lane + 32 * j;
+                        row[j] = (unsigned)page[j] < (unsigned)a.pages
+                                     ? page[j] * a.page_size +
+                                           (g.page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size)
+                                     : -1;
+                        const int64_t at = (int64_t)max(row[j], 0) * a.Hk + t.hk;
+                        cp_async4((values ? v_scale : k_scale)[n % kRing] + lane + 32 * j, scales + at, row[j] >= 0 ? 4 : 0);
+                    }
+                    constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+                    const int64_t pitch = (int64_t)a.Hk * D;
+                    const uint8_t* src = pool + (int64_t)t.hk * D + 16 * (lane % kLanes);
+#pragma unroll
+                    for (int i = 0; i < kKT / kRows; ++i) {
+                        const int r = i * kRows + lane / kLanes;
+                        const int from = __shfl_sync(FULL, row[i * kRows / 32], r & 31);
+                        cp_async16(to + r * D + 16 * code_chunk<D>(r, lane % kLanes), src + max(from, 0) * pitch, from >= 0 ? 16 : 0);
+                    }
+                }
+                cp_async_arrive(&staged[st]);
+                if (stop) break;
+            }
+            cp_async_wait_all();  // no copy may be in flight when the CTA exits
+            if (!values && lane == 0) {
+                g.head[2 * blockIdx.x] = walk.starts;
+                g.head[2 * blockIdx.x + 1] = make_int4(walk.starts_head, 0, 0, 0);
+            }
+        } else if (warp == 1) {
+            // ---- MMAs ---------------------------------------------------------------------
+            constexpr uint32_t id_s = idesc_f16(kM, kKT, false), id_o = idesc_f16(kM, D, true);
+            const uint64_t k0 = smem_desc(ktiles, 16), v0 = smem_desc(vtiles, 8192);
+            auto pv = [&](int j) -> bool {  // O(j) = P(j) V(j)
+                const int bf = j & 1, st = j % kSlots;
+                if (!warp_wait(&p_full[bf], j >> 1, kErrQ8Mma) || !warp_wait(&v_ready[st], j / kSlots, kErrQ8Mma) ||
+                    (j >= 2 && !warp_wait(&o_free[bf], (j >> 1) - 1, kErrQ8Mma)))
+                    return false;
+                tc_fence_after();
+                const uint32_t d = tmem + C::kColO + bf * D, p = tmem + C::kColS + bf * kKT;
+                const uint64_t v = v0 + st * (C::kTile >> 4);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < kKT / 16; ++k)
+                        mma_f16_ts(d, p + 32 * (k >> 1) + 8 * (k & 1) + 16, v + (2048 >> 4) * k, id_o, k > 0 ? 1u : 0u);
+#pragma unroll
+                    for (int k = 0; k < kKT / 16; ++k)
+                        mma_f16_ts(d, p + 32 * (k >> 1) + 8 * (k & 1), v + (2048 >> 4) * k, id_o, 1u);
+                    mma_commit(&v_free[st]);
+                    mma_commit(&o_full[bf]);
+                }
+                __syncwarp();
+                return true;
+            };
+            for (int n = 0;; ++n) {
+                const int st = n % kSlots;
+                if (!warp_wait(&k_ready[st], n / kSlots, kErrQ8Mma)) break;
+                const int flags = tile_s[n % kTiles].flags;
+                if (flags & kStop) {
+                    // The others learn of it in turn, once they have taken their last tiles.
+                    if (n > 0 && !pv(n - 1)) break;
+                    if (n >= 2 && !warp_wait(&o_free[n & 1], (n >> 1) - 1, kErrQ8Mma)) break;
+                    if (lane == 0) {
+                        mbar_arrive(&s_full[n & 1]);
+                        mbar_arrive(&s_full[(n + 1) & 1]);
+                        mbar_arrive(&o_full[n & 1]);
+                    }
+                    break;
+                }
+                if ((flags & kFirst) && !warp_wait(&q_full, tile_s[n % kTiles].piece, kErrQ8Mma)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + C::kColS + (n & 1) * kKT;
+                const uint64_t k = k0 + st * (C::kTile >> 4);
+                if (elect_one()) {
+                    auto off = [](int i) -> uint64_t { return (uint64_t)(i >> 2) * (8192 >> 4) + 2 * (i & 3); };
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) mma_f16_ts(d, tmem + C::kColQlo + 8 * i, k + off(i), id_s, i > 0 ? 1u : 0u);
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) mma_f16_ts(d, tmem + C::kColQhi + 8 * i, k + off(i), id_s, 1u);
+                    mma_commit(&k_free[st]);
+                    mma_commit(&s_full[n & 1]);
+                }
+                __syncwarp();
+                if (n > 0 && !pv(n - 1)) break;
+            }
+        }
+    } else if (warp < 8) {
+        // ---- queries and fold: thread = virtual row --------------------------------------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        const int w = warp & 3, i = 32 * w + lane;
+        const uint32_t lanes = (uint32_t)(32 * w) << 16;
+        bool ok = true;
+        // The queries of the piece that tile j begins: times qk_mul and a power of two that brings
+        // the row's largest element to [2^13, 2^14).  False at the list's end.
+        auto load_queries = [&](int j) -> bool {
+            if (!warp_wait(&k_ready[j % kSlots], j / kSlots, kErrQ8Mma)) {  // what tile j is
+                ok = false;
+                return false;
+            }
+            const Tile t = tile_s[j % kTiles];
+            if (t.flags & kStop) return false;
+            const Q8Req rq = q8_load_req(a, t.b);
+            const int v = t.rb * kM + i, row = v / a.G;
+            const bool alive = v < rq.T * a.G;
+            const float* q = a.q + (((int64_t)rq.row0 + row) * a.H + (int64_t)t.hk * a.G + (v - row * a.G)) * D;
+            auto load4 = [&](int d) -> float4 {
+                if (!alive) return make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 y = __ldg(reinterpret_cast<const float4*>(q + d));
+                return make_float4(y.x * a.qk_mul, y.y * a.qk_mul, y.z * a.qk_mul, y.w * a.qk_mul);
+            };
+            float top = 0.f;
+#pragma unroll 8
+            for (int d = 0; d < D; d += 4) top = q8_abs_top(top, load4(d));
+            const float sc = mma_row_scale(top, 13);
+            q_back[t.piece & 3][i] = 1.f / sc;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D / 2; c0 += 16) {
+                float qh[16], ql[16];
+#pragma unroll
+                for (int c = 0; c < 16; c += 2) {
+                    const float4 y = load4(2 * (c0 + c));
+                    uint32_t h0, l0, h1, l1;
+                    mma_split(y.x * sc, y.y * sc, h0, l0);
+                    mma_split(y.z * sc, y.w * sc, h1, l1);
+                    qh[c] = __uint_as_float(h0);
+                    qh[c + 1] = __uint_as_float(h1);
+                    ql[c] = __uint_as_float(l0);
+                    ql[c + 1] = __uint_as_float(l1);
+                }
+                tmem_st16(tmem + lanes + C::kColQhi + c0, qh);
+                tmem_st16(tmem + lanes + C::kColQlo + c0, ql);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full);
+            return true;
+        };
+        // The next piece's queries go in once the scores of this one's last tile are done: S(n + 1)
+        // is issued before PV(n), so O(n) tells.
+        bool more = load_queries(0);
+        if (more && (tile_s[0].flags & kLast)) {
+            more = warp_wait(&s_full[0], 0, kErrQ8Mma);
+            ok = more;
+            tc_fence_after();
+            if (more) load_queries(1);
+        }
+        float acc[D], M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int d = 0; d < D; ++d) acc[d] = 0.f;
+        for (int n = 0; ok && more; ++n) {
+            if (!warp_wait(&o_full[n & 1], n >> 1, kErrQ8Mma)) break;
+            tc_fence_after();
+            const Tile t = tile_s[n % kTiles];
+            if (t.flags & kStop) break;
+            const Tile after = tile_s[(n + 1) % kTiles];  // its scores have been issued
+            if (!(after.flags & kStop) && (after.flags & kLast)) load_queries(n + 2);
+            if (!ok) break;
+            const float4 st = stat[n & 3][i];
+            const float Mn = fmaxf(M, st.x), mu = Mn == -INFINITY ? 0.f : Mn;
+            const float alpha = fast_exp2(M - mu), beta = fast_exp2(st.x - mu);
+            M = Mn;
+            L = fmaf(L, alpha, st.y * beta);
+            const float bo = beta * st.z;
+            const uint64_t al = f2_pack(alpha, alpha), be = f2_pack(bo, bo);
+            const uint32_t at = tmem + lanes + C::kColO + (n & 1) * D;
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                float x[32];
+                tmem_ld32(at + c0, x);
+                tmem_wait_ld();
+                if (c0 == D - 32) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_free[n & 1]);
+                }
+#pragma unroll
+                for (int d = 0; d < 32; d += 2)
+                    f2_unpack(f2_fma(f2_pack(x[d], x[d + 1]), be, f2_mul(f2_pack(acc[c0 + d], acc[c0 + d + 1]), al)), acc[c0 + d],
+                              acc[c0 + d + 1]);
+            }
+            if (t.flags & kLast) {
+                const int slot = ((t.flags >> kSlotShift) & 3) - 1, v = t.rb * kM + i;
+                const Q8Req rq = q8_load_req(a, t.b);
+                float inv = L != 0.f ? 1.f / L : 0.f;
+                if (a.tree) pdl_wait();  // the drafted rows' part
+                if (v < rq.T * a.G) {
+                    float* to;
+                    Q8Share share{1.f, -0.f};
+                    if (slot < 0) {
+                        const int64_t row = ((int64_t)rq.row0 + v / a.G) * a.H + (int64_t)t.hk * a.G + v % a.G;
+                        to = a.out + row * D;
+                        if (a.tree) share = q8_share(M, L, __ldcg(g.draft + row));
+                    } else {
+                        to = g.part_o + part_row(slot, i) * D;
+                        g.part_m[part_row(slot, i)] = M;
+                        g.part_l[part_row(slot, i)] = L;
+                    }
+                    inv *= share.own;
+#pragma unroll
+                    for (int d = 0; d < D; d += 4) {
+                        float4 y = make_float4(acc[d] * inv, acc[d + 1] * inv, acc[d + 2] * inv, acc[d + 3] * inv);
+                        if (!q8_nothing(share.draft)) {
+                            const float4 z = __ldcg(reinterpret_cast<const float4*>(to + d));
+                            y = make_float4(fmaf(share.draft, z.x, y.x), fmaf(share.draft, z.y, y.y), fmaf(share.draft, z.z, y.z),
+                                            fmaf(share.draft, z.w, y.w));
+                        }
+                        *reinterpret_cast<float4*>(to + d) = y;
+                    }
+                }
+                __syncwarp();
+                M = -INFINITY;
+                L = 0.f;
+#pragma unroll
+                for (int d = 0; d < D; ++d) acc[d] = 0.f;
+            }
+        }
+    } else if (warp < 16) {
+        // ---- softmax: thread = virtual row, every other tile ------------------------------------
+        const int turn = (warp - 8) >> 2, i = 32 * (warp & 3) + lane;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        int piece = -1, hi = 0, lo = 0, sinks = 0;
+        bool alive = false;
+        for (int n = turn;; n += 2) {
+            if (!warp_wait(&s_full[turn], n >> 1, kErrQ8Mma)) break;
+            const Tile t = tile_s[n % kTiles];
+            if (t.flags & kStop) break;
+            if (t.piece != piece) {
+                piece = t.piece;
+                const Q8Req rq = q8_load_req(a, t.b);
+                const int v = t.rb * kM + i, row = v / a.G;
+                alive = v < rq.T * a.G;
+                int p = a.tree ? rq.len : rq.len - rq.n + row;
+                if (a.tree && a.window > 0 && alive) p = __ldg(a.positions + rq.row0 + row);
+                // Keys of the cache that the row sees: [lo, hi], and those before `sinks`.
+                hi = a.tree ? rq.len - 1 : min(p, rq.len - 1);
+                lo = a.window > 0 ? (int)max((int64_t)p - a.window + 1, (int64_t)0) : 0;
+                sinks = (int)min(a.sinks, (int64_t)rq.len);
+            }
+            tc_fence_after();
+            const bool all = !alive || (hi - t.key >= kKT - 1 && lo <= t.key);
+            const bool whole = __all_sync(FULL, all);
+            RowTile rt;
+            rt.at = tmem + lanes + C::kColS + turn * kKT;
+            rt.ks = k_scale[n % kRing];
+            rt.see = ~0ull;
+            rt.rf = q_back[piece & 3][i];
+            rt.cap = a.cap_log2;
+            if (!all) {
+                auto below = [](int c) -> uint64_t { return c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1; };
+                rt.see = below(hi - t.key + 1) & (~below(lo - t.key) | below(sinks - t.key));
+            }
+            const float mt = whole ? row_max<CAP, true>(rt) : row_max<CAP, false>(rt);
+            const float mu = mt == -INFINITY ? 0.f : mt, back = v_back[n % kRing];
+            float sum, factor = back;
+            if (back == 0.f) {  // rare
+                float lift;
+                sum = far_weights<CAP>(rt, v_scale[n % kRing], mu, &lift);
+                factor = exp2f(lift - (float)kShift);
+            } else {
+                sum = whole ? row_weights<CAP, true>(rt, v_norm[n % kRing], mu) : row_weights<CAP, false>(rt, v_norm[n % kRing], mu);
+            }
+            stat[n & 3][i] = make_float4(mt, sum, factor, 0.f);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[turn]);
+        }
+    } else {
+        // ---- codes to f16 ------------------------------------------------------------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        const int w = warp & 3;
+        for (int n = 0;; ++n) {
+            const int st = n % kStages, sl = n % kSlots, rg = n % kRing;
+            if (!warp_wait(&staged[st], n / kStages, kErrQ8Load)) break;
+            const bool stop = tile_s[n % kTiles].flags & kStop;
+            if (n >= kSlots && !warp_wait(&k_free[sl], n / kSlots - 1, kErrQ8Free)) break;
+            if (stop) {
+                if (lane == 0) mbar_arrive(&k_ready[sl]);
+                break;
+            }
+            if (w == 0) {  // the range of the values' scales
+                const float v0 = v_scale[rg][lane], v1 = v_scale[rg][lane + 32];
+                const uint32_t b0 = __float_as_uint(v0) & 0x7fffffffu, b1 = __float_as_uint(v1) & 0x7fffffffu;
+                const uint32_t most = __reduce_max_sync(FULL, max(b0, b1));
+                const uint32_t least = __reduce_min_sync(FULL, min(b0 ? b0 : ~0u, b1 ? b1 : ~0u));
+                // E, where 2^(kShift - E) and its inverse are normal numbers.
+                int e = (int)(most >> 23) - 127;
+                const bool far = most > least && (most - least > (uint32_t)kFar << 23 || e > 110 || e < -100);
+                e = e < -100 ? -100 : e > 110 ? 110 : e;
+                const float up = __uint_as_float((uint32_t)(127 + kShift - e) << 23);
+                v_norm[rg][lane] = v0 * up;
+                v_norm[rg][lane + 32] = v1 * up;
+                if (lane == 0) v_back[rg] = far || e == 110 ? 0.f : __uint_as_float((uint32_t)(127 - kShift + e) << 23);
+            }
+            convert<D, FORM>(codes + (size_t)2 * st * C::kCodes, ktiles + sl * C::kTile, w, lane);
+            asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&k_ready[sl]);
+            if (n >= kSlots && !warp_wait(&v_free[sl], n / kSlots - 1, kErrQ8Free)) break;
+            convert<D, FORM>(codes + (size_t)(2 * st + 1) * C::kCodes, vtiles + sl * C::kTile, w, lane);
+            asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&v_ready[sl]);
+                mbar_arrive(&unstaged[st]);
+            }
+        }
+    }
+
+    pdl_wait();  // this grid may not be done before the one that it overlaps
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the partials of the unit that CTA blockIdx.x starts, always in the same order: a warp per
+// virtual row.
+template <int D>
+__global__ void __launch_bounds__(256) q8_tc_merge_kernel(const __grid_constant__ TcArgs g) {
+    constexpr int kPer = D / 32;
+    pdl_wait();
+    const PagedDesc& a = g.a;
+    const int4 h = __ldcg(&g.head[2 * blockIdx.x]);
+    const int hk = __ldcg(&g.head[2 * blockIdx.x + 1].x);
+    const int lane = threadIdx.x & 31, i = blockIdx.y * 8 + (threadIdx.x >> 5), v = h.y + i;
+    if (h.x < 0 || v >= h.z) return;
+    const int count = h.x - blockIdx.x + 1;
+    auto row = [&](int k) -> int64_t { return (int64_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * kM + i; };
+    auto load = [&](int k) -> float2 {
+        return k < count ? make_float2(__ldcg(g.part_m + row(k)), __ldcg(g.part_l + row(k))) : make_float2(-INFINITY, 0.f);
+    };
+    const float2 own = load(lane);
+    float m = own.x;
+    for (int k = lane + 32; k < count; k += 32) m = fmaxf(m, __ldcg(g.part_m + row(k)));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, off));
+    // -0 where a piece saw nothing and left no output; +0 counts (0 x inf is NaN).
+    auto weight = [&](float2 p) -> float { return p.y != 0.f ? fast_exp2(p.x - m) * p.y : -0.f; };
+    float den = weight(own);
+    for (int k = lane + 32; k < count; k += 32) den += weight(load(k));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(FULL, den, off);
+    const float inv = den != 0.f ? 1.f / den : 0.f;
+    float acc[kPer];
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
+    for (int k0 = 0; k0 < count; k0 += 32) {
+        const float wgt = weight(k0 == 0 ? own : load(k0 + lane)) * inv;
+        const int here = min(count - k0, 32);
+#pragma unroll 4
+        for (int k = 0; k < here; ++k) {
+            const float f = __shfl_sync(FULL, wgt, k);
+            if (q8_nothing(f)) continue;
+            const float* src = g.part_o + row(k0 + k) * D;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) acc[c] = fmaf(f, __ldcg(src + lane + 32 * c), acc[c]);
+        }
+    }
+    const int t = v / a.G;
+    const int64_t at = ((int64_t)h.w + t) * a.H + (int64_t)hk * a.G + (v - t * a.G);
+    float* out = a.out + at * D;
+    if (a.tree) {
+        const Q8Share w = q8_share(m, den, __ldcg(g.draft + at));
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) {
+            const float z = q8_nothing(w.draft) ? 0.f : __ldcg(out + lane + 32 * c);
+            acc[c] = fmaf(w.own, acc[c], w.draft * z);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) out[lane + 32 * c] = acc[c];
+}
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+struct Scratch {
+    size_t m, l, o, head, draft, total;
+};
+Scratch scratch_of(int D, int64_t draft_rows) {
+    const size_t rows = (size_t)2 * kPagedMaxCtas * kM;
+    Scratch s;
+    s.m = kWorkspaceHeader;
+    s.l = s.m + up256(rows * 4);
+    s.o = s.l + up256(rows * 4);
+    s.head = s.o + up256(rows * D * 4);
+    s.draft = s.head + up256((size_t)2 * kPagedMaxCtas * sizeof(int4));
+    s.total = s.draft + up256((size_t)draft_rows * sizeof(float2));
+    return s;
+}
+
+template <int D, int FORM>
+cudaError_t launch_form(const PagedDesc& a, const Q8Pools& p, int num_sms, void* workspace, cudaStream_t stream) {
+    TcArgs g;
+    std::memset(&g, 0, sizeof(g));
+    g.a = a;
+    g.p = p;
+    g.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (a.page_size == 1 << i) g.page_shift = i;
+    const Scratch s = scratch_of(D, 0);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    g.part_m = reinterpret_cast<float*>(ws + s.m);
+    g.part_l = reinterpret_cast<float*>(ws + s.l);
+    g.part_o = reinterpret_cast<float*>(ws + s.o);
+    g.head = reinterpret_cast<int4*>(ws + s.head);
+    float2* draft = reinterpret_cast<float2*>(ws + s.draft);
+    g.draft = draft;
+    const int ctas = num_sms < kPagedMaxCtas ? num_sms : kPagedMaxCtas;
+    auto kern = a.softcap_on ? q8_tc_kernel<D, FORM, true> : q8_tc_kernel<D, FORM, false>;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), (int)Cfg<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    if (a.tree) {  // the cached part runs beside the drafted one and waits for it at the end
+        e = launch_paged_q8_draft(a, draft, stream);
+        if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(kThreads), Cfg<D>::kSmem, stream, g);
+    } else {
+        kern<<<ctas, kThreads, Cfg<D>::kSmem, stream>>>(g);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return e;
+    const int64_t most = (int64_t)a.max_rows * a.G;
+    return launch_pdl(q8_tc_merge_kernel<D>, dim3((unsigned)ctas, (unsigned)((most < kM ? most : kM) + 7) / 8), dim3(256), 0,
+                      stream, g);
+}
+
+}  // namespace
+
+size_t paged_q8_tc_workspace(const PagedDesc& a) { return scratch_of(a.D, a.tree ? a.rows * a.H : 0).total; }
+
+cudaError_t launch_paged_q8_tc(const PagedDesc& a, const Q8Pools& p, int num_sms, void* workspace, cudaStream_t stream) {
+    if (a.D == 128)
+        return p.form == kFormInt8 ? launch_form<128, kFormInt8>(a, p, num_sms, workspace, stream)
+                                   : launch_form<128, kFormE4m3>(a, p, num_sms, workspace, stream);
+    return p.form == kFormInt8 ? launch_form<64, kFormInt8>(a, p, num_sms, workspace, stream)
+                               : launch_form<64, kFormE4m3>(a, p, num_sms, workspace, stream);
+}
+
+unsigned int paged_q8_tc_take_device_error() {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_q8_tc_device_error, sizeof(v)) != cudaSuccess) return 0;
+    if (v) {
+        const unsigned int zero = 0;
+        cudaMemcpyToSymbol(g_q8_tc_device_error, &zero, sizeof(zero));
+    }
+    return v;
+}
+
+}  // namespace vtmu

@@ -1279,6 +1279,10 @@ vtmu_status vtmu_paged_read_q8(const void* k_pool, const void* v_pool, const flo
     return ok();
 }
 
+static size_t paged_q8_workspace(const vtmu::PagedDesc& a) {
+    return vtmu::paged_q8_few_rows(a) ? vtmu::paged_q8_mma_workspace(a) : vtmu::paged_q8_tc_workspace(a);
+}
+
 vtmu_status vtmu_paged_q8_workspace_size(const vtmu_paged_params* p, size_t* bytes) {
     if (!bytes) return fail(VTMU_ERR_INVALID, "bytes is NULL");
     vtmu::PagedDesc a;
@@ -1288,7 +1292,7 @@ vtmu_status vtmu_paged_q8_workspace_size(const vtmu_paged_params* p, size_t* byt
     const bool tc = p->kernel != VTMU_PAGED_CUDA_CORES && vtmu::paged_q8_mma_supported(a);
     if (!tc && p->kernel == VTMU_PAGED_TENSOR_CORES)
         return fail(VTMU_ERR_UNSUPPORTED, "paged q8: kernel TENSOR_CORES covers headDim 64 and 128 (got headDim %d)", a.D);
-    *bytes = tc ? vtmu::paged_q8_mma_workspace(a) : 0;
+    *bytes = tc ? paged_q8_workspace(a) : 0;
     return ok();
 }
 
@@ -1338,15 +1342,16 @@ vtmu_status vtmu_paged_attention_q8(const float* q, const void* k_pool, const vo
                     "out (got headDim %d)",
                     a.D);
     if (tc) {
-        const size_t need = vtmu::paged_q8_mma_workspace(a);
+        const size_t need = paged_q8_workspace(a);
         if (!workspace || workspace_bytes < need)
             return fail(VTMU_ERR_WORKSPACE, "paged q8 attention needs a workspace of %zu bytes (got %zu)", need,
                         workspace ? workspace_bytes : (size_t)0);
         if (reinterpret_cast<uintptr_t>(workspace) & 255u)
             return fail(VTMU_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     }
-    const cudaError_t e = tc ? vtmu::launch_paged_q8_mma(a, pools, device_sm_count(), workspace, stream)
-                             : vtmu::launch_paged_q8_ffma(a, pools, stream);
+    const cudaError_t e = !tc                          ? vtmu::launch_paged_q8_ffma(a, pools, stream)
+                          : vtmu::paged_q8_few_rows(a) ? vtmu::launch_paged_q8_mma(a, pools, device_sm_count(), workspace, stream)
+                                                       : vtmu::launch_paged_q8_tc(a, pools, device_sm_count(), workspace, stream);
     if (e != cudaSuccess) return cuda_fail(e, "paged q8 attention launch");
     return ok();
 }
@@ -1450,7 +1455,7 @@ vtmu_status vtmu_device_error(unsigned int* flags) {
     *flags = vtmu::decode_take_device_error() | vtmu::decode_tc_take_device_error() | vtmu::tc_take_device_error() |
              vtmu::mla_take_device_error() |
              vtmu::mla_tc_take_device_error() | vtmu::paged_take_device_error() |
-             vtmu::paged_q8_take_device_error();
+             vtmu::paged_q8_take_device_error() | vtmu::paged_q8_tc_take_device_error();
     return ok();
 }
 
