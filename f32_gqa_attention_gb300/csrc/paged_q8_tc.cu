@@ -18,15 +18,19 @@
 // block) units evenly.  A unit cut by a CTA's end leaves partials (m, l, o / l) that
 // q8_tc_merge_kernel joins in a fixed order.
 //
-// Warps, with their share of the 480 registers a lane that five warpgroups launch with:
-//   0, 2    page ids and 16-byte asynchronous copies of K and of V codes and scales
+// Warps, with their share of the 480 registers a lane that six warpgroups launch with:
+//   0, 2    page ids, TMA loads of K and of V codes (a box per page) and copies of scales
 //   1       MMAs: S(n), then O(n - 1); one elected lane issues                      (56)
 //   4 - 7   queries to TMEM, and the fold; a thread is a row, acc in registers     (184)
-//   8 - 15  softmax of even and of odd tiles; a thread is a row                  (2 x 96)
-//   16 - 19 codes to f16 tiles, and the scales' range                               (48)
+//   8 - 15  softmax of even and of odd tiles; a thread is a row                  (2 x 72)
+//   16 - 23 codes to f16 tiles, and the scales' range                           (2 x 48)
 // TMEM: Q hi, lo (D columns), two S / P buffers (128), two O buffers (2 D).
 // Every wait is bounded; one that gives up sets a bit of the device flag.
 #include <cstring>
+#include <mutex>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "attn_common.cuh"
 #include "launch_cache.h"
@@ -44,7 +48,7 @@ __device__ unsigned int g_q8_tc_device_error;
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int kKT = 64, kM = 128, kThreads = 640;
+constexpr int kKT = 64, kM = 128, kThreads = 768, kConverters = 8;
 constexpr int kStages = 4;  // tiles of codes
 constexpr int kSlots = 3;   // tiles of f16, of K and of V
 constexpr int kRing = 8;    // scales of a tile: stage n is loaded once PV(n - 7) is done, so softmax(n - 8) is
@@ -62,6 +66,7 @@ struct TcArgs {
     PagedDesc a;
     Q8Pools p;
     int32_t page_shift;
+    int32_t sub;    // rows of a TMA box: the largest power of two that divides a page, at most 64
     float* part_m;  // [2 CTAs][128]: slot 0 goes on with a unit, slot 1 starts one
     float* part_l;
     float* part_o;  // [2 CTAs][128][D], divided by l
@@ -79,7 +84,7 @@ struct Cfg {
 };
 
 struct Tile {
-    int b, rb, key, flags, hk, piece, pad0, pad1;
+    int b, rb, key, flags, hk, piece, rows, pad;  // rows: of the cache, from key on
 };
 
 // A CTA's place in the list, for the producers.
@@ -140,6 +145,7 @@ struct Walk {
         t.hk = hk;
         t.piece = piece;
         t.key = (u < n_sink ? u : lo_tile + u - n_sink) * kKT;
+        t.rows = max(len - t.key, 0);
         t.flags = (first ? kFirst : 0) | (u + 1 == u1 ? kLast : 0) | (slot + 1) << kSlotShift;
         first = false;
         ++u;
@@ -177,49 +183,55 @@ __device__ __forceinline__ bool elect_one() {
 }
 // mbar_wait, bounded in the same way, that looks at the clock late and seldom: reading the
 // global timer takes as long as a whole hand-over.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
-#pragma unroll 1
-    for (int i = 0; i < 4096; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    do {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-    } while (global_ns() - t0 <= kWaitLimitNs);
-    return false;
-}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase, unsigned int error) {
-    if (__all_sync(FULL, wait_for(bar, (uint32_t)(phase & 1)))) return true;
+    const uint32_t parity = (uint32_t)(phase & 1);
+    uint64_t t0 = 0;
+    bool ok = mbar_try_wait(bar, parity);
+#pragma unroll 1
+    for (int i = 1; !ok; ++i) {
+        ok = mbar_try_wait(bar, parity);
+        if ((i & 1023) == 0 && !ok) {
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) break;
+        }
+    }
+    if (__all_sync(FULL, ok)) return true;
     raise_device_error(&g_q8_tc_device_error, error);
     return false;
 }
 
-// Chunk c (16 bytes) of row `row` of a tile of codes: the converting lanes read 64 bytes of
-// two neighbouring rows at a time.
-template <int D>
-__device__ __forceinline__ int code_chunk(int row, int c) {
-    return D == 128 ? c ^ ((row & 1) << 2) : c;
-}
-
-// Codes of a tile to f16: four warps, 16 rows each, a lane 16 codes at a time.
+// Codes of a tile to f16: eight warps, 8 rows each, a lane 16 codes at a time.  TMA leaves
+// chunk c (16 bytes) of row r at c ^ (r % 8) (headDim 128; 64: where it was).  A quarter of the
+// warp takes 64 bytes of two rows; rows r and r ^ 5 (64: neighbours) meet no bank twice, neither
+// as codes nor in the f16 tile's swizzle.
 template <int D, int FORM>
 __device__ __forceinline__ void convert(const unsigned char* codes, unsigned char* tile, int w, int lane) {
-    const int sub = lane & 7;
+    const int sub = lane & 7, q = lane >> 3;
 #pragma unroll
-    for (int i = 0; i < (D == 128 ? 4 : 2); ++i) {
-        const int row = 16 * w + 8 * (i & 1) + 2 * (lane >> 3) + (sub >> 2), c = (sub & 3) + 4 * (i >> 1);
-        const uint4 x = *reinterpret_cast<const uint4*>(codes + row * D + 16 * code_chunk<D>(row, c));
+    for (int i = 0; i < D / 64; ++i) {
+        const int row = 8 * w + (D == 128 ? q ^ (sub & 4 ? 5 : 0) : 2 * q + (sub >> 2));
+        const int c = (sub & 3) + 4 * i, sw = row & 7;
+        const uint4 x = *reinterpret_cast<const uint4*>(codes + row * D + 16 * (D == 128 ? c ^ sw : c));
         uint32_t h[8];
         q8_halves<FORM>(x.x, h[0], h[1]);
         q8_halves<FORM>(x.y, h[2], h[3]);
         q8_halves<FORM>(x.z, h[4], h[5]);
         q8_halves<FORM>(x.w, h[6], h[7]);
         unsigned char* to = tile + (c >> 2) * 8192 + row * 128;
-        const int j = 2 * (c & 3), sw = row & 7;
+        const int j = 2 * (c & 3);
         *reinterpret_cast<uint4*>(to + 16 * (j ^ sw)) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4*>(to + 16 * ((j + 1) ^ sw)) = make_uint4(h[4], h[5], h[6], h[7]);
     }
+}
+// Rows from `rows` on of a tile of value codes: what a page holds behind a request's last row may
+// be a NaN, which no weight of zero takes away.
+template <int D>
+__device__ __noinline__ void clear_rows(unsigned char* codes, int rows, int w, int lane) {
+    for (int i = 8 * w * D + 16 * lane; i < 8 * (w + 1) * D; i += 512)
+        if (i / D >= rows) *reinterpret_cast<uint4*>(codes + i) = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // before the next tile's copies
+    __syncwarp();
 }
 
 // What a softmax thread needs of its row and tile.
@@ -229,64 +241,63 @@ struct RowTile {
     uint64_t see;      // keys that it sees (not read when WHOLE)
     float rf, cap;     // a score of the MMA times ks rf is one in base-2 units (the argument of tanh with a cap)
 };
-// 32 scores from key 32 c on: in base-2 units with a cap, else still to be multiplied by rf.
+// 16 scores from key k0 on: in base-2 units with a cap, else still to be multiplied by rf.
 template <bool CAP, bool WHOLE>
-__device__ __forceinline__ void row_scores(const RowTile& r, int c, float (&x)[32]) {
-    tmem_ld32(r.at + 32 * c, x);
+__device__ __forceinline__ void row_scores(const RowTile& r, int k0, float (&x)[16]) {
+    tmem_ld16(r.at + k0, x);
     tmem_wait_ld();
 #pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-        const float4 s = *reinterpret_cast<const float4*>(r.ks + 32 * c + k);
+    for (int k = 0; k < 16; k += 4) {
+        const float4 s = *reinterpret_cast<const float4*>(r.ks + k0 + k);
         f2_unpack(f2_mul(f2_pack(x[k], x[k + 1]), f2_pack(s.x, s.y)), x[k], x[k + 1]);
         f2_unpack(f2_mul(f2_pack(x[k + 2], x[k + 3]), f2_pack(s.z, s.w)), x[k + 2], x[k + 3]);
     }
-    if constexpr (CAP) softcap_tile<32>(x, r.rf, r.cap);
+    if constexpr (CAP) softcap_tile<16>(x, r.rf, r.cap);
     if constexpr (!WHOLE) {
-        const uint32_t bits = (uint32_t)(r.see >> (32 * c));
+        const uint32_t bits = (uint32_t)(r.see >> k0);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = (bits >> k) & 1u ? x[k] : -INFINITY;
+        for (int k = 0; k < 16; ++k) x[k] = (bits >> k) & 1u ? x[k] : -INFINITY;
     }
 }
-template <bool CAP, bool WHOLE>
-__device__ __forceinline__ float row_max(const RowTile& r) {
-    float mt = -INFINITY;
-#pragma unroll 1
-    for (int c = 0; c < 2; ++c) {
-        float x[32];
-        row_scores<CAP, WHOLE>(r, c, x);
+// 16 weights as f16 hi (8 columns) and lo (8).
+__device__ __forceinline__ void store_weights(uint32_t at, const float* w) {
+    float y[16];
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) mt = fmaxf(fmaxf(mt, x[k]), x[k + 1]);
-    }
-    return CAP ? mt : mt * r.rf;
-}
-// 32 weights as f16 hi (16 columns) and lo (16) over their scores.
-__device__ __forceinline__ void store_weights(uint32_t at, const float (&w)[32]) {
-    float hi[16], lo[16];
-#pragma unroll
-    for (int k = 0; k < 32; k += 2) {
+    for (int k = 0; k < 16; k += 2) {
         uint32_t h, l;
         mma_split(w[k], w[k + 1], h, l);
-        hi[k / 2] = __uint_as_float(h);
-        lo[k / 2] = __uint_as_float(l);
+        y[k / 2] = __uint_as_float(h);
+        y[8 + k / 2] = __uint_as_float(l);
     }
-    tmem_st16(at, hi);
-    tmem_st16(at + 16, lo);
+    tmem_st16(at, y);
 }
-// Weights 2^(x2 - mu) vn over the scores; returns the sum of the exponentials.  vn: the values'
-// scales times 2^(kShift - E).
+// The row's largest score m, and weights 2^(x2 - m) vn over its scores (vn: the values' scales
+// times 2^(kShift - E)); returns m and the sum of the exponentials.
+// Short loops on purpose: the roles' code has to stay in the instruction cache together (with
+// this one unrolled over all 64 scores large trees took 695 us instead of 613).
 template <bool CAP, bool WHOLE>
-__device__ __forceinline__ float row_weights(const RowTile& r, const float* vn, float mu) {
+__device__ __forceinline__ float2 row_softmax(const RowTile& r, const float* vn) {
+    float m = -INFINITY;
+#pragma unroll 1
+    for (int k0 = 0; k0 < kKT; k0 += 16) {
+        float x[16];
+        row_scores<CAP, WHOLE>(r, k0, x);
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) m = fmaxf(fmaxf(m, x[k]), x[k + 1]);
+    }
     const float mul = CAP ? 1.f : r.rf;
+    m *= mul;
+    const float mu = m == -INFINITY ? 0.f : m;
     const uint64_t mul2 = f2_pack(mul, mul), sub2 = f2_pack(-mu, -mu);
     uint64_t sum = 0;
 #pragma unroll 1
-    for (int c = 0; c < 2; ++c) {
-        float x[32];
-        row_scores<CAP, WHOLE>(r, c, x);
-        const uint32_t bits = (uint32_t)(r.see >> (32 * c));
+    for (int k0 = 0; k0 < kKT; k0 += 16) {
+        float x[16];
+        row_scores<CAP, WHOLE>(r, k0, x);
+        const uint32_t bits = (uint32_t)(r.see >> k0);
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(vn + 32 * c + k);
+        for (int k = 0; k < 16; k += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(vn + k0 + k);
             const float vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int j = 0; j < 4; j += 2) {
@@ -301,49 +312,59 @@ __device__ __forceinline__ float row_weights(const RowTile& r, const float* vn, 
                 }
             }
         }
-        store_weights(r.at + 32 * c, x);
+        store_weights(r.at + k0, x);
     }
     float a, b;
     f2_unpack(sum, a, b);
-    return a + b;
+    return make_float2(m, a + b);
 }
 // The same with scales of very different size: relative to the row's largest product
 // 2^(x2 - mu) 2^e, e the scales' exponents.  Returns the sum, and that product's exponent.
 template <bool CAP>
-__device__ __noinline__ float far_weights(const RowTile& r, const float* vs, float mu, float* lift) {
+__device__ __noinline__ float4 far_softmax(const RowTile r, const float* vs) {  // m, sum, exponent
     auto power = [](float v) -> float { return (float)((int)((__float_as_uint(v) >> 23) & 255u) - 127); };
     const float mul = CAP ? 1.f : r.rf;
-    float top = -300.f;
-#pragma unroll 1
-    for (int c = 0; c < 2; ++c) {
-        float x[32];
-        row_scores<CAP, false>(r, c, x);
+    auto score = [&](int k) -> float {  // one at a time: code this rare stays short
+        float x[16];
+        tmem_ld16(r.at + (k & ~15), x);
+        tmem_wait_ld();
+        float y = x[0];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) top = fmaxf(top, fmaf(x[k], mul, -mu) + power(vs[32 * c + k]));
-    }
+        for (int i = 1; i < 16; ++i) y = (k & 15) == i ? x[i] : y;
+        y *= r.ks[k];
+        if (CAP) y = r.cap * softcap_tanh(y * r.rf);
+        return (r.see >> k) & 1u ? y * mul : -INFINITY;
+    };
+    float m = -INFINITY, top = -300.f, sum = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < kKT; ++k) m = fmaxf(m, score(k));
+    const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+    for (int k = 0; k < kKT; ++k) top = fmaxf(top, (score(k) - mu) + power(vs[k]));
     top = ceilf(fminf(top, 126.f));
-    *lift = top;
-    float sum = 0.f;
 #pragma unroll 1
-    for (int c = 0; c < 2; ++c) {
-        float x[32];
-        row_scores<CAP, false>(r, c, x);
-        const uint32_t bits = (uint32_t)(r.see >> (32 * c));
+    for (int c = 0; c < kKT; c += 16) {
+        float w[16];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-            const float v = vs[32 * c + k], e = power(v), y = fmaf(x[k], mul, -mu);
+        for (int i = 0; i < 16; ++i) w[i] = 0.f;
+#pragma unroll 1
+        for (int k = c; k < c + 16; ++k) {
+            const float v = vs[k], e = power(v), y = score(k) - mu;
             const float part = v * (e > 0.f ? exp2f(-e) : exp2f(-e - 1.f) * 2.f);  // the scale's mantissa; 0 stays 0
             sum += fast_exp2(y);
-            const float w = fast_exp2(y + (e - top)) * part * (float)(1 << kShift);
-            x[k] = (bits >> k) & 1u ? w : 0.f;
+            const float u = (r.see >> k) & 1u ? fast_exp2(y + (e - top)) * part * (float)(1 << kShift) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = (k & 15) == i ? u : w[i];
         }
-        store_weights(r.at + 32 * c, x);
+        store_weights(r.at + c, w);
     }
-    return sum;
+    return make_float4(m, sum, top, 0.f);
 }
 
 template <int D, int FORM, bool CAP>
-__global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constant__ TcArgs g) {
+__global__ void __launch_bounds__(kThreads, 1) 
+    q8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ TcArgs g) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -367,12 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&staged[i], 2 * 32 + 1);  // two warps' copies, and what the tile is
-            mbar_init(&unstaged[i], 4);
+            mbar_init(&staged[i], 2 * 33 + 1);  // two warps' bytes and scales, and what the tile is
+            mbar_init(&unstaged[i], kConverters);
         }
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&k_ready[i], 4);
-            mbar_init(&v_ready[i], 4);
+            mbar_init(&k_ready[i], kConverters);
+            mbar_init(&v_ready[i], kConverters);
             mbar_init(&k_free[i], 1);
             mbar_init(&v_free[i], 1);
         }
@@ -452,13 +473,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
                                               (g.page_shift >= 0 ? key >> g.page_shift : key / a.page_size));
                 }
             };
-            look();
-            for (int n = 0;; ++n) {
+            for (int n = -1;; ++n) {
                 t = ahead;
                 page[0] = page_ahead[0];
                 page[1] = page_ahead[1];
-                const bool stop = t.flags & kStop;
+                const bool stop = n >= 0 && (t.flags & kStop);
                 if (!stop) look();
+                if (n < 0) continue;
                 const int st = n % kStages;
                 if (n >= kStages && !warp_wait(&unstaged[st], n / kStages - 1, kErrQ8Free)) break;
                 if (!values && lane == 0) {
@@ -466,27 +487,23 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
                     if (stop) tile_s[(n + 1) % kTiles] = t;  // for the other softmax warps
                     mbar_arrive(&staged[st]);
                 }
+                if (lane == 0) mbar_arrive_expect_tx(&staged[st], stop ? 0u : C::kCodes);
+                __syncwarp();
                 if (!stop) {
                     unsigned char* to = codes + (size_t)(2 * st + (values ? 1 : 0)) * C::kCodes;
-                    int row[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int key = t.key + lane + 32 * j;
-                        row[j] = (unsigned)page[j] < (unsigned)a.pages
-                                     ? page[j] * a.page_size +
-                                           (g.page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size)
-                                     : -1;
-                        const int64_t at = (int64_t)max(row[j], 0) * a.Hk + t.hk;
-                        cp_async4((values ? v_scale : k_scale)[n % kRing] + lane + 32 * j, scales + at, row[j] >= 0 ? 4 : 0);
-                    }
-                    constexpr int kLanes = D / 16, kRows = 32 / kLanes;
-                    const int64_t pitch = (int64_t)a.Hk * D;
-                    const uint8_t* src = pool + (int64_t)t.hk * D + 16 * (lane % kLanes);
-#pragma unroll
-                    for (int i = 0; i < kKT / kRows; ++i) {
-                        const int r = i * kRows + lane / kLanes;
-                        const int from = __shfl_sync(FULL, row[i * kRows / 32], r & 31);
-                        cp_async16(to + r * D + 16 * code_chunk<D>(r, lane % kLanes), src + max(from, 0) * pitch, from >= 0 ? 16 : 0);
+                        const int r = lane + 32 * j, key = t.key + r;
+                        const int row = (unsigned)page[j] < (unsigned)a.pages
+                                            ? page[j] * a.page_size +
+                                                  (g.page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size)
+                                            : -1;
+                        // A box a page (or the tile's part of one); rows of no page are out of bounds: zeros.
+                        if ((r & (g.sub - 1)) == 0)
+                            tma_load_2d(to + r * D, values ? &tm_v : &tm_k, t.hk * D, row < 0 ? (int)(a.pages * a.page_size) : row,
+                                        &staged[st]);
+                        const int64_t at = (int64_t)max(row, 0) * a.Hk + t.hk;
+                        cp_async4((values ? v_scale : k_scale)[n % kRing] + r, scales + at, row >= 0 ? 4 : 0);
                     }
                 }
                 cp_async_arrive(&staged[st]);
@@ -510,12 +527,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
                 const uint32_t d = tmem + C::kColO + bf * D, p = tmem + C::kColS + bf * kKT;
                 const uint64_t v = v0 + st * (C::kTile >> 4);
                 if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < kKT / 16; ++k)
-                        mma_f16_ts(d, p + 32 * (k >> 1) + 8 * (k & 1) + 16, v + (2048 >> 4) * k, id_o, k > 0 ? 1u : 0u);
-#pragma unroll
+                        mma_f16_ts(d, p + 16 * k + 8, v + (2048 >> 4) * k, id_o, k > 0 ? 1u : 0u);
+#pragma unroll 1
                     for (int k = 0; k < kKT / 16; ++k)
-                        mma_f16_ts(d, p + 32 * (k >> 1) + 8 * (k & 1), v + (2048 >> 4) * k, id_o, 1u);
+                        mma_f16_ts(d, p + 16 * k, v + (2048 >> 4) * k, id_o, 1u);
                     mma_commit(&v_free[st]);
                     mma_commit(&o_full[bf]);
                 }
@@ -526,9 +543,25 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
                 const int st = n % kSlots;
                 if (!warp_wait(&k_ready[st], n / kSlots, kErrQ8Mma)) break;
                 const int flags = tile_s[n % kTiles].flags;
+                if (!(flags & kStop)) {
+                    if ((flags & kFirst) && !warp_wait(&q_full, tile_s[n % kTiles].piece, kErrQ8Mma)) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + C::kColS + (n & 1) * kKT;
+                    const uint64_t k = k0 + st * (C::kTile >> 4);
+                    if (elect_one()) {
+                        auto off = [](int i) -> uint64_t { return (uint64_t)(i >> 2) * (8192 >> 4) + 2 * (i & 3); };
+#pragma unroll 2
+                        for (int i = 0; i < D / 16; ++i) mma_f16_ts(d, tmem + C::kColQlo + 8 * i, k + off(i), id_s, i > 0 ? 1u : 0u);
+#pragma unroll 2
+                        for (int i = 0; i < D / 16; ++i) mma_f16_ts(d, tmem + C::kColQhi + 8 * i, k + off(i), id_s, 1u);
+                        mma_commit(&k_free[st]);
+                        mma_commit(&s_full[n & 1]);
+                    }
+                    __syncwarp();
+                }
+                if (n > 0 && !pv(n - 1)) break;
                 if (flags & kStop) {
                     // The others learn of it in turn, once they have taken their last tiles.
-                    if (n > 0 && !pv(n - 1)) break;
                     if (n >= 2 && !warp_wait(&o_free[n & 1], (n >> 1) - 1, kErrQ8Mma)) break;
                     if (lane == 0) {
                         mbar_arrive(&s_full[n & 1]);
@@ -537,21 +570,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
                     }
                     break;
                 }
-                if ((flags & kFirst) && !warp_wait(&q_full, tile_s[n % kTiles].piece, kErrQ8Mma)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + C::kColS + (n & 1) * kKT;
-                const uint64_t k = k0 + st * (C::kTile >> 4);
-                if (elect_one()) {
-                    auto off = [](int i) -> uint64_t { return (uint64_t)(i >> 2) * (8192 >> 4) + 2 * (i & 3); };
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) mma_f16_ts(d, tmem + C::kColQlo + 8 * i, k + off(i), id_s, i > 0 ? 1u : 0u);
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) mma_f16_ts(d, tmem + C::kColQhi + 8 * i, k + off(i), id_s, 1u);
-                    mma_commit(&k_free[st]);
-                    mma_commit(&s_full[n & 1]);
-                }
-                __syncwarp();
-                if (n > 0 && !pv(n - 1)) break;
             }
         }
     } else if (warp < 8) {
@@ -632,21 +650,26 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
             M = Mn;
             L = fmaf(L, alpha, st.y * beta);
             const float bo = beta * st.z;
-            const uint64_t al = f2_pack(alpha, alpha), be = f2_pack(bo, bo);
+            if (__any_sync(FULL, alpha != 1.f)) {  // a maximum moved
+                const uint64_t al = f2_pack(alpha, alpha);
+#pragma unroll
+                for (int d = 0; d < D; d += 2) f2_unpack(f2_mul(f2_pack(acc[d], acc[d + 1]), al), acc[d], acc[d + 1]);
+            }
+            const uint64_t be = f2_pack(bo, bo);
             const uint32_t at = tmem + lanes + C::kColO + (n & 1) * D;
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 32) {
-                float x[32];
-                tmem_ld32(at + c0, x);
+            for (int c0 = 0; c0 < D; c0 += 16) {
+                float x[16];
+                tmem_ld16(at + c0, x);
                 tmem_wait_ld();
-                if (c0 == D - 32) {
+                if (c0 == D - 16) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&o_free[n & 1]);
                 }
 #pragma unroll
-                for (int d = 0; d < 32; d += 2)
-                    f2_unpack(f2_fma(f2_pack(x[d], x[d + 1]), be, f2_mul(f2_pack(acc[c0 + d], acc[c0 + d + 1]), al)), acc[c0 + d],
+                for (int d = 0; d < 16; d += 2)
+                    f2_unpack(f2_fma(f2_pack(x[d], x[d + 1]), be, f2_pack(acc[c0 + d], acc[c0 + d + 1])), acc[c0 + d],
                               acc[c0 + d + 1]);
             }
             if (t.flags & kLast) {
@@ -687,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
         }
     } else if (warp < 16) {
         // ---- softmax: thread = virtual row, every other tile ------------------------------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int turn = (warp - 8) >> 2, i = 32 * (warp & 3) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         int piece = -1, hi = 0, lo = 0, sinks = 0;
@@ -720,17 +744,16 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
                 auto below = [](int c) -> uint64_t { return c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1; };
                 rt.see = below(hi - t.key + 1) & (~below(lo - t.key) | below(sinks - t.key));
             }
-            const float mt = whole ? row_max<CAP, true>(rt) : row_max<CAP, false>(rt);
-            const float mu = mt == -INFINITY ? 0.f : mt, back = v_back[n % kRing];
-            float sum, factor = back;
+            const float back = v_back[n % kRing];
+            float4 st;
             if (back == 0.f) {  // rare
-                float lift;
-                sum = far_weights<CAP>(rt, v_scale[n % kRing], mu, &lift);
-                factor = exp2f(lift - (float)kShift);
+                st = far_softmax<CAP>(rt, v_scale[n % kRing]);
+                st.z = exp2f(st.z - (float)kShift);
             } else {
-                sum = whole ? row_weights<CAP, true>(rt, v_norm[n % kRing], mu) : row_weights<CAP, false>(rt, v_norm[n % kRing], mu);
+                const float2 ml = whole ? row_softmax<CAP, true>(rt, v_norm[n % kRing]) : row_softmax<CAP, false>(rt, v_norm[n % kRing]);
+                st = make_float4(ml.x, ml.y, back, 0.f);
             }
-            stat[n & 3][i] = make_float4(mt, sum, factor, 0.f);
+            stat[n & 3][i] = st;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -739,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
     } else {
         // ---- codes to f16 ------------------------------------------------------------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        const int w = warp & 3;
+        const int w = warp - 16;
         for (int n = 0;; ++n) {
             const int st = n % kStages, sl = n % kSlots, rg = n % kRing;
             if (!warp_wait(&staged[st], n / kStages, kErrQ8Load)) break;
@@ -763,18 +786,21 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
                 v_norm[rg][lane + 32] = v1 * up;
                 if (lane == 0) v_back[rg] = far || e == 110 ? 0.f : __uint_as_float((uint32_t)(127 - kShift + e) << 23);
             }
-            convert<D, FORM>(codes + (size_t)2 * st * C::kCodes, ktiles + sl * C::kTile, w, lane);
-            asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&k_ready[sl]);
-            if (n >= kSlots && !warp_wait(&v_free[sl], n / kSlots - 1, kErrQ8Free)) break;
-            convert<D, FORM>(codes + (size_t)(2 * st + 1) * C::kCodes, vtiles + sl * C::kTile, w, lane);
-            asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&v_ready[sl]);
-                mbar_arrive(&unstaged[st]);
+            // Short loops on purpose, K and V through the same code: six warps with code of their own share
+            // a scheduler, and unrolled roles ran at the rate of instruction fetches.
+            bool ok = true;
+#pragma unroll 1
+            for (int kv = 0; kv < 2 && ok; ++kv) {
+                if (kv) ok = n < kSlots || warp_wait(&v_free[sl], n / kSlots - 1, kErrQ8Free);
+                if (FORM == kFormE4m3 && kv && tile_s[n % kTiles].rows < kKT)
+                    clear_rows<D>(codes + (size_t)(2 * st + 1) * C::kCodes, tile_s[n % kTiles].rows, w, lane);
+                convert<D, FORM>(codes + (size_t)(2 * st + kv) * C::kCodes, (kv ? vtiles : ktiles) + sl * C::kTile, w, lane);
+                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
+                __syncwarp();
+                if (lane == 0) mbar_arrive(kv ? &v_ready[sl] : &k_ready[sl]);
             }
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(&unstaged[st]);
         }
     }
 
@@ -846,6 +872,33 @@ __global__ void __launch_bounds__(256) q8_tc_merge_kernel(const __grid_constant_
     for (int c = 0; c < kPer; ++c) out[lane + 32 * c] = acc[c];
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 q8_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+// Boxes of `sub` rows of one head out of row-major codes [rows, cols].
+template <int D>
+bool encode_rows(CUtensorMap* map, const uint8_t* p, int64_t rows, int64_t cols, int sub) {
+    return cached_tensor_map(map, p, rows, cols, D, sub, 8, [&](CUtensorMap* m) {
+        auto fn = q8_encoder();
+        if (!fn) return false;
+        const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)cols};
+        const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)sub}, ones[2] = {1, 1};
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    });
+}
+
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 struct Scratch {
@@ -880,15 +933,21 @@ cudaError_t launch_form(const PagedDesc& a, const Q8Pools& p, int num_sms, void*
     g.head = reinterpret_cast<int4*>(ws + s.head);
     float2* draft = reinterpret_cast<float2*>(ws + s.draft);
     g.draft = draft;
+    g.sub = 1;
+    while (g.sub < kKT && a.page_size % (2 * g.sub) == 0) g.sub *= 2;
+    CUtensorMap tk, tv;
+    if (!encode_rows<D>(&tk, p.k, a.pages * a.page_size, (int64_t)a.Hk * D, g.sub) ||
+        !encode_rows<D>(&tv, p.v, a.pages * a.page_size, (int64_t)a.Hk * D, g.sub))
+        return cudaErrorInvalidValue;
     const int ctas = num_sms < kPagedMaxCtas ? num_sms : kPagedMaxCtas;
     auto kern = a.softcap_on ? q8_tc_kernel<D, FORM, true> : q8_tc_kernel<D, FORM, false>;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), (int)Cfg<D>::kSmem);
     if (e != cudaSuccess) return e;
     if (a.tree) {  // the cached part runs beside the drafted one and waits for it at the end
         e = launch_paged_q8_draft(a, draft, stream);
-        if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(kThreads), Cfg<D>::kSmem, stream, g);
+        if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(kThreads), Cfg<D>::kSmem, stream, tk, tv, g);
     } else {
-        kern<<<ctas, kThreads, Cfg<D>::kSmem, stream>>>(g);
+        kern<<<ctas, kThreads, Cfg<D>::kSmem, stream>>>(tk, tv, g);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
