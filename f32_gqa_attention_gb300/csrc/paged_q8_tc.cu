@@ -66,7 +66,7 @@ struct TcArgs {
     PagedDesc a;
     Q8Pools p;
     int32_t page_shift;
-    int32_t sub;    // rows of a TMA box: the largest power of two that divides a page, at most 64
+    int32_t sub_shift;  // log2 of the rows of a TMA box: the largest power of two that divides a page, at most 64
     float* part_m;  // [2 CTAs][128]: slot 0 goes on with a unit, slot 1 starts one
     float* part_l;
     float* part_o;  // [2 CTAs][128][D], divided by l
@@ -456,30 +456,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             const uint8_t* pool = values ? g.p.v : g.p.k;
             const float* scales = values ? g.p.v_scale : g.p.k_scale;
-            // Lane i looks up rows i and i + 32, a tile ahead of its copies.
-            Tile t, ahead;
-            int page[2], page_ahead[2];
-            auto look = [&]() {
-                if (!walk.next(a, prefix, ahead, empty)) {
-                    ahead.flags = kStop;
-                    ahead.key = 0;
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    page_ahead[j] = -1;
-                    const int key = ahead.key + lane + 32 * j;
-                    if (!(ahead.flags & kStop) && key < walk.len)
-                        page_ahead[j] = __ldg(a.block_table + (int64_t)ahead.b * a.max_pages +
-                                              (g.page_shift >= 0 ? key >> g.page_shift : key / a.page_size));
-                }
-            };
-            for (int n = -1;; ++n) {
-                t = ahead;
-                page[0] = page_ahead[0];
-                page[1] = page_ahead[1];
-                const bool stop = n >= 0 && (t.flags & kStop);
-                if (!stop) look();
-                if (n < 0) continue;
+            // 32 boxes of a request are looked up at a time, a lane each: the first row of each in the
+            // pool, -1 for rows of no page.
+            int y_cur = -1, batch = -1, of_piece = -1;
+            for (int n = 0;; ++n) {
+                Tile t;
+                const bool stop = !walk.next(a, prefix, t, empty);
+                if (stop) t.flags = kStop;
                 const int st = n % kStages;
                 if (n >= kStages && !warp_wait(&unstaged[st], n / kStages - 1, kErrQ8Free)) break;
                 if (!values && lane == 0) {
@@ -490,20 +473,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive_expect_tx(&staged[st], stop ? 0u : C::kCodes);
                 __syncwarp();
                 if (!stop) {
+                    if (t.piece != of_piece) batch = -1;
+                    of_piece = t.piece;
                     unsigned char* to = codes + (size_t)(2 * st + (values ? 1 : 0)) * C::kCodes;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int r = lane + 32 * j, key = t.key + r;
-                        const int row = (unsigned)page[j] < (unsigned)a.pages
-                                            ? page[j] * a.page_size +
-                                                  (g.page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size)
-                                            : -1;
-                        // A box a page (or the tile's part of one); rows of no page are out of bounds: zeros.
-                        if ((r & (g.sub - 1)) == 0)
-                            tma_load_2d(to + r * D, values ? &tm_v : &tm_k, t.hk * D, row < 0 ? (int)(a.pages * a.page_size) : row,
+                        const int q0 = (t.key + 32 * j) >> g.sub_shift;  // the half's first box
+                        if ((q0 >> 5) != batch) {
+                            batch = q0 >> 5;
+                            const int row = ((batch << 5) + lane) << g.sub_shift;
+                            y_cur = -1;
+                            if (row < walk.len) {
+                                const int col = g.page_shift >= 0 ? row >> g.page_shift : row / a.page_size;
+                                const int page = __ldg(a.block_table + (int64_t)t.b * a.max_pages + col);
+                                if ((unsigned)page < (unsigned)a.pages) y_cur = page * a.page_size + (row - col * a.page_size);
+                            }
+                        }
+                        const int r = lane + 32 * j, key = t.key + r, in = key & ((1 << g.sub_shift) - 1);
+                        const int y = __shfl_sync(FULL, y_cur, (key >> g.sub_shift) & 31);
+                        // Rows of no page are out of bounds: zeros.
+                        if (in == 0)
+                            tma_load_2d(to + r * D, values ? &tm_v : &tm_k, t.hk * D, y < 0 ? (int)(a.pages * a.page_size) : y,
                                         &staged[st]);
-                        const int64_t at = (int64_t)max(row, 0) * a.Hk + t.hk;
-                        cp_async4((values ? v_scale : k_scale)[n % kRing] + r, scales + at, row >= 0 ? 4 : 0);
+                        const bool there = y >= 0 && key < walk.len;
+                        const int64_t at = (int64_t)(there ? y + in : 0) * a.Hk + t.hk;
+                        cp_async4((values ? v_scale : k_scale)[n % kRing] + r, scales + at, there ? 4 : 0);
                     }
                 }
                 cp_async_arrive(&staged[st]);
@@ -933,11 +927,11 @@ cudaError_t launch_form(const PagedDesc& a, const Q8Pools& p, int num_sms, void*
     g.head = reinterpret_cast<int4*>(ws + s.head);
     float2* draft = reinterpret_cast<float2*>(ws + s.draft);
     g.draft = draft;
-    g.sub = 1;
-    while (g.sub < kKT && a.page_size % (2 * g.sub) == 0) g.sub *= 2;
+    while ((1 << g.sub_shift) < kKT && a.page_size % (2 << g.sub_shift) == 0) ++g.sub_shift;
+    const int sub = 1 << g.sub_shift;
     CUtensorMap tk, tv;
-    if (!encode_rows<D>(&tk, p.k, a.pages * a.page_size, (int64_t)a.Hk * D, g.sub) ||
-        !encode_rows<D>(&tv, p.v, a.pages * a.page_size, (int64_t)a.Hk * D, g.sub))
+    if (!encode_rows<D>(&tk, p.k, a.pages * a.page_size, (int64_t)a.Hk * D, sub) ||
+        !encode_rows<D>(&tv, p.v, a.pages * a.page_size, (int64_t)a.Hk * D, sub))
         return cudaErrorInvalidValue;
     const int ctas = num_sms < kPagedMaxCtas ? num_sms : kPagedMaxCtas;
     auto kern = a.softcap_on ? q8_tc_kernel<D, FORM, true> : q8_tc_kernel<D, FORM, false>;
