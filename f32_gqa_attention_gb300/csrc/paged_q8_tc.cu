@@ -24,7 +24,7 @@
 //   4 - 7   queries to TMEM, and the fold; a thread is a row, acc in registers     (184)
 //   8 - 15  softmax of even and of odd tiles; a thread is a row                  (2 x 72)
 //   16 - 23 codes to f16 tiles, and the scales' range                           (2 x 48)
-// TMEM: Q hi, lo (D columns), two S / P buffers (128), two O buffers (2 D).
+// TMEM: Q hi, lo (D columns), four S / P buffers (256), O (D).
 // Every wait is bounded; one that gives up sets a bit of the device flag.
 #include <cstring>
 #include <mutex>
@@ -50,8 +50,9 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kKT = 64, kM = 128, kThreads = 768, kConverters = 8;
 constexpr int kStages = 4;  // tiles of codes
-constexpr int kSlots = 3;   // tiles of f16, of K and of V
-constexpr int kRing = 8;    // scales of a tile: stage n is loaded once PV(n - 7) is done, so softmax(n - 8) is
+constexpr int kSlotsK = 3, kSlotsV = 4;  // tiles of f16
+constexpr int kScores = 4;  // S / P buffers: with two, S(n + 2) waited for P V(n), and a softmax warpgroup for it
+constexpr int kRing = 8;    // scales of a tile: stage n is loaded once V(n - 4) is converted, and so PV(n - 8) done
 constexpr int kTiles = 16;  // what it is: the fold of a tile that far back may not have begun
 constexpr int kShift = 14;  // of weights in f16
 constexpr int kFar = 6;     // log2 by which a tile's scales may differ on the short way
@@ -77,10 +78,10 @@ struct TcArgs {
 template <int D>
 struct Cfg {
     static constexpr uint32_t kCodes = kKT * D, kTile = 2 * kCodes;  // bytes of a tile, as codes and as f16
-    static constexpr size_t kSmem = 1024 + 2 * kSlots * kTile + kStages * 2 * kCodes + (kPagedMaxRequests + 1) * 8;
-    static constexpr uint32_t kColQhi = 0, kColQlo = D / 2, kColS = D, kColO = D + 2 * kKT;
-    static_assert(kColO + 2 * D <= 512, "TMEM budget");
-    static_assert(kSmem + 16 * 1024 <= 232448, "shared memory budget");
+    static constexpr size_t kSmem = 1024 + (kSlotsK + kSlotsV) * kTile + kStages * 2 * kCodes + (kPagedMaxRequests + 1) * 8;
+    static constexpr uint32_t kColQhi = 0, kColQlo = D / 2, kColS = D, kColO = D + kScores * kKT;
+    static_assert(kColO + D <= 512, "TMEM budget");
+    static_assert(kSmem + 24 * 1024 <= 232448, "shared memory budget");
 };
 
 struct Tile {
@@ -168,12 +169,13 @@ __device__ __forceinline__ uint64_t smem_desc(const void* tile, uint32_t next) {
     d |= (uint64_t)2 << 61;
     return d;
 }
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// The descriptor in its words: the upper one is the same for every tile.
+template <bool ACC>
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred p;\n .reg .b64 b;\n mov.b64 b, {%2, %3};\n setp.ne.b32 p, %5, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC ? 1 : 0)
         : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
@@ -183,6 +185,16 @@ __device__ __forceinline__ bool elect_one() {
 }
 // mbar_wait, bounded in the same way, that looks at the clock late and seldom: reading the
 // global timer takes as long as a whole hand-over.
+// Whether the phase is over, without a wait.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase, unsigned int error) {
     const uint32_t parity = (uint32_t)(phase & 1);
     uint64_t t0 = 0;
@@ -369,18 +381,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* ktiles = tiles;
-    unsigned char* vtiles = tiles + kSlots * C::kTile;
-    unsigned char* codes = tiles + 2 * kSlots * C::kTile;  // stage: K, V
+    unsigned char* vtiles = tiles + kSlotsK * C::kTile;
+    unsigned char* codes = vtiles + kSlotsV * C::kTile;  // stage: K, V
     long long* prefix = reinterpret_cast<long long*>(codes + (size_t)kStages * 2 * C::kCodes);
-    __shared__ __align__(8) uint64_t staged[kStages], unstaged[kStages], k_ready[kSlots], k_free[kSlots], v_ready[kSlots],
-        v_free[kSlots], q_full, s_full[2], p_full[2], o_full[2], o_free[2];
+    __shared__ __align__(8) uint64_t staged[kStages], unstaged[kStages], k_ready[kSlotsK], k_free[kSlotsK],
+        v_ready[kSlotsV], v_free[kSlotsV], q_full, q_free, s_full[kScores], p_full[kScores], o_full, o_free;
     __shared__ uint32_t tmem_base_s;
     __shared__ long long scan_s[kThreads / 32];
     __shared__ __align__(16) float k_scale[kRing][kKT], v_scale[kRing][kKT], v_norm[kRing][kKT];
     __shared__ float v_back[kRing];              // 2^(E - kShift); 0: the scales differ too much
     __shared__ __align__(16) Tile tile_s[kTiles];
     __shared__ float q_back[4][kM];              // by piece: what the queries' power of two takes back
-    __shared__ __align__(16) float4 stat[4][kM]; // by tile: m, l, factor of its output
+    __shared__ float2 stat[kRing][kM];           // by tile: m, l
+    __shared__ float stat_back[kRing][kM];       // factor of its output
+    __shared__ int piece_end[4];                 // by piece: the tile after it
 
     const PagedDesc& a = g.a;
     const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -391,18 +405,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&staged[i], 2 * 33 + 1);  // two warps' bytes and scales, and what the tile is
             mbar_init(&unstaged[i], kConverters);
         }
-        for (int i = 0; i < kSlots; ++i) {
+        for (int i = 0; i < kSlotsK; ++i) {
             mbar_init(&k_ready[i], kConverters);
-            mbar_init(&v_ready[i], kConverters);
             mbar_init(&k_free[i], 1);
+        }
+        for (int i = 0; i < kSlotsV; ++i) {
+            mbar_init(&v_ready[i], kConverters);
             mbar_init(&v_free[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kScores; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
-            mbar_init(&o_full[i], 1);
-            mbar_init(&o_free[i], 4);
         }
+        mbar_init(&o_full, 1);
+        mbar_init(&o_free, 4);
+        mbar_init(&q_free, 2);  // the MMAs' commit, and an arrival that publishes piece_end
         mbar_init(&q_full, 4);
         fence_barrier_init();
     }
@@ -512,58 +529,98 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- MMAs ---------------------------------------------------------------------
             constexpr uint32_t id_s = idesc_f16(kM, kKT, false), id_o = idesc_f16(kM, D, true);
             const uint64_t k0 = smem_desc(ktiles, 16), v0 = smem_desc(vtiles, 8192);
-            auto pv = [&](int j) -> bool {  // O(j) = P(j) V(j)
-                const int bf = j & 1, st = j % kSlots;
-                if (!warp_wait(&p_full[bf], j >> 1, kErrQ8Mma) || !warp_wait(&v_ready[st], j / kSlots, kErrQ8Mma) ||
-                    (j >= 2 && !warp_wait(&o_free[bf], (j >> 1) - 1, kErrQ8Mma)))
-                    return false;
-                tc_fence_after();
-                const uint32_t d = tmem + C::kColO + bf * D, p = tmem + C::kColS + bf * kKT;
-                const uint64_t v = v0 + st * (C::kTile >> 4);
-                if (elect_one()) {
-#pragma unroll 1
-                    for (int k = 0; k < kKT / 16; ++k)
-                        mma_f16_ts(d, p + 16 * k + 8, v + (2048 >> 4) * k, id_o, k > 0 ? 1u : 0u);
-#pragma unroll 1
-                    for (int k = 0; k < kKT / 16; ++k)
-                        mma_f16_ts(d, p + 16 * k, v + (2048 >> 4) * k, id_o, 1u);
-                    mma_commit(&v_free[st]);
-                    mma_commit(&o_full[bf]);
+            const uint32_t k_lo = (uint32_t)k0, k_hi = (uint32_t)(k0 >> 32), v_lo = (uint32_t)v0, v_hi = (uint32_t)(v0 >> 32);
+            // S runs up to kScores tiles ahead of P V, but does not wait for its keys or queries while there
+            // is a P V to issue.
+            int sn = 0, vn = 0;
+            bool end = false, k_ok = false;
+            for (;;) {
+                if (!end && sn - vn < kScores) {
+                    const bool must = sn == vn;
+                    const int st = sn % kSlotsK;
+                    if (!k_ok) {
+                        k_ok = __all_sync(FULL, mbar_test(&k_ready[st], (uint32_t)((sn / kSlotsK) & 1)));
+                        if (!k_ok && must) {
+                            k_ok = warp_wait(&k_ready[st], sn / kSlotsK, kErrQ8Mma);
+                            if (!k_ok) break;
+                        }
+                    }
+                    if (k_ok) {
+                        const int flags = tile_s[sn % kTiles].flags, piece = tile_s[sn % kTiles].piece;
+                        bool q_ok = true;
+                        if (flags & kStop) {
+                            end = true;
+                            continue;
+                        }
+                        if (flags & kFirst) {
+                            q_ok = __all_sync(FULL, mbar_test(&q_full, (uint32_t)(piece & 1)));
+                            if (!q_ok && must) {
+                                q_ok = warp_wait(&q_full, piece, kErrQ8Mma);
+                                if (!q_ok) break;
+                            }
+                        }
+                        if (q_ok) {
+                            tc_fence_after();
+                            const uint32_t d = tmem + C::kColS + (sn % kScores) * kKT;
+                            const uint32_t k = k_lo + st * (C::kTile >> 4);
+                            if (elect_one()) {
+                                // Unrolled, with little but the MMA itself to an issue: the warp has a sixth of its
+                                // scheduler, and with loops and 64-bit sums S took 1500 cycles to issue.
+#pragma unroll
+                                for (int i = 0; i < D / 16; ++i) {
+                                    const uint32_t at = k + (i >> 2) * (8192 >> 4) + 2 * (i & 3);
+                                    if (i == 0) mma_f16_ts<false>(d, tmem + C::kColQlo, at, k_hi, id_s);
+                                    else mma_f16_ts<true>(d, tmem + C::kColQlo + 8 * i, at, k_hi, id_s);
+                                }
+#pragma unroll
+                                for (int i = 0; i < D / 16; ++i)
+                                    mma_f16_ts<true>(d, tmem + C::kColQhi + 8 * i, k + (i >> 2) * (8192 >> 4) + 2 * (i & 3), k_hi, id_s);
+                                mma_commit(&k_free[st]);
+                                mma_commit(&s_full[sn % kScores]);
+                                if (flags & kLast) {
+                                    piece_end[piece & 3] = sn + 1;
+                                    mma_commit(&q_free);
+                                    mbar_arrive(&q_free);  // publishes piece_end
+                                }
+                            }
+                            __syncwarp();
+                            ++sn;
+                            k_ok = false;
+                            continue;
+                        }
+                    }
                 }
-                __syncwarp();
-                return true;
-            };
-            for (int n = 0;; ++n) {
-                const int st = n % kSlots;
-                if (!warp_wait(&k_ready[st], n / kSlots, kErrQ8Mma)) break;
-                const int flags = tile_s[n % kTiles].flags;
-                if (!(flags & kStop)) {
-                    if ((flags & kFirst) && !warp_wait(&q_full, tile_s[n % kTiles].piece, kErrQ8Mma)) break;
+                if (vn < sn) {  // O(vn) = P(vn) V(vn)
+                    const int bf = vn % kScores, st = vn % kSlotsV;
+                    if (!warp_wait(&p_full[bf], vn / kScores, kErrQ8Mma) || !warp_wait(&v_ready[st], vn / kSlotsV, kErrQ8Mma) ||
+                        (vn > 0 && !warp_wait(&o_free, vn - 1, kErrQ8Mma)))
+                        break;
                     tc_fence_after();
-                    const uint32_t d = tmem + C::kColS + (n & 1) * kKT;
-                    const uint64_t k = k0 + st * (C::kTile >> 4);
+                    const uint32_t d = tmem + C::kColO, p = tmem + C::kColS + bf * kKT;
+                    const uint32_t v = v_lo + st * (C::kTile >> 4);
                     if (elect_one()) {
-                        auto off = [](int i) -> uint64_t { return (uint64_t)(i >> 2) * (8192 >> 4) + 2 * (i & 3); };
-#pragma unroll 2
-                        for (int i = 0; i < D / 16; ++i) mma_f16_ts(d, tmem + C::kColQlo + 8 * i, k + off(i), id_s, i > 0 ? 1u : 0u);
-#pragma unroll 2
-                        for (int i = 0; i < D / 16; ++i) mma_f16_ts(d, tmem + C::kColQhi + 8 * i, k + off(i), id_s, 1u);
-                        mma_commit(&k_free[st]);
-                        mma_commit(&s_full[n & 1]);
+#pragma unroll
+                        for (int k = 0; k < kKT / 16; ++k) {
+                            if (k == 0) mma_f16_ts<false>(d, p + 8, v, v_hi, id_o);
+                            else mma_f16_ts<true>(d, p + 16 * k + 8, v + (2048 >> 4) * k, v_hi, id_o);
+                        }
+#pragma unroll
+                        for (int k = 0; k < kKT / 16; ++k) mma_f16_ts<true>(d, p + 16 * k, v + (2048 >> 4) * k, v_hi, id_o);
+                        mma_commit(&v_free[st]);
+                        mma_commit(&o_full);
                     }
                     __syncwarp();
+                    ++vn;
+                    continue;
                 }
-                if (n > 0 && !pv(n - 1)) break;
-                if (flags & kStop) {
-                    // The others learn of it in turn, once they have taken their last tiles.
-                    if (n >= 2 && !warp_wait(&o_free[n & 1], (n >> 1) - 1, kErrQ8Mma)) break;
-                    if (lane == 0) {
-                        mbar_arrive(&s_full[n & 1]);
-                        mbar_arrive(&s_full[(n + 1) & 1]);
-                        mbar_arrive(&o_full[n & 1]);
-                    }
-                    break;
+                // The end: the others learn of it in turn, once they have taken their last tiles.
+                if (vn > 0 && !warp_wait(&o_free, vn - 1, kErrQ8Mma)) break;
+                if (lane == 0) {
+                    mbar_arrive(&s_full[sn % kScores]);
+                    mbar_arrive(&s_full[(sn + 1) % kScores]);
+                    mbar_arrive(&o_full);
                 }
+                break;
             }
         }
     } else if (warp < 8) {
@@ -571,14 +628,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int w = warp & 3, i = 32 * w + lane;
         const uint32_t lanes = (uint32_t)(32 * w) << 16;
-        bool ok = true;
         // The queries of the piece that tile j begins: times qk_mul and a power of two that brings
         // the row's largest element to [2^13, 2^14).  False at the list's end.
         auto load_queries = [&](int j) -> bool {
-            if (!warp_wait(&k_ready[j % kSlots], j / kSlots, kErrQ8Mma)) {  // what tile j is
-                ok = false;
-                return false;
-            }
             const Tile t = tile_s[j % kTiles];
             if (t.flags & kStop) return false;
             const Q8Req rq = q8_load_req(a, t.b);
@@ -618,39 +670,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&q_full);
             return true;
         };
-        // The next piece's queries go in once the scores of this one's last tile are done: S(n + 1)
-        // is issued before PV(n), so O(n) tells.
-        bool more = load_queries(0);
-        if (more && (tile_s[0].flags & kLast)) {
-            more = warp_wait(&s_full[0], 0, kErrQ8Mma);
-            ok = more;
-            tc_fence_after();
-            if (more) load_queries(1);
-        }
+        bool more = warp_wait(&k_ready[0], 0, kErrQ8Mma) && load_queries(0);
+        int loaded = 0;     // pieces after the first whose queries are in; -1: there are no more
+        int folded = 0;     // pieces that are done: tile n is one of the next piece's
         float acc[D], M = -INFINITY, L = 0.f;
 #pragma unroll
         for (int d = 0; d < D; ++d) acc[d] = 0.f;
-        for (int n = 0; ok && more; ++n) {
-            if (!warp_wait(&o_full[n & 1], n >> 1, kErrQ8Mma)) break;
+        for (int n = 0; more; ++n) {
+            // The next piece's queries go in once this one's scores are done and its first tile is
+            // known: the scores run ahead of O, so a look a tile mostly finds that in time.
+            if (loaded >= 0) {
+                const bool must = loaded < folded;
+                bool free = __all_sync(FULL, mbar_test(&q_free, (uint32_t)(loaded & 1)));
+                if (must && !free && !(free = warp_wait(&q_free, loaded, kErrQ8Mma))) break;
+                if (free) {
+                    const int e = piece_end[loaded & 3];
+                    bool known = __all_sync(FULL, mbar_test(&k_ready[e % kSlotsK], (uint32_t)((e / kSlotsK) & 1)));
+                    if (must && !known && !(known = warp_wait(&k_ready[e % kSlotsK], e / kSlotsK, kErrQ8Mma))) break;
+                    if (known) {
+                        tc_fence_after();
+                        loaded = load_queries(e) ? loaded + 1 : -1;
+                    }
+                }
+            }
+            if (!warp_wait(&o_full, n, kErrQ8Mma)) break;
             tc_fence_after();
             const Tile t = tile_s[n % kTiles];
             if (t.flags & kStop) break;
-            const Tile after = tile_s[(n + 1) % kTiles];  // its scores have been issued
-            if (!(after.flags & kStop) && (after.flags & kLast)) load_queries(n + 2);
-            if (!ok) break;
-            const float4 st = stat[n & 3][i];
+            const float2 st = stat[n % kRing][i];
             const float Mn = fmaxf(M, st.x), mu = Mn == -INFINITY ? 0.f : Mn;
             const float alpha = fast_exp2(M - mu), beta = fast_exp2(st.x - mu);
             M = Mn;
             L = fmaf(L, alpha, st.y * beta);
-            const float bo = beta * st.z;
+            const float bo = beta * stat_back[n % kRing][i];
             if (__any_sync(FULL, alpha != 1.f)) {  // a maximum moved
                 const uint64_t al = f2_pack(alpha, alpha);
 #pragma unroll
                 for (int d = 0; d < D; d += 2) f2_unpack(f2_mul(f2_pack(acc[d], acc[d + 1]), al), acc[d], acc[d + 1]);
             }
             const uint64_t be = f2_pack(bo, bo);
-            const uint32_t at = tmem + lanes + C::kColO + (n & 1) * D;
+            const uint32_t at = tmem + lanes + C::kColO;
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 16) {
                 float x[16];
@@ -659,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c0 == D - 16) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&o_free[n & 1]);
+                    if (lane == 0) mbar_arrive(&o_free);
                 }
 #pragma unroll
                 for (int d = 0; d < 16; d += 2)
@@ -696,6 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 __syncwarp();
+                ++folded;
                 M = -INFINITY;
                 L = 0.f;
 #pragma unroll
@@ -710,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int piece = -1, hi = 0, lo = 0, sinks = 0;
         bool alive = false;
         for (int n = turn;; n += 2) {
-            if (!warp_wait(&s_full[turn], n >> 1, kErrQ8Mma)) break;
+            if (!warp_wait(&s_full[n % kScores], n / kScores, kErrQ8Mma)) break;
             const Tile t = tile_s[n % kTiles];
             if (t.flags & kStop) break;
             if (t.piece != piece) {
@@ -729,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool all = !alive || (hi - t.key >= kKT - 1 && lo <= t.key);
             const bool whole = __all_sync(FULL, all);
             RowTile rt;
-            rt.at = tmem + lanes + C::kColS + turn * kKT;
+            rt.at = tmem + lanes + C::kColS + (n % kScores) * kKT;
             rt.ks = k_scale[n % kRing];
             rt.see = ~0ull;
             rt.rf = q_back[piece & 3][i];
@@ -739,31 +799,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 rt.see = below(hi - t.key + 1) & (~below(lo - t.key) | below(sinks - t.key));
             }
             const float back = v_back[n % kRing];
-            float4 st;
+            float2 ml;
+            float factor = back;
             if (back == 0.f) {  // rare
-                st = far_softmax<CAP>(rt, v_scale[n % kRing]);
-                st.z = exp2f(st.z - (float)kShift);
+                const float4 far = far_softmax<CAP>(rt, v_scale[n % kRing]);
+                ml = make_float2(far.x, far.y);
+                factor = exp2f(far.z - (float)kShift);
             } else {
-                const float2 ml = whole ? row_softmax<CAP, true>(rt, v_norm[n % kRing]) : row_softmax<CAP, false>(rt, v_norm[n % kRing]);
-                st = make_float4(ml.x, ml.y, back, 0.f);
+                ml = whole ? row_softmax<CAP, true>(rt, v_norm[n % kRing]) : row_softmax<CAP, false>(rt, v_norm[n % kRing]);
             }
-            stat[n & 3][i] = st;
+            stat[n % kRing][i] = ml;
+            stat_back[n % kRing][i] = factor;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[turn]);
+            if (lane == 0) mbar_arrive(&p_full[n % kScores]);
         }
     } else {
         // ---- codes to f16 ------------------------------------------------------------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         const int w = warp - 16;
         for (int n = 0;; ++n) {
-            const int st = n % kStages, sl = n % kSlots, rg = n % kRing;
+            const int st = n % kStages, kl = n % kSlotsK, vl = n % kSlotsV, rg = n % kRing;
             if (!warp_wait(&staged[st], n / kStages, kErrQ8Load)) break;
             const bool stop = tile_s[n % kTiles].flags & kStop;
-            if (n >= kSlots && !warp_wait(&k_free[sl], n / kSlots - 1, kErrQ8Free)) break;
+            if (n >= kSlotsK && !warp_wait(&k_free[kl], n / kSlotsK - 1, kErrQ8Free)) break;
             if (stop) {
-                if (lane == 0) mbar_arrive(&k_ready[sl]);
+                if (lane == 0) mbar_arrive(&k_ready[kl]);
                 break;
             }
             if (w == 0) {  // the range of the values' scales
@@ -785,13 +847,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
 #pragma unroll 1
             for (int kv = 0; kv < 2 && ok; ++kv) {
-                if (kv) ok = n < kSlots || warp_wait(&v_free[sl], n / kSlots - 1, kErrQ8Free);
+                if (kv) ok = n < kSlotsV || warp_wait(&v_free[vl], n / kSlotsV - 1, kErrQ8Free);
                 if (FORM == kFormE4m3 && kv && tile_s[n % kTiles].rows < kKT)
                     clear_rows<D>(codes + (size_t)(2 * st + 1) * C::kCodes, tile_s[n % kTiles].rows, w, lane);
-                convert<D, FORM>(codes + (size_t)(2 * st + kv) * C::kCodes, (kv ? vtiles : ktiles) + sl * C::kTile, w, lane);
+                convert<D, FORM>(codes + (size_t)(2 * st + kv) * C::kCodes, kv ? vtiles + vl * C::kTile : ktiles + kl * C::kTile, w, lane);
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
                 __syncwarp();
-                if (lane == 0) mbar_arrive(kv ? &v_ready[sl] : &k_ready[sl]);
+                if (lane == 0) mbar_arrive(kv ? &v_ready[vl] : &k_ready[kl]);
             }
             if (!ok) break;
             if (lane == 0) mbar_arrive(&unstaged[st]);
