@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -904,9 +905,21 @@ def paged_write(k_pool, v_pool, k_new, v_new, slots, *, stream=None):
     return k_pool, v_pool
 
 
+@functools.lru_cache(maxsize=256)
+def _paged_params(rows, pages, requests, max_rows, page_size, max_pages, heads, kv_heads, head_dim, tree, scale, softcap,
+                  kernel, window, sinks, q8):
+    """(params, workspace bytes) of a paged call; read only, so one for all equal calls."""
+    p = vtmu_paged_params(rows=rows, pages=pages, requests=requests, max_rows=max_rows, page_size=page_size,
+                          max_pages=max_pages, heads=heads, kv_heads=kv_heads, head_dim=head_dim, tree=tree,
+                          has_scale=0 if scale is None else 1, scale=0.0 if scale is None else scale, softcap=softcap,
+                          kernel=kernel, window=window, sinks=sinks)
+    return p, (vtmu_paged_q8_workspace_size if q8 else vtmu_paged_workspace_size)(p)
+
+
 def _paged_call(q, width, pool_rows, block_table, lens, cu_rows, heads, headDim, pageSize, maxRows, kvHeads, tree, scale,
-                softcap, window, sinks, kernel, out):
-    """What the paged attentions check and lay out alike: (params, out, k_new, v_new, masks, positions)."""
+                softcap, window, sinks, kernel, out, q8):
+    """What the paged attentions check and lay out alike: (params, workspace bytes, out, k_new,
+    v_new, masks, positions)."""
     import torch
     dev = q.device
     f32, i32 = torch.float32, torch.int32
@@ -935,13 +948,11 @@ def _paged_call(q, width, pool_rows, block_table, lens, cu_rows, heads, headDim,
     _need("out", out, f32, dev)
     if out.shape != q.shape:
         raise ValueError("paged_attention: out [rows, heads*headDim]")
-    p = vtmu_paged_params(rows=rows, pages=pool_rows // pageSize, requests=n,
-                          max_rows=max(min(maxRows, rows), -1), page_size=pageSize,
-                          max_pages=block_table.shape[1], heads=heads, kv_heads=hk, head_dim=headDim,
-                          tree=0 if tree is None else 1, has_scale=0 if scale is None else 1,
-                          scale=0.0 if scale is None else scale, softcap=softcap or 0.0, kernel=kernel,
-                          window=window or 0, sinks=sinks or 0)
-    return p, out, k_new, v_new, masks, positions
+    with _on(dev):
+        p, nbytes = _paged_params(rows, pool_rows // pageSize, n, max(min(maxRows, rows), -1), pageSize,
+                                  block_table.shape[1], heads, hk, headDim, 0 if tree is None else 1, scale,
+                                  softcap or 0.0, kernel, window or 0, sinks or 0, q8)
+    return p, nbytes, out, k_new, v_new, masks, positions
 
 
 def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, headDim, pageSize, maxRows, kvHeads=None,
@@ -961,11 +972,10 @@ def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, hea
         _need(name, t, torch.float32, dev)
     if k_pool.dim() != 2 or k_pool.shape != v_pool.shape:
         raise ValueError("paged_attention: pools [pages*pageSize, kvHeads*headDim]")
-    p, out, k_new, v_new, masks, positions = _paged_call(
+    p, nbytes, out, k_new, v_new, masks, positions = _paged_call(
         q, k_pool.shape[1], k_pool.shape[0], block_table, lens, cu_rows, heads, headDim, pageSize, maxRows, kvHeads, tree,
-        scale, softcap, window, sinks, kernel, out)
+        scale, softcap, window, sinks, kernel, out, False)
     with _on(dev):
-        nbytes = vtmu_paged_workspace_size(p)
         st = _raw_stream(dev) if stream is None else stream
         buf, cap = _scratch(workspace, dev, st, nbytes, counters=False)
         vtmu_paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, k_new, v_new, masks, positions, out, p,
@@ -1053,11 +1063,10 @@ def paged_attention_q8(q, k_pool, v_pool, k_scale, v_scale, block_table, lens, c
     kind, total, hk, d = _q8_pools("paged_attention_q8", k_pool, v_pool, k_scale, v_scale)
     if k_pool.device != dev or hk != (heads if kvHeads is None else kvHeads) or d != headDim:
         raise ValueError("paged_attention_q8: pools on q's device, kvHeads scales and kvHeads*headDim codes a row")
-    p, out, k_new, v_new, masks, positions = _paged_call(
+    p, nbytes, out, k_new, v_new, masks, positions = _paged_call(
         q, k_pool.shape[1], total, block_table, lens, cu_rows, heads, headDim, pageSize, maxRows, kvHeads, tree, scale,
-        softcap, window, sinks, kernel, out)
+        softcap, window, sinks, kernel, out, True)
     with _on(dev):
-        nbytes = vtmu_paged_q8_workspace_size(p)
         st = _raw_stream(dev) if stream is None else stream
         buf, cap = _scratch(workspace, dev, st, nbytes, counters=False)
         vtmu_paged_attention_q8(q, k_pool, v_pool, k_scale, v_scale, kind, block_table, lens, cu_rows, k_new, v_new,
@@ -1080,6 +1089,13 @@ def make_norm_rope_params(*, headDim, norm=True, eps=1e-6, weightOffset=0.0, sec
             p.sections[i] = int(n)
     p.dealt = 1 if dealt else 0
     return p
+
+
+@functools.lru_cache(maxsize=64)
+def _norm_rope_params(headDim, norm, eps, weightOffset, sections, dealt, rope):
+    """make_norm_rope_params of equal calls; read only."""
+    return make_norm_rope_params(headDim=headDim, norm=norm, eps=eps, weightOffset=weightOffset, sections=sections,
+                                 dealt=dealt, **dict(rope))
 
 
 def norm_rope(q, k, positions, *, headDim, qWeight=None, kWeight=None, norm=True, eps=1e-6, weightOffset=0.0,
@@ -1107,8 +1123,12 @@ def norm_rope(q, k, positions, *, headDim, qWeight=None, kWeight=None, norm=True
             (k is not None and (k.dim() != 2 or k.shape[0] != T or k.shape[1] % headDim or k_out.shape != k.shape)) or
             any(w is not None and w.shape != (headDim,) for w in (qWeight, kWeight))):
         raise ValueError("norm_rope: q and k [T, heads*headDim], positions [T] or [axes, T], weights [headDim], out as q and k")
-    p = make_norm_rope_params(headDim=headDim, norm=norm, eps=eps, weightOffset=weightOffset, sections=sections, dealt=dealt,
-                              **rope)
+    args = (headDim, norm, eps, weightOffset, None if sections is None else tuple(sections), dealt, tuple(rope.items()))
+    if rope.get("scaling") is None and rope.get("invFreq") is None:
+        p = _norm_rope_params(*args)
+    else:  # may not be hashable, or change
+        p = make_norm_rope_params(headDim=headDim, norm=norm, eps=eps, weightOffset=weightOffset, sections=sections,
+                                  dealt=dealt, **rope)
     with _on(dev):
         st = _raw_stream(dev) if stream is None else stream
         vtmu_norm_rope(q, k, qWeight, kWeight, q_out, k_out, T, q.shape[1] // headDim,

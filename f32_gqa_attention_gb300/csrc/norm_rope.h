@@ -19,9 +19,11 @@ struct NormRopeArgs {
     const int32_t* positions;  // [axes, T]
     int64_t T;
     int32_t H, Hk, D, axes, norm;
-    float eps, weight_offset;
+    float eps, weight_offset, inv_d;  // inv_d: 1 / D
+    int32_t half, interleaved;    // as RopeDev's
+    float attn;
     uint8_t axis[kRopeMaxPairs];  // of each pair
-    RopeDev r;
+    uint64_t turn[kRopeMaxPairs]; // inv_freq / (2 pi) less its whole part, times 2^64
 };
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
 

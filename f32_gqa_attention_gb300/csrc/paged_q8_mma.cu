@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
     constexpr int NV = 8 * NT, S = kStages, KC = D / 64, MT = D / 16;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long scan_s[kConsumers + kProducers];
-    __shared__ __align__(8) uint64_t full[S], freed[S], x_put, x_got;
+    __shared__ __align__(8) uint64_t known[S], full[S], freed[S], x_put, x_got;
     __shared__ __align__(16) Tile tile_s[S];
     const PagedDesc& a = g.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t4 = lane & 3;
@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], 32 * kProducers + 1);  // every producer lane's copies, and what the tile is
+            mbar_init(&known[i], 1);                // what the tile is
+            mbar_init(&full[i], 32 * kProducers);  // every producer lane's copies
             mbar_init(&freed[i], consumers);
         }
         mbar_init(&x_put, consumers - g.hb > 0 ? consumers - g.hb : 1);
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
             unsigned char* to = smem + (size_t)st * g.stage;
             if (pw == 0 && lane == 0) {
                 tile_s[st] = t;
-                mbar_arrive(&full[st]);
+                mbar_arrive(&known[st]);
             }
             if (t.key >= 0) {
                 const int hb = min(g.hb, a.Hk - h0), chunks = hb * (D / 16);  // of a row
@@ -365,10 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
     int sinks = 0, pieces = 0;
     for (int n = 0;; ++n) {
         const int st = n % S;
-        if (!__all_sync(FULL, mbar_wait(&full[st], (uint32_t)((n / S) & 1)))) {
+        auto wait = [&](uint64_t* bar) -> bool {
+            if (__all_sync(FULL, mbar_wait(bar, (uint32_t)((n / S) & 1)))) return true;
             raise_device_error(&g_q8_device_error, kErrQ8Load);
-            break;
-        }
+            return false;
+        };
+        if (!wait(&known[st])) break;
         Tile tile = tile_s[st];
         if (tile.flags & kStop) break;
         const int hk = (tile.flags >> kBlockShift) * g.hb + head_w;
@@ -444,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
             }
         }
 
+        if (!wait(&full[st])) break;  // a piece's queries are asked for beside its first keys
         // ---- scores: x[block of 16 keys][nt]: keys gr (0, 1) and gr + 8 (2, 3), rows 2 t4 and + 1 ----
         float x[2][NT][4];
         float vs[2][2];  // value scales of keys gr, gr + 8

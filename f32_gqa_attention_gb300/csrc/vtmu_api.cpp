@@ -269,6 +269,15 @@ vtmu_status resolve_rope(const vtmu_rope_params* r, vtmu::RopeDev* out) {
     }
     const float af = r->attention_factor == 0.f ? 1.f : r->attention_factor;
     if (!std::isfinite(af)) return fail(VTMU_ERR_INVALID, "rope.scaling: attention_factor must be finite");
+    // The powers of the last parameters on this thread: 64 of them take 2 to 3 us, as long as a
+    // small launch.  Explicit frequencies are read at every call.
+    thread_local vtmu_rope_params last_p;
+    thread_local vtmu::RopeDev last;
+    thread_local bool known = false;
+    if (known && !r->inv_freq && std::memcmp(r, &last_p, sizeof(last_p)) == 0) {
+        *out = last;
+        return ok();
+    }
     std::memset(out, 0, sizeof(*out));
     out->half = rd / 2;
     out->interleaved = r->interleaved ? 1 : 0;
@@ -277,6 +286,11 @@ vtmu_status resolve_rope(const vtmu_rope_params* r, vtmu::RopeDev* out) {
         double f = r->inv_freq ? (double)r->inv_freq[j] : std::pow(base, -2.0 * j / rd);
         if (!std::isfinite(f)) return fail(VTMU_ERR_INVALID, "rope.scaling: inv_freq[%d] is not finite", j);
         out->inv_freq[j] = f / divisor;
+    }
+    if (!r->inv_freq) {
+        std::memcpy(&last_p, r, sizeof(last_p));
+        last = *out;
+        known = true;
     }
     return ok();
 }
@@ -1356,6 +1370,15 @@ vtmu_status vtmu_paged_attention_q8(const float* q, const void* k_pool, const vo
     return ok();
 }
 
+// The part of hi + lo behind the point, times 2^64.
+static uint64_t turn_of(double hi, double lo) {
+    hi -= std::floor(hi);  // exact
+    const double top = std::floor(std::ldexp(hi, 32)), rest = std::ldexp(hi, 32) - top;  // 32 bits, and what is left, exact
+    // rest 2^32 + lo 2^64, of either sign, onto top 2^32; carries and borrows wrap as turns do.
+    const double low = std::ldexp(rest, 32), more = std::ldexp(std::fmod(lo, 1.0), 64);
+    return ((uint64_t)top << 32) + (uint64_t)low + (uint64_t)(int64_t)std::fmin(std::fmax(std::rint(more), -9.2e18), 9.2e18);
+}
+
 void vtmu_norm_rope_params_init(vtmu_norm_rope_params* p) {
     if (!p) return;
     std::memset(p, 0, sizeof(*p));
@@ -1371,8 +1394,12 @@ vtmu_status vtmu_norm_rope(const float* q, const float* k, const float* q_weight
     if (!p) return fail(VTMU_ERR_INVALID, "norm_rope params is NULL");
     vtmu::NormRopeArgs a;
     std::memset(&a, 0, sizeof(a));
-    const vtmu_status st = resolve_rope(&p->rope, &a.r);
+    vtmu::RopeDev rd;
+    const vtmu_status st = resolve_rope(&p->rope, &rd);
     if (st != VTMU_OK) return st;
+    a.half = rd.half;
+    a.interleaved = rd.interleaved;
+    a.attn = rd.attn;
     if (T < 0 || heads <= 0 || kv_heads < 0)
         return fail(VTMU_ERR_INVALID, "norm_rope: T %lld, heads %d and kv_heads %d must be >= 0, > 0 and >= 0",
                     (long long)T, heads, kv_heads);
@@ -1387,10 +1414,10 @@ vtmu_status vtmu_norm_rope(const float* q, const float* k, const float* q_weight
             if (p->sections[i] < 0) return fail(VTMU_ERR_INVALID, "norm_rope: sections[%d] is negative", i);
             sum += p->sections[i];
         }
-        if (sum != a.r.half)
-            return fail(VTMU_ERR_INVALID, "norm_rope: sections add up to %lld pairs of %d", (long long)sum, a.r.half);
+        if (sum != a.half)
+            return fail(VTMU_ERR_INVALID, "norm_rope: sections add up to %lld pairs of %d", (long long)sum, a.half);
         int dealt[VTMU_MAX_AXES] = {0, 0, 0, 0};
-        for (int j = 0, run = 0, left = p->sections[0]; j < a.r.half; ++j) {
+        for (int j = 0, run = 0, left = p->sections[0]; j < a.half; ++j) {
             if (p->dealt) {
                 const int i = j % p->axes;
                 a.axis[j] = (uint8_t)(j < p->axes * (int64_t)p->sections[i] ? i : 0);
@@ -1420,6 +1447,12 @@ vtmu_status vtmu_norm_rope(const float* q, const float* k, const float* q_weight
                           {q_weight, wb}, {k_weight, wb}, {positions, (size_t)p->axes * T * 4}};
     if (outputs_overlap(spans, 2, 7))
         return fail(VTMU_ERR_INVALID, "norm_rope: an output overlaps another buffer (other than its own input, in place)");
+    for (int j = 0; j < a.half; ++j) {
+        // 1 / (2 pi) as a double and the double nearest its remainder: the product to 2^-100 or so.
+        const double hi = rd.inv_freq[j] * 0.15915494309189535, lo = std::fma(rd.inv_freq[j], 0.15915494309189535, -hi) +
+                                                                      rd.inv_freq[j] * -9.839338337591243e-18;
+        a.turn[j] = turn_of(hi, lo);
+    }
     a.q = q;
     a.k = k;
     a.qw = q_weight;
@@ -1435,6 +1468,7 @@ vtmu_status vtmu_norm_rope(const float* q, const float* k, const float* q_weight
     a.norm = p->norm;
     a.eps = p->eps;
     a.weight_offset = p->weight_offset;
+    a.inv_d = 1.f / (float)p->rope.head_dim;
     const cudaError_t e = vtmu::launch_norm_rope(a, stream);
     if (e != cudaSuccess) return cuda_fail(e, "norm_rope launch");
     return ok();
