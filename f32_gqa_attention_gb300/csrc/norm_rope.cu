@@ -216,7 +216,7 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
     while (8 << log_l < a.D) ++log_l;
     const int64_t heads = (int64_t)a.H + a.Hk, side = 32 >> (log_l < 5 ? log_l : 5);
     // Quads of four pairs and 16-byte accesses; other widths turn a pair at a time.
-    if ((mis & 15u) == 0 && a.D % 8 == 0 && a.D <= 256 && a.half % 4 == 0 && a.T * heads < ((int64_t)1 << 32)) {
+    if ((mis & 15u) == 0 && a.D % 8 == 0 && a.D <= 256 && a.half % 4 == 0 && a.T * heads < ((int64_t)1 << 31)) {
         // Few rows: a turn a job, for the latency.
         const bool few = a.T * heads < 16 * kWave * side;
         const int64_t each = (few ? 1 : 4) * side, chunks = (heads + each - 1) / each, ctas = (a.T * chunks + 3) / 4;

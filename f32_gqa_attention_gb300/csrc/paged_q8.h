@@ -53,10 +53,12 @@ size_t paged_q8_tc_workspace(const PagedDesc& a);
 cudaError_t launch_paged_q8_tc(const PagedDesc& a, const Q8Pools& p, int num_sms, void* workspace, cudaStream_t stream);
 unsigned int paged_q8_tc_take_device_error();
 // Which of the two: virtual rows (rows of a request x heads of a group) above kQ8FewRows take the
-// blocks of 128; its boxes of 64-byte rows want pages of an even size.
+// blocks of 128; its boxes of 64-byte rows want pages of an even size, and the box behind the
+// pool, which stands for bad pages, coordinates below 2^31.
 constexpr int kQ8FewRows = 16;
 inline bool paged_q8_few_rows(const PagedDesc& a) {
-    return (int64_t)a.max_rows * a.G <= kQ8FewRows || (a.D == 64 && a.page_size % 2 != 0);
+    return (int64_t)a.max_rows * a.G <= kQ8FewRows || (a.D == 64 && a.page_size % 2 != 0) ||
+           a.pages * a.page_size >= ((int64_t)1 << 31) - 256;
 }
 // The drafted rows' part of every row: its output to a.out, its maximum and sum to ml [rows][H].
 cudaError_t launch_paged_q8_draft(const PagedDesc& a, float2* ml, cudaStream_t stream);

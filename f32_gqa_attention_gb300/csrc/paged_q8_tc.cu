@@ -833,14 +833,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t b0 = __float_as_uint(v0) & 0x7fffffffu, b1 = __float_as_uint(v1) & 0x7fffffffu;
                 const uint32_t most = __reduce_max_sync(FULL, max(b0, b1));
                 const uint32_t least = __reduce_min_sync(FULL, min(b0 ? b0 : ~0u, b1 ? b1 : ~0u));
-                // E, where 2^(kShift - E) and its inverse are normal numbers.
+                // E, where 2^(kShift - E) and its inverse are normal numbers (a tile whose scales are all below
+                // 2^-110 keeps 23 bits of its largest weight).
                 int e = (int)(most >> 23) - 127;
-                const bool far = most > least && (most - least > (uint32_t)kFar << 23 || e > 110 || e < -100);
-                e = e < -100 ? -100 : e > 110 ? 110 : e;
+                const bool far = e > 110 || (most > least && most - least > (uint32_t)kFar << 23);
+                e = e < -110 ? -110 : e > 110 ? 110 : e;
                 const float up = __uint_as_float((uint32_t)(127 + kShift - e) << 23);
                 v_norm[rg][lane] = v0 * up;
                 v_norm[rg][lane + 32] = v1 * up;
-                if (lane == 0) v_back[rg] = far || e == 110 ? 0.f : __uint_as_float((uint32_t)(127 - kShift + e) << 23);
+                if (lane == 0) v_back[rg] = far ? 0.f : __uint_as_float((uint32_t)(127 - kShift + e) << 23);
             }
             // Short loops on purpose, K and V through the same code: six warps with code of their own share
             // a scheduler, and unrolled roles ran at the rate of instruction fetches.

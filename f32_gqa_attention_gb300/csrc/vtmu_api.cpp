@@ -1244,8 +1244,8 @@ static vtmu_status check_q8(const char* what, int64_t pool_rows, int32_t kv_head
     if (format != VTMU_KV_INT8 && format != VTMU_KV_E4M3)
         return fail(VTMU_ERR_INVALID, "%s: format %d is not a vtmu_kv_format", what, format);
     if (head_dim > 256) return fail(VTMU_ERR_UNSUPPORTED, "%s: head_dim %d > 256 is not supported", what, head_dim);
-    if ((pool_rows | rows | (int64_t)kv_heads * head_dim) >> 31 || rows * kv_heads >= ((int64_t)1 << 31))
-        return fail(VTMU_ERR_UNSUPPORTED, "%s: sizes must be below 2^31", what);
+    if ((pool_rows | rows) >> 31 || (int64_t)kv_heads * head_dim >> 30 || rows * kv_heads >= ((int64_t)1 << 31))
+        return fail(VTMU_ERR_UNSUPPORTED, "%s: sizes must be below 2^31, kv_heads x head_dim below 2^30", what);
     return VTMU_OK;
 }
 
@@ -1434,9 +1434,8 @@ vtmu_status vtmu_norm_rope(const float* q, const float* k, const float* q_weight
                             p->sections[i]);
     }
     if (!p->norm && (q_weight || k_weight)) return fail(VTMU_ERR_INVALID, "norm_rope: weights without a norm");
-    if ((int64_t)heads * p->rope.head_dim >= ((int64_t)1 << 31) || (int64_t)kv_heads * p->rope.head_dim >= ((int64_t)1 << 31) ||
-        (int64_t)heads + kv_heads >= ((int64_t)1 << 31) - 256)
-        return fail(VTMU_ERR_UNSUPPORTED, "norm_rope: heads x headDim must be below 2^31");
+    if (((int64_t)heads + kv_heads) * p->rope.head_dim >= ((int64_t)1 << 30) || T >= ((int64_t)1 << 31))
+        return fail(VTMU_ERR_UNSUPPORTED, "norm_rope: T must be below 2^31, (heads + kv_heads) x headDim below 2^30");
     if (T == 0) return ok();
     if (!q || !q_out || !positions || (kv_heads > 0 ? !k || !k_out : k || k_out || k_weight))
         return fail(VTMU_ERR_INVALID, "norm_rope: q, q_out, positions, and k, k_out exactly with kv_heads, must be given");

@@ -717,7 +717,7 @@ typedef enum vtmu_kv_format {
  *   DEVICE.  None may overlap another.  head_dim 1..256.
  * Errors: VTMU_ERR_INVALID (null pointer with rows > 0, bad size or format,
  * misaligned or overlapping buffers), VTMU_ERR_UNSUPPORTED (head_dim above 256,
- * a size of 2^31 or more), VTMU_ERR_CUDA.
+ * a size of 2^31 or more, kv_heads*head_dim of 2^30 or more), VTMU_ERR_CUDA.
  */
 VTMU_API vtmu_status vtmu_paged_write_q8(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
                                          int64_t pool_rows, int32_t kv_heads, int32_t head_dim, int32_t format,
@@ -746,11 +746,15 @@ VTMU_API vtmu_status vtmu_paged_q8_workspace_size(const vtmu_paged_params* p, si
  * (k_new and v_new of a tree are f32).  A head whose scale is NaN is a key or a value
  * that is not finite.  `format`: vtmu_kv_format.
  * Kernels: p->kernel forces the CUDA cores or the tensor cores; AUTO takes the tensor
- * cores where they cover the call (headDim 64 or 128, 16-byte aligned q, out, pools and, in
- * a tree, k_new and v_new).  Scores and sums are f32 in both.  The tensor cores
- * take the codes as they are, keep 22 bits of the largest element of each row and head of q
- * and of drafted rows, and weights, or the products of weight and value scale, to 2^-36
- * of the largest among a tile's keys.
+ * cores where they cover the call (headDim 64 or 128, pages of any size, at least one in the
+ * pool, 16-byte aligned q, out, pools and, in a tree, k_new and v_new).  Scores and sums are f32
+ * in both.  The tensor cores take the codes as they are (exact in f16) and keep 22 bits of the
+ * largest element of each row and head of q and of drafted rows.  A weight times its value's
+ * scale has 22 bits, and is kept to 2^-35 of the largest such product so far (up to 16 rows x
+ * heads of a group) or to 2^-32 of the largest in its 64 keys (above; to 2^-23 where all their
+ * scales are below 2^-110).  On the tensor cores a drafted head with an element that is not finite
+ * counts as NaN throughout, and an e4m3 code that is NaN (0x7f, 0xff: vtmu_paged_write_q8
+ * stores none) among a request's values may make its column NaN in every row of the request.
  */
 VTMU_API vtmu_status vtmu_paged_attention_q8(const float* q, const void* k_pool, const void* v_pool,
                                              const float* k_scale, const float* v_scale, int32_t format,
@@ -801,7 +805,8 @@ VTMU_API void vtmu_norm_rope_params_init(vtmu_norm_rope_params* p);
  * head of zeros with eps == 0 is 0 / 0, NaN.
  * Errors: those of vtmu_rope, VTMU_ERR_INVALID (axes, sections, eps or
  * weight_offset out of range, weights without a norm, null, misaligned or
- * overlapping buffers), VTMU_ERR_CUDA.
+ * overlapping buffers), VTMU_ERR_UNSUPPORTED (T of 2^31 or more, or
+ * (heads + kv_heads)*head_dim of 2^30 or more), VTMU_ERR_CUDA.
  */
 VTMU_API vtmu_status vtmu_norm_rope(const float* q, const float* k, const float* q_weight, const float* k_weight,
                                     float* q_out, float* k_out, int64_t T, int32_t heads, int32_t kv_heads,

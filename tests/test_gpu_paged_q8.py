@@ -220,6 +220,19 @@ def test_norm_rope_with_no_norm_is_rope_at():
         assert float((y - want).abs().max()) <= 1.2 * 2.0 ** -20 * 2 * float(x.abs().max())
 
 
+@pytest.mark.parametrize("D,kw", [(128, dict()), (128, dict(sections=[24, 20, 20], dealt=True)), (10, dict())])
+def test_norm_rope_at_far_positions(D, kw):
+    """Positions up to 2^31 - 1.  The plain angle is a double that rounds at 2^31 2^-53, the kernel's a
+    fixed-point number off by 2^31 2^-65 turns: 2^-21 more."""
+    g = np.random.default_rng(2)
+    axes = len(kw.get("sections", [0]))
+    pos = (2 ** 31 - 1 - g.integers(0, 50, (axes, 6))).astype(np.int32)
+    x = g.standard_normal((6, 4 * D), dtype=np.float32)
+    y, _ = vtmu.norm_rope(dev(x), None, dev(pos if axes > 1 else pos[0]), headDim=D, **kw)
+    want, size = q8.norm_rope(x, pos, headDim=D, **kw)
+    assert np.all(np.abs(y.cpu().numpy() - want) <= (2.0 ** -20 + 2.0 ** -21 + 2.0 ** -22 + 2.0 ** -21) * size)
+
+
 def test_norm_rope_wrong_arguments():
     x, p = torch.zeros(4, 256, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
     w = torch.ones(128, device="cuda")
@@ -347,6 +360,368 @@ def test_bad_pages_and_lengths():
         d["table"] = t
         for kernel in kernels_of(64):
             check(attend(d, kernel=kernel, **size), want)
+
+
+# Calls of more than 16 rows x heads of a group take kernels of their own: each of the
+# following comes with few rows and with many.
+def size_of(H, hk, D, page):
+    return dict(heads=H, kvHeads=hk, headDim=D, pageSize=page)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows", [3, 20])
+@pytest.mark.parametrize("Hk", [1, 3])
+@pytest.mark.parametrize("lens", [[4 * 64], [3 * 64 + 1, 1], [64 * 151], [64 * 152, 64], [64 * 304 + 5], [64 * 609]])
+def test_units_cut_at_every_kind_of_boundary(lens, Hk, rows, form):
+    size = size_of(Hk, Hk, 64, 16)
+    d = q8.batch(31, lens, [rows] * len(lens), form=form, **size)
+    check(attend(d, kernel=TENSOR, **size), expect(d, **size))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hk", list(range(1, 10)) + [17])
+def test_numbers_of_heads(Hk, D):
+    size = size_of(2 * Hk, Hk, D, 16)
+    for counts, tree in (([4, 1, 7], False), ([3, 8, 2], True), ([30, 9, 1], True)):
+        d = q8.batch(Hk, [300, 33, 1000], counts, form=FORMS[Hk % 2], tree=tree, **size)
+        check(attend(d, kernel=TENSOR, **size), expect(d, **size))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [1, 2, 5, 7, 12, 24, 48, 256, 1000])
+def test_page_sizes(page, D, form):
+    size = size_of(4, 2, D, page)
+    for counts, tree in (([2, 5], False), ([40, 33], False), ([30, 12], True)):
+        d = q8.batch(page, [77, 501], counts, form=form, tree=tree, **size)
+        check(attend(d, kernel=TENSOR, **size), expect(d, **size))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("counts", [[5, 6], [40, 61]])
+@pytest.mark.parametrize("kw", [dict(window=1), dict(window=33, sinks=70), dict(window=700, softcap=3.0),
+                                dict(window=64, sinks=1, scale=1.0), dict(softcap=50.0)])
+def test_windows_and_caps(kw, counts, tree, form):
+    """Rows before a request's first position and rows whose window leaves nothing are zeros."""
+    size = size_of(6, 2, 128, 16)
+    d = q8.batch(17, [3, 640], counts, form=form, tree=tree, **size)
+    want = expect(d, **size, **kw)
+    for kernel in (CUDA, TENSOR):
+        got = attend(d, kernel=kernel, **size, **kw)
+        check(got, want)
+        assert np.all(got[np.abs(want).max(1) == 0] == 0)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("counts", [[4], [30]])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, 3e38])
+def test_what_a_row_does_not_see_does_not_reach_it(bad, counts, form):
+    """Scales of any kind, and any codes, at keys that a window, causality or the end hides."""
+    size = size_of(4, 2, 64, 16)
+    n = counts[0]
+    d = q8.batch(41, [400], counts, form=form, **size)
+    at = d["table"][0, np.arange(400) // 16].astype(np.int64) * 16 + np.arange(400) % 16
+    want = expect(d, **size, window=100)
+    last = 400 - n  # the first row's position
+    hidden = np.arange(400) < last - 99  # from every row; the newest key, from all but the last row
+    d["ks"][at[hidden]], d["vs"][at[hidden]] = bad, bad
+    d["ks"][at[399]], d["vs"][at[399]] = bad, bad
+    unowned = np.setdiff1d(np.arange(len(d["ks"])), at)
+    d["ks"][unowned], d["vs"][unowned] = bad, bad
+    d["kc"][unowned], d["vc"][unowned] = 0x7f, 0xff  # NaN as e4m3
+    for kernel in (CUDA, TENSOR):
+        got = attend(d, kernel=kernel, **size, window=100)
+        check(got[:n - 1], want[:n - 1])  # the last row alone sees key 399
+        if np.isnan(bad):
+            assert np.all(np.isnan(got[n - 1]))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("counts", [[3, 2], [20, 18]])
+@pytest.mark.parametrize("which", ["spread", "tiny values", "subnormal values", "huge values", "huge keys", "zero heads"])
+def test_rows_of_any_size(which, counts, form):
+    """By heads, whose outputs differ in size: 2^-15 in the 2-norm, as of test_heads_of_far_sizes, and
+    for values below 2^-126 the last place of theirs."""
+    size = size_of(8, 4, 64, 16)
+    mul = np.ones(8)
+
+    def gain(k, v):
+        g = np.random.default_rng(9)
+        heads = 2.0 ** np.array([-40.0, 0, 3, 40])
+        if which == "spread":
+            k, v = k * np.repeat(heads, 64), v * np.repeat(heads[::-1], 64) * 2.0 ** g.integers(-15, 15, (v.shape[0], 1))
+            k[:, ::32] *= 8
+            mul[:] = np.repeat(1 / heads, 2) * [1, 1, 1, 1, 1, 1, 1, 1]
+        elif which == "tiny values":
+            v = v * 2.0 ** -112 * np.repeat([1.0, 2.0 ** -3, 2.0 ** 4, 2.0 ** 10], 64)
+        elif which == "subnormal values":
+            v = v * 2.0 ** -121
+        elif which == "huge values":
+            v = v * 2.0 ** 121
+        elif which == "huge keys":
+            k, mul[:] = k * 2.0 ** 100, 2.0 ** -100
+        else:
+            v = v.copy()
+            v[:, 64:128] = 0
+            v[::3, 128:192] = 0
+        return k.astype(np.float32), v.astype(np.float32)
+
+    d = q8.batch(5, [300, 70], counts, form=form, gain=gain, **size)
+    d["q"] = (d["q"] * np.repeat(mul, 64)).astype(np.float32)
+    want = expect(d, **size)
+    for kernel in (CUDA, TENSOR):
+        got = attend(d, kernel=kernel, **size).astype(np.float64)
+        for h in range(8):
+            c = slice(64 * h, 64 * h + 64)
+            for t in range(sum(counts)):
+                n = np.linalg.norm(want[t, c])
+                e = np.linalg.norm(got[t, c] - want[t, c])
+                assert e <= 2.0 ** -15 * n + 64 * 2.0 ** -149, (kernel, h, t, e, n)
+
+
+@pytest.mark.parametrize("counts", [[6], [40]])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_drafted_rows_that_are_not_finite(bad, counts):
+    size = size_of(4, 2, 64, 16)
+    for form in FORMS:
+        d = q8.batch(16, [100], counts, form=form, tree=True, **size)
+        kn, vn, masks, pos = d["tree"]
+        want = expect(d, **size)
+        sees = [np.array([(int(m) >> j) & 1 for m in masks], bool) for j in (2, 3)]
+        kn[2, 5], vn[3, 64 + 7] = bad, bad  # a key of KV head 0, a value of head 1
+        got = attend(d, kernel=TENSOR, **size)
+        assert np.all(np.isnan(got[sees[0]][:, :128])) and np.all(np.isnan(got[sees[1]][:, 128:]))
+        good = np.ones(got.shape, bool)
+        good[np.ix_(sees[0], range(128))] = False
+        good[np.ix_(sees[1], range(128, 256))] = False
+        assert np.all(np.isfinite(got[good])) and np.abs(got - want)[good].max() <= 1e-4
+
+
+@pytest.mark.parametrize("counts", [[6], [40]])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("tree", [False, True])
+def test_queries_that_are_not_finite(bad, counts, tree):
+    size = size_of(4, 2, 128, 16)
+    for form in FORMS:
+        d = q8.batch(16, [100], counts, form=form, tree=tree, **size)
+        want = expect(d, **size)
+        d["q"][3, 130] = bad  # head 1
+        got = attend(d, kernel=TENSOR, **size)
+        assert np.all(np.isnan(got[3, 128:256]))
+        got[3, 128:256] = want[3, 128:256]
+        check(got, want)
+
+
+@pytest.mark.parametrize("counts,tree", [([2, 1], False), ([40, 9], False), ([3, 4], True), ([40, 9], True)])
+def test_bad_pages(counts, tree):
+    """Page ids outside the pool stand for zeros, as do all of them where the pool has none."""
+    size = size_of(4, 2, 128, 16)
+    for form in FORMS:
+        d = q8.batch(7, [100, 60], counts, form=form, tree=tree, extra_cols=0, **size)
+        t = d["table"].copy()
+        t[0, 2], t[1, 0], t[0, 4] = 10 ** 6, -5, 2 ** 31 - 1
+        zero = len(d["k_pool"]) // 16
+        kf, vf = (np.concatenate([np.nan_to_num(d[x]), np.zeros((16, 256))]) for x in ("k_pool", "v_pool"))
+        want = ref.attention(d["q"], kf, vf, np.where((t < 0) | (t >= zero), zero, t), d["lens"], d["cu"], tree=d["tree"], **size)
+        d["table"] = t
+        for kernel in (CUDA, TENSOR):
+            check(attend(d, kernel=kernel, **size), want)
+        d["kc"], d["vc"], d["ks"], d["vs"] = (d[x][:0] for x in ("kc", "vc", "ks", "vs"))
+        want = ref.attention(d["q"], 0 * kf, 0 * vf, np.minimum(np.maximum(t, 0), 0), d["lens"], d["cu"], tree=d["tree"], **size)
+        check(attend(d, kernel=vtmu.VTMU_PAGED_AUTO, **size), want)
+
+
+@pytest.mark.parametrize("counts", [[5, 9, 2], [50, 33, 2]])
+def test_rows_past_max_rows_stay_as_they_were(counts):
+    size = size_of(4, 2, 64, 16)
+    for most in (1, counts[1] - 2):
+        d = q8.batch(9, [200, 90, 500], counts, form=q8.INT8, **size)
+        want = expect(d, **size)
+        for kernel in (CUDA, TENSOR):
+            got = attend(d, kernel=kernel, out=torch.full(d["q"].shape, 3.0, device="cuda"), maxRows=most, **size)
+            for b in range(3):
+                a, e = d["cu"][b], d["cu"][b + 1]
+                check(got[a:min(e, a + most)], want[a:min(e, a + most)])
+                assert np.all(got[min(e, a + most):e] == 3.0)
+
+
+def test_many_small_requests():
+    size = size_of(2, 1, 64, 16)
+    for counts in ([1] * 1024, [20] * 700 + [0] * 324):
+        d = q8.batch(12, [(7 * b) % 90 for b in range(1024)], counts, form=q8.E4M3, **size)
+        check(attend(d, kernel=TENSOR, **size), expect(d, **size))
+
+
+@pytest.mark.parametrize("counts,tree", [([3, 2], False), ([40, 30], False), ([3, 2], True), ([40, 30], True)])
+def test_same_call_gives_the_same_bits(counts, tree):
+    size = size_of(8, 2, 128, 16)
+    d = q8.batch(13, [5000, 3000], counts, form=q8.INT8, tree=tree, **size)
+    first = attend(d, kernel=TENSOR, **size)
+    for _ in range(4):
+        assert np.array_equal(attend(d, kernel=TENSOR, **size), first)
+
+
+@pytest.mark.parametrize("which", ["q", "kc", "vc", "out", "k_new", "ks"])
+def test_misaligned_tensors(which):
+    """They take the CUDA cores (scales off the 16-byte grid do not)."""
+    size = size_of(8, 4, 64, 16)
+    d = q8.batch(14, [150], [20], form=q8.E4M3, tree=True, **size)
+    want = expect(d, **size)
+
+    def shifted(t):
+        raw_ = torch.empty(t.numel() + 4, dtype=t.dtype, device="cuda")
+        return raw_[1:1 + t.numel()].view(t.shape).copy_(t)
+
+    ts = dict(q=dev(d["q"]), kc=codes(d["kc"], d["form"]), vc=codes(d["vc"], d["form"]), ks=dev(d["ks"]), out=torch.zeros(d["q"].shape, device="cuda"),
+              k_new=dev(d["tree"][0]))
+    ts[which] = shifted(ts[which])
+
+    def call(kernel):
+        return vtmu.paged_attention_q8(ts["q"], ts["kc"], ts["vc"], ts["ks"], dev(d["vs"]), dev(d["table"]), dev(d["lens"]),
+                                       dev(d["cu"]), tree=(ts["k_new"], *(dev(x) for x in d["tree"][1:])), maxRows=20,
+                                       kernel=kernel, out=ts["out"], **size)
+
+    check(call(vtmu.VTMU_PAGED_AUTO).cpu().numpy(), want)
+    if which != "ks":
+        with pytest.raises(vtmu.VtmuError) as e:
+            call(TENSOR)
+        assert e.value.status == vtmu.VTMU_ERR_UNSUPPORTED
+
+
+def test_offsets_past_32_bits():
+    """Pools of 4.3 GB of codes: written, read and attended over at their end."""
+    hk, D, P = 8, 128, 16
+    size = size_of(8, hk, D, P)
+    pages = (1 << 32) // (hk * D * P) + 40
+    d = q8.batch(15, [200, 330], [3, 2], form=q8.INT8, extra_cols=0, **size)
+    many = q8.batch(15, [200, 330], [30, 20], form=q8.INT8, extra_cols=0, **size)
+    kp, vp = (torch.zeros(pages * P, hk * D, dtype=torch.int8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(pages * P, hk, device="cuda") for _ in range(2))
+    used = len(d["ks"])
+    rows = slice(pages * P - used, pages * P)
+    up = pages - used // P
+    for x in (d, many):
+        kp[rows], vp[rows] = codes(x["kc"], q8.INT8), codes(x["vc"], q8.INT8)
+        ks[rows], vs[rows] = dev(x["ks"]), dev(x["vs"])
+        table = np.where(x["table"] >= 0, x["table"] + up, -1).astype(np.int32)
+        want = expect(x, **size)
+        for kernel in (CUDA, TENSOR):
+            got = vtmu.paged_attention_q8(dev(x["q"]), kp, vp, ks, vs, dev(table), dev(x["lens"]), dev(x["cu"]), kernel=kernel,
+                                          maxRows=int(np.diff(x["cu"]).max()), **size)
+            check(got.cpu().numpy(), want)
+    g = np.random.default_rng(2)
+    x = [g.standard_normal((2, hk * D), dtype=np.float32) for _ in range(2)]
+    slots = dev(np.array([pages * P - 1, pages * P - 7], np.int32))
+    vtmu.paged_write_q8(kp, vp, ks, vs, dev(x[0]), dev(x[1]), slots)
+    for y, new in zip(vtmu.paged_read_q8(kp, vp, ks, vs, slots), x):
+        want = q8.values(*q8.quantise(new, hk, q8.INT8), q8.INT8)
+        assert np.all(np.abs(y.cpu().numpy() - want) <= 2.0 ** -24 * np.abs(want))
+
+
+@pytest.mark.parametrize("counts,tree", [([3, 2], False), ([40, 30], False), ([3, 2], True), ([40, 30], True)])
+@pytest.mark.parametrize("given", [False, True])
+def test_captured_and_replayed_with_other_lengths(counts, tree, given):
+    """Two graphs of one workspace, replayed with other contents of the same buffers."""
+    size = size_of(8, 2, 128, 16)
+    cases = [q8.batch(50 + i, lens, counts, form=q8.INT8, tree=tree, extra_cols=0, **size)
+             for i, lens in enumerate(([900, 64], [1, 880], [300, 300]))]
+    pages, cols = max(len(d["ks"]) for d in cases), max(d["table"].shape[1] for d in cases)
+
+    def fit(d):
+        pad = lambda a, n, v: np.concatenate([a, np.full((n - len(a),) + a.shape[1:], v, a.dtype)])
+        table = np.full((2, cols), -1, np.int32)
+        table[:, :d["table"].shape[1]] = d["table"]
+        t = [dev(d["q"]), codes(pad(d["kc"], pages, 0), q8.INT8), codes(pad(d["vc"], pages, 0), q8.INT8),
+             dev(pad(d["ks"], pages, np.nan)), dev(pad(d["vs"], pages, np.nan)), dev(table), dev(d["lens"]), dev(d["cu"])]
+        return t + ([dev(x) for x in d["tree"]] if tree else [])
+
+    fitted = [fit(d) for d in cases]
+    static = [t.clone() for t in fitted[0]]
+    ws = vtmu.Workspace() if given else None
+    kw = dict(size, maxRows=max(counts), tree=tuple(static[8:]) if tree else None, workspace=ws)
+    if given:  # grown before the capture
+        vtmu.paged_attention_q8(*static[:8], **kw)
+    graphs = []
+    for _ in range(2):
+        out = torch.zeros_like(static[0])
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            vtmu.paged_attention_q8(*static[:8], out=out, **kw)
+        graphs.append((g, out))
+    for i in (1, 0, 2, 1):
+        for s, x in zip(static, fitted[i]):
+            s.copy_(x)
+        want = expect(cases[i], **size)
+        for g, out in graphs:
+            g.replay()
+            check(out.cpu().numpy(), want)
+    assert vtmu.vtmu_device_error() == 0
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_two_streams(given):
+    """Calls in flight together, few rows and many, with a workspace each or none."""
+    size = size_of(8, 2, 128, 16)
+    ds = [q8.batch(19 + i, [2000, 700], counts, form=q8.E4M3, tree=True, **size) for i, counts in enumerate(([2, 1], [3, 30]))]
+    streams = [torch.cuda.Stream() for _ in ds]
+    spaces = [vtmu.Workspace() if given else None for _ in ds]
+    ins = [([dev(d["q"]), codes(d["kc"], d["form"]), codes(d["vc"], d["form"])] + [dev(d[k]) for k in ("ks", "vs", "table", "lens", "cu")],
+            tuple(dev(x) for x in d["tree"])) for d in ds]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                outs[i].append(vtmu.paged_attention_q8(*ins[i][0], tree=ins[i][1], maxRows=30 if i else 2, workspace=spaces[i], **size))
+    torch.cuda.synchronize()
+    for i, d in enumerate(ds):
+        want = expect(d, **size)
+        for o in outs[i]:
+            check(o.cpu().numpy(), want)
+
+
+def test_a_captured_step():
+    """norm_rope, paged_write_q8, attention and paged_read_q8 of one token in a graph; the same bits as eager."""
+    H, hk, D, P, cols = 8, 2, 64, 16, 30
+    size = size_of(H, hk, D, P)
+    g = np.random.default_rng(4)
+    pages = 64
+    pools = [torch.zeros(pages * P, hk * D, dtype=torch.int8, device="cuda") for _ in range(2)]
+    pools += [torch.zeros(pages * P, hk, device="cuda") for _ in range(2)]
+    table = dev(g.permutation(pages)[:2 * cols].reshape(2, cols).astype(np.int32))
+    cu = dev(np.arange(3, dtype=np.int32))
+    q, k, v = (torch.zeros(2, n * D, device="cuda") for n in (H, hk, hk))
+    lens, pos, slots = (torch.zeros(2, dtype=torch.int32, device="cuda") for _ in range(3))
+
+    def step():
+        qt, kt = vtmu.norm_rope(q, k, pos, headDim=D)
+        vtmu.paged_write_q8(*pools, kt, v, slots)
+        out = vtmu.paged_attention_q8(qt, *pools, table, lens, cu, maxRows=1, **size)
+        return (out, *vtmu.paged_read_q8(*pools, slots))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = step()
+    for t in range(40):
+        for x in (q, k, v):
+            x.copy_(dev(g.standard_normal(x.shape, dtype=np.float32)))
+        pos.fill_(t)
+        lens.fill_(t + 1)
+        slots.copy_(table[:, t // P] * P + t % P)
+        before = [p.clone() for p in pools]
+        graph.replay()
+        one = [x.clone() for x in got]
+        after = [p.clone() for p in pools]
+        for p, x in zip(pools, before):
+            p.copy_(x)
+        two = step()
+        assert all(torch.equal(x, y) for x, y in zip(one + after, list(two) + pools))
+    assert vtmu.vtmu_device_error() == 0
 
 
 # ------------------------------------------------------------------ together

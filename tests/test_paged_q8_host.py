@@ -24,7 +24,7 @@ BOTH = [
     (dict(total=-1), INV, "bad size"), (dict(rows=-1), INV, "bad size"), (dict(hk=0), INV, "bad size"),
     (dict(d=0), INV, "bad size"), (dict(form=0), INV, "format 0"), (dict(form=3), INV, "format 3"),
     (dict(d=257), UNS, "257"), (dict(rows=1 << 31), UNS, "2^31"), (dict(total=1 << 31), UNS, "2^31"),
-    (dict(hk=1 << 25), UNS, "2^31"), (dict(rows=1 << 28, hk=8), UNS, "2^31"),
+    (dict(hk=1 << 25), UNS, "2^31"), (dict(hk=1 << 24), UNS, "2^30"), (dict(rows=1 << 28, hk=8), UNS, "2^31"),
     (dict(kp=None), INV, "NULL"), (dict(vs=None), INV, "NULL"), (dict(kn=None), INV, "NULL"),
     (dict(slots=None), INV, "NULL"), (dict(ks=A[2] + 2), INV, "aligned"), (dict(kn=A[4] + 1), INV, "aligned"),
     (dict(kn=A[0] + 64), INV, "overlaps"), (dict(vn=A[6]), INV, "overlaps"), (dict(vn=A[3]), INV, "overlaps"),
@@ -91,6 +91,32 @@ def test_no_workspace_for_the_cuda_cores(lib):  # noqa: F811
     assert vtmu.vtmu_paged_q8_workspace_size(params(head_dim=96)) == 0
 
 
+@host_only
+def test_workspaces_are_refused(lib):  # noqa: F811
+    for kw in (dict(), dict(max_rows=64, rows=64)):
+        p = params(**kw)
+        need = vtmu.vtmu_paged_q8_workspace_size(p)
+        assert need > 0
+        for ws, n in ((None, need), (A[9], need - 1), (A[9] + 128, need)):
+            e = _err(lambda: attend(p, ws=ws, nbytes=n))
+            assert e.status == WS, str(e)
+
+
+@host_only
+def test_forced_tensor_cores_are_refused(lib):  # noqa: F811
+    for kw in (dict(q=A[0] + 4), dict(k=A[1] + 8), dict(v=A[2] + 1), dict(out=A[8] + 4)):
+        e = _err(lambda: attend(params(kernel=2), **kw))
+        assert e.status == UNS and "16-byte" in str(e), str(e)
+    e = _err(lambda: vtmu.vtmu_paged_q8_workspace_size(params(kernel=2, pages=0)))
+    assert e.status == UNS
+
+
+def test_workspace_holds_the_drafted_rows_part(lib):  # noqa: F811
+    for rows in (16, 64):
+        more = [vtmu.vtmu_paged_q8_workspace_size(params(rows=n, max_rows=rows, tree=1)) for n in (64, 4096)]
+        assert more[1] >= more[0] + (4096 - 64) * 8
+
+
 def test_norm_rope_defaults(lib):  # noqa: F811
     p = vtmu.vtmu_norm_rope_params_init()
     assert (p.norm, p.axes, p.dealt, p.weight_offset, p.rope.base) == (1, 1, 0, 0.0, 0.0)  # base 0: 10000
@@ -111,7 +137,7 @@ def norm_rope(q=A[0], k=A[1], qw=A[2], kw=A[3], qo=A[4], ko=A[5], T=3, heads=4, 
     (dict(pos=None), INV, "must be given"), (dict(k=None), INV, "must be given"), (dict(kv=0), INV, "must be given"),
     (dict(q=A[0] + 2), INV, "aligned"), (dict(qo=A[0] + 16), INV, "overlaps"), (dict(qo=A[1]), INV, "overlaps"),
     (dict(ko=A[4]), INV, "overlaps"), (dict(ko=A[6]), INV, "overlaps"), (dict(qo=A[2]), INV, "overlaps"),
-    (dict(heads=1 << 25), UNS, "2^31"),
+    (dict(heads=1 << 25), UNS, "2^30"), (dict(heads=1 << 23, kv=1 << 23), UNS, "2^30"), (dict(T=1 << 31), UNS, "2^31"),
 ])
 def test_norm_rope_refusals(lib, kw, status, word):  # noqa: F811
     e = _err(lambda: norm_rope(**kw))
