@@ -48,11 +48,13 @@ __device__ unsigned int g_q8_tc_device_error;
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int kKT = 64, kM = 128, kThreads = 768, kConverters = 8;
-constexpr int kStages = 4;  // tiles of codes
-constexpr int kSlotsK = 3, kSlotsV = 4;  // tiles of f16
-constexpr int kScores = 4;  // S / P buffers: with two, S(n + 2) waited for P V(n), and a softmax warpgroup for it
-constexpr int kRing = 8;    // scales of a tile: stage n is loaded once V(n - 4) is converted, and so PV(n - 8) done
+constexpr int kKT = 128, kM = 128, kThreads = 768;
+constexpr int kStages = 2;      // tiles of codes
+constexpr int kSlots = 2;       // tiles of f16
+constexpr int kScores = 2;      // S / P buffers
+constexpr int kConverters = 4;  // warps that convert K; as many V
+constexpr int kRing = 8;   // scales of a tile: tile n is loaded once S(n - 4) is done, and so O(n - 6) issued
+constexpr int kStats = 4;  // a tile's maximum and sum: S(n) is issued once O(n - 3) is folded
 constexpr int kTiles = 16;  // what it is: the fold of a tile that far back may not have begun
 constexpr int kShift = 14;  // of weights in f16
 constexpr int kFar = 6;     // log2 by which a tile's scales may differ on the short way
@@ -78,14 +80,14 @@ struct TcArgs {
 template <int D>
 struct Cfg {
     static constexpr uint32_t kCodes = kKT * D, kTile = 2 * kCodes;  // bytes of a tile, as codes and as f16
-    static constexpr size_t kSmem = 1024 + (kSlotsK + kSlotsV) * kTile + kStages * 2 * kCodes + (kPagedMaxRequests + 1) * 8;
+    static constexpr size_t kSmem = 1024 + 2 * (kSlots * kTile + kStages * kCodes) + (kPagedMaxRequests + 1) * 8;
     static constexpr uint32_t kColQhi = 0, kColQlo = D / 2, kColS = D, kColO = D + kScores * kKT;
     static_assert(kColO + D <= 512, "TMEM budget");
     static_assert(kSmem + 24 * 1024 <= 232448, "shared memory budget");
 };
 
 struct Tile {
-    int b, rb, key, flags, hk, piece, rows, pad;  // rows: of the cache, from key on
+    int b, rb, key, flags, hk, piece, pad[2];
 };
 
 // A CTA's place in the list, for the producers.
@@ -146,7 +148,6 @@ struct Walk {
         t.hk = hk;
         t.piece = piece;
         t.key = (u < n_sink ? u : lo_tile + u - n_sink) * kKT;
-        t.rows = max(len - t.key, 0);
         t.flags = (first ? kFirst : 0) | (u + 1 == u1 ? kLast : 0) | (slot + 1) << kSlotShift;
         first = false;
         ++u;
@@ -158,8 +159,9 @@ struct Walk {
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool mn) {
     return (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// A tile's blocks of 64 channels, [64 rows][128 bytes] with the 128-byte swizzle, 8 KB apart.
+// A tile's blocks of 64 channels, [128 rows][128 bytes] with the 128-byte swizzle, kBlock bytes apart.
 // K-major: a row's channels along K.  MN-major: the rows are K, the next 64 channels a block on.
+constexpr uint32_t kBlock = kKT * 128;
 __device__ __forceinline__ uint64_t smem_desc(const void* tile, uint32_t next) {
     const uint64_t addr = smem_u32(tile);
     uint64_t d = (addr >> 4) & 0x3FFFull;
@@ -213,7 +215,28 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase, unsigned int
     return false;
 }
 
-// Codes of a tile to f16: eight warps, 8 rows each, a lane 16 codes at a time.  TMA leaves
+// Whether `other` is over while `bar` is not; false once `bar` is, or time ran out.
+__device__ __forceinline__ bool warp_wait_either(uint64_t* bar, int phase, uint64_t* other, int other_phase, unsigned int error) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (int i = 1;; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"((uint32_t)(phase & 1)), "r"(100u)  // ns
+            : "memory");
+        if (__all_sync(FULL, done != 0)) return false;
+        if (__all_sync(FULL, mbar_test(other, (uint32_t)(other_phase & 1)))) return true;
+        if ((i & 255) == 0) {
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            if (__any_sync(FULL, now - t0 > kWaitLimitNs)) return false;  // the wait on `bar` says so
+        }
+    }
+}
+
+// Codes of a tile to f16, 8 rows (the w-th) a warp at a time, 16 codes a lane.  TMA leaves
 // chunk c (16 bytes) of row r at c ^ (r % 8) (headDim 128; 64: where it was).  A quarter of the
 // warp takes 64 bytes of two rows; rows r and r ^ 5 (64: neighbours) meet no bank twice, neither
 // as codes nor in the f16 tile's swizzle.
@@ -230,17 +253,17 @@ __device__ __forceinline__ void convert(const unsigned char* codes, unsigned cha
         q8_halves<FORM>(x.y, h[2], h[3]);
         q8_halves<FORM>(x.z, h[4], h[5]);
         q8_halves<FORM>(x.w, h[6], h[7]);
-        unsigned char* to = tile + (c >> 2) * 8192 + row * 128;
+        unsigned char* to = tile + (c >> 2) * kBlock + row * 128;
         const int j = 2 * (c & 3);
         *reinterpret_cast<uint4*>(to + 16 * (j ^ sw)) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4*>(to + 16 * ((j + 1) ^ sw)) = make_uint4(h[4], h[5], h[6], h[7]);
     }
 }
-// Rows from `rows` on of a tile of value codes: what a page holds behind a request's last row may
-// be a NaN, which no weight of zero takes away.
+// Rows from `rows` on of a tile of value codes, a warp's 32: what a page holds behind a request's last
+// row may be a NaN, which no weight of zero takes away.
 template <int D>
 __device__ __noinline__ void clear_rows(unsigned char* codes, int rows, int w, int lane) {
-    for (int i = 8 * w * D + 16 * lane; i < 8 * (w + 1) * D; i += 512)
+    for (int i = 32 * w * D + 16 * lane; i < 32 * (w + 1) * D; i += 512)
         if (i / D >= rows) *reinterpret_cast<uint4*>(codes + i) = make_uint4(0, 0, 0, 0);
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // before the next tile's copies
     __syncwarp();
@@ -250,8 +273,9 @@ __device__ __noinline__ void clear_rows(unsigned char* codes, int rows, int w, i
 struct RowTile {
     uint32_t at;       // TMEM of its scores
     const float* ks;   // the keys' scales
-    uint64_t see;      // keys that it sees (not read when WHOLE)
+    uint64_t see0, see1;  // keys that it sees (not read when WHOLE)
     float rf, cap;     // a score of the MMA times ks rf is one in base-2 units (the argument of tanh with a cap)
+    __device__ uint32_t sees(int k) const { return (uint32_t)((k & 64 ? see1 : see0) >> (k & 63)); }  // from key k on
 };
 // 16 scores from key k0 on: in base-2 units with a cap, else still to be multiplied by rf.
 template <bool CAP, bool WHOLE>
@@ -266,7 +290,7 @@ __device__ __forceinline__ void row_scores(const RowTile& r, int k0, float (&x)[
     }
     if constexpr (CAP) softcap_tile<16>(x, r.rf, r.cap);
     if constexpr (!WHOLE) {
-        const uint32_t bits = (uint32_t)(r.see >> k0);
+        const uint32_t bits = r.sees(k0);
 #pragma unroll
         for (int k = 0; k < 16; ++k) x[k] = (bits >> k) & 1u ? x[k] : -INFINITY;
     }
@@ -306,7 +330,7 @@ __device__ __forceinline__ float2 row_softmax(const RowTile& r, const float* vn)
     for (int k0 = 0; k0 < kKT; k0 += 16) {
         float x[16];
         row_scores<CAP, WHOLE>(r, k0, x);
-        const uint32_t bits = (uint32_t)(r.see >> k0);
+        const uint32_t bits = WHOLE ? ~0u : r.sees(k0);
 #pragma unroll
         for (int k = 0; k < 16; k += 4) {
             const float4 v = *reinterpret_cast<const float4*>(vn + k0 + k);
@@ -345,7 +369,7 @@ __device__ __noinline__ float4 far_softmax(const RowTile r, const float* vs) {  
         for (int i = 1; i < 16; ++i) y = (k & 15) == i ? x[i] : y;
         y *= r.ks[k];
         if (CAP) y = r.cap * softcap_tanh(y * r.rf);
-        return (r.see >> k) & 1u ? y * mul : -INFINITY;
+        return r.sees(k) & 1u ? y * mul : -INFINITY;
     };
     float m = -INFINITY, top = -300.f, sum = 0.f;
 #pragma unroll 1
@@ -364,7 +388,7 @@ __device__ __noinline__ float4 far_softmax(const RowTile r, const float* vs) {  
             const float v = vs[k], e = power(v), y = score(k) - mu;
             const float part = v * (e > 0.f ? exp2f(-e) : exp2f(-e - 1.f) * 2.f);  // the scale's mantissa; 0 stays 0
             sum += fast_exp2(y);
-            const float u = (r.see >> k) & 1u ? fast_exp2(y + (e - top)) * part * (float)(1 << kShift) : 0.f;
+            const float u = r.sees(k) & 1u ? fast_exp2(y + (e - top)) * part * (float)(1 << kShift) : 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = (k & 15) == i ? u : w[i];
         }
@@ -381,20 +405,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* ktiles = tiles;
-    unsigned char* vtiles = tiles + kSlotsK * C::kTile;
-    unsigned char* codes = vtiles + kSlotsV * C::kTile;  // stage: K, V
+    unsigned char* vtiles = tiles + kSlots * C::kTile;
+    unsigned char* codes = vtiles + kSlots * C::kTile;  // stages of K, stages of V
     long long* prefix = reinterpret_cast<long long*>(codes + (size_t)kStages * 2 * C::kCodes);
-    __shared__ __align__(8) uint64_t staged[kStages], unstaged[kStages], k_ready[kSlotsK], k_free[kSlotsK],
-        v_ready[kSlotsV], v_free[kSlotsV], q_full, q_free, s_full[kScores], p_full[kScores], o_full, o_free;
+    __shared__ __align__(8) uint64_t staged[2][kStages], unstaged[2][kStages], ranged[kRing], k_ready[kSlots], k_free[kSlots],
+        v_ready[kSlots], v_free[kSlots], q_full, q_free, s_full[kScores], p_full[kScores], o_full, o_free;
     __shared__ uint32_t tmem_base_s;
     __shared__ long long scan_s[kThreads / 32];
     __shared__ __align__(16) float k_scale[kRing][kKT], v_scale[kRing][kKT], v_norm[kRing][kKT];
     __shared__ float v_back[kRing];              // 2^(E - kShift); 0: the scales differ too much
     __shared__ __align__(16) Tile tile_s[kTiles];
     __shared__ float q_back[4][kM];              // by piece: what the queries' power of two takes back
-    __shared__ float2 stat[kRing][kM];           // by tile: m, l
-    __shared__ float stat_back[kRing][kM];       // factor of its output
+    __shared__ float2 stat[kStats][kM];          // by tile: m, l
+    __shared__ float stat_back[kStats][kM];      // factor of its output
     __shared__ int piece_end[4];                 // by piece: the tile after it
+    __shared__ int v_rows[kRing];                // of a tile that there are, as V's producer knows; -1: the end
 
     const PagedDesc& a = g.a;
     const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -402,14 +427,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&staged[i], 2 * 33 + 1);  // two warps' bytes and scales, and what the tile is
-            mbar_init(&unstaged[i], kConverters);
+            for (int kv = 0; kv < 2; ++kv) {
+                mbar_init(&staged[kv][i], 33);  // bytes, and every lane's scales
+                mbar_init(&unstaged[kv][i], kConverters + kv);  // and the warp that takes the range of V's scales
+            }
         }
-        for (int i = 0; i < kSlotsK; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
             mbar_init(&k_ready[i], kConverters);
             mbar_init(&k_free[i], 1);
-        }
-        for (int i = 0; i < kSlotsV; ++i) {
             mbar_init(&v_ready[i], kConverters);
             mbar_init(&v_free[i], 1);
         }
@@ -417,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
         }
+        for (int i = 0; i < kRing; ++i) mbar_init(&ranged[i], 1);
         mbar_init(&o_full, 1);
         mbar_init(&o_free, 4);
         mbar_init(&q_free, 2);  // the MMAs' commit, and an arrival that publishes piece_end
@@ -471,7 +497,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     g.part_l[part_row(slot, i)] = 0.f;
                 }
             };
-            const uint8_t* pool = values ? g.p.v : g.p.k;
             const float* scales = values ? g.p.v_scale : g.p.k_scale;
             // 32 boxes of a request are looked up at a time, a lane each: the first row of each in the
             // pool, -1 for rows of no page.
@@ -481,23 +506,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool stop = !walk.next(a, prefix, t, empty);
                 if (stop) t.flags = kStop;
                 const int st = n % kStages;
-                if (n >= kStages && !warp_wait(&unstaged[st], n / kStages - 1, kErrQ8Free)) break;
-                if (!values && lane == 0) {
-                    tile_s[n % kTiles] = t;
-                    if (stop) tile_s[(n + 1) % kTiles] = t;  // for the other softmax warps
-                    mbar_arrive(&staged[st]);
+                if (n >= kStages && !warp_wait(&unstaged[values][st], n / kStages - 1, kErrQ8Free)) break;
+                if (lane == 0) {
+                    if (values) {
+                        v_rows[n % kRing] = stop ? -1 : max(walk.len - t.key, 0);
+                    } else {
+                        tile_s[n % kTiles] = t;
+                        if (stop) tile_s[(n + 1) % kTiles] = t;  // for the other softmax warps
+                    }
+                    mbar_arrive_expect_tx(&staged[values][st], stop ? 0u : C::kCodes);
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&staged[st], stop ? 0u : C::kCodes);
                 __syncwarp();
                 if (!stop) {
                     if (t.piece != of_piece) batch = -1;
                     of_piece = t.piece;
-                    unsigned char* to = codes + (size_t)(2 * st + (values ? 1 : 0)) * C::kCodes;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int q0 = (t.key + 32 * j) >> g.sub_shift;  // the half's first box
-                        if ((q0 >> 5) != batch) {
-                            batch = q0 >> 5;
+                    unsigned char* to = codes + (size_t)(st + (values ? kStages : 0)) * C::kCodes;
+                    float* to_scale = (values ? v_scale : k_scale)[n % kRing];
+                    const int boxes = kKT >> g.sub_shift, q0 = t.key >> g.sub_shift;
+#pragma unroll 1
+                    for (int c = 0; c < boxes; c += 32) {
+                        if (((q0 + c) >> 5) != batch) {
+                            batch = (q0 + c) >> 5;
                             const int row = ((batch << 5) + lane) << g.sub_shift;
                             y_cur = -1;
                             if (row < walk.len) {
@@ -506,18 +535,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if ((unsigned)page < (unsigned)a.pages) y_cur = page * a.page_size + (row - col * a.page_size);
                             }
                         }
-                        const int r = lane + 32 * j, key = t.key + r, in = key & ((1 << g.sub_shift) - 1);
-                        const int y = __shfl_sync(FULL, y_cur, (key >> g.sub_shift) & 31);
                         // Rows of no page are out of bounds: zeros.
-                        if (in == 0)
-                            tma_load_2d(to + r * D, values ? &tm_v : &tm_k, t.hk * D, y < 0 ? (int)(a.pages * a.page_size) : y,
-                                        &staged[st]);
-                        const bool there = y >= 0 && key < walk.len;
-                        const int64_t at = (int64_t)(there ? y + in : 0) * a.Hk + t.hk;
-                        cp_async4((values ? v_scale : k_scale)[n % kRing] + r, scales + at, there ? 4 : 0);
+                        const int y = __shfl_sync(FULL, y_cur, (q0 + lane) & 31);
+                        if (lane < boxes)
+                            tma_load_2d(to + ((c + lane) << g.sub_shift) * D, values ? &tm_v : &tm_k, t.hk * D,
+                                        y < 0 ? (int)(a.pages * a.page_size) : y, &staged[values][st]);
+                        const int keys = min(kKT, 32 << g.sub_shift);  // of these boxes
+                        for (int k = (c << g.sub_shift) + lane; k < (c << g.sub_shift) + keys; k += 32) {
+                            const int key = t.key + k;
+                            const int first = __shfl_sync(FULL, y_cur, (key >> g.sub_shift) & 31);
+                            const bool there = first >= 0 && key < walk.len;
+                            const int64_t at = there ? (int64_t)(first + (key & ((1 << g.sub_shift) - 1))) * a.Hk + t.hk : 0;
+                            cp_async4(to_scale + k, scales + at, there ? 4 : 0);
+                        }
                     }
                 }
-                cp_async_arrive(&staged[st]);
+                cp_async_arrive(&staged[values][st]);
                 if (stop) break;
             }
             cp_async_wait_all();  // no copy may be in flight when the CTA exits
@@ -525,10 +558,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                 g.head[2 * blockIdx.x] = walk.starts;
                 g.head[2 * blockIdx.x + 1] = make_int4(walk.starts_head, 0, 0, 0);
             }
+        } else if (warp == 3) {
+            // ---- the range of a tile's value scales ----------------------------------------
+            for (int n = 0;; ++n) {
+                const int st = n % kStages, rg = n % kRing;
+                if (!warp_wait(&staged[1][st], n / kStages, kErrQ8Load)) break;
+                const bool stop = v_rows[rg] < 0;
+                const float* vs = v_scale[rg];
+                if (stop) break;
+                float v[4];
+                uint32_t most = 0, least = ~0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = vs[lane + 32 * i];
+                    const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
+                    most = max(most, b);
+                    least = min(least, b ? b : ~0u);
+                }
+                most = __reduce_max_sync(FULL, most);
+                least = __reduce_min_sync(FULL, least);
+                // E, where 2^(kShift - E) and its inverse are normal numbers (a tile whose scales are all below
+                // 2^-110 keeps 23 bits of its largest weight).
+                int e = (int)(most >> 23) - 127;
+                const bool far = e > 110 || (most > least && most - least > (uint32_t)kFar << 23);
+                e = e < -110 ? -110 : e > 110 ? 110 : e;
+                const float up = __uint_as_float((uint32_t)(127 + kShift - e) << 23);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v_norm[rg][lane + 32 * i] = v[i] * up;
+                if (lane == 0) v_back[rg] = far ? 0.f : __uint_as_float((uint32_t)(127 - kShift + e) << 23);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&ranged[rg]);
+                    mbar_arrive(&unstaged[1][st]);
+                }
+            }
         } else if (warp == 1) {
             // ---- MMAs ---------------------------------------------------------------------
             constexpr uint32_t id_s = idesc_f16(kM, kKT, false), id_o = idesc_f16(kM, D, true);
-            const uint64_t k0 = smem_desc(ktiles, 16), v0 = smem_desc(vtiles, 8192);
+            const uint64_t k0 = smem_desc(ktiles, 16), v0 = smem_desc(vtiles, kBlock);
             const uint32_t k_lo = (uint32_t)k0, k_hi = (uint32_t)(k0 >> 32), v_lo = (uint32_t)v0, v_hi = (uint32_t)(v0 >> 32);
             // S runs up to kScores tiles ahead of P V, but does not wait for its keys or queries while there
             // is a P V to issue.
@@ -537,11 +604,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (;;) {
                 if (!end && sn - vn < kScores) {
                     const bool must = sn == vn;
-                    const int st = sn % kSlotsK;
+                    const int st = sn % kSlots;
                     if (!k_ok) {
-                        k_ok = __all_sync(FULL, mbar_test(&k_ready[st], (uint32_t)((sn / kSlotsK) & 1)));
+                        k_ok = __all_sync(FULL, mbar_test(&k_ready[st], (uint32_t)((sn / kSlots) & 1)));
                         if (!k_ok && must) {
-                            k_ok = warp_wait(&k_ready[st], sn / kSlotsK, kErrQ8Mma);
+                            k_ok = warp_wait(&k_ready[st], sn / kSlots, kErrQ8Mma);
                             if (!k_ok) break;
                         }
                     }
@@ -568,13 +635,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 // scheduler, and with loops and 64-bit sums S took 1500 cycles to issue.
 #pragma unroll
                                 for (int i = 0; i < D / 16; ++i) {
-                                    const uint32_t at = k + (i >> 2) * (8192 >> 4) + 2 * (i & 3);
+                                    const uint32_t at = k + (i >> 2) * (kBlock >> 4) + 2 * (i & 3);
                                     if (i == 0) mma_f16_ts<false>(d, tmem + C::kColQlo, at, k_hi, id_s);
                                     else mma_f16_ts<true>(d, tmem + C::kColQlo + 8 * i, at, k_hi, id_s);
                                 }
 #pragma unroll
                                 for (int i = 0; i < D / 16; ++i)
-                                    mma_f16_ts<true>(d, tmem + C::kColQhi + 8 * i, k + (i >> 2) * (8192 >> 4) + 2 * (i & 3), k_hi, id_s);
+                                    mma_f16_ts<true>(d, tmem + C::kColQhi + 8 * i, k + (i >> 2) * (kBlock >> 4) + 2 * (i & 3), k_hi, id_s);
                                 mma_commit(&k_free[st]);
                                 mma_commit(&s_full[sn % kScores]);
                                 if (flags & kLast) {
@@ -591,8 +658,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (vn < sn) {  // O(vn) = P(vn) V(vn)
-                    const int bf = vn % kScores, st = vn % kSlotsV;
-                    if (!warp_wait(&p_full[bf], vn / kScores, kErrQ8Mma) || !warp_wait(&v_ready[st], vn / kSlotsV, kErrQ8Mma) ||
+                    const int bf = vn % kScores, st = vn % kSlots;
+                    if (!end && sn - vn < kScores) {
+                        // Whichever comes first: these weights, or what the next S lacks.
+                        uint64_t* other = k_ok ? &q_full : &k_ready[sn % kSlots];
+                        const int phase = k_ok ? tile_s[sn % kTiles].piece : sn / kSlots;
+                        if (warp_wait_either(&p_full[bf], vn / kScores, other, phase, kErrQ8Mma)) continue;
+                    }
+                    if (!warp_wait(&p_full[bf], vn / kScores, kErrQ8Mma) || !warp_wait(&v_ready[st], vn / kSlots, kErrQ8Mma) ||
                         (vn > 0 && !warp_wait(&o_free, vn - 1, kErrQ8Mma)))
                         break;
                     tc_fence_after();
@@ -685,8 +758,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (must && !free && !(free = warp_wait(&q_free, loaded, kErrQ8Mma))) break;
                 if (free) {
                     const int e = piece_end[loaded & 3];
-                    bool known = __all_sync(FULL, mbar_test(&k_ready[e % kSlotsK], (uint32_t)((e / kSlotsK) & 1)));
-                    if (must && !known && !(known = warp_wait(&k_ready[e % kSlotsK], e / kSlotsK, kErrQ8Mma))) break;
+                    bool known = __all_sync(FULL, mbar_test(&k_ready[e % kSlots], (uint32_t)((e / kSlots) & 1)));
+                    if (must && !known && !(known = warp_wait(&k_ready[e % kSlots], e / kSlots, kErrQ8Mma))) break;
                     if (known) {
                         tc_fence_after();
                         loaded = load_queries(e) ? loaded + 1 : -1;
@@ -697,12 +770,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const Tile t = tile_s[n % kTiles];
             if (t.flags & kStop) break;
-            const float2 st = stat[n % kRing][i];
+            const float2 st = stat[n % kStats][i];
             const float Mn = fmaxf(M, st.x), mu = Mn == -INFINITY ? 0.f : Mn;
             const float alpha = fast_exp2(M - mu), beta = fast_exp2(st.x - mu);
             M = Mn;
             L = fmaf(L, alpha, st.y * beta);
-            const float bo = beta * stat_back[n % kRing][i];
+            const float bo = beta * stat_back[n % kStats][i];
             if (__any_sync(FULL, alpha != 1.f)) {  // a maximum moved
                 const uint64_t al = f2_pack(alpha, alpha);
 #pragma unroll
@@ -791,13 +864,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             RowTile rt;
             rt.at = tmem + lanes + C::kColS + (n % kScores) * kKT;
             rt.ks = k_scale[n % kRing];
-            rt.see = ~0ull;
+            rt.see0 = rt.see1 = ~0ull;
             rt.rf = q_back[piece & 3][i];
             rt.cap = a.cap_log2;
             if (!all) {
                 auto below = [](int c) -> uint64_t { return c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1; };
-                rt.see = below(hi - t.key + 1) & (~below(lo - t.key) | below(sinks - t.key));
+                auto from = [&](int k) -> uint64_t { return below(hi - k + 1) & (~below(lo - k) | below(sinks - k)); };
+                rt.see0 = from(t.key);
+                rt.see1 = from(t.key + 64);
             }
+            if (!warp_wait(&ranged[n % kRing], n / kRing, kErrQ8Load)) break;
             const float back = v_back[n % kRing];
             float2 ml;
             float factor = back;
@@ -808,8 +884,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 ml = whole ? row_softmax<CAP, true>(rt, v_norm[n % kRing]) : row_softmax<CAP, false>(rt, v_norm[n % kRing]);
             }
-            stat[n % kRing][i] = ml;
-            stat_back[n % kRing][i] = factor;
+            stat[n % kStats][i] = ml;
+            stat_back[n % kStats][i] = factor;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -818,46 +894,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ---- codes to f16 ------------------------------------------------------------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        const int w = warp - 16;
+        // Four warps for K, four for V.  Short loops on purpose: six warps with code of their own share a
+        // scheduler, and unrolled roles ran at the rate of instruction fetches.
+        const int kv = warp >= 20, w = warp & 3;
+        uint64_t *ready = kv ? v_ready : k_ready, *freed = kv ? v_free : k_free;
         for (int n = 0;; ++n) {
-            const int st = n % kStages, kl = n % kSlotsK, vl = n % kSlotsV, rg = n % kRing;
-            if (!warp_wait(&staged[st], n / kStages, kErrQ8Load)) break;
-            const bool stop = tile_s[n % kTiles].flags & kStop;
-            if (n >= kSlotsK && !warp_wait(&k_free[kl], n / kSlotsK - 1, kErrQ8Free)) break;
-            if (stop) {
-                if (lane == 0) mbar_arrive(&k_ready[kl]);
+            const int st = n % kStages, sl = n % kSlots;
+            if (!warp_wait(&staged[kv][st], n / kStages, kErrQ8Load)) break;
+            const int rows = kv ? v_rows[n % kRing] : tile_s[n % kTiles].flags & kStop ? -1 : kKT;
+            if (n >= kSlots && !warp_wait(&freed[sl], n / kSlots - 1, kErrQ8Free)) break;
+            if (rows < 0) {
+                if (lane == 0) mbar_arrive(&ready[sl]);
                 break;
             }
-            if (w == 0) {  // the range of the values' scales
-                const float v0 = v_scale[rg][lane], v1 = v_scale[rg][lane + 32];
-                const uint32_t b0 = __float_as_uint(v0) & 0x7fffffffu, b1 = __float_as_uint(v1) & 0x7fffffffu;
-                const uint32_t most = __reduce_max_sync(FULL, max(b0, b1));
-                const uint32_t least = __reduce_min_sync(FULL, min(b0 ? b0 : ~0u, b1 ? b1 : ~0u));
-                // E, where 2^(kShift - E) and its inverse are normal numbers (a tile whose scales are all below
-                // 2^-110 keeps 23 bits of its largest weight).
-                int e = (int)(most >> 23) - 127;
-                const bool far = e > 110 || (most > least && most - least > (uint32_t)kFar << 23);
-                e = e < -110 ? -110 : e > 110 ? 110 : e;
-                const float up = __uint_as_float((uint32_t)(127 + kShift - e) << 23);
-                v_norm[rg][lane] = v0 * up;
-                v_norm[rg][lane + 32] = v1 * up;
-                if (lane == 0) v_back[rg] = far ? 0.f : __uint_as_float((uint32_t)(127 - kShift + e) << 23);
-            }
-            // Short loops on purpose, K and V through the same code: six warps with code of their own share
-            // a scheduler, and unrolled roles ran at the rate of instruction fetches.
-            bool ok = true;
+            unsigned char* from = codes + (size_t)(st + kv * kStages) * C::kCodes;
+            unsigned char* to = (kv ? vtiles : ktiles) + sl * C::kTile;
+            if (FORM == kFormE4m3 && rows < kKT) clear_rows<D>(from, rows, w, lane);
 #pragma unroll 1
-            for (int kv = 0; kv < 2 && ok; ++kv) {
-                if (kv) ok = n < kSlotsV || warp_wait(&v_free[vl], n / kSlotsV - 1, kErrQ8Free);
-                if (FORM == kFormE4m3 && kv && tile_s[n % kTiles].rows < kKT)
-                    clear_rows<D>(codes + (size_t)(2 * st + 1) * C::kCodes, tile_s[n % kTiles].rows, w, lane);
-                convert<D, FORM>(codes + (size_t)(2 * st + kv) * C::kCodes, kv ? vtiles + vl * C::kTile : ktiles + kl * C::kTile, w, lane);
-                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
-                __syncwarp();
-                if (lane == 0) mbar_arrive(kv ? &v_ready[vl] : &k_ready[kl]);
+            for (int i = 0; i < 4; ++i) convert<D, FORM>(from, to, 4 * w + i, lane);
+            asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&unstaged[kv][st]);
+                mbar_arrive(&ready[sl]);
             }
-            if (!ok) break;
-            if (lane == 0) mbar_arrive(&unstaged[st]);
         }
     }
 
@@ -990,7 +1050,7 @@ cudaError_t launch_form(const PagedDesc& a, const Q8Pools& p, int num_sms, void*
     g.head = reinterpret_cast<int4*>(ws + s.head);
     float2* draft = reinterpret_cast<float2*>(ws + s.draft);
     g.draft = draft;
-    while ((1 << g.sub_shift) < kKT && a.page_size % (2 << g.sub_shift) == 0) ++g.sub_shift;
+    while ((1 << g.sub_shift) < 64 && a.page_size % (2 << g.sub_shift) == 0) ++g.sub_shift;
     const int sub = 1 << g.sub_shift;
     CUtensorMap tk, tv;
     if (!encode_rows<D>(&tk, p.k, a.pages * a.page_size, (int64_t)a.Hk * D, sub) ||
