@@ -48,12 +48,14 @@ __device__ unsigned int g_q8_tc_device_error;
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int kKT = 128, kM = 128, kThreads = 768;
+constexpr int kKT = 128, kHalf = 64;  // keys of a tile, and of a softmax warp's half
+constexpr int kM = 128, kThreads = 768;
 constexpr int kStages = 2;      // tiles of codes
 constexpr int kSlots = 2;       // tiles of f16
 constexpr int kScores = 2;      // S / P buffers
 constexpr int kConverters = 4;  // warps that convert K; as many V
-constexpr int kRing = 8;   // scales of a tile: tile n is loaded once S(n - 4) is done, and so O(n - 6) issued
+constexpr int kRing = 8;   // scales of K: tile n is loaded once S(n - 4) is done, and so O(n - 6) issued
+constexpr int kRingV = 4;  // of V: once O(n - 4) is done
 constexpr int kStats = 4;  // a tile's maximum and sum: S(n) is issued once O(n - 3) is folded
 constexpr int kTiles = 16;  // what it is: the fold of a tile that far back may not have begun
 constexpr int kShift = 14;  // of weights in f16
@@ -215,49 +217,56 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase, unsigned int
     return false;
 }
 
-// Whether `other` is over while `bar` is not; false once `bar` is, or time ran out.
-__device__ __forceinline__ bool warp_wait_either(uint64_t* bar, int phase, uint64_t* other, int other_phase, unsigned int error) {
+// Three at once: a look at each takes as long as one.
+__device__ __forceinline__ bool warp_wait3(uint64_t* a, int pa, uint64_t* b, int pb, uint64_t* c, int pc, unsigned int error) {
+    const uint32_t xa = smem_u32(a), xb = smem_u32(b), xc = smem_u32(c);
+    const uint32_t ya = (uint32_t)(pa & 1), yb = (uint32_t)(pb & 1), yc = (uint32_t)(pc & 1);
     uint64_t t0 = 0;
+    uint32_t done = 0;
 #pragma unroll 1
     for (int i = 1;; ++i) {
-        uint32_t done;
         asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+            "{\n .reg .pred p, q, r;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            " mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n"
+            " and.pred p, p, q;\n and.pred p, p, r;\n selp.u32 %0, 1, 0, p;\n}\n"
             : "=r"(done)
-            : "r"(smem_u32(bar)), "r"((uint32_t)(phase & 1)), "r"(100u)  // ns
+            : "r"(xa), "r"(ya), "r"(xb), "r"(yb), "r"(xc), "r"(yc)
             : "memory");
-        if (__all_sync(FULL, done != 0)) return false;
-        if (__all_sync(FULL, mbar_test(other, (uint32_t)(other_phase & 1)))) return true;
-        if ((i & 255) == 0) {
+        if (__all_sync(FULL, done != 0)) return true;
+        if ((i & 1023) == 0) {
             const uint64_t now = global_ns();
             if (t0 == 0) t0 = now;
-            if (__any_sync(FULL, now - t0 > kWaitLimitNs)) return false;  // the wait on `bar` says so
+            if (__any_sync(FULL, now - t0 > kWaitLimitNs)) break;
         }
     }
+    raise_device_error(&g_q8_tc_device_error, error);
+    return false;
 }
 
-// Codes of a tile to f16, 8 rows (the w-th) a warp at a time, 16 codes a lane.  TMA leaves
+// Codes of a tile to f16: four warps, 32 rows each, a lane 16 codes at a time.  TMA leaves
 // chunk c (16 bytes) of row r at c ^ (r % 8) (headDim 128; 64: where it was).  A quarter of the
 // warp takes 64 bytes of two rows; rows r and r ^ 5 (64: neighbours) meet no bank twice, neither
-// as codes nor in the f16 tile's swizzle.
+// as codes nor in the f16 tile's swizzle.  A lane's places in 8 rows are its places in the next 8.
 template <int D, int FORM>
 __device__ __forceinline__ void convert(const unsigned char* codes, unsigned char* tile, int w, int lane) {
     const int sub = lane & 7, q = lane >> 3;
+    const int row = 32 * w + (D == 128 ? q ^ (sub & 4 ? 5 : 0) : 2 * q + (sub >> 2));
+    const int c = sub & 3, sw = row & 7, j = 2 * c;  // 16 codes; the other 64 channels' are 4 chunks on
+    const unsigned char* from = codes + row * D;
+    unsigned char* to = tile + row * 128;
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        const int row = 8 * w + (D == 128 ? q ^ (sub & 4 ? 5 : 0) : 2 * q + (sub >> 2));
-        const int c = (sub & 3) + 4 * i, sw = row & 7;
-        const uint4 x = *reinterpret_cast<const uint4*>(codes + row * D + 16 * (D == 128 ? c ^ sw : c));
-        uint32_t h[8];
-        q8_halves<FORM>(x.x, h[0], h[1]);
-        q8_halves<FORM>(x.y, h[2], h[3]);
-        q8_halves<FORM>(x.z, h[4], h[5]);
-        q8_halves<FORM>(x.w, h[6], h[7]);
-        unsigned char* to = tile + (c >> 2) * kBlock + row * 128;
-        const int j = 2 * (c & 3);
-        *reinterpret_cast<uint4*>(to + 16 * (j ^ sw)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(to + 16 * ((j + 1) ^ sw)) = make_uint4(h[4], h[5], h[6], h[7]);
-    }
+    for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+        for (int r = 0; r < 32; r += 8) {
+            const uint4 x = *reinterpret_cast<const uint4*>(from + 16 * (D == 128 ? (c + 4 * i) ^ sw : c) + r * D);
+            uint32_t h[8];
+            q8_halves<FORM>(x.x, h[0], h[1]);
+            q8_halves<FORM>(x.y, h[2], h[3]);
+            q8_halves<FORM>(x.z, h[4], h[5]);
+            q8_halves<FORM>(x.w, h[6], h[7]);
+            *reinterpret_cast<uint4*>(to + 16 * (j ^ sw) + i * kBlock + r * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(to + 16 * ((j + 1) ^ sw) + i * kBlock + r * 128) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
 }
 // Rows from `rows` on of a tile of value codes, a warp's 32: what a page holds behind a request's last
 // row may be a NaN, which no weight of zero takes away.
@@ -269,13 +278,12 @@ __device__ __noinline__ void clear_rows(unsigned char* codes, int rows, int w, i
     __syncwarp();
 }
 
-// What a softmax thread needs of its row and tile.
+// What a softmax thread needs of its row and its half of a tile.
 struct RowTile {
     uint32_t at;       // TMEM of its scores
     const float* ks;   // the keys' scales
-    uint64_t see0, see1;  // keys that it sees (not read when WHOLE)
+    uint64_t see;      // keys that it sees (not read when WHOLE)
     float rf, cap;     // a score of the MMA times ks rf is one in base-2 units (the argument of tanh with a cap)
-    __device__ uint32_t sees(int k) const { return (uint32_t)((k & 64 ? see1 : see0) >> (k & 63)); }  // from key k on
 };
 // 16 scores from key k0 on: in base-2 units with a cap, else still to be multiplied by rf.
 template <bool CAP, bool WHOLE>
@@ -290,7 +298,7 @@ __device__ __forceinline__ void row_scores(const RowTile& r, int k0, float (&x)[
     }
     if constexpr (CAP) softcap_tile<16>(x, r.rf, r.cap);
     if constexpr (!WHOLE) {
-        const uint32_t bits = r.sees(k0);
+        const uint32_t bits = (uint32_t)(r.see >> k0);
 #pragma unroll
         for (int k = 0; k < 16; ++k) x[k] = (bits >> k) & 1u ? x[k] : -INFINITY;
     }
@@ -307,30 +315,36 @@ __device__ __forceinline__ void store_weights(uint32_t at, const float* w) {
     }
     tmem_st16(at, y);
 }
-// The row's largest score m, and weights 2^(x2 - m) vn over its scores (vn: the values' scales
-// times 2^(kShift - E)); returns m and the sum of the exponentials.
+// The row's largest score of the half, in base-2 units; leaves the masked scores as row_scores makes them.
 // Short loops on purpose: the roles' code has to stay in the instruction cache together (with
-// this one unrolled over all 64 scores large trees took 695 us instead of 613).
+// these unrolled large trees took 695 us instead of 613).
 template <bool CAP, bool WHOLE>
-__device__ __forceinline__ float2 row_softmax(const RowTile& r, const float* vn) {
+__device__ __forceinline__ float row_max(const RowTile& r) {
     float m = -INFINITY;
 #pragma unroll 1
-    for (int k0 = 0; k0 < kKT; k0 += 16) {
+    for (int k0 = 0; k0 < kHalf; k0 += 16) {
         float x[16];
         row_scores<CAP, WHOLE>(r, k0, x);
+        tmem_st16(r.at + k0, x);
 #pragma unroll
         for (int k = 0; k < 16; k += 2) m = fmaxf(fmaxf(m, x[k]), x[k + 1]);
     }
+    tmem_wait_st();
+    return CAP ? m : m * r.rf;
+}
+// Weights 2^(x2 - mu) vn over its scores (vn: the values' scales times 2^(kShift - E)); returns the
+// sum of the exponentials.
+template <bool CAP, bool WHOLE>
+__device__ __forceinline__ float row_weights(const RowTile& r, const float* vn, float mu) {
     const float mul = CAP ? 1.f : r.rf;
-    m *= mul;
-    const float mu = m == -INFINITY ? 0.f : m;
     const uint64_t mul2 = f2_pack(mul, mul), sub2 = f2_pack(-mu, -mu);
     uint64_t sum = 0;
 #pragma unroll 1
-    for (int k0 = 0; k0 < kKT; k0 += 16) {
+    for (int k0 = 0; k0 < kHalf; k0 += 16) {
         float x[16];
-        row_scores<CAP, WHOLE>(r, k0, x);
-        const uint32_t bits = WHOLE ? ~0u : r.sees(k0);
+        tmem_ld16(r.at + k0, x);
+        tmem_wait_ld();
+        const uint32_t bits = (uint32_t)(r.see >> k0);
 #pragma unroll
         for (int k = 0; k < 16; k += 4) {
             const float4 v = *reinterpret_cast<const float4*>(vn + k0 + k);
@@ -352,49 +366,35 @@ __device__ __forceinline__ float2 row_softmax(const RowTile& r, const float* vn)
     }
     float a, b;
     f2_unpack(sum, a, b);
-    return make_float2(m, a + b);
+    return a + b;
 }
 // The same with scales of very different size: relative to the row's largest product
-// 2^(x2 - mu) 2^e, e the scales' exponents.  Returns the sum, and that product's exponent.
-template <bool CAP>
-__device__ __noinline__ float4 far_softmax(const RowTile r, const float* vs) {  // m, sum, exponent
+// 2^(x2 - mu) 2^e, e the scales' exponents.  WEIGHTS = false: that product's exponent in the half,
+// true: the weights times 2^(kShift - top), and the sum.
+template <bool CAP, bool WEIGHTS>
+__device__ __forceinline__ float far_softmax(const RowTile r, const float* vs, float mu, float top) {
     auto power = [](float v) -> float { return (float)((int)((__float_as_uint(v) >> 23) & 255u) - 127); };
     const float mul = CAP ? 1.f : r.rf;
-    auto score = [&](int k) -> float {  // one at a time: code this rare stays short
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < kHalf; c += 16) {
         float x[16];
-        tmem_ld16(r.at + (k & ~15), x);
+        tmem_ld16(r.at + c, x);
         tmem_wait_ld();
-        float y = x[0];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) y = (k & 15) == i ? x[i] : y;
-        y *= r.ks[k];
-        if (CAP) y = r.cap * softcap_tanh(y * r.rf);
-        return r.sees(k) & 1u ? y * mul : -INFINITY;
-    };
-    float m = -INFINITY, top = -300.f, sum = 0.f;
-#pragma unroll 1
-    for (int k = 0; k < kKT; ++k) m = fmaxf(m, score(k));
-    const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-    for (int k = 0; k < kKT; ++k) top = fmaxf(top, (score(k) - mu) + power(vs[k]));
-    top = ceilf(fminf(top, 126.f));
-#pragma unroll 1
-    for (int c = 0; c < kKT; c += 16) {
-        float w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = 0.f;
-#pragma unroll 1
-        for (int k = c; k < c + 16; ++k) {
-            const float v = vs[k], e = power(v), y = score(k) - mu;
-            const float part = v * (e > 0.f ? exp2f(-e) : exp2f(-e - 1.f) * 2.f);  // the scale's mantissa; 0 stays 0
-            sum += fast_exp2(y);
-            const float u = r.sees(k) & 1u ? fast_exp2(y + (e - top)) * part * (float)(1 << kShift) : 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = (k & 15) == i ? u : w[i];
+        for (int i = 0; i < 16; ++i) {
+            const float v = vs[c + i], e = power(v), y = x[i] * mul - mu;
+            if constexpr (!WEIGHTS) {
+                top = fmaxf(top, y + e);
+            } else {
+                const float part = v * (e > 0.f ? exp2f(-e) : exp2f(-e - 1.f) * 2.f);  // the scale's mantissa; 0 stays 0
+                sum += fast_exp2(y);
+                x[i] = (r.see >> (c + i)) & 1u ? fast_exp2(y + (e - top)) * part * (float)(1 << kShift) : 0.f;
+            }
         }
-        store_weights(r.at + c, w);
+        if constexpr (WEIGHTS) store_weights(r.at + c, x);
     }
-    return make_float4(m, sum, top, 0.f);
+    return WEIGHTS ? sum : top;
 }
 
 template <int D, int FORM, bool CAP>
@@ -408,18 +408,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char* vtiles = tiles + kSlots * C::kTile;
     unsigned char* codes = vtiles + kSlots * C::kTile;  // stages of K, stages of V
     long long* prefix = reinterpret_cast<long long*>(codes + (size_t)kStages * 2 * C::kCodes);
-    __shared__ __align__(8) uint64_t staged[2][kStages], unstaged[2][kStages], ranged[kRing], k_ready[kSlots], k_free[kSlots],
-        v_ready[kSlots], v_free[kSlots], q_full, q_free, s_full[kScores], p_full[kScores], o_full, o_free;
+    __shared__ __align__(8) uint64_t staged[2][kStages], unstaged[2][kStages], ranged[kRingV], k_ready[kSlots], k_free[kSlots],
+        v_ready[kSlots], v_free[kSlots], q_full, q_free, s_full[kScores], p_full[kScores], met[4], o_full, o_free;
     __shared__ uint32_t tmem_base_s;
     __shared__ long long scan_s[kThreads / 32];
-    __shared__ __align__(16) float k_scale[kRing][kKT], v_scale[kRing][kKT], v_norm[kRing][kKT];
-    __shared__ float v_back[kRing];              // 2^(E - kShift); 0: the scales differ too much
+    __shared__ __align__(16) float k_scale[kRing][kKT], v_scale[kRingV][kKT], v_norm[kRingV][kKT];
+    __shared__ float v_back[kRingV];             // 2^(E - kShift); 0: the scales differ too much
     __shared__ __align__(16) Tile tile_s[kTiles];
     __shared__ float q_back[4][kM];              // by piece: what the queries' power of two takes back
-    __shared__ float2 stat[kStats][kM];          // by tile: m, l
-    __shared__ float stat_back[kStats][kM];      // factor of its output
+    __shared__ float stat[kStats][4][kM];        // by tile: m, l of either half, factor of its output
+    __shared__ float meet[2][2][kM];             // what the halves of a row tell one another
     __shared__ int piece_end[4];                 // by piece: the tile after it
-    __shared__ int v_rows[kRing];                // of a tile that there are, as V's producer knows; -1: the end
+    __shared__ int v_rows[kRingV];               // of a tile that there are, as V's producer knows; -1: the end
 
     const PagedDesc& a = g.a;
     const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -440,9 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kScores; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[i], 8);
         }
-        for (int i = 0; i < kRing; ++i) mbar_init(&ranged[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&met[i], 2);
+        for (int i = 0; i < kRingV; ++i) mbar_init(&ranged[i], 1);
         mbar_init(&o_full, 1);
         mbar_init(&o_free, 4);
         mbar_init(&q_free, 2);  // the MMAs' commit, and an arrival that publishes piece_end
@@ -509,10 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n >= kStages && !warp_wait(&unstaged[values][st], n / kStages - 1, kErrQ8Free)) break;
                 if (lane == 0) {
                     if (values) {
-                        v_rows[n % kRing] = stop ? -1 : max(walk.len - t.key, 0);
+                        v_rows[n % kRingV] = stop ? -1 : max(walk.len - t.key, 0);
                     } else {
                         tile_s[n % kTiles] = t;
-                        if (stop) tile_s[(n + 1) % kTiles] = t;  // for the other softmax warps
                     }
                     mbar_arrive_expect_tx(&staged[values][st], stop ? 0u : C::kCodes);
                 }
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (t.piece != of_piece) batch = -1;
                     of_piece = t.piece;
                     unsigned char* to = codes + (size_t)(st + (values ? kStages : 0)) * C::kCodes;
-                    float* to_scale = (values ? v_scale : k_scale)[n % kRing];
+                    float* to_scale = values ? v_scale[n % kRingV] : k_scale[n % kRing];
                     const int boxes = kKT >> g.sub_shift, q0 = t.key >> g.sub_shift;
 #pragma unroll 1
                     for (int c = 0; c < boxes; c += 32) {
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 3) {
             // ---- the range of a tile's value scales ----------------------------------------
             for (int n = 0;; ++n) {
-                const int st = n % kStages, rg = n % kRing;
+                const int st = n % kStages, rg = n % kRingV;
                 if (!warp_wait(&staged[1][st], n / kStages, kErrQ8Load)) break;
                 const bool stop = v_rows[rg] < 0;
                 const float* vs = v_scale[rg];
@@ -597,77 +597,66 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t id_s = idesc_f16(kM, kKT, false), id_o = idesc_f16(kM, D, true);
             const uint64_t k0 = smem_desc(ktiles, 16), v0 = smem_desc(vtiles, kBlock);
             const uint32_t k_lo = (uint32_t)k0, k_hi = (uint32_t)(k0 >> 32), v_lo = (uint32_t)v0, v_hi = (uint32_t)(v0 >> 32);
-            // S runs up to kScores tiles ahead of P V, but does not wait for its keys or queries while there
-            // is a P V to issue.
-            int sn = 0, vn = 0;
-            bool end = false, k_ok = false;
+            // S goes first where its keys and queries are there; what it is, is looked up before the wait for
+            // the weights of O.
+            int sn = 0, vn = 0, flags = 0, piece = 0;
+            bool end = false, k_ok = false, q_ok = false;
             for (;;) {
-                if (!end && sn - vn < kScores) {
-                    const bool must = sn == vn;
-                    const int st = sn % kSlots;
-                    if (!k_ok) {
-                        k_ok = __all_sync(FULL, mbar_test(&k_ready[st], (uint32_t)((sn / kSlots) & 1)));
-                        if (!k_ok && must) {
-                            k_ok = warp_wait(&k_ready[st], sn / kSlots, kErrQ8Mma);
-                            if (!k_ok) break;
-                        }
+                const int sl = sn % kSlots;
+                const bool must = sn == vn;
+                if (!end && !k_ok) {
+                    k_ok = __all_sync(FULL, mbar_test(&k_ready[sl], (uint32_t)((sn / kSlots) & 1)));
+                    if (!k_ok && must) {
+                        k_ok = warp_wait(&k_ready[sl], sn / kSlots, kErrQ8Mma);
+                        if (!k_ok) break;
                     }
                     if (k_ok) {
-                        const int flags = tile_s[sn % kTiles].flags, piece = tile_s[sn % kTiles].piece;
-                        bool q_ok = true;
-                        if (flags & kStop) {
-                            end = true;
-                            continue;
-                        }
-                        if (flags & kFirst) {
-                            q_ok = __all_sync(FULL, mbar_test(&q_full, (uint32_t)(piece & 1)));
-                            if (!q_ok && must) {
-                                q_ok = warp_wait(&q_full, piece, kErrQ8Mma);
-                                if (!q_ok) break;
-                            }
-                        }
-                        if (q_ok) {
-                            tc_fence_after();
-                            const uint32_t d = tmem + C::kColS + (sn % kScores) * kKT;
-                            const uint32_t k = k_lo + st * (C::kTile >> 4);
-                            if (elect_one()) {
-                                // Unrolled, with little but the MMA itself to an issue: the warp has a sixth of its
-                                // scheduler, and with loops and 64-bit sums S took 1500 cycles to issue.
+                        flags = tile_s[sn % kTiles].flags;
+                        piece = tile_s[sn % kTiles].piece;
+                        end = flags & kStop;
+                        q_ok = !(flags & kFirst);
+                    }
+                }
+                if (!end && k_ok && !q_ok) {
+                    q_ok = __all_sync(FULL, mbar_test(&q_full, (uint32_t)(piece & 1)));
+                    if (!q_ok && must) {
+                        q_ok = warp_wait(&q_full, piece, kErrQ8Mma);
+                        if (!q_ok) break;
+                    }
+                }
+                if (!end && k_ok && q_ok && sn - vn < kScores) {
+                    tc_fence_after();
+                    const uint32_t d = tmem + C::kColS + (sn % kScores) * kKT;
+                    const uint32_t k = k_lo + sl * (C::kTile >> 4);
+                    if (elect_one()) {
+                        // Unrolled, with little but the MMA itself to an issue: the warp has a sixth of its
+                        // scheduler, and with loops and 64-bit sums S took 1500 cycles to issue.
 #pragma unroll
-                                for (int i = 0; i < D / 16; ++i) {
-                                    const uint32_t at = k + (i >> 2) * (kBlock >> 4) + 2 * (i & 3);
-                                    if (i == 0) mma_f16_ts<false>(d, tmem + C::kColQlo, at, k_hi, id_s);
-                                    else mma_f16_ts<true>(d, tmem + C::kColQlo + 8 * i, at, k_hi, id_s);
-                                }
+                        for (int i = 0; i < D / 16; ++i) {
+                            const uint32_t at = k + (i >> 2) * (kBlock >> 4) + 2 * (i & 3);
+                            if (i == 0) mma_f16_ts<false>(d, tmem + C::kColQlo, at, k_hi, id_s);
+                            else mma_f16_ts<true>(d, tmem + C::kColQlo + 8 * i, at, k_hi, id_s);
+                        }
 #pragma unroll
-                                for (int i = 0; i < D / 16; ++i)
-                                    mma_f16_ts<true>(d, tmem + C::kColQhi + 8 * i, k + (i >> 2) * (kBlock >> 4) + 2 * (i & 3), k_hi, id_s);
-                                mma_commit(&k_free[st]);
-                                mma_commit(&s_full[sn % kScores]);
-                                if (flags & kLast) {
-                                    piece_end[piece & 3] = sn + 1;
-                                    mma_commit(&q_free);
-                                    mbar_arrive(&q_free);  // publishes piece_end
-                                }
-                            }
-                            __syncwarp();
-                            ++sn;
-                            k_ok = false;
-                            continue;
+                        for (int i = 0; i < D / 16; ++i)
+                            mma_f16_ts<true>(d, tmem + C::kColQhi + 8 * i, k + (i >> 2) * (kBlock >> 4) + 2 * (i & 3), k_hi, id_s);
+                        mma_commit(&k_free[sl]);
+                        mma_commit(&s_full[sn % kScores]);
+                        if (flags & kLast) {
+                            piece_end[piece & 3] = sn + 1;
+                            mma_commit(&q_free);
+                            mbar_arrive(&q_free);  // publishes piece_end
                         }
                     }
+                    __syncwarp();
+                    ++sn;
+                    k_ok = false;
+                    continue;
                 }
                 if (vn < sn) {  // O(vn) = P(vn) V(vn)
                     const int bf = vn % kScores, st = vn % kSlots;
-                    if (!end && sn - vn < kScores) {
-                        // Whichever comes first: these weights, or what the next S lacks.
-                        uint64_t* other = k_ok ? &q_full : &k_ready[sn % kSlots];
-                        const int phase = k_ok ? tile_s[sn % kTiles].piece : sn / kSlots;
-                        if (warp_wait_either(&p_full[bf], vn / kScores, other, phase, kErrQ8Mma)) continue;
-                    }
-                    if (!warp_wait(&p_full[bf], vn / kScores, kErrQ8Mma) || !warp_wait(&v_ready[st], vn / kSlots, kErrQ8Mma) ||
-                        (vn > 0 && !warp_wait(&o_free, vn - 1, kErrQ8Mma)))
-                        break;
+                    // o_free's phases begin with a tile's O: the one before the first is over.
+                    if (!warp_wait3(&p_full[bf], vn / kScores, &v_ready[st], vn / kSlots, &o_free, vn - 1, kErrQ8Mma)) break;
                     tc_fence_after();
                     const uint32_t d = tmem + C::kColO, p = tmem + C::kColS + bf * kKT;
                     const uint32_t v = v_lo + st * (C::kTile >> 4);
@@ -690,7 +679,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (vn > 0 && !warp_wait(&o_free, vn - 1, kErrQ8Mma)) break;
                 if (lane == 0) {
                     mbar_arrive(&s_full[sn % kScores]);
-                    mbar_arrive(&s_full[(sn + 1) % kScores]);
                     mbar_arrive(&o_full);
                 }
                 break;
@@ -770,12 +758,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const Tile t = tile_s[n % kTiles];
             if (t.flags & kStop) break;
-            const float2 st = stat[n % kStats][i];
-            const float Mn = fmaxf(M, st.x), mu = Mn == -INFINITY ? 0.f : Mn;
-            const float alpha = fast_exp2(M - mu), beta = fast_exp2(st.x - mu);
+            const float* st = &stat[n % kStats][0][i];
+            const float mt = st[0], lt = st[kM] + st[2 * kM];
+            const float Mn = fmaxf(M, mt), mu = Mn == -INFINITY ? 0.f : Mn;
+            const float alpha = fast_exp2(M - mu), beta = fast_exp2(mt - mu);
             M = Mn;
-            L = fmaf(L, alpha, st.y * beta);
-            const float bo = beta * stat_back[n % kStats][i];
+            L = fmaf(L, alpha, lt * beta);
+            const float bo = beta * st[3 * kM];
             if (__any_sync(FULL, alpha != 1.f)) {  // a maximum moved
                 const uint64_t al = f2_pack(alpha, alpha);
 #pragma unroll
@@ -836,13 +825,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp < 16) {
-        // ---- softmax: thread = virtual row, every other tile ------------------------------------
+        // ---- softmax: thread = virtual row, one half of every tile ------------------------------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        const int turn = (warp - 8) >> 2, i = 32 * (warp & 3) + lane;
+        const int half = (warp - 8) >> 2, i = 32 * (warp & 3) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         int piece = -1, hi = 0, lo = 0, sinks = 0;
         bool alive = false;
-        for (int n = turn;; n += 2) {
+        int meets = 0;
+        // The larger of a row's two halves, by a slot each, two meetings in turn.
+        auto larger = [&](float x, bool& ok) -> float {
+            meet[meets & 1][half][i] = x;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&met[warp & 3]);
+            ok = warp_wait(&met[warp & 3], meets, kErrQ8Mma);
+            const float y = meet[meets & 1][half ^ 1][i];
+            ++meets;
+            return fmaxf(x, y);
+        };
+        for (int n = 0;; ++n) {
             if (!warp_wait(&s_full[n % kScores], n / kScores, kErrQ8Mma)) break;
             const Tile t = tile_s[n % kTiles];
             if (t.flags & kStop) break;
@@ -859,33 +859,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sinks = (int)min(a.sinks, (int64_t)rq.len);
             }
             tc_fence_after();
-            const bool all = !alive || (hi - t.key >= kKT - 1 && lo <= t.key);
+            const int key = t.key + kHalf * half;
+            const bool all = !alive || (hi - key >= kHalf - 1 && lo <= key);
             const bool whole = __all_sync(FULL, all);
             RowTile rt;
-            rt.at = tmem + lanes + C::kColS + (n % kScores) * kKT;
-            rt.ks = k_scale[n % kRing];
-            rt.see0 = rt.see1 = ~0ull;
+            rt.at = tmem + lanes + C::kColS + (n % kScores) * kKT + kHalf * half;
+            rt.ks = k_scale[n % kRing] + kHalf * half;
+            rt.see = ~0ull;
             rt.rf = q_back[piece & 3][i];
             rt.cap = a.cap_log2;
             if (!all) {
                 auto below = [](int c) -> uint64_t { return c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1; };
-                auto from = [&](int k) -> uint64_t { return below(hi - k + 1) & (~below(lo - k) | below(sinks - k)); };
-                rt.see0 = from(t.key);
-                rt.see1 = from(t.key + 64);
+                rt.see = below(hi - key + 1) & (~below(lo - key) | below(sinks - key));
             }
-            if (!warp_wait(&ranged[n % kRing], n / kRing, kErrQ8Load)) break;
-            const float back = v_back[n % kRing];
-            float2 ml;
-            float factor = back;
-            if (back == 0.f) {  // rare
-                const float4 far = far_softmax<CAP>(rt, v_scale[n % kRing]);
-                ml = make_float2(far.x, far.y);
-                factor = exp2f(far.z - (float)kShift);
+            bool ok;
+            const float m = larger(whole ? row_max<CAP, true>(rt) : row_max<CAP, false>(rt), ok);
+            const float mu = m == -INFINITY ? 0.f : m;
+            if (!ok || !warp_wait(&ranged[n % kRingV], n / kRingV, kErrQ8Load)) break;
+            float factor = v_back[n % kRingV], l;
+            if (factor == 0.f) {  // rare
+                const float* vs = v_scale[n % kRingV] + kHalf * half;
+                const float top = ceilf(fminf(larger(far_softmax<CAP, false>(rt, vs, mu, -300.f), ok), 126.f));
+                if (!ok) break;
+                l = far_softmax<CAP, true>(rt, vs, mu, top);
+                factor = exp2f(top - (float)kShift);
             } else {
-                ml = whole ? row_softmax<CAP, true>(rt, v_norm[n % kRing]) : row_softmax<CAP, false>(rt, v_norm[n % kRing]);
+                const float* vn = v_norm[n % kRingV] + kHalf * half;
+                l = whole ? row_weights<CAP, true>(rt, vn, mu) : row_weights<CAP, false>(rt, vn, mu);
             }
-            stat[n % kStats][i] = ml;
-            stat_back[n % kStats][i] = factor;
+            stat[n % kStats][1 + half][i] = l;
+            if (half == 0) {
+                stat[n % kStats][0][i] = m;
+                stat[n % kStats][3][i] = factor;
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -901,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0;; ++n) {
             const int st = n % kStages, sl = n % kSlots;
             if (!warp_wait(&staged[kv][st], n / kStages, kErrQ8Load)) break;
-            const int rows = kv ? v_rows[n % kRing] : tile_s[n % kTiles].flags & kStop ? -1 : kKT;
+            const int rows = kv ? v_rows[n % kRingV] : tile_s[n % kTiles].flags & kStop ? -1 : kKT;
             if (n >= kSlots && !warp_wait(&freed[sl], n / kSlots - 1, kErrQ8Free)) break;
             if (rows < 0) {
                 if (lane == 0) mbar_arrive(&ready[sl]);
@@ -910,8 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned char* from = codes + (size_t)(st + kv * kStages) * C::kCodes;
             unsigned char* to = (kv ? vtiles : ktiles) + sl * C::kTile;
             if (FORM == kFormE4m3 && rows < kKT) clear_rows<D>(from, rows, w, lane);
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) convert<D, FORM>(from, to, 4 * w + i, lane);
+            convert<D, FORM>(from, to, w, lane);
             asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
             __syncwarp();
             if (lane == 0) {
