@@ -35,6 +35,10 @@
 // channels that are its rows of the transposed product: S^T = K q^T, O^T = V^T P^T, keys and
 // channels fill the 16-row side, 8 virtual rows the other.  P^T changes layout by movmatrix.
 // Every wait is bounded; one that gives up sets a bit of the device flag.
+//
+// Measured (a replayed graph): 24 requests of 8192 to 32704 rows, 32 heads over 8 of 128, e4m3
+// (1.08 GB) 175 us, 91 % of the copy rate; 32 of 517 to 8111, int8 (304 MB) 71 us, 63 %: of 24 us
+// above the copy's the launches, the scan of the requests, the first loads and the join take most.
 #include <cstring>
 
 #include "attn_common.cuh"

@@ -2,14 +2,14 @@
 // the tcgen05 tensor cores, headDim 64 or 128: trees of drafted tokens, chunks of prompts.
 //
 // Mathematics as in paged_q8_mma.cu, for row blocks of 128 virtual rows (t G + g) and tiles of
-// 64 keys.  Codes are exact in f16, so S = Q K^T and O = P V are two f16 products each: hi and
+// 128 keys.  Codes are exact in f16, so S = Q K^T and O = P V are two f16 products each: hi and
 // lo of the queries and of the weights, lo first.  Every tile stands alone: its weights are
 // 2^(x2 - m_t), m_t the row's largest score in the tile, times the value's scale over 2^E, E
 // the largest scale's exponent; its output O_t and sum l_t come with m_t and E, and the
 // fold joins them in f32 by the log-sum-exp rule,
 //   acc = acc 2^(M - M') + O_t 2^(m_t + E - M'),  M' = max(M, m_t).
-// So no tile waits for another one's maximum, two softmax warpgroups take tiles in turn, and
-// no sum runs long inside the tensor cores, which round towards zero at every step.
+// So no tile waits for another one's maximum, and no sum runs long inside the tensor cores,
+// which round towards zero at every step.
 // A weight has 2^14 as a factor: kept to 2^-39 of the largest scale times 1.  Where a tile's
 // scales differ by more than 2^6 a small one may be what counts, so each row of such a tile
 // takes the exponent of its own largest product instead (rare).
@@ -20,12 +20,21 @@
 //
 // Warps, with their share of the 480 registers a lane that six warpgroups launch with:
 //   0, 2    page ids, TMA loads of K and of V codes (a box per page) and copies of scales
-//   1       MMAs: S(n), then O(n - 1); one elected lane issues                      (56)
+//   1       MMAs; one elected lane issues
+//   3       the range of a tile's value scales                                      (56)
 //   4 - 7   queries to TMEM, and the fold; a thread is a row, acc in registers     (184)
-//   8 - 15  softmax of even and of odd tiles; a thread is a row                  (2 x 72)
-//   16 - 23 codes to f16 tiles, and the scales' range                           (2 x 48)
-// TMEM: Q hi, lo (D columns), four S / P buffers (256), O (D).
+//   8 - 15  softmax, a warpgroup for either half of a tile; a thread is a row    (2 x 72)
+//   16 - 23 codes to f16 tiles, four warps for K, four for V                     (2 x 48)
+// TMEM: Q hi, lo (D columns), two S / P buffers (256), O (D).
 // Every wait is bounded; one that gives up sets a bit of the device flag.
+//
+// What bounds it.  8 trees of 64 rows beside 16384 to 32704 cached ones, 32 heads of 128 over 8 (large
+// trees below), take 444 us; the two f16 products of 2.17e11 FLOP would take 228 at the measured
+// rate.  The scores and outputs of a tile take 1024 cycles of MMAs, a tile 3900 to 4200: the softmax
+// warps are at it all of that time (1100 to the maximum, 2600 from there to the weights), and the
+// roles together issue some 12 000 warp instructions, most of a tile's slots once packed f32 ones
+// count twice.  More instructions in the softmax show (always masked: 476 us), and so does more
+// code: with the next 16 scores loaded ahead in a loop twice as long, 463.
 #include <cstring>
 #include <mutex>
 
@@ -187,8 +196,6 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
     return r != 0;
 }
-// mbar_wait, bounded in the same way, that looks at the clock late and seldom: reading the
-// global timer takes as long as a whole hand-over.
 // Whether the phase is over, without a wait.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     uint32_t done;
@@ -199,6 +206,8 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
         : "memory");
     return done != 0;
 }
+// mbar_wait, bounded in the same way, that looks at the clock late and seldom: reading the
+// global timer takes as long as a whole hand-over.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase, unsigned int error) {
     const uint32_t parity = (uint32_t)(phase & 1);
     uint64_t t0 = 0;
@@ -317,7 +326,7 @@ __device__ __forceinline__ void store_weights(uint32_t at, const float* w) {
 }
 // The row's largest score of the half, in base-2 units; leaves the masked scores as row_scores makes them.
 // Short loops on purpose: the roles' code has to stay in the instruction cache together (with
-// these unrolled large trees took 695 us instead of 613).
+// these unrolled, in tiles of 64 keys, large trees took 695 us instead of 613).
 template <bool CAP, bool WHOLE>
 __device__ __forceinline__ float row_max(const RowTile& r) {
     float m = -INFINITY;
@@ -630,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t k = k_lo + sl * (C::kTile >> 4);
                     if (elect_one()) {
                         // Unrolled, with little but the MMA itself to an issue: the warp has a sixth of its
-                        // scheduler, and with loops and 64-bit sums S took 1500 cycles to issue.
+                        // scheduler.  950 cycles; with loops and 64-bit sums half of these took 1500.
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             const uint32_t at = k + (i >> 2) * (kBlock >> 4) + 2 * (i & 3);
@@ -900,8 +909,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ---- codes to f16 ------------------------------------------------------------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        // Four warps for K, four for V.  Short loops on purpose: six warps with code of their own share a
-        // scheduler, and unrolled roles ran at the rate of instruction fetches.
+        // Four warps for K, four for V, so that K does not wait for an earlier O with V (eight for
+        // both, K first, in halves of a tile: 519 us).
         const int kv = warp >= 20, w = warp & 3;
         uint64_t *ready = kv ? v_ready : k_ready, *freed = kv ? v_free : k_free;
         for (int n = 0;; ++n) {
