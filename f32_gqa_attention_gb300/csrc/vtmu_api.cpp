@@ -1446,12 +1446,21 @@ vtmu_status vtmu_norm_rope(const float* q, const float* k, const float* q_weight
                           {q_weight, wb}, {k_weight, wb}, {positions, (size_t)p->axes * T * 4}};
     if (outputs_overlap(spans, 2, 7))
         return fail(VTMU_ERR_INVALID, "norm_rope: an output overlaps another buffer (other than its own input, in place)");
-    for (int j = 0; j < a.half; ++j) {
-        // 1 / (2 pi) as a double and the double nearest its remainder: the product to 2^-100 or so.
-        const double hi = rd.inv_freq[j] * 0.15915494309189535, lo = std::fma(rd.inv_freq[j], 0.15915494309189535, -hi) +
-                                                                      rd.inv_freq[j] * -9.839338337591243e-18;
-        a.turn[j] = turn_of(hi, lo);
+    // Of the last frequencies on this thread: forming 64 takes a microsecond or two.
+    thread_local double last_freq[vtmu::kRopeMaxPairs];
+    thread_local uint64_t last_turn[vtmu::kRopeMaxPairs];
+    thread_local int last_half = 0;
+    if (a.half > last_half || std::memcmp(rd.inv_freq, last_freq, sizeof(double) * (size_t)a.half) != 0) {
+        for (int j = 0; j < a.half; ++j) {
+            // 1 / (2 pi) as a double and the double nearest its remainder: the product to 2^-100 or so.
+            const double hi = rd.inv_freq[j] * 0.15915494309189535, lo = std::fma(rd.inv_freq[j], 0.15915494309189535, -hi) +
+                                                                          rd.inv_freq[j] * -9.839338337591243e-18;
+            last_freq[j] = rd.inv_freq[j];
+            last_turn[j] = turn_of(hi, lo);
+        }
+        last_half = a.half;
     }
+    std::memcpy(a.turn, last_turn, sizeof(uint64_t) * (size_t)a.half);
     a.q = q;
     a.k = k;
     a.qw = q_weight;
