@@ -29,12 +29,13 @@
 // Every wait is bounded; one that gives up sets a bit of the device flag.
 //
 // What bounds it.  8 trees of 64 rows beside 16384 to 32704 cached ones, 32 heads of 128 over 8 (large
-// trees below), take 444 us; the two f16 products of 2.17e11 FLOP would take 228 at the measured
-// rate.  The scores and outputs of a tile take 1024 cycles of MMAs, a tile 3900 to 4200: the softmax
-// warps are at it all of that time (1100 to the maximum, 2600 from there to the weights), and the
-// roles together issue some 12 000 warp instructions, most of a tile's slots once packed f32 ones
-// count twice.  More instructions in the softmax show (always masked: 476 us), and so does more
-// code: with the next 16 scores loaded ahead in a loop twice as long, 463.
+// trees below), take 412 us with the drafted rows' part and the join; the two f16 products of 2.17e11
+// FLOP would take 228 at the measured rate.  The scores and outputs of a tile take 1024 cycles of MMAs, a
+// tile 3900 to 4200: the softmax warps are at it all of that time (1100 to the maximum, 2600 from
+// there to the weights), and the roles together issue most of a tile's slots once packed f32
+// instructions count twice.  More instructions in the softmax show (always masked: 476 us where 446
+// was), and so does more code: with the next 16 scores loaded ahead in a loop twice as long, 463.  A
+// change of piece costs 16 000 cycles more (code that runs once a piece is fetched anew).
 #include <cstring>
 #include <mutex>
 
