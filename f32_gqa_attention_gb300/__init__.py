@@ -945,13 +945,13 @@ def _paged_call(q, width, pool_rows, block_table, lens, cu_rows, heads, headDim,
             raise ValueError("paged_attention: k_new and v_new [rows, kvHeads*headDim], masks and positions [rows]")
     if out is None:
         out = torch.empty_like(q)
-    _need("out", out, f32, dev)
-    if out.shape != q.shape:
-        raise ValueError("paged_attention: out [rows, heads*headDim]")
-    with _on(dev):
-        p, nbytes = _paged_params(rows, pool_rows // pageSize, n, max(min(maxRows, rows), -1), pageSize,
-                                  block_table.shape[1], heads, hk, headDim, 0 if tree is None else 1, scale,
-                                  softcap or 0.0, kernel, window or 0, sinks or 0, q8)
+    else:
+        _need("out", out, f32, dev)
+        if out.shape != q.shape:
+            raise ValueError("paged_attention: out [rows, heads*headDim]")
+    p, nbytes = _paged_params(rows, pool_rows // pageSize, n, max(min(maxRows, rows), -1), pageSize, block_table.shape[1],
+                              heads, hk, headDim, 0 if tree is None else 1, scale, softcap or 0.0, kernel, window or 0,
+                              sinks or 0, q8)
     return p, nbytes, out, k_new, v_new, masks, positions
 
 
@@ -984,6 +984,7 @@ def paged_attention(q, k_pool, v_pool, block_table, lens, cu_rows, *, heads, hea
 
 
 # -------------------------------------------------------- 8-bit paged caches
+@functools.lru_cache(maxsize=None)
 def _q8_format(dtype):
     import torch
     kind = {torch.int8: VTMU_KV_INT8, torch.float8_e4m3fn: VTMU_KV_E4M3}.get(dtype)
@@ -1001,11 +1002,11 @@ def _q8_pools(what, k_pool, v_pool, k_scale, v_scale):
         _need(name, t, k_pool.dtype, dev)
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
         _need(name, t, torch.float32, dev)
-    if (k_pool.dim() != 2 or v_pool.shape != k_pool.shape or k_scale.dim() != 2 or v_scale.shape != k_scale.shape or
-            k_scale.shape[0] != k_pool.shape[0] or k_scale.shape[1] < 1 or k_pool.shape[1] < k_scale.shape[1] or
-            k_pool.shape[1] % k_scale.shape[1]):
+    codes, scales = k_pool.shape, k_scale.shape
+    if (len(codes) != 2 or v_pool.shape != codes or len(scales) != 2 or v_scale.shape != scales or scales[0] != codes[0] or
+            scales[1] < 1 or codes[1] < scales[1] or codes[1] % scales[1]):
         raise ValueError(f"{what}: pools [poolRows, kvHeads*headDim], scales [poolRows, kvHeads]")
-    return kind, k_pool.shape[0], k_scale.shape[1], k_pool.shape[1] // k_scale.shape[1]
+    return kind, codes[0], scales[1], codes[1] // scales[1]
 
 
 def paged_write_q8(k_pool, v_pool, k_scale, v_scale, k_new, v_new, slots, *, stream=None):
@@ -1037,15 +1038,17 @@ def paged_read_q8(k_pool, v_pool, k_scale, v_scale, slots, *, out=None, stream=N
     dev = k_pool.device
     kind, total, hk, d = _q8_pools("paged_read_q8", k_pool, v_pool, k_scale, v_scale)
     _need("slots", slots, torch.int32, dev)
+    if slots.dim() != 1:
+        raise ValueError("paged_read_q8: slots [rows]")
     n = slots.shape[0]
     if out is None:
         k, v = (torch.empty((n, hk * d), dtype=torch.float32, device=dev) for _ in range(2))
     else:
         k, v = out
-    for name, t in (("k", k), ("v", v)):
-        _need(name, t, torch.float32, dev)
-    if slots.dim() != 1 or k.shape != (n, hk * d) or v.shape != k.shape:
-        raise ValueError("paged_read_q8: slots [rows], out [rows, kvHeads*headDim]")
+        for name, t in (("k", k), ("v", v)):
+            _need(name, t, torch.float32, dev)
+        if k.shape != (n, hk * d) or v.shape != k.shape:
+            raise ValueError("paged_read_q8: out [rows, kvHeads*headDim]")
     with _on(dev):
         st = _raw_stream(dev) if stream is None else stream
         vtmu_paged_read_q8(k_pool, v_pool, k_scale, v_scale, total, hk, d, kind, slots, k, v, n, st)
@@ -1111,18 +1114,27 @@ def norm_rope(q, k, positions, *, headDim, qWeight=None, kWeight=None, norm=True
     f32 = torch.float32
     _need("q", q, f32)
     _need("positions", positions, torch.int32, dev)
-    q_out, k_out = (torch.empty_like(q), None if k is None else torch.empty_like(k)) if out is None else out
-    for name, t in (("k", k), ("qWeight", qWeight), ("kWeight", kWeight), ("q of out", q_out), ("k of out", k_out)):
+    for name, t in (("k", k), ("qWeight", qWeight), ("kWeight", kWeight)):
         if t is not None:
             _need(name, t, f32, dev)
     T = q.shape[0]
     axes = 1 if sections is None else len(sections)
     if (headDim < 1 or q.dim() != 2 or q.shape[1] % headDim or positions.numel() != axes * T or
-            positions.shape not in ((T,), (axes, T)) or q_out is None or q_out.shape != q.shape or
-            (k is None) != (k_out is None) or
-            (k is not None and (k.dim() != 2 or k.shape[0] != T or k.shape[1] % headDim or k_out.shape != k.shape)) or
-            any(w is not None and w.shape != (headDim,) for w in (qWeight, kWeight))):
-        raise ValueError("norm_rope: q and k [T, heads*headDim], positions [T] or [axes, T], weights [headDim], out as q and k")
+            positions.shape not in ((T,), (axes, T)) or
+            (k is not None and (k.dim() != 2 or k.shape[0] != T or k.shape[1] % headDim)) or
+            (qWeight is not None and qWeight.shape != (headDim,)) or (kWeight is not None and kWeight.shape != (headDim,))):
+        raise ValueError("norm_rope: q and k [T, heads*headDim], positions [T] or [axes, T], weights [headDim]")
+    if out is None:
+        q_out, k_out = torch.empty_like(q), None if k is None else torch.empty_like(k)
+    else:
+        q_out, k_out = out
+        if q_out is None or (k is None) != (k_out is None):
+            raise ValueError("norm_rope: out as q and k")
+        for name, t, x in (("q of out", q_out, q), ("k of out", k_out, k)):
+            if x is not None:
+                _need(name, t, f32, dev)
+                if t.shape != x.shape:
+                    raise ValueError("norm_rope: out as q and k")
     args = (headDim, norm, eps, weightOffset, None if sections is None else tuple(sections), dealt, tuple(rope.items()))
     if rope.get("scaling") is None and rope.get("invFreq") is None:
         p = _norm_rope_params(*args)

@@ -712,7 +712,7 @@ typedef enum vtmu_kv_format {
  * code is the nearest one to x / scale, ties to even (the exact quotient).  A head with an
  * element that is not finite is stored as NaN: scale NaN, codes 0.  A row whose
  * slot is outside 0 .. pool_rows - 1 is skipped, pool rows without a slot are
- * untouched; the slots of one call are distinct.
+ * untouched; the slots of one call are distinct (two rows of one slot leave it undefined).
  *   k_new, v_new [rows, kv_heads*head_dim]: f32, DEVICE; slots [rows]: int32,
  *   DEVICE.  None may overlap another.  head_dim 1..256.
  * Errors: VTMU_ERR_INVALID (null pointer with rows > 0, bad size or format,
