@@ -29,7 +29,7 @@
 // Every wait is bounded; one that gives up sets a bit of the device flag.
 //
 // What bounds it.  8 trees of 64 rows beside 16384 to 32704 cached ones, 32 heads of 128 over 8 (large
-// trees below), take 412 us with the drafted rows' part and the join; the two f16 products of 2.17e11
+// trees below), take 405 us with the drafted rows' part and the join; the two f16 products of 2.17e11
 // FLOP would take 228 at the measured rate.  The scores and outputs of a tile take 1024 cycles of MMAs, a
 // tile 3900 to 4200: the softmax warps are at it all of that time (1100 to the maximum, 2600 from
 // there to the weights), and the roles together issue most of a tile's slots once packed f32
@@ -407,6 +407,62 @@ __device__ __forceinline__ float far_softmax(const RowTile r, const float* vs, f
     return WEIGHTS ? sum : top;
 }
 
+// 16 lanes x 8 columns of tensor memory: lane l holds columns 2 (l % 4) and the next of rows l / 4
+// (v[0], v[1]) and l / 4 + 8.
+__device__ __forceinline__ void tmem_st_16x8(uint32_t at, const uint32_t (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]));
+}
+// The queries of the piece that tile t begins, a warp's 32 virtual rows of its block: to tensor memory
+// as hi and lo, times qk_mul and a power of two that brings the row's largest element to
+// [2^13, 2^14); `back` gets what that takes back.  Four lanes share a row, so that a load touches 8
+// lines: with a row a lane, 32 lines, large trees took 412 us instead of 405, chunks 210 instead of 203.
+template <int D>
+__device__ __forceinline__ void row_queries(const PagedDesc& a, const Tile& t, int w, int lane, uint32_t at_hi, uint32_t at_lo,
+                                            float* back) {
+    const Q8Req rq = q8_load_req(a, t.b);
+    const int quad = lane & 3;
+#pragma unroll 1
+    for (int half = 0; half < 32; half += 16) {
+        const float* q[2];
+        float sc[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = 32 * w + half + (lane >> 2) + 8 * h, v = t.rb * kM + i, row = v / a.G;
+            q[h] = v < rq.T * a.G
+                       ? a.q + (((int64_t)rq.row0 + row) * a.H + (int64_t)t.hk * a.G + (v - row * a.G)) * D + 4 * quad
+                       : nullptr;
+        }
+        auto load4 = [&](int h, int d) -> float4 {
+            if (!q[h]) return make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 y = __ldg(reinterpret_cast<const float4*>(q[h] + d));
+            return make_float4(y.x * a.qk_mul, y.y * a.qk_mul, y.z * a.qk_mul, y.w * a.qk_mul);
+        };
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float top = 0.f;
+#pragma unroll 8
+            for (int d = 0; d < D; d += 16) top = q8_abs_top(top, load4(h, d));
+            top = q8_nan_max(top, __shfl_xor_sync(FULL, top, 1));
+            top = q8_nan_max(top, __shfl_xor_sync(FULL, top, 2));
+            sc[h] = mma_row_scale(top, 13);
+            if (quad == 0) back[32 * w + half + (lane >> 2) + 8 * h] = 1.f / sc[h];
+        }
+#pragma unroll 2
+        for (int d = 0; d < D; d += 16) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 y = load4(h, d);
+                mma_split(y.x * sc[h], y.y * sc[h], hi[2 * h], lo[2 * h]);
+                mma_split(y.z * sc[h], y.w * sc[h], hi[2 * h + 1], lo[2 * h + 1]);
+            }
+            tmem_st_16x8(at_hi + ((uint32_t)half << 16) + d / 2, hi);
+            tmem_st_16x8(at_lo + ((uint32_t)half << 16) + d / 2, lo);
+        }
+    }
+    tmem_wait_st();
+}
+
 template <int D, int FORM, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1) 
     q8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -699,43 +755,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int w = warp & 3, i = 32 * w + lane;
         const uint32_t lanes = (uint32_t)(32 * w) << 16;
-        // The queries of the piece that tile j begins: times qk_mul and a power of two that brings
-        // the row's largest element to [2^13, 2^14).  False at the list's end.
+        // The queries of the piece that tile j begins.  False at the list's end.
         auto load_queries = [&](int j) -> bool {
             const Tile t = tile_s[j % kTiles];
             if (t.flags & kStop) return false;
-            const Q8Req rq = q8_load_req(a, t.b);
-            const int v = t.rb * kM + i, row = v / a.G;
-            const bool alive = v < rq.T * a.G;
-            const float* q = a.q + (((int64_t)rq.row0 + row) * a.H + (int64_t)t.hk * a.G + (v - row * a.G)) * D;
-            auto load4 = [&](int d) -> float4 {
-                if (!alive) return make_float4(0.f, 0.f, 0.f, 0.f);
-                const float4 y = __ldg(reinterpret_cast<const float4*>(q + d));
-                return make_float4(y.x * a.qk_mul, y.y * a.qk_mul, y.z * a.qk_mul, y.w * a.qk_mul);
-            };
-            float top = 0.f;
-#pragma unroll 8
-            for (int d = 0; d < D; d += 4) top = q8_abs_top(top, load4(d));
-            const float sc = mma_row_scale(top, 13);
-            q_back[t.piece & 3][i] = 1.f / sc;
-#pragma unroll 1
-            for (int c0 = 0; c0 < D / 2; c0 += 16) {
-                float qh[16], ql[16];
-#pragma unroll
-                for (int c = 0; c < 16; c += 2) {
-                    const float4 y = load4(2 * (c0 + c));
-                    uint32_t h0, l0, h1, l1;
-                    mma_split(y.x * sc, y.y * sc, h0, l0);
-                    mma_split(y.z * sc, y.w * sc, h1, l1);
-                    qh[c] = __uint_as_float(h0);
-                    qh[c + 1] = __uint_as_float(h1);
-                    ql[c] = __uint_as_float(l0);
-                    ql[c + 1] = __uint_as_float(l1);
-                }
-                tmem_st16(tmem + lanes + C::kColQhi + c0, qh);
-                tmem_st16(tmem + lanes + C::kColQlo + c0, ql);
-            }
-            tmem_wait_st();
+            row_queries<D>(a, t, w, lane, tmem + lanes + C::kColQhi, tmem + lanes + C::kColQlo, q_back[t.piece & 3]);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full);
