@@ -35,7 +35,7 @@
 // there to the weights), and the roles together issue most of a tile's slots once packed f32
 // instructions count twice.  More instructions in the softmax show (always masked: 476 us where 446
 // was), and so does more code: with the next 16 scores loaded ahead in a loop twice as long, 463.  A
-// change of piece costs 16 000 cycles more (code that runs once a piece is fetched anew).
+// change of piece costs a CTA some 16 000 cycles more: queries, the output's rows, an empty pipeline.
 #include <cstring>
 #include <mutex>
 
