@@ -16,6 +16,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import operator
 import os
 import threading
 
@@ -908,7 +909,8 @@ def paged_write(k_pool, v_pool, k_new, v_new, slots, *, stream=None):
 @functools.lru_cache(maxsize=256)
 def _paged_params(rows, pages, requests, max_rows, page_size, max_pages, heads, kv_heads, head_dim, tree, scale, softcap,
                   kernel, window, sinks, q8):
-    """(params, workspace bytes) of a paged call; read only, so one for all equal calls."""
+    """(params, workspace bytes) of a paged call; read only, so one for all equal calls.  Its
+    arguments are plain ints and floats: a tensor would be known by its identity, and could change."""
     p = vtmu_paged_params(rows=rows, pages=pages, requests=requests, max_rows=max_rows, page_size=page_size,
                           max_pages=max_pages, heads=heads, kv_heads=kv_heads, head_dim=head_dim, tree=tree,
                           has_scale=0 if scale is None else 1, scale=0.0 if scale is None else scale, softcap=softcap,
@@ -922,11 +924,12 @@ def _paged_call(q, width, pool_rows, block_table, lens, cu_rows, heads, headDim,
     v_new, masks, positions)."""
     import torch
     dev = q.device
-    f32, i32 = torch.float32, torch.int32
+    f32, i32, whole = torch.float32, torch.int32, operator.index
     _need("q", q, f32, dev)
     for name, t in (("block_table", block_table), ("lens", lens), ("cu_rows", cu_rows)):
         _need(name, t, i32, dev)
-    hk = heads if kvHeads is None else kvHeads
+    heads, headDim, pageSize = whole(heads), whole(headDim), whole(pageSize)
+    hk = heads if kvHeads is None else whole(kvHeads)
     rows, n = q.shape[0], lens.shape[0]
     if (not 0 < pageSize < 1 << 31 or q.shape != (rows, heads * headDim) or width != hk * headDim or
             pool_rows % pageSize or block_table.dim() != 2 or block_table.shape[0] != n or cu_rows.shape != (n + 1,)):
@@ -949,9 +952,10 @@ def _paged_call(q, width, pool_rows, block_table, lens, cu_rows, heads, headDim,
         _need("out", out, f32, dev)
         if out.shape != q.shape:
             raise ValueError("paged_attention: out [rows, heads*headDim]")
-    p, nbytes = _paged_params(rows, pool_rows // pageSize, n, max(min(maxRows, rows), -1), pageSize, block_table.shape[1],
-                              heads, hk, headDim, 0 if tree is None else 1, scale, softcap or 0.0, kernel, window or 0,
-                              sinks or 0, q8)
+    p, nbytes = _paged_params(rows, pool_rows // pageSize, n, whole(max(min(maxRows, rows), -1)), pageSize,
+                              block_table.shape[1], heads, hk, headDim, 0 if tree is None else 1,
+                              None if scale is None else float(scale), float(softcap or 0.0), whole(kernel),
+                              whole(window or 0), whole(sinks or 0), q8)
     return p, nbytes, out, k_new, v_new, masks, positions
 
 
@@ -1094,9 +1098,12 @@ def make_norm_rope_params(*, headDim, norm=True, eps=1e-6, weightOffset=0.0, sec
     return p
 
 
+_ROPE_VALUES = dict(base=float, attentionFactor=float, rotaryDim=int, interleaved=bool)  # what make_rope_params reads them as
+
+
 @functools.lru_cache(maxsize=64)
 def _norm_rope_params(headDim, norm, eps, weightOffset, sections, dealt, rope):
-    """make_norm_rope_params of equal calls; read only."""
+    """make_norm_rope_params of equal calls; read only, its arguments plain numbers."""
     return make_norm_rope_params(headDim=headDim, norm=norm, eps=eps, weightOffset=weightOffset, sections=sections,
                                  dealt=dealt, **dict(rope))
 
@@ -1135,9 +1142,10 @@ def norm_rope(q, k, positions, *, headDim, qWeight=None, kWeight=None, norm=True
                 _need(name, t, f32, dev)
                 if t.shape != x.shape:
                     raise ValueError("norm_rope: out as q and k")
-    args = (headDim, norm, eps, weightOffset, None if sections is None else tuple(sections), dealt, tuple(rope.items()))
     if rope.get("scaling") is None and rope.get("invFreq") is None:
-        p = _norm_rope_params(*args)
+        p = _norm_rope_params(int(headDim), bool(norm), float(eps), float(weightOffset),
+                              None if sections is None else tuple(int(n) for n in sections), bool(dealt),
+                              tuple((k, x if x is None or k not in _ROPE_VALUES else _ROPE_VALUES[k](x)) for k, x in rope.items()))
     else:  # may not be hashable, or change
         p = make_norm_rope_params(headDim=headDim, norm=norm, eps=eps, weightOffset=weightOffset, sections=sections,
                                   dealt=dealt, **rope)
