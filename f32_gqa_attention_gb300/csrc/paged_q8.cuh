@@ -75,6 +75,15 @@ __device__ __forceinline__ uint32_t q8_codes4(const float4& x, const Q8Scale& s)
            (uint32_t)q8_code<FORM>(x.w, s) << 24;
 }
 
+// What takes a sum of products of codes and scaled queries to a score: a key's scale times the row's
+// `back`.  At most the largest number: a product beyond it, of scales whose codes and
+// queries cancel to 0, would make a NaN of that (and a sum that is not 0 leaves f32 with either).
+__device__ __forceinline__ float q8_score_unit(float scale, float back) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(scale * back), "f"(3.402823466e38f));
+    return r;
+}
+
 // The number that a code stands for, before its scale.
 template <int FORM>
 __device__ __forceinline__ float q8_value(uint8_t c) {

@@ -70,6 +70,9 @@ constexpr int kStats = 4;  // a tile's maximum and sum: S(n) is issued once O(n 
 constexpr int kTiles = 16;  // what it is: the fold of a tile that far back may not have begun
 constexpr int kShift = 14;  // of weights in f16
 constexpr int kFar = 6;     // log2 by which a tile's scales may differ on the short way
+// Scores of the MMA are sums of headDim products of at most 2^14 and 448, below 2^30: times a key's scale
+// below this one they stay in f32.
+constexpr float kFarKey = 0x1p98f;
 enum : int { kFirst = 1, kLast = 2, kStop = 4, kSlotShift = 3 };  // flags of a tile; slot + 1 above them
 enum : unsigned int {
     kErrQ8Load = 1u << 3,  // the paged kernels' bits: a tile that did not come,
@@ -295,6 +298,20 @@ struct RowTile {
     uint64_t see;      // keys that it sees (not read when WHOLE)
     float rf, cap;     // a score of the MMA times ks rf is one in base-2 units (the argument of tanh with a cap)
 };
+// Scores beside keys of kFarKey and more (rare): times ks rf in one, which is in range where the score is,
+// back to tensor memory; their keys then have scales of 1.
+__device__ __forceinline__ void far_scores(const RowTile& r) {
+#pragma unroll 1
+    for (int c = 0; c < kHalf; c += 16) {
+        float x[16];
+        tmem_ld16(r.at + c, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] *= q8_score_unit(r.ks[c + k], r.rf);
+        tmem_st16(r.at + c, x);
+    }
+    tmem_wait_st();
+}
 // 16 scores from key k0 on: in base-2 units with a cap, else still to be multiplied by rf.
 template <bool CAP, bool WHOLE>
 __device__ __forceinline__ void row_scores(const RowTile& r, int k0, float (&x)[16]) {
@@ -484,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ float q_back[4][kM];              // by piece: what the queries' power of two takes back
     __shared__ float stat[kStats][4][kM];        // by tile: m, l of either half, factor of its output
     __shared__ float meet[2][2][kM];             // what the halves of a row tell one another
+    __shared__ __align__(16) float ones[kHalf];  // scales of keys whose scores have theirs
     __shared__ int piece_end[4];                 // by piece: the tile after it
     __shared__ int v_rows[kRingV];               // of a tile that there are, as V's producer knows; -1: the end
 
@@ -516,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&q_full, 4);
         fence_barrier_init();
     }
+    if (threadIdx.x < kHalf) ones[threadIdx.x] = 1.f;
     if (warp == 1) tmem_alloc(&tmem_base_s, 512);
     // The requests' tiles and their running sum.
     long long carry = 0;
@@ -905,6 +924,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!all) {
                 auto below = [](int c) -> uint64_t { return c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1; };
                 rt.see = below(hi - key + 1) & (~below(lo - key) | below(sinks - key));
+            }
+            const float2 ks2 = reinterpret_cast<const float2*>(rt.ks)[lane];
+            if (__any_sync(FULL, fmaxf(ks2.x, ks2.y) >= kFarKey)) {
+                far_scores(rt);
+                rt.ks = ones;
+                rt.rf = 1.f;
             }
             bool ok;
             const float m = larger(whole ? row_max<CAP, true>(rt) : row_max<CAP, false>(rt), ok);

@@ -1,0 +1,47 @@
+"""The 8-bit caches' attention and norm_rope at the ends of f32's range, against plain 64-bit
+implementations.
+
+Tolerance of attention, by row and head, whose outputs differ in size: 2^-15 of the 2-norm, as of
+test_rows_of_any_size (a score's products are each off by 2^-20 of their size, sizes add up to less
+than 2^3, so a weight is off by less than 2^-17 of itself and an output by 2^-16)."""
+import numpy as np
+import pytest
+
+import paged_q8_ref as q8
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import f32_gqa_attention_gb300 as vtmu  # noqa: E402
+from test_gpu_paged import dev  # noqa: E402
+from test_gpu_paged_q8 import CUDA, FORMS, TENSOR, attend, expect, size_of  # noqa: E402
+
+
+def check_heads(got, want, D):
+    got, want = (x.reshape(-1, D).astype(np.float64) for x in (got, want))
+    assert np.all(np.isfinite(got)), np.flatnonzero(~np.isfinite(got).all(1))
+    biggest = np.abs(want).max(1, keepdims=True) + (np.abs(want).max(1, keepdims=True) == 0)  # squares would overflow
+    err, norm = (np.linalg.norm(x / biggest, axis=1) for x in (got - want, want))
+    assert np.all(err <= 2.0 ** -15 * norm), (err / norm).max()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows", [3, 20])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("power,q_power", [(118, -100), (112, -96), (100, -90)])
+def test_scores_of_large_keys_stay_in_range(power, q_power, D, rows, form):
+    """Keys all alike but for their sign: those of the larger score weigh the same, the others nothing.
+    The codes times the scaled queries times the keys' scale alone would leave f32."""
+    size = size_of(4, 2, D, 16)
+
+    def gain(k, v):
+        g = np.random.default_rng(5)
+        k[:] = np.where(g.random((k.shape[0], 1)) < 0.5, -1, 1) * 2.0 ** power
+        return k, v
+
+    d = q8.batch(20, [300, 70], [rows, 2], form=form, gain=gain, waste=0.0, **size)
+    d["q"][:] = 2.0 ** q_power
+    check_heads(attend(d, kernel=TENSOR, **size), expect(d, **size), D)
