@@ -16,11 +16,12 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
 
-// The power of two that brings a row's largest |element| to [2^bits, 2^(bits + 1)); it
-// and its inverse are normal numbers.
+// The power of two that brings a row's largest |element| to [2^bits, 2^(bits + 1)), or, where that is
+// above 2^126, 2^126: it and its inverse are normal numbers.  With bits 8 and 13 that leaves normal elements
+// at 1 and more, whose 22 bits f16 pairs hold (they end at 2^-24).
 __device__ __forceinline__ float mma_row_scale(float top, int bits) {
     int e = (int)(__float_as_uint(top) >> 23) - 127;
-    e = e < -100 ? -100 : e > 127 ? 127 : e;
+    e = e < bits - 126 ? bits - 126 : e > 127 ? 127 : e;
     return __uint_as_float((uint32_t)(bits - e + 127) << 23);
 }
 

@@ -45,3 +45,18 @@ def test_scores_of_large_keys_stay_in_range(power, q_power, D, rows, form):
     d = q8.batch(20, [300, 70], [rows, 2], form=form, gain=gain, waste=0.0, **size)
     d["q"][:] = 2.0 ** q_power
     check_heads(attend(d, kernel=TENSOR, **size), expect(d, **size), D)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows", [3, 20])
+@pytest.mark.parametrize("power", [118, 124])
+@pytest.mark.parametrize("softcap", [None, 20.0])
+@pytest.mark.parametrize("D,tree", [(64, False), (128, False), (64, True)])
+def test_large_keys_and_small_queries(D, tree, softcap, power, rows, form):
+    """Scores of ordinary size, on the tensor cores."""
+    size = size_of(4, 2, D, 16)
+    d = q8.batch(21, [300, 70], [rows, 2], form=form, tree=tree, gain=lambda k, v: (k * np.float32(2.0 ** power), v), **size)
+    d["q"] = d["q"] * np.float32(2.0 ** -power)
+    if tree:
+        d["tree"][0][:] *= np.float32(2.0 ** power)
+    check_heads(attend(d, kernel=TENSOR, softcap=softcap, **size), expect(d, softcap=softcap, **size), D)
