@@ -38,8 +38,8 @@ __device__ __forceinline__ float apply_cap(const PagedDesc& a, float dot) {
     return a.softcap_on ? a.cap_log2 * softcap_tanh(dot * a.qk_mul) : dot * a.qk_mul;
 }
 
-// FORM: what the pool holds.  Codes are taken as the numbers they stand for, a row's
-// scale multiplies its score and its value; drafted rows are f32 all the same.
+// FORM: what the pool holds.  Codes are taken as the numbers they stand for, each times its row's
+// scale; drafted rows are f32 all the same.
 template <bool VEC4, int FORM>
 __global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc a, const Q8Pools p8) {
     __shared__ __align__(16) float sq[kR][kMaxD];
@@ -152,10 +152,13 @@ __global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc
             }
         }
         if constexpr (FORM != kFormF32) {
+            // The elements themselves, code x scale: products of codes and large queries may leave f32 where a
+            // score does not.
             if (any && kcode) {
+                const float ks = __ldg(p8.k_scale + coded);
                 if constexpr (VEC4) {
                     for (int d = 0; d < D; d += 4) {
-                        const float4 kv = q8_values4<FORM>(__ldg(reinterpret_cast<const uint32_t*>(kcode + d)), 1.f);
+                        const float4 kv = q8_values4<FORM>(__ldg(reinterpret_cast<const uint32_t*>(kcode + d)), ks);
 #pragma unroll
                         for (int r = 0; r < kR; ++r) {
                             const float4 qv = *reinterpret_cast<const float4*>(&sq[r][d]);
@@ -164,14 +167,11 @@ __global__ void __launch_bounds__(32 * kWarps) paged_ffma_kernel(const PagedDesc
                     }
                 } else {
                     for (int d = 0; d < D; ++d) {
-                        const float kv = q8_value<FORM>(__ldg(kcode + d));
+                        const float kv = q8_value<FORM>(__ldg(kcode + d)) * ks;
 #pragma unroll
                         for (int r = 0; r < kR; ++r) x[r] = fmaf(sq[r][d], kv, x[r]);
                     }
                 }
-                const float ks = __ldg(p8.k_scale + coded);
-#pragma unroll
-                for (int r = 0; r < kR; ++r) x[r] *= ks;
             }
         }
         float p[kR];

@@ -60,3 +60,13 @@ def test_large_keys_and_small_queries(D, tree, softcap, power, rows, form):
     if tree:
         d["tree"][0][:] *= np.float32(2.0 ** power)
     check_heads(attend(d, kernel=TENSOR, softcap=softcap, **size), expect(d, softcap=softcap, **size), D)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows", [3, 20])
+@pytest.mark.parametrize("power", [118, 124, -118, -124])
+def test_far_queries_and_keys_on_the_cuda_cores(power, rows, form):
+    size = size_of(4, 2, 64, 16)
+    d = q8.batch(23, [300, 70], [rows, 2], form=form, gain=lambda k, v: (k * np.float32(2.0 ** -power), v), **size)
+    d["q"] = d["q"] * np.float32(2.0 ** power)
+    check_heads(attend(d, kernel=CUDA, **size), expect(d, **size), 64)
