@@ -73,7 +73,8 @@ constexpr int kFar = 6;     // log2 by which a tile's scales may differ on the s
 // Scores of the MMA are sums of headDim products of at most 2^14 and 448, below 2^30: times a key's scale
 // below this one they stay in f32.
 constexpr float kFarKey = 0x1p98f;
-enum : int { kFirst = 1, kLast = 2, kStop = 4, kSlotShift = 3 };  // flags of a tile; slot + 1 above them
+// Flags of a tile; slot + 1 in two bits from kSlotShift on.  K's converters add kFarKeys where a key's scale is kFarKey or more.
+enum : int { kFirst = 1, kLast = 2, kStop = 4, kSlotShift = 3, kFarKeys = 32 };
 enum : unsigned int {
     kErrQ8Load = 1u << 3,  // the paged kernels' bits: a tile that did not come,
     kErrQ8Free = 1u << 4,  // a buffer that was not given back,
@@ -300,15 +301,15 @@ struct RowTile {
 };
 // Scores beside keys of kFarKey and more (rare): times ks rf in one, which is in range where the score is,
 // back to tensor memory; their keys then have scales of 1.
-__device__ __forceinline__ void far_scores(const RowTile& r) {
+__device__ __noinline__ void far_scores(uint32_t at, const float* ks, float rf) {
 #pragma unroll 1
     for (int c = 0; c < kHalf; c += 16) {
         float x[16];
-        tmem_ld16(r.at + c, x);
+        tmem_ld16(at + c, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] *= q8_score_unit(r.ks[c + k], r.rf);
-        tmem_st16(r.at + c, x);
+        for (int k = 0; k < 16; ++k) x[k] *= q8_score_unit(ks[c + k], rf);
+        tmem_st16(at + c, x);
     }
     tmem_wait_st();
 }
@@ -898,7 +899,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0;; ++n) {
             if (!warp_wait(&s_full[n % kScores], n / kScores, kErrQ8Mma)) break;
             const Tile t = tile_s[n % kTiles];
-            if (t.flags & kStop) break;
+            RowTile rt;
+            rt.at = tmem + lanes + C::kColS + (n % kScores) * kKT + kHalf * half;
+            rt.ks = k_scale[n % kRing] + kHalf * half;
+            rt.rf = q_back[t.piece & 3][i];
+            if (t.flags & (kStop | kFarKeys)) {
+                if (t.flags & kStop) break;
+                tc_fence_after();
+                far_scores(rt.at, rt.ks, rt.rf);
+                rt.ks = ones;
+                rt.rf = 1.f;
+            }
             if (t.piece != piece) {
                 piece = t.piece;
                 const Q8Req rq = q8_load_req(a, t.b);
@@ -915,21 +926,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int key = t.key + kHalf * half;
             const bool all = !alive || (hi - key >= kHalf - 1 && lo <= key);
             const bool whole = __all_sync(FULL, all);
-            RowTile rt;
-            rt.at = tmem + lanes + C::kColS + (n % kScores) * kKT + kHalf * half;
-            rt.ks = k_scale[n % kRing] + kHalf * half;
             rt.see = ~0ull;
-            rt.rf = q_back[piece & 3][i];
             rt.cap = a.cap_log2;
             if (!all) {
                 auto below = [](int c) -> uint64_t { return c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1; };
                 rt.see = below(hi - key + 1) & (~below(lo - key) | below(sinks - key));
-            }
-            const float2 ks2 = reinterpret_cast<const float2*>(rt.ks)[lane];
-            if (__any_sync(FULL, fmaxf(ks2.x, ks2.y) >= kFarKey)) {
-                far_scores(rt);
-                rt.ks = ones;
-                rt.rf = 1.f;
             }
             bool ok;
             const float m = larger(whole ? row_max<CAP, true>(rt) : row_max<CAP, false>(rt), ok);
@@ -974,6 +975,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             unsigned char* from = codes + (size_t)(st + kv * kStages) * C::kCodes;
             unsigned char* to = (kv ? vtiles : ktiles) + sl * C::kTile;
+            if (!kv) {
+                const bool far = k_scale[n % kRing][32 * w + lane] >= kFarKey;
+                if (__any_sync(FULL, far) && lane == 0) atomicOr(&tile_s[n % kTiles].flags, (int)kFarKeys);
+            }
             if (FORM == kFormE4m3 && rows < kKT) clear_rows<D>(from, rows, w, lane);
             convert<D, FORM>(from, to, w, lane);
             asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA
