@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(32 * kMostWarps) q8_draft_kernel(const __grid_
                 }
             }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[k][e] *= ks[e >> 1] * rf[e & 1];
+        for (int e = 0; e < 4; ++e) x[k][e] *= q8_score_unit(ks[e >> 1], rf[e & 1]);
     }
     if (a.softcap_on) {
 #pragma unroll

@@ -363,7 +363,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
     if (warp >= consumers) return;
     const int group = warp / g.hb, head_w = warp - group * g.hb;
     uint32_t qf[KC][4][NT][4];  // hi and lo, two registers each, of k-step s of chunk c
-    float o[MT][NT][4], m[NT][2], l[NT][2], r[NT][2], unit[NT][2], rf[NT][2];
+    // What the queries' power of two takes back, as a factor of at most 1 for the keys' scales and one of at
+    // least 1 for the scores: neither a scale's product nor a score then leaves f32 where x2 does
+    // not, and a score of 0 stays 0.
+    float rf[NT][2], up[NT][2];
+    float o[MT][NT][4], m[NT][2], l[NT][2], r[NT][2], unit[NT][2];
     int hi[NT][2], lo[NT][2];
     float limit = -1.f;  // a tile whose scales are at most this takes the fast way
     Q8Req rq{};
@@ -432,6 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     rf[nt][e] = __shfl_sync(FULL, back, 4 * (2 * t4 + e));
+                    up[nt][e] = fmaxf(rf[nt][e], 1.f);
+                    rf[nt][e] = fminf(rf[nt][e], 1.f);
                     const int w = tile.rb * NV + 8 * nt + 2 * t4 + e, tw = w / a.G;
                     const bool on = w < rq.T * a.G;
                     int p = a.tree ? rq.len : rq.len - rq.n + tw;
@@ -496,7 +502,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[b][nt][e] = a.cap_log2 * softcap_tanh(x[b][nt][e]);
+                    for (int e = 0; e < 4; ++e) {
+                        const float f = up[nt][e & 1];
+                        x[b][nt][e] = a.cap_log2 * softcap_tanh(x[b][nt][e] * f) * (1.f / f);
+                    }
         }
         // ---- mask: bit (b, nt, e) of `see` ----
         uint32_t see = FULL;
@@ -536,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                mt[nt][e] = fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e]));
+                mt[nt][e] = fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e])) * up[nt][e];
                 beaten = beaten || mt[nt][e] > m[nt][e] + kLazy;
             }
         if (__any_sync(FULL, beaten)) {
@@ -582,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float mu = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-                        const float p = fast_exp2(x[b][nt][e] - mu);
+                        const float p = fast_exp2(fmaf(x[b][nt][e], up[nt][e & 1], -mu));
                         l[nt][e & 1] += p;
                         w[b][nt][e] = p * (vs[b][e >> 1] * unit[nt][e & 1]);
                     }
@@ -598,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) top = fmaxf(top, (x[b][nt][2 * h + e] - mu) + power(b, h));
+                        for (int h = 0; h < 2; ++h) top = fmaxf(top, fmaf(x[b][nt][2 * h + e], up[nt][e], -mu) + power(b, h));
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, off));
                     // Products up to 2^(top + 1): r from there, at most the largest exponent.
@@ -617,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const float y = x[b][nt][2 * h + e] - mu, ex = power(b, h);
+                            const float y = fmaf(x[b][nt][2 * h + e], up[nt][e], -mu), ex = power(b, h);
                             // The mantissa of the scale (0 stays 0), its exponent in the power.
                             const float f = vs[b][h] * (ex > 0.f ? exp2f(-ex) : exp2f(-ex - 1.f) * 2.f);
                             l[nt][e] += fast_exp2(y);

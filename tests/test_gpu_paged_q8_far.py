@@ -64,9 +64,57 @@ def test_large_keys_and_small_queries(D, tree, softcap, power, rows, form):
 
 @pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("rows", [3, 20])
+@pytest.mark.parametrize("kernel", [CUDA, TENSOR])
+def test_some_large_keys_beside_small_ones(kernel, rows, form):
+    """Keys of 2^120 that a window hides, or that are orthogonal to the queries, in the tiles of ordinary ones."""
+    size = size_of(4, 2, 64, 16)
+
+    def gain(k, v):
+        k[:, ::64] = 0
+        k[::3, 1:] = 0
+        k[::3, ::64] = 2.0 ** 120  # beside a query of 0 there
+        return k, v
+
+    d = q8.batch(22, [300, 70], [rows, 2], form=form, gain=gain, waste=0.0, **size)
+    d["q"][:, ::64] = 0
+    check_heads(attend(d, kernel=kernel, **size), expect(d, **size), 64)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows", [3, 20])
 @pytest.mark.parametrize("power", [118, 124, -118, -124])
 def test_far_queries_and_keys_on_the_cuda_cores(power, rows, form):
     size = size_of(4, 2, 64, 16)
     d = q8.batch(23, [300, 70], [rows, 2], form=form, gain=lambda k, v: (k * np.float32(2.0 ** -power), v), **size)
     d["q"] = d["q"] * np.float32(2.0 ** power)
     check_heads(attend(d, kernel=CUDA, **size), expect(d, **size), 64)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows", [3, 20])
+@pytest.mark.parametrize("power", [118, 124])
+def test_large_queries_and_small_keys(power, rows, form):
+    size = size_of(4, 2, 64, 16)
+    d = q8.batch(24, [300, 70], [rows, 2], form=form, gain=lambda k, v: (k * np.float32(2.0 ** -power), v), **size)
+    d["q"] = d["q"] * np.float32(2.0 ** power)
+    check_heads(attend(d, kernel=TENSOR, **size), expect(d, **size), 64)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows", [3, 20])
+def test_scores_of_zero_between_large_rows(rows, form, tree):
+    """Queries along one channel, keys along another: every key weighs the same."""
+    size = size_of(4, 2, 64, 16)
+
+    def gain(k, v):
+        k[:] = 0
+        k[:, 1::64] = 2.0 ** 100
+        return k, v
+
+    d = q8.batch(25, [90, 40], [rows, 2], form=form, tree=tree, gain=gain, **size)
+    d["q"][:] = 0
+    d["q"][:, ::64] = 2.0 ** 100
+    if tree:
+        gain(d["tree"][0], None)
+    check_heads(attend(d, kernel=TENSOR, **size), expect(d, **size), 64)
