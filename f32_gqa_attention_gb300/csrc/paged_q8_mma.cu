@@ -176,7 +176,10 @@ __device__ __forceinline__ int v_chunk(int row, int c) {
     return c ^ (D == 128 ? ((row >> 1) & 3) << 1 : (row >> 1) & 3);
 }
 
-template <int D, int NT, int FORM>
+// GROUPS: more than one key group (fewer than five KV heads).  Without their join in it the kernel
+// takes 80.8 us instead of 83.3 for 32 requests of 517 to 8111 rows over 8 heads, 193 instead of 196
+// for 24 of 8192 to 32704 (replayed graphs, caches flushed).
+template <int D, int NT, int FORM, bool GROUPS>
 __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_constant__ MmaArgs g) {
     constexpr int NV = 8 * NT, S = kStages, KC = D / 64, MT = D / 16;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
     // Shares of the launch's registers: 8 x 224 + 4 x 56 = 12 x 168 a lane.
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     if (warp >= consumers) return;
-    const int group = warp / g.hb, head_w = warp - group * g.hb;
+    const int group = GROUPS ? warp / g.hb : 0, head_w = warp - group * g.hb;
     uint32_t qf[KC][4][NT][4];  // hi and lo, two registers each, of k-step s of chunk c
     // What the queries' power of two takes back, as a factor of at most 1 for the keys' scales and one of at
     // least 1 for the scores: neither a scale's product nor a score then leaves f32 where x2 does
@@ -704,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
             const int slot = ((tile.flags >> kSlotShift) & 3) - 1;
             // Key groups: the others leave theirs as partials in slot 2, group 0 takes them in.
             const uint32_t turn = (uint32_t)(pieces++ & 1);
-            if (g.kg > 1) {
+            if (GROUPS) {
                 uint64_t* bar = group ? &x_got : &x_put;
                 if ((group == 0 || pieces > 1) && !__all_sync(FULL, mbar_wait(bar, group ? turn ^ 1 : turn))) {
                     raise_device_error(&g_q8_device_error, kErrQ8Load);
@@ -728,19 +731,30 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
                             y[2 * k + 1] = o[k][nt][2 + e] * inv * back;
                         }
                     }
-                    if (g.kg > 1 && group == 0) {  // by the log-sum-exp rule, in the groups' order
-                        float all = top;
-                        for (int k = 1; k < g.kg; ++k) all = fmaxf(all, __ldcg(g.part_m + part_row(2, k * g.hb + head_w, i)));
-                        // A part that saw nothing has no weight; one that comes to 0 counts (0 x inf is NaN).
-                        float den = sum != 0.f ? fast_exp2(top - all) * sum : 0.f;
+                    if (GROUPS && group == 0) {  // by the log-sum-exp rule: the row's lane gr has group gr's part
+                        float all = top, share = sum;
+                        if (gr > 0) {
+                            const int64_t at = part_row(2, gr * g.hb + head_w, i);
+                            all = gr < g.kg ? __ldcg(g.part_m + at) : -INFINITY;
+                            share = gr < g.kg ? __ldcg(g.part_l + at) : 0.f;
+                        }
+                        const float mine = all;
 #pragma unroll
-                        for (int k = 0; k < D / 8; ++k) y[k] = sum != 0.f ? y[k] * den : 0.f;
+                        for (int off = 4; off < 32; off <<= 1) all = fmaxf(all, __shfl_xor_sync(FULL, all, off));
+                        // A part that saw nothing has no weight (-0); one that comes to 0 counts (0 x inf is NaN).
+                        share = share != 0.f ? fast_exp2(mine - all) * share : -0.f;
+                        float den = share;
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) den += __shfl_xor_sync(FULL, den, off);
+                        // Shares of the whole sum, so that what is added up stays below the largest value.
+                        share *= den != 0.f ? 1.f / den : 0.f;
+                        const float own = __shfl_sync(FULL, share, t4);
+#pragma unroll
+                        for (int k = 0; k < D / 8; ++k) y[k] = q8_nothing(own) ? 0.f : y[k] * own;
                         for (int k = 1; k < g.kg; ++k) {
+                            const float w = __shfl_sync(FULL, share, 4 * k + t4);
+                            if (q8_nothing(w)) continue;
                             const int64_t at = part_row(2, k * g.hb + head_w, i);
-                            const float lk = __ldcg(g.part_l + at);
-                            if (lk == 0.f) continue;
-                            const float w = fast_exp2(__ldcg(g.part_m + at) - all) * lk;
-                            den += w;
 #pragma unroll
                             for (int d = 0; d < D / 8; d += 4) {
                                 const float4 z = __ldcg(reinterpret_cast<const float4*>(g.part_o + at * D + (D / 8) * gr + d));
@@ -750,14 +764,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
                                 y[d + 3] = fmaf(w, z.w, y[d + 3]);
                             }
                         }
-                        const float inv = den != 0.f ? 1.f / den : 0.f;
-#pragma unroll
-                        for (int k = 0; k < D / 8; ++k) y[k] *= inv;
                         sum = den;
                         top = all;
                     }
                     float* to = nullptr;
-                    const int where = group ? 2 : slot;
+                    const int where = GROUPS && group ? 2 : slot;
                     if (where < 0) {
                         if (v < rq.T * a.G) {
                             const int64_t row = ((int64_t)rq.row0 + t) * a.H + (int64_t)hk * a.G + (v - t * a.G);
@@ -790,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
                             *reinterpret_cast<float4*>(to + d) = make_float4(y[d], y[d + 1], y[d + 2], y[d + 3]);
                     }
                 }
-            if (g.kg > 1) {
+            if (GROUPS) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(group ? &x_put : &x_got);
             }
@@ -898,7 +909,7 @@ cudaError_t launch_form(MmaArgs& g, int num_sms, void* workspace, cudaStream_t s
     g.head = reinterpret_cast<int4*>(ws + s.head);
     float2* draft = reinterpret_cast<float2*>(ws + s.draft);
     g.draft = draft;
-    auto kern = q8_mma_kernel<D, NT, FORM>;
+    auto kern = g.kg > 1 ? q8_mma_kernel<D, NT, FORM, true> : q8_mma_kernel<D, NT, FORM, false>;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), (int)kSmemMost);
     if (e != cudaSuccess) return e;
     const size_t smem = (size_t)kStages * g.stage + (size_t)(a.B + 1) * 8;

@@ -73,6 +73,10 @@ constexpr int kFar = 6;     // log2 by which a tile's scales may differ on the s
 // Scores of the MMA are sums of headDim products of at most 2^14 and 448, below 2^30: times a key's scale
 // below this one they stay in f32.
 constexpr float kFarKey = 0x1p98f;
+// A tile's output, below 2^31, times its factor and added to those of up to 2^24 tiles stays in f32 where the
+// factor is below this one.  Rows that meet a larger one keep their sums times 2^-32 from there on: up to 2^31
+// weights of at most 1 times any value fit, and what that drops lies below 2^-117.
+constexpr float kHugeFactor = 0x1p72f;
 // Flags of a tile; slot + 1 in two bits from kSlotShift on.  K's converters add kFarKeys where a key's scale is kFarKey or more.
 enum : int { kFirst = 1, kLast = 2, kStop = 4, kSlotShift = 3, kFarKeys = 32 };
 enum : unsigned int {
@@ -788,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool more = warp_wait(&k_ready[0], 0, kErrQ8Mma) && load_queries(0);
         int loaded = 0;     // pieces after the first whose queries are in; -1: there are no more
         int folded = 0;     // pieces that are done: tile n is one of the next piece's
-        float acc[D], M = -INFINITY, L = 0.f;
+        float acc[D], M = -INFINITY, L = 0.f, down = 1.f;  // down: of acc
 #pragma unroll
         for (int d = 0; d < D; ++d) acc[d] = 0.f;
         for (int n = 0; more; ++n) {
@@ -818,12 +822,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float alpha = fast_exp2(M - mu), beta = fast_exp2(mt - mu);
             M = Mn;
             L = fmaf(L, alpha, lt * beta);
-            const float bo = beta * st[3 * kM];
-            if (__any_sync(FULL, alpha != 1.f)) {  // a maximum moved
-                const uint64_t al = f2_pack(alpha, alpha);
+            const float factor = beta * st[3 * kM];
+            if (__any_sync(FULL, alpha != 1.f || factor >= kHugeFactor)) {  // a maximum moved, or a factor is huge
+                float by = alpha;
+                if (factor >= kHugeFactor && down == 1.f) {
+                    by *= 0x1p-32f;
+                    down = 0x1p-32f;
+                }
+                const uint64_t al = f2_pack(by, by);
 #pragma unroll
                 for (int d = 0; d < D; d += 2) f2_unpack(f2_mul(f2_pack(acc[d], acc[d + 1]), al), acc[d], acc[d + 1]);
             }
+            const float bo = factor * down;
             const uint64_t be = f2_pack(bo, bo);
             const uint32_t at = tmem + lanes + C::kColO;
 #pragma unroll
@@ -844,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t.flags & kLast) {
                 const int slot = ((t.flags >> kSlotShift) & 3) - 1, v = t.rb * kM + i;
                 const Q8Req rq = q8_load_req(a, t.b);
-                float inv = L != 0.f ? 1.f / L : 0.f;
+                float inv = L != 0.f ? 1.f / L / down : 0.f;
                 if (a.tree) pdl_wait();  // the drafted rows' part
                 if (v < rq.T * a.G) {
                     float* to;
@@ -874,6 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++folded;
                 M = -INFINITY;
                 L = 0.f;
+                down = 1.f;
 #pragma unroll
                 for (int d = 0; d < D; ++d) acc[d] = 0.f;
             }

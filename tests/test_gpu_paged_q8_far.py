@@ -118,3 +118,24 @@ def test_scores_of_zero_between_large_rows(rows, form, tree):
     if tree:
         gain(d["tree"][0], None)
     check_heads(attend(d, kernel=TENSOR, **size), expect(d, **size), 64)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows", [3, 20])
+@pytest.mark.parametrize("Hk", [1, 2, 8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_outputs_up_to_the_end_of_the_range(D, Hk, rows, form, tree):
+    """Values of 2e38 to 3e38, of one sign a column: any sum of two leaves f32."""
+    size = size_of(Hk, Hk, D, 16)
+
+    def gain(k, v):
+        g = np.random.default_rng(3)
+        sign = np.where(g.random(v.shape[1]) < 0.5, -1, 1)
+        v[:] = g.uniform(2e38, 3e38, v.shape) * sign
+        return k, v
+
+    d = q8.batch(26, [3000, 70], [rows, 2], form=form, tree=tree, gain=gain, **size)
+    if tree:
+        gain(None, d["tree"][1])
+    check_heads(attend(d, kernel=TENSOR, **size), expect(d, **size), D)
