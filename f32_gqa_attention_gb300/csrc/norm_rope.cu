@@ -40,17 +40,17 @@ __device__ __forceinline__ float2 cos_sin(const NormRopeArgs& a, const Pair& p, 
     return make_float2(c * a.attn, s * a.attn);
 }
 
-// Sums of squares that leave f32's range (elements from about 2^63 on), or its precision
+// Sums of squares that leave f32's range (elements from about 2^63 on, or beside an eps like that), or its precision
 // (all below 2^-40, with no eps to speak of), are taken once more of the elements times a
-// power of two, `pre`, which the elements then keep: kDown or kUp.  Both ends' squares fit, 256
+// power of two, `pre`, which the elements then keep: kDown or kUp.  Both ends' squares fit, 4096
 // of them too.
 constexpr float kDown = 0x1p-96f, kUp = 0x1p90f;
 __device__ __forceinline__ float pre_of(float ss, const NormRopeArgs& a) {
-    if (!(ss <= 3.0e38f)) return kDown;
+    if (!(ss + a.eps <= 3.0e38f)) return kDown;
     return ss < 0x1p-80f && a.eps < 0x1p-80f ? kUp : 1.f;
 }
 __device__ __forceinline__ float factor_of(float ss, float pre, const NormRopeArgs& a) {
-    const float eps = pre == 1.f ? a.eps : pre == kUp ? a.eps * kUp * kUp : 0.f;
+    const float eps = a.eps * pre * pre;  // below 2^100, and 0 where it says nothing beside the squares
     return rsqrtf(fmaf(ss, a.inv_d, eps));
 }
 

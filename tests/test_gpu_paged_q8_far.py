@@ -139,3 +139,16 @@ def test_outputs_up_to_the_end_of_the_range(D, Hk, rows, form, tree):
     if tree:
         gain(None, d["tree"][1])
     check_heads(attend(d, kernel=TENSOR, **size), expect(d, **size), D)
+
+
+# ----------------------------------------------------------------- norm_rope
+@pytest.mark.parametrize("D", [128, 100, 2])
+@pytest.mark.parametrize("size,eps", [(3e19, 3e38), (1e18, 1e38), (2e19, 1e36), (1e20, 3.4e38), (1e18, 3.4e38), (1.5e19, 3e38)])
+def test_an_eps_beside_squares_that_leave_the_range(D, size, eps):
+    g = np.random.default_rng(1)
+    x = (g.uniform(-1, 1, (5, 3 * D)) * size).astype(np.float32)
+    pos = np.arange(5, dtype=np.int32)
+    y, _ = vtmu.norm_rope(dev(x), None, dev(pos), headDim=D, eps=eps)
+    want, big = q8.norm_rope(x, pos, headDim=D, eps=eps)
+    # As in test_gpu_paged_q8: 2^-20 of the norm, 2^-20 of sine and cosine, 2^-22 of products and sum.
+    assert np.all(np.abs(y.cpu().numpy() - want) <= (2.0 ** -19 + 2.0 ** -22) * big)
