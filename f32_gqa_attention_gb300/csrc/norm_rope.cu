@@ -42,16 +42,19 @@ __device__ __forceinline__ float2 cos_sin(const NormRopeArgs& a, const Pair& p, 
 
 // Sums of squares that leave f32's range (elements from about 2^63 on, or beside an eps like that), or its precision
 // (all below 2^-40, with no eps to speak of), are taken once more of the elements times a
-// power of two, `pre`, which the elements then keep: kDown or kUp.  Both ends' squares fit, 4096
+// power of two, `pre`: kDown or kUp.  Both ends' squares fit, 4096
 // of them too.
 constexpr float kDown = 0x1p-96f, kUp = 0x1p90f;
 __device__ __forceinline__ float pre_of(float ss, const NormRopeArgs& a) {
     if (!(ss + a.eps <= 3.0e38f)) return kDown;
     return ss < 0x1p-80f && a.eps < 0x1p-80f ? kUp : 1.f;
 }
-__device__ __forceinline__ float factor_of(float ss, float pre, const NormRopeArgs& a) {
+// What an element is multiplied by, one after the other: `pre` first on the way up; on the way down last, where
+// small elements keep their bits (x first is at most 64 2^96).
+__device__ __forceinline__ float2 factors_of(float ss, float pre, const NormRopeArgs& a) {
     const float eps = a.eps * pre * pre;  // below 2^100, and 0 where it says nothing beside the squares
-    return rsqrtf(fmaf(ss, a.inv_d, eps));
+    const float f = rsqrtf(fmaf(ss, a.inv_d, eps));
+    return pre == kDown ? make_float2(f, pre) : make_float2(pre, f);
 }
 
 __device__ __forceinline__ float sq4(const float4& x, float f) {
@@ -130,14 +133,15 @@ __global__ void __launch_bounds__(128, 6) norm_rope_fast(const __grid_constant__
                 // The rare second sum is taken by every group of the warp where one wants it.
                 float ss = sum(1.f);
                 const float pre = pre_of(ss, a);
-                if (__any_sync(FULL, pre != 1.f)) {
-                    ss = sum(pre);
-                    p = make_float4(p.x * pre, p.y * pre, p.z * pre, p.w * pre);
-                    q = make_float4(q.x * pre, q.y * pre, q.z * pre, q.w * pre);
+                const bool far = __any_sync(FULL, pre != 1.f);
+                if (far) ss = sum(pre);
+                const float2 f = factors_of(ss, pre, a);
+                if (far) {
+                    p = make_float4(p.x * f.x, p.y * f.x, p.z * f.x, p.w * f.x);
+                    q = make_float4(q.x * f.x, q.y * f.x, q.z * f.x, q.w * f.x);
                 }
-                const float f = factor_of(ss, pre, a);
-                p = scale4(p, f, query ? wq[0] : wk[0]);
-                q = scale4(q, f, query ? wq[1] : wk[1]);
+                p = scale4(p, f.y, query ? wq[0] : wk[0]);
+                q = scale4(q, f.y, query ? wq[1] : wk[1]);
             }
             if (!live) continue;
             if (turns) {
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(256) norm_rope_any(const __grid_constant__ Nor
             const float* x = query ? a.q + (t * a.H + h) * D : a.k + (t * a.Hk + (h - a.H)) * D;
             float* o = query ? a.q_out + (t * a.H + h) * D : a.k_out + (t * a.Hk + (h - a.H)) * D;
             const float* w = query ? a.qw : a.kw;
-            float f = 1.f, pre = 1.f;
+            float2 f = make_float2(1.f, 1.f);
             if (a.norm) {
                 auto sum = [&](float m) {
                     float ss = 0.f;
@@ -188,12 +192,12 @@ __global__ void __launch_bounds__(256) norm_rope_any(const __grid_constant__ Nor
                     return ss;
                 };
                 float ss = sum(1.f);
-                pre = pre_of(ss, a);
+                const float pre = pre_of(ss, a);
                 if (pre != 1.f) ss = sum(pre);
-                f = factor_of(ss, pre, a);
+                f = factors_of(ss, pre, a);
             }
             __syncwarp();  // in place: every lane has read the head before one writes it
-            auto normed = [&](int d) { return a.norm ? x[d] * pre * f * (w ? __ldg(w + d) + a.weight_offset : 1.f) : x[d]; };
+            auto normed = [&](int d) { return a.norm ? x[d] * f.x * f.y * (w ? __ldg(w + d) + a.weight_offset : 1.f) : x[d]; };
             for (int j = lane; j < half; j += 32) {
                 const int ia = a.interleaved ? 2 * j : j, ib = a.interleaved ? 2 * j + 1 : j + half;
                 const float y = normed(ia), z = normed(ib);

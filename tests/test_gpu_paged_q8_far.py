@@ -152,3 +152,17 @@ def test_an_eps_beside_squares_that_leave_the_range(D, size, eps):
     want, big = q8.norm_rope(x, pos, headDim=D, eps=eps)
     # As in test_gpu_paged_q8: 2^-20 of the norm, 2^-20 of sine and cosine, 2^-22 of products and sum.
     assert np.all(np.abs(y.cpu().numpy() - want) <= (2.0 ** -19 + 2.0 ** -22) * big)
+
+
+@pytest.mark.parametrize("D", [128, 100])
+@pytest.mark.parametrize("top,rest", [(2.0 ** 70, 2.0 ** -50), (2.0 ** 120, 2.0 ** 5), (2.0 ** 64, 2.0 ** -55)])
+def test_small_elements_of_a_head_of_large_ones(D, top, rest):
+    """At position 0, where nothing turns: each element to 2^-20 of itself."""
+    g = np.random.default_rng(2)
+    x = (g.uniform(0.5, 1, (4, 2 * D)) * rest).astype(np.float32)
+    x[:, ::D] = top
+    pos = np.zeros(4, np.int32)
+    y, _ = vtmu.norm_rope(dev(x), None, dev(pos), headDim=D)
+    want, _ = q8.norm_rope(x, pos, headDim=D)
+    assert np.abs(want).min() >= 2.0 ** -126
+    assert np.all(np.abs(y.cpu().numpy() - want) <= 2.0 ** -20 * np.abs(want))
