@@ -1370,13 +1370,24 @@ vtmu_status vtmu_paged_attention_q8(const float* q, const void* k_pool, const vo
     return ok();
 }
 
-// The part of hi + lo behind the point, times 2^64.
-static uint64_t turn_of(double hi, double lo) {
-    hi -= std::floor(hi);  // exact
-    const double top = std::floor(std::ldexp(hi, 32)), rest = std::ldexp(hi, 32) - top;  // 32 bits, and what is left, exact
-    // rest 2^32 + lo 2^64, of either sign, onto top 2^32; carries and borrows wrap as turns do.
-    const double low = std::ldexp(rest, 32), more = std::ldexp(std::fmod(lo, 1.0), 64);
-    return ((uint64_t)top << 32) + (uint64_t)low + (uint64_t)(int64_t)std::fmin(std::fmax(std::rint(more), -9.2e18), 9.2e18);
+// The part of f / (2 pi) behind the point, times 2^64, to the nearest unit or the next: f is m 2^e with a whole m
+// of 53 bits, and of 1 / (2 pi) = sum kInv[i] 2^(-64 (i + 1)) the 128 bits behind the first e count, those before
+// them being whole turns.  The bits reach as far as the quotients of f32 numbers do.
+static uint64_t turn_of(double f) {
+    static const uint64_t kInv[6] = {0x28be60db9391054aull, 0x7f09d5f47d4d3770ull,
+                                       0x36d8a5664f10e410ull, 0x7f9458eaf7aef158ull,
+                                       0x6dc91b8e909374b8ull, 0x01924bba82746487ull};
+    typedef unsigned __int128 Wide;
+    int e;
+    const uint64_t m = (uint64_t)std::ldexp(std::frexp(std::fabs(f), &e), 53);
+    e -= 53;
+    if (m == 0 || e > 255) return 0;  // 2^128 over the least scaling factor, the largest there is, has 225
+    const int skip = e > 0 ? e : 0, word = skip / 64, bit = skip % 64;
+    auto bits = [&](int i) -> uint64_t { return bit ? kInv[i] << bit | kInv[i + 1] >> (64 - bit) : kInv[i]; };
+    const Wide all = (Wide)m * bits(word) + (((Wide)m * bits(word + 1)) >> 64);  // m / (2 pi) 2^skip, times 2^64
+    const int down = e < 0 ? -e : 0;
+    const uint64_t t = down == 0 ? (uint64_t)all : down > 127 ? 0 : (uint64_t)(((all >> (down - 1)) + 1) >> 1);
+    return f < 0 ? 0 - t : t;
 }
 
 void vtmu_norm_rope_params_init(vtmu_norm_rope_params* p) {
@@ -1452,11 +1463,8 @@ vtmu_status vtmu_norm_rope(const float* q, const float* k, const float* q_weight
     thread_local int last_half = 0;
     if (a.half > last_half || std::memcmp(rd.inv_freq, last_freq, sizeof(double) * (size_t)a.half) != 0) {
         for (int j = 0; j < a.half; ++j) {
-            // 1 / (2 pi) as a double and the double nearest its remainder: the product to 2^-100 or so.
-            const double hi = rd.inv_freq[j] * 0.15915494309189535, lo = std::fma(rd.inv_freq[j], 0.15915494309189535, -hi) +
-                                                                          rd.inv_freq[j] * -9.839338337591243e-18;
             last_freq[j] = rd.inv_freq[j];
-            last_turn[j] = turn_of(hi, lo);
+            last_turn[j] = turn_of(rd.inv_freq[j]);
         }
         last_half = a.half;
     }

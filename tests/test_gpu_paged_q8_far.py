@@ -166,3 +166,43 @@ def test_small_elements_of_a_head_of_large_ones(D, top, rest):
     want, _ = q8.norm_rope(x, pos, headDim=D)
     assert np.abs(want).min() >= 2.0 ** -126
     assert np.all(np.abs(y.cpu().numpy() - want) <= 2.0 ** -20 * np.abs(want))
+
+
+def turns(freqs, positions):
+    """position x frequency / (2 pi) less its whole part, from whole numbers of 2000 bits."""
+    bits = 2000
+
+    def atan_inv(n):  # atan(1 / n), in units of 2^-bits
+        total, term, k = 0, (1 << bits) // n, 0
+        while term:
+            total += (-term if k & 1 else term) // (2 * k + 1)
+            term //= n * n
+            k += 1
+        return total
+
+    two_pi = 8 * (4 * atan_inv(5) - atan_inv(239))  # Machin's formula
+    out = np.zeros((len(positions), len(freqs)))
+    for j, f in enumerate(freqs):
+        num, den = float(f).as_integer_ratio()
+        for t, p in enumerate(positions):
+            part = (((int(p) * num << 2 * bits) // (den * two_pi)) % (1 << bits)) >> (bits - 64)
+            out[t, j] = part / 2.0 ** 64
+    return out
+
+
+@pytest.mark.parametrize("size", [1e-20, 1e-3, 1.0, 1e9, 6e16, 3e17, 1e20, 1e30, 3e38])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("D", [64, 10])
+def test_explicit_frequencies_of_any_size(D, sign, size):
+    """Sine and cosine to 2^-20 (the angle's and the sine's own error), 2^-22 of products and sum."""
+    g = np.random.default_rng(4)
+    half = D // 2
+    freqs = (sign * size * g.uniform(0.3, 1, half)).astype(np.float32)
+    pos = np.array([0, 1, 2, 77, 100003, 2 ** 31 - 1], np.int32)
+    x = g.standard_normal((len(pos), 2 * D), dtype=np.float32)
+    y, _ = vtmu.norm_rope(dev(x), None, dev(pos), headDim=D, norm=False, invFreq=freqs.tolist())
+    th = 2 * np.pi * turns(freqs, pos)[:, None, :]
+    a, b = np.split(x.reshape(len(pos), 2, D).astype(np.float64), 2, axis=2)
+    want = np.concatenate([a * np.cos(th) - b * np.sin(th), b * np.cos(th) + a * np.sin(th)], 2)
+    bound = (2.0 ** -20 + 2.0 ** -22) * np.concatenate([np.abs(a) + np.abs(b)] * 2, 2)
+    assert np.all(np.abs(y.cpu().numpy().reshape(want.shape) - want) <= bound)
