@@ -261,6 +261,16 @@ __device__ __forceinline__ bool warp_wait3(uint64_t* a, int pa, uint64_t* b, int
     return false;
 }
 
+// No copy may be in flight when the CTA exits, whether the producer gave up or those that wait for its tiles
+// did: of n tiles asked for the last one of each stage has to be there (the one before it was when that
+// one was asked for).
+__device__ __noinline__ void drain(uint64_t* staged, int n) {
+    cp_async_wait_all();
+#pragma unroll 1
+    for (int i = max(n - kStages, 0); i < n; ++i)
+        if (!warp_wait(staged + i % kStages, i / kStages, kErrQ8Free)) break;
+}
+
 // Codes of a tile to f16: four warps, 32 rows each, a lane 16 codes at a time.  TMA leaves
 // chunk c (16 bytes) of row r at c ^ (r % 8) (headDim 128; 64: where it was).  A quarter of the
 // warp takes 64 bytes of two rows; rows r and r ^ 5 (64: neighbours) meet no bank twice, neither
@@ -591,10 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* scales = values ? g.p.v_scale : g.p.k_scale;
             // 32 boxes of a request are looked up at a time, a lane each: the first row of each in the
             // pool, -1 for rows of no page.
-            int y_cur = -1, batch = -1, of_piece = -1;
-            for (int n = 0;; ++n) {
+            int y_cur = -1, batch = -1, of_piece = -1, n = 0;
+            for (bool stop = false; !stop; ++n) {
                 Tile t;
-                const bool stop = !walk.next(a, prefix, t, empty);
+                stop = !walk.next(a, prefix, t, empty);
                 if (stop) t.flags = kStop;
                 const int st = n % kStages;
                 if (n >= kStages && !warp_wait(&unstaged[values][st], n / kStages - 1, kErrQ8Free)) break;
@@ -641,9 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 cp_async_arrive(&staged[values][st]);
-                if (stop) break;
             }
-            cp_async_wait_all();  // no copy may be in flight when the CTA exits
+            drain(staged[values], n);
             if (!values && lane == 0) {
                 g.head[2 * blockIdx.x] = walk.starts;
                 g.head[2 * blockIdx.x + 1] = make_int4(walk.starts_head, 0, 0, 0);
