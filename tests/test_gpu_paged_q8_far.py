@@ -206,3 +206,20 @@ def test_explicit_frequencies_of_any_size(D, sign, size):
     want = np.concatenate([a * np.cos(th) - b * np.sin(th), b * np.cos(th) + a * np.sin(th)], 2)
     bound = (2.0 ** -20 + 2.0 ** -22) * np.concatenate([np.abs(a) + np.abs(b)] * 2, 2)
     assert np.all(np.abs(y.cpu().numpy().reshape(want.shape) - want) <= bound)
+
+
+@pytest.mark.parametrize("D", [128, 100])
+@pytest.mark.parametrize("kw", [dict(), dict(interleaved=True), dict(sections="dealt")])
+def test_rotation_alone(D, kw):
+    """Without a norm.  The angle in f32 is off by 2^-25 (its turn), 2^-25 (the factor) and 2^-24 (the product) of
+    pi at most, 3.8e-7; the sine by 2^-21.41 and the cosine by 2^-21.19 more, 4.2e-7: 8.0e-7.  A product and an FMA
+    round at 2^-24 each of |a| + |b|: 9.2e-7, below 2^-20."""
+    g = np.random.default_rng(6)
+    T, half = 3000, D // 2
+    kw = dict(kw, sections=[half - 2 * (half // 3), half // 3, half // 3], dealt=True) if "sections" in kw else kw
+    axes = len(kw.get("sections", [0]))
+    pos = g.integers(0, 2 ** 20, (axes, T)).astype(np.int32)
+    x = g.standard_normal((T, 2 * D), dtype=np.float32)
+    y, _ = vtmu.norm_rope(dev(x), None, dev(pos if axes > 1 else pos[0]), headDim=D, norm=False, **kw)
+    want, size = q8.norm_rope(x, pos, headDim=D, norm=False, **kw)
+    assert np.all(np.abs(y.cpu().numpy() - want) <= 2.0 ** -20 * size)
