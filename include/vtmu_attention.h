@@ -717,7 +717,7 @@ typedef enum vtmu_kv_format {
  *   DEVICE.  None may overlap another.  head_dim 1..256.
  * Errors: VTMU_ERR_INVALID (null pointer with rows > 0, bad size or format,
  * misaligned or overlapping buffers), VTMU_ERR_UNSUPPORTED (head_dim above 256,
- * a size of 2^31 or more, kv_heads*head_dim of 2^30 or more), VTMU_ERR_CUDA.
+ * a size of 2^31 or more, rows*kv_heads among them, kv_heads*head_dim of 2^30 or more), VTMU_ERR_CUDA.
  */
 VTMU_API vtmu_status vtmu_paged_write_q8(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
                                          int64_t pool_rows, int32_t kv_heads, int32_t head_dim, int32_t format,
@@ -751,8 +751,11 @@ VTMU_API vtmu_status vtmu_paged_q8_workspace_size(const vtmu_paged_params* p, si
  * in both.  The tensor cores take the codes as they are (exact in f16) and keep 22 bits of the
  * largest element of each row and head of q and of drafted rows.  A weight times its value's
  * scale has 22 bits, and is kept to 2^-35 of the largest such product so far (up to 16 rows x
- * heads of a group) or to 2^-32 of the largest in its 64 keys (above; to 2^-23 where all their
- * scales are below 2^-110).  On the tensor cores a drafted head with an element that is not finite
+ * heads of a group; to 2^-25 where all scales are below 2^-116) or to 2^-32 of the largest in its
+ * 128 keys (above; to 2^-23 where all their scales are below 2^-110).  The CUDA cores' sums of
+ * weight x value overflow where the keys' number times |value| passes 3.4e38; the tensor cores' do not.
+ * With a tree and a cu_rows that falls, a row that two requests claim holds a mixture of theirs.
+ * On the tensor cores a drafted head with an element that is not finite
  * counts as NaN throughout, and an e4m3 code that is NaN (0x7f, 0xff: vtmu_paged_write_q8
  * stores none) among a request's values may make its column NaN in every row of the request.
  */
@@ -802,7 +805,7 @@ VTMU_API void vtmu_norm_rope_params_init(vtmu_norm_rope_params* p);
  *   positions [axes, T]: int32, DEVICE.  A row with a negative position on an axis
  *   is left as it was in q_out and k_out.
  * Squares are summed in f32, of elements scaled where their squares leave its range.  A
- * head of zeros with eps == 0 is 0 / 0, NaN.
+ * head of zeros with eps == 0 is 0 / 0, NaN.  Sine and cosine are off by less than 2^-20.
  * Errors: those of vtmu_rope, VTMU_ERR_INVALID (axes, sections, eps or
  * weight_offset out of range, weights without a norm, null, misaligned or
  * overlapping buffers), VTMU_ERR_UNSUPPORTED (T of 2^31 or more, or
