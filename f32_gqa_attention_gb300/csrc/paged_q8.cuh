@@ -76,8 +76,9 @@ __device__ __forceinline__ uint32_t q8_codes4(const float4& x, const Q8Scale& s)
 }
 
 // What takes a sum of products of codes and scaled queries to a score: a key's scale times the row's
-// `back`.  At most the largest number: a product beyond it, of scales whose codes and
-// queries cancel to 0, would make a NaN of that (and a sum that is not 0 leaves f32 with either).
+// `back`.  At most the largest number: a product beyond it would make a NaN of codes and queries that
+// cancel to 0.  Sums of 1 and more leave f32 with either; smaller ones are within what 22 bits of
+// queries scaled to 2^13 leave open.
 __device__ __forceinline__ float q8_score_unit(float scale, float back) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(scale * back), "f"(3.402823466e38f));

@@ -15,7 +15,7 @@
 // takes the exponent of its own largest product instead (rare).
 //
 // Work.  One persistent CTA per SM; the CTAs divide the tiles of all (request, KV head, row
-// block) units evenly.  A unit cut by a CTA's end leaves partials (m, l, o / l) that
+// block) units evenly, each counted with its request's whole range (paged_q8_list.cuh).  A unit cut by a CTA's end leaves partials (m, l, o / l) that
 // q8_tc_merge_kernel joins in a fixed order.
 //
 // Warps, with their share of the 480 registers a lane that six warpgroups launch with:
