@@ -1098,7 +1098,7 @@ def make_norm_rope_params(*, headDim, norm=True, eps=1e-6, weightOffset=0.0, sec
     return p
 
 
-_ROPE_VALUES = dict(base=float, attentionFactor=float, rotaryDim=int, interleaved=bool)  # what make_rope_params reads them as
+_PLAIN = {bool, int, float, type(None)}  # values that cannot change
 
 
 @functools.lru_cache(maxsize=64)
@@ -1142,11 +1142,10 @@ def norm_rope(q, k, positions, *, headDim, qWeight=None, kWeight=None, norm=True
                 _need(name, t, f32, dev)
                 if t.shape != x.shape:
                     raise ValueError("norm_rope: out as q and k")
-    if rope.get("scaling") is None and rope.get("invFreq") is None:
-        p = _norm_rope_params(int(headDim), bool(norm), float(eps), float(weightOffset),
-                              None if sections is None else tuple(int(n) for n in sections), bool(dealt),
-                              tuple((k, x if x is None or k not in _ROPE_VALUES else _ROPE_VALUES[k](x)) for k, x in rope.items()))
-    else:  # may not be hashable, or change
+    pairs = None if sections is None else tuple(sections)
+    if _PLAIN.issuperset(map(type, (headDim, norm, eps, weightOffset, dealt, *rope.values(), *(pairs or ())))):
+        p = _norm_rope_params(headDim, norm, eps, weightOffset, pairs, dealt, tuple(rope.items()))
+    else:  # tensors, arrays and lists may change
         p = make_norm_rope_params(headDim=headDim, norm=norm, eps=eps, weightOffset=weightOffset, sections=sections,
                                   dealt=dealt, **rope)
     with _on(dev):
