@@ -272,14 +272,16 @@ __global__ void __launch_bounds__(32 * kMostWarps) q8_draft_kernel(const __grid_
     for (int e = 0; e < 2; ++e) {
         const int v = v0 + 2 * t4 + e, t = v / a.G;
         if (v >= rq.T * a.G) continue;
-        const float inv = l[e] != 0.f ? 1.f / l[e] : 0.f, half = exp2f(0.5f * (r[e] - 14.f));  // 2^(r - 14), in two steps
+        // 2^(r - 14) in two steps, each a whole power of two and a normal number.
+        const float inv = l[e] != 0.f ? 1.f / l[e] : 0.f, half = floorf(0.5f * (r[e] - 14.f));
+        const float p0 = exp2f(half), p1 = exp2f((r[e] - 14.f) - half);
         const int64_t row = ((int64_t)rq.row0 + t) * a.H + (int64_t)hk * a.G + (v - t * a.G);
         float* to = a.out + row * D + (D / 8) * gr;
 #pragma unroll
         for (int i = 0; i < MT; i += 2)
             *reinterpret_cast<float4*>(to + 2 * i) =
-                make_float4(o[i][e] * inv * half * half, o[i][2 + e] * inv * half * half, o[i + 1][e] * inv * half * half,
-                            o[i + 1][2 + e] * inv * half * half);
+                make_float4(o[i][e] * inv * p0 * p1, o[i][2 + e] * inv * p0 * p1, o[i + 1][e] * inv * p0 * p1,
+                            o[i + 1][2 + e] * inv * p0 * p1);
         if (gr == 0) ml[row] = make_float2(m[e], l[e]);
     }
 }

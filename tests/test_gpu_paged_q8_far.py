@@ -223,3 +223,19 @@ def test_rotation_alone(D, kw):
     y, _ = vtmu.norm_rope(dev(x), None, dev(pos if axes > 1 else pos[0]), headDim=D, norm=False, **kw)
     want, size = q8.norm_rope(x, pos, headDim=D, norm=False, **kw)
     assert np.all(np.abs(y.cpu().numpy() - want) <= 2.0 ** -20 * size)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[0, 0], [40, 0]])
+def test_a_drafted_row_alone_is_its_value(D, lens):
+    """A request whose one drafted row sees nothing else gives its value, of 22 bits or fewer, as it is,
+    whatever its size."""
+    size = size_of(2, 2, D, 16)
+    d = q8.batch(27, lens, [3, 1], form=q8.INT8, tree=True, **size)
+    g = np.random.default_rng(7)
+    for e in range(-120, 127, 3):
+        for power in (e, e + 1):
+            v = np.ldexp(g.integers(2 ** 21, 2 ** 22, 2 * D).astype(np.float32), power - 21).astype(np.float32)
+            d["tree"][1][3] = v
+            got = attend(d, kernel=TENSOR, **size)
+            assert np.array_equal(got[3], v), power
