@@ -16,8 +16,8 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import f32_gqa_attention_gb300 as vtmu  # noqa: E402
-from test_gpu_paged import dev  # noqa: E402
-from test_gpu_paged_q8 import CUDA, FORMS, TENSOR, attend, expect, size_of  # noqa: E402
+from test_gpu_paged import check, dev  # noqa: E402
+from test_gpu_paged_q8 import CUDA, FORMS, TENSOR, attend, codes, expect, size_of  # noqa: E402
 
 
 def check_heads(got, want, D):
@@ -239,3 +239,31 @@ def test_a_drafted_row_alone_is_its_value(D, lens):
             d["tree"][1][3] = v
             got = attend(d, kernel=TENSOR, **size)
             assert np.array_equal(got[3], v), power
+
+
+@pytest.mark.parametrize("kernel", [CUDA, TENSOR])
+@pytest.mark.parametrize("rows", [3, 20])
+@pytest.mark.parametrize("page", [8, 32, 64])
+@pytest.mark.parametrize("tree", [False, True])
+def test_a_request_as_long_as_its_table_allows(tree, page, rows, kernel):
+    """Row numbers up to 2^31 - 1: the last rows of the longest request, seen through a window,
+    are those of a short one with the same last rows."""
+    last, window = 256, 100
+    size = size_of(4, 2, 64, page)
+    d = q8.batch(54, [last], [rows], form=q8.INT8, tree=tree, **size)
+    want = expect(d, window=window, **size)
+    cols = (1 << 31) // page - 1
+    n = cols * page
+    table = torch.zeros(1, cols, dtype=torch.int32, device="cuda")
+    table[0, cols - last // page:] = dev(d["table"][0, :last // page])
+    drafted = None
+    if tree:
+        kn, vn, masks, positions = d["tree"]
+        drafted = tuple(dev(x) for x in (kn, vn, masks, (positions.astype(np.int64) + n - last).astype(np.int32)))
+        if int(positions.max()) + n - last >= 2 ** 31:
+            pytest.skip("no position is left for rows as deep as these")
+    got = vtmu.paged_attention_q8(dev(d["q"]), codes(d["kc"], q8.INT8), codes(d["vc"], q8.INT8), dev(d["ks"]), dev(d["vs"]), table,
+                                  dev(np.array([n], np.int32)), dev(d["cu"]), tree=drafted, maxRows=rows, kernel=kernel,
+                                  window=window, **size)
+    check(got.cpu().numpy(), want)
+    assert vtmu.vtmu_device_error() == 0
