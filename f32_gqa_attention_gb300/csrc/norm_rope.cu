@@ -7,8 +7,8 @@
 // needs the whole head before its first output, so a head stays in the registers of
 // L lanes: eight elements each, the two quads of four pairs, so that the rotation
 // needs no exchange; a lane past the rotated channels holds eight that pass through.
-// Memory-bound: 8 bytes an element.  8111 rows of 32 + 8 heads of 128 (332 MB) take 60 us, 5.5 TB/s
-// (82 % of the copy rate); without the streaming accesses 67, with a CTA per row and a table of
+// Memory-bound: 8 bytes an element.  8111 rows of 32 + 8 heads of 128 (332 MB) take 61 us, 5.4 TB/s
+// (81 % of the copy rate); without the streaming accesses 67, with a CTA per row and a table of
 // sines in shared memory 74 to 100.  A few rows: 3.2 us in a replayed graph.
 #include "norm_rope.h"
 #include "rope.cuh"

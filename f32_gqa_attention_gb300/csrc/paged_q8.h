@@ -55,8 +55,9 @@ unsigned int paged_q8_tc_take_device_error();
 // Which of the two: virtual rows (rows of a request x heads of a group) above kQ8FewRows take the
 // blocks of 128; its boxes of 64-byte rows want pages of an even size, and the box behind the
 // pool, which stands for bad pages, coordinates below 2^31.
-// 32 requests of 517 to 8111 rows, 4 heads a group: 16 virtual rows take 137 us with few rows' kernel,
-// 20 to 32 take 218 to 230 there and 185 to 195 in blocks, 64 take 408 and 204.
+// 32 requests of 517 to 8111 rows, 4 heads a group: 16 virtual rows take 132 us with few rows' kernel,
+// 20 to 32 take 218 to 230 there and 193 to 202 in blocks, 64 take 408 and 210 (8 heads a group: 129 us at
+// 16, 196 at 24, 208 at 64).
 constexpr int kQ8FewRows = 16;
 inline bool paged_q8_few_rows(const PagedDesc& a) {
     return (int64_t)a.max_rows * a.G <= kQ8FewRows || (a.D == 64 && a.page_size % 2 != 0) ||

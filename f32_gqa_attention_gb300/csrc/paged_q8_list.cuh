@@ -28,8 +28,8 @@ __device__ __forceinline__ Q8Req q8_load_req(const PagedDesc& a, int b) {
 // block; tiles that causality hides from a whole block are skipped when a CTA gets to them
 // (q8_seen_tiles), those before its window are computed for nothing.  So the CTAs' shares are even for trees
 // and for a few rows behind a long cache.  A prompt of 4096 rows (32 heads over 8) gives the busiest CTA
-// 213 live tiles of 128 keys where an even share is 111, and takes 1.40 ms; one of 8192 with a window of 1024
-// walks 66 560 tiles where 17 280 hold a key that is seen, 5.23 ms (2048 rows: 0.38 ms, 4096: 1.37).
+// 213 live tiles of 128 keys where an even share is 111, and takes 1.39 ms; one of 8192 with a window of 1024
+// walks 66 560 tiles where 17 280 hold a key that is seen, 5.27 ms (2048 rows: 0.38 ms, 4096: 1.41).
 struct Q8Units {
     int lo_tile, n_sink, nt;
 };

@@ -37,7 +37,7 @@
 // Every wait is bounded; one that gives up sets a bit of the device flag.
 //
 // Measured (a replayed graph): 24 requests of 8192 to 32704 rows, 32 heads over 8 of 128, e4m3
-// (1.08 GB) 175 us, 91 % of the copy rate; 32 of 517 to 8111, int8 (304 MB) 71 us, 63 %: of 24 us
+// (1.08 GB) 177 us, 91 % of the copy rate; 32 of 517 to 8111, int8 (304 MB) 71 us, 64 %: of 24 us
 // above the copy's the launches, the scan of the requests, the first loads and the join take most.
 #include <cstring>
 
@@ -303,6 +303,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mma_kernel(const __grid_consta
                 const uint8_t* vs = g.p.v + (int64_t)h0 * D;
                 const int64_t pitch = (int64_t)a.Hk * D;
                 // 8 kg rows of `chunks` chunks each.
+                // Rows of 1024 bytes (8 heads of 128) have a loop without divisions.  32 requests of 517 to 8112 rows:
+                // 292 MB of such rows 76 us; by the other loop 146 MB of 4 heads of 128 66, 150 MB of 8 of 64 72, 182 MB of
+                // 5 of 128 86.
                 if (chunks == 64) {  // two accesses a row
 #pragma unroll 8
                     for (int i = 0; i < 8; ++i) {

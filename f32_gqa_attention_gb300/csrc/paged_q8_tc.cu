@@ -29,12 +29,13 @@
 // Every wait is bounded; one that gives up sets a bit of the device flag.
 //
 // What bounds it.  8 trees of 64 rows beside 16384 to 32704 cached ones, 32 heads of 128 over 8 (large
-// trees below), take 405 us with the drafted rows' part and the join; the two f16 products of 2.17e11
-// FLOP would take 228 at the measured rate.  The scores and outputs of a tile take 1024 cycles of MMAs, a
+// trees below), take 411 us with the drafted rows' part and the join; the two f16 products of 2.17e11
+// FLOP would take 220 at the measured rate.  The scores and outputs of a tile take 1024 cycles of MMAs, a
 // tile 3900 to 4200: the softmax warps are at it all of that time (1100 to the maximum, 2600 from
 // there to the weights), and the roles together issue most of a tile's slots once packed f32
 // instructions count twice.  More instructions in the softmax show (always masked: 476 us where 446
-// was), and so does more code: with the next 16 scores loaded ahead in a loop twice as long, 463.  A
+// was), and so does more code: with the next 16 scores loaded ahead in a loop twice as long, 463; the places of
+// the rare paths alone move it by some per cent (433 with the far scales' path left out).  A
 // change of piece costs a CTA some 16 000 cycles more: queries, the output's rows, an empty pipeline.
 #include <cstring>
 #include <mutex>
@@ -447,7 +448,7 @@ __device__ __forceinline__ void tmem_st_16x8(uint32_t at, const uint32_t (&v)[4]
 // The queries of the piece that tile t begins, a warp's 32 virtual rows of its block: to tensor memory
 // as hi and lo, times qk_mul and a power of two that brings the row's largest element to
 // [2^13, 2^14); `back` gets what that takes back.  Four lanes share a row, so that a load touches 8
-// lines: with a row a lane, 32 lines, large trees took 412 us instead of 405, chunks 210 instead of 203.
+// lines: with a row a lane, 32 lines, large trees took 412 us where this took 405, chunks 210 and 203.
 template <int D>
 __device__ __forceinline__ void row_queries(const PagedDesc& a, const Tile& t, int w, int lane, uint32_t at_hi, uint32_t at_lo,
                                             float* back) {
