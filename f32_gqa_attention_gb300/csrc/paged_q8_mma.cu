@@ -20,9 +20,9 @@
 //
 // Work.  Lengths are known to the device alone, so the launch is one persistent CTA per
 // SM, and the CTAs divide the tiles of all (request, head block, row block) units
-// evenly (each unit counted with its request's whole range: paged_q8_list.cuh).  A tile is 32 keys for each of kg key groups, hb KV heads wide (all of them up
-// to eight), hb kg <= 8: a consumer warp per head and key group, which shares nothing with
-// the others until the piece ends.  A CTA so reads whole rows of the pool; with a worker
+// evenly (each unit counted with its request's whole range: paged_q8_list.cuh).  A tile is
+// 32 keys for each of kg key groups, hb KV heads wide (all of them up to eight), hb kg <= 8: a
+// consumer warp per head and key group, which shares nothing with the others until the piece ends.  A CTA so reads whole rows of the pool; with a worker
 // per head that loaded its own 128 bytes of each row, the heads drifted apart and HBM
 // gave 3.2 TB/s.  Key groups are joined inside the CTA; a unit cut by a CTA's end leaves
 // partials (m, l, o / l) that q8_merge_kernel joins in a fixed order: no atomics.

@@ -15,8 +15,8 @@
 // takes the exponent of its own largest product instead (rare).
 //
 // Work.  One persistent CTA per SM; the CTAs divide the tiles of all (request, KV head, row
-// block) units evenly, each counted with its request's whole range (paged_q8_list.cuh).  A unit cut by a CTA's end leaves partials (m, l, o / l) that
-// q8_tc_merge_kernel joins in a fixed order.
+// block) units evenly, each counted with its request's whole range (paged_q8_list.cuh).  A unit cut
+// by a CTA's end leaves partials (m, l, o / l) that q8_tc_merge_kernel joins in a fixed order.
 //
 // Warps, with their share of the 480 registers a lane that six warpgroups launch with:
 //   0, 2    page ids, TMA loads of K and of V codes (a box per page) and copies of scales
@@ -78,7 +78,8 @@ constexpr float kFarKey = 0x1p98f;
 // factor is below this one.  Rows that meet a larger one keep their sums times 2^-32 from there on: up to 2^31
 // weights of at most 1 times any value fit, and what that drops lies below 2^-117.
 constexpr float kHugeFactor = 0x1p72f;
-// Flags of a tile; slot + 1 in two bits from kSlotShift on.  K's converters add kFarKeys where a key's scale is kFarKey or more.
+// Flags of a tile; slot + 1 in two bits from kSlotShift on.  K's converters add kFarKeys where a key's
+// scale is kFarKey or more.
 enum : int { kFirst = 1, kLast = 2, kStop = 4, kSlotShift = 3, kFarKeys = 32 };
 enum : unsigned int {
     kErrQ8Load = 1u << 3,  // the paged kernels' bits: a tile that did not come,
